@@ -1,0 +1,578 @@
+// gdn_attn_rows.cu -- attention of a few query rows per key/value head over the paged cache: the
+// decode step (one token per sequence), and short runs of new tokens.
+//
+//   o_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = 2^(s_rj - m_r),   s_rj = scale log2(e) q_r . k_j
+//
+// with one pass over the keys: m_r is a reference that follows the running maximum (it only has to
+// stay within 2^8 of it, so the accumulator is rescaled when a maximum outgrows it by that much,
+// not at every step) and every sum is f32.
+//
+// What bounds it: the cache is read once, 2 D elements per key and head, for at most 16 rows, so
+// the floor is its bytes at the HBM rate.  Everything else must hide behind the loads:
+//  * a producer warp keeps a ring of 64-key stages full with TMA tensor copies (a box is 16 keys of
+//    one page, 128-byte swizzled), page numbers fetched one stage ahead;
+//  * each consumer warp takes 16 keys of a stage and runs its own softmax, so warps meet only at
+//    the end of a tile, where their accumulators are added in a fixed order;
+//  * the products are m16n8k16 MMAs on registers.  Sixteen rows fill that shape; the 128-row
+//    tcgen05 shape would run 7/8 empty here, needs the probabilities to cross TMEM, and could not
+//    be faster than the loads, which already set the pace;
+//  * 8-bit caches are converted in registers (exactly, to bf16), with the scales applied to the
+//    scores and to the probabilities instead of the elements.
+#include "gdn_attn.cuh"
+#include "gdn_tmap.h"
+
+namespace gdn {
+
+using namespace tc;
+
+namespace attn {
+
+constexpr int kRows = 16;
+constexpr int kTileKeys = 64;
+
+template <int D, bool Q8>
+struct RowsCfg {
+  // D = 256: the accumulators take 128 registers of a thread, so one CTA of eight consumer warps
+  // (two teams, alternate stages) instead of two CTAs of four.
+  static constexpr int kConsumers = D == 256 && Q8 ? 8 : 4;
+  static constexpr int kTeams = kConsumers / 4;
+  static constexpr int kCtas = D == 256 ? 1 : 2;
+  static constexpr int kThreads = (kConsumers + 1) * 32;
+  static constexpr int kElem = Q8 ? 1 : 2;
+  static constexpr int kGroupBytes = 16 * D * kElem;             // 16 keys (or values)
+  static constexpr int kHalfBytes = 4 * kGroupBytes;             // a stage's keys
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kRing = kCtas == 1 ? 196608 : 98304;
+  static constexpr int kFit = kRing / (kStageBytes + (Q8 ? 1024 : 0));   // with the scale bytes
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kBox = D * kElem >= 128 ? 128 : 64;       // swizzle span, bytes
+  static constexpr int kLd = D + 8;                              // merge buffer row
+};
+
+template <int D, bool Q8>
+struct __align__(1024) RowsSmem {
+  using C = RowsCfg<D, Q8>;
+  uint8_t ring[C::kStages][C::kStageBytes];
+  // scale bytes of a stage's four 16-key groups (16 bytes each: TMA wants 128-byte destinations)
+  uint8_t scales[Q8 ? C::kStages : 1][2][4][128];
+  uint4 q[D / 16][32];                    // A fragments of the 16 rows
+  float o[kRows][C::kLd];
+  float ml[C::kConsumers][kRows][2];
+  LineScan<kRows, C::kThreads> scan;
+  uint64_t full[C::kStages];
+  uint64_t empty[C::kStages];
+  int dead;
+};
+
+__device__ __forceinline__ void mma16816(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A bounded wait: a timeout marks the CTA dead, after which no wait blocks and the (wrong) results
+// are flagged by the status bit.
+__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
+  if (*dead) return;
+  if (!mbar_wait(bar, parity)) {
+    *dead = 1;
+    set_status(status, GDN_STATUS_TIMEOUT);
+  }
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(RowsCfg<D, Q8>::kThreads, RowsCfg<D, Q8>::kCtas)
+rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, long long least,
+            const __grid_constant__ KvMaps maps) {
+  using C = RowsCfg<D, Q8>;
+  constexpr int R = kRows, TK = kTileKeys, NC = C::kConsumers * 32;
+  extern __shared__ uint8_t smem_raw[];
+  RowsSmem<D, Q8>& sm = *reinterpret_cast<RowsSmem<D, Q8>*>(
+      smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 4);
+    }
+    sm.dead = 0;
+    mbar_fence_init();
+  }
+  pdl_begin();
+  zero_padding(a, b, D);
+  bool bad = false;
+  int pieces;
+  const int cta = blockIdx.x;
+  locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad);
+  if (bad) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
+  if (cta >= pieces) return;
+  const long long x0 = piece_bound(sm.scan.total, pieces, cta);
+  SegIter<R, TK> it;
+  it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
+           piece_bound(sm.scan.total, pieces, cta + 1) - x0);
+  Segment sg;
+
+  if (warp == C::kConsumers) {
+    // ---------------------------------------------------------------- producer
+    int stage = 0;
+    uint32_t phase = 0;
+    while (it.next(&sg)) {
+      if (sg.ta >= sg.tb) continue;
+      const int* table = b.table + (long long)sg.seq * b.table_ld;
+      const int keys = min(sg.info.len, tile_keys<R>(sg.info, a.g, sg.tile));
+      // lane i < 4 looks after the stage's i-th 16 keys
+      int k0 = sg.ta * TK + (lane & 3) * 16;
+      int page = k0 < keys ? __ldg(table + (k0 >> c.page_shift)) : 0;
+      for (int i = sg.ta; i < sg.tb; ++i) {
+        const int k1 = k0 + TK;
+        int page_next = 0;
+        if (i + 1 < sg.tb && k1 < keys) page_next = __ldg(table + (k1 >> c.page_shift));
+        wait_or_die(&sm.empty[stage], phase ^ 1u, &sm.dead, c.status);
+        const int live = min(4, (keys - i * TK + 15) >> 4);
+        uint64_t* full = &sm.full[stage];
+        if (lane == 0)
+          mbar_arrive_expect_tx(full, (uint32_t)live * (2 * C::kGroupBytes + (Q8 ? 32 : 0)));
+        __syncwarp();
+        if (lane < live) {
+          if (page < 0 || page >= c.num_pages) {
+            set_status(c.status, GDN_STATUS_PAGE_RANGE);
+            page = c.num_pages;            // outside the map: the copy fills zeros
+          }
+          const int off = k0 & ((1 << c.page_shift) - 1);
+          uint8_t* st = sm.ring[stage] + lane * C::kGroupBytes;
+          tma_load_5d(st, &maps.k, 0, off, 0, sg.head, page, full);
+          tma_load_5d(st + C::kHalfBytes, &maps.v, 0, off, 0, sg.head, page, full);
+          if constexpr (Q8) {
+            tma_load_3d(sm.scales[stage][0][lane], &maps.ks, off, sg.head, page, full);
+            tma_load_3d(sm.scales[stage][1][lane], &maps.vs, off, sg.head, page, full);
+          }
+        }
+        __syncwarp();
+        page = page_next;
+        k0 = k1;
+        if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int t = lane & 3, n = lane >> 2;
+  const int grp = warp & 3, team = warp >> 2;
+  int stage = 0;
+  uint32_t phase = 0;
+  unsigned turn = 0;
+  while (it.next(&sg)) {
+    const SeqInfo info = sg.info;
+    const int row_base = sg.tile * R;
+    const int rows = min((long long)R, (long long)info.tokens * a.g - row_base);
+    if (sg.ta >= sg.tb) {
+      if (sg.owns_empty)
+        for (int i = tid; i < rows * (D / 8); i += NC) {
+          int tok, head;
+          row_of(info, a.g, sg.head, row_base + i / (D / 8), &tok, &head);
+          *reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D + (i % (D / 8)) * 8) =
+              make_uint4(0, 0, 0, 0);
+        }
+      continue;
+    }
+    const int keys = min(info.len, tile_keys<R>(info, a.g, sg.tile));
+    const int before = info.len - info.tokens;          // position of the first new token
+    // Q fragments: word (row, k pair) of k-step ks; the 8-bit form permutes k inside 64-element
+    // blocks so that a lane's 16 bytes of a key are consecutive.
+    for (int i = tid; i < (D / 16) * 32; i += NC) {
+      const int ks = i >> 5, ln = i & 31, qt = ln & 3, qn = ln >> 2;
+      const int d0 = Q8 ? (ks >> 2) * 64 + qt * 16 + (ks & 3) * 4 : ks * 16 + 2 * qt;
+      const int d1 = Q8 ? d0 + 2 : d0 + 8;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      int tok, head;
+      if (qn < rows) {
+        row_of(info, a.g, sg.head, row_base + qn, &tok, &head);
+        const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
+        v.x = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
+        v.z = __ldg(reinterpret_cast<const uint32_t*>(p + d1));
+      }
+      if (qn + 8 < rows) {
+        row_of(info, a.g, sg.head, row_base + qn + 8, &tok, &head);
+        const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
+        v.y = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
+        v.w = __ldg(reinterpret_cast<const uint32_t*>(p + d1));
+      }
+      sm.q[ks][ln] = v;
+    }
+    bar_sync(1, NC);
+    // last position each of this thread's two rows sees
+    const int pos0 = before + (row_base + n) / a.g, pos1 = before + (row_base + n + 8) / a.g;
+    const int pos_min = before + row_base / a.g;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    for (int i = sg.ta; i < sg.tb; ++i, ++turn) {
+      const int st = stage;
+      const uint32_t ph = phase;
+      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+      if (C::kTeams > 1 && (int)(turn % C::kTeams) != team) continue;
+      wait_or_die(&sm.full[st], ph, &sm.dead, c.status);
+      const int k0 = i * TK + grp * 16;
+      if (k0 < keys) {
+        const uint32_t kb = smem_u32(sm.ring[st]) + grp * C::kGroupBytes;
+        const uint32_t vb = kb + C::kHalfBytes;
+        // ---- scores: 16 rows x 16 keys
+        float s[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        if constexpr (!Q8) {
+          const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+          const uint32_t row = kb + key * 128;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t r[4];
+            ldsm4(row + (ks >> 2) * 2048 + ((((ks & 3) * 2 + half) ^ (key & 7)) << 4), r);
+            const uint4 q = sm.q[ks][lane];
+            mma16816(s[0], q, r[0], r[1]);
+            mma16816(s[1], q, r[2], r[3]);
+          }
+        } else {
+          // column n of score tile j is key (n >> 1) + 4 (2 j + (n & 1)): the order in which the
+          // value fragments below want them
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb) {
+            uint4 w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int key = (n >> 1) + 4 * (2 * j + (n & 1));
+              const int chunk = (C::kBox == 128) ? (((cb & 1) * 4 + t) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
+              w[j] = lds128(kb + (C::kBox == 128 ? (cb >> 1) * 2048 : 0) + key * C::kBox + chunk * 16);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 q = sm.q[cb * 4 + e][lane];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t x = e == 0 ? w[j].x : e == 1 ? w[j].y : e == 2 ? w[j].z : w[j].w;
+                uint32_t b0, b1;
+                e4m3x4_to_bf16(x, b0, b1);
+                mma16816(s[j], q, b0, b1);
+              }
+            }
+          }
+        }
+        float vs[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float f = a.scale_log2;
+            if constexpr (Q8) {
+              const int key = t + 4 * (2 * j + e);
+              f *= scale_f32(sm.scales[st][0][grp][key]);
+              vs[j][e] = scale_f32(sm.scales[st][1][grp][key]);
+            } else {
+              vs[j][e] = 1.f;
+            }
+            s[j][e] *= f;
+            s[j][e + 2] *= f;
+          }
+        const bool partial = k0 + 15 > pos_min;       // some row does not see all 16 keys
+        if (partial) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = k0 + (Q8 ? t + 4 * (2 * j + e) : j * 8 + 2 * t + e);
+              if (key > pos0) s[j][e] = -INFINITY;
+              if (key > pos1) s[j][e + 2] = -INFINITY;
+            }
+        }
+        // ---- softmax of this warp's keys
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        // 2^8 above the reference is harmless in f32 and in the bf16 probabilities alike
+        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+          const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+          const float f0 = m0 == n0 ? 1.f : ex2(m0 - n0), f1 = m1 == n1 ? 1.f : ex2(m1 - n1);
+          m0 = n0; m1 = n1;
+          l0 *= f0; l1 *= f1;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            o[d][0] *= f0; o[d][1] *= f0; o[d][2] *= f1; o[d][3] *= f1;
+          }
+        }
+        const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[j][e] = ex2(s[j][e] - r0);
+            s[j][e + 2] = ex2(s[j][e + 2] - r1);
+            l0 += s[j][e];
+            l1 += s[j][e + 2];
+          }
+        uint4 p;
+        if constexpr (Q8) {
+          // the value's scale; a hidden key stays at zero even if its vector reads as NaN
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = k0 + t + 4 * (2 * j + e);
+              s[j][e] = key > pos0 ? 0.f : s[j][e] * vs[j][e];
+              s[j][e + 2] = key > pos1 ? 0.f : s[j][e + 2] * vs[j][e];
+            }
+        }
+        p.x = pack_bf16(s[0][0], s[0][1]);
+        p.y = pack_bf16(s[0][2], s[0][3]);
+        p.z = pack_bf16(s[1][0], s[1][1]);
+        p.w = pack_bf16(s[1][2], s[1][3]);
+        // ---- values
+        if constexpr (!Q8) {
+          const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+          const uint32_t row = vb + key * 128;
+          // keys past the sequence's end: their rows may hold anything, and 0 x NaN is NaN
+          const bool tail = k0 + 16 > keys;
+          uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
+          if (tail) {
+            const int u = k0 + 2 * t;
+            z0 = (u < keys ? 0xffffu : 0u) | (u + 1 < keys ? 0xffff0000u : 0u);
+            z1 = (u + 8 < keys ? 0xffffu : 0u) | (u + 9 < keys ? 0xffff0000u : 0u);
+          }
+          bool finite = true;
+          if (partial && info.tokens > 1) {
+            // a key hidden from some rows and seen by others: its value must be finite for the
+            // matrix product to leave the former alone
+            uint32_t seen = 0;
+#pragma unroll 4
+            for (int d = 0; d < D / 16; ++d) {
+              uint32_t r[4];
+              ldsm4t(row + (d >> 2) * 2048 + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
+              seen |= ((r[0] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[1] & z1 & 0x7f807f80u) + 0x00800080u) |
+                      ((r[2] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[3] & z1 & 0x7f807f80u) + 0x00800080u);
+            }
+            finite = !__any_sync(0xffffffffu, (seen & 0x80008000u) != 0);
+          }
+          if (finite) {
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              uint32_t r[4];
+              ldsm4t(row + (d >> 2) * 2048 + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
+              if (tail) { r[0] &= z0; r[1] &= z1; r[2] &= z0; r[3] &= z1; }
+              mma16816(o[2 * d], p, r[0], r[1]);
+              mma16816(o[2 * d + 1], p, r[2], r[3]);
+            }
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < 16 && k0 + j < keys; ++j) {
+              const int src = (lane & ~3) | ((j & 7) >> 1);
+              const float u0 = j & 8 ? (j & 1 ? s[1][1] : s[1][0]) : (j & 1 ? s[0][1] : s[0][0]);
+              const float u1 = j & 8 ? (j & 1 ? s[1][3] : s[1][2]) : (j & 1 ? s[0][3] : s[0][2]);
+              const float p0 = __shfl_sync(0xffffffffu, u0, src), p1 = __shfl_sync(0xffffffffu, u1, src);
+              const bool see0 = k0 + j <= pos0, see1 = k0 + j <= pos1;
+#pragma unroll
+              for (int d = 0; d < D / 8; ++d) {
+                const uint32_t w = lds32(vb + j * 128 + (d >> 3) * 2048 + (((d & 7) ^ (j & 7)) << 4) + t * 4);
+                const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
+                if (see0) { o[d][0] = fmaf(p0, v0, o[d][0]); o[d][1] = fmaf(p0, v1, o[d][1]); }
+                if (see1) { o[d][2] = fmaf(p1, v0, o[d][2]); o[d][3] = fmaf(p1, v1, o[d][3]); }
+              }
+            }
+          }
+        } else if constexpr (D >= 128) {
+          // lane (n, t) reads 16 bytes (16 columns) of keys t, t + 4, t + 8, t + 12; byte jn of
+          // them is this lane's column n of output tile jn
+          const int col = (n & 1) * 4 + (n >> 1);
+#pragma unroll
+          for (int blk = 0; blk < D / 128; ++blk) {
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int key = t + 4 * j;
+              w[j] = lds128(vb + blk * 2048 + key * 128 + ((col ^ (key & 7)) << 4));
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t e0 = q == 0 ? w[0].x : q == 1 ? w[0].y : q == 2 ? w[0].z : w[0].w;
+              const uint32_t e1 = q == 0 ? w[1].x : q == 1 ? w[1].y : q == 2 ? w[1].z : w[1].w;
+              const uint32_t e2 = q == 0 ? w[2].x : q == 1 ? w[2].y : q == 2 ? w[2].z : w[2].w;
+              const uint32_t e3 = q == 0 ? w[3].x : q == 1 ? w[3].y : q == 2 ? w[3].z : w[3].w;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                // byte y of e0 into byte 1, of e1 into byte 3 (the other two are masked away)
+                const uint32_t sel = (uint32_t)((4 + y) << 12 | y << 4);
+                mma16816(o[blk * 16 + q * 4 + y], p, e4m3_hi_to_bf16x2(__byte_perm(e0, e1, sel)),
+                         e4m3_hi_to_bf16x2(__byte_perm(e2, e3, sel)));
+              }
+            }
+          }
+        } else {
+          // D = 64: 64-byte rows, 8 columns (8 bytes) per lane
+          uint2 w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = t + 4 * j;
+            w[j] = lds64(vb + key * 64 + (((n >> 1) ^ ((key >> 1) & 3)) << 4) + (n & 1) * 8);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t sel = (uint32_t)((4 + y) << 12 | y << 4);
+              mma16816(o[q * 4 + y], p,
+                       e4m3_hi_to_bf16x2(__byte_perm(q ? w[0].y : w[0].x, q ? w[1].y : w[1].x, sel)),
+                       e4m3_hi_to_bf16x2(__byte_perm(q ? w[2].y : w[2].x, q ? w[3].y : w[3].x, sel)));
+            }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
+    }
+
+    // ---- the warps' results of this tile become one
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // a NaN sum must survive the merge even when its reference never left -infinity
+    if (l0 != l0) m0 = INFINITY;
+    if (l1 != l1) m1 = INFINITY;
+    if (t == 0) {
+      sm.ml[warp][n][0] = m0; sm.ml[warp][n][1] = l0;
+      sm.ml[warp][n + 8][0] = m1; sm.ml[warp][n + 8][1] = l1;
+    }
+    bar_sync(1, NC);
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < C::kConsumers; ++w) {
+      M0 = fmaxf(M0, sm.ml[w][n][0]);
+      M1 = fmaxf(M1, sm.ml[w][n + 8][0]);
+    }
+    const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
+    for (int w = 0; w < C::kConsumers; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          // columns of o[d][0], o[d][1]
+          int ca, cb;
+          if constexpr (!Q8) { ca = d * 8 + 2 * t; cb = ca + 1; }
+          else if constexpr (D >= 128) { ca = (d >> 4) * 128 + t * 16 + (d & 15); cb = ca + 64; }
+          else { ca = 2 * t * 8 + d; cb = ca + 8; }
+          const float a0 = o[d][0] * f0, a1 = o[d][1] * f0, a2 = o[d][2] * f1, a3 = o[d][3] * f1;
+          if (w == 0) {
+            sm.o[n][ca] = a0; sm.o[n][cb] = a1; sm.o[n + 8][ca] = a2; sm.o[n + 8][cb] = a3;
+          } else {
+            sm.o[n][ca] += a0; sm.o[n][cb] += a1; sm.o[n + 8][ca] += a2; sm.o[n + 8][cb] += a3;
+          }
+        }
+      }
+      bar_sync(1, NC);
+    }
+    const bool whole = sg.whole();
+    float* prow = Partials<R, D>::rows(a.ws, cta, sg.slot);
+    float* pml = Partials<R, D>::ml(a.ws, cta, sg.slot);
+    for (int i = tid; i < rows * (D / 4); i += NC) {
+      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      float M = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::kConsumers; ++w) M = fmaxf(M, sm.ml[w][r][0]);
+#pragma unroll
+      for (int w = 0; w < C::kConsumers; ++w) {
+        const float mw = sm.ml[w][r][0];
+        if (mw != -INFINITY) l += sm.ml[w][r][1] * ex2(mw - M);
+      }
+      float4 v = *reinterpret_cast<const float4*>(&sm.o[r][d]);
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+        int tok, head;
+        row_of(info, a.g, sg.head, row_base + r, &tok, &head);
+        store_out4(a, D, tok, head, d, v);
+      } else {
+        __stcg(reinterpret_cast<float4*>(prow + (size_t)r * D + d), v);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(pml + 2 * r), make_float2(M, l));
+      }
+    }
+    bar_sync(1, NC);
+  }
+}
+
+template <int D, bool Q8>
+int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
+  using C = RowsCfg<D, Q8>;
+  constexpr size_t smem = sizeof(RowsSmem<D, Q8>) + 1024;
+  static_assert((smem + 1024) * C::kCtas <= 233472, "shared memory of an SM");
+  static const cudaError_t set = cudaFuncSetAttribute(
+      rows_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (set != cudaSuccess) return GDN_ERR_CUDA;
+  KvMaps maps;
+  if (!make_kv_maps(c, 16, &maps)) return GDN_ERR_CUDA;
+  const int grid = rows_grid(D, sms), fix = 64 * a.g;
+  const long long least = 256LL * a.g;
+  int rc = launch_dependent(rows_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
+                            fix, least, maps);
+  if (rc != GDN_OK) return rc;
+  return launch_dependent(merge_kernel<kRows, kTileKeys, D>, dim3((unsigned)(grid - 1), 4), 256, 0, stream, c, b, a,
+                          grid, fix, least);
+}
+
+int rows_grid(int D, int sms) { return min(1024, D == 256 ? sms : 2 * sms); }
+
+size_t rows_ws_bytes(int D, int sms) {
+  const int grid = rows_grid(D, sms);
+  return D == 64 ? Partials<kRows, 64>::bytes(grid)
+       : D == 128 ? Partials<kRows, 128>::bytes(grid) : Partials<kRows, 256>::bytes(grid);
+}
+
+int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
+  const bool q8 = c.ks != nullptr;
+  if (c.D == 64) return q8 ? launch_rows<64, true>(c, b, a, sms, stream) : launch_rows<64, false>(c, b, a, sms, stream);
+  if (c.D == 128) return q8 ? launch_rows<128, true>(c, b, a, sms, stream) : launch_rows<128, false>(c, b, a, sms, stream);
+  return q8 ? launch_rows<256, true>(c, b, a, sms, stream) : launch_rows<256, false>(c, b, a, sms, stream);
+}
+
+}  // namespace attn
+}  // namespace gdn

@@ -97,4 +97,44 @@ int launch_proj_pack(const void* w, int N, int K, void* packed, cudaStream_t str
 int launch_proj(const void* x, const void* wp, int M, int N, int K, int ks, const ProjRoute& route,
                 int32_t* status, cudaStream_t stream);
 
+// RMSNorm with the residual's addition (kind: a gdn_norm_out).
+int launch_rms_norm(const void* x, long long x_ld, const void* residual, long long residual_ld,
+                    const void* weight, float weight_offset, float eps, int rows, int n,
+                    gdn_dtype act, int kind, void* sum_out, void* y, float* scales,
+                    cudaStream_t stream);
+
+// The paged key/value cache and the new tokens of a call, by value to every kernel.
+struct KvView {
+  void* k;
+  void* v;
+  uint8_t* ks;    // exponent bytes; NULL for a bf16 cache
+  uint8_t* vs;
+  int32_t* status;
+  int num_pages, page_shift, H, D;
+};
+
+struct KvBatchView {
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* table;
+  int num_seqs, total, table_ld, max_tokens;
+};
+
+int launch_kv_append(const KvView& c, const KvBatchView& b, const void* k, long long k_ld,
+                     const void* v, long long v_ld, cudaStream_t stream);
+int launch_kv_read(const KvView& c, const KvBatchView& b, void* k, void* v, cudaStream_t stream);
+
+struct AttnArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* gate;
+  __nv_bfloat16* out;
+  long long q_ld, q_head_ld, gate_ld, gate_head_ld;
+  int Hq, g;           // query heads; query heads per key/value head
+  float scale_log2;    // softmax scale times log2(e)
+  float* ws;
+};
+
+size_t attn_ws_bytes(const KvView& c, int Hq);
+int launch_attn(const KvView& c, const KvBatchView& b, const AttnArgs& a, cudaStream_t stream);
+
 }  // namespace gdn

@@ -1,0 +1,85 @@
+// gdn_kv.cuh -- the paged key/value cache as the kernels see it: geometry, a token's place, and
+// the exact e4m3 -> bf16 conversion.
+#pragma once
+
+#include "gdn_internal.h"
+
+namespace gdn {
+
+// Where a packed token lives: page < 0 when it has no place.
+struct Place {
+  int page, off;
+};
+
+// The sequence holding packed token t: the largest s with cu[s] <= t, by a 32-way search of the
+// whole warp (all lanes with the same t, or each lane its own: the search follows the least t of
+// the warp and every lane then steps forward to its own).
+__device__ __forceinline__ int find_seq(const KvBatchView& b, int t) {
+  const int lane = threadIdx.x & 31;
+  const int t0 = __reduce_min_sync(0xffffffffu, t);
+  int lo = 0, hi = b.num_seqs;                  // cu[lo] <= t0 (cu[0] = 0), answer in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int i = lo + lane * step;
+    const bool le = i < hi && (lane == 0 || __ldg(b.cu + i) <= t0);
+    const int k = __popc(__ballot_sync(0xffffffffu, le));   // lanes 0..k-1 when cu is monotone
+    lo += (k - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  while (lo + 1 < b.num_seqs && __ldg(b.cu + lo + 1) <= t) ++lo;
+  return lo;
+}
+
+// The place of packed token t (all 32 lanes of the warp call this together).
+__device__ __forceinline__ Place find_place(const KvView& c, const KvBatchView& b, int t) {
+  const int s = find_seq(b, t);
+  const int c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1);
+  Place p{-1, 0};
+  if (t >= c1 && s == b.num_seqs - 1 && c1 >= c0) return p;    // padding past the last sequence
+  const long long len = __ldg(b.lens + s);
+  if (t < c0 || t >= c1 || c1 > b.total || len < 0 || len > ((long long)b.table_ld << c.page_shift)) {
+    set_status(c.status, GDN_STATUS_BAD_SEQLENS);
+    return p;
+  }
+  const long long pos = len - (c1 - t);
+  if (pos < 0) return p;
+  const int page = __ldg(b.table + (long long)s * b.table_ld + (pos >> c.page_shift));
+  if (page < 0 || page >= c.num_pages) {
+    set_status(c.status, GDN_STATUS_PAGE_RANGE);
+    return p;
+  }
+  p.page = page;
+  p.off = (int)(pos & ((1 << c.page_shift) - 1));
+  return p;
+}
+
+// ------------------------------------------------------------------ e4m3 -> bf16
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The e4m3 codes in the upper bytes of w's two halves as bf16 values.  A code's exponent and
+// mantissa, moved to the low four exponent bits and the high three mantissa bits of a bf16, are
+// the value times 2^-120 (the biases 127 and 7 apart; subnormals included), so one exact multiply
+// by 2^120 finishes.  The NaN codes 0x7f / 0xff (which the cache never holds) come out as +-480.
+__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t w) {
+  const uint32_t u = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  return mul_bf16x2(u, 0x7b807b80u);
+}
+
+// Four codes b0..b3 (b0 lowest) -> the bf16 pairs (b0, b1) and (b2, b3).
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  p01 = e4m3_hi_to_bf16x2(__byte_perm(w, 0, 0x1404));
+  p23 = e4m3_hi_to_bf16x2(__byte_perm(w, 0, 0x3424));
+}
+
+// The bf16 bits of the scale with exponent byte b (255: NaN).
+__device__ __forceinline__ uint32_t scale_bits(uint32_t b) { return b == 255 ? 0x7fc0u : b << 7; }
+
+// The same as an f32.
+__device__ __forceinline__ float scale_f32(uint32_t b) { return __uint_as_float(scale_bits(b) << 16); }
+
+}  // namespace gdn

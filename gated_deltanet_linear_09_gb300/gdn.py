@@ -20,6 +20,14 @@ GDN_BF16 = 1
 GDN_MAX_COMPACT_PAIRS = 2048
 GDN_STATUS_SLOT_RANGE = 1
 GDN_STATUS_BAD_SEQLENS = 2
+GDN_STATUS_TIMEOUT = 4
+GDN_STATUS_PAGE_RANGE = 8
+GDN_NORM_ACT = 0
+GDN_NORM_E4M3_ROW = 1
+GDN_NORM_E4M3_BLOCK = 2
+GDN_MAX_NORM_WIDTH = 32768
+GDN_KV_BF16 = 0
+GDN_KV_E4M3 = 1
 
 _CODES = {
     0: "GDN_OK", -1: "GDN_ERR_INVALID_ARG", -2: "GDN_ERR_UNSUPPORTED_SHAPE",
@@ -33,7 +41,8 @@ EXPORTED = ("gdn_state_slot_bytes", "gdn_conv1d_update", "gdn_decode_step", "gdn
             "gdn_status_string", "gdn_prefill_chunked_noalloc", "gdn_decode_graphs_create",
             "gdn_decode_graphs_buffers", "gdn_decode_graphs_launch", "gdn_decode_graphs_destroy",
             "gdn_proj_packed_bytes", "gdn_proj_pack", "gdn_linear_bf16", "gdn_in_proj",
-            "gdn_out_proj")
+            "gdn_out_proj", "gdn_rms_norm", "gdn_kv_append", "gdn_kv_read",
+            "gdn_paged_attention_workspace_bytes", "gdn_paged_attention")
 GDN_MAX_DECODE_TOKENS = 8
 GDN_MAX_GRAPH_BUCKETS = 16
 GDN_NOALLOC_PREFILL_SCRATCH_BYTES = 64 << 20
@@ -69,6 +78,21 @@ class gdn_proj_route(ctypes.Structure):
 class gdn_pool(ctypes.Structure):
     _fields_ = [("rec_state", ctypes.c_void_p), ("conv_state", ctypes.c_void_p),
                 ("num_slots", ctypes.c_int32), ("status", ctypes.c_void_p)]
+
+
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("type", ctypes.c_int), ("status", ctypes.c_void_p)]
+
+
+class gdn_kv_batch(ctypes.Structure):
+    _fields_ = [("cu_seqlens", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int32), ("table_ld", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32)]
 
 
 _lib = None
@@ -128,6 +152,19 @@ def load(build_if_missing: bool = False):
     lib.gdn_in_proj.argtypes = [_P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P]
     lib.gdn_out_proj.restype = ctypes.c_int
     lib.gdn_out_proj.argtypes = [_P, _P, _P, _I32, _I32, _P, _P, _P]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.gdn_rms_norm.restype = ctypes.c_int
+    lib.gdn_rms_norm.argtypes = [_P, i64, _P, i64, _P, f32, f32, _I32, _I32, ctypes.c_int,
+                                 ctypes.c_int, _P, _P, _P, _P]
+    lib.gdn_kv_append.restype = ctypes.c_int
+    lib.gdn_kv_append.argtypes = [_P, _P, _P, i64, _P, i64, _P]
+    lib.gdn_kv_read.restype = ctypes.c_int
+    lib.gdn_kv_read.argtypes = [_P, _P, _P, _P, _P]
+    lib.gdn_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_paged_attention_workspace_bytes.argtypes = [_P, _I32]
+    lib.gdn_paged_attention.restype = ctypes.c_int
+    lib.gdn_paged_attention.argtypes = [_P, _P, _I32, _P, i64, i64, _P, i64, i64, f32, _P, _P,
+                                        ctypes.c_size_t, _P]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     _lib = lib
@@ -308,6 +345,61 @@ def gdn_out_proj(dims, out, w_out_packed, y, status=None, stream=None):
     rows, H = int(out.shape[0]), int(y.shape[1])
     _check("gdn_out_proj", load().gdn_out_proj(
         ctypes.byref(dims), _ptr(out), _ptr(w_out_packed), rows, H, _ptr(y), _ptr(status),
+        _stream(stream)))
+
+
+def make_kv_cache(k_pages, v_pages, k_scales=None, v_scales=None, status=None) -> gdn_kv_cache:
+    """Pages [num_pages][num_kv_heads][page_size][head_dim] (bf16 or float8_e4m3fn) as a struct."""
+    np_, heads, page, dim = (int(x) for x in k_pages.shape)
+    q8 = k_pages.dtype == torch.float8_e4m3fn
+    if not q8 and k_pages.dtype != torch.bfloat16:
+        raise ValueError(f"unsupported cache dtype {k_pages.dtype}")
+    return gdn_kv_cache(_ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), np_, page,
+                        heads, dim, GDN_KV_E4M3 if q8 else GDN_KV_BF16, _ptr(status))
+
+
+def make_kv_batch(cu_seqlens, kv_lens, block_table, total_tokens: int, max_tokens: int = 0) -> gdn_kv_batch:
+    """Device int32 tensors: cu_seqlens [n + 1], kv_lens [n], block_table [n][table_ld] (rows may be
+    strided)."""
+    return gdn_kv_batch(_ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), int(kv_lens.shape[0]),
+                        int(total_tokens), int(block_table.stride(0)) if block_table.shape[0] > 1
+                        else int(block_table.shape[1]), int(max_tokens))
+
+
+def gdn_rms_norm(x, weight, y, residual=None, sum_out=None, scales=None, weight_offset=0.0, eps=1e-6,
+                 out_kind=GDN_NORM_ACT, stream=None):
+    """x, residual [rows][n] (rows may be strided), y / sum_out dense [rows][n], scales f32."""
+    rows, n = x.shape
+    _check("gdn_rms_norm", load().gdn_rms_norm(
+        x.data_ptr(), x.stride(0) if rows > 1 else n, _ptr(residual),
+        0 if residual is None else residual.stride(0) if rows > 1 else n, weight.data_ptr(),
+        weight_offset, eps, rows, n, act_code(x.dtype), out_kind, _ptr(sum_out), y.data_ptr(),
+        _ptr(scales), _stream(stream)))
+
+
+def gdn_kv_append(cache, batch, k, v, stream=None):
+    """k, v: bf16 [tokens][heads][dim], token rows may be strided."""
+    _check("gdn_kv_append", load().gdn_kv_append(
+        ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), k.stride(0), v.data_ptr(),
+        v.stride(0), _stream(stream)))
+
+
+def gdn_kv_read(cache, batch, k, v, stream=None):
+    """k, v: dense bf16 [tokens][heads][dim] outputs."""
+    _check("gdn_kv_read", load().gdn_kv_read(
+        ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), v.data_ptr(), _stream(stream)))
+
+
+def gdn_paged_attention_workspace_bytes(cache, num_q_heads: int) -> int:
+    return int(load().gdn_paged_attention_workspace_bytes(ctypes.byref(cache), int(num_q_heads)))
+
+
+def gdn_paged_attention(cache, batch, q, out, workspace, gate=None, scale=0.0, stream=None):
+    """q, gate: bf16 [tokens][heads][dim] (tokens and heads may be strided), out dense."""
+    _check("gdn_paged_attention", load().gdn_paged_attention(
+        ctypes.byref(cache), ctypes.byref(batch), q.shape[1], q.data_ptr(), q.stride(0), q.stride(1),
+        _ptr(gate), 0 if gate is None else gate.stride(0), 0 if gate is None else gate.stride(1),
+        scale, out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream(stream)))
 
 

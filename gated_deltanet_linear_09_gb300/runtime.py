@@ -178,3 +178,147 @@ class DecodeGraphs:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- the full-attention layers' side
+
+_NORM_KINDS = {"none": gdn.GDN_NORM_ACT, "row": gdn.GDN_NORM_E4M3_ROW, "block": gdn.GDN_NORM_E4M3_BLOCK}
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant="none", stream=None):
+    """RMSNorm of x (+ residual), rows [rows][n] of bf16 or f32: returns (y, scales, total).
+
+    total is x + residual in the activation dtype (None without a residual).  quant "none": y in
+    the activation dtype, scales None; "row" / "block": y float8_e4m3fn with f32 scales per row
+    [rows][1] or per 128 columns [rows][ceil(n / 128)]."""
+    if x.dim() != 2 or x.stride(1) != 1 or x.dtype != weight.dtype or weight.shape != (x.shape[1],) or \
+            weight.stride(0) != 1:
+        raise ValueError("rms_norm takes rows [rows][n] and a weight [n] of one dtype")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or
+                                 residual.stride(1) != 1):
+        raise ValueError("residual must have the shape and dtype of x")
+    kind = _NORM_KINDS[quant]
+    rows, n = x.shape
+    scales = None
+    if kind == gdn.GDN_NORM_ACT:
+        y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+    else:
+        y = torch.empty((rows, n), dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty((rows, 1 if quant == "row" else (n + 127) // 128), dtype=torch.float32,
+                             device=x.device)
+    total = None if residual is None else torch.empty((rows, n), dtype=x.dtype, device=x.device)
+    gdn.gdn_rms_norm(x, weight, y, residual, total, scales, weight_offset, eps, kind, stream)
+    return y, scales, total
+
+
+class KVBatch:
+    """The new tokens of one step: device int32 cu_seqlens [n + 1], kv_lens [n] (cached positions
+    including the new tokens) and block_table [n][pages].  total_tokens: packed token rows;
+    max_tokens: host bound on one sequence's new tokens (0: unknown)."""
+
+    def __init__(self, cu_seqlens, kv_lens, block_table, total_tokens: int, max_tokens: int = 0):
+        for t in (cu_seqlens, kv_lens, block_table):
+            if t.dtype != torch.int32 or (t.numel() > 1 and t.stride(-1) != 1):
+                raise ValueError("cu_seqlens, kv_lens and block_table are int32 with contiguous rows")
+        if block_table.dim() != 2 or cu_seqlens.shape[0] != kv_lens.shape[0] + 1 or \
+                block_table.shape[0] != kv_lens.shape[0]:
+            raise ValueError("cu_seqlens [n + 1], kv_lens [n] and block_table [n][pages] expected")
+        self.tensors = (cu_seqlens, kv_lens, block_table)     # kept alive with the struct
+        self.total_tokens = int(total_tokens)
+        self.c = gdn.make_kv_batch(cu_seqlens, kv_lens, block_table, total_tokens, max_tokens)
+
+
+class PagedKVCache:
+    """Key/value pages [num_pages][num_kv_heads][page_size][head_dim], bf16 or 8-bit e4m3 with one
+    power-of-two scale per vector, and the attention workspace of this cache."""
+
+    def __init__(self, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+                 quantised: bool = False, device="cuda"):
+        shape = (num_pages, num_kv_heads, page_size, head_dim)
+        if quantised:
+            pages = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                     for _ in range(2)]
+            scales = [torch.full(shape[:3], 127, dtype=torch.uint8, device=device) for _ in range(2)]
+        else:
+            pages = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)]
+            scales = [None, None]
+        self._bind(*pages, *scales)
+
+    @classmethod
+    def over(cls, k_pages, v_pages, k_scales=None, v_scales=None) -> "PagedKVCache":
+        """A cache over existing page tensors."""
+        self = cls.__new__(cls)
+        self._bind(k_pages, v_pages, k_scales, v_scales)
+        return self
+
+    def _bind(self, k_pages, v_pages, k_scales, v_scales):
+        q8 = k_pages.dtype == torch.float8_e4m3fn
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or \
+                not k_pages.is_contiguous() or not v_pages.is_contiguous():
+            raise ValueError("k_pages and v_pages: contiguous [pages][heads][page_size][head_dim], one dtype")
+        for s in (k_scales, v_scales):
+            if (s is not None) != q8 or (q8 and (s.dtype != torch.uint8 or s.shape != k_pages.shape[:3] or
+                                                 not s.is_contiguous())):
+                raise ValueError("an 8-bit cache has contiguous uint8 scales [pages][heads][page_size]")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self.num_kv_heads, self.head_dim = int(k_pages.shape[1]), int(k_pages.shape[3])
+        self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
+        self.c = gdn.make_kv_cache(k_pages, v_pages, k_scales, v_scales, self.status)
+        self._ws = {}
+
+    def workspace(self, num_q_heads: int) -> torch.Tensor:
+        """The attention's workspace for this many query heads (one per cache and stream: calls that
+        overlap need their own, see attend's argument)."""
+        ws = self._ws.get(num_q_heads)
+        if ws is None:
+            need = gdn.gdn_paged_attention_workspace_bytes(self.c, num_q_heads)
+            if need == 0:
+                raise ValueError(f"{num_q_heads} query heads over this cache are not supported")
+            ws = self._ws[num_q_heads] = torch.empty(need, dtype=torch.uint8, device=self.k_pages.device)
+        return ws
+
+    def _check(self, t, batch, what):
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != batch.total_tokens or \
+                t.shape[2] != self.head_dim or t.stride(2) != 1:
+            raise ValueError(f"{what}: bf16 [total_tokens][heads][head_dim] with contiguous vectors expected")
+
+    def append(self, batch: KVBatch, k, v, stream=None):
+        """Stores the new tokens' keys and values, bf16 [total_tokens][num_kv_heads][head_dim]."""
+        for t, what in ((k, "k"), (v, "v")):
+            self._check(t, batch, what)
+            if t.shape[1] != self.num_kv_heads or t.stride(1) != self.head_dim:
+                raise ValueError(f"{what}: {self.num_kv_heads} adjacent heads expected")
+        if batch.total_tokens:
+            gdn.gdn_kv_append(self.c, batch.c, k, v, stream)
+
+    def read(self, batch: KVBatch, k=None, v=None, stream=None):
+        """The batch's tokens' keys and values back as bf16 (k, v)."""
+        shape = (batch.total_tokens, self.num_kv_heads, self.head_dim)
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_pages.device)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_pages.device)
+        for t in (k, v):
+            if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
+                raise ValueError("k, v: contiguous bf16 [total_tokens][num_kv_heads][head_dim]")
+        if batch.total_tokens:
+            gdn.gdn_kv_read(self.c, batch.c, k, v, stream)
+        return k, v
+
+    def attend(self, batch: KVBatch, q, gate=None, scale=0.0, out=None, workspace=None, stream=None):
+        """Causal attention of the new tokens' queries, bf16 [total_tokens][num_q_heads][head_dim]
+        (times sigmoid(gate)), over the cache, which already holds their keys and values."""
+        self._check(q, batch, "q")
+        if gate is not None:
+            self._check(gate, batch, "gate")
+            if gate.shape != q.shape:
+                raise ValueError("gate must have the shape of q")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+            raise ValueError("out: contiguous bf16 with the shape of q")
+        if batch.total_tokens:
+            if workspace is None:
+                workspace = self.workspace(q.shape[1])
+            gdn.gdn_paged_attention(self.c, batch.c, q, out, workspace, gate, scale, stream)
+        return out

@@ -82,6 +82,7 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 #define GDN_STATUS_SLOT_RANGE 1
 #define GDN_STATUS_BAD_SEQLENS 2
 #define GDN_STATUS_TIMEOUT 4       /* a bounded device-side wait gave up; outputs are invalid */
+#define GDN_STATUS_PAGE_RANGE 8    /* a needed block_table entry outside [0, num_pages)       */
 
 /* Rank-local layer geometry ("local_linear_*" head counts of one tensor-parallel rank; one
  * GPU holds them all here).  q_scale = 0 selects 1/sqrt(head_k_dim).  l2norm divides by
@@ -336,6 +337,119 @@ int gdn_in_proj(const gdn_dims* dims, const void* hidden, const void* w_in_packe
  * library's k_split. */
 int gdn_out_proj(const gdn_dims* dims, const void* out, const void* w_out_packed, int32_t rows,
                  int32_t hidden_size, void* y, int32_t* status, cudaStream_t stream);
+
+/* ---- The full-attention layers of the hybrid models -----------------------------------------
+ * The layers between the linear-attention ones: the residual RMSNorm that every layer is entered
+ * through, a paged key/value cache (bf16, or 8-bit with a scale per vector), and attention of the
+ * sequences' new tokens over it.  The calls keep the conventions above: the caller owns every
+ * buffer, nothing is allocated, no device data is read on the host (so each call can be captured
+ * in a CUDA graph), and the kernels are programmatic dependents of the previous kernel. */
+
+/* What gdn_rms_norm writes to y. */
+typedef enum {
+  GDN_NORM_ACT = 0,        /* y in the activation dtype                                        */
+  GDN_NORM_E4M3_ROW = 1,   /* y in 8-bit e4m3 with one f32 scale per row: scales [rows]        */
+  GDN_NORM_E4M3_BLOCK = 2  /* the same with one per 128 columns: scales [rows][ceil(n/128)]    */
+} gdn_norm_out;
+
+/* Largest row width of gdn_rms_norm. */
+#define GDN_MAX_NORM_WIDTH 32768
+
+/* RMSNorm with the residual's addition, for `rows` rows of n elements (1 <= n <=
+ * GDN_MAX_NORM_WIDTH, GDN_ERR_TOO_LARGE above):
+ *   h = x + residual (f32; residual may be NULL: h = x),  sum_out = h in the activation dtype,
+ *   y = h / sqrt(mean h^2 + eps) * (weight_offset + weight).
+ * weight_offset is 1 for zero-centred weights, else 0.  The norm is taken of the unrounded f32 h.
+ * 8-bit outputs: over each row (or each 128 columns of a row, the last group possibly shorter)
+ *   scale = max(max|y| / 448, 2^-120),  y8 = e4m3(y / scale) (nearest, ties to even);
+ * a group that holds a NaN gets a NaN scale and NaN codes.
+ *   x, residual, weight: activation dtype, rows x_ld / residual_ld elements apart (>= n); sum_out
+ *   (NULL: not written; it may be the same buffer as residual or x, with equal row distance n) and
+ *   y dense [rows][n]; scales f32, NULL for GDN_NORM_ACT.  Any n and any row distance is accepted;
+ *   bases are 16-byte aligned, and rows whose starts all are (n, x_ld, residual_ld multiples of 16
+ *   bytes) move in 16-byte vectors.  rows = 0 is a no-op.  One kernel launch. */
+int gdn_rms_norm(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld,
+                 const void* weight, float weight_offset, float eps, int32_t rows, int32_t n,
+                 gdn_dtype act, gdn_norm_out out_kind, void* sum_out, void* y, float* scales,
+                 cudaStream_t stream);
+
+typedef enum { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1 } gdn_kv_type;
+
+/* A paged key/value cache.  k_pages, v_pages: [num_pages][num_kv_heads][page_size][head_dim], bf16
+ * or e4m3; k_scales, v_scales (GDN_KV_E4M3 only, else NULL): uint8
+ * [num_pages][num_kv_heads][page_size], the exponent byte b of each vector's scale 2^(b - 127)
+ * (255: the vector reads as NaN).  head_dim in {64, 128, 256}; page_size in {16, 32, 64, 128, 256};
+ * bases 16-byte aligned.  status: optional device int32 error word. */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  gdn_kv_type type;
+  int32_t* status;
+} gdn_kv_cache;
+
+/* The new tokens of one call (device arrays, any alignment of their element type).  Sequence n has
+ * T_n = cu_seqlens[n+1] - cu_seqlens[n] new tokens, packed rows [cu_seqlens[n], cu_seqlens[n+1]) of
+ * the call's token buffers, and kv_lens[n] cached positions including them: its token i sits at
+ * position p = kv_lens[n] - T_n + i, in page block_table[n * table_ld + p / page_size].  cu_seqlens
+ * int32[num_seqs + 1] non-decreasing from 0; rows in [cu_seqlens[num_seqs], total_tokens) are
+ * padding; max_tokens >= every T_n (host bound; 0: unknown).  A token whose position is negative
+ * (kv_lens[n] < T_n) has no place: it is not stored, reads as zero, and attends to nothing.
+ * Entries of block_table past the sequence's pages are never read.  A sequence with kv_lens[n]
+ * outside [0, table_ld * page_size] or an inconsistent cu_seqlens sets GDN_STATUS_BAD_SEQLENS and
+ * is treated as having no cached positions; a needed page outside [0, num_pages) sets
+ * GDN_STATUS_PAGE_RANGE, is not written, and its keys and values read as zero.  num_seqs <= 65535. */
+typedef struct {
+  const int32_t* cu_seqlens;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  int32_t num_seqs;
+  int32_t total_tokens;
+  int32_t table_ld;
+  int32_t max_tokens;
+} gdn_kv_batch;
+
+/* Writes the new tokens' keys and values into their places.  k, v: bf16
+ * [total_tokens][num_kv_heads][head_dim], rows k_ld / v_ld elements apart (multiples of 8, >=
+ * num_kv_heads * head_dim), 16-byte aligned.  GDN_KV_E4M3: each vector of head_dim elements gets
+ * the least power of two 2^(b - 127), b >= 10, with max|x| <= 448 * 2^(b - 127) (b = 127 for a zero
+ * vector), and holds e4m3(x / 2^(b - 127)), nearest, ties to even; a vector with an infinity or a
+ * NaN gets b = 255 and reads as NaN throughout.  Places must be distinct.  One kernel launch. */
+int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_batch* batch, const void* k, int64_t k_ld,
+                  const void* v, int64_t v_ld, cudaStream_t stream);
+
+/* The inverse: reads the places of the same tokens back into dense bf16
+ * [total_tokens][num_kv_heads][head_dim] (exact: an 8-bit value times its power of two is a bf16
+ * value).  With cu_seqlens the prefix sums of kv_lens it returns whole sequences.  Padding tokens
+ * and tokens without a place read as zero.  One kernel launch. */
+int gdn_kv_read(const gdn_kv_cache* cache, const gdn_kv_batch* batch, void* k, void* v,
+                cudaStream_t stream);
+
+/* Bytes of workspace gdn_paged_attention needs for this cache and number of query heads (whatever
+ * the batch): partial results of the work split along the cache.  0 for unsupported geometry. */
+size_t gdn_paged_attention_workspace_bytes(const gdn_kv_cache* cache, int32_t num_q_heads);
+
+/* Causal attention of every new token over its sequence's cache (which holds the new tokens
+ * themselves: append first).  Query head h reads key/value head h / (num_q_heads / num_kv_heads):
+ *   o = softmax_j(scale q . k_j) v_j over the positions j <= p of the token,
+ * then, with a gate, o * sigmoid(gate); one rounding to bf16.  A token that sees no position gets
+ * zero.  Keys and values at positions a token does not see have no influence, whatever they hold.
+ *   q, gate (NULL: none): bf16, element (t, h, d) at t * ld + h * head_ld + d; ld and head_ld
+ *   multiples of 8, 16-byte aligned -- a projection's [q | gate] per head is read in place.
+ *   scale: 0 selects 1/sqrt(head_dim).  out: bf16 [total_tokens][num_q_heads][head_dim], dense.
+ *   num_q_heads % num_kv_heads == 0 (GDN_ERR_HEAD_DIVISIBILITY); total_tokens * num_q_heads <=
+ *   2^30 (GDN_ERR_TOO_LARGE).  workspace: device, 256-byte aligned, contents undefined on entry
+ *   and exit.  Results do not depend on the workspace's contents and are bitwise reproducible.
+ * Two kernel launches. */
+int gdn_paged_attention(const gdn_kv_cache* cache, const gdn_kv_batch* batch, int32_t num_q_heads,
+                        const void* q, int64_t q_ld, int64_t q_head_ld, const void* gate,
+                        int64_t gate_ld, int64_t gate_head_ld, float scale, void* out,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Text for a return code. */
 const char* gdn_status_string(int code);
