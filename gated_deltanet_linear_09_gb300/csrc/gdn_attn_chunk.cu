@@ -1,0 +1,655 @@
+// gdn_attn_chunk.cu -- attention of runs of new tokens (prompts, chunks of prompts) over the paged
+// cache, on the tcgen05 tensor cores.
+//
+//   S = Q K^T,   P = 2^(scale log2(e) S - m),   O += P V,   o = O / l,   l = sum P
+//
+// in one pass over 128-key tiles.  A CTA holds a tile of query rows (row = new token x head of the
+// key/value head's group): two blocks of 128 rows for head dims up to 128, one for 256.  S and O
+// live in TMEM (256 + 2 D columns, or 2 x 128 + 256), P replaces S in place as the TMEM operand of
+// the second product.
+//
+// What bounds it: 4 D flops per (row, key) on the tensor pipe and one exponential per (row, key)
+// on the special-function units, of which D = 128 takes about as long for both; so neither may
+// wait for the other:
+//  * a softmax warpgroup per block of rows (a thread owns a row: no shuffles), one warp issuing
+//    MMAs, one warp issuing TMA copies, for 8-bit caches four more that turn e4m3 tiles into bf16
+//    operands;
+//  * the MMA order PV_0(i), QK_0(i+1), PV_1(i), QK_1(i+1) keeps the pipe on one block while the
+//    other block's softmax runs (D = 256: two S buffers, PV(i), QK(i+2));
+//  * the reference m follows the running maximum only when that outgrows it by 2^8, so O is almost
+//    never rescaled, and never by a warpgroup of its own;
+//  * the next tile's queries are loaded, and its first product issued, before the last tile's
+//    output leaves.
+// Values whose key some rows do not see must be finite for the product to leave those rows alone:
+// in tiles that the causal edge crosses, the first warpgroup replaces non-finite ones (and
+// whatever lies past the sequence's end) by zero, and notes column and position, so that the rows
+// that do see them get their NaN.
+#include "gdn_attn.cuh"
+#include "gdn_tmap.h"
+
+namespace gdn {
+
+using namespace tc;
+
+namespace attn {
+
+constexpr int kKeys = 128;         // keys of a tile
+
+template <int D, bool Q8>
+struct ChunkCfg {
+  static constexpr int kBlocks = D == 256 ? 1 : 2;          // 128-row query blocks
+  static constexpr int kSBufs = D == 256 ? 2 : 1;           // S buffers per block
+  static constexpr int kRows = 128 * kBlocks;
+  static constexpr int kCols = D == 64 ? 64 : 128;          // columns of a ring stage
+  static constexpr int kHalves = D / kCols;                 // stages of a K or V tile
+  static constexpr int kStageBytes = kKeys * kCols * 2;
+  static constexpr int kStages = D == 64 ? (Q8 ? 4 : 8) : (Q8 ? 3 : 5);
+  static constexpr int kRawBytes = kKeys * kCols;
+  static constexpr int kRawStages = Q8 ? 3 : 0;
+  static constexpr int kSoftWarps = 4 * kBlocks;
+  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kConvWarp = kSoftWarps + 2;
+  static constexpr int kThreads = (kSoftWarps + 2 + (Q8 ? 4 : 0)) * 32;
+  static constexpr int kQBytes = 128 * D * 2;               // one block
+  static constexpr int kO = 256;                            // TMEM column of O (block b: + b D)
+};
+
+template <int D, bool Q8>
+struct __align__(1024) ChunkSmem {
+  using C = ChunkCfg<D, Q8>;
+  uint8_t q[C::kBlocks][C::kQBytes];
+  uint8_t ring[C::kStages][C::kStageBytes];
+  uint8_t raw[Q8 ? C::kRawStages : 1][Q8 ? C::kRawBytes : 16];
+  uint8_t scales[Q8 ? C::kRawStages : 1][8][Q8 ? 128 : 16];
+  LineScan<C::kRows, C::kThreads> scan;
+  int bad[D];                       // first position with a non-finite value, per column
+  int any_bad;
+  uint32_t tmem;
+  int dead;
+  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t raw_full[Q8 ? C::kRawStages : 1], raw_empty[Q8 ? C::kRawStages : 1];
+  uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2];
+  uint64_t v_ready;                 // the current tile's values are in the ring
+};
+
+// K-major 128-byte-swizzled operand tile: 8-row groups 1,024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return sdesc(saddr, lbo, sbo) | (2ull << 61);
+}
+
+// A bounded wait of a whole warp: a timeout marks the CTA dead, after which no wait blocks and the
+// (wrong) results are flagged by the status bit.
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
+  if (!mbar_try_wait(bar, parity) && !*dead && !mbar_wait(bar, parity)) {
+    *dead = 1;
+    set_status(status, GDN_STATUS_TIMEOUT);
+  }
+  __syncwarp();
+}
+
+// Barrier over n threads that returns whether any of them passed true.
+__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbarrier.cta.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  tmem_ld16_nw(addr, r);
+  tmem_ld16_nw(addr + 16, r + 16);
+  tmem_wait_ld();
+  reg_fence16(r);
+  reg_fence16(r + 16);
+}
+
+// Position of a stage in the ring.
+template <int N>
+struct RingPos {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++stage == N) { stage = 0; phase ^= 1u; }
+  }
+};
+
+// The ring's order within a segment of n tiles: K0, K1, V0, K2, V1, ... (each kHalves stages).
+// Calls f(is_v, tile index from 0, half).
+template <int HALVES, typename F>
+__device__ __forceinline__ void ring_order(int n, F f) {
+  for (int h = 0; h < HALVES; ++h) f(false, 0, h);
+  for (int i = 0; i < n; ++i) {
+    if (i + 1 < n)
+      for (int h = 0; h < HALVES; ++h) f(false, i + 1, h);
+    for (int h = 0; h < HALVES; ++h) f(true, i, h);
+  }
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1)
+chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, long long least,
+             const __grid_constant__ KvMaps maps) {
+  using C = ChunkCfg<D, Q8>;
+  constexpr int R = C::kRows, TK = kKeys;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  ChunkSmem<D, Q8>& sm = *reinterpret_cast<ChunkSmem<D, Q8>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sm.full[i], Q8 ? 4 : 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    if (Q8)
+      for (int i = 0; i < C::kRawStages; ++i) {
+        mbar_init(&sm.raw_full[i], 1);
+        mbar_init(&sm.raw_empty[i], 4);
+      }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_ready[i], 4);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_ready[i], 4);
+      mbar_init(&sm.o_done[i], 1);
+    }
+    mbar_init(&sm.v_ready, 1);
+    sm.dead = 0;
+    sm.any_bad = 0;
+    mbar_fence_init();
+  }
+  for (int i = tid; i < D; i += C::kThreads) sm.bad[i] = INT32_MAX;
+  pdl_begin();
+  zero_padding(a, b, D);
+  bool bad_len = false;
+  int pieces;
+  const int cta = blockIdx.x;
+  locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad_len);
+  if (bad_len) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
+  if (cta >= pieces) return;
+  if (warp == C::kMmaWarp) tmem_alloc(&sm.tmem, 512);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  SegIter<R, TK> it;
+  {
+    const long long x0 = piece_bound(sm.scan.total, pieces, cta);
+    it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
+             piece_bound(sm.scan.total, pieces, cta + 1) - x0);
+  }
+  Segment sg;
+
+  if (warp == C::kLoadWarp) {
+    // ---------------------------------------------------------------- TMA
+    const int box = min(1 << c.page_shift, TK);            // keys of one copy
+    constexpr int kBoxCols = Q8 ? C::kCols : 64;
+    constexpr int kBlk = C::kCols / kBoxCols;
+    const int pages = TK / box;                             // 1 to 8
+    RingPos<Q8 ? C::kRawStages : C::kStages> pos;
+    uint64_t* full = Q8 ? sm.raw_full : sm.full;
+    uint64_t* empty = Q8 ? sm.raw_empty : sm.empty;
+    const int my_page = lane / kBlk, my_blk = lane % kBlk;
+    while (it.next(&sg)) {
+      const int n = sg.tb - sg.ta;
+      if (n <= 0) continue;
+      const int* table = b.table + (long long)sg.seq * b.table_ld;
+      const int len = sg.info.len;
+      auto lookup = [&](int i) {                            // this lane's page of tile i
+        const int k = (sg.ta + i) * TK + my_page * box;
+        if (i >= n || my_page >= pages || k >= len) return c.num_pages;   // zeros
+        int p = __ldg(table + (k >> c.page_shift));
+        if (p < 0 || p >= c.num_pages) {
+          set_status(c.status, GDN_STATUS_PAGE_RANGE);
+          p = c.num_pages;
+        }
+        return p;
+      };
+      int p_cur = 0, p_next = lookup(0), p_ahead = lookup(1);   // pages of tiles i, i + 1, i + 2
+      ring_order<C::kHalves>(n, [&](bool is_v, int i, int half) {
+        if (!is_v && half == 0 && i > 0) {
+          p_cur = p_next;
+          p_next = p_ahead;
+          p_ahead = lookup(i + 1);
+        }
+        // K tiles run one ahead of V tiles; after the last K tile V is the newest tile
+        const int page = !is_v ? p_next : (i + 1 < n ? p_cur : p_next);
+        wait_bar(&empty[pos.stage], pos.phase ^ 1u, &sm.dead, c.status);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[pos.stage],
+                                Q8 ? (half == 0 ? C::kRawBytes + TK : C::kRawBytes) : C::kStageBytes);
+        __syncwarp();
+        if (my_page < pages) {
+          const int off = (((sg.ta + i) * TK) & ((1 << c.page_shift) - 1));   // 0 unless pages exceed a tile
+          if constexpr (Q8) {
+            tma_load_5d(sm.raw[pos.stage] + my_page * box * C::kCols, is_v ? &maps.v : &maps.k, 0, off,
+                        half, sg.head, page, &full[pos.stage]);
+            if (half == 0)
+              tma_load_3d(sm.scales[pos.stage][my_page], is_v ? &maps.vs : &maps.ks, off, sg.head, page,
+                          &full[pos.stage]);
+          } else {
+            tma_load_5d(sm.ring[pos.stage] + my_blk * (TK * 128) + my_page * box * 128, is_v ? &maps.v : &maps.k, 0,
+                        off, half * kBlk + my_blk, sg.head, page, &full[pos.stage]);
+          }
+        }
+        __syncwarp();
+        pos.step();
+      });
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ---------------------------------------------------------------- MMA
+    RingPos<C::kStages> pos;
+    uint32_t cnt[2] = {0, 0};          // tiles issued per block
+    uint32_t s_cnt = 0;                // S buffers issued (one block)
+    uint32_t q_phase[2] = {0, 0};
+    constexpr uint32_t kIdQK = idesc_bf16(128, 128);
+    constexpr uint32_t kIdPV = idesc_bf16_bmn(128, C::kCols);
+    const uint32_t ring = smem_u32(sm.ring[0]);
+    while (it.next(&sg)) {
+      const int n = sg.tb - sg.ta;
+      if (n <= 0) continue;
+      const int rows = (int)min((long long)R, (long long)sg.info.tokens * a.g - (long long)sg.tile * R);
+      const int blocks = rows > 128 ? 2 : 1;
+      auto qk_half = [&](int blk, int buf, uint32_t kaddr, int half) {
+        if (lane == 0) {
+          const uint64_t qd = desc_sw128(smem_u32(sm.q[blk]) + half * (C::kCols / 64) * (128 * 128), 16, 1024);
+          const uint64_t kd = desc_sw128(kaddr, 16, 1024);
+#pragma unroll
+          for (int ks = 0; ks < C::kCols / 16; ++ks) {
+            const uint32_t o = (uint32_t)(ks >> 2) * (128 * 128) + (uint32_t)(ks & 3) * 32;
+            mma_bf16(tmem + buf * 128, desc_add(qd, o), desc_add(kd, o), kIdQK, half > 0 || ks > 0);
+          }
+        }
+        __syncwarp();
+      };
+      auto pv_half = [&](int blk, int buf, uint32_t vaddr, int half, bool acc) {
+        if (lane == 0) {
+          const uint64_t vd = desc_sw128(vaddr, 128 * 128, 1024);
+          const uint32_t o = tmem + C::kO + blk * D + half * C::kCols;
+#pragma unroll
+          for (int ks = 0; ks < TK / 16; ++ks)
+            mma_bf16_tmem_a(o, tmem + buf * 128 + ks * 8, desc_add(vd, ks * 2048), kIdPV, acc || ks > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (lane == 0) mma_commit(bar);
+        __syncwarp();
+      };
+      for (int blk = 0; blk < blocks; ++blk) {
+        wait_bar(&sm.q_ready[blk], q_phase[blk], &sm.dead, c.status);
+        q_phase[blk] ^= 1u;
+      }
+      fence_after_sync();
+      if constexpr (C::kBlocks == 2) {
+        wait_bar(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
+        fence_after_sync();
+        for (int blk = 0; blk < blocks; ++blk) {
+          qk_half(blk, blk, ring + pos.stage * C::kStageBytes, 0);
+          commit(&sm.s_full[blk]);
+        }
+        commit(&sm.empty[pos.stage]);
+        pos.step();
+        for (int i = 0; i < n; ++i) {
+          RingPos<C::kStages> kpos = pos;
+          const bool more = i + 1 < n;
+          if (more) pos.step();
+          const RingPos<C::kStages> vpos = pos;
+          pos.step();
+          wait_bar(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
+          if (lane == 0) mbar_arrive(&sm.v_ready);
+          if (more) wait_bar(&sm.full[kpos.stage], kpos.phase, &sm.dead, c.status);
+          for (int blk = 0; blk < blocks; ++blk) {
+            wait_bar(&sm.p_ready[blk], cnt[blk] & 1u, &sm.dead, c.status);
+            ++cnt[blk];
+            fence_after_sync();
+            pv_half(blk, blk, ring + vpos.stage * C::kStageBytes, 0, i > 0);
+            commit(&sm.o_done[blk]);
+            if (blk == blocks - 1) commit(&sm.empty[vpos.stage]);
+            if (more) {
+              qk_half(blk, blk, ring + kpos.stage * C::kStageBytes, 0);
+              commit(&sm.s_full[blk]);
+              if (blk == blocks - 1) commit(&sm.empty[kpos.stage]);
+            }
+          }
+        }
+      } else {
+        auto qk_tile = [&]() {
+          const int buf = (int)(s_cnt & 1u);
+          for (int h = 0; h < C::kHalves; ++h) {
+            wait_bar(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
+            fence_after_sync();
+            qk_half(0, buf, ring + pos.stage * C::kStageBytes, h);
+            commit(&sm.empty[pos.stage]);
+            pos.step();
+          }
+          commit(&sm.s_full[buf]);
+          ++s_cnt;
+        };
+        qk_tile();
+        if (n > 1) qk_tile();
+        for (int i = 0; i < n; ++i) {
+          const int buf = (int)(cnt[0] & 1u);
+          RingPos<C::kStages> vpos = pos;
+          for (int h = 0; h < C::kHalves; ++h, vpos.step())
+            wait_bar(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
+          if (lane == 0) mbar_arrive(&sm.v_ready);
+          wait_bar(&sm.p_ready[0], cnt[0] & 1u, &sm.dead, c.status);
+          ++cnt[0];
+          fence_after_sync();
+          for (int h = 0; h < C::kHalves; ++h) {
+            pv_half(0, buf, ring + pos.stage * C::kStageBytes, h, i > 0);
+            commit(&sm.empty[pos.stage]);
+            pos.step();
+          }
+          commit(&sm.o_done[0]);
+          if (i + 2 < n) qk_tile();
+        }
+      }
+    }
+  } else if (Q8 && warp >= C::kConvWarp) {
+    // ---------------------------------------------------------------- e4m3 -> bf16
+    const int ct = tid - C::kConvWarp * 32;
+    const int box = min(1 << c.page_shift, TK), shift = 31 - __clz(box);
+    RingPos<C::kRawStages ? C::kRawStages : 1> src;
+    RingPos<C::kStages> dst;
+    constexpr int kPer = C::kCols / 8;                      // 8-element pieces of a row
+    const int piece = ct % kPer;
+    while (it.next(&sg)) {
+      const int n = sg.tb - sg.ta;
+      if (n <= 0) continue;
+      uint32_t byte[128 * kPer / 128] = {};                  // scale bytes of this thread's rows
+      ring_order<C::kHalves>(n, [&](bool, int, int half) {
+        wait_bar(&sm.raw_full[src.stage], src.phase, &sm.dead, c.status);
+        wait_bar(&sm.empty[dst.stage], dst.phase ^ 1u, &sm.dead, c.status);
+        const uint8_t* raw = sm.raw[src.stage];
+        uint8_t* out = sm.ring[dst.stage];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int row = j * (128 / kPer) + ct / kPer;
+          // a tile's scale bytes come with its first half
+          if (half == 0) byte[j] = sm.scales[src.stage][row >> shift][row & (box - 1)];
+          const uint2 u = *reinterpret_cast<const uint2*>(raw + row * C::kCols + piece * 8);
+          uint32_t w[4];
+          e4m3x4_to_bf16(u.x, w[0], w[1]);
+          e4m3x4_to_bf16(u.y, w[2], w[3]);
+          const uint32_t s = scale_bits(byte[j]), s2 = s | (s << 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = mul_bf16x2(w[e], s2);
+          *reinterpret_cast<uint4*>(out + (piece >> 3) * (TK * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.full[dst.stage]);
+          mbar_arrive(&sm.raw_empty[src.stage]);
+        }
+        src.step();
+        dst.step();
+      });
+    }
+  } else if (warp < C::kSoftWarps) {
+    // ---------------------------------------------------------------- softmax and output
+    const int blk = warp >> 2, r = tid & 127, lbase = (warp & 3) * 32;
+    const uint32_t tl = tmem + ((uint32_t)lbase << 16);
+    uint32_t cnt = 0;                  // tiles of this block so far
+    RingPos<C::kStages> ring;          // first stage of the current segment (block 0 only)
+    auto load_q = [&](const Segment& s) {
+      // thread groups of D / 8 lanes take a row at a time: 16-byte pieces, swizzled
+      const int rows = (int)min((long long)R, (long long)s.info.tokens * a.g - (long long)s.tile * R) - blk * 128;
+      constexpr int kPer = D / 8;
+      const int piece = r % kPer;
+      for (int row = r / kPer; row < 128; row += 128 / kPer) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < rows) {
+          int tok, head;
+          row_of(s.info, a.g, s.head, s.tile * R + blk * 128 + row, &tok, &head);
+          v = __ldg(reinterpret_cast<const uint4*>(a.q + tok * a.q_ld + head * a.q_head_ld + piece * 8));
+        }
+        *reinterpret_cast<uint4*>(sm.q[blk] + (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_ready[blk]);
+    };
+    auto active = [&](const Segment& s) {
+      return s.tb > s.ta && (blk == 0 || (long long)s.info.tokens * a.g - (long long)s.tile * R > 128);
+    };
+    bool have = it.next(&sg);
+    if (have && active(sg)) load_q(sg);
+    while (have) {
+      const Segment cur = sg;
+      const SeqInfo info = cur.info;
+      const int rows = (int)min((long long)R, (long long)info.tokens * a.g - (long long)cur.tile * R);
+      const int n = cur.tb - cur.ta;
+      const int row = cur.tile * R + blk * 128 + r;              // this thread's row
+      const bool live = blk * 128 + r < rows;
+      const int before = info.len - info.tokens;
+      if (!active(cur)) {
+        if (cur.owns_empty && live) {
+          int tok, head;
+          row_of(info, a.g, cur.head, row, &tok, &head);
+          uint4* o = reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D);
+          for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+        }
+        have = it.next(&sg);
+        if (have && active(sg)) load_q(sg);
+      } else {
+        const int last_row = info.tokens * a.g - 1;
+        const int pos = before + min(row, last_row) / a.g;
+        const int pos_min = before + min(cur.tile * R + blk * 128, last_row) / a.g;
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < n; ++i, ++cnt) {
+          const int buf = C::kBlocks == 2 ? blk : (int)(cnt & 1u);
+          wait_bar(&sm.s_full[buf], (C::kBlocks == 2 ? cnt : cnt >> 1) & 1u, &sm.dead, c.status);
+          fence_after_sync();
+          const uint32_t s_addr = tl + buf * 128;
+          const int k0 = (cur.ta + i) * TK;
+          const bool partial = k0 + TK - 1 > pos_min;
+          const int lim = pos - k0;                               // columns 0..lim are seen
+          float x = -INFINITY;
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t v[32];
+            tmem_ld32(s_addr + cc * 32, v);
+            if (partial) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (cc * 32 + e > lim) v[e] = 0xff800000u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x = fmaxf(x, __uint_as_float(v[e]));
+          }
+          x *= a.scale_log2;
+          if (__any_sync(0xffffffffu, x > m + 8.f)) {
+            const float mn = fmaxf(m, x);
+            const float f = mn == m ? 1.f : ex2f(m - mn);
+            m = mn;
+            l *= f;
+            if (i > 0) {
+              wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
+              fence_after_sync();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 16) {
+                float o[16];
+                tmem_ld16(tl + C::kO + blk * D + d, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tmem_st16_nw(tl + C::kO + blk * D + d, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t v[32];
+            tmem_ld32(s_addr + cc * 32, v);
+            if (partial) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (cc * 32 + e > lim) v[e] = 0xff800000u;
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ex2f(fmaf(__uint_as_float(v[2 * e]), a.scale_log2, -ref));
+              const float p1 = ex2f(fmaf(__uint_as_float(v[2 * e + 1]), a.scale_log2, -ref));
+              l0 += p0;
+              l1 += p1;
+              w[e] = pack2(p0, p1);
+            }
+            tmem_st16w_nw(s_addr + cc * 16, w);
+          }
+          l += l0 + l1;
+          // A parity wait tells a phase from the one before it only when no phase is skipped: so
+          // v_ready is waited for at every tile (the ring's own barriers, which K tiles use too,
+          // would not do), and so is o_done where s_full does not imply the product before.
+          if (blk == 0) wait_bar(&sm.v_ready, cnt & 1u, &sm.dead, c.status);
+          if (C::kBlocks == 1 && i > 0) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
+          if (partial && blk == 0) {
+            // this tile's values: zero past the end, zero and noted where not finite
+            RingPos<C::kStages> vp = ring;
+            const int ahead = C::kHalves * (min(i + 2, n) + i);
+            vp.phase ^= (uint32_t)((vp.stage + ahead) / C::kStages) & 1u;
+            vp.stage = (vp.stage + ahead) % C::kStages;
+            for (int h = 0; h < C::kHalves; ++h, vp.step()) {
+              // keys from the first row's position on (earlier ones are seen by all rows)
+              const int j0 = max(0, pos_min + 1 - k0), j1 = TK;
+              constexpr int kPer = C::kCols / 8;
+              const int piece = r % kPer;
+              for (int j = j0 + r / kPer; j < j1; j += 128 / kPer) {
+                uint4* p = reinterpret_cast<uint4*>(sm.ring[vp.stage] + (piece >> 3) * (TK * 128) + j * 128 +
+                                                    (((piece & 7) ^ (j & 7)) << 4));
+                if (k0 + j >= info.len) {
+                  *p = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                const uint4 u = *p;
+                uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint32_t hit = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) hit |= ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                if (hit) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    if (((w[e >> 1] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
+                      w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                      atomicMin(&sm.bad[h * C::kCols + piece * 8 + e], k0 + j);
+                    }
+                  sm.any_bad = 1;
+                  *p = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          tmem_wait_st();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_ready[blk]);
+        }
+        // the next tile's queries, before this one's output: every QK of this one has completed
+        have = it.next(&sg);
+        if (have && active(sg)) load_q(sg);
+        wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
+        fence_after_sync();
+        const bool whole = cur.whole(), bad = *(volatile int*)&sm.any_bad != 0;
+        int tok = 0, head = 0;
+        if (live) row_of(info, a.g, cur.head, row, &tok, &head);
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+        const int pr = blk * 128 + r;
+        float* prow = Partials<R, D>::rows(a.ws, cta, cur.slot) + (size_t)pr * D;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 16) {
+          float o[16];
+          tmem_ld16(tl + C::kO + blk * D + d, o);
+          if (live) {
+            if (bad) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (sm.bad[d + e] <= pos) o[e] = __int_as_float(0x7fffffff);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 v = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+              if (whole) store_out4(a, D, tok, head, d + e, v);
+              else __stcg(reinterpret_cast<float4*>(prow + d + e), v);
+            }
+          }
+          __syncwarp();
+        }
+        if (!whole && live) {
+          // a NaN sum must survive the merge even when its reference never left -infinity
+          __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, cur.slot) + 2 * pr),
+                 make_float2(l != l ? INFINITY : m, l));
+        }
+        fence_before_sync();           // O has been read before the next tile's p_ready
+      }
+      if (n > 0) {
+        const int ahead = 2 * n * C::kHalves;
+        ring.phase ^= (uint32_t)((ring.stage + ahead) / C::kStages) & 1u;
+        ring.stage = (ring.stage + ahead) % C::kStages;
+      }
+      // both blocks are done with the notes on non-finite values
+      if (bar_any(1, C::kSoftWarps * 32, *(volatile int*)&sm.any_bad != 0)) {
+        for (int i = tid; i < D; i += C::kSoftWarps * 32) sm.bad[i] = INT32_MAX;
+        if (tid == 0) sm.any_bad = 0;
+        asm volatile("bar.sync 1, %0;\n" ::"n"(C::kSoftWarps * 32) : "memory");
+      }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool Q8>
+int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
+  using C = ChunkCfg<D, Q8>;
+  constexpr size_t smem = sizeof(ChunkSmem<D, Q8>);
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  static const cudaError_t set = cudaFuncSetAttribute(
+      chunk_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (set != cudaSuccess) return GDN_ERR_CUDA;
+  KvMaps maps;
+  const int P = 1 << c.page_shift;
+  if (!make_tile_maps(c, P < kKeys ? P : kKeys, Q8 ? C::kCols : 64, !Q8, &maps)) return GDN_ERR_CUDA;
+  const int grid = sms, fix = 128 * a.g;
+  const long long least = 512LL * a.g;
+  int rc = launch_dependent(chunk_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
+                            fix, least, maps);
+  if (rc != GDN_OK) return rc;
+  return launch_dependent(merge_kernel<C::kRows, kKeys, D>, dim3((unsigned)(grid - 1), 16), 256, 0, stream, c, b, a,
+                          grid, fix, least);
+}
+
+size_t chunk_ws_bytes(int D, int sms) {
+  return D == 64 ? Partials<ChunkCfg<64, false>::kRows, 64>::bytes(sms)
+       : D == 128 ? Partials<ChunkCfg<128, false>::kRows, 128>::bytes(sms)
+                  : Partials<ChunkCfg<256, false>::kRows, 256>::bytes(sms);
+}
+
+int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
+  const bool q8 = c.ks != nullptr;
+  if (c.D == 64) return q8 ? launch_chunk<64, true>(c, b, a, sms, stream) : launch_chunk<64, false>(c, b, a, sms, stream);
+  if (c.D == 128) return q8 ? launch_chunk<128, true>(c, b, a, sms, stream) : launch_chunk<128, false>(c, b, a, sms, stream);
+  return q8 ? launch_chunk<256, true>(c, b, a, sms, stream) : launch_chunk<256, false>(c, b, a, sms, stream);
+}
+
+}  // namespace attn
+}  // namespace gdn

@@ -44,7 +44,8 @@ struct RowsCfg {
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRing = kCtas == 1 ? 196608 : 98304;
   static constexpr int kFit = kRing / (kStageBytes + (Q8 ? 1024 : 0));   // with the scale bytes
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  // a multiple of the teams: a stage is always the same team's, which waits for each of its phases
+  static constexpr int kStages = (kFit > 8 ? 8 : kFit) / kTeams * kTeams;
   static constexpr int kBox = D * kElem >= 128 ? 128 : 64;       // swizzle span, bytes
   static constexpr int kLd = D + 8;                              // merge buffer row
 };

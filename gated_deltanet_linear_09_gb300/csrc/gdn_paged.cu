@@ -37,19 +37,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-}  // namespace
-
-bool make_kv_maps(const KvView& c, int rows, KvMaps* maps) {
-  const auto encode = encode_fn();
-  if (!encode) return false;
+// The maps of keys and values (same geometry) and of an 8-bit cache's scale bytes.
+bool encode_all(const KvView& c, PFN_cuTensorMapEncodeTiled_v12000 encode, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box, int rows, CUtensorMapSwizzle swizzle, KvMaps* maps) {
   const bool q8 = c.ks != nullptr;
-  const uint64_t elem = q8 ? 1 : 2, row = c.D * elem, span = row < 128 ? row : 128;
   const uint64_t P = 1ull << c.page_shift;
-  const cuuint64_t dims[5] = {span / elem, P, row / span, (cuuint64_t)c.H, (cuuint64_t)c.num_pages};
-  const cuuint64_t strides[4] = {row, span, P * row, c.H * P * row};
-  const cuuint32_t box[5] = {(cuuint32_t)(span / elem), (cuuint32_t)rows, (cuuint32_t)(row / span), 1, 1};
   const cuuint32_t one[5] = {1, 1, 1, 1, 1};
-  const CUtensorMapSwizzle swizzle = span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   for (int i = 0; i < 2; ++i)
     if (encode(i ? &maps->v : &maps->k, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
                i ? c.v : c.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
@@ -71,16 +64,49 @@ bool make_kv_maps(const KvView& c, int rows, KvMaps* maps) {
   return true;
 }
 
+}  // namespace
+
+bool make_tile_maps(const KvView& c, int rows, int cols, bool swizzled, KvMaps* maps) {
+  const auto encode = encode_fn();
+  if (!encode) return false;
+  const bool q8 = c.ks != nullptr;
+  const uint64_t elem = q8 ? 1 : 2, row = c.D * elem, span = cols * elem;
+  const uint64_t P = 1ull << c.page_shift;
+  const cuuint64_t dims[5] = {(cuuint64_t)cols, P, row / span, (cuuint64_t)c.H, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[4] = {row, span, P * row, c.H * P * row};
+  const cuuint32_t box[5] = {(cuuint32_t)cols, (cuuint32_t)rows, 1, 1, 1};
+  return encode_all(c, encode, dims, strides, box, rows,
+                    !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE
+                              : span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    maps);
+}
+
+bool make_kv_maps(const KvView& c, int rows, KvMaps* maps) {
+  const auto encode = encode_fn();
+  if (!encode) return false;
+  const bool q8 = c.ks != nullptr;
+  const uint64_t elem = q8 ? 1 : 2, row = c.D * elem, span = row < 128 ? row : 128;
+  const uint64_t P = 1ull << c.page_shift;
+  const cuuint64_t dims[5] = {span / elem, P, row / span, (cuuint64_t)c.H, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[4] = {row, span, P * row, c.H * P * row};
+  const cuuint32_t box[5] = {(cuuint32_t)(span / elem), (cuuint32_t)rows, (cuuint32_t)(row / span), 1, 1};
+  return encode_all(c, encode, dims, strides, box, rows,
+                    span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, maps);
+}
+
 size_t attn_ws_bytes(const KvView& c, int) {
   const int sms = sm_count();
-  // without a device (host-side sizing) the largest part's SM count
-  return attn::rows_ws_bytes(c.D, sms > 0 ? sms : 160);
+  const int n = sms > 0 ? sms : 160;   // without a device (host-side sizing): at least the part's SMs
+  const size_t few = attn::rows_ws_bytes(c.D, n), many = attn::chunk_ws_bytes(c.D, n);
+  return few > many ? few : many;
 }
 
 int launch_attn(const KvView& c, const KvBatchView& b, const AttnArgs& a, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return GDN_ERR_CUDA;
-  return attn::launch_rows(c, b, a, sms, stream);
+  const long long most = b.max_tokens > 0 ? b.max_tokens : b.total;
+  if (most * a.g <= 16) return attn::launch_rows(c, b, a, sms, stream);
+  return attn::launch_chunk(c, b, a, sms, stream);
 }
 
 }  // namespace gdn

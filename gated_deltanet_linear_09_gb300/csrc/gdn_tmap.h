@@ -17,10 +17,15 @@ struct KvMaps {
 // in shared memory, 128-byte swizzled (64-byte rows and swizzle when head_dim is 64 bytes).
 bool make_kv_maps(const KvView& c, int rows, KvMaps* maps);
 
+// Maps whose box is `rows` keys by `cols` columns: [rows][cols], swizzled over its row's bytes or not.
+bool make_tile_maps(const KvView& c, int rows, int cols, bool swizzled, KvMaps* maps);
+
 namespace attn {
 int rows_grid(int D, int sms);
 size_t rows_ws_bytes(int D, int sms);
 int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream);
+size_t chunk_ws_bytes(int D, int sms);
+int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream);
 }  // namespace attn
 
 #ifdef __CUDACC__
