@@ -16,6 +16,11 @@
 namespace gdn {
 namespace attn {
 
+// 64-bit division that is a 32-bit one whenever it can be.
+__device__ __forceinline__ long long div_small(long long a, int b) {
+  return (unsigned long long)a >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 struct SeqInfo {
   int row0;        // first packed token
   int tokens;      // new tokens
@@ -88,7 +93,10 @@ struct SegIter {
     info = load_seq(*b, page_shift, s, &bad);
     work = seq_work<R>(info, g, fix);
     const long long per = work.prefix(work.tiles, R);
-    h = per > 0 ? (int)(into / per) : 0;
+    h = 0;
+    if (into >= per && per > 0) {        // heads are few: a division would cost as much
+      h = (int)(into / per);
+    }
     into -= (long long)h * per;
     int lo = 0, hi = work.tiles;      // largest k with prefix(k) <= into
     while (hi - lo > 1) {
@@ -100,8 +108,7 @@ struct SegIter {
   }
 
   __device__ __forceinline__ int key_tile(long long o, int nt) const {
-    const long long keys = (o - fix) / g;
-    return (int)min((long long)nt, max(0LL, keys) / TK);
+    return o <= fix ? 0 : (int)min((long long)nt, div_small(o - fix, g * TK));
   }
 
   // The next segment; false at the end of the piece.
@@ -135,9 +142,20 @@ struct SegIter {
   }
 };
 
-__device__ __forceinline__ long long piece_bound(long long total, int pieces, int i) {
-  // total < 2^56, pieces <= 1024
-  return total / pieces * i + total % pieces * i / pieces;
+// The line cut into pieces as equal as whole units allow: the first `more` are one unit longer.
+struct Pieces {
+  int count, more;
+  long long each;
+  __device__ __forceinline__ long long bound(int i) const { return each * i + min(i, more); }
+};
+
+// The number of pieces worth cutting a line of this length into.
+__device__ __forceinline__ Pieces make_pieces(long long total, int grid, int least) {
+  Pieces p;
+  p.count = (int)min((long long)grid, max(1LL, div_small(total, least)));
+  p.each = div_small(total, p.count);
+  p.more = (int)(total - p.each * p.count);
+  return p;
 }
 
 // Block-wide (NT threads, NT a multiple of 32, at most 1,024): the total work of all sequences,
@@ -184,17 +202,11 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   return v + before;
 }
 
-// The number of pieces worth cutting a line of this length into.
-__device__ __forceinline__ int pieces_for(long long total, int grid, long long least) {
-  const long long p = total / least;
-  return (int)min((long long)grid, max(1LL, p));
-}
-
 // Fills sc->total and sc->at[i] for the piece bounds first, first + 1 (all NT threads).  A bound at
 // the very end of the line is located past the last sequence.
 template <int R, int NT>
 __device__ __forceinline__ void locate_piece(const KvView& c, const KvBatchView& b, int g, int fix, int grid,
-                                             long long least, int first, int* pieces, LineScan<R, NT>* sc,
+                                             int least, int first, Pieces* pieces, LineScan<R, NT>* sc,
                                              bool* bad) {
   long long total = 0, v0 = 0, incl0 = 0;
   for (int s0 = 0; s0 < b.num_seqs; s0 += NT) {
@@ -204,7 +216,7 @@ __device__ __forceinline__ void locate_piece(const KvView& c, const KvBatchView&
     if (s0 == 0) { v0 = v; incl0 = incl; }
     total += sum;
   }
-  const int p = pieces_for(total, grid, least);
+  const Pieces p = make_pieces(total, grid, least);
   *pieces = p;
   if (threadIdx.x == 0) {
     sc->total = total;
@@ -223,8 +235,8 @@ __device__ __forceinline__ void locate_piece(const KvView& c, const KvBatchView&
     const long long lo = before + incl - v, hi = before + incl;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (first + i > p) continue;
-      const long long x = piece_bound(total, p, first + i);
+      if (first + i > p.count) continue;
+      const long long x = p.bound(first + i);
       if (v > 0 && lo <= x && x < hi) {
         sc->at[i].seq = s0 + (int)threadIdx.x;
         sc->at[i].into = x - lo;
@@ -286,21 +298,24 @@ __device__ __forceinline__ void zero_padding(const AttnArgs& a, const KvBatchVie
 // Block (i, y) looks at the bound between pieces i and i + 1.  If it falls inside a tile and is the
 // first to do so, the block merges rows y, y + gridDim.y, ... of the tile over the pieces that
 // share it: each piece's rows count 2^(m - M), M the largest reference.
+constexpr int kMaxPieces = 1024;
+
 template <int R, int TK, int D>
 __global__ void __launch_bounds__(256) merge_kernel(const KvView c, const KvBatchView b, const AttnArgs a,
-                                                    int grid, int fix, long long least) {
-  constexpr int NT = 256;
+                                                    int grid, int fix, int least) {
+  constexpr int NT = 256, W = NT / 32, Q = (D + 127) / 128;
   __shared__ LineScan<R, NT> scan;
-  __shared__ float4 acc[NT / 32][D / 4];
-  __shared__ float weight[1024];
+  __shared__ float4 acc[W][D / 4];
+  __shared__ float acc_l[W];
+  __shared__ int source[kMaxPieces];      // partial slot of each piece of the tile, -1: it left none
+  __shared__ float weight[kMaxPieces];
   pdl_begin();
   bool bad = false;
-  int pieces;
+  Pieces pieces;
   const int i = blockIdx.x;
   locate_piece<R, NT>(c, b, a.g, fix, grid, least, i, &pieces, &scan, &bad);
-  if (i + 1 >= pieces) return;
-  const long long total = scan.total;
-  const long long x = piece_bound(total, pieces, i + 1), x_prev = piece_bound(total, pieces, i);
+  if (i + 1 >= pieces.count) return;
+  const long long x = pieces.bound(i + 1), x_prev = pieces.bound(i);
   if (x == x_prev) return;
   // the tile that holds x
   SegIter<R, TK> it;
@@ -312,45 +327,55 @@ __global__ void __launch_bounds__(256) merge_kernel(const KvView c, const KvBatc
   const int keys = tile_keys<R>(it.info, a.g, it.k);
   const int nt = (keys + TK - 1) / TK;
   if (nt == 0) return;                                  // zeros, written by piece i
-  // the pieces i .. last share the tile; those with an empty share left nothing behind
-  int last = i + 1;
-  while (last + 1 < pieces && piece_bound(total, pieces, last + 1) < t0 + cost) ++last;
-  const int count = last - i + 1;                       // at most the grid, at most 1,024
-  for (int p = i; p <= last; ++p) {
-    const long long o0 = max(0LL, piece_bound(total, pieces, p) - t0);
-    const long long o1 = p + 1 <= pieces ? min(cost, piece_bound(total, pieces, p + 1) - t0) : cost;
-    const int ta = it.key_tile(o0, nt), tb = o1 == cost ? nt : it.key_tile(o1, nt);
-    if (ta == 0 && tb == nt) return;                    // one piece did it all and finished it
-  }
-  const int rows = min((long long)R, (long long)it.info.tokens * a.g - (long long)it.k * R);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float m_max = -INFINITY;
-    for (int j = threadIdx.x; j < count; j += NT) {
-      const int p = i + j;
-      const long long o0 = max(0LL, piece_bound(total, pieces, p) - t0);
-      const long long o1 = p + 1 <= pieces ? min(cost, piece_bound(total, pieces, p + 1) - t0) : cost;
+  const int rows = (int)min((long long)R, (long long)it.info.tokens * a.g - (long long)it.k * R);
+  if ((int)blockIdx.y >= rows) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the pieces i .. i + count - 1 share the tile
+  int count = 0;
+  bool one = false;
+  for (int j0 = 0;; j0 += NT) {
+    const int j = j0 + tid, p = i + j;
+    const bool in = p < pieces.count && pieces.bound(p) < t0 + cost;
+    if (in) {
+      const long long o0 = max(0LL, pieces.bound(p) - t0), o1 = min(cost, pieces.bound(p + 1) - t0);
       const int ta = it.key_tile(o0, nt), tb = o1 == cost ? nt : it.key_tile(o1, nt);
-      float m = -INFINITY;
-      if (ta < tb) m = __ldcg(Partials<R, D>::ml(a.ws, p, o0 > 0 ? 0 : 1) + 2 * r);
-      weight[j] = m;
+      source[j] = ta < tb ? 2 * p + (o0 > 0 ? 0 : 1) : -1;
+      one |= ta == 0 && tb == nt;                       // one piece did it all and finished it
     }
-    __syncthreads();
-    for (int j = 0; j < count; ++j) m_max = fmaxf(m_max, weight[j]);
-    float4 sum[D / 128 > 0 ? D / 128 : 1];
+    const int n = __syncthreads_count(in);
+    count += n;
+    if (n < NT) break;
+  }
+  if (__syncthreads_or(one)) return;
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float top = -INFINITY;
+    for (int j = tid; j < count; j += NT) {
+      const int s = source[j];
+      const float m = s < 0 ? -INFINITY : __ldcg(Partials<R, D>::ml(a.ws, s >> 1, s & 1) + 2 * r);
+      weight[j] = m;
+      top = fmaxf(top, m);
+    }
 #pragma unroll
-    for (int q = 0; q < (D + 127) / 128; ++q) sum[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) acc_l[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = fmaxf(top, acc_l[w]);
+    __syncthreads();
+    float4 sum[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) sum[q] = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll 4
-    for (int j = warp; j < count; j += NT / 32) {
+    for (int j = warp; j < count; j += W) {
       const float m = weight[j];
       if (m == -INFINITY) continue;
-      const int p = i + j, slot = piece_bound(total, pieces, p) > t0 ? 0 : 1;
-      const float w = exp2f(m - m_max);
-      l += w * __ldcg(Partials<R, D>::ml(a.ws, p, slot) + 2 * r + 1);
-      const float4* src = reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, p, slot) + (size_t)r * D);
+      const int s = source[j];
+      const float w = exp2f(m - top);
+      l += w * __ldcg(Partials<R, D>::ml(a.ws, s >> 1, s & 1) + 2 * r + 1);
+      const float4* src = reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, s >> 1, s & 1) + (size_t)r * D);
 #pragma unroll
-      for (int q = 0; q < (D + 127) / 128; ++q) {
+      for (int q = 0; q < Q; ++q) {
         const int col = q * 32 + lane;
         if (col < D / 4) {
           const float4 v = __ldcg(src + col);
@@ -359,28 +384,27 @@ __global__ void __launch_bounds__(256) merge_kernel(const KvView c, const KvBatc
         }
       }
     }
-    __syncthreads();                                     // weight[] read by all; acc[] free
 #pragma unroll
-    for (int q = 0; q < (D + 127) / 128; ++q) {
+    for (int q = 0; q < Q; ++q) {
       const int col = q * 32 + lane;
       if (col < D / 4) acc[warp][col] = sum[q];
     }
-    if (lane == 0) weight[warp] = l;
+    if (lane == 0) acc_l[warp] = l;
     __syncthreads();
-    if (threadIdx.x < D / 4) {
+    if (tid < D / 4) {
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float lt = 0.f;
 #pragma unroll
-      for (int q = 0; q < NT / 32; ++q) {
-        const float4 v = acc[q][threadIdx.x];
+      for (int w = 0; w < W; ++w) {
+        const float4 v = acc[w][tid];
         o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-        lt += weight[q];
+        lt += acc_l[w];
       }
       const float inv = lt == 0.f ? 0.f : 1.0f / lt;
       o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
       int tok, head;
       row_of(it.info, a.g, it.h, it.k * R + r, &tok, &head);
-      store_out4(a, D, tok, head, threadIdx.x * 4, o);
+      store_out4(a, D, tok, head, tid * 4, o);
     }
     __syncthreads();
   }

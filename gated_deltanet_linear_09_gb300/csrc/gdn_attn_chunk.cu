@@ -140,7 +140,7 @@ __device__ __forceinline__ void ring_order(int n, F f) {
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1)
-chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, long long least,
+chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, int least,
              const __grid_constant__ KvMaps maps) {
   using C = ChunkCfg<D, Q8>;
   constexpr int R = C::kRows, TK = kKeys;
@@ -172,11 +172,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   pdl_begin();
   zero_padding(a, b, D);
   bool bad_len = false;
-  int pieces;
+  Pieces pieces;
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad_len);
   if (bad_len) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
-  if (cta >= pieces) return;
+  if (cta >= pieces.count) return;
   if (warp == C::kMmaWarp) tmem_alloc(&sm.tmem, 512);
   fence_before_sync();
   __syncthreads();
@@ -184,9 +184,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   const uint32_t tmem = sm.tmem;
   SegIter<R, TK> it;
   {
-    const long long x0 = piece_bound(sm.scan.total, pieces, cta);
-    it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
-             piece_bound(sm.scan.total, pieces, cta + 1) - x0);
+      it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
+             pieces.bound(cta + 1) - pieces.bound(cta));
   }
   Segment sg;
 
@@ -630,7 +629,7 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   const int P = 1 << c.page_shift;
   if (!make_tile_maps(c, P < kKeys ? P : kKeys, Q8 ? C::kCols : 64, !Q8, &maps)) return GDN_ERR_CUDA;
   const int grid = sms, fix = 128 * a.g;
-  const long long least = 512LL * a.g;
+  const int least = 512 * a.g;
   int rc = launch_dependent(chunk_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;

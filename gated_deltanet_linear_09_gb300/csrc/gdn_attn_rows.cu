@@ -123,7 +123,7 @@ __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, vola
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(RowsCfg<D, Q8>::kThreads, RowsCfg<D, Q8>::kCtas)
-rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, long long least,
+rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, int least,
             const __grid_constant__ KvMaps maps) {
   using C = RowsCfg<D, Q8>;
   constexpr int R = kRows, TK = kTileKeys, NC = C::kConsumers * 32;
@@ -142,15 +142,14 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   pdl_begin();
   zero_padding(a, b, D);
   bool bad = false;
-  int pieces;
+  Pieces pieces;
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad);
   if (bad) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
-  if (cta >= pieces) return;
-  const long long x0 = piece_bound(sm.scan.total, pieces, cta);
+  if (cta >= pieces.count) return;
   SegIter<R, TK> it;
   it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
-           piece_bound(sm.scan.total, pieces, cta + 1) - x0);
+           pieces.bound(cta + 1) - pieces.bound(cta));
   Segment sg;
 
   if (warp == C::kConsumers) {
@@ -552,7 +551,7 @@ int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sm
   KvMaps maps;
   if (!make_kv_maps(c, 16, &maps)) return GDN_ERR_CUDA;
   const int grid = rows_grid(D, sms), fix = 64 * a.g;
-  const long long least = 256LL * a.g;
+  const int least = 256 * a.g;
   int rc = launch_dependent(rows_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
@@ -560,7 +559,7 @@ int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sm
                           grid, fix, least);
 }
 
-int rows_grid(int D, int sms) { return min(1024, D == 256 ? sms : 2 * sms); }
+int rows_grid(int D, int sms) { return min(kMaxPieces, D == 256 ? sms : 2 * sms); }
 
 size_t rows_ws_bytes(int D, int sms) {
   const int grid = rows_grid(D, sms);
