@@ -34,6 +34,15 @@ using namespace tc;
 namespace attn {
 
 constexpr int kKeys = 128;         // keys of a tile
+constexpr int kSegs = 4;           // segments known ahead
+
+// A segment as the roles need it, published by the scheduling warp.
+struct SegDesc {
+  int seq, row0, tokens, len;      // the sequence
+  int head, tile;                  // key/value head, tile of rows
+  int ta, n;                       // first key tile, number of them; n < 0: no more segments
+  int whole, owns_empty, slot;
+};
 
 template <int D, bool Q8>
 struct ChunkCfg {
@@ -47,8 +56,19 @@ struct ChunkCfg {
   static constexpr int kRawBytes = kKeys * kCols;
   static constexpr int kRawStages = Q8 ? 3 : 0;
   static constexpr int kSoftWarps = 4 * kBlocks;
-  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kConvWarp = kSoftWarps + 2;
-  static constexpr int kThreads = (kSoftWarps + 2 + (Q8 ? 4 : 0)) * 32;
+  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kSchedWarp = kSoftWarps + 2, kConvWarp = kSoftWarps + 4;
+  // whole warpgroups: softmax (one per block), control (MMA and TMA warps), conversion
+  static constexpr int kGroups = kBlocks + 1 + (Q8 ? 1 : 0);
+  static constexpr int kThreads = kGroups * 128;
+  static constexpr int kReaders = kSoftWarps + 2 + (Q8 ? 4 : 0);   // warps that read a segment
+  // registers per thread at launch (65,536 shared by the CTA's threads, in eights) and after the
+  // warpgroups have traded: their sum over the warpgroups is the launch's
+  static constexpr int kLaunchRegs = kGroups == 2 ? 255 : kGroups == 3 ? 168 : 128;
+  static constexpr int kSoftRegs = kGroups == 3 ? (Q8 ? 216 : 208) : kGroups == 4 ? 176 : 0;
+  static constexpr int kCtrlRegs = kGroups == 3 ? (Q8 ? 120 : 88) : kGroups == 4 ? 64 : 0;
+  static constexpr int kConvRegs = kGroups == 3 ? 168 : kGroups == 4 ? 96 : 0;
+  static_assert(kGroups == 2 || kBlocks * kSoftRegs + kCtrlRegs + (Q8 ? kConvRegs : 0) <= kGroups * kLaunchRegs,
+                "a share above the launch's registers would wait for ever");
   static constexpr int kQBytes = 128 * D * 2;               // one block
   static constexpr int kO = 256;                            // TMEM column of O (block b: + b D)
 };
@@ -62,12 +82,14 @@ struct __align__(1024) ChunkSmem {
   uint8_t scales[Q8 ? C::kRawStages : 1][8][Q8 ? 128 : 16];
   LineScan<C::kRows, C::kThreads> scan;
   int bad[D];                       // first position with a non-finite value, per column
+  SegDesc segs[kSegs];
   int any_bad;
   uint32_t tmem;
   int dead;
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t raw_full[Q8 ? C::kRawStages : 1], raw_empty[Q8 ? C::kRawStages : 1];
   uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t v_ready;                 // the current tile's values are in the ring
 };
 
@@ -108,13 +130,45 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// 32 lanes x 32 columns; no wait.
+__device__ __forceinline__ void tmem_ld32_nw(uint32_t addr, uint32_t* r) {
   tmem_ld16_nw(addr, r);
   tmem_ld16_nw(addr + 16, r + 16);
-  tmem_wait_ld();
-  reg_fence16(r);
-  reg_fence16(r + 16);
 }
+
+// Pairs of f32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
 // Position of a stage in the ring.
 template <int N>
@@ -163,6 +217,10 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       mbar_init(&sm.p_ready[i], 4);
       mbar_init(&sm.o_done[i], 1);
     }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&sm.seg_full[i], 1);
+      mbar_init(&sm.seg_empty[i], C::kReaders);
+    }
     mbar_init(&sm.v_ready, 1);
     sm.dead = 0;
     sm.any_bad = 0;
@@ -182,14 +240,40 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  SegIter<R, TK> it;
-  {
-      it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
-             pieces.bound(cta + 1) - pieces.bound(cta));
-  }
-  Segment sg;
+  auto seg_wait = [&](const RingPos<kSegs>& p) -> const SegDesc& {
+    wait_bar(&sm.seg_full[p.stage], p.phase, &sm.dead, c.status);
+    return sm.segs[p.stage];
+  };
+  auto seg_done = [&](RingPos<kSegs>& p) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.seg_empty[p.stage]);
+    p.step();
+  };
+  RingPos<kSegs> seg;
 
-  if (warp == C::kLoadWarp) {
+  // All four warps of the control warpgroup (one is idle) give their registers up together.
+  if (C::kGroups > 2 && warp >= C::kMmaWarp && warp < C::kConvWarp) regs_down<C::kCtrlRegs ? C::kCtrlRegs : 24>();
+  if (warp == C::kSchedWarp) {
+    // ---------------------------------------------------------------- segments
+    SegIter<R, TK> it;
+    it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
+             pieces.bound(cta + 1) - pieces.bound(cta));
+    Segment s;
+    for (bool more = true; more;) {
+      more = it.next(&s);
+      const int n = s.tb - s.ta;
+      if (more && n <= 0 && !s.owns_empty) continue;
+      wait_bar(&sm.seg_empty[seg.stage], seg.phase ^ 1u, &sm.dead, c.status);
+      if (lane == 0) {
+        sm.segs[seg.stage] = more ? SegDesc{s.seq, s.info.row0, s.info.tokens, s.info.len, s.head, s.tile, s.ta,
+                                            max(n, 0), s.whole(), s.owns_empty, s.slot}
+                                  : SegDesc{0, 0, 0, 0, 0, 0, 0, -1, 0, 0, 0};
+        mbar_arrive(&sm.seg_full[seg.stage]);
+      }
+      __syncwarp();
+      seg.step();
+    }
+  } else if (warp == C::kLoadWarp) {
     // ---------------------------------------------------------------- TMA
     const int box = min(1 << c.page_shift, TK);            // keys of one copy
     constexpr int kBoxCols = Q8 ? C::kCols : 64;
@@ -199,13 +283,15 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     uint64_t* full = Q8 ? sm.raw_full : sm.full;
     uint64_t* empty = Q8 ? sm.raw_empty : sm.empty;
     const int my_page = lane / kBlk, my_blk = lane % kBlk;
-    while (it.next(&sg)) {
-      const int n = sg.tb - sg.ta;
-      if (n <= 0) continue;
-      const int* table = b.table + (long long)sg.seq * b.table_ld;
-      const int len = sg.info.len;
+    while (true) {
+      const SegDesc& sd = seg_wait(seg);
+      const int n = sd.n, ta = sd.ta, len = sd.len, head = sd.head;
+      const int* table = b.table + (long long)sd.seq * b.table_ld;
+      seg_done(seg);
+      if (n < 0) break;
+      if (n == 0) continue;
       auto lookup = [&](int i) {                            // this lane's page of tile i
-        const int k = (sg.ta + i) * TK + my_page * box;
+        const int k = (ta + i) * TK + my_page * box;
         if (i >= n || my_page >= pages || k >= len) return c.num_pages;   // zeros
         int p = __ldg(table + (k >> c.page_shift));
         if (p < 0 || p >= c.num_pages) {
@@ -229,16 +315,16 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
                                 Q8 ? (half == 0 ? C::kRawBytes + TK : C::kRawBytes) : C::kStageBytes);
         __syncwarp();
         if (my_page < pages) {
-          const int off = (((sg.ta + i) * TK) & ((1 << c.page_shift) - 1));   // 0 unless pages exceed a tile
+          const int off = (((ta + i) * TK) & ((1 << c.page_shift) - 1));   // 0 unless pages exceed a tile
           if constexpr (Q8) {
             tma_load_5d(sm.raw[pos.stage] + my_page * box * C::kCols, is_v ? &maps.v : &maps.k, 0, off,
-                        half, sg.head, page, &full[pos.stage]);
+                        half, head, page, &full[pos.stage]);
             if (half == 0)
-              tma_load_3d(sm.scales[pos.stage][my_page], is_v ? &maps.vs : &maps.ks, off, sg.head, page,
+              tma_load_3d(sm.scales[pos.stage][my_page], is_v ? &maps.vs : &maps.ks, off, head, page,
                           &full[pos.stage]);
           } else {
             tma_load_5d(sm.ring[pos.stage] + my_blk * (TK * 128) + my_page * box * 128, is_v ? &maps.v : &maps.k, 0,
-                        off, half * kBlk + my_blk, sg.head, page, &full[pos.stage]);
+                        off, half * kBlk + my_blk, head, page, &full[pos.stage]);
           }
         }
         __syncwarp();
@@ -254,10 +340,12 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     constexpr uint32_t kIdQK = idesc_bf16(128, 128);
     constexpr uint32_t kIdPV = idesc_bf16_bmn(128, C::kCols);
     const uint32_t ring = smem_u32(sm.ring[0]);
-    while (it.next(&sg)) {
-      const int n = sg.tb - sg.ta;
-      if (n <= 0) continue;
-      const int rows = (int)min((long long)R, (long long)sg.info.tokens * a.g - (long long)sg.tile * R);
+    while (true) {
+      const SegDesc& sd = seg_wait(seg);
+      const int n = sd.n, rows = (int)min((long long)R, (long long)sd.tokens * a.g - (long long)sd.tile * R);
+      seg_done(seg);
+      if (n < 0) break;
+      if (n == 0) continue;
       const int blocks = rows > 128 ? 2 : 1;
       auto qk_half = [&](int blk, int buf, uint32_t kaddr, int half) {
         if (lane == 0) {
@@ -358,15 +446,18 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     }
   } else if (Q8 && warp >= C::kConvWarp) {
     // ---------------------------------------------------------------- e4m3 -> bf16
+    if constexpr (C::kConvRegs && C::kConvRegs < C::kLaunchRegs) regs_down<C::kConvRegs>();
     const int ct = tid - C::kConvWarp * 32;
     const int box = min(1 << c.page_shift, TK), shift = 31 - __clz(box);
     RingPos<C::kRawStages ? C::kRawStages : 1> src;
     RingPos<C::kStages> dst;
     constexpr int kPer = C::kCols / 8;                      // 8-element pieces of a row
     const int piece = ct % kPer;
-    while (it.next(&sg)) {
-      const int n = sg.tb - sg.ta;
-      if (n <= 0) continue;
+    while (true) {
+      const int n = seg_wait(seg).n;
+      seg_done(seg);
+      if (n < 0) break;
+      if (n == 0) continue;
       uint32_t byte[128 * kPer / 128] = {};                  // scale bytes of this thread's rows
       ring_order<C::kHalves>(n, [&](bool, int, int half) {
         wait_bar(&sm.raw_full[src.stage], src.phase, &sm.dead, c.status);
@@ -400,52 +491,60 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     }
   } else if (warp < C::kSoftWarps) {
     // ---------------------------------------------------------------- softmax and output
+    if constexpr (C::kSoftRegs > 0) regs_up<C::kSoftRegs>();
     const int blk = warp >> 2, r = tid & 127, lbase = (warp & 3) * 32;
     const uint32_t tl = tmem + ((uint32_t)lbase << 16);
     uint32_t cnt = 0;                  // tiles of this block so far
     RingPos<C::kStages> ring;          // first stage of the current segment (block 0 only)
-    auto load_q = [&](const Segment& s) {
-      // thread groups of D / 8 lanes take a row at a time: 16-byte pieces, swizzled
-      const int rows = (int)min((long long)R, (long long)s.info.tokens * a.g - (long long)s.tile * R) - blk * 128;
+    auto load_q = [&](const SegDesc& s) {
+      // D / 8 lanes take a row at a time: 16-byte pieces, swizzled, all in flight at once
+      const int rows = (int)min((long long)R, (long long)s.tokens * a.g - (long long)s.tile * R) - blk * 128;
       constexpr int kPer = D / 8;
       const int piece = r % kPer;
+      const uint32_t dst = smem_u32(sm.q[blk]) + (piece >> 3) * (128 * 128);
+      int t = (s.tile * R + blk * 128 + r / kPer) / a.g;
+      int hh = s.tile * R + blk * 128 + r / kPer - t * a.g;
+#pragma unroll 4
       for (int row = r / kPer; row < 128; row += 128 / kPer) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-          int tok, head;
-          row_of(s.info, a.g, s.head, s.tile * R + blk * 128 + row, &tok, &head);
-          v = __ldg(reinterpret_cast<const uint4*>(a.q + tok * a.q_ld + head * a.q_head_ld + piece * 8));
-        }
-        *reinterpret_cast<uint4*>(sm.q[blk] + (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
+        const __nv_bfloat16* src =
+            a.q + (s.row0 + t) * a.q_ld + (s.head * a.g + hh) * a.q_head_ld + piece * 8;
+        cp_async16(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), row < rows ? src : a.q, row < rows);
+        hh += 128 / kPer;
+        while (hh >= a.g) { hh -= a.g; ++t; }
       }
+      cp_async_wait_all();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_ready[blk]);
     };
-    auto active = [&](const Segment& s) {
-      return s.tb > s.ta && (blk == 0 || (long long)s.info.tokens * a.g - (long long)s.tile * R > 128);
+    auto active = [&](const SegDesc& s) {
+      return s.n > 0 && (blk == 0 || (long long)s.tokens * a.g - (long long)s.tile * R > 128);
     };
-    bool have = it.next(&sg);
-    if (have && active(sg)) load_q(sg);
-    while (have) {
-      const Segment cur = sg;
-      const SeqInfo info = cur.info;
-      const int rows = (int)min((long long)R, (long long)info.tokens * a.g - (long long)cur.tile * R);
-      const int n = cur.tb - cur.ta;
+    {
+      const SegDesc& first = seg_wait(seg);
+      if (active(first)) load_q(first);
+    }
+    while (true) {
+      const SegDesc& cur = sm.segs[seg.stage];                   // released at the end
+      const int n = cur.n;
+      if (n < 0) break;
+      const int rows = (int)min((long long)R, (long long)cur.tokens * a.g - (long long)cur.tile * R);
       const int row = cur.tile * R + blk * 128 + r;              // this thread's row
       const bool live = blk * 128 + r < rows;
-      const int before = info.len - info.tokens;
+      const int before = cur.len - cur.tokens;
+      RingPos<kSegs> ahead_seg = seg;
+      ahead_seg.step();
       if (!active(cur)) {
         if (cur.owns_empty && live) {
           int tok, head;
-          row_of(info, a.g, cur.head, row, &tok, &head);
+          row_of(SeqInfo{cur.row0, cur.tokens, cur.len}, a.g, cur.head, row, &tok, &head);
           uint4* o = reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D);
           for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
         }
-        have = it.next(&sg);
-        if (have && active(sg)) load_q(sg);
+        const SegDesc& next = seg_wait(ahead_seg);
+        if (active(next)) load_q(next);
       } else {
-        const int last_row = info.tokens * a.g - 1;
+        const int last_row = cur.tokens * a.g - 1, len = cur.len, ta = cur.ta;
         const int pos = before + min(row, last_row) / a.g;
         const int pos_min = before + min(cur.tile * R + blk * 128, last_row) / a.g;
         float m = -INFINITY, l = 0.f;
@@ -454,23 +553,27 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           wait_bar(&sm.s_full[buf], (C::kBlocks == 2 ? cnt : cnt >> 1) & 1u, &sm.dead, c.status);
           fence_after_sync();
           const uint32_t s_addr = tl + buf * 128;
-          const int k0 = (cur.ta + i) * TK;
+          const int k0 = (ta + i) * TK;
           const bool partial = k0 + TK - 1 > pos_min;
           const int lim = pos - k0;                               // columns 0..lim are seen
-          float x = -INFINITY;
+          uint32_t v[128];
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t v[32];
-            tmem_ld32(s_addr + cc * 32, v);
-            if (partial) {
+          for (int cc = 0; cc < 4; ++cc) tmem_ld32_nw(s_addr + cc * 32, v + cc * 32);
+          tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (cc * 32 + e > lim) v[e] = 0xff800000u;
-            }
+          for (int cc = 0; cc < 8; ++cc) reg_fence16(v + cc * 16);
+          if (partial) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x = fmaxf(x, __uint_as_float(v[e]));
+            for (int e = 0; e < 128; ++e)
+              if (e > lim) v[e] = 0xff800000u;
           }
-          x *= a.scale_log2;
+          float xs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 128; e += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              xs[j] = fmaxf(xs[j], fmaxf(__uint_as_float(v[e + 2 * j]), __uint_as_float(v[e + 2 * j + 1])));
+          const float x = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])) * a.scale_log2;
           if (__any_sync(0xffffffffu, x > m + 8.f)) {
             const float mn = fmaxf(m, x);
             const float f = mn == m ? 1.f : ex2f(m - mn);
@@ -491,28 +594,29 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          float l0 = 0.f, l1 = 0.f;
+          const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), ref2 = pair(-ref, -ref);
+          uint64_t l2[2] = {pair(l, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t v[32];
-            tmem_ld32(s_addr + cc * 32, v);
-            if (partial) {
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t w[8];
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (cc * 32 + e > lim) v[e] = 0xff800000u;
-            }
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2f(fmaf(__uint_as_float(v[2 * e]), a.scale_log2, -ref));
-              const float p1 = ex2f(fmaf(__uint_as_float(v[2 * e + 1]), a.scale_log2, -ref));
-              l0 += p0;
-              l1 += p1;
+            for (int e = 0; e < 8; ++e) {
+              const int j = cc * 16 + 2 * e;
+              float p0, p1;
+              unpair(fma2(pair(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, ref2), p0, p1);
+              p0 = ex2f(p0);
+              p1 = ex2f(p1);
+              l2[e & 1] = add2(l2[e & 1], pair(p0, p1));
               w[e] = pack2(p0, p1);
             }
-            tmem_st16w_nw(s_addr + cc * 16, w);
+            tmem_st8w_nw(s_addr + cc * 8, w);
           }
-          l += l0 + l1;
+          {
+            float l0, l1, l3, l4;
+            unpair(l2[0], l0, l1);
+            unpair(l2[1], l3, l4);
+            l = (l0 + l1) + (l3 + l4);
+          }
           // A parity wait tells a phase from the one before it only when no phase is skipped: so
           // v_ready is waited for at every tile (the ring's own barriers, which K tiles use too,
           // would not do), and so is o_done where s_full does not imply the product before.
@@ -532,7 +636,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
               for (int j = j0 + r / kPer; j < j1; j += 128 / kPer) {
                 uint4* p = reinterpret_cast<uint4*>(sm.ring[vp.stage] + (piece >> 3) * (TK * 128) + j * 128 +
                                                     (((piece & 7) ^ (j & 7)) << 4));
-                if (k0 + j >= info.len) {
+                if (k0 + j >= len) {
                   *p = make_uint4(0, 0, 0, 0);
                   continue;
                 }
@@ -562,31 +666,55 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           if (lane == 0) mbar_arrive(&sm.p_ready[blk]);
         }
         // the next tile's queries, before this one's output: every QK of this one has completed
-        have = it.next(&sg);
-        if (have && active(sg)) load_q(sg);
+        const SegDesc& next = seg_wait(ahead_seg);
+        if (active(next)) load_q(next);
         wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
         fence_after_sync();
-        const bool whole = cur.whole(), bad = *(volatile int*)&sm.any_bad != 0;
+        const bool whole = cur.whole, bad = *(volatile int*)&sm.any_bad != 0;
         int tok = 0, head = 0;
-        if (live) row_of(info, a.g, cur.head, row, &tok, &head);
+        if (live) row_of(SeqInfo{cur.row0, cur.tokens, cur.len}, a.g, cur.head, row, &tok, &head);
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
         const int pr = blk * 128 + r;
         float* prow = Partials<R, D>::rows(a.ws, cta, cur.slot) + (size_t)pr * D;
+        const uint4* gate = a.gate && whole && live
+                                ? reinterpret_cast<const uint4*>(a.gate + tok * a.gate_ld + head * a.gate_head_ld)
+                                : nullptr;
+        uint4* orow = reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D);
 #pragma unroll 1
-        for (int d = 0; d < D; d += 16) {
-          float o[16];
-          tmem_ld16(tl + C::kO + blk * D + d, o);
+        for (int d = 0; d < D; d += 32) {
+          uint4 z[4];
+          if (gate)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = __ldg(gate + d / 8 + e);
+          uint32_t o[32];
+          tmem_ld32_nw(tl + C::kO + blk * D + d, o);
+          tmem_wait_ld();
+          reg_fence16(o);
+          reg_fence16(o + 16);
           if (live) {
             if (bad) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (sm.bad[d + e] <= pos) o[e] = __int_as_float(0x7fffffff);
+              for (int e = 0; e < 32; ++e)
+                if (sm.bad[d + e] <= pos) o[e] = 0x7fffffffu;
             }
+            if (whole) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 v = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
-              if (whole) store_out4(a, D, tok, head, d + e, v);
-              else __stcg(reinterpret_cast<float4*>(prow + d + e), v);
+              for (int e = 0; e < 4; ++e) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(o[8 * e + k]) * inv;
+                if (gate) {
+                  const uint32_t zw[4] = {z[e].x, z[e].y, z[e].z, z[e].w};
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    y[k] *= gate_of(__uint_as_float(k & 1 ? zw[k >> 1] & 0xffff0000u : zw[k >> 1] << 16));
+                }
+                orow[d / 8 + e] = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                __stcg(reinterpret_cast<uint4*>(prow + d + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
             }
           }
           __syncwarp();
@@ -609,6 +737,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         if (tid == 0) sm.any_bad = 0;
         asm volatile("bar.sync 1, %0;\n" ::"n"(C::kSoftWarps * 32) : "memory");
       }
+      seg_done(seg);
     }
   }
   fence_before_sync();
