@@ -93,18 +93,42 @@ struct __align__(1024) ChunkSmem {
   uint64_t v_ready;                 // the current tile's values are in the ring
 };
 
-// K-major 128-byte-swizzled operand tile: 8-row groups 1,024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return sdesc(saddr, lbo, sbo) | (2ull << 61);
+// Operand descriptors of 128-byte-swizzled tiles (8-row groups 1,024 bytes apart).  Only the low
+// word changes from one MMA to the next: the start address, in sixteen-byte units, beside a constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);          // SBO, version, swizzle
+constexpr uint32_t kDescK = (16u >> 4) << 16;                                  // K-major: LBO unused
+constexpr uint32_t kDescMN = ((128u * 128u) >> 4) << 16;                       // MN-major: 64-column blocks
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t kind) { return ((saddr & 0x3FFFFu) >> 4) | kind; }
+
+// The issuing thread's instructions between two MMAs are what the tensor pipe waits for when they
+// are many: 32-bit operands, constants where possible.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
 }
 
-// A bounded wait of a whole warp: a timeout marks the CTA dead, after which no wait blocks and the
-// (wrong) results are flagged by the status bit.
-__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
+// A bounded wait: a timeout marks the CTA dead, after which no wait blocks and the (wrong) results
+// are flagged by the status bit.
+__device__ __forceinline__ void wait_one(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
   if (!mbar_try_wait(bar, parity) && !*dead && !mbar_wait(bar, parity)) {
     *dead = 1;
     set_status(status, GDN_STATUS_TIMEOUT);
   }
+}
+// The same for a whole warp.
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
+  wait_one(bar, parity, dead, status);
   __syncwarp();
 }
 
@@ -239,7 +263,13 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = sm.tmem;
+  // all 512 columns: they start at column 0, and TMEM addresses are constants from here on
+  constexpr uint32_t tmem = 0;
+  if (sm.tmem != 0) {
+    if (tid == 0) set_status(c.status, GDN_STATUS_TIMEOUT);
+    if (warp == C::kMmaWarp) tmem_dealloc(sm.tmem, 512);
+    return;
+  }
   auto seg_wait = [&](const RingPos<kSegs>& p) -> const SegDesc& {
     wait_bar(&sm.seg_full[p.stage], p.phase, &sm.dead, c.status);
     return sm.segs[p.stage];
@@ -332,118 +362,128 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       });
     }
   } else if (warp == C::kMmaWarp) {
-    // ---------------------------------------------------------------- MMA
-    RingPos<C::kStages> pos;
-    uint32_t cnt[2] = {0, 0};          // tiles issued per block
-    uint32_t s_cnt = 0;                // S buffers issued (one block)
-    uint32_t q_phase[2] = {0, 0};
-    constexpr uint32_t kIdQK = idesc_bf16(128, 128);
-    constexpr uint32_t kIdPV = idesc_bf16_bmn(128, C::kCols);
-    const uint32_t ring = smem_u32(sm.ring[0]);
-    while (true) {
-      const SegDesc& sd = seg_wait(seg);
-      const int n = sd.n, rows = (int)min((long long)R, (long long)sd.tokens * a.g - (long long)sd.tile * R);
-      seg_done(seg);
-      if (n < 0) break;
-      if (n == 0) continue;
-      const int blocks = rows > 128 ? 2 : 1;
-      auto qk_half = [&](int blk, int buf, uint32_t kaddr, int half) {
-        if (lane == 0) {
-          const uint64_t qd = desc_sw128(smem_u32(sm.q[blk]) + half * (C::kCols / 64) * (128 * 128), 16, 1024);
-          const uint64_t kd = desc_sw128(kaddr, 16, 1024);
+    // ---------------------------------------------------------------- MMA (one thread)
+    if (lane == 0) {
+      RingPos<C::kStages> pos;
+      uint32_t cnt[2] = {0, 0};          // tiles of each block
+      uint32_t s_cnt = 0;                // S buffers filled (one block)
+      uint32_t q_phase[2] = {0, 0};
+      constexpr uint32_t kIdQK = idesc_bf16(128, 128);
+      constexpr uint32_t kIdPV = idesc_bf16_bmn(128, C::kCols);
+      constexpr uint32_t kStage16 = C::kStageBytes / 16;
+      const uint32_t ring_k = desc_lo(smem_u32(sm.ring[0]), kDescK), ring_v = desc_lo(smem_u32(sm.ring[0]), kDescMN);
+      const uint32_t q0 = desc_lo(smem_u32(sm.q[0]), kDescK);
+      // S[buf] (+)= Q K^T over the columns of one stage; O += P[buf] V into those columns
+      auto qk_half = [&](int blk, int buf, uint32_t k_lo, int half) {
+        const uint32_t q_lo = q0 + (blk * C::kQBytes + half * (C::kCols / 64) * (128 * 128)) / 16;
 #pragma unroll
-          for (int ks = 0; ks < C::kCols / 16; ++ks) {
-            const uint32_t o = (uint32_t)(ks >> 2) * (128 * 128) + (uint32_t)(ks & 3) * 32;
-            mma_bf16(tmem + buf * 128, desc_add(qd, o), desc_add(kd, o), kIdQK, half > 0 || ks > 0);
+        for (int ks = 0; ks < C::kCols / 16; ++ks) {
+          const uint32_t o = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16;
+          mma_ss(buf * 128, q_lo + o, k_lo + o, kIdQK, half > 0 || ks > 0);
+        }
+      };
+      auto pv_half = [&](int blk, int buf, uint32_t v_lo, int half, bool acc) {
+#pragma unroll
+        for (int ks = 0; ks < TK / 16; ++ks)
+          mma_ts(C::kO + blk * D + half * C::kCols, buf * 128 + ks * 8, v_lo + ks * (2048 / 16), kIdPV, acc || ks > 0);
+      };
+      while (true) {
+        wait_one(&sm.seg_full[seg.stage], seg.phase, &sm.dead, c.status);
+        const SegDesc& sd = sm.segs[seg.stage];
+        const int n = sd.n;
+        const bool two = (long long)sd.tokens * a.g - (long long)sd.tile * R > 128;
+        mbar_arrive(&sm.seg_empty[seg.stage]);
+        seg.step();
+        if (n < 0) break;
+        if (n == 0) continue;
+        wait_one(&sm.q_ready[0], q_phase[0], &sm.dead, c.status);
+        q_phase[0] ^= 1u;
+        if (C::kBlocks == 2 && two) {
+          wait_one(&sm.q_ready[1], q_phase[1], &sm.dead, c.status);
+          q_phase[1] ^= 1u;
+        }
+        if constexpr (C::kBlocks == 2) {
+          wait_one(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
+          fence_after_sync();
+          qk_half(0, 0, ring_k + pos.stage * kStage16, 0);
+          mma_commit(&sm.s_full[0]);
+          if (two) {
+            qk_half(1, 1, ring_k + pos.stage * kStage16, 0);
+            mma_commit(&sm.s_full[1]);
           }
-        }
-        __syncwarp();
-      };
-      auto pv_half = [&](int blk, int buf, uint32_t vaddr, int half, bool acc) {
-        if (lane == 0) {
-          const uint64_t vd = desc_sw128(vaddr, 128 * 128, 1024);
-          const uint32_t o = tmem + C::kO + blk * D + half * C::kCols;
-#pragma unroll
-          for (int ks = 0; ks < TK / 16; ++ks)
-            mma_bf16_tmem_a(o, tmem + buf * 128 + ks * 8, desc_add(vd, ks * 2048), kIdPV, acc || ks > 0);
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (lane == 0) mma_commit(bar);
-        __syncwarp();
-      };
-      for (int blk = 0; blk < blocks; ++blk) {
-        wait_bar(&sm.q_ready[blk], q_phase[blk], &sm.dead, c.status);
-        q_phase[blk] ^= 1u;
-      }
-      fence_after_sync();
-      if constexpr (C::kBlocks == 2) {
-        wait_bar(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
-        fence_after_sync();
-        for (int blk = 0; blk < blocks; ++blk) {
-          qk_half(blk, blk, ring + pos.stage * C::kStageBytes, 0);
-          commit(&sm.s_full[blk]);
-        }
-        commit(&sm.empty[pos.stage]);
-        pos.step();
-        for (int i = 0; i < n; ++i) {
-          RingPos<C::kStages> kpos = pos;
-          const bool more = i + 1 < n;
-          if (more) pos.step();
-          const RingPos<C::kStages> vpos = pos;
+          mma_commit(&sm.empty[pos.stage]);
           pos.step();
-          wait_bar(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
-          if (lane == 0) mbar_arrive(&sm.v_ready);
-          if (more) wait_bar(&sm.full[kpos.stage], kpos.phase, &sm.dead, c.status);
-          for (int blk = 0; blk < blocks; ++blk) {
-            wait_bar(&sm.p_ready[blk], cnt[blk] & 1u, &sm.dead, c.status);
-            ++cnt[blk];
+          for (int i = 0; i < n; ++i) {
+            const RingPos<C::kStages> kpos = pos;
+            const bool more = i + 1 < n;
+            if (more) pos.step();
+            const RingPos<C::kStages> vpos = pos;
+            pos.step();
+            const uint32_t k_lo = ring_k + kpos.stage * kStage16, v_lo = ring_v + vpos.stage * kStage16;
+            wait_one(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
+            mbar_arrive(&sm.v_ready);
+            wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
             fence_after_sync();
-            pv_half(blk, blk, ring + vpos.stage * C::kStageBytes, 0, i > 0);
-            commit(&sm.o_done[blk]);
-            if (blk == blocks - 1) commit(&sm.empty[vpos.stage]);
+            pv_half(0, 0, v_lo, 0, i > 0);
+            mma_commit(&sm.o_done[0]);
             if (more) {
-              qk_half(blk, blk, ring + kpos.stage * C::kStageBytes, 0);
-              commit(&sm.s_full[blk]);
-              if (blk == blocks - 1) commit(&sm.empty[kpos.stage]);
+              wait_one(&sm.full[kpos.stage], kpos.phase, &sm.dead, c.status);
+              qk_half(0, 0, k_lo, 0);
+              mma_commit(&sm.s_full[0]);
+            }
+            if (two) {
+              wait_one(&sm.p_ready[1], cnt[1]++ & 1u, &sm.dead, c.status);
+              fence_after_sync();
+              pv_half(1, 1, v_lo, 0, i > 0);
+              mma_commit(&sm.o_done[1]);
+            }
+            mma_commit(&sm.empty[vpos.stage]);
+            if (more) {
+              if (two) {
+                qk_half(1, 1, k_lo, 0);
+                mma_commit(&sm.s_full[1]);
+              }
+              mma_commit(&sm.empty[kpos.stage]);
             }
           }
-        }
-      } else {
-        auto qk_tile = [&]() {
-          const int buf = (int)(s_cnt & 1u);
-          for (int h = 0; h < C::kHalves; ++h) {
-            wait_bar(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
+        } else {
+          auto qk_tile = [&]() {
+            const int buf = (int)(s_cnt & 1u);
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+              wait_one(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
+              fence_after_sync();
+              qk_half(0, buf, ring_k + pos.stage * kStage16, h);
+              mma_commit(&sm.empty[pos.stage]);
+              pos.step();
+            }
+            mma_commit(&sm.s_full[buf]);
+            ++s_cnt;
+          };
+          qk_tile();
+          if (n > 1) qk_tile();
+          for (int i = 0; i < n; ++i) {
+            const int buf = (int)(cnt[0] & 1u);
+            RingPos<C::kStages> vpos = pos;
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h, vpos.step())
+              wait_one(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
+            mbar_arrive(&sm.v_ready);
+            wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
             fence_after_sync();
-            qk_half(0, buf, ring + pos.stage * C::kStageBytes, h);
-            commit(&sm.empty[pos.stage]);
-            pos.step();
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+              pv_half(0, buf, ring_v + pos.stage * kStage16, h, i > 0);
+              mma_commit(&sm.empty[pos.stage]);
+              pos.step();
+            }
+            mma_commit(&sm.o_done[0]);
+            if (i + 2 < n) qk_tile();
           }
-          commit(&sm.s_full[buf]);
-          ++s_cnt;
-        };
-        qk_tile();
-        if (n > 1) qk_tile();
-        for (int i = 0; i < n; ++i) {
-          const int buf = (int)(cnt[0] & 1u);
-          RingPos<C::kStages> vpos = pos;
-          for (int h = 0; h < C::kHalves; ++h, vpos.step())
-            wait_bar(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
-          if (lane == 0) mbar_arrive(&sm.v_ready);
-          wait_bar(&sm.p_ready[0], cnt[0] & 1u, &sm.dead, c.status);
-          ++cnt[0];
-          fence_after_sync();
-          for (int h = 0; h < C::kHalves; ++h) {
-            pv_half(0, buf, ring + pos.stage * C::kStageBytes, h, i > 0);
-            commit(&sm.empty[pos.stage]);
-            pos.step();
-          }
-          commit(&sm.o_done[0]);
-          if (i + 2 < n) qk_tile();
         }
       }
     }
+    __syncwarp();
   } else if (Q8 && warp >= C::kConvWarp) {
     // ---------------------------------------------------------------- e4m3 -> bf16
     if constexpr (C::kConvRegs && C::kConvRegs < C::kLaunchRegs) regs_down<C::kConvRegs>();
