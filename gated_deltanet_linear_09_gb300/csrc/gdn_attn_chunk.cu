@@ -24,6 +24,8 @@
 // in tiles that the causal edge crosses, the first warpgroup replaces non-finite ones (and
 // whatever lies past the sequence's end) by zero, and notes column and position, so that the rows
 // that do see them get their NaN.
+#include <cuda_fp16.h>
+
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 
@@ -51,10 +53,14 @@ struct ChunkCfg {
   static constexpr int kRows = 128 * kBlocks;
   static constexpr int kCols = D == 64 ? 64 : 128;          // columns of a ring stage
   static constexpr int kHalves = D / kCols;                 // stages of a K or V tile
-  static constexpr int kStageBytes = kKeys * kCols * 2;
-  static constexpr int kStages = D == 64 ? (Q8 ? 4 : 8) : (Q8 ? 3 : 5);
-  static constexpr int kRawBytes = kKeys * kCols;
-  static constexpr int kRawStages = Q8 ? 3 : 0;
+  // K stages: bf16, or the e4m3 codes themselves; V stages: bf16; R stages: the codes of V
+  static constexpr int kKBytes = kKeys * kCols * (Q8 ? 1 : 2), kVBytes = kKeys * kCols * 2, kRBytes = kKeys * kCols;
+  static constexpr int kKStages = D == 64 ? 4 : Q8 ? 3 : D == 128 ? 2 : 3;
+  static constexpr int kVStages = Q8 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kRStages = Q8 ? 2 : 0;
+  // tiles whose scales are held: a tile's place is taken after the values of two tiles before it
+  // have been converted, which with two V stages means that four before it are through
+  static constexpr int kScales = Q8 ? 4 : 0;
   static constexpr int kSoftWarps = 4 * kBlocks;
   static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kSchedWarp = kSoftWarps + 2, kConvWarp = kSoftWarps + 4;
   // whole warpgroups: softmax (one per block), control (MMA and TMA warps), conversion
@@ -77,25 +83,29 @@ template <int D, bool Q8>
 struct __align__(1024) ChunkSmem {
   using C = ChunkCfg<D, Q8>;
   uint8_t q[C::kBlocks][C::kQBytes];
-  uint8_t ring[C::kStages][C::kStageBytes];
-  uint8_t raw[Q8 ? C::kRawStages : 1][Q8 ? C::kRawBytes : 16];
-  uint8_t scales[Q8 ? C::kRawStages : 1][8][Q8 ? 128 : 16];
+  uint8_t k[C::kKStages][C::kKBytes];
+  uint8_t v[C::kVStages][C::kVBytes];
+  uint8_t raw[Q8 ? C::kRStages : 1][Q8 ? C::kRBytes : 128];
+  uint8_t scales[Q8 ? C::kScales : 1][2][Q8 ? 8 : 1][128];   // bytes of a tile's keys and values, by page
+  float k_scale[Q8 ? C::kScales : 1][kKeys];
+  float q_scale[2][C::kBlocks][Q8 ? 128 : 1];                // of this segment's rows and the next's
   LineScan<C::kRows, C::kThreads> scan;
   int bad[D];                       // first position with a non-finite value, per column
   SegDesc segs[kSegs];
   int any_bad;
   uint32_t tmem;
   int dead;
-  uint64_t full[C::kStages], empty[C::kStages];
-  uint64_t raw_full[Q8 ? C::kRawStages : 1], raw_empty[Q8 ? C::kRawStages : 1];
+  uint64_t k_full[C::kKStages], k_empty[C::kKStages], v_full[C::kVStages], v_empty[C::kVStages];
+  uint64_t r_full[Q8 ? C::kRStages : 1], r_empty[Q8 ? C::kRStages : 1];
+  uint64_t s_bytes[Q8 ? C::kScales : 1], s_free[Q8 ? C::kScales : 1], s_ready[Q8 ? C::kScales : 1];
   uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t v_ready;                 // the current tile's values are in the ring
 };
 
 // Operand descriptors of 128-byte-swizzled tiles (8-row groups 1,024 bytes apart).  Only the low
 // word changes from one MMA to the next: the start address, in sixteen-byte units, beside a constant.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);          // SBO, version, swizzle
+constexpr uint32_t kDescHi64 = (512u >> 4) | (1u << 14) | (4u << 29);          // 64-byte rows and swizzle
 constexpr uint32_t kDescK = (16u >> 4) << 16;                                  // K-major: LBO unused
 constexpr uint32_t kDescMN = ((128u * 128u) >> 4) << 16;                       // MN-major: 64-column blocks
 
@@ -109,6 +119,19 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
       : "memory");
+}
+// The same on e4m3 operands (32 columns an MMA); HI as above.
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(HI)
+      : "memory");
+}
+// kind::f8f6f4, e4m3 A and B (both K-major), f32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -183,10 +206,27 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// (x, y) = hi + lo in e4m3 codes, |x|, |y| <= 448.
+__device__ __forceinline__ void split_e4m3(float x, float y, uint32_t& hi, uint32_t& lo) {
+  uint16_t h, l;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
+  uint32_t f;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(y - v.y), "f"(x - v.x));
+  hi = h;
+  lo = l;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
@@ -226,15 +266,23 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   ChunkSmem<D, Q8>& sm = *reinterpret_cast<ChunkSmem<D, Q8>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&sm.full[i], Q8 ? 4 : 1);
-      mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < C::kKStages; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
     }
-    if (Q8)
-      for (int i = 0; i < C::kRawStages; ++i) {
-        mbar_init(&sm.raw_full[i], 1);
-        mbar_init(&sm.raw_empty[i], 4);
-      }
+    for (int i = 0; i < C::kVStages; ++i) {
+      mbar_init(&sm.v_full[i], Q8 ? 4 : 1);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < C::kRStages; ++i) {
+      mbar_init(&sm.r_full[i], 1);
+      mbar_init(&sm.r_empty[i], 4);
+    }
+    for (int i = 0; i < C::kScales; ++i) {
+      mbar_init(&sm.s_bytes[i], 1);
+      mbar_init(&sm.s_free[i], 4);
+      mbar_init(&sm.s_ready[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_ready[i], 4);
       mbar_init(&sm.s_full[i], 1);
@@ -245,7 +293,6 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       mbar_init(&sm.seg_full[i], 1);
       mbar_init(&sm.seg_empty[i], C::kReaders);
     }
-    mbar_init(&sm.v_ready, 1);
     sm.dead = 0;
     sm.any_bad = 0;
     mbar_fence_init();
@@ -309,9 +356,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     constexpr int kBoxCols = Q8 ? C::kCols : 64;
     constexpr int kBlk = C::kCols / kBoxCols;
     const int pages = TK / box;                             // 1 to 8
-    RingPos<Q8 ? C::kRawStages : C::kStages> pos;
-    uint64_t* full = Q8 ? sm.raw_full : sm.full;
-    uint64_t* empty = Q8 ? sm.raw_empty : sm.empty;
+    RingPos<C::kKStages> kp;
+    RingPos<Q8 ? C::kRStages : C::kVStages> vp;
+    RingPos<Q8 ? C::kScales : 1> sp;
+    uint64_t* v_full = Q8 ? sm.r_full : sm.v_full;
+    uint64_t* v_empty = Q8 ? sm.r_empty : sm.v_empty;
     const int my_page = lane / kBlk, my_blk = lane % kBlk;
     while (true) {
       const SegDesc& sd = seg_wait(seg);
@@ -339,53 +388,72 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         }
         // K tiles run one ahead of V tiles; after the last K tile V is the newest tile
         const int page = !is_v ? p_next : (i + 1 < n ? p_cur : p_next);
-        wait_bar(&empty[pos.stage], pos.phase ^ 1u, &sm.dead, c.status);
-        if (lane == 0)
-          mbar_arrive_expect_tx(&full[pos.stage],
-                                Q8 ? (half == 0 ? C::kRawBytes + TK : C::kRawBytes) : C::kStageBytes);
+        const int off = (((ta + i) * TK) & ((1 << c.page_shift) - 1));   // 0 unless pages exceed a tile
+        if (Q8 && !is_v && half == 0) {                     // the tile's scale bytes, keys and values
+          wait_bar(&sm.s_free[sp.stage], sp.phase ^ 1u, &sm.dead, c.status);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.s_bytes[sp.stage], 2 * TK);
+          __syncwarp();
+          if (lane < pages) {
+            tma_load_3d(sm.scales[sp.stage][0][lane], &maps.ks, off, head, page, &sm.s_bytes[sp.stage]);
+            tma_load_3d(sm.scales[sp.stage][1][lane], &maps.vs, off, head, page, &sm.s_bytes[sp.stage]);
+          }
+          __syncwarp();
+          sp.step();
+        }
+        uint64_t* full = is_v ? &v_full[vp.stage] : &sm.k_full[kp.stage];
+        if (is_v) wait_bar(&v_empty[vp.stage], vp.phase ^ 1u, &sm.dead, c.status);
+        else wait_bar(&sm.k_empty[kp.stage], kp.phase ^ 1u, &sm.dead, c.status);
+        if (lane == 0) mbar_arrive_expect_tx(full, is_v ? (Q8 ? C::kRBytes : C::kVBytes) : C::kKBytes);
         __syncwarp();
         if (my_page < pages) {
-          const int off = (((ta + i) * TK) & ((1 << c.page_shift) - 1));   // 0 unless pages exceed a tile
-          if constexpr (Q8) {
-            tma_load_5d(sm.raw[pos.stage] + my_page * box * C::kCols, is_v ? &maps.v : &maps.k, 0, off,
-                        half, head, page, &full[pos.stage]);
-            if (half == 0)
-              tma_load_3d(sm.scales[pos.stage][my_page], is_v ? &maps.vs : &maps.ks, off, head, page,
-                          &full[pos.stage]);
-          } else {
-            tma_load_5d(sm.ring[pos.stage] + my_blk * (TK * 128) + my_page * box * 128, is_v ? &maps.v : &maps.k, 0,
-                        off, half * kBlk + my_blk, head, page, &full[pos.stage]);
-          }
+          uint8_t* dst = is_v ? (Q8 ? sm.raw[vp.stage] : sm.v[vp.stage]) : sm.k[kp.stage];
+          dst += Q8 ? my_page * box * C::kCols : my_blk * (TK * 128) + my_page * box * 128;
+          tma_load_5d(dst, is_v ? &maps.v : &maps.k, 0, off, half * kBlk + my_blk, head, page, full);
         }
         __syncwarp();
-        pos.step();
+        if (is_v) vp.step();
+        else kp.step();
       });
     }
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA (one thread)
     if (lane == 0) {
-      RingPos<C::kStages> pos;
+      RingPos<C::kKStages> kp;
+      RingPos<C::kVStages> vp;
       uint32_t cnt[2] = {0, 0};          // tiles of each block
       uint32_t s_cnt = 0;                // S buffers filled (one block)
       uint32_t q_phase[2] = {0, 0};
-      constexpr uint32_t kIdQK = idesc_bf16(128, 128);
+      constexpr uint32_t kIdQK = Q8 ? idesc_e4m3(128, 128) : idesc_bf16(128, 128);
       constexpr uint32_t kIdPV = idesc_bf16_bmn(128, C::kCols);
-      constexpr uint32_t kStage16 = C::kStageBytes / 16;
-      const uint32_t ring_k = desc_lo(smem_u32(sm.ring[0]), kDescK), ring_v = desc_lo(smem_u32(sm.ring[0]), kDescMN);
+      const uint32_t k0 = desc_lo(smem_u32(sm.k[0]), kDescK), v0 = desc_lo(smem_u32(sm.v[0]), kDescMN);
       const uint32_t q0 = desc_lo(smem_u32(sm.q[0]), kDescK);
+      auto k_lo = [&]() { return k0 + kp.stage * (C::kKBytes / 16); };
+      auto v_lo = [&]() { return v0 + vp.stage * (C::kVBytes / 16); };
       // S[buf] (+)= Q K^T over the columns of one stage; O += P[buf] V into those columns
-      auto qk_half = [&](int blk, int buf, uint32_t k_lo, int half) {
-        const uint32_t q_lo = q0 + (blk * C::kQBytes + half * (C::kCols / 64) * (128 * 128)) / 16;
+      auto qk_half = [&](int blk, int buf, uint32_t k, int half) {
+        if constexpr (!Q8) {
+          const uint32_t q = q0 + (blk * C::kQBytes + half * (C::kCols / 64) * (128 * 128)) / 16;
 #pragma unroll
-        for (int ks = 0; ks < C::kCols / 16; ++ks) {
-          const uint32_t o = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16;
-          mma_ss(buf * 128, q_lo + o, k_lo + o, kIdQK, half > 0 || ks > 0);
+          for (int ks = 0; ks < C::kCols / 16; ++ks) {
+            const uint32_t o = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16;
+            mma_ss(buf * 128, q + o, k + o, kIdQK, half > 0 || ks > 0);
+          }
+        } else {
+          // both parts of the queries against the same codes
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t q = q0 + (blk * C::kQBytes + part * (C::kQBytes / 2) + half * (128 * C::kCols)) / 16;
+#pragma unroll
+            for (int ks = 0; ks < C::kCols / 32; ++ks)
+              mma_ss_e4m3<C::kCols == 128 ? kDescHi : kDescHi64>(buf * 128, q + ks * 2, k + ks * 2, kIdQK,
+                                                                half > 0 || part > 0 || ks > 0);
+          }
         }
       };
-      auto pv_half = [&](int blk, int buf, uint32_t v_lo, int half, bool acc) {
+      auto pv_half = [&](int blk, int buf, uint32_t v, int half, bool acc) {
 #pragma unroll
         for (int ks = 0; ks < TK / 16; ++ks)
-          mma_ts(C::kO + blk * D + half * C::kCols, buf * 128 + ks * 8, v_lo + ks * (2048 / 16), kIdPV, acc || ks > 0);
+          mma_ts(C::kO + blk * D + half * C::kCols, buf * 128 + ks * 8, v + ks * (2048 / 16), kIdPV, acc || ks > 0);
       };
       while (true) {
         wait_one(&sm.seg_full[seg.stage], seg.phase, &sm.dead, c.status);
@@ -403,47 +471,43 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           q_phase[1] ^= 1u;
         }
         if constexpr (C::kBlocks == 2) {
-          wait_one(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
+          wait_one(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
           fence_after_sync();
-          qk_half(0, 0, ring_k + pos.stage * kStage16, 0);
+          qk_half(0, 0, k_lo(), 0);
           mma_commit(&sm.s_full[0]);
           if (two) {
-            qk_half(1, 1, ring_k + pos.stage * kStage16, 0);
+            qk_half(1, 1, k_lo(), 0);
             mma_commit(&sm.s_full[1]);
           }
-          mma_commit(&sm.empty[pos.stage]);
-          pos.step();
+          mma_commit(&sm.k_empty[kp.stage]);
+          kp.step();
           for (int i = 0; i < n; ++i) {
-            const RingPos<C::kStages> kpos = pos;
             const bool more = i + 1 < n;
-            if (more) pos.step();
-            const RingPos<C::kStages> vpos = pos;
-            pos.step();
-            const uint32_t k_lo = ring_k + kpos.stage * kStage16, v_lo = ring_v + vpos.stage * kStage16;
-            wait_one(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
-            mbar_arrive(&sm.v_ready);
+            wait_one(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
             wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
             fence_after_sync();
-            pv_half(0, 0, v_lo, 0, i > 0);
+            pv_half(0, 0, v_lo(), 0, i > 0);
             mma_commit(&sm.o_done[0]);
             if (more) {
-              wait_one(&sm.full[kpos.stage], kpos.phase, &sm.dead, c.status);
-              qk_half(0, 0, k_lo, 0);
+              wait_one(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
+              qk_half(0, 0, k_lo(), 0);
               mma_commit(&sm.s_full[0]);
             }
             if (two) {
               wait_one(&sm.p_ready[1], cnt[1]++ & 1u, &sm.dead, c.status);
               fence_after_sync();
-              pv_half(1, 1, v_lo, 0, i > 0);
+              pv_half(1, 1, v_lo(), 0, i > 0);
               mma_commit(&sm.o_done[1]);
             }
-            mma_commit(&sm.empty[vpos.stage]);
+            mma_commit(&sm.v_empty[vp.stage]);
+            vp.step();
             if (more) {
               if (two) {
-                qk_half(1, 1, k_lo, 0);
+                qk_half(1, 1, k_lo(), 0);
                 mma_commit(&sm.s_full[1]);
               }
-              mma_commit(&sm.empty[kpos.stage]);
+              mma_commit(&sm.k_empty[kp.stage]);
+              kp.step();
             }
           }
         } else {
@@ -451,11 +515,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             const int buf = (int)(s_cnt & 1u);
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
-              wait_one(&sm.full[pos.stage], pos.phase, &sm.dead, c.status);
+              wait_one(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
               fence_after_sync();
-              qk_half(0, buf, ring_k + pos.stage * kStage16, h);
-              mma_commit(&sm.empty[pos.stage]);
-              pos.step();
+              qk_half(0, buf, k_lo(), h);
+              mma_commit(&sm.k_empty[kp.stage]);
+              kp.step();
             }
             mma_commit(&sm.s_full[buf]);
             ++s_cnt;
@@ -464,18 +528,14 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           if (n > 1) qk_tile();
           for (int i = 0; i < n; ++i) {
             const int buf = (int)(cnt[0] & 1u);
-            RingPos<C::kStages> vpos = pos;
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h, vpos.step())
-              wait_one(&sm.full[vpos.stage], vpos.phase, &sm.dead, c.status);
-            mbar_arrive(&sm.v_ready);
             wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
             fence_after_sync();
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
-              pv_half(0, buf, ring_v + pos.stage * kStage16, h, i > 0);
-              mma_commit(&sm.empty[pos.stage]);
-              pos.step();
+              wait_one(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
+              pv_half(0, buf, v_lo(), h, i > 0);
+              mma_commit(&sm.v_empty[vp.stage]);
+              vp.step();
             }
             mma_commit(&sm.o_done[0]);
             if (i + 2 < n) qk_tile();
@@ -489,8 +549,9 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     if constexpr (C::kConvRegs && C::kConvRegs < C::kLaunchRegs) regs_down<C::kConvRegs>();
     const int ct = tid - C::kConvWarp * 32;
     const int box = min(1 << c.page_shift, TK), shift = 31 - __clz(box);
-    RingPos<C::kRawStages ? C::kRawStages : 1> src;
-    RingPos<C::kStages> dst;
+    RingPos<Q8 ? C::kRStages : 1> src;
+    RingPos<C::kVStages> dst;
+    RingPos<Q8 ? C::kScales : 1> ks, vs;
     constexpr int kPer = C::kCols / 8;                      // 8-element pieces of a row
     const int piece = ct % kPer;
     while (true) {
@@ -498,33 +559,52 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       seg_done(seg);
       if (n < 0) break;
       if (n == 0) continue;
-      uint32_t byte[128 * kPer / 128] = {};                  // scale bytes of this thread's rows
-      ring_order<C::kHalves>(n, [&](bool, int, int half) {
-        wait_bar(&sm.raw_full[src.stage], src.phase, &sm.dead, c.status);
-        wait_bar(&sm.empty[dst.stage], dst.phase ^ 1u, &sm.dead, c.status);
+      ring_order<C::kHalves>(n, [&](bool is_v, int, int half) {
+        if (!is_v) {
+          // The scales of a tile's keys, one per thread.  Their place was last read by the softmax
+          // four tiles ago, which is over: a V stage of a later tile has come back since.
+          if (half == 0) {
+            wait_bar(&sm.s_bytes[ks.stage], ks.phase, &sm.dead, c.status);
+            sm.k_scale[ks.stage][ct] = scale_f32(sm.scales[ks.stage][0][ct >> shift][ct & (box - 1)]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_ready[ks.stage]);
+            ks.step();
+          }
+          return;
+        }
+        wait_bar(&sm.r_full[src.stage], src.phase, &sm.dead, c.status);
+        wait_bar(&sm.v_empty[dst.stage], dst.phase ^ 1u, &sm.dead, c.status);
         const uint8_t* raw = sm.raw[src.stage];
-        uint8_t* out = sm.ring[dst.stage];
-#pragma unroll
+        uint8_t* out = sm.v[dst.stage];
+#pragma unroll 8
         for (int j = 0; j < kPer; ++j) {
           const int row = j * (128 / kPer) + ct / kPer;
-          // a tile's scale bytes come with its first half
-          if (half == 0) byte[j] = sm.scales[src.stage][row >> shift][row & (box - 1)];
+          const uint32_t bb = sm.scales[vs.stage][1][row >> shift][row & (box - 1)];
           const uint2 u = *reinterpret_cast<const uint2*>(raw + row * C::kCols + piece * 8);
+          // the code's bits are the value times 2^-120: one multiply by 2^120 times the scale where
+          // that is a bf16 value, else two
+          const uint32_t f = bb <= 134 ? (bb + 120) << 7 : 0x7b80u, f2 = f | (f << 16);
           uint32_t w[4];
-          e4m3x4_to_bf16(u.x, w[0], w[1]);
-          e4m3x4_to_bf16(u.y, w[2], w[3]);
-          const uint32_t s = scale_bits(byte[j]), s2 = s | (s << 16);
+          w[0] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.x, 0, 0x1404)), f2);
+          w[1] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.x, 0, 0x3424)), f2);
+          w[2] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.y, 0, 0x1404)), f2);
+          w[3] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.y, 0, 0x3424)), f2);
+          if (bb > 134) {
+            const uint32_t s = scale_bits(bb), s2 = s | (s << 16);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = mul_bf16x2(w[e], s2);
+            for (int e = 0; e < 4; ++e) w[e] = mul_bf16x2(w[e], s2);
+          }
           *reinterpret_cast<uint4*>(out + (piece >> 3) * (TK * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sm.full[dst.stage]);
-          mbar_arrive(&sm.raw_empty[src.stage]);
+          mbar_arrive(&sm.v_full[dst.stage]);
+          mbar_arrive(&sm.r_empty[src.stage]);
+          if (half == C::kHalves - 1) mbar_arrive(&sm.s_free[vs.stage]);
         }
+        if (half == C::kHalves - 1) vs.step();
         src.step();
         dst.step();
       });
@@ -535,24 +615,72 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     const int blk = warp >> 2, r = tid & 127, lbase = (warp & 3) * 32;
     const uint32_t tl = tmem + ((uint32_t)lbase << 16);
     uint32_t cnt = 0;                  // tiles of this block so far
-    RingPos<C::kStages> ring;          // first stage of the current segment (block 0 only)
+    RingPos<C::kVStages> vp;           // block 0 follows the V ring
+    RingPos<Q8 ? C::kScales : 1> sp;   // 8-bit: the scales' ring
+    uint32_t loads = 0;                // segments whose queries this block has loaded
     auto load_q = [&](const SegDesc& s) {
       // D / 8 lanes take a row at a time: 16-byte pieces, swizzled, all in flight at once
       const int rows = (int)min((long long)R, (long long)s.tokens * a.g - (long long)s.tile * R) - blk * 128;
-      constexpr int kPer = D / 8;
+      constexpr int kPer = D / 8, kStep = 128 / kPer;
       const int piece = r % kPer;
-      const uint32_t dst = smem_u32(sm.q[blk]) + (piece >> 3) * (128 * 128);
       int t = (s.tile * R + blk * 128 + r / kPer) / a.g;
       int hh = s.tile * R + blk * 128 + r / kPer - t * a.g;
-#pragma unroll 4
-      for (int row = r / kPer; row < 128; row += 128 / kPer) {
-        const __nv_bfloat16* src =
-            a.q + (s.row0 + t) * a.q_ld + (s.head * a.g + hh) * a.q_head_ld + piece * 8;
-        cp_async16(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), row < rows ? src : a.q, row < rows);
-        hh += 128 / kPer;
+      auto source = [&]() {
+        return a.q + (s.row0 + t) * a.q_ld + (s.head * a.g + hh) * a.q_head_ld + piece * 8;
+      };
+      auto advance = [&]() {
+        hh += kStep;
         while (hh >= a.g) { hh -= a.g; ++t; }
+      };
+      if constexpr (!Q8) {
+        const uint32_t dst = smem_u32(sm.q[blk]) + (piece >> 3) * (128 * 128);
+#pragma unroll 4
+        for (int row = r / kPer; row < 128; row += kStep) {
+          cp_async16(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), row < rows ? source() : a.q, row < rows);
+          advance();
+        }
+        cp_async_wait_all();
+      } else {
+        // A row, brought to (224, 448] by a power of two, is the sum of two e4m3 vectors: the codes
+        // nearest to it, and what they leave, which fits their four significant bits again (bf16
+        // has eight).  Elements below 2^-10 of the row's largest lose bits at 2^-18 of it.
+        constexpr int kBatch = 8;
+        for (int row0 = r / kPer; row0 < 128; row0 += kStep * kBatch) {
+          uint4 u[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            u[j] = make_uint4(0, 0, 0, 0);
+            if (row0 + j * kStep < rows) u[j] = __ldg(reinterpret_cast<const uint4*>(source()));
+            advance();
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int row = row0 + j * kStep;
+            const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = kPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int bb = scale_byte(top);
+            const float inv = __uint_as_float((uint32_t)(254 - (bb == 255 ? 127 : bb)) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              split_e4m3(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
+            if (row < 128) {
+              if (piece == 0) sm.q_scale[loads & 1u][blk][row] = scale_f32(bb) * a.scale_log2;
+              const int col = piece * 8;                             // byte in the row
+              uint8_t* d = sm.q[blk] + (col >> 7) * (128 * 128) +
+                           (C::kCols == 128 ? row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
+                                            : row * 64 + (((col >> 4) ^ ((row >> 1) & 3)) << 4)) + (col & 8);
+              *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+              *reinterpret_cast<uint2*>(d + C::kQBytes / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            }
+          }
+        }
       }
-      cp_async_wait_all();
+      ++loads;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_ready[blk]);
@@ -581,6 +709,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           uint4* o = reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D);
           for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
         }
+        if (Q8)
+          for (int i = 0; i < n; ++i) sp.step();      // the other block's tiles
         const SegDesc& next = seg_wait(ahead_seg);
         if (active(next)) load_q(next);
       } else {
@@ -602,6 +732,24 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           tmem_wait_ld();
 #pragma unroll
           for (int cc = 0; cc < 8; ++cc) reg_fence16(v + cc * 16);
+          float scale = a.scale_log2;
+          if constexpr (Q8) {
+            // each key's scale here, the row's with the softmax scale below; a hidden key's scale
+            // may be anything, so hide after scaling
+            scale = sm.q_scale[(loads - 1) & 1u][blk][r];
+            wait_bar(&sm.s_ready[sp.stage], sp.phase, &sm.dead, c.status);
+            const float4* f = reinterpret_cast<const float4*>(sm.k_scale[sp.stage]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float4 g = f[e];
+              float y[4];
+              unpair(mul2(pair(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])), pair(g.x, g.y)), y[0], y[1]);
+              unpair(mul2(pair(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])), pair(g.z, g.w)), y[2], y[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[4 * e + k] = __float_as_uint(y[k]);
+            }
+            sp.step();
+          }
           if (partial) {
 #pragma unroll
             for (int e = 0; e < 128; ++e)
@@ -613,7 +761,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               xs[j] = fmaxf(xs[j], fmaxf(__uint_as_float(v[e + 2 * j]), __uint_as_float(v[e + 2 * j + 1])));
-          const float x = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])) * a.scale_log2;
+          const float x = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])) * scale;
           if (__any_sync(0xffffffffu, x > m + 8.f)) {
             const float mn = fmaxf(m, x);
             const float f = mn == m ? 1.f : ex2f(m - mn);
@@ -634,7 +782,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), ref2 = pair(-ref, -ref);
+          const uint64_t sc2 = pair(scale, scale), ref2 = pair(-ref, -ref);
           uint64_t l2[2] = {pair(l, 0.f), pair(0.f, 0.f)};
 #pragma unroll
           for (int cc = 0; cc < 8; ++cc) {
@@ -658,23 +806,20 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             l = (l0 + l1) + (l3 + l4);
           }
           // A parity wait tells a phase from the one before it only when no phase is skipped: so
-          // v_ready is waited for at every tile (the ring's own barriers, which K tiles use too,
-          // would not do), and so is o_done where s_full does not imply the product before.
-          if (blk == 0) wait_bar(&sm.v_ready, cnt & 1u, &sm.dead, c.status);
+          // block 0 waits for every V stage, needed or not, and so is o_done waited for where
+          // s_full does not imply the product before.
           if (C::kBlocks == 1 && i > 0) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
-          if (partial && blk == 0) {
-            // this tile's values: zero past the end, zero and noted where not finite
-            RingPos<C::kStages> vp = ring;
-            const int ahead = C::kHalves * (min(i + 2, n) + i);
-            vp.phase ^= (uint32_t)((vp.stage + ahead) / C::kStages) & 1u;
-            vp.stage = (vp.stage + ahead) % C::kStages;
+          if (blk == 0) {
+            // a causal-edge tile's values: zero past the end, zero and noted where not finite
             for (int h = 0; h < C::kHalves; ++h, vp.step()) {
+              wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
+              if (!partial) continue;
               // keys from the first row's position on (earlier ones are seen by all rows)
               const int j0 = max(0, pos_min + 1 - k0), j1 = TK;
               constexpr int kPer = C::kCols / 8;
               const int piece = r % kPer;
               for (int j = j0 + r / kPer; j < j1; j += 128 / kPer) {
-                uint4* p = reinterpret_cast<uint4*>(sm.ring[vp.stage] + (piece >> 3) * (TK * 128) + j * 128 +
+                uint4* p = reinterpret_cast<uint4*>(sm.v[vp.stage] + (piece >> 3) * (TK * 128) + j * 128 +
                                                     (((piece & 7) ^ (j & 7)) << 4));
                 if (k0 + j >= len) {
                   *p = make_uint4(0, 0, 0, 0);
@@ -697,7 +842,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
                 }
               }
             }
-            fence_proxy_async_smem();
+            if (partial) fence_proxy_async_smem();
           }
           __syncwarp();
           tmem_wait_st();
@@ -766,11 +911,6 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         }
         fence_before_sync();           // O has been read before the next tile's p_ready
       }
-      if (n > 0) {
-        const int ahead = 2 * n * C::kHalves;
-        ring.phase ^= (uint32_t)((ring.stage + ahead) / C::kStages) & 1u;
-        ring.stage = (ring.stage + ahead) % C::kStages;
-      }
       // both blocks are done with the notes on non-finite values
       if (bar_any(1, C::kSoftWarps * 32, *(volatile int*)&sm.any_bad != 0)) {
         for (int i = tid; i < D; i += C::kSoftWarps * 32) sm.bad[i] = INT32_MAX;
@@ -796,7 +936,7 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   if (set != cudaSuccess) return GDN_ERR_CUDA;
   KvMaps maps;
   const int P = 1 << c.page_shift;
-  if (!make_tile_maps(c, P < kKeys ? P : kKeys, Q8 ? C::kCols : 64, !Q8, &maps)) return GDN_ERR_CUDA;
+  if (!make_tile_maps(c, P < kKeys ? P : kKeys, Q8 ? C::kCols : 64, &maps)) return GDN_ERR_CUDA;
   const int grid = sms, fix = 128 * a.g;
   const int least = 512 * a.g;
   int rc = launch_dependent(chunk_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,

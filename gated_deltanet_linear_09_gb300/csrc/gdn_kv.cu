@@ -28,16 +28,6 @@ __device__ __forceinline__ void unpack8(const uint4 u, float* v) {
   }
 }
 
-// The exponent byte of a vector whose largest magnitude has the bf16 bits `top` (sign cleared):
-// 1.m * 2^(E - 127) <= 448 = 1.75 * 2^8 asks for 2^(E - 135), one more when 1.m > 1.75.  Bytes
-// below 10 would put the least e4m3 value times the scale outside bf16's normal range.
-__device__ __forceinline__ int scale_byte(uint32_t top) {
-  if (top >= 0x7f80u) return 255;
-  if (top == 0) return 127;
-  const int e = (int)(top >> 7) - 8 + ((top & 0x7f) > 0x60 ? 1 : 0);
-  return e < 10 ? 10 : e;
-}
-
 // 8 e4m3 codes -> 8 bf16 (4 words), times the scale of exponent byte b.
 __device__ __forceinline__ uint4 dequant8(uint2 u, uint32_t b) {
   uint32_t w[4];

@@ -65,10 +65,10 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // mantissa, moved to the low four exponent bits and the high three mantissa bits of a bf16, are
 // the value times 2^-120 (the biases 127 and 7 apart; subnormals included), so one exact multiply
 // by 2^120 finishes.  The NaN codes 0x7f / 0xff (which the cache never holds) come out as +-480.
-__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t w) {
-  const uint32_t u = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-  return mul_bf16x2(u, 0x7b807b80u);
+__device__ __forceinline__ uint32_t e4m3_hi_bits(uint32_t w) {
+  return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
 }
+__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t w) { return mul_bf16x2(e4m3_hi_bits(w), 0x7b807b80u); }
 
 // Four codes b0..b3 (b0 lowest) -> the bf16 pairs (b0, b1) and (b2, b3).
 __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& p01, uint32_t& p23) {
@@ -81,5 +81,15 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t b) { return b == 255 ? 0
 
 // The same as an f32.
 __device__ __forceinline__ float scale_f32(uint32_t b) { return __uint_as_float(scale_bits(b) << 16); }
+
+// The exponent byte of a vector whose largest magnitude has the bf16 bits `top` (sign cleared):
+// 1.m * 2^(E - 127) <= 448 = 1.75 * 2^8 asks for 2^(E - 135), one more when 1.m > 1.75.  Bytes
+// below 10 would put the least e4m3 value times the scale outside bf16's normal range.
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+  if (top >= 0x7f80u) return 255;
+  if (top == 0) return 127;
+  const int e = (int)(top >> 7) - 8 + ((top & 0x7f) > 0x60 ? 1 : 0);
+  return e < 10 ? 10 : e;
+}
 
 }  // namespace gdn

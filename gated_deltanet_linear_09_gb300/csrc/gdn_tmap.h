@@ -17,8 +17,9 @@ struct KvMaps {
 // in shared memory, 128-byte swizzled (64-byte rows and swizzle when head_dim is 64 bytes).
 bool make_kv_maps(const KvView& c, int rows, KvMaps* maps);
 
-// Maps whose box is `rows` keys by `cols` columns: [rows][cols], swizzled over its row's bytes or not.
-bool make_tile_maps(const KvView& c, int rows, int cols, bool swizzled, KvMaps* maps);
+// Maps whose box is `rows` keys by `cols` columns: [rows][cols], swizzled over the row's bytes -- all
+// but 8-bit values, which a warp reads to convert them.
+bool make_tile_maps(const KvView& c, int rows, int cols, KvMaps* maps);
 
 namespace attn {
 int rows_grid(int D, int sms);
