@@ -88,7 +88,7 @@ struct __align__(1024) ChunkSmem {
   uint8_t raw[Q8 ? C::kRStages : 1][Q8 ? C::kRBytes : 128];
   uint8_t scales[Q8 ? C::kScales : 1][2][Q8 ? 8 : 1][128];   // bytes of a tile's keys and values, by page
   float k_scale[Q8 ? C::kScales : 1][kKeys];
-  float q_scale[2][C::kBlocks][Q8 ? 128 : 1];                // of this segment's rows and the next's
+  float q_scale[C::kBlocks][Q8 ? 128 : 1];
   LineScan<C::kRows, C::kThreads> scan;
   int bad[D];                       // first position with a non-finite value, per column
   SegDesc segs[kSegs];
@@ -417,6 +417,9 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     }
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA (one thread)
+    // The tensor pipe queues only a few MMAs, so what this thread does between them leaves the pipe
+    // idle (a commit costs some 40 cycles, a wait that finds its phase complete twice that): it
+    // waits for p_ready alone where that implies the tiles are there, and commits what is needed.
     if (lane == 0) {
       RingPos<C::kKStages> kp;
       RingPos<C::kVStages> vp;
@@ -481,35 +484,39 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           }
           mma_commit(&sm.k_empty[kp.stage]);
           kp.step();
-          for (int i = 0; i < n; ++i) {
-            const bool more = i + 1 < n;
-            wait_one(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
+          // Block 0's softmax of tile i has seen V(i) and K(i + 1) arrive before it says p_ready.
+          for (int i = 0; i + 1 < n; ++i) {
             wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
             fence_after_sync();
             pv_half(0, 0, v_lo(), 0, i > 0);
-            mma_commit(&sm.o_done[0]);
-            if (more) {
-              wait_one(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
-              qk_half(0, 0, k_lo(), 0);
-              mma_commit(&sm.s_full[0]);
-            }
+            qk_half(0, 0, k_lo(), 0);
+            mma_commit(&sm.s_full[0]);
             if (two) {
               wait_one(&sm.p_ready[1], cnt[1]++ & 1u, &sm.dead, c.status);
               fence_after_sync();
               pv_half(1, 1, v_lo(), 0, i > 0);
-              mma_commit(&sm.o_done[1]);
+              mma_commit(&sm.v_empty[vp.stage]);
+              qk_half(1, 1, k_lo(), 0);
+              mma_commit(&sm.s_full[1]);
+            } else {
+              mma_commit(&sm.v_empty[vp.stage]);
             }
-            mma_commit(&sm.v_empty[vp.stage]);
+            mma_commit(&sm.k_empty[kp.stage]);
             vp.step();
-            if (more) {
-              if (two) {
-                qk_half(1, 1, k_lo(), 0);
-                mma_commit(&sm.s_full[1]);
-              }
-              mma_commit(&sm.k_empty[kp.stage]);
-              kp.step();
-            }
+            kp.step();
           }
+          wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
+          fence_after_sync();
+          pv_half(0, 0, v_lo(), 0, n > 1);
+          mma_commit(&sm.o_done[0]);
+          if (two) {
+            wait_one(&sm.p_ready[1], cnt[1]++ & 1u, &sm.dead, c.status);
+            fence_after_sync();
+            pv_half(1, 1, v_lo(), 0, n > 1);
+            mma_commit(&sm.o_done[1]);
+          }
+          mma_commit(&sm.v_empty[vp.stage]);
+          vp.step();
         } else {
           auto qk_tile = [&]() {
             const int buf = (int)(s_cnt & 1u);
@@ -532,7 +539,6 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             fence_after_sync();
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
-              wait_one(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
               pv_half(0, buf, v_lo(), h, i > 0);
               mma_commit(&sm.v_empty[vp.stage]);
               vp.step();
@@ -615,29 +621,27 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     const int blk = warp >> 2, r = tid & 127, lbase = (warp & 3) * 32;
     const uint32_t tl = tmem + ((uint32_t)lbase << 16);
     uint32_t cnt = 0;                  // tiles of this block so far
-    RingPos<C::kVStages> vp;           // block 0 follows the V ring
+    uint32_t segments = 0;
+    RingPos<C::kVStages> vp;           // block 0 follows the rings
+    RingPos<C::kKStages> kp;
     RingPos<Q8 ? C::kScales : 1> sp;   // 8-bit: the scales' ring
-    uint32_t loads = 0;                // segments whose queries this block has loaded
     auto load_q = [&](const SegDesc& s) {
-      // D / 8 lanes take a row at a time: 16-byte pieces, swizzled, all in flight at once
-      const int rows = (int)min((long long)R, (long long)s.tokens * a.g - (long long)s.tile * R) - blk * 128;
-      constexpr int kPer = D / 8, kStep = 128 / kPer;
-      const int piece = r % kPer;
-      int t = (s.tile * R + blk * 128 + r / kPer) / a.g;
-      int hh = s.tile * R + blk * 128 + r / kPer - t * a.g;
-      auto source = [&]() {
-        return a.q + (s.row0 + t) * a.q_ld + (s.head * a.g + hh) * a.q_head_ld + piece * 8;
-      };
-      auto advance = [&]() {
-        hh += kStep;
-        while (hh >= a.g) { hh -= a.g; ++t; }
-      };
+      // A warp loads its own 32 rows (lane i knows where row i is), D / 8 lanes a row at a time:
+      // 16-byte pieces, swizzled, all in flight at once.
+      const int base = s.tile * R + blk * 128 + lbase;
+      const int rows = (int)min(32LL, (long long)s.tokens * a.g - base);      // may be negative
+      constexpr int kPer = D / 8, kStep = 32 / kPer;
+      const int piece = lane % kPer, first = lane / kPer;
+      const int mine = min(base + lane, s.tokens * a.g - 1);
+      const int t = mine / a.g;
+      const long long where = (s.row0 + t) * a.q_ld + (s.head * a.g + (mine - t * a.g)) * a.q_head_ld;
       if constexpr (!Q8) {
-        const uint32_t dst = smem_u32(sm.q[blk]) + (piece >> 3) * (128 * 128);
-#pragma unroll 4
-        for (int row = r / kPer; row < 128; row += kStep) {
-          cp_async16(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), row < rows ? source() : a.q, row < rows);
-          advance();
+        const uint32_t dst = smem_u32(sm.q[blk]) + (piece >> 3) * (128 * 128) + lbase * 128;
+#pragma unroll 8
+        for (int j = 0; j < 32 / kStep; ++j) {
+          const int row = j * kStep + first;
+          const long long w = __shfl_sync(0xffffffffu, where, row);
+          cp_async16(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), a.q + w + piece * 8, row < rows);
         }
         cp_async_wait_all();
       } else {
@@ -645,17 +649,18 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         // nearest to it, and what they leave, which fits their four significant bits again (bf16
         // has eight).  Elements below 2^-10 of the row's largest lose bits at 2^-18 of it.
         constexpr int kBatch = 8;
-        for (int row0 = r / kPer; row0 < 128; row0 += kStep * kBatch) {
+        for (int j0 = 0; j0 < 32 / kStep; j0 += kBatch) {
           uint4 u[kBatch];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
+            const int row = (j0 + j) * kStep + first;
+            const long long w = __shfl_sync(0xffffffffu, where, row & 31);
             u[j] = make_uint4(0, 0, 0, 0);
-            if (row0 + j * kStep < rows) u[j] = __ldg(reinterpret_cast<const uint4*>(source()));
-            advance();
+            if (row < rows) u[j] = __ldg(reinterpret_cast<const uint4*>(a.q + w + piece * 8));
           }
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int row = row0 + j * kStep;
+            const int row = (j0 + j) * kStep + first;
             const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
             uint32_t top = 0;
 #pragma unroll
@@ -668,19 +673,18 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               split_e4m3(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
-            if (row < 128) {
-              if (piece == 0) sm.q_scale[loads & 1u][blk][row] = scale_f32(bb) * a.scale_log2;
+            if (row < 32) {
+              if (piece == 0) sm.q_scale[blk][lbase + row] = scale_f32(bb) * a.scale_log2;
               const int col = piece * 8;                             // byte in the row
               uint8_t* d = sm.q[blk] + (col >> 7) * (128 * 128) +
-                           (C::kCols == 128 ? row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
-                                            : row * 64 + (((col >> 4) ^ ((row >> 1) & 3)) << 4)) + (col & 8);
+                           (C::kCols == 128 ? (lbase + row) * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
+                                            : (lbase + row) * 64 + (((col >> 4) ^ ((row >> 1) & 3)) << 4)) + (col & 8);
               *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
               *reinterpret_cast<uint2*>(d + C::kQBytes / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
             }
           }
         }
       }
-      ++loads;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_ready[blk]);
@@ -736,7 +740,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           if constexpr (Q8) {
             // each key's scale here, the row's with the softmax scale below; a hidden key's scale
             // may be anything, so hide after scaling
-            scale = sm.q_scale[(loads - 1) & 1u][blk][r];
+            scale = sm.q_scale[blk][r];
             wait_bar(&sm.s_ready[sp.stage], sp.phase, &sm.dead, c.status);
             const float4* f = reinterpret_cast<const float4*>(sm.k_scale[sp.stage]);
 #pragma unroll
@@ -768,7 +772,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             m = mn;
             l *= f;
             if (i > 0) {
-              wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
+              // two blocks: s_full of this tile came after the product of the one before
+              if (C::kBlocks == 1) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
               fence_after_sync();
 #pragma unroll 1
               for (int d = 0; d < D; d += 16) {
@@ -806,10 +811,17 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             l = (l0 + l1) + (l3 + l4);
           }
           // A parity wait tells a phase from the one before it only when no phase is skipped: so
-          // block 0 waits for every V stage, needed or not, and so is o_done waited for where
-          // s_full does not imply the product before.
+          // block 0 waits for every stage of the rings, needed or not, and one block alone for
+          // every o_done.
           if (C::kBlocks == 1 && i > 0) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
           if (blk == 0) {
+            if (C::kBlocks == 2) {
+              if (i == 0) kp.step();
+              if (i + 1 < n) {
+                wait_bar(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
+                kp.step();
+              }
+            }
             // a causal-edge tile's values: zero past the end, zero and noted where not finite
             for (int h = 0; h < C::kHalves; ++h, vp.step()) {
               wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
@@ -850,56 +862,71 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.p_ready[blk]);
         }
-        // the next tile's queries, before this one's output: every QK of this one has completed
-        const SegDesc& next = seg_wait(ahead_seg);
-        if (active(next)) load_q(next);
-        wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
+        // two blocks: one phase of o_done a segment
+        wait_bar(&sm.o_done[blk], (C::kBlocks == 2 ? segments++ : cnt - 1) & 1u, &sm.dead, c.status);
         fence_after_sync();
         const bool whole = cur.whole, bad = *(volatile int*)&sm.any_bad != 0;
         int tok = 0, head = 0;
-        if (live) row_of(SeqInfo{cur.row0, cur.tokens, cur.len}, a.g, cur.head, row, &tok, &head);
+        row_of(SeqInfo{cur.row0, cur.tokens, cur.len}, a.g, cur.head, min(row, last_row), &tok, &head);
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
         const int pr = blk * 128 + r;
-        float* prow = Partials<R, D>::rows(a.ws, cta, cur.slot) + (size_t)pr * D;
-        const uint4* gate = a.gate && whole && live
-                                ? reinterpret_cast<const uint4*>(a.gate + tok * a.gate_ld + head * a.gate_head_ld)
-                                : nullptr;
-        uint4* orow = reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D);
+        float* prow = Partials<R, D>::rows(a.ws, cta, cur.slot) + (size_t)(blk * 128 + lbase) * D;
+        // The queries have been read: the place of this warp's 32 rows turns rows held by a thread
+        // each into rows of consecutive lanes, D / 2 columns of f32 at a time.
+        constexpr bool kNarrow = Q8 && D == 64;                 // 64-byte query rows, in two parts
+        auto place = [&](int rr, int piece) {
+          return reinterpret_cast<float4*>(
+              sm.q[blk] + (kNarrow ? (piece >> 2) * 8192 + (lbase + rr) * 64 + (((piece & 3) ^ ((rr >> 1) & 3)) << 4)
+                                   : (piece >> 3) * 16384 + (lbase + rr) * 128 + (((piece & 7) ^ (rr & 7)) << 4)));
+        };
+        const int rows32 = min(32, rows - blk * 128 - lbase);
+        const long long orow = ((long long)tok * a.Hq + head) * D;
+        const long long grow = a.gate ? tok * a.gate_ld + head * a.gate_head_ld : 0;
+        constexpr int kPer = D / 8, kStep = 32 / kPer;          // 16-byte pieces of half a row
+        const int piece = lane % kPer, first = lane / kPer;
 #pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
-          uint4 z[4];
-          if (gate)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = __ldg(gate + d / 8 + e);
-          uint32_t o[32];
-          tmem_ld32_nw(tl + C::kO + blk * D + d, o);
-          tmem_wait_ld();
-          reg_fence16(o);
-          reg_fence16(o + 16);
-          if (live) {
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+          for (int d = 0; d < D / 2; d += 32) {
+            uint32_t o[32];
+            tmem_ld32_nw(tl + C::kO + blk * D + half * (D / 2) + d, o);
+            tmem_wait_ld();
+            reg_fence16(o);
+            reg_fence16(o + 16);
             if (bad) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (sm.bad[d + e] <= pos) o[e] = 0x7fffffffu;
+                if (sm.bad[half * (D / 2) + d + e] <= pos) o[e] = 0x7fffffffu;
             }
-            if (whole) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float y[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(o[8 * e + k]) * inv;
-                if (gate) {
-                  const uint32_t zw[4] = {z[e].x, z[e].y, z[e].z, z[e].w};
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    y[k] *= gate_of(__uint_as_float(k & 1 ? zw[k >> 1] & 0xffff0000u : zw[k >> 1] << 16));
+            for (int e = 0; e < 32; e += 4)
+              *place(lane, (d + e) / 4) =
+                  make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                              __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+          }
+          __syncwarp();
+          const int col = half * (D / 2) + piece * 4;
+          if (whole) {
+#pragma unroll 4
+            for (int j = 0; j < 32 / kStep; ++j) {
+              const int rr = j * kStep + first;
+              const long long at = __shfl_sync(0xffffffffu, orow, rr);
+              float4 y = *place(rr, piece);
+              if (a.gate) {
+                const long long ga = __shfl_sync(0xffffffffu, grow, rr);
+                if (rr < rows32) {
+                  const float4 z = Act<__nv_bfloat16>::ldg4(a.gate + ga + col);
+                  y.x *= gate_of(z.x); y.y *= gate_of(z.y); y.z *= gate_of(z.z); y.w *= gate_of(z.w);
                 }
-                orow[d / 8 + e] = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
               }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                __stcg(reinterpret_cast<uint4*>(prow + d + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+              if (rr < rows32) Act<__nv_bfloat16>::store4(a.out + at + col, y);
+            }
+          } else {
+#pragma unroll 4
+            for (int j = 0; j < 32 / kStep; ++j) {
+              const int rr = j * kStep + first;
+              const float4 y = *place(rr, piece);
+              if (rr < rows32) __stcg(reinterpret_cast<float4*>(prow + (size_t)rr * D + col), y);
             }
           }
           __syncwarp();
@@ -909,7 +936,10 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, cur.slot) + 2 * pr),
                  make_float2(l != l ? INFINITY : m, l));
         }
-        fence_before_sync();           // O has been read before the next tile's p_ready
+        fence_before_sync();           // O has been read before the next segment's p_ready
+        __syncwarp();
+        const SegDesc& next = seg_wait(ahead_seg);
+        if (active(next)) load_q(next);
       }
       // both blocks are done with the notes on non-finite values
       if (bar_any(1, C::kSoftWarps * 32, *(volatile int*)&sm.any_bad != 0)) {
