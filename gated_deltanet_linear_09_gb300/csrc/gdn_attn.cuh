@@ -52,7 +52,7 @@ struct SeqWork {
 template <int R>
 __device__ __forceinline__ SeqWork seq_work(const SeqInfo& s, int g, int fix) {
   SeqWork w;
-  w.tiles = (int)(((long long)s.tokens * g + R - 1) / R);
+  w.tiles = (s.tokens * g + R - 1) / R;
   w.base = (long long)max(s.len - s.tokens, 0) * g + fix;
   return w;
 }
@@ -64,15 +64,34 @@ struct Segment {
   int ta, tb, nt;       // key tiles [ta, tb) of the tile's nt
   bool owns_empty;      // the tile sees no key and this piece holds its start: write zeros
   int slot;             // partial slot: 0 when the piece begins inside the tile, else 1
+  bool split;           // the tile begins in this piece and ends in a later one
   __device__ __forceinline__ bool whole() const { return ta == 0 && tb == nt; }
 };
 
 // Keys the rows of a tile see at most: those of its last row.
 template <int R>
 __device__ __forceinline__ int tile_keys(const SeqInfo& s, int g, int tile) {
-  const long long last = min((long long)(tile + 1) * R, (long long)s.tokens * g) - 1;
-  return max(0, s.len - s.tokens + (int)(last / g) + 1);
+  const int last = min((tile + 1) * R, s.tokens * g) - 1;        // rows fit 31 bits
+  return max(0, s.len - s.tokens + last / g + 1);
 }
+
+// The line cut into pieces as equal as whole units allow: the first `more` are one unit longer.
+struct Pieces {
+  int count, more;
+  long long each;
+  __device__ __forceinline__ long long bound(int i) const { return each * i + min(i, more); }
+  // the piece that holds line position x
+  __device__ __forceinline__ int at(long long x) const {
+    const long long longer = (each + 1) * more;
+    return x < longer ? (int)(x / (each + 1)) : more + (int)((x - longer) / each);
+  }
+};
+
+// A place on the line.
+struct Located {
+  int seq;
+  long long into;     // offset inside the sequence
+};
 
 // Walks the tiles of a piece of the line.  All arithmetic is 64-bit and the same in every thread.
 template <int R, int TK>
@@ -81,34 +100,63 @@ struct SegIter {
   int page_shift, H, g, fix;
   long long left;           // work left in the piece
   long long off;            // offset of the piece inside the current tile
+  long long line;           // the current tile's place on the line
+  Pieces pieces;
+  int piece;
   int s, h, k;              // current sequence, head, tile
   SeqInfo info;
   SeqWork work;
   bool bad;
 
   __device__ __forceinline__ void start(const KvBatchView* bt, int shift, int heads, int group, int fix_,
-                                        int seq, long long into, long long amount) {
-    b = bt; page_shift = shift; H = heads; g = group; fix = fix_; left = amount; s = seq; bad = false;
+                                        const Pieces& p, int index, const Located& at) {
+    b = bt; page_shift = shift; H = heads; g = group; fix = fix_; pieces = p; piece = index; bad = false;
+    left = p.bound(index + 1) - p.bound(index);
     if (left <= 0) return;
+    s = at.seq;
     info = load_seq(*b, page_shift, s, &bad);
     work = seq_work<R>(info, g, fix);
     const long long per = work.prefix(work.tiles, R);
+    long long into = at.into;
     h = 0;
-    if (into >= per && per > 0) {        // heads are few: a division would cost as much
-      h = (int)(into / per);
+    if (into >= per && per > 0) {
+      h = (per >> 32) == 0 && (into >> 32) == 0 ? (int)((unsigned)into / (unsigned)per) : (int)(into / per);
+      into -= (long long)h * per;
     }
-    into -= (long long)h * per;
-    int lo = 0, hi = work.tiles;      // largest k with prefix(k) <= into
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (work.prefix(mid, R) <= into) lo = mid; else hi = mid;
-    }
-    k = lo;
+    // largest k with prefix(k) <= into: the root of R/2 k^2 + (base + R/2) k = into, then exactly
+    const float bb = (float)work.base + 0.5f * R;
+    k = (int)(2.f * (float)into / (bb + sqrtf(bb * bb + 2.f * R * (float)into)));
+    k = max(0, min(k, work.tiles - 1));
+    while (k > 0 && work.prefix(k, R) > into) --k;
+    while (k + 1 < work.tiles && work.prefix(k + 1, R) <= into) ++k;
     off = into - work.prefix(k, R);
+    line = p.bound(index) - off;
   }
 
   __device__ __forceinline__ int key_tile(long long o, int nt) const {
     return o <= fix ? 0 : (int)min((long long)nt, div_small(o - fix, g * TK));
+  }
+
+  // Key tiles of piece p in the tile at `line` of this cost.
+  __device__ __forceinline__ void share(int p, long long cost, int nt, int* ta, int* tb) const {
+    const long long o0 = max(0LL, pieces.bound(p) - line), o1 = min(cost, pieces.bound(p + 1) - line);
+    *ta = key_tile(o0, nt);
+    *tb = o1 == cost ? nt : key_tile(o1, nt);
+  }
+
+  // After next() gave a split tile: the pieces that share it; 0 when one of them has all its key
+  // tiles (and finishes it) or it has none.
+  __device__ __forceinline__ int sharing(int nt) {
+    if (nt == 0) return 0;
+    const long long cost = work.base + (long long)k * R;    // next() went past the tile
+    line -= cost;
+    int ta = 0, tb = 0;
+    for (int p = piece; p < pieces.count && ta == 0; ++p) {
+      share(p, cost, nt, &ta, &tb);
+      if (ta == 0 && tb == nt) return 0;
+      if (tb > 0) break;
+    }
+    return pieces.at(line + cost - 1) - piece + 1;
   }
 
   // The next segment; false at the end of the piece.
@@ -135,18 +183,13 @@ struct SegIter {
     out->tb = end == cost ? out->nt : key_tile(end, out->nt);
     out->owns_empty = out->nt == 0 && off == 0;
     out->slot = off > 0 ? 0 : 1;
+    out->split = off == 0 && end < cost;
     left -= end - off;
     off = 0;
+    line += cost;
     ++k;
     return true;
   }
-};
-
-// The line cut into pieces as equal as whole units allow: the first `more` are one unit longer.
-struct Pieces {
-  int count, more;
-  long long each;
-  __device__ __forceinline__ long long bound(int i) const { return each * i + min(i, more); }
 };
 
 // The number of pieces worth cutting a line of this length into.
@@ -158,18 +201,11 @@ __device__ __forceinline__ Pieces make_pieces(long long total, int grid, int lea
   return p;
 }
 
-// Block-wide (NT threads, NT a multiple of 32, at most 1,024): the total work of all sequences,
-// and where the line positions x[0..NX) (given as functions of the total by `bounds`) fall.
-struct Located {
-  int seq;
-  long long into;     // offset inside the sequence
-};
-
+// Block-wide (NT threads, NT a multiple of 32, at most 1,024) view of the line.
 template <int R, int NT>
 struct LineScan {
   long long warp_sum[32];
-  long long total;
-  Located at[2];
+  Located at;
 };
 
 template <int R, int NT>
@@ -202,12 +238,30 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   return v + before;
 }
 
-// Fills sc->total and sc->at[i] for the piece bounds first, first + 1 (all NT threads).  A bound at
-// the very end of the line is located past the last sequence.
+// Cuts the line and finds where piece `index` begins (all NT threads).
 template <int R, int NT>
 __device__ __forceinline__ void locate_piece(const KvView& c, const KvBatchView& b, int g, int fix, int grid,
-                                             int least, int first, Pieces* pieces, LineScan<R, NT>* sc,
-                                             bool* bad) {
+                                             int least, int index, Pieces* pieces, LineScan<R, NT>* sc, bool* bad) {
+  if (b.num_seqs <= 32) {              // every warp by itself; one of them writes
+    const int lane = threadIdx.x & 31;
+    const long long v = seq_cost<R, NT>(c, b, g, fix, lane, bad);
+    long long incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    *pieces = make_pieces(__shfl_sync(0xffffffffu, incl, 31), grid, least);
+    if (threadIdx.x < 32 && index < pieces->count) {
+      const long long x = pieces->bound(index), lo = incl - v;
+      if (v > 0 && lo <= x && x < incl) {
+        sc->at.seq = lane;
+        sc->at.into = x - lo;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   long long total = 0, v0 = 0, incl0 = 0;
   for (int s0 = 0; s0 < b.num_seqs; s0 += NT) {
     const long long v = seq_cost<R, NT>(c, b, g, fix, s0 + (int)threadIdx.x, bad);
@@ -218,47 +272,81 @@ __device__ __forceinline__ void locate_piece(const KvView& c, const KvBatchView&
   }
   const Pieces p = make_pieces(total, grid, least);
   *pieces = p;
-  if (threadIdx.x == 0) {
-    sc->total = total;
-    sc->at[0].seq = sc->at[1].seq = b.num_seqs;
-    sc->at[0].into = sc->at[1].into = 0;
-  }
-  __syncthreads();
-  long long before = 0;
-  for (int s0 = 0; s0 < b.num_seqs; s0 += NT) {
-    long long v = v0, incl = incl0, sum = 0;
-    if (s0 > 0 || b.num_seqs > NT) {
-      bool ignore = false;
-      v = seq_cost<R, NT>(c, b, g, fix, s0 + (int)threadIdx.x, &ignore);
-      incl = block_scan<NT>(v, sc->warp_sum, &sum);
-    }
-    const long long lo = before + incl - v, hi = before + incl;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (first + i > p.count) continue;
-      const long long x = p.bound(first + i);
-      if (v > 0 && lo <= x && x < hi) {
-        sc->at[i].seq = s0 + (int)threadIdx.x;
-        sc->at[i].into = x - lo;
+  if (index < p.count) {
+    const long long x = p.bound(index);
+    long long before = 0;
+    for (int s0 = 0; s0 < b.num_seqs; s0 += NT) {
+      long long v = v0, incl = incl0, sum = 0;
+      if (b.num_seqs > NT) {
+        bool ignore = false;
+        v = seq_cost<R, NT>(c, b, g, fix, s0 + (int)threadIdx.x, &ignore);
+        incl = block_scan<NT>(v, sc->warp_sum, &sum);
       }
+      const long long lo = before + incl - v;
+      if (v > 0 && lo <= x && x < lo + v) {
+        sc->at.seq = s0 + (int)threadIdx.x;
+        sc->at.into = x - lo;
+      }
+      before += sum;
     }
-    before += sum;
   }
   __syncthreads();
 }
 
 // ------------------------------------------------------------------ partial results
 
-// Slot layout: [G][2 slots] x ( R x D floats, then R (m, l) pairs ).
+// A split tile, noted by the piece it begins in: its pieces are first (slot 1) and the count - 1
+// after it (slot 0).
+struct MergeDesc {
+  int row0, tokens, head, tile, rows, count;
+};
+
+constexpr int kMaxPieces = 1024;
+constexpr int kMergeWarps = 8;
+
+// Warps of a merging block that share a row: all when many pieces have to be read one after
+// another, else one each.
+__host__ __device__ constexpr bool whole_block_rows(int count) { return count > 16; }
+
+// Workspace: [G][2 slots] x (R x D floats, then R (m, l) pairs), then G descriptors and G counts
+// of merging work.  The floats are rows of D for tiles of few rows, which are written and read by
+// rows; for R >= 128, where a thread holds a row, [D / 4][R] groups of four columns, so that both
+// sides move 32 rows' groups at a time.
 template <int R, int D>
 struct Partials {
+  static constexpr bool kByColumns = R >= 128;
+  // merging work of a tile: units of 32 rows x 32 columns, or 8 rows, or a row for a whole block
+  static __host__ __device__ int work(int rows, int count) {
+    return kByColumns ? (rows + 31) / 32 * (D / 32)
+                      : whole_block_rows(count) ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
+  }
   static constexpr size_t kSlotFloats = (size_t)R * D + 2 * R;
-  static __host__ __device__ size_t bytes(int grid) { return (size_t)grid * 2 * kSlotFloats * 4; }
+  static __host__ __device__ size_t slots_bytes(int grid) { return (size_t)grid * 2 * kSlotFloats * 4; }
+  static __host__ __device__ size_t bytes(int grid) {
+    return slots_bytes(grid) + (size_t)grid * (sizeof(MergeDesc) + sizeof(int));
+  }
   static __device__ __forceinline__ float* rows(float* ws, int cta, int slot) {
     return ws + ((size_t)cta * 2 + slot) * kSlotFloats;
   }
   static __device__ __forceinline__ float* ml(float* ws, int cta, int slot) {
     return rows(ws, cta, slot) + (size_t)R * D;
+  }
+  static __device__ __forceinline__ MergeDesc* desc(float* ws, int grid) {
+    return reinterpret_cast<MergeDesc*>(reinterpret_cast<char*>(ws) + slots_bytes(grid));
+  }
+  static __device__ __forceinline__ int* units(float* ws, int grid) {
+    return reinterpret_cast<int*>(desc(ws, grid) + grid);
+  }
+  // One thread of CTA cta: what the merge has to do for the tile that begins in the piece and is
+  // shared by `count` (0: nothing).
+  static __device__ __forceinline__ void note(float* ws, int grid, int cta, int g, const Segment* s, int count) {
+    int n = 0;
+    if (count > 0) {
+      const int r = min(R, s->info.tokens * g - s->tile * R);
+      desc(ws, grid)[cta] = MergeDesc{s->info.row0, s->info.tokens, s->head, s->tile, r, count};
+      n = work(r, count);
+    }
+    units(ws, grid)[cta] = n;
   }
 };
 
@@ -295,118 +383,153 @@ __device__ __forceinline__ void zero_padding(const AttnArgs& a, const KvBatchVie
 
 // ------------------------------------------------------------------ merging split tiles
 
-// Block (i, y) looks at the bound between pieces i and i + 1.  If it falls inside a tile and is the
-// first to do so, the block merges rows y, y + gridDim.y, ... of the tile over the pieces that
-// share it: each piece's rows count 2^(m - M), M the largest reference.
-constexpr int kMaxPieces = 1024;
-
-template <int R, int TK, int D>
-__global__ void __launch_bounds__(256) merge_kernel(const KvView c, const KvBatchView b, const AttnArgs a,
-                                                    int grid, int fix, int least) {
-  constexpr int NT = 256, W = NT / 32, Q = (D + 127) / 128;
-  __shared__ LineScan<R, NT> scan;
-  __shared__ float4 acc[W][D / 4];
-  __shared__ float acc_l[W];
-  __shared__ int source[kMaxPieces];      // partial slot of each piece of the tile, -1: it left none
-  __shared__ float weight[kMaxPieces];
-  pdl_begin();
-  bool bad = false;
-  Pieces pieces;
-  const int i = blockIdx.x;
-  locate_piece<R, NT>(c, b, a.g, fix, grid, least, i, &pieces, &scan, &bad);
-  if (i + 1 >= pieces.count) return;
-  const long long x = pieces.bound(i + 1), x_prev = pieces.bound(i);
-  if (x == x_prev) return;
-  // the tile that holds x
-  SegIter<R, TK> it;
-  it.start(&b, c.page_shift, c.H, a.g, fix, scan.at[1].seq, scan.at[1].into, 1);
-  if (it.off == 0) return;                              // a tile begins at the bound
-  const long long t0 = x - it.off;                      // the tile's place on the line
-  if (x_prev > t0) return;                              // an earlier bound lies inside this tile
-  const long long cost = it.work.base + (long long)(it.k + 1) * R;
-  const int keys = tile_keys<R>(it.info, a.g, it.k);
-  const int nt = (keys + TK - 1) / TK;
-  if (nt == 0) return;                                  // zeros, written by piece i
-  const int rows = (int)min((long long)R, (long long)it.info.tokens * a.g - (long long)it.k * R);
-  if ((int)blockIdx.y >= rows) return;
+// Merges the split tiles: each piece's rows count 2^(m - M), M the largest reference of the row.
+// The work (8 rows, or one row read by all 8 warps) is spread over the grid by the counts that
+// every CTA of the attention kernel left.
+template <int R, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const AttnArgs a, int grid) {
+  constexpr int NT = kMergeWarps * 32, Q = (D + 127) / 128, kPer = kMaxPieces / NT;
+  __shared__ int before[kMaxPieces + 1];
+  __shared__ int warp_total[kMergeWarps];
+  __shared__ float4 acc[kMergeWarps][D / 4];
+  __shared__ float2 acc_ml[kMergeWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the pieces i .. i + count - 1 share the tile
-  int count = 0;
-  bool one = false;
-  for (int j0 = 0;; j0 += NT) {
-    const int j = j0 + tid, p = i + j;
-    const bool in = p < pieces.count && pieces.bound(p) < t0 + cost;
-    if (in) {
-      const long long o0 = max(0LL, pieces.bound(p) - t0), o1 = min(cost, pieces.bound(p + 1) - t0);
-      const int ta = it.key_tile(o0, nt), tb = o1 == cost ? nt : it.key_tile(o1, nt);
-      source[j] = ta < tb ? 2 * p + (o0 > 0 ? 0 : 1) : -1;
-      one |= ta == 0 && tb == nt;                       // one piece did it all and finished it
+  pdl_begin();
+  // prefix sums of the counts, kPer per thread
+  {
+    const int* units = Partials<R, D>::units(a.ws, grid);
+    int v[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * kPer + j;
+      v[j] = i < grid ? __ldcg(units + i) : 0;
+      sum += v[j];
     }
-    const int n = __syncthreads_count(in);
-    count += n;
-    if (n < NT) break;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < warp; ++w) base += warp_total[w];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      before[tid * kPer + j] = base;
+      base += v[j];
+    }
+    if (tid == NT - 1) before[kMaxPieces] = base;
+    __syncthreads();
   }
-  if (__syncthreads_or(one)) return;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float top = -INFINITY;
-    for (int j = tid; j < count; j += NT) {
-      const int s = source[j];
-      const float m = s < 0 ? -INFINITY : __ldcg(Partials<R, D>::ml(a.ws, s >> 1, s & 1) + 2 * r);
-      weight[j] = m;
-      top = fmaxf(top, m);
+  const int total = before[kMaxPieces];
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int lo = 0, hi = kMaxPieces;            // the piece whose work holds u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= u) lo = mid; else hi = mid;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) acc_l[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) top = fmaxf(top, acc_l[w]);
-    __syncthreads();
+    const MergeDesc d = Partials<R, D>::desc(a.ws, grid)[lo];
+    if constexpr (Partials<R, D>::kByColumns) {
+      // lane = row, warp = four columns
+      const int v = u - before[lo], r = v / (D / 32) * 32 + lane, col = (v % (D / 32)) * 32 + warp * 4;
+      if (r < d.rows) {
+        float top = -INFINITY, l = 0.f;
+#pragma unroll 8
+        for (int j = 0; j < d.count; ++j)
+          top = fmaxf(top, __ldcg(Partials<R, D>::ml(a.ws, lo + j, j == 0 ? 1 : 0) + 2 * r));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int j = 0; j < d.count; ++j) {
+          const int slot = j == 0 ? 1 : 0;
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(Partials<R, D>::ml(a.ws, lo + j, slot) + 2 * r));
+          if (ml.x == -INFINITY) continue;           // an empty share left only its (m, l)
+          const float w = exp2f(ml.x - top);
+          const float4 p = __ldcg(reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, lo + j, slot)) +
+                                  (size_t)(col / 4) * R + r);
+          l += w * ml.y;
+          o.x = fmaf(w, p.x, o.x); o.y = fmaf(w, p.y, o.y);
+          o.z = fmaf(w, p.z, o.z); o.w = fmaf(w, p.w, o.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        int tok, head;
+        row_of(SeqInfo{d.row0, d.tokens, 0}, a.g, d.head, d.tile * R + r, &tok, &head);
+        store_out4(a, D, tok, head, col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      }
+      continue;
+    }
+    const bool together = whole_block_rows(d.count);
+    const int r = together ? u - before[lo] : (u - before[lo]) * kMergeWarps + warp;
+    const int j0 = together ? warp : 0, step = together ? kMergeWarps : 1;
     float4 sum[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) sum[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int j = warp; j < count; j += W) {
-      const float m = weight[j];
-      if (m == -INFINITY) continue;
-      const int s = source[j];
-      const float w = exp2f(m - top);
-      l += w * __ldcg(Partials<R, D>::ml(a.ws, s >> 1, s & 1) + 2 * r + 1);
-      const float4* src = reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, s >> 1, s & 1) + (size_t)r * D);
+    float top = -INFINITY, l = 0.f;
+    if (r < d.rows) {
+      // the references first: a lane each
+      float m0 = -INFINITY;
+      for (int j = lane; j < d.count; j += 32)
+        m0 = fmaxf(m0, __ldcg(Partials<R, D>::ml(a.ws, lo + j, j == 0 ? 1 : 0) + 2 * r));
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const int col = q * 32 + lane;
-        if (col < D / 4) {
-          const float4 v = __ldcg(src + col);
-          sum[q].x = fmaf(w, v.x, sum[q].x); sum[q].y = fmaf(w, v.y, sum[q].y);
-          sum[q].z = fmaf(w, v.z, sum[q].z); sum[q].w = fmaf(w, v.w, sum[q].w);
+      for (int o = 16; o > 0; o >>= 1) m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+      top = m0;
+#pragma unroll 4
+      for (int j = j0; j < d.count; j += step) {
+        const int slot = j == 0 ? 1 : 0;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(Partials<R, D>::ml(a.ws, lo + j, slot) + 2 * r));
+        const float4* src = reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, lo + j, slot) + (size_t)r * D);
+        const bool some = ml.x != -INFINITY;      // an empty share left only its (m, l)
+        const float w = some ? exp2f(ml.x - top) : 0.f;
+        if (some) l += w * ml.y;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int col = q * 32 + lane;
+          if (some && col < D / 4) {
+            const float4 v = __ldcg(src + col);
+            sum[q].x = fmaf(w, v.x, sum[q].x); sum[q].y = fmaf(w, v.y, sum[q].y);
+            sum[q].z = fmaf(w, v.z, sum[q].z); sum[q].w = fmaf(w, v.w, sum[q].w);
+          }
         }
       }
     }
+    const SeqInfo info{d.row0, d.tokens, 0};
+    int tok = 0, head = 0;
+    if (!together) {
+      if (r < d.rows) {
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        row_of(info, a.g, d.head, d.tile * R + r, &tok, &head);
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int col = q * 32 + lane;
-      if (col < D / 4) acc[warp][col] = sum[q];
-    }
-    if (lane == 0) acc_l[warp] = l;
-    __syncthreads();
-    if (tid < D / 4) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float lt = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float4 v = acc[w][tid];
-        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-        lt += acc_l[w];
+        for (int q = 0; q < Q; ++q) {
+          const int col = q * 32 + lane;
+          if (col < D / 4)
+            store_out4(a, D, tok, head, col * 4,
+                       make_float4(sum[q].x * inv, sum[q].y * inv, sum[q].z * inv, sum[q].w * inv));
+        }
       }
-      const float inv = lt == 0.f ? 0.f : 1.0f / lt;
-      o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-      int tok, head;
-      row_of(it.info, a.g, it.h, it.k * R + r, &tok, &head);
-      store_out4(a, D, tok, head, tid * 4, o);
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int col = q * 32 + lane;
+        if (col < D / 4) acc[warp][col] = sum[q];
+      }
+      if (lane == 0) acc_ml[warp] = make_float2(top, l);
+      __syncthreads();
+      if (tid < D / 4) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lt = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+          const float4 v = acc[w][tid];
+          o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+          lt += acc_ml[w].y;
+        }
+        const float inv = lt == 0.f ? 0.f : 1.0f / lt;
+        row_of(info, a.g, d.head, d.tile * R + r, &tok, &head);
+        store_out4(a, D, tok, head, tid * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 

@@ -305,7 +305,10 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad_len);
   if (bad_len) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
-  if (cta >= pieces.count) return;
+  if (cta >= pieces.count) {
+    if (tid == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, nullptr, 0);
+    return;
+  }
   if (warp == C::kMmaWarp) tmem_alloc(&sm.tmem, 512);
   fence_before_sync();
   __syncthreads();
@@ -333,13 +336,13 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   if (warp == C::kSchedWarp) {
     // ---------------------------------------------------------------- segments
     SegIter<R, TK> it;
-    it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
-             pieces.bound(cta + 1) - pieces.bound(cta));
+    it.start(&b, c.page_shift, c.H, a.g, fix, pieces, cta, sm.scan.at);
     Segment s;
+    s.split = false;
     for (bool more = true; more;) {
       more = it.next(&s);
       const int n = s.tb - s.ta;
-      if (more && n <= 0 && !s.owns_empty) continue;
+      if (more && n <= 0 && !s.owns_empty && s.nt == 0) continue;
       wait_bar(&sm.seg_empty[seg.stage], seg.phase ^ 1u, &sm.dead, c.status);
       if (lane == 0) {
         sm.segs[seg.stage] = more ? SegDesc{s.seq, s.info.row0, s.info.tokens, s.info.len, s.head, s.tile, s.ta,
@@ -350,6 +353,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       __syncwarp();
       seg.step();
     }
+    // the piece's last tile may be shared with the next ones
+    if (lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &s, s.split ? it.sharing(s.nt) : 0);
   } else if (warp == C::kLoadWarp) {
     // ---------------------------------------------------------------- TMA
     const int box = min(1 << c.page_shift, TK);            // keys of one copy
@@ -419,7 +424,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     // ---------------------------------------------------------------- MMA (one thread)
     // The tensor pipe queues only a few MMAs, so what this thread does between them leaves the pipe
     // idle (a commit costs some 40 cycles, a wait that finds its phase complete twice that): it
-    // waits for p_ready alone where that implies the tiles are there, and commits what is needed.
+    // waits for p_ready alone where that implies the tiles are there, and (two blocks) leaves it to
+    // the softmax to hand the rings' stages back.
     if (lane == 0) {
       RingPos<C::kKStages> kp;
       RingPos<C::kVStages> vp;
@@ -482,7 +488,6 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             qk_half(1, 1, k_lo(), 0);
             mma_commit(&sm.s_full[1]);
           }
-          mma_commit(&sm.k_empty[kp.stage]);
           kp.step();
           // Block 0's softmax of tile i has seen V(i) and K(i + 1) arrive before it says p_ready.
           for (int i = 0; i + 1 < n; ++i) {
@@ -495,13 +500,9 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
               wait_one(&sm.p_ready[1], cnt[1]++ & 1u, &sm.dead, c.status);
               fence_after_sync();
               pv_half(1, 1, v_lo(), 0, i > 0);
-              mma_commit(&sm.v_empty[vp.stage]);
               qk_half(1, 1, k_lo(), 0);
               mma_commit(&sm.s_full[1]);
-            } else {
-              mma_commit(&sm.v_empty[vp.stage]);
             }
-            mma_commit(&sm.k_empty[kp.stage]);
             vp.step();
             kp.step();
           }
@@ -515,7 +516,6 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             pv_half(1, 1, v_lo(), 0, n > 1);
             mma_commit(&sm.o_done[1]);
           }
-          mma_commit(&sm.v_empty[vp.stage]);
           vp.step();
         } else {
           auto qk_tile = [&]() {
@@ -623,7 +623,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     uint32_t cnt = 0;                  // tiles of this block so far
     uint32_t segments = 0;
     RingPos<C::kVStages> vp;           // block 0 follows the rings
-    RingPos<C::kKStages> kp;
+    RingPos<C::kKStages> kp, k_out;    // (two blocks) and hands their stages back, or block 1 does
+    RingPos<C::kVStages> v_out, v_at;
     RingPos<Q8 ? C::kScales : 1> sp;   // 8-bit: the scales' ring
     auto load_q = [&](const SegDesc& s) {
       // A warp loads its own 32 rows (lane i knows where row i is), D / 8 lanes a row at a time:
@@ -689,6 +690,14 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_ready[blk]);
     };
+    // 16-byte piece p of row rr of this warp's 32 rows in the queries' place: the rows that this warp
+    // loads, so warps do not meet in it
+    auto row_piece = [&](int rr, int p) {
+      constexpr bool kNarrow = Q8 && D == 64;                 // 64-byte query rows, in two parts
+      return reinterpret_cast<uint4*>(
+          sm.q[blk] + (kNarrow ? (p >> 2) * 8192 + (lbase + rr) * 64 + (((p & 3) ^ ((rr >> 1) & 3)) << 4)
+                               : (p >> 3) * 16384 + (lbase + rr) * 128 + (((p & 7) ^ (rr & 7)) << 4)));
+    };
     auto active = [&](const SegDesc& s) {
       return s.n > 0 && (blk == 0 || (long long)s.tokens * a.g - (long long)s.tile * R > 128);
     };
@@ -713,19 +722,48 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           uint4* o = reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D);
           for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
         }
-        if (Q8)
-          for (int i = 0; i < n; ++i) sp.step();      // the other block's tiles
+        if (n == 0 && !cur.owns_empty && live)         // an empty share of a split tile
+          __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, cur.slot) + 2 * (blk * 128 + r)),
+                 make_float2(-INFINITY, 0.f));
+        for (int i = 0; i < n; ++i) {                   // the other block's tiles
+          if (Q8) sp.step();
+          k_out.step();
+          v_out.step();
+        }
         const SegDesc& next = seg_wait(ahead_seg);
         if (active(next)) load_q(next);
       } else {
         const int last_row = cur.tokens * a.g - 1, len = cur.len, ta = cur.ta;
         const int pos = before + min(row, last_row) / a.g;
         const int pos_min = before + min(cur.tile * R + blk * 128, last_row) / a.g;
+        const bool releases = blk == (rows > 128 ? 1 : 0);
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < n; ++i, ++cnt) {
           const int buf = C::kBlocks == 2 ? blk : (int)(cnt & 1u);
+          // A parity wait tells a phase from the one before it only when no phase is skipped: so
+          // block 0 waits for every stage of the rings, needed or not.  Its p_ready then tells the
+          // MMA thread that V(i) (and, with two blocks, K(i + 1)) are there.
+          if (C::kBlocks == 2 && blk == 0) {
+            v_at = vp;
+            wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
+            vp.step();
+            {
+              if (i == 0) kp.step();
+              if (i + 1 < n) {
+                wait_bar(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
+                kp.step();
+              }
+            }
+          }
           wait_bar(&sm.s_full[buf], (C::kBlocks == 2 ? cnt : cnt >> 1) & 1u, &sm.dead, c.status);
           fence_after_sync();
+          if (C::kBlocks == 2 && releases && warp == 4 * blk && lane == 0) {
+            // the last block's scores are there: K(i) has been read, and V(i - 1)
+            mbar_arrive(&sm.k_empty[k_out.stage]);
+            if (i > 0) mbar_arrive(&sm.v_empty[v_out.stage]);
+          }
+          k_out.step();
+          if (i > 0) v_out.step();
           const uint32_t s_addr = tl + buf * 128;
           const int k0 = (ta + i) * TK;
           const bool partial = k0 + TK - 1 > pos_min;
@@ -810,28 +848,21 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             unpair(l2[1], l3, l4);
             l = (l0 + l1) + (l3 + l4);
           }
-          // A parity wait tells a phase from the one before it only when no phase is skipped: so
-          // block 0 waits for every stage of the rings, needed or not, and one block alone for
-          // every o_done.
+          // for its parity's sake every tile: one block's s_full does not imply the product before
           if (C::kBlocks == 1 && i > 0) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
-          if (blk == 0) {
-            if (C::kBlocks == 2) {
-              if (i == 0) kp.step();
-              if (i + 1 < n) {
-                wait_bar(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
-                kp.step();
-              }
-            }
+          if (C::kBlocks == 1) {         // (one block: two V stages hold one tile, which comes late)
+            v_at = vp;
+            for (int h = 0; h < C::kHalves; ++h, vp.step()) wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
+          }
+          if (blk == 0 && partial) {
             // a causal-edge tile's values: zero past the end, zero and noted where not finite
-            for (int h = 0; h < C::kHalves; ++h, vp.step()) {
-              wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
-              if (!partial) continue;
+            for (int h = 0; h < C::kHalves; ++h, v_at.step()) {
               // keys from the first row's position on (earlier ones are seen by all rows)
               const int j0 = max(0, pos_min + 1 - k0), j1 = TK;
               constexpr int kPer = C::kCols / 8;
               const int piece = r % kPer;
               for (int j = j0 + r / kPer; j < j1; j += 128 / kPer) {
-                uint4* p = reinterpret_cast<uint4*>(sm.v[vp.stage] + (piece >> 3) * (TK * 128) + j * 128 +
+                uint4* p = reinterpret_cast<uint4*>(sm.v[v_at.stage] + (piece >> 3) * (TK * 128) + j * 128 +
                                                     (((piece & 7) ^ (j & 7)) << 4));
                 if (k0 + j >= len) {
                   *p = make_uint4(0, 0, 0, 0);
@@ -854,7 +885,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
                 }
               }
             }
-            if (partial) fence_proxy_async_smem();
+            fence_proxy_async_smem();
           }
           __syncwarp();
           tmem_wait_st();
@@ -862,74 +893,95 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.p_ready[blk]);
         }
+        int tok = 0, head = 0;
+        row_of(SeqInfo{cur.row0, cur.tokens, cur.len}, a.g, cur.head, min(row, last_row), &tok, &head);
+        if (a.gate && cur.whole) {
+          // every product with these queries is through: their place takes the gate in
+          const long long grow = tok * a.gate_ld + head * a.gate_head_ld;
+          constexpr int kPer = D / 8, kStep = 32 / kPer;
+          const int piece = lane % kPer, first = lane / kPer;
+#pragma unroll 8
+          for (int j = 0; j < 32 / kStep; ++j) {
+            const int rr = j * kStep + first;
+            const long long at = __shfl_sync(0xffffffffu, grow, rr);
+            cp_async16(smem_u32(row_piece(rr, piece)), a.gate + at + piece * 8, true);
+          }
+        }
         // two blocks: one phase of o_done a segment
         wait_bar(&sm.o_done[blk], (C::kBlocks == 2 ? segments++ : cnt - 1) & 1u, &sm.dead, c.status);
         fence_after_sync();
+        if (C::kBlocks == 2) {
+          if (releases && warp == 4 * blk && lane == 0) mbar_arrive(&sm.v_empty[v_out.stage]);
+          v_out.step();
+        }
         const bool whole = cur.whole, bad = *(volatile int*)&sm.any_bad != 0;
-        int tok = 0, head = 0;
-        row_of(SeqInfo{cur.row0, cur.tokens, cur.len}, a.g, cur.head, min(row, last_row), &tok, &head);
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
         const int pr = blk * 128 + r;
-        float* prow = Partials<R, D>::rows(a.ws, cta, cur.slot) + (size_t)(blk * 128 + lbase) * D;
-        // The queries have been read: the place of this warp's 32 rows turns rows held by a thread
-        // each into rows of consecutive lanes, D / 2 columns of f32 at a time.
-        constexpr bool kNarrow = Q8 && D == 64;                 // 64-byte query rows, in two parts
-        auto place = [&](int rr, int piece) {
-          return reinterpret_cast<float4*>(
-              sm.q[blk] + (kNarrow ? (piece >> 2) * 8192 + (lbase + rr) * 64 + (((piece & 3) ^ ((rr >> 1) & 3)) << 4)
-                                   : (piece >> 3) * 16384 + (lbase + rr) * 128 + (((piece & 7) ^ (rr & 7)) << 4)));
-        };
         const int rows32 = min(32, rows - blk * 128 - lbase);
-        const long long orow = ((long long)tok * a.Hq + head) * D;
-        const long long grow = a.gate ? tok * a.gate_ld + head * a.gate_head_ld : 0;
-        constexpr int kPer = D / 8, kStep = 32 / kPer;          // 16-byte pieces of half a row
-        const int piece = lane % kPer, first = lane / kPer;
+        auto read_o = [&](int d, uint32_t* o) {
+          tmem_ld32_nw(tl + C::kO + blk * D + d, o);
+          tmem_wait_ld();
+          reg_fence16(o);
+          reg_fence16(o + 16);
+          if (bad) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (sm.bad[d + e] <= pos) o[e] = 0x7fffffffu;
+          }
+        };
+        if (whole) {
+          // The queries have been read: the place of this warp's 32 rows (a piece is 16 bytes) took
+          // the gate in meanwhile, and turns rows held by a thread each into rows of consecutive lanes.
+          if (a.gate) {
+            cp_async_wait_all();
+            __syncwarp();
+          }
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-          for (int d = 0; d < D / 2; d += 32) {
+          for (int d = 0; d < D; d += 32) {
             uint32_t o[32];
-            tmem_ld32_nw(tl + C::kO + blk * D + half * (D / 2) + d, o);
-            tmem_wait_ld();
-            reg_fence16(o);
-            reg_fence16(o + 16);
-            if (bad) {
+            read_o(d, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (sm.bad[half * (D / 2) + d + e] <= pos) o[e] = 0x7fffffffu;
-            }
+            for (int e = 0; e < 4; ++e) {
+              uint4* at = row_piece(lane, d / 8 + e);
+              float y[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *place(lane, (d + e) / 4) =
-                  make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                              __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-          }
-          __syncwarp();
-          const int col = half * (D / 2) + piece * 4;
-          if (whole) {
-#pragma unroll 4
-            for (int j = 0; j < 32 / kStep; ++j) {
-              const int rr = j * kStep + first;
-              const long long at = __shfl_sync(0xffffffffu, orow, rr);
-              float4 y = *place(rr, piece);
+              for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(o[8 * e + k]) * inv;
               if (a.gate) {
-                const long long ga = __shfl_sync(0xffffffffu, grow, rr);
-                if (rr < rows32) {
-                  const float4 z = Act<__nv_bfloat16>::ldg4(a.gate + ga + col);
-                  y.x *= gate_of(z.x); y.y *= gate_of(z.y); y.z *= gate_of(z.z); y.w *= gate_of(z.w);
-                }
+                const uint4 z = *at;
+                const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  y[k] *= gate_of(__uint_as_float(k & 1 ? zw[k >> 1] & 0xffff0000u : zw[k >> 1] << 16));
               }
-              if (rr < rows32) Act<__nv_bfloat16>::store4(a.out + at + col, y);
-            }
-          } else {
-#pragma unroll 4
-            for (int j = 0; j < 32 / kStep; ++j) {
-              const int rr = j * kStep + first;
-              const float4 y = *place(rr, piece);
-              if (rr < rows32) __stcg(reinterpret_cast<float4*>(prow + (size_t)rr * D + col), y);
+              *at = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
             }
           }
           __syncwarp();
+          const long long orow = ((long long)tok * a.Hq + head) * D;
+          constexpr int kPer = D / 8, kStep = 32 / kPer;
+          const int piece = lane % kPer, first = lane / kPer;
+#pragma unroll 8
+          for (int j = 0; j < 32 / kStep; ++j) {
+            const int rr = j * kStep + first;
+            const long long at = __shfl_sync(0xffffffffu, orow, rr);
+            const uint4 y = *row_piece(rr, piece);
+            if (rr < rows32) *reinterpret_cast<uint4*>(a.out + at + piece * 8) = y;
+          }
+          __syncwarp();
+        } else {
+          float4* part = reinterpret_cast<float4*>(Partials<R, D>::rows(a.ws, cta, cur.slot)) + pr;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            uint32_t o[32];
+            read_o(d, o);
+            if (live)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                __stcg(part + (size_t)(d + e) / 4 * R,
+                       make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                   __uint_as_float(o[e + 3])));
+            __syncwarp();
+          }
         }
         if (!whole && live) {
           // a NaN sum must survive the merge even when its reference never left -infinity
@@ -967,13 +1019,12 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   KvMaps maps;
   const int P = 1 << c.page_shift;
   if (!make_tile_maps(c, P < kKeys ? P : kKeys, Q8 ? C::kCols : 64, &maps)) return GDN_ERR_CUDA;
-  const int grid = sms, fix = 128 * a.g;
+  const int grid = sms, fix = 512 * a.g;
   const int least = 512 * a.g;
   int rc = launch_dependent(chunk_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
-  return launch_dependent(merge_kernel<C::kRows, kKeys, D>, dim3((unsigned)(grid - 1), 16), 256, 0, stream, c, b, a,
-                          grid, fix, least);
+  return launch_dependent(merge_kernel<C::kRows, D>, dim3((unsigned)(2 * sms)), kMergeWarps * 32, 0, stream, a, grid);
 }
 
 size_t chunk_ws_bytes(int D, int sms) {

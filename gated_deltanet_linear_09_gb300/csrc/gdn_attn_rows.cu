@@ -146,11 +146,14 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad);
   if (bad) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
-  if (cta >= pieces.count) return;
+  if (cta >= pieces.count) {
+    if (tid == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, nullptr, 0);
+    return;
+  }
   SegIter<R, TK> it;
-  it.start(&b, c.page_shift, c.H, a.g, fix, sm.scan.at[0].seq, sm.scan.at[0].into,
-           pieces.bound(cta + 1) - pieces.bound(cta));
+  it.start(&b, c.page_shift, c.H, a.g, fix, pieces, cta, sm.scan.at);
   Segment sg;
+  sg.split = false;
 
   if (warp == C::kConsumers) {
     // ---------------------------------------------------------------- producer
@@ -193,6 +196,8 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
       }
     }
+    // the piece's last tile may be shared with the next ones
+    if (lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &sg, sg.split ? it.sharing(sg.nt) : 0);
     return;
   }
 
@@ -214,6 +219,9 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
           *reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D + (i % (D / 8)) * 8) =
               make_uint4(0, 0, 0, 0);
         }
+      else if (sg.nt > 0)                                // an empty share of a split tile
+        for (int i = tid; i < rows; i += NC)
+          __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, sg.slot) + 2 * i), make_float2(-INFINITY, 0.f));
       continue;
     }
     const int keys = min(info.len, tile_keys<R>(info, a.g, sg.tile));
@@ -555,8 +563,7 @@ int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sm
   int rc = launch_dependent(rows_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
-  return launch_dependent(merge_kernel<kRows, kTileKeys, D>, dim3((unsigned)(grid - 1), 4), 256, 0, stream, c, b, a,
-                          grid, fix, least);
+  return launch_dependent(merge_kernel<kRows, D>, dim3((unsigned)(2 * sms)), kMergeWarps * 32, 0, stream, a, grid);
 }
 
 int rows_grid(int D, int sms) { return min(kMaxPieces, D == 256 ? sms : 2 * sms); }
