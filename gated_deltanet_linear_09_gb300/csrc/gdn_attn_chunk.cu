@@ -24,8 +24,6 @@
 // in tiles that the causal edge crosses, the first warpgroup replaces non-finite ones (and
 // whatever lies past the sequence's end) by zero, and notes column and position, so that the rows
 // that do see them get their NaN.
-#include <cuda_fp16.h>
-
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 
@@ -215,18 +213,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
-}
-
-// (x, y) = hi + lo in e4m3 codes, |x|, |y| <= 448.
-__device__ __forceinline__ void split_e4m3(float x, float y, uint32_t& hi, uint32_t& lo) {
-  uint16_t h, l;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
-  uint32_t f;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
-  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(y - v.y), "f"(x - v.x));
-  hi = h;
-  lo = l;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
@@ -646,9 +632,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         }
         cp_async_wait_all();
       } else {
-        // A row, brought to (224, 448] by a power of two, is the sum of two e4m3 vectors: the codes
-        // nearest to it, and what they leave, which fits their four significant bits again (bf16
-        // has eight).  Elements below 2^-10 of the row's largest lose bits at 2^-18 of it.
+        // the rows as two e4m3 parts (see split_e4m3)
         constexpr int kBatch = 8;
         for (int j0 = 0; j0 < 32 / kStep; j0 += kBatch) {
           uint4 u[kBatch];

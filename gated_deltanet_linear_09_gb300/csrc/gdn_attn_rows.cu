@@ -16,8 +16,11 @@
 //  * the products are m16n8k16 MMAs on registers.  Sixteen rows fill that shape; the 128-row
 //    tcgen05 shape would run 7/8 empty here, needs the probabilities to cross TMEM, and could not
 //    be faster than the loads, which already set the pace;
-//  * 8-bit caches are converted in registers (exactly, to bf16), with the scales applied to the
-//    scores and to the probabilities instead of the elements.
+//  * 8-bit caches: the keys' codes are e4m3 MMA operands as they are (the queries as two e4m3
+//    parts, whose sum is exact), their scales applied to the scores; the values' codes become f16 by
+//    the conversion instruction, their scales applied to the probabilities.  Halving the bytes
+//    halves the time the arithmetic may take: converting both to bf16 by bit operations, 2.5 per
+//    element, held the kernel to 3.7 of the 6.7 TB/s.
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 
@@ -32,10 +35,8 @@ constexpr int kTileKeys = 64;
 
 template <int D, bool Q8>
 struct RowsCfg {
-  // D = 256: the accumulators take 128 registers of a thread, so one CTA of eight consumer warps
-  // (two teams, alternate stages) instead of two CTAs of four.
-  static constexpr int kConsumers = D == 256 && Q8 ? 8 : 4;
-  static constexpr int kTeams = kConsumers / 4;
+  // D = 256: the accumulators take 128 registers of a thread, and a stage twice the bytes.
+  static constexpr int kConsumers = 4;
   static constexpr int kCtas = D == 256 ? 1 : 2;
   static constexpr int kThreads = (kConsumers + 1) * 32;
   static constexpr int kElem = Q8 ? 1 : 2;
@@ -44,8 +45,7 @@ struct RowsCfg {
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRing = kCtas == 1 ? 196608 : 98304;
   static constexpr int kFit = kRing / (kStageBytes + (Q8 ? 1024 : 0));   // with the scale bytes
-  // a multiple of the teams: a stage is always the same team's, which waits for each of its phases
-  static constexpr int kStages = (kFit > 8 ? 8 : kFit) / kTeams * kTeams;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kBox = D * kElem >= 128 ? 128 : 64;       // swizzle span, bytes
   static constexpr int kLd = D + 8;                              // merge buffer row
 };
@@ -56,7 +56,8 @@ struct __align__(1024) RowsSmem {
   uint8_t ring[C::kStages][C::kStageBytes];
   // scale bytes of a stage's four 16-key groups (16 bytes each: TMA wants 128-byte destinations)
   uint8_t scales[Q8 ? C::kStages : 1][2][4][128];
-  uint4 q[D / 16][32];                    // A fragments of the 16 rows
+  uint4 q[D / 16][32];                    // A fragments of the 16 rows (8-bit: of their two parts)
+  float q_scale[kRows];
   float o[kRows][C::kLd];
   float ml[C::kConsumers][kRows][2];
   LineScan<kRows, C::kThreads> scan;
@@ -70,6 +71,37 @@ __device__ __forceinline__ void mma16816(float* c, const uint4& a, uint32_t b0, 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_f16(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16832_e4m3(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+// Two 16 x 16 byte matrices, transposed: lane (n, t) gets columns n and n + 8 of the first, then of
+// the second, each word four consecutive rows 4 t .. 4 t + 3.
+__device__ __forceinline__ void ldsm2t_b8(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// The e4m3 codes of w's low or high half as f16 values.
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint16_t h) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -86,11 +118,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -203,10 +230,9 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 
   // ------------------------------------------------------------------ consumers
   const int t = lane & 3, n = lane >> 2;
-  const int grp = warp & 3, team = warp >> 2;
+  const int grp = warp;
   int stage = 0;
   uint32_t phase = 0;
-  unsigned turn = 0;
   while (it.next(&sg)) {
     const SeqInfo info = sg.info;
     const int row_base = sg.tile * R;
@@ -226,42 +252,94 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     }
     const int keys = min(info.len, tile_keys<R>(info, a.g, sg.tile));
     const int before = info.len - info.tokens;          // position of the first new token
-    // Q fragments: word (row, k pair) of k-step ks; the 8-bit form permutes k inside 64-element
-    // blocks so that a lane's 16 bytes of a key are consecutive.
-    for (int i = tid; i < (D / 16) * 32; i += NC) {
-      const int ks = i >> 5, ln = i & 31, qt = ln & 3, qn = ln >> 2;
-      const int d0 = Q8 ? (ks >> 2) * 64 + qt * 16 + (ks & 3) * 4 : ks * 16 + 2 * qt;
-      const int d1 = Q8 ? d0 + 2 : d0 + 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      int tok, head;
-      if (qn < rows) {
-        row_of(info, a.g, sg.head, row_base + qn, &tok, &head);
-        const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
-        v.x = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
-        v.z = __ldg(reinterpret_cast<const uint32_t*>(p + d1));
+    if constexpr (!Q8) {
+      // Q fragments: words (row, two neighbouring columns) of k-step ks
+#pragma unroll 4
+      for (int i = tid; i < (D / 16) * 32; i += NC) {
+        const int ks = i >> 5, ln = i & 31, qn = ln >> 2, d0 = ks * 16 + 2 * (ln & 3);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        int tok, head;
+        if (qn < rows) {
+          row_of(info, a.g, sg.head, row_base + qn, &tok, &head);
+          const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
+          v.x = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
+          v.z = __ldg(reinterpret_cast<const uint32_t*>(p + d0 + 8));
+        }
+        if (qn + 8 < rows) {
+          row_of(info, a.g, sg.head, row_base + qn + 8, &tok, &head);
+          const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
+          v.y = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
+          v.w = __ldg(reinterpret_cast<const uint32_t*>(p + d0 + 8));
+        }
+        sm.q[ks][ln] = v;
       }
-      if (qn + 8 < rows) {
-        row_of(info, a.g, sg.head, row_base + qn + 8, &tok, &head);
-        const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
-        v.y = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
-        v.w = __ldg(reinterpret_cast<const uint32_t*>(p + d1));
+    } else {
+      // A warp splits four rows: brought to (224, 448] by a power of two, a row is the sum of two
+      // e4m3 vectors (see split_e4m3).  The k order inside a 64-column block follows the keys'
+      // loads: lane t of a quad reads 16 consecutive columns, eight to a k-step.
+      constexpr int kEl = D == 256 ? 8 : 4;              // columns of a lane (D = 64: half the lanes)
+      const int d0 = lane * kEl;
+      uint32_t w[4][kEl / 2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = warp * 4 + j;
+#pragma unroll
+        for (int e = 0; e < kEl / 2; ++e) w[j][e] = 0;
+        if (r < rows && d0 < D) {
+          int tok, head;
+          row_of(info, a.g, sg.head, row_base + r, &tok, &head);
+          const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld + d0;
+#pragma unroll
+          for (int e = 0; e < kEl / 4; ++e) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p) + e);
+            w[j][2 * e] = u.x;
+            w[j][2 * e + 1] = u.y;
+          }
+        }
       }
-      sm.q[ks][ln] = v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = warp * 4 + j;
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < kEl / 2; ++e) top = max(top, max(w[j][e] & 0x7fffu, (w[j][e] >> 16) & 0x7fffu));
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int bb = scale_byte(top);
+        const float inv = __uint_as_float((uint32_t)(254 - (bb == 255 ? 127 : bb)) << 23);
+        if (lane == 0) sm.q_scale[r] = scale_f32(bb) * a.scale_log2;
+#pragma unroll
+        for (int e = 0; e < kEl / 4; ++e) {
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            split_e4m3(__uint_as_float(w[j][2 * e + k] << 16) * inv,
+                       __uint_as_float(w[j][2 * e + k] & 0xffff0000u) * inv, hi[k], lo[k]);
+          const int d = d0 + 4 * e;
+          if (d < D) {
+            const int ks = (d >> 6) * 2 + ((d >> 3) & 1), ln = (r & 7) * 4 + ((d >> 4) & 3);
+            const int reg = (r >> 3) + 2 * ((d >> 2) & 1);
+            reinterpret_cast<uint32_t*>(&sm.q[ks][ln])[reg] = hi[0] | (hi[1] << 16);
+            reinterpret_cast<uint32_t*>(&sm.q[D / 32 + ks][ln])[reg] = lo[0] | (lo[1] << 16);
+          }
+        }
+      }
     }
     bar_sync(1, NC);
     // last position each of this thread's two rows sees
     const int pos0 = before + (row_base + n) / a.g, pos1 = before + (row_base + n + 8) / a.g;
     const int pos_min = before + row_base / a.g;
+    const float scale0 = Q8 ? sm.q_scale[n] : a.scale_log2, scale1 = Q8 ? sm.q_scale[n + 8] : a.scale_log2;
+    // 8-bit values: the accumulators count in 2^(v_ref - 134), v_ref the largest scale byte so far
+    int v_ref = 0;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    for (int i = sg.ta; i < sg.tb; ++i, ++turn) {
+    for (int i = sg.ta; i < sg.tb; ++i) {
       const int st = stage;
       const uint32_t ph = phase;
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-      if (C::kTeams > 1 && (int)(turn % C::kTeams) != team) continue;
       wait_or_die(&sm.full[st], ph, &sm.dead, c.status);
       const int k0 = i * TK + grp * 16;
       if (k0 < keys) {
@@ -283,53 +361,56 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             mma16816(s[1], q, r[2], r[3]);
           }
         } else {
-          // column n of score tile j is key (n >> 1) + 4 (2 j + (n & 1)): the order in which the
-          // value fragments below want them
+          // column n of score tile j is key 4 (n >> 1) + 2 j + (n & 1): the order in which the
+          // transposed loads below hand out the values
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb) {
             uint4 w[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int key = (n >> 1) + 4 * (2 * j + (n & 1));
+              const int key = 4 * (n >> 1) + 2 * j + (n & 1);
               const int chunk = (C::kBox == 128) ? (((cb & 1) * 4 + t) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
               w[j] = lds128(kb + (C::kBox == 128 ? (cb >> 1) * 2048 : 0) + key * C::kBox + chunk * 16);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 q = sm.q[cb * 4 + e][lane];
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t x = e == 0 ? w[j].x : e == 1 ? w[j].y : e == 2 ? w[j].z : w[j].w;
-                uint32_t b0, b1;
-                e4m3x4_to_bf16(x, b0, b1);
-                mma16816(s[j], q, b0, b1);
+              for (int part = 0; part < 2; ++part) {
+                const uint4 q = sm.q[part * (D / 32) + cb * 2 + e][lane];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  mma16832_e4m3(s[j], q, e ? w[j].z : w[j].x, e ? w[j].w : w[j].y);
               }
-            }
           }
         }
-        float vs[2][2];
+        uint32_t v_bytes = 0;                          // scale bytes of the values of keys 4 t .. 4 t + 3
+        if constexpr (Q8) {
+          const uint32_t k_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][0][grp][4 * t]);
+          v_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][1][grp][4 * t]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float f = a.scale_log2;
-            if constexpr (Q8) {
-              const int key = t + 4 * (2 * j + e);
-              f *= scale_f32(sm.scales[st][0][grp][key]);
-              vs[j][e] = scale_f32(sm.scales[st][1][grp][key]);
-            } else {
-              vs[j][e] = 1.f;
+            for (int e = 0; e < 2; ++e) {
+              const float f = scale_f32((k_bytes >> (8 * (2 * j + e))) & 0xffu);
+              s[j][e] *= f * scale0;
+              s[j][e + 2] *= f * scale1;
             }
-            s[j][e] *= f;
-            s[j][e + 2] *= f;
-          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              s[j][e] *= scale0;
+              s[j][e + 2] *= scale1;
+            }
+        }
         const bool partial = k0 + 15 > pos_min;       // some row does not see all 16 keys
         if (partial) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int key = k0 + (Q8 ? t + 4 * (2 * j + e) : j * 8 + 2 * t + e);
+              const int key = k0 + (Q8 ? 4 * t + 2 * j + e : j * 8 + 2 * t + e);
               if (key > pos0) s[j][e] = -INFINITY;
               if (key > pos1) s[j][e + 2] = -INFINITY;
             }
@@ -362,24 +443,10 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             l0 += s[j][e];
             l1 += s[j][e + 2];
           }
-        uint4 p;
-        if constexpr (Q8) {
-          // the value's scale; a hidden key stays at zero even if its vector reads as NaN
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = k0 + t + 4 * (2 * j + e);
-              s[j][e] = key > pos0 ? 0.f : s[j][e] * vs[j][e];
-              s[j][e + 2] = key > pos1 ? 0.f : s[j][e + 2] * vs[j][e];
-            }
-        }
-        p.x = pack_bf16(s[0][0], s[0][1]);
-        p.y = pack_bf16(s[0][2], s[0][3]);
-        p.z = pack_bf16(s[1][0], s[1][1]);
-        p.w = pack_bf16(s[1][2], s[1][3]);
         // ---- values
         if constexpr (!Q8) {
+          const uint4 p = make_uint4(pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
+                                     pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3]));
           const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
           const uint32_t row = vb + key * 128;
           // keys past the sequence's end: their rows may hold anything, and 0 x NaN is NaN
@@ -430,50 +497,75 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
               }
             }
           }
-        } else if constexpr (D >= 128) {
-          // lane (n, t) reads 16 bytes (16 columns) of keys t, t + 4, t + 8, t + 12; byte jn of
-          // them is this lane's column n of output tile jn
-          const int col = (n & 1) * 4 + (n >> 1);
+        } else {
+          // The probabilities take the values' scales 2^(b - 127) as 2^(b - v_ref + 7), v_ref the
+          // largest b so far: f16 has eleven bits for them from 2^15 down to 2^-14, which is room
+          // for scales 2^18 apart.  Where they are further apart, bf16 operands instead.
+          uint32_t most = 0, least = 255;
 #pragma unroll
-          for (int blk = 0; blk < D / 128; ++blk) {
-            uint4 w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int key = t + 4 * j;
-              w[j] = lds128(vb + blk * 2048 + key * 128 + ((col ^ (key & 7)) << 4));
+          for (int i2 = 0; i2 < 4; ++i2) {
+            const uint32_t bb = (v_bytes >> (8 * i2)) & 0xffu;
+            if (k0 + 4 * t + i2 < keys && bb != 255) {
+              most = max(most, bb);
+              least = min(least, bb);
             }
+          }
+          most = __reduce_max_sync(0xffffffffu, most);
+          least = __reduce_min_sync(0xffffffffu, least);
+          if ((int)most > v_ref) {
+            const int d = v_ref - (int)most;
+            const float f = d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23);
+            v_ref = (int)most;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t e0 = q == 0 ? w[0].x : q == 1 ? w[0].y : q == 2 ? w[0].z : w[0].w;
-              const uint32_t e1 = q == 0 ? w[1].x : q == 1 ? w[1].y : q == 2 ? w[1].z : w[1].w;
-              const uint32_t e2 = q == 0 ? w[2].x : q == 1 ? w[2].y : q == 2 ? w[2].z : w[2].w;
-              const uint32_t e3 = q == 0 ? w[3].x : q == 1 ? w[3].y : q == 2 ? w[3].z : w[3].w;
+            for (int i2 = 0; i2 < D / 8; ++i2) {
+              o[i2][0] *= f; o[i2][1] *= f; o[i2][2] *= f; o[i2][3] *= f;
+            }
+          }
+          const bool wide = v_ref - (int)least > 18;
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                // byte y of e0 into byte 1, of e1 into byte 3 (the other two are masked away)
-                const uint32_t sel = (uint32_t)((4 + y) << 12 | y << 4);
-                mma16816(o[blk * 16 + q * 4 + y], p, e4m3_hi_to_bf16x2(__byte_perm(e0, e1, sel)),
-                         e4m3_hi_to_bf16x2(__byte_perm(e2, e3, sel)));
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = k0 + 4 * t + 2 * j + e;
+              const int bb = (int)((v_bytes >> (8 * (2 * j + e))) & 0xffu);
+              const float f = bb == 255 ? __int_as_float(0x7fffffff)
+                                        : __uint_as_float((uint32_t)max(bb - v_ref + 134, 0) << 23);
+              // a hidden key stays at zero even if its vector reads as NaN
+              s[j][e] = key > pos0 ? 0.f : s[j][e] * f;
+              s[j][e + 2] = key > pos1 ? 0.f : s[j][e + 2] * f;
+            }
+          const int key = lane & 15;
+          const uint32_t row = vb + key * C::kBox;
+          if (!wide) {
+            const uint4 p = make_uint4(pack_f16(s[0][0], s[0][1]), pack_f16(s[0][2], s[0][3]),
+                                       pack_f16(s[1][0], s[1][1]), pack_f16(s[1][2], s[1][3]));
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+              const int chunk = 2 * d + (lane >> 4);
+              uint32_t r[4];
+              ldsm2t_b8(C::kBox == 128 ? row + (d >> 2) * 2048 + (((chunk & 7) ^ (key & 7)) << 4)
+                                       : row + ((chunk ^ ((key >> 1) & 3)) << 4), r);
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2)
+                mma16816_f16(o[4 * d + i2], p, e4m3_to_f16x2((uint16_t)r[i2]), e4m3_to_f16x2((uint16_t)(r[i2] >> 16)));
+            }
+          } else {
+            const uint4 p = make_uint4(pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
+                                       pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3]));
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+              const int chunk = 2 * d + (lane >> 4);
+              uint32_t r[4];
+              ldsm2t_b8(C::kBox == 128 ? row + (d >> 2) * 2048 + (((chunk & 7) ^ (key & 7)) << 4)
+                                       : row + ((chunk ^ ((key >> 1) & 3)) << 4), r);
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) {
+                uint32_t b0, b1;
+                e4m3x4_to_bf16(r[i2], b0, b1);
+                mma16816(o[4 * d + i2], p, b0, b1);
               }
             }
           }
-        } else {
-          // D = 64: 64-byte rows, 8 columns (8 bytes) per lane
-          uint2 w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = t + 4 * j;
-            w[j] = lds64(vb + key * 64 + (((n >> 1) ^ ((key >> 1) & 3)) << 4) + (n & 1) * 8);
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t sel = (uint32_t)((4 + y) << 12 | y << 4);
-              mma16816(o[q * 4 + y], p,
-                       e4m3_hi_to_bf16x2(__byte_perm(q ? w[0].y : w[0].x, q ? w[1].y : w[1].x, sel)),
-                       e4m3_hi_to_bf16x2(__byte_perm(q ? w[2].y : w[2].x, q ? w[3].y : w[3].x, sel)));
-            }
         }
       }
       __syncwarp();
@@ -499,16 +591,17 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       M0 = fmaxf(M0, sm.ml[w][n][0]);
       M1 = fmaxf(M1, sm.ml[w][n + 8][0]);
     }
-    const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
+    float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
+    if (Q8) {
+      const float unit = v_ref == 0 ? 0.f : __uint_as_float((uint32_t)(v_ref - 7) << 23);   // 2^(v_ref - 134)
+      f0 *= unit;
+      f1 *= unit;
+    }
     for (int w = 0; w < C::kConsumers; ++w) {
       if (warp == w) {
 #pragma unroll
         for (int d = 0; d < D / 8; ++d) {
-          // columns of o[d][0], o[d][1]
-          int ca, cb;
-          if constexpr (!Q8) { ca = d * 8 + 2 * t; cb = ca + 1; }
-          else if constexpr (D >= 128) { ca = (d >> 4) * 128 + t * 16 + (d & 15); cb = ca + 64; }
-          else { ca = 2 * t * 8 + d; cb = ca + 8; }
+          const int ca = d * 8 + 2 * t, cb = ca + 1;
           const float a0 = o[d][0] * f0, a1 = o[d][1] * f0, a2 = o[d][2] * f1, a3 = o[d][3] * f1;
           if (w == 0) {
             sm.o[n][ca] = a0; sm.o[n][cb] = a1; sm.o[n + 8][ca] = a2; sm.o[n + 8][cb] = a3;

@@ -2,6 +2,8 @@
 // the exact e4m3 -> bf16 conversion.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -90,6 +92,21 @@ __device__ __forceinline__ int scale_byte(uint32_t top) {
   if (top == 0) return 127;
   const int e = (int)(top >> 7) - 8 + ((top & 0x7f) > 0x60 ? 1 : 0);
   return e < 10 ? 10 : e;
+}
+
+// (x, y) = hi + lo in e4m3 codes, |x|, |y| <= 448.  A query row brought to (224, 448] by a power of
+// two is the sum of two e4m3 vectors: the codes nearest to it, and what they leave, which fits their
+// four significant bits again (bf16 has eight).  Elements below 2^-10 of the row's largest lose bits
+// at 2^-18 of it.
+__device__ __forceinline__ void split_e4m3(float x, float y, uint32_t& hi, uint32_t& lo) {
+  uint16_t h, l;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
+  uint32_t f;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(y - v.y), "f"(x - v.x));
+  hi = h;
+  lo = l;
 }
 
 }  // namespace gdn

@@ -237,3 +237,19 @@ def test_graph_other_stream_and_reuse():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[1], first[1]) and not torch.equal(out[0], first[0])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("apart", [6, 17, 40])
+def test_scales_far_apart(dim, apart):
+    """Vectors of one head whose magnitudes differ by up to 2^apart, in and across key tiles, with
+    the large values both seen strongly and not at all."""
+    for new, length in ((1, 700), (40, 300)):
+        case = ref.Case([new], [length], 1, dim, 32, True, seed=13)
+        e = torch.randint(-apart, 1, (length, 1, 1), generator=torch.Generator().manual_seed(apart)).float()
+        case.v[0] = (case.v[0].float() * torch.exp2(e)).to(torch.bfloat16)
+        case.k[0] = (case.k[0].float() * torch.exp2((e / 8).round())).to(torch.bfloat16)
+        _check(case, 4)
+        case.v[0][::7] *= 2.0 ** 20
+        case.k[0][::7] = 0
+        _check(case, 4)
