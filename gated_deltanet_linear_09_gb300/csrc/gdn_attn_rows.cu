@@ -44,42 +44,45 @@ struct RowsCfg {
   static constexpr int kHalfBytes = 4 * kGroupBytes;             // a stage's keys
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRing = kCtas == 1 ? 196608 : 98304;
-  static constexpr int kFit = kRing / (kStageBytes + (Q8 ? 1024 : 0));   // with the scale bytes
+  static constexpr int kFit = (kRing - (Q8 ? 64 * D : 0)) / kStageBytes;   // beside the queries' parts
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kBox = D * kElem >= 128 ? 128 : 64;       // swizzle span, bytes
-  static constexpr int kLd = D + 8;                              // merge buffer row
+  static constexpr int kQLd = 2 * D + 16;                        // bytes of a staged query row
+  static constexpr int kChunk = D / 4;                           // columns merged at a time
+  static constexpr int kMLd = kChunk + 4;
 };
 
 template <int D, bool Q8>
 struct __align__(1024) RowsSmem {
   using C = RowsCfg<D, Q8>;
   uint8_t ring[C::kStages][C::kStageBytes];
-  // scale bytes of a stage's four 16-key groups (16 bytes each: TMA wants 128-byte destinations)
-  uint8_t scales[Q8 ? C::kStages : 1][2][4][128];
-  uint4 q[D / 16][32];                    // A fragments of the 16 rows (8-bit: of their two parts)
+  uint8_t scales[Q8 ? C::kStages : 1][2][kTileKeys];    // scale bytes of a stage's keys and values
+  uint8_t q[kRows][C::kQLd];              // the rows, as copied
+  uint4 q_parts[Q8 ? D / 16 : 1][32];     // 8-bit caches: A fragments of their two e4m3 parts
   float q_scale[kRows];
-  float o[kRows][C::kLd];
+  float o[C::kConsumers][kRows][C::kMLd];
   float ml[C::kConsumers][kRows][2];
   LineScan<kRows, C::kThreads> scan;
   uint64_t full[C::kStages];
   uint64_t empty[C::kStages];
+  uint64_t q_full, q_empty;
   int dead;
 };
 
 __device__ __forceinline__ void mma16816(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma16816_f16(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma16832_e4m3(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
@@ -115,11 +118,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
@@ -136,6 +134,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// 16 bytes (zeros when !fill) by cp.async, and one arrival on bar when they are there.
+__device__ __forceinline__ void cp_async16_mbar(uint32_t dst, const void* src, bool fill, uint64_t* bar) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;\n"
+               "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%3];\n" ::"r"(dst),
+               "l"(src), "r"(fill ? 16 : 0), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // A bounded wait: a timeout marks the CTA dead, after which no wait blocks and the (wrong) results
@@ -160,12 +166,19 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.full[i], Q8 ? 9 : 1);
       mbar_init(&sm.empty[i], 4);
     }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, C::kConsumers);
     sm.dead = 0;
     mbar_fence_init();
   }
+  // rows past a tile's last are multiplied too: nothing comes of them, but what they hold must not
+  // differ from run to run (all rows of a warp move their references together)
+  for (int i = tid; i < R * C::kQLd / 16; i += C::kThreads)
+    reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   pdl_begin();
   zero_padding(a, b, D);
   bool bad = false;
@@ -185,12 +198,18 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   if (warp == C::kConsumers) {
     // ---------------------------------------------------------------- producer
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, q_phase = 0;
     while (it.next(&sg)) {
       if (sg.ta >= sg.tb) continue;
+      const int rows = (int)min((long long)R, (long long)sg.info.tokens * a.g - sg.tile * R);
+      // the queries' place is free when the tile before has been scored: after what the ring takes
+      const int q_after = min(sg.tb, sg.ta + C::kStages - 1) - 1;
       const int* table = b.table + (long long)sg.seq * b.table_ld;
       const int keys = min(sg.info.len, tile_keys<R>(sg.info, a.g, sg.tile));
-      // lane i < 4 looks after the stage's i-th 16 keys
+      // Lane i looks after the i & 3-th 16 keys of a stage: their page, fetched a stage ahead, and,
+      // for an 8-bit cache, the scale bytes of the keys (lanes 0 to 3) and of the values (4 to 7).
+      // Lanes 0 to 3 copy the boxes that begin at their keys (a box is a page's part of the stage).
+      const int box = min(1 << c.page_shift, TK);
       int k0 = sg.ta * TK + (lane & 3) * 16;
       int page = k0 < keys ? __ldg(table + (k0 >> c.page_shift)) : 0;
       for (int i = sg.ta; i < sg.tb; ++i) {
@@ -198,26 +217,39 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         int page_next = 0;
         if (i + 1 < sg.tb && k1 < keys) page_next = __ldg(table + (k1 >> c.page_shift));
         wait_or_die(&sm.empty[stage], phase ^ 1u, &sm.dead, c.status);
-        const int live = min(4, (keys - i * TK + 15) >> 4);
         uint64_t* full = &sm.full[stage];
-        if (lane == 0)
-          mbar_arrive_expect_tx(full, (uint32_t)live * (2 * C::kGroupBytes + (Q8 ? 32 : 0)));
+        const int live = (min(TK, keys - i * TK) + box - 1) / box;            // boxes
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(live * box * 2 * D * C::kElem));
         __syncwarp();
-        if (lane < live) {
-          if (page < 0 || page >= c.num_pages) {
-            set_status(c.status, GDN_STATUS_PAGE_RANGE);
-            page = c.num_pages;            // outside the map: the copy fills zeros
-          }
-          const int off = k0 & ((1 << c.page_shift) - 1);
+        if (k0 < keys && (page < 0 || page >= c.num_pages)) {
+          set_status(c.status, GDN_STATUS_PAGE_RANGE);
+          page = c.num_pages;            // outside the map: the copy fills zeros
+        }
+        const int off = k0 & ((1 << c.page_shift) - 1);
+        if (lane < 4 && k0 < keys && ((lane * 16) & (box - 1)) == 0) {
           uint8_t* st = sm.ring[stage] + lane * C::kGroupBytes;
           tma_load_5d(st, &maps.k, 0, off, 0, sg.head, page, full);
           tma_load_5d(st + C::kHalfBytes, &maps.v, 0, off, 0, sg.head, page, full);
-          if constexpr (Q8) {
-            tma_load_3d(sm.scales[stage][0][lane], &maps.ks, off, sg.head, page, full);
-            tma_load_3d(sm.scales[stage][1][lane], &maps.vs, off, sg.head, page, full);
-          }
+        }
+        if (Q8 && lane < 8) {
+          const bool in = k0 < keys && page < c.num_pages;
+          const uint8_t* src = (lane < 4 ? c.ks : c.vs);
+          if (in) src += (((long long)page * c.H + sg.head) << c.page_shift) + off;
+          cp_async16_mbar(smem_u32(&sm.scales[stage][lane >> 2][(lane & 3) * 16]), src, in, full);
         }
         __syncwarp();
+        if (i == q_after) {
+          wait_or_die(&sm.q_empty, q_phase ^ 1u, &sm.dead, c.status);
+          q_phase ^= 1u;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)rows * 2 * D);
+          __syncwarp();
+          if (lane < rows) {
+            int tok, head;
+            row_of(sg.info, a.g, sg.head, sg.tile * R + lane, &tok, &head);
+            bulk_g2s(sm.q[lane], a.q + tok * a.q_ld + head * a.q_head_ld, 2 * D, &sm.q_full);
+          }
+          __syncwarp();
+        }
         page = page_next;
         k0 = k1;
         if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
@@ -231,8 +263,12 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   // ------------------------------------------------------------------ consumers
   const int t = lane & 3, n = lane >> 2;
   const int grp = warp;
+  // a box of `box` keys is [column blocks][box][128 bytes]
+  const int box = min(1 << c.page_shift, TK);
+  const uint32_t blk_bytes = box * C::kBox;
+  const uint32_t grp_at = (grp * 16 / box) * (box * D * C::kElem) + (grp * 16 % box) * C::kBox;
   int stage = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, q_phase = 0;
   while (it.next(&sg)) {
     const SeqInfo info = sg.info;
     const int row_base = sg.tile * R;
@@ -252,57 +288,26 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     }
     const int keys = min(info.len, tile_keys<R>(info, a.g, sg.tile));
     const int before = info.len - info.tokens;          // position of the first new token
-    if constexpr (!Q8) {
-      // Q fragments: words (row, two neighbouring columns) of k-step ks
-#pragma unroll 4
-      for (int i = tid; i < (D / 16) * 32; i += NC) {
-        const int ks = i >> 5, ln = i & 31, qn = ln >> 2, d0 = ks * 16 + 2 * (ln & 3);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        int tok, head;
-        if (qn < rows) {
-          row_of(info, a.g, sg.head, row_base + qn, &tok, &head);
-          const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
-          v.x = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
-          v.z = __ldg(reinterpret_cast<const uint32_t*>(p + d0 + 8));
-        }
-        if (qn + 8 < rows) {
-          row_of(info, a.g, sg.head, row_base + qn + 8, &tok, &head);
-          const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld;
-          v.y = __ldg(reinterpret_cast<const uint32_t*>(p + d0));
-          v.w = __ldg(reinterpret_cast<const uint32_t*>(p + d0 + 8));
-        }
-        sm.q[ks][ln] = v;
-      }
-    } else {
-      // A warp splits four rows: brought to (224, 448] by a power of two, a row is the sum of two
-      // e4m3 vectors (see split_e4m3).  The k order inside a 64-column block follows the keys'
-      // loads: lane t of a quad reads 16 consecutive columns, eight to a k-step.
+    wait_or_die(&sm.q_full, q_phase, &sm.dead, c.status);
+    q_phase ^= 1u;
+    if constexpr (Q8) {
+      // A warp splits four rows into their parts (see split_e4m3).  The k order inside a 64-column
+      // block follows the keys' loads: lane t of a quad reads 16 consecutive columns, eight to a
+      // k-step.
       constexpr int kEl = D == 256 ? 8 : 4;              // columns of a lane (D = 64: half the lanes)
       const int d0 = lane * kEl;
-      uint32_t w[4][kEl / 2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = warp * 4 + j;
+        uint32_t w[kEl / 2], top = 0;
 #pragma unroll
-        for (int e = 0; e < kEl / 2; ++e) w[j][e] = 0;
-        if (r < rows && d0 < D) {
-          int tok, head;
-          row_of(info, a.g, sg.head, row_base + r, &tok, &head);
-          const __nv_bfloat16* p = a.q + tok * a.q_ld + head * a.q_head_ld + d0;
-#pragma unroll
-          for (int e = 0; e < kEl / 4; ++e) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p) + e);
-            w[j][2 * e] = u.x;
-            w[j][2 * e + 1] = u.y;
-          }
+        for (int e = 0; e < kEl / 4; ++e) {
+          const uint2 u = d0 < D ? reinterpret_cast<const uint2*>(sm.q[r] + 2 * d0)[e] : make_uint2(0, 0);
+          w[2 * e] = u.x;
+          w[2 * e + 1] = u.y;
         }
-      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = warp * 4 + j;
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < kEl / 2; ++e) top = max(top, max(w[j][e] & 0x7fffu, (w[j][e] >> 16) & 0x7fffu));
+        for (int e = 0; e < kEl / 2; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         top = __reduce_max_sync(0xffffffffu, top);
         const int bb = scale_byte(top);
         const float inv = __uint_as_float((uint32_t)(254 - (bb == 255 ? 127 : bb)) << 23);
@@ -312,19 +317,20 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            split_e4m3(__uint_as_float(w[j][2 * e + k] << 16) * inv,
-                       __uint_as_float(w[j][2 * e + k] & 0xffff0000u) * inv, hi[k], lo[k]);
+            split_e4m3(__uint_as_float(w[2 * e + k] << 16) * inv, __uint_as_float(w[2 * e + k] & 0xffff0000u) * inv,
+                       hi[k], lo[k]);
           const int d = d0 + 4 * e;
           if (d < D) {
             const int ks = (d >> 6) * 2 + ((d >> 3) & 1), ln = (r & 7) * 4 + ((d >> 4) & 3);
             const int reg = (r >> 3) + 2 * ((d >> 2) & 1);
-            reinterpret_cast<uint32_t*>(&sm.q[ks][ln])[reg] = hi[0] | (hi[1] << 16);
-            reinterpret_cast<uint32_t*>(&sm.q[D / 32 + ks][ln])[reg] = lo[0] | (lo[1] << 16);
+            reinterpret_cast<uint32_t*>(&sm.q_parts[ks][ln])[reg] = hi[0] | (hi[1] << 16);
+            reinterpret_cast<uint32_t*>(&sm.q_parts[D / 32 + ks][ln])[reg] = lo[0] | (lo[1] << 16);
           }
         }
       }
+      bar_sync(1, NC);
+      if (lane == 0) mbar_arrive(&sm.q_empty);
     }
-    bar_sync(1, NC);
     // last position each of this thread's two rows sees
     const int pos0 = before + (row_base + n) / a.g, pos1 = before + (row_base + n + 8) / a.g;
     const int pos_min = before + row_base / a.g;
@@ -336,57 +342,86 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
+    // raw scores of this warp's 16 keys of a stage: 16 rows x 2 columns of 8 keys
+    auto scores = [&](int st, float (&s)[2][4]) {
+      const uint8_t* kb = sm.ring[st] + grp_at;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      if constexpr (!Q8) {
+        const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+        const uint32_t row = smem_u32(kb) + key * 128;
+        const uint32_t q_row = smem_u32(sm.q[lane & 15]) + (lane >> 4) * 16;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t r[4];
+          uint4 q;
+          ldsm4(row + (ks >> 2) * blk_bytes + ((((ks & 3) * 2 + half) ^ (key & 7)) << 4), r);
+          ldsm4(q_row + ks * 32, &q.x);
+          mma16816(s[0], q, r[0], r[1]);
+          mma16816(s[1], q, r[2], r[3]);
+        }
+      } else {
+        // column n of score tile j is key 4 (n >> 1) + 2 j + (n & 1): the order in which the
+        // transposed loads below hand out the values
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb) {
+          uint4 w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int key = 4 * (n >> 1) + 2 * j + (n & 1);
+            const int chunk = (C::kBox == 128) ? (((cb & 1) * 4 + t) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
+            w[j] = *reinterpret_cast<const uint4*>(kb + (C::kBox == 128 ? (cb >> 1) * blk_bytes : 0) + key * C::kBox +
+                                                   chunk * 16);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const uint4 q = sm.q_parts[part * (D / 32) + cb * 2 + e][lane];
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma16832_e4m3(s[j], q, e ? w[j].z : w[j].x, e ? w[j].w : w[j].y);
+            }
+        }
+      }
+    };
+    // One iteration's scores are computed during the one before (8-bit caches: with half the bytes to
+    // wait for, the chain from a key's arrival to its product is what would set the pace; bf16
+    // caches are bound by the loads without it).
+    constexpr bool kAhead = Q8;
+    float ahead[2][4];
+    auto advance = [&]() {
+      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+    };
+    if (kAhead) {
+      wait_or_die(&sm.full[stage], phase, &sm.dead, c.status);
+      scores(stage, ahead);
+    }
     for (int i = sg.ta; i < sg.tb; ++i) {
       const int st = stage;
-      const uint32_t ph = phase;
-      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-      wait_or_die(&sm.full[st], ph, &sm.dead, c.status);
+      float s[2][4];
+      if constexpr (kAhead) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] = ahead[j][e];
+        advance();
+        if (i + 1 < sg.tb) {
+          wait_or_die(&sm.full[stage], phase, &sm.dead, c.status);
+          scores(stage, ahead);
+        }
+      } else {
+        wait_or_die(&sm.full[st], phase, &sm.dead, c.status);
+        scores(st, s);
+        advance();
+      }
       const int k0 = i * TK + grp * 16;
       if (k0 < keys) {
-        const uint32_t kb = smem_u32(sm.ring[st]) + grp * C::kGroupBytes;
-        const uint32_t vb = kb + C::kHalfBytes;
-        // ---- scores: 16 rows x 16 keys
-        float s[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        if constexpr (!Q8) {
-          const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
-          const uint32_t row = kb + key * 128;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t r[4];
-            ldsm4(row + (ks >> 2) * 2048 + ((((ks & 3) * 2 + half) ^ (key & 7)) << 4), r);
-            const uint4 q = sm.q[ks][lane];
-            mma16816(s[0], q, r[0], r[1]);
-            mma16816(s[1], q, r[2], r[3]);
-          }
-        } else {
-          // column n of score tile j is key 4 (n >> 1) + 2 j + (n & 1): the order in which the
-          // transposed loads below hand out the values
-#pragma unroll
-          for (int cb = 0; cb < D / 64; ++cb) {
-            uint4 w[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int key = 4 * (n >> 1) + 2 * j + (n & 1);
-              const int chunk = (C::kBox == 128) ? (((cb & 1) * 4 + t) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
-              w[j] = lds128(kb + (C::kBox == 128 ? (cb >> 1) * 2048 : 0) + key * C::kBox + chunk * 16);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                const uint4 q = sm.q[part * (D / 32) + cb * 2 + e][lane];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  mma16832_e4m3(s[j], q, e ? w[j].z : w[j].x, e ? w[j].w : w[j].y);
-              }
-          }
-        }
+        const uint32_t vb = smem_u32(sm.ring[st]) + grp_at + C::kHalfBytes;
         uint32_t v_bytes = 0;                          // scale bytes of the values of keys 4 t .. 4 t + 3
         if constexpr (Q8) {
-          const uint32_t k_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][0][grp][4 * t]);
-          v_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][1][grp][4 * t]);
+          const uint32_t k_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][0][grp * 16 + 4 * t]);
+          v_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][1][grp * 16 + 4 * t]);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -465,7 +500,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll 4
             for (int d = 0; d < D / 16; ++d) {
               uint32_t r[4];
-              ldsm4t(row + (d >> 2) * 2048 + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
+              ldsm4t(row + (d >> 2) * blk_bytes + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
               seen |= ((r[0] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[1] & z1 & 0x7f807f80u) + 0x00800080u) |
                       ((r[2] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[3] & z1 & 0x7f807f80u) + 0x00800080u);
             }
@@ -475,7 +510,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
               uint32_t r[4];
-              ldsm4t(row + (d >> 2) * 2048 + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
+              ldsm4t(row + (d >> 2) * blk_bytes + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
               if (tail) { r[0] &= z0; r[1] &= z1; r[2] &= z0; r[3] &= z1; }
               mma16816(o[2 * d], p, r[0], r[1]);
               mma16816(o[2 * d + 1], p, r[2], r[3]);
@@ -490,7 +525,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
               const bool see0 = k0 + j <= pos0, see1 = k0 + j <= pos1;
 #pragma unroll
               for (int d = 0; d < D / 8; ++d) {
-                const uint32_t w = lds32(vb + j * 128 + (d >> 3) * 2048 + (((d & 7) ^ (j & 7)) << 4) + t * 4);
+                const uint32_t w = lds32(vb + j * 128 + (d >> 3) * blk_bytes + (((d & 7) ^ (j & 7)) << 4) + t * 4);
                 const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
                 if (see0) { o[d][0] = fmaf(p0, v0, o[d][0]); o[d][1] = fmaf(p0, v1, o[d][1]); }
                 if (see1) { o[d][2] = fmaf(p1, v0, o[d][2]); o[d][3] = fmaf(p1, v1, o[d][3]); }
@@ -540,14 +575,20 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             const uint4 p = make_uint4(pack_f16(s[0][0], s[0][1]), pack_f16(s[0][2], s[0][3]),
                                        pack_f16(s[1][0], s[1][1]), pack_f16(s[1][2], s[1][3]));
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-              const int chunk = 2 * d + (lane >> 4);
-              uint32_t r[4];
-              ldsm2t_b8(C::kBox == 128 ? row + (d >> 2) * 2048 + (((chunk & 7) ^ (key & 7)) << 4)
-                                       : row + ((chunk ^ ((key >> 1) & 3)) << 4), r);
+            for (int d0 = 0; d0 < D / 32; d0 += 2) {
+              uint32_t r[2][4];
 #pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2)
-                mma16816_f16(o[4 * d + i2], p, e4m3_to_f16x2((uint16_t)r[i2]), e4m3_to_f16x2((uint16_t)(r[i2] >> 16)));
+              for (int d = 0; d < 2; ++d) {
+                const int chunk = 2 * (d0 + d) + (lane >> 4);
+                ldsm2t_b8(C::kBox == 128 ? row + ((d0 + d) >> 2) * blk_bytes + (((chunk & 7) ^ (key & 7)) << 4)
+                                         : row + ((chunk ^ ((key >> 1) & 3)) << 4), r[d]);
+              }
+#pragma unroll
+              for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2)
+                  mma16816_f16(o[4 * (d0 + d) + i2], p, e4m3_to_f16x2((uint16_t)r[d][i2]),
+                               e4m3_to_f16x2((uint16_t)(r[d][i2] >> 16)));
             }
           } else {
             const uint4 p = make_uint4(pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
@@ -556,7 +597,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             for (int d = 0; d < D / 32; ++d) {
               const int chunk = 2 * d + (lane >> 4);
               uint32_t r[4];
-              ldsm2t_b8(C::kBox == 128 ? row + (d >> 2) * 2048 + (((chunk & 7) ^ (key & 7)) << 4)
+              ldsm2t_b8(C::kBox == 128 ? row + (d >> 2) * blk_bytes + (((chunk & 7) ^ (key & 7)) << 4)
                                        : row + ((chunk ^ ((key >> 1) & 3)) << 4), r);
 #pragma unroll
               for (int i2 = 0; i2 < 4; ++i2) {
@@ -571,6 +612,8 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[st]);
     }
+
+    if (!Q8 && lane == 0) mbar_arrive(&sm.q_empty);
 
     // ---- the warps' results of this tile become one
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
@@ -597,45 +640,54 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       f0 *= unit;
       f1 *= unit;
     }
-    for (int w = 0; w < C::kConsumers; ++w) {
-      if (warp == w) {
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          const int ca = d * 8 + 2 * t, cb = ca + 1;
-          const float a0 = o[d][0] * f0, a1 = o[d][1] * f0, a2 = o[d][2] * f1, a3 = o[d][3] * f1;
-          if (w == 0) {
-            sm.o[n][ca] = a0; sm.o[n][cb] = a1; sm.o[n + 8][ca] = a2; sm.o[n + 8][cb] = a3;
-          } else {
-            sm.o[n][ca] += a0; sm.o[n][cb] += a1; sm.o[n + 8][ca] += a2; sm.o[n + 8][cb] += a3;
-          }
-        }
-      }
-      bar_sync(1, NC);
-    }
     const bool whole = sg.whole();
     float* prow = Partials<R, D>::rows(a.ws, cta, sg.slot);
-    float* pml = Partials<R, D>::ml(a.ws, cta, sg.slot);
-    for (int i = tid; i < rows * (D / 4); i += NC) {
-      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-      float M = -INFINITY, l = 0.f;
+    // A quarter of the columns at a time: every warp lays its part down, and each thread adds the
+    // warps' values of the four columns it then writes.
+    constexpr int kPieces = C::kChunk / 4, kStep = NC / kPieces;
+    const int piece = tid % kPieces;
 #pragma unroll
-      for (int w = 0; w < C::kConsumers; ++w) M = fmaxf(M, sm.ml[w][r][0]);
+    for (int ch = 0; ch < 4; ++ch) {
 #pragma unroll
-      for (int w = 0; w < C::kConsumers; ++w) {
-        const float mw = sm.ml[w][r][0];
-        if (mw != -INFINITY) l += sm.ml[w][r][1] * ex2(mw - M);
+      for (int d = 0; d < C::kChunk / 8; ++d) {
+        const float* v = o[ch * (C::kChunk / 8) + d];
+        *reinterpret_cast<float2*>(&sm.o[warp][n][d * 8 + 2 * t]) = make_float2(v[0] * f0, v[1] * f0);
+        *reinterpret_cast<float2*>(&sm.o[warp][n + 8][d * 8 + 2 * t]) = make_float2(v[2] * f1, v[3] * f1);
       }
-      float4 v = *reinterpret_cast<const float4*>(&sm.o[r][d]);
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-        int tok, head;
-        row_of(info, a.g, sg.head, row_base + r, &tok, &head);
-        store_out4(a, D, tok, head, d, v);
-      } else {
-        __stcg(reinterpret_cast<float4*>(prow + (size_t)r * D + d), v);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(pml + 2 * r), make_float2(M, l));
+      bar_sync(1, NC);
+      for (int r = tid / kPieces; r < rows; r += kStep) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::kConsumers; ++w) {
+          const float4 u = *reinterpret_cast<const float4*>(&sm.o[w][r][piece * 4]);
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        const int d = ch * C::kChunk + piece * 4;
+        if (whole || (ch == 0 && piece == 0)) {
+          float M = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int w = 0; w < C::kConsumers; ++w) M = fmaxf(M, sm.ml[w][r][0]);
+#pragma unroll
+          for (int w = 0; w < C::kConsumers; ++w) {
+            const float mw = sm.ml[w][r][0];
+            if (mw != -INFINITY) l += sm.ml[w][r][1] * ex2(mw - M);
+          }
+          if (whole) {
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+          } else {
+            __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, sg.slot) + 2 * r), make_float2(M, l));
+          }
+        }
+        if (whole) {
+          int tok, head;
+          row_of(info, a.g, sg.head, row_base + r, &tok, &head);
+          store_out4(a, D, tok, head, d, v);
+        } else {
+          __stcg(reinterpret_cast<float4*>(prow + (size_t)r * D + d), v);
+        }
       }
+      if (ch < 3) bar_sync(1, NC);
     }
     bar_sync(1, NC);
   }
@@ -650,7 +702,8 @@ int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sm
       rows_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (set != cudaSuccess) return GDN_ERR_CUDA;
   KvMaps maps;
-  if (!make_kv_maps(c, 16, &maps)) return GDN_ERR_CUDA;
+  const int P = 1 << c.page_shift;
+  if (!make_kv_maps(c, P < kTileKeys ? P : kTileKeys, &maps)) return GDN_ERR_CUDA;
   const int grid = rows_grid(D, sms), fix = 64 * a.g;
   const int least = 256 * a.g;
   int rc = launch_dependent(rows_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
