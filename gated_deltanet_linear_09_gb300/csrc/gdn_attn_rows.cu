@@ -31,24 +31,25 @@ using namespace tc;
 namespace attn {
 
 constexpr int kRows = 16;
-constexpr int kTileKeys = 64;
 
 template <int D, bool Q8>
 struct RowsCfg {
   // D = 256: the accumulators take 128 registers of a thread, and a stage twice the bytes.
   static constexpr int kConsumers = 4;
   static constexpr int kCtas = D == 256 ? 1 : 2;
-  static constexpr int kThreads = (kConsumers + 1) * 32;
+  static constexpr int kThreads = (kConsumers + 2) * 32;         // and two producers: keys, values
   static constexpr int kElem = Q8 ? 1 : 2;
-  static constexpr int kGroupBytes = 16 * D * kElem;             // 16 keys (or values)
-  static constexpr int kHalfBytes = 4 * kGroupBytes;             // a stage's keys
+  // Groups of 16 keys that a warp takes of a stage.  An MMA's result takes some 70 cycles; with half
+  // the bytes to wait for, an 8-bit cache wants the chains of two groups side by side.
+  static constexpr int kGroups = Q8 ? 2 : 1;
+  static constexpr int kKeys = 64 * kGroups;                     // of a stage
+  static constexpr int kHalfBytes = kKeys * D * kElem;           // a stage's keys
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRing = kCtas == 1 ? 196608 : 98304;
-  static constexpr int kFit = (kRing - (Q8 ? 64 * D : 0)) / kStageBytes;   // beside the queries' parts
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kStages = kRing / kStageBytes;
   static constexpr int kBox = D * kElem >= 128 ? 128 : 64;       // swizzle span, bytes
   static constexpr int kQLd = 2 * D + 16;                        // bytes of a staged query row
-  static constexpr int kChunk = D / 4;                           // columns merged at a time
+  static constexpr int kChunk = D / (Q8 && D > 64 ? 8 : 4);      // columns merged at a time
   static constexpr int kMLd = kChunk + 4;
 };
 
@@ -56,7 +57,7 @@ template <int D, bool Q8>
 struct __align__(1024) RowsSmem {
   using C = RowsCfg<D, Q8>;
   uint8_t ring[C::kStages][C::kStageBytes];
-  uint8_t scales[Q8 ? C::kStages : 1][2][kTileKeys];    // scale bytes of a stage's keys and values
+  uint8_t scales[Q8 ? C::kStages : 1][2][C::kKeys];    // scale bytes of a stage's keys and values
   uint8_t q[kRows][C::kQLd];              // the rows, as copied
   uint4 q_parts[Q8 ? D / 16 : 1][32];     // 8-bit caches: A fragments of their two e4m3 parts
   float q_scale[kRows];
@@ -159,14 +160,13 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8>::kThreads, RowsCfg<D, Q8>::kCta
 rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, int least,
             const __grid_constant__ KvMaps maps) {
   using C = RowsCfg<D, Q8>;
-  constexpr int R = kRows, TK = kTileKeys, NC = C::kConsumers * 32;
-  extern __shared__ uint8_t smem_raw[];
-  RowsSmem<D, Q8>& sm = *reinterpret_cast<RowsSmem<D, Q8>*>(
-      smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  constexpr int R = kRows, TK = C::kKeys, NC = C::kConsumers * 32;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  RowsSmem<D, Q8>& sm = *reinterpret_cast<RowsSmem<D, Q8>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&sm.full[i], Q8 ? 9 : 1);
+      mbar_init(&sm.full[i], Q8 ? 2 + TK / 8 : 2);
       mbar_init(&sm.empty[i], 4);
     }
     mbar_init(&sm.q_full, 1);
@@ -195,8 +195,11 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   Segment sg;
   sg.split = false;
 
-  if (warp == C::kConsumers) {
-    // ---------------------------------------------------------------- producer
+  if (warp >= C::kConsumers) {
+    // ---------------------------------------------------------------- producers
+    // Copies of one warp go out one after another (some 150 cycles each), hence a warp for the keys
+    // and one for the values.
+    const bool values = warp > C::kConsumers;
     int stage = 0;
     uint32_t phase = 0, q_phase = 0;
     while (it.next(&sg)) {
@@ -206,11 +209,11 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       const int q_after = min(sg.tb, sg.ta + C::kStages - 1) - 1;
       const int* table = b.table + (long long)sg.seq * b.table_ld;
       const int keys = min(sg.info.len, tile_keys<R>(sg.info, a.g, sg.tile));
-      // Lane i looks after the i & 3-th 16 keys of a stage: their page, fetched a stage ahead, and,
-      // for an 8-bit cache, the scale bytes of the keys (lanes 0 to 3) and of the values (4 to 7).
-      // Lanes 0 to 3 copy the boxes that begin at their keys (a box is a page's part of the stage).
+      // Lane i < TK / 16 looks after the i-th 16 keys of a stage: their page, fetched a stage ahead,
+      // the box that begins with them (a box is a page's part of the stage), and their scale bytes.
+      constexpr int kLanes = TK / 16;
       const int box = min(1 << c.page_shift, TK);
-      int k0 = sg.ta * TK + (lane & 3) * 16;
+      int k0 = sg.ta * TK + (lane % kLanes) * 16;
       int page = k0 < keys ? __ldg(table + (k0 >> c.page_shift)) : 0;
       for (int i = sg.ta; i < sg.tb; ++i) {
         const int k1 = k0 + TK;
@@ -219,26 +222,24 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         wait_or_die(&sm.empty[stage], phase ^ 1u, &sm.dead, c.status);
         uint64_t* full = &sm.full[stage];
         const int live = (min(TK, keys - i * TK) + box - 1) / box;            // boxes
-        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(live * box * 2 * D * C::kElem));
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(live * box * D * C::kElem));
         __syncwarp();
         if (k0 < keys && (page < 0 || page >= c.num_pages)) {
           set_status(c.status, GDN_STATUS_PAGE_RANGE);
           page = c.num_pages;            // outside the map: the copy fills zeros
         }
         const int off = k0 & ((1 << c.page_shift) - 1);
-        if (lane < 4 && k0 < keys && ((lane * 16) & (box - 1)) == 0) {
-          uint8_t* st = sm.ring[stage] + lane * C::kGroupBytes;
-          tma_load_5d(st, &maps.k, 0, off, 0, sg.head, page, full);
-          tma_load_5d(st + C::kHalfBytes, &maps.v, 0, off, 0, sg.head, page, full);
-        }
-        if (Q8 && lane < 8) {
+        if (lane < kLanes && k0 < keys && ((lane * 16) & (box - 1)) == 0)
+          tma_load_5d(sm.ring[stage] + (values ? C::kHalfBytes : 0) + lane * 16 * D * C::kElem,
+                      values ? &maps.v : &maps.k, 0, off, 0, sg.head, page, full);
+        if (Q8 && lane < kLanes) {
           const bool in = k0 < keys && page < c.num_pages;
-          const uint8_t* src = (lane < 4 ? c.ks : c.vs);
+          const uint8_t* src = values ? c.vs : c.ks;
           if (in) src += (((long long)page * c.H + sg.head) << c.page_shift) + off;
-          cp_async16_mbar(smem_u32(&sm.scales[stage][lane >> 2][(lane & 3) * 16]), src, in, full);
+          cp_async16_mbar(smem_u32(&sm.scales[stage][values][lane * 16]), src, in, full);
         }
         __syncwarp();
-        if (i == q_after) {
+        if (values && i == q_after) {
           wait_or_die(&sm.q_empty, q_phase ^ 1u, &sm.dead, c.status);
           q_phase ^= 1u;
           if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)rows * 2 * D);
@@ -256,17 +257,22 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       }
     }
     // the piece's last tile may be shared with the next ones
-    if (lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &sg, sg.split ? it.sharing(sg.nt) : 0);
+    if (!values && lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &sg, sg.split ? it.sharing(sg.nt) : 0);
     return;
   }
 
   // ------------------------------------------------------------------ consumers
   const int t = lane & 3, n = lane >> 2;
-  const int grp = warp;
+  constexpr int G = C::kGroups;
   // a box of `box` keys is [column blocks][box][128 bytes]
   const int box = min(1 << c.page_shift, TK);
   const uint32_t blk_bytes = box * C::kBox;
-  const uint32_t grp_at = (grp * 16 / box) * (box * D * C::kElem) + (grp * 16 % box) * C::kBox;
+  uint32_t at[G];                                        // this warp's groups in a stage's half
+#pragma unroll
+  for (int u = 0; u < G; ++u) {
+    const int k = (warp * G + u) * 16;
+    at[u] = (k / box) * (box * D * C::kElem) + (k % box) * C::kBox;
+  }
   int stage = 0;
   uint32_t phase = 0, q_phase = 0;
   while (it.next(&sg)) {
@@ -342,122 +348,108 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    // raw scores of this warp's 16 keys of a stage: 16 rows x 2 columns of 8 keys
-    auto scores = [&](int st, float (&s)[2][4]) {
-      const uint8_t* kb = sm.ring[st] + grp_at;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      if constexpr (!Q8) {
-        const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
-        const uint32_t row = smem_u32(kb) + key * 128;
-        const uint32_t q_row = smem_u32(sm.q[lane & 15]) + (lane >> 4) * 16;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t r[4];
-          uint4 q;
-          ldsm4(row + (ks >> 2) * blk_bytes + ((((ks & 3) * 2 + half) ^ (key & 7)) << 4), r);
-          ldsm4(q_row + ks * 32, &q.x);
-          mma16816(s[0], q, r[0], r[1]);
-          mma16816(s[1], q, r[2], r[3]);
-        }
-      } else {
-        // column n of score tile j is key 4 (n >> 1) + 2 j + (n & 1): the order in which the
-        // transposed loads below hand out the values
-#pragma unroll
-        for (int cb = 0; cb < D / 64; ++cb) {
-          uint4 w[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int key = 4 * (n >> 1) + 2 * j + (n & 1);
-            const int chunk = (C::kBox == 128) ? (((cb & 1) * 4 + t) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
-            w[j] = *reinterpret_cast<const uint4*>(kb + (C::kBox == 128 ? (cb >> 1) * blk_bytes : 0) + key * C::kBox +
-                                                   chunk * 16);
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              const uint4 q = sm.q_parts[part * (D / 32) + cb * 2 + e][lane];
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma16832_e4m3(s[j], q, e ? w[j].z : w[j].x, e ? w[j].w : w[j].y);
-            }
-        }
-      }
-    };
-    // One iteration's scores are computed during the one before (8-bit caches: with half the bytes to
-    // wait for, the chain from a key's arrival to its product is what would set the pace; bf16
-    // caches are bound by the loads without it).
-    constexpr bool kAhead = Q8;
-    float ahead[2][4];
-    auto advance = [&]() {
-      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-    };
-    if (kAhead) {
-      wait_or_die(&sm.full[stage], phase, &sm.dead, c.status);
-      scores(stage, ahead);
-    }
     for (int i = sg.ta; i < sg.tb; ++i) {
       const int st = stage;
-      float s[2][4];
-      if constexpr (kAhead) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] = ahead[j][e];
-        advance();
-        if (i + 1 < sg.tb) {
-          wait_or_die(&sm.full[stage], phase, &sm.dead, c.status);
-          scores(stage, ahead);
-        }
-      } else {
-        wait_or_die(&sm.full[st], phase, &sm.dead, c.status);
-        scores(st, s);
-        advance();
-      }
-      const int k0 = i * TK + grp * 16;
+      wait_or_die(&sm.full[st], phase, &sm.dead, c.status);
+      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+      const int k0 = i * TK + warp * G * 16;
       if (k0 < keys) {
-        const uint32_t vb = smem_u32(sm.ring[st]) + grp_at + C::kHalfBytes;
-        uint32_t v_bytes = 0;                          // scale bytes of the values of keys 4 t .. 4 t + 3
-        if constexpr (Q8) {
-          const uint32_t k_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][0][grp * 16 + 4 * t]);
-          v_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][1][grp * 16 + 4 * t]);
+        const uint8_t* kb = sm.ring[st];
+        const uint32_t vb = smem_u32(kb) + C::kHalfBytes;
+        // ---- scores: 16 rows x 2 columns of 8 keys, for each group
+        float s[G][2][4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+        for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float f = scale_f32((k_bytes >> (8 * (2 * j + e))) & 0xffu);
-              s[j][e] *= f * scale0;
-              s[j][e + 2] *= f * scale1;
+          for (int j = 0; j < 2; ++j) s[u][j][0] = s[u][j][1] = s[u][j][2] = s[u][j][3] = 0.f;
+        if constexpr (!Q8) {
+          const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+          const uint32_t q_row = smem_u32(sm.q[lane & 15]) + (lane >> 4) * 16;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint4 q;
+            ldsm4(q_row + ks * 32, &q.x);
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+              uint32_t r[4];
+              ldsm4(smem_u32(kb) + at[u] + key * 128 + (ks >> 2) * blk_bytes +
+                        ((((ks & 3) * 2 + half) ^ (key & 7)) << 4), r);
+              mma16816(s[u][0], q, r[0], r[1]);
+              mma16816(s[u][1], q, r[2], r[3]);
             }
+          }
         } else {
+          // column n of score tile j is key 4 (n >> 1) + 2 j + (n & 1): the order in which the
+          // transposed loads below hand out the values
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb) {
+            uint4 w[G][2];
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int key = 4 * (n >> 1) + 2 * j + (n & 1);
+                const int chunk = (C::kBox == 128) ? (((cb & 1) * 4 + t) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
+                w[u][j] = *reinterpret_cast<const uint4*>(kb + at[u] + (C::kBox == 128 ? (cb >> 1) * blk_bytes : 0) +
+                                                          key * C::kBox + chunk * 16);
+              }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                const uint4 q = sm.q_parts[part * (D / 32) + cb * 2 + e][lane];
+#pragma unroll
+                for (int u = 0; u < G; ++u)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+                    mma16832_e4m3(s[u][j], q, e ? w[u][j].z : w[u][j].x, e ? w[u][j].w : w[u][j].y);
+              }
+          }
+        }
+        uint32_t v_bytes[G];                           // scale bytes of the values of keys 4 t .. 4 t + 3
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+          uint32_t k_bytes = 0;
+          v_bytes[u] = 0;
+          if constexpr (Q8) {
+            k_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][0][(warp * G + u) * 16 + 4 * t]);
+            v_bytes[u] = *reinterpret_cast<const uint32_t*>(&sm.scales[st][1][(warp * G + u) * 16 + 4 * t]);
+          }
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              s[j][e] *= scale0;
-              s[j][e + 2] *= scale1;
+              const float f = Q8 ? scale_f32((k_bytes >> (8 * (2 * j + e))) & 0xffu) : 1.f;
+              s[u][j][e] *= f * scale0;
+              s[u][j][e + 2] *= f * scale1;
             }
         }
-        const bool partial = k0 + 15 > pos_min;       // some row does not see all 16 keys
+        // the key of a lane's score (u, j, e)
+        auto key_of = [&](int u, int j, int e) { return k0 + 16 * u + (Q8 ? 4 * t + 2 * j + e : j * 8 + 2 * t + e); };
+        const bool partial = k0 + 16 * G - 1 > pos_min;       // some row does not see all keys
         if (partial) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = k0 + (Q8 ? 4 * t + 2 * j + e : j * 8 + 2 * t + e);
-              if (key > pos0) s[j][e] = -INFINITY;
-              if (key > pos1) s[j][e + 2] = -INFINITY;
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (key_of(u, j, e) > pos0) s[u][j][e] = -INFINITY;
+                if (key_of(u, j, e) > pos1) s[u][j][e + 2] = -INFINITY;
+              }
         }
         // ---- softmax of this warp's keys
-        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+          x0 = fmaxf(x0, fmaxf(fmaxf(s[u][0][0], s[u][0][1]), fmaxf(s[u][1][0], s[u][1][1])));
+          x1 = fmaxf(x1, fmaxf(fmaxf(s[u][0][2], s[u][0][3]), fmaxf(s[u][1][2], s[u][1][3])));
+        }
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-        // 2^8 above the reference is harmless in f32 and in the bf16 probabilities alike
+        // 2^8 above the reference is harmless in f32 and in the 16-bit probabilities alike
         if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
           const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
           const float f0 = m0 == n0 ? 1.f : ex2(m0 - n0), f1 = m1 == n1 ? 1.f : ex2(m1 - n1);
@@ -470,20 +462,24 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         }
         const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int u = 0; u < G; ++u)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[j][e] = ex2(s[j][e] - r0);
-            s[j][e + 2] = ex2(s[j][e + 2] - r1);
-            l0 += s[j][e];
-            l1 += s[j][e + 2];
-          }
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              s[u][j][e] = ex2(s[u][j][e] - r0);
+              s[u][j][e + 2] = ex2(s[u][j][e + 2] - r1);
+              l0 += s[u][j][e];
+              l1 += s[u][j][e + 2];
+            }
         // ---- values
         if constexpr (!Q8) {
-          const uint4 p = make_uint4(pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
-                                     pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3]));
+          static_assert(Q8 || G == 1, "the bf16 values are written for one group");
+          const float(&p4)[2][4] = s[0];
+          const uint4 p = make_uint4(pack_bf16(p4[0][0], p4[0][1]), pack_bf16(p4[0][2], p4[0][3]),
+                                     pack_bf16(p4[1][0], p4[1][1]), pack_bf16(p4[1][2], p4[1][3]));
           const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
-          const uint32_t row = vb + key * 128;
+          const uint32_t row = vb + at[0] + key * 128;
           // keys past the sequence's end: their rows may hold anything, and 0 x NaN is NaN
           const bool tail = k0 + 16 > keys;
           uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
@@ -519,13 +515,13 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll 1
             for (int j = 0; j < 16 && k0 + j < keys; ++j) {
               const int src = (lane & ~3) | ((j & 7) >> 1);
-              const float u0 = j & 8 ? (j & 1 ? s[1][1] : s[1][0]) : (j & 1 ? s[0][1] : s[0][0]);
-              const float u1 = j & 8 ? (j & 1 ? s[1][3] : s[1][2]) : (j & 1 ? s[0][3] : s[0][2]);
+              const float u0 = j & 8 ? (j & 1 ? p4[1][1] : p4[1][0]) : (j & 1 ? p4[0][1] : p4[0][0]);
+              const float u1 = j & 8 ? (j & 1 ? p4[1][3] : p4[1][2]) : (j & 1 ? p4[0][3] : p4[0][2]);
               const float p0 = __shfl_sync(0xffffffffu, u0, src), p1 = __shfl_sync(0xffffffffu, u1, src);
               const bool see0 = k0 + j <= pos0, see1 = k0 + j <= pos1;
 #pragma unroll
               for (int d = 0; d < D / 8; ++d) {
-                const uint32_t w = lds32(vb + j * 128 + (d >> 3) * blk_bytes + (((d & 7) ^ (j & 7)) << 4) + t * 4);
+                const uint32_t w = lds32(vb + at[0] + j * 128 + (d >> 3) * blk_bytes + (((d & 7) ^ (j & 7)) << 4) + t * 4);
                 const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
                 if (see0) { o[d][0] = fmaf(p0, v0, o[d][0]); o[d][1] = fmaf(p0, v1, o[d][1]); }
                 if (see1) { o[d][2] = fmaf(p1, v0, o[d][2]); o[d][3] = fmaf(p1, v1, o[d][3]); }
@@ -535,16 +531,19 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         } else {
           // The probabilities take the values' scales 2^(b - 127) as 2^(b - v_ref + 7), v_ref the
           // largest b so far: f16 has eleven bits for them from 2^15 down to 2^-14, which is room
-          // for scales 2^18 apart.  Where they are further apart, bf16 operands instead.
+          // for scales 2^18 apart.  Where they are further apart, and past the sequence's end (codes
+          // there may be NaN's, which the bit conversion makes 480), bf16 operands instead.
           uint32_t most = 0, least = 255;
 #pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) {
-            const uint32_t bb = (v_bytes >> (8 * i2)) & 0xffu;
-            if (k0 + 4 * t + i2 < keys && bb != 255) {
-              most = max(most, bb);
-              least = min(least, bb);
+          for (int u = 0; u < G; ++u)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t bb = (v_bytes[u] >> (8 * y)) & 0xffu;
+              if (k0 + 16 * u + 4 * t + y < keys && bb != 255) {
+                most = max(most, bb);
+                least = min(least, bb);
+              }
             }
-          }
           most = __reduce_max_sync(0xffffffffu, most);
           least = __reduce_min_sync(0xffffffffu, least);
           if ((int)most > v_ref) {
@@ -552,58 +551,74 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             const float f = d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23);
             v_ref = (int)most;
 #pragma unroll
-            for (int i2 = 0; i2 < D / 8; ++i2) {
-              o[i2][0] *= f; o[i2][1] *= f; o[i2][2] *= f; o[i2][3] *= f;
+            for (int y = 0; y < D / 8; ++y) {
+              o[y][0] *= f; o[y][1] *= f; o[y][2] *= f; o[y][3] *= f;
             }
           }
-          const bool wide = v_ref - (int)least > 18;
+          const bool wide = v_ref - (int)least > 18 || k0 + 16 * G > keys;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = k0 + 4 * t + 2 * j + e;
-              const int bb = (int)((v_bytes >> (8 * (2 * j + e))) & 0xffu);
-              const float f = bb == 255 ? __int_as_float(0x7fffffff)
-                                        : __uint_as_float((uint32_t)max(bb - v_ref + 134, 0) << 23);
-              // a hidden key stays at zero even if its vector reads as NaN
-              s[j][e] = key > pos0 ? 0.f : s[j][e] * f;
-              s[j][e + 2] = key > pos1 ? 0.f : s[j][e + 2] * f;
-            }
-          const int key = lane & 15;
-          const uint32_t row = vb + key * C::kBox;
-          if (!wide) {
-            const uint4 p = make_uint4(pack_f16(s[0][0], s[0][1]), pack_f16(s[0][2], s[0][3]),
-                                       pack_f16(s[1][0], s[1][1]), pack_f16(s[1][2], s[1][3]));
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int d0 = 0; d0 < D / 32; d0 += 2) {
-              uint32_t r[2][4];
-#pragma unroll
-              for (int d = 0; d < 2; ++d) {
-                const int chunk = 2 * (d0 + d) + (lane >> 4);
-                ldsm2t_b8(C::kBox == 128 ? row + ((d0 + d) >> 2) * blk_bytes + (((chunk & 7) ^ (key & 7)) << 4)
-                                         : row + ((chunk ^ ((key >> 1) & 3)) << 4), r[d]);
+              for (int e = 0; e < 2; ++e) {
+                const int bb = (int)((v_bytes[u] >> (8 * (2 * j + e))) & 0xffu);
+                const float f = bb == 255 ? __int_as_float(0x7fffffff)
+                                          : __uint_as_float((uint32_t)max(bb - v_ref + 134, 0) << 23);
+                s[u][j][e] *= f;
+                s[u][j][e + 2] *= f;
               }
+          if (partial) {       // a hidden key stays at zero even if its vector reads as NaN
 #pragma unroll
-              for (int d = 0; d < 2; ++d)
+            for (int u = 0; u < G; ++u)
 #pragma unroll
-                for (int i2 = 0; i2 < 4; ++i2)
-                  mma16816_f16(o[4 * (d0 + d) + i2], p, e4m3_to_f16x2((uint16_t)r[d][i2]),
-                               e4m3_to_f16x2((uint16_t)(r[d][i2] >> 16)));
-            }
-          } else {
-            const uint4 p = make_uint4(pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
-                                       pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3]));
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  if (key_of(u, j, e) > pos0) s[u][j][e] = 0.f;
+                  if (key_of(u, j, e) > pos1) s[u][j][e + 2] = 0.f;
+                }
+          }
+          const int key = lane & 15;
+          auto value_at = [&](int u, int d) {           // 16 keys x 32 columns from column 32 d on
+            const int chunk = 2 * d + (lane >> 4);
+            return vb + at[u] + key * C::kBox +
+                   (C::kBox == 128 ? (d >> 2) * blk_bytes + (((chunk & 7) ^ (key & 7)) << 4)
+                                   : (chunk ^ ((key >> 1) & 3)) << 4);
+          };
+          if (!wide) {
+            uint4 p[G];
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+              p[u] = make_uint4(pack_f16(s[u][0][0], s[u][0][1]), pack_f16(s[u][0][2], s[u][0][3]),
+                                pack_f16(s[u][1][0], s[u][1][1]), pack_f16(s[u][1][2], s[u][1][3]));
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) {
-              const int chunk = 2 * d + (lane >> 4);
-              uint32_t r[4];
-              ldsm2t_b8(C::kBox == 128 ? row + (d >> 2) * blk_bytes + (((chunk & 7) ^ (key & 7)) << 4)
-                                       : row + ((chunk ^ ((key >> 1) & 3)) << 4), r);
+              uint32_t r[G][4];
 #pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2) {
-                uint32_t b0, b1;
-                e4m3x4_to_bf16(r[i2], b0, b1);
-                mma16816(o[4 * d + i2], p, b0, b1);
+              for (int u = 0; u < G; ++u) ldsm2t_b8(value_at(u, d), r[u]);
+#pragma unroll
+              for (int u = 0; u < G; ++u)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  mma16816_f16(o[4 * d + y], p[u], e4m3_to_f16x2((uint16_t)r[u][y]),
+                               e4m3_to_f16x2((uint16_t)(r[u][y] >> 16)));
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+              const uint4 p = make_uint4(pack_bf16(s[u][0][0], s[u][0][1]), pack_bf16(s[u][0][2], s[u][0][3]),
+                                         pack_bf16(s[u][1][0], s[u][1][1]), pack_bf16(s[u][1][2], s[u][1][3]));
+#pragma unroll
+              for (int d = 0; d < D / 32; ++d) {
+                uint32_t r[4];
+                ldsm2t_b8(value_at(u, d), r);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  uint32_t b0, b1;
+                  e4m3x4_to_bf16(r[y], b0, b1);
+                  mma16816(o[4 * d + y], p, b0, b1);
+                }
               }
             }
           }
@@ -642,12 +657,12 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     }
     const bool whole = sg.whole();
     float* prow = Partials<R, D>::rows(a.ws, cta, sg.slot);
-    // A quarter of the columns at a time: every warp lays its part down, and each thread adds the
+    // Some of the columns at a time: every warp lays its part down, and each thread adds the
     // warps' values of the four columns it then writes.
     constexpr int kPieces = C::kChunk / 4, kStep = NC / kPieces;
     const int piece = tid % kPieces;
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
+    for (int ch = 0; ch < D / C::kChunk; ++ch) {
 #pragma unroll
       for (int d = 0; d < C::kChunk / 8; ++d) {
         const float* v = o[ch * (C::kChunk / 8) + d];
@@ -687,7 +702,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
           __stcg(reinterpret_cast<float4*>(prow + (size_t)r * D + d), v);
         }
       }
-      if (ch < 3) bar_sync(1, NC);
+      if (ch + 1 < D / C::kChunk) bar_sync(1, NC);
     }
     bar_sync(1, NC);
   }
@@ -696,14 +711,14 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 template <int D, bool Q8>
 int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
   using C = RowsCfg<D, Q8>;
-  constexpr size_t smem = sizeof(RowsSmem<D, Q8>) + 1024;
-  static_assert((smem + 1024) * C::kCtas <= 233472, "shared memory of an SM");
+  constexpr size_t smem = sizeof(RowsSmem<D, Q8>);
+  static_assert(smem <= 232448 && (smem + 1024) * C::kCtas <= 233472, "shared memory of an SM");
   static const cudaError_t set = cudaFuncSetAttribute(
       rows_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (set != cudaSuccess) return GDN_ERR_CUDA;
   KvMaps maps;
   const int P = 1 << c.page_shift;
-  if (!make_kv_maps(c, P < kTileKeys ? P : kTileKeys, &maps)) return GDN_ERR_CUDA;
+  if (!make_kv_maps(c, P < C::kKeys ? P : C::kKeys, &maps)) return GDN_ERR_CUDA;
   const int grid = rows_grid(D, sms), fix = 64 * a.g;
   const int least = 256 * a.g;
   int rc = launch_dependent(rows_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,

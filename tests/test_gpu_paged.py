@@ -253,3 +253,17 @@ def test_scales_far_apart(dim, apart):
         case.v[0][::7] *= 2.0 ** 20
         case.k[0][::7] = 0
         _check(case, 4)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_nan_codes_past_the_end(dim):
+    """What lies in a sequence's last page past its end may be anything, NaN codes among it."""
+    for new, length in ((1, 45), (1, 130), (50, 170)):
+        case = ref.Case([new], [length], 2, dim, 64, True, seed=14)
+        cache = case.empty_cache(runtime)
+        for p in (cache.k_pages, cache.v_pages):
+            p.view(torch.uint8).fill_(0x7f)
+        for s in (cache.k_scales, cache.v_scales):
+            s.fill_(200)
+        cache.append(case.whole_batch(runtime), torch.cat(case.k).cuda(), torch.cat(case.v).cuda())
+        _check(case, 8, cache=cache)
