@@ -7,20 +7,21 @@
 // stay within 2^8 of it, so the accumulator is rescaled when a maximum outgrows it by that much,
 // not at every step) and every sum is f32.
 //
-// What bounds it: the cache is read once, 2 D elements per key and head, for at most 16 rows, so
-// the floor is its bytes at the HBM rate.  Everything else must hide behind the loads:
-//  * a producer warp keeps a ring of 64-key stages full with TMA tensor copies (a box is 16 keys of
-//    one page, 128-byte swizzled), page numbers fetched one stage ahead;
-//  * each consumer warp takes 16 keys of a stage and runs its own softmax, so warps meet only at
-//    the end of a tile, where their accumulators are added in a fixed order;
-//  * the products are m16n8k16 MMAs on registers.  Sixteen rows fill that shape; the 128-row
-//    tcgen05 shape would run 7/8 empty here, needs the probabilities to cross TMEM, and could not
-//    be faster than the loads, which already set the pace;
+// What bounds it: the cache is read once, 2 D elements per key and head, for 8 or 16 rows, so the
+// floor is its bytes at the HBM rate.  Everything else must hide behind the loads:
+//  * two producer warps (keys, values) keep a ring of stages full with TMA tensor copies (a box is a
+//    page's part of a stage, 128-byte swizzled), page numbers fetched one stage ahead;
+//  * each consumer warp takes its own 16 or 32 keys of a stage and runs its own softmax, so warps
+//    meet only at the end of a tile, where their results are added in a fixed order;
+//  * the products are MMAs on registers, in the transposed form: S^T = K Q^T and O^T = V^T P^T have
+//    the keys (columns) as their 16 rows and 8 query rows as their columns, which fits the groups of
+//    4 and 8 that share a key/value head without empty rows (the other way round half the MMAs and
+//    half the accumulators were).  P^T becomes an operand by a transposing register move.  The
+//    128-row tcgen05 shape would run 15/16 empty, needs the probabilities to cross TMEM, and could
+//    not be faster than the loads;
 //  * 8-bit caches: the keys' codes are e4m3 MMA operands as they are (the queries as two e4m3
 //    parts, whose sum is exact), their scales applied to the scores; the values' codes become f16 by
-//    the conversion instruction, their scales applied to the probabilities.  Halving the bytes
-//    halves the time the arithmetic may take: converting both to bf16 by bit operations, 2.5 per
-//    element, held the kernel to 3.7 of the 6.7 TB/s.
+//    the conversion instruction, their scales applied to the probabilities.
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 
@@ -30,40 +31,42 @@ using namespace tc;
 
 namespace attn {
 
-constexpr int kRows = 16;
 
-template <int D, bool Q8>
+// NT: tiles of 8 query rows.
+template <int D, bool Q8, int NT>
 struct RowsCfg {
-  // D = 256: the accumulators take 128 registers of a thread, and a stage twice the bytes.
-  static constexpr int kConsumers = 4;
-  static constexpr int kCtas = D == 256 ? 1 : 2;
-  static constexpr int kThreads = (kConsumers + 2) * 32;         // and two producers: keys, values
+  static constexpr int kRows = 8 * NT;
   static constexpr int kElem = Q8 ? 1 : 2;
-  // Groups of 16 keys that a warp takes of a stage.  An MMA's result takes some 70 cycles; with half
-  // the bytes to wait for, an 8-bit cache wants the chains of two groups side by side.
-  static constexpr int kGroups = Q8 ? 2 : 1;
-  static constexpr int kKeys = 64 * kGroups;                     // of a stage
+  // D = 256: twice the accumulators and bytes, so one CTA of an SM, with more warps where they fit
+  static constexpr int kCtas = D == 256 ? 1 : 2;
+  static constexpr int kConsumers = D == 256 && Q8 && NT == 1 ? 8 : 4;
+  static constexpr int kThreads = (kConsumers + 2) * 32;
+  // Groups of 16 keys that a warp takes of a stage: with half the bytes to wait for, an 8-bit cache
+  // wants the chains of two side by side.
+  static constexpr int kGroups = Q8 && kConsumers == 4 ? 2 : 1;
+  static constexpr int kKeys = 16 * kGroups * kConsumers;        // of a stage
   static constexpr int kHalfBytes = kKeys * D * kElem;           // a stage's keys
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRing = kCtas == 1 ? 196608 : 98304;
   static constexpr int kStages = kRing / kStageBytes;
+  static constexpr bool kQRegs = NT * D <= 128;                  // query operands stay in registers
   static constexpr int kBox = D * kElem >= 128 ? 128 : 64;       // swizzle span, bytes
   static constexpr int kQLd = 2 * D + 16;                        // bytes of a staged query row
   static constexpr int kChunk = D / (Q8 && D > 64 ? 8 : 4);      // columns merged at a time
   static constexpr int kMLd = kChunk + 4;
 };
 
-template <int D, bool Q8>
+template <int D, bool Q8, int NT>
 struct __align__(1024) RowsSmem {
-  using C = RowsCfg<D, Q8>;
+  using C = RowsCfg<D, Q8, NT>;
   uint8_t ring[C::kStages][C::kStageBytes];
-  uint8_t scales[Q8 ? C::kStages : 1][2][C::kKeys];    // scale bytes of a stage's keys and values
-  uint8_t q[kRows][C::kQLd];              // the rows, as copied
-  uint4 q_parts[Q8 ? D / 16 : 1][32];     // 8-bit caches: A fragments of their two e4m3 parts
-  float q_scale[kRows];
-  float o[C::kConsumers][kRows][C::kMLd];
-  float ml[C::kConsumers][kRows][2];
-  LineScan<kRows, C::kThreads> scan;
+  uint8_t scales[Q8 ? C::kStages : 1][2][C::kKeys];     // scale bytes of a stage's keys and values
+  uint8_t q[C::kRows][C::kQLd];                         // the rows, as copied
+  uint2 q_part[Q8 ? D / 16 : 1][NT][32];                // 8-bit caches: operands of their two e4m3 parts
+  float q_scale[C::kRows];
+  float o[C::kConsumers][C::kRows][C::kMLd];
+  float ml[C::kConsumers][C::kRows][2];
+  LineScan<C::kRows, C::kThreads> scan;
   uint64_t full[C::kStages];
   uint64_t empty[C::kStages];
   uint64_t q_full, q_empty;
@@ -107,6 +110,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The 8 x 8 matrix of 16-bit elements that the warp holds (lane (g, t): row g, columns 2 t, 2 t + 1),
+// transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -119,10 +129,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(addr) : "memory");
+  return __uint_as_float((uint32_t)v << 16);
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -155,19 +165,19 @@ __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, vola
   }
 }
 
-template <int D, bool Q8>
-__global__ void __launch_bounds__(RowsCfg<D, Q8>::kThreads, RowsCfg<D, Q8>::kCtas)
+template <int D, bool Q8, int NT>
+__global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, RowsCfg<D, Q8, NT>::kCtas)
 rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, int least,
             const __grid_constant__ KvMaps maps) {
-  using C = RowsCfg<D, Q8>;
-  constexpr int R = kRows, TK = C::kKeys, NC = C::kConsumers * 32;
+  using C = RowsCfg<D, Q8, NT>;
+  constexpr int R = C::kRows, TK = C::kKeys, NC = C::kConsumers * 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  RowsSmem<D, Q8>& sm = *reinterpret_cast<RowsSmem<D, Q8>*>(smem_raw);
+  RowsSmem<D, Q8, NT>& sm = *reinterpret_cast<RowsSmem<D, Q8, NT>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sm.full[i], Q8 ? 2 + TK / 8 : 2);
-      mbar_init(&sm.empty[i], 4);
+      mbar_init(&sm.empty[i], C::kConsumers);
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, C::kConsumers);
@@ -262,7 +272,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   }
 
   // ------------------------------------------------------------------ consumers
-  const int t = lane & 3, n = lane >> 2;
+  const int t = lane & 3, g = lane >> 2;
   constexpr int G = C::kGroups;
   // a box of `box` keys is [column blocks][box][128 bytes]
   const int box = min(1 << c.page_shift, TK);
@@ -297,14 +307,12 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     wait_or_die(&sm.q_full, q_phase, &sm.dead, c.status);
     q_phase ^= 1u;
     if constexpr (Q8) {
-      // A warp splits four rows into their parts (see split_e4m3).  The k order inside a 64-column
-      // block follows the keys' loads: lane t of a quad reads 16 consecutive columns, eight to a
-      // k-step.
+      // A warp splits some rows into their parts (see split_e4m3), a lane some columns of them.
       constexpr int kEl = D == 256 ? 8 : 4;              // columns of a lane (D = 64: half the lanes)
       const int d0 = lane * kEl;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = warp * 4 + j;
+      for (int j = 0; j < R / C::kConsumers; ++j) {
+        const int r = warp * (R / C::kConsumers) + j;
         uint32_t w[kEl / 2], top = 0;
 #pragma unroll
         for (int e = 0; e < kEl / 4; ++e) {
@@ -325,28 +333,57 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
           for (int k = 0; k < 2; ++k)
             split_e4m3(__uint_as_float(w[2 * e + k] << 16) * inv, __uint_as_float(w[2 * e + k] & 0xffff0000u) * inv,
                        hi[k], lo[k]);
-          const int d = d0 + 4 * e;
-          if (d < D) {
-            const int ks = (d >> 6) * 2 + ((d >> 3) & 1), ln = (r & 7) * 4 + ((d >> 4) & 3);
-            const int reg = (r >> 3) + 2 * ((d >> 2) & 1);
-            reinterpret_cast<uint32_t*>(&sm.q_parts[ks][ln])[reg] = hi[0] | (hi[1] << 16);
-            reinterpret_cast<uint32_t*>(&sm.q_parts[D / 32 + ks][ln])[reg] = lo[0] | (lo[1] << 16);
+          if (d0 < D) {
+            const int d = d0 + 4 * e, ks = d / 64 * 2 + ((d >> 3) & 1), ln = (r & 7) * 4 + ((d >> 4) & 3);
+            uint32_t* at0 = &sm.q_part[ks][r >> 3][ln].x + ((d >> 2) & 1);
+            at0[0] = hi[0] | (hi[1] << 16);
+            at0[D / 32 * NT * 64] = lo[0] | (lo[1] << 16);
           }
         }
       }
       bar_sync(1, NC);
       if (lane == 0) mbar_arrive(&sm.q_empty);
     }
-    // last position each of this thread's two rows sees
-    const int pos0 = before + (row_base + n) / a.g, pos1 = before + (row_base + n + 8) / a.g;
+    // Query operands of k-step ks and row tile nt: column g is the row, and the columns of the
+    // k-step are 16 ks + 2 t, + 1, + 8, + 9; for 8-bit keys (k-step (part, ks)) the eight from
+    // 64 (ks / 2) + 16 t + 8 (ks % 2) on, so that a lane's columns of a key are sixteen together.
+    constexpr int kSteps = D / 16;                       // of a score: D / 32 for each part, or D / 16
+    auto query = [&](int ks, int nt) {
+      if constexpr (!Q8) {
+        const uint8_t* q = sm.q[8 * nt + g] + 2 * (16 * ks + 2 * t);
+        return make_uint2(*reinterpret_cast<const uint32_t*>(q), *reinterpret_cast<const uint32_t*>(q + 16));
+      } else {
+        return sm.q_part[ks][nt][lane];
+      }
+    };
+    uint2 qr[C::kQRegs ? kSteps : 1][NT];
+    if constexpr (C::kQRegs) {
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) qr[ks][nt] = query(ks, nt);
+    }
+    // this thread's rows: 8 nt + 2 t + e; the last position each sees
     const int pos_min = before + row_base / a.g;
-    const float scale0 = Q8 ? sm.q_scale[n] : a.scale_log2, scale1 = Q8 ? sm.q_scale[n + 8] : a.scale_log2;
+    int pos[NT][2];
+    float scale[NT][2], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nt + 2 * t + e;
+        pos[nt][e] = before + (row_base + r) / a.g;
+        scale[nt][e] = Q8 ? sm.q_scale[r] : a.scale_log2;
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
     // 8-bit values: the accumulators count in 2^(v_ref - 134), v_ref the largest scale byte so far
     int v_ref = 0;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float o[D / 8][4];
+    float o[D / 16][NT][4];       // (columns 16 i + g and + 8) x (rows 2 t, 2 t + 1)
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
 
     for (int i = sg.ta; i < sg.tb; ++i) {
       const int st = stage;
@@ -356,137 +393,155 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       if (k0 < keys) {
         const uint8_t* kb = sm.ring[st];
         const uint32_t vb = smem_u32(kb) + C::kHalfBytes;
-        // ---- scores: 16 rows x 2 columns of 8 keys, for each group
-        float s[G][2][4];
+        // The key, of a group's 16, of MMA row g + 8 f.  8-bit caches: the order that gives the
+        // transposed value loads (whose lane t holds four neighbouring rows) and the keys' 16-byte
+        // loads alike eight different bank groups.
+        auto key_in = [&](int f) { return Q8 ? (g & 1) << 2 | f << 1 | ((g >> 1) & 1) | (g >> 2) << 3 : g + 8 * f; };
+        // ---- scores: element (f, e) is key f of row e
+        float s[G][NT][4];
 #pragma unroll
         for (int u = 0; u < G; ++u)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) s[u][j][0] = s[u][j][1] = s[u][j][2] = s[u][j][3] = 0.f;
+          for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
         if constexpr (!Q8) {
-          const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
-          const uint32_t q_row = smem_u32(sm.q[lane & 15]) + (lane >> 4) * 16;
+          const int key = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            uint4 q;
-            ldsm4(q_row + ks * 32, &q.x);
+          for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
             for (int u = 0; u < G; ++u) {
               uint32_t r[4];
               ldsm4(smem_u32(kb) + at[u] + key * 128 + (ks >> 2) * blk_bytes +
                         ((((ks & 3) * 2 + half) ^ (key & 7)) << 4), r);
-              mma16816(s[u][0], q, r[0], r[1]);
-              mma16816(s[u][1], q, r[2], r[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint2 q = C::kQRegs ? qr[C::kQRegs ? ks : 0][nt] : query(ks, nt);
+                mma16816(s[u][nt], make_uint4(r[0], r[1], r[2], r[3]), q.x, q.y);
+              }
             }
-          }
         } else {
-          // column n of score tile j is key 4 (n >> 1) + 2 j + (n & 1): the order in which the
-          // transposed loads below hand out the values
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb) {
             uint4 w[G][2];
 #pragma unroll
             for (int u = 0; u < G; ++u)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int key = 4 * (n >> 1) + 2 * j + (n & 1);
+              for (int f = 0; f < 2; ++f) {
+                const int key = key_in(f);
                 const int chunk = (C::kBox == 128) ? (((cb & 1) * 4 + t) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
-                w[u][j] = *reinterpret_cast<const uint4*>(kb + at[u] + (C::kBox == 128 ? (cb >> 1) * blk_bytes : 0) +
+                w[u][f] = *reinterpret_cast<const uint4*>(kb + at[u] + (C::kBox == 128 ? (cb >> 1) * blk_bytes : 0) +
                                                           key * C::kBox + chunk * 16);
               }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                const uint4 q = sm.q_parts[part * (D / 32) + cb * 2 + e][lane];
+              for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int u = 0; u < G; ++u)
+                for (int nt = 0; nt < NT; ++nt) {
+                  constexpr int kPart = D / 32;
+                  const int ks = part * kPart + cb * 2 + e;
+                  const uint2 q = C::kQRegs ? qr[C::kQRegs ? ks : 0][nt] : query(ks, nt);
 #pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    mma16832_e4m3(s[u][j], q, e ? w[u][j].z : w[u][j].x, e ? w[u][j].w : w[u][j].y);
-              }
+                  for (int u = 0; u < G; ++u)
+                    mma16832_e4m3(s[u][nt], e ? make_uint4(w[u][0].z, w[u][1].z, w[u][0].w, w[u][1].w)
+                                              : make_uint4(w[u][0].x, w[u][1].x, w[u][0].y, w[u][1].y), q.x, q.y);
+                }
           }
         }
-        uint32_t v_bytes[G];                           // scale bytes of the values of keys 4 t .. 4 t + 3
+        uint32_t v_byte[G][2];
 #pragma unroll
-        for (int u = 0; u < G; ++u) {
-          uint32_t k_bytes = 0;
-          v_bytes[u] = 0;
-          if constexpr (Q8) {
-            k_bytes = *reinterpret_cast<const uint32_t*>(&sm.scales[st][0][(warp * G + u) * 16 + 4 * t]);
-            v_bytes[u] = *reinterpret_cast<const uint32_t*>(&sm.scales[st][1][(warp * G + u) * 16 + 4 * t]);
-          }
+        for (int u = 0; u < G; ++u)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float f = Q8 ? scale_f32((k_bytes >> (8 * (2 * j + e))) & 0xffu) : 1.f;
-              s[u][j][e] *= f * scale0;
-              s[u][j][e + 2] *= f * scale1;
+          for (int f = 0; f < 2; ++f) {
+            float ks = 1.f;
+            v_byte[u][f] = 0;
+            if constexpr (Q8) {
+              ks = scale_f32(sm.scales[st][0][(warp * G + u) * 16 + key_in(f)]);
+              v_byte[u][f] = sm.scales[st][1][(warp * G + u) * 16 + key_in(f)];
             }
-        }
-        // the key of a lane's score (u, j, e)
-        auto key_of = [&](int u, int j, int e) { return k0 + 16 * u + (Q8 ? 4 * t + 2 * j + e : j * 8 + 2 * t + e); };
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              s[u][nt][2 * f] *= ks * scale[nt][0];
+              s[u][nt][2 * f + 1] *= ks * scale[nt][1];
+            }
+          }
         const bool partial = k0 + 16 * G - 1 > pos_min;       // some row does not see all keys
         if (partial) {
 #pragma unroll
           for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int f = 0; f < 2; ++f)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (key_of(u, j, e) > pos0) s[u][j][e] = -INFINITY;
-                if (key_of(u, j, e) > pos1) s[u][j][e + 2] = -INFINITY;
-              }
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (k0 + 16 * u + key_in(f) > pos[nt][e]) s[u][nt][2 * f + e] = -INFINITY;
         }
         // ---- softmax of this warp's keys
-        float x0 = -INFINITY, x1 = -INFINITY;
+        float x[NT][2];
+        bool above = false;
 #pragma unroll
-        for (int u = 0; u < G; ++u) {
-          x0 = fmaxf(x0, fmaxf(fmaxf(s[u][0][0], s[u][0][1]), fmaxf(s[u][1][0], s[u][1][1])));
-          x1 = fmaxf(x1, fmaxf(fmaxf(s[u][0][2], s[u][0][3]), fmaxf(s[u][1][2], s[u][1][3])));
-        }
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-        // 2^8 above the reference is harmless in f32 and in the 16-bit probabilities alike
-        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
-          const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-          const float f0 = m0 == n0 ? 1.f : ex2(m0 - n0), f1 = m1 == n1 ? 1.f : ex2(m1 - n1);
-          m0 = n0; m1 = n1;
-          l0 *= f0; l1 *= f1;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            o[d][0] *= f0; o[d][1] *= f0; o[d][2] *= f1; o[d][3] *= f1;
+          for (int e = 0; e < 2; ++e) {
+            float v = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < G; ++u) v = fmaxf(v, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+            x[nt][e] = v;
+            above |= v > m[nt][e] + 8.f;
           }
-        }
-        const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+        // 2^8 above the reference is harmless in f32 and in the 16-bit probabilities alike
+        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int u = 0; u < G; ++u)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              s[u][j][e] = ex2(s[u][j][e] - r0);
-              s[u][j][e + 2] = ex2(s[u][j][e + 2] - r1);
-              l0 += s[u][j][e];
-              l1 += s[u][j][e + 2];
+              const float to = fmaxf(m[nt][e], x[nt][e]);
+              const float f = m[nt][e] == to ? 1.f : ex2(m[nt][e] - to);
+              m[nt][e] = to;
+              l[nt][e] *= f;
+#pragma unroll
+              for (int d = 0; d < D / 16; ++d) {
+                o[d][nt][e] *= f;
+                o[d][nt][2 + e] *= f;
+              }
             }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                const float p = ex2(s[u][nt][2 * f + e] - ref);
+                s[u][nt][2 * f + e] = p;
+                l[nt][e] += p;
+              }
+          }
         // ---- values
         if constexpr (!Q8) {
           static_assert(Q8 || G == 1, "the bf16 values are written for one group");
-          const float(&p4)[2][4] = s[0];
-          const uint4 p = make_uint4(pack_bf16(p4[0][0], p4[0][1]), pack_bf16(p4[0][2], p4[0][3]),
-                                     pack_bf16(p4[1][0], p4[1][1]), pack_bf16(p4[1][2], p4[1][3]));
-          const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+          uint2 p[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            p[nt] = make_uint2(transpose8x8(pack_bf16(s[0][nt][0], s[0][nt][1])),
+                               transpose8x8(pack_bf16(s[0][nt][2], s[0][nt][3])));
+          const int key = (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;
           const uint32_t row = vb + at[0] + key * 128;
+          auto load_v = [&](int d, uint32_t* r) {         // columns 16 d + g, + 8; keys 2 t, + 1, + 8, + 9
+            ldsm4t(row + (d >> 2) * blk_bytes + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
+          };
           // keys past the sequence's end: their rows may hold anything, and 0 x NaN is NaN
           const bool tail = k0 + 16 > keys;
           uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
           if (tail) {
-            const int u = k0 + 2 * t;
-            z0 = (u < keys ? 0xffffu : 0u) | (u + 1 < keys ? 0xffff0000u : 0u);
-            z1 = (u + 8 < keys ? 0xffffu : 0u) | (u + 9 < keys ? 0xffff0000u : 0u);
+            const int y = k0 + 2 * t;
+            z0 = (y < keys ? 0xffffu : 0u) | (y + 1 < keys ? 0xffff0000u : 0u);
+            z1 = (y + 8 < keys ? 0xffffu : 0u) | (y + 9 < keys ? 0xffff0000u : 0u);
           }
           bool finite = true;
           if (partial && info.tokens > 1) {
@@ -496,9 +551,9 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll 4
             for (int d = 0; d < D / 16; ++d) {
               uint32_t r[4];
-              ldsm4t(row + (d >> 2) * blk_bytes + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
-              seen |= ((r[0] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[1] & z1 & 0x7f807f80u) + 0x00800080u) |
-                      ((r[2] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[3] & z1 & 0x7f807f80u) + 0x00800080u);
+              load_v(d, r);
+              seen |= ((r[0] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[1] & z0 & 0x7f807f80u) + 0x00800080u) |
+                      ((r[2] & z1 & 0x7f807f80u) + 0x00800080u) | ((r[3] & z1 & 0x7f807f80u) + 0x00800080u);
             }
             finite = !__any_sync(0xffffffffu, (seen & 0x80008000u) != 0);
           }
@@ -506,25 +561,35 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
               uint32_t r[4];
-              ldsm4t(row + (d >> 2) * blk_bytes + ((((d & 3) * 2 + half) ^ (key & 7)) << 4), r);
-              if (tail) { r[0] &= z0; r[1] &= z1; r[2] &= z0; r[3] &= z1; }
-              mma16816(o[2 * d], p, r[0], r[1]);
-              mma16816(o[2 * d + 1], p, r[2], r[3]);
+              load_v(d, r);
+              if (tail) { r[0] &= z0; r[1] &= z0; r[2] &= z1; r[3] &= z1; }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(o[d][nt], make_uint4(r[0], r[1], r[2], r[3]), p[nt].x, p[nt].y);
             }
           } else {
 #pragma unroll 1
             for (int j = 0; j < 16 && k0 + j < keys; ++j) {
-              const int src = (lane & ~3) | ((j & 7) >> 1);
-              const float u0 = j & 8 ? (j & 1 ? p4[1][1] : p4[1][0]) : (j & 1 ? p4[0][1] : p4[0][0]);
-              const float u1 = j & 8 ? (j & 1 ? p4[1][3] : p4[1][2]) : (j & 1 ? p4[0][3] : p4[0][2]);
-              const float p0 = __shfl_sync(0xffffffffu, u0, src), p1 = __shfl_sync(0xffffffffu, u1, src);
-              const bool see0 = k0 + j <= pos0, see1 = k0 + j <= pos1;
+              const int src = (j & 7) * 4 + t;
+              float pj[NT][2];
 #pragma unroll
-              for (int d = 0; d < D / 8; ++d) {
-                const uint32_t w = lds32(vb + at[0] + j * 128 + (d >> 3) * blk_bytes + (((d & 7) ^ (j & 7)) << 4) + t * 4);
-                const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
-                if (see0) { o[d][0] = fmaf(p0, v0, o[d][0]); o[d][1] = fmaf(p0, v1, o[d][1]); }
-                if (see1) { o[d][2] = fmaf(p1, v0, o[d][2]); o[d][3] = fmaf(p1, v1, o[d][3]); }
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  pj[nt][e] = __shfl_sync(0xffffffffu, j & 8 ? s[0][nt][2 + e] : s[0][nt][e], src);
+#pragma unroll
+              for (int d = 0; d < D / 16; ++d) {
+                const uint32_t v = vb + at[0] + j * 128 + (d >> 2) * blk_bytes + g * 2;
+                const float v0 = lds_bf16(v + ((((d & 3) * 2) ^ (j & 7)) << 4));
+                const float v1 = lds_bf16(v + ((((d & 3) * 2 + 1) ^ (j & 7)) << 4));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (k0 + j <= pos[nt][e]) {
+                      o[d][nt][e] = fmaf(pj[nt][e], v0, o[d][nt][e]);
+                      o[d][nt][2 + e] = fmaf(pj[nt][e], v1, o[d][nt][2 + e]);
+                    }
               }
             }
           }
@@ -537,13 +602,11 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
           for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t bb = (v_bytes[u] >> (8 * y)) & 0xffu;
-              if (k0 + 16 * u + 4 * t + y < keys && bb != 255) {
-                most = max(most, bb);
-                least = min(least, bb);
+            for (int f = 0; f < 2; ++f)
+              if (k0 + 16 * u + key_in(f) < keys && v_byte[u][f] != 255) {
+                most = max(most, v_byte[u][f]);
+                least = min(least, v_byte[u][f]);
               }
-            }
           most = __reduce_max_sync(0xffffffffu, most);
           least = __reduce_min_sync(0xffffffffu, least);
           if ((int)most > v_ref) {
@@ -551,76 +614,81 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             const float f = d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23);
             v_ref = (int)most;
 #pragma unroll
-            for (int y = 0; y < D / 8; ++y) {
-              o[y][0] *= f; o[y][1] *= f; o[y][2] *= f; o[y][3] *= f;
-            }
+            for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                o[y][nt][0] *= f; o[y][nt][1] *= f; o[y][nt][2] *= f; o[y][nt][3] *= f;
+              }
           }
           const bool wide = v_ref - (int)least > 18 || k0 + 16 * G > keys;
 #pragma unroll
           for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int f = 0; f < 2; ++f) {
+              const int bb = (int)v_byte[u][f];
+              const float y = bb == 255 ? __int_as_float(0x7fffffff)
+                                        : __uint_as_float((uint32_t)max(bb - v_ref + 134, 0) << 23);
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int bb = (int)((v_bytes[u] >> (8 * (2 * j + e))) & 0xffu);
-                const float f = bb == 255 ? __int_as_float(0x7fffffff)
-                                          : __uint_as_float((uint32_t)max(bb - v_ref + 134, 0) << 23);
-                s[u][j][e] *= f;
-                s[u][j][e + 2] *= f;
-              }
-          if (partial) {       // a hidden key stays at zero even if its vector reads as NaN
-#pragma unroll
-            for (int u = 0; u < G; ++u)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  if (key_of(u, j, e) > pos0) s[u][j][e] = 0.f;
-                  if (key_of(u, j, e) > pos1) s[u][j][e + 2] = 0.f;
+                  s[u][nt][2 * f + e] *= y;
+                  // a hidden key stays at zero even if its vector reads as NaN
+                  if (partial && k0 + 16 * u + key_in(f) > pos[nt][e]) s[u][nt][2 * f + e] = 0.f;
                 }
-          }
-          const int key = lane & 15;
-          auto value_at = [&](int u, int d) {           // 16 keys x 32 columns from column 32 d on
+            }
+          // lane i & 15 points at the key of matrix row i: rows 4 t + 2 f + e are MMA rows 2 t + e + 8 f
+          const int key = (lane & 1) << 2 | (lane & 2) | ((lane >> 2) & 1) | (lane & 8);
+          auto load_v = [&](int u, int d, uint32_t* r) {  // columns 32 d + g, + 8, + 16, + 24
             const int chunk = 2 * d + (lane >> 4);
-            return vb + at[u] + key * C::kBox +
-                   (C::kBox == 128 ? (d >> 2) * blk_bytes + (((chunk & 7) ^ (key & 7)) << 4)
-                                   : (chunk ^ ((key >> 1) & 3)) << 4);
+            ldsm2t_b8(vb + at[u] + key * C::kBox +
+                          (C::kBox == 128 ? (d >> 2) * blk_bytes + (((chunk & 7) ^ (key & 7)) << 4)
+                                          : (chunk ^ ((key >> 1) & 3)) << 4), r);
           };
-          if (!wide) {
-            uint4 p[G];
+          uint2 p[G][NT];
 #pragma unroll
-            for (int u = 0; u < G; ++u)
-              p[u] = make_uint4(pack_f16(s[u][0][0], s[u][0][1]), pack_f16(s[u][0][2], s[u][0][3]),
-                                pack_f16(s[u][1][0], s[u][1][1]), pack_f16(s[u][1][2], s[u][1][3]));
+          for (int u = 0; u < G; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float* y = s[u][nt];
+              p[u][nt] = wide ? make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]))
+                              : make_uint2(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]));
+              p[u][nt].x = transpose8x8(p[u][nt].x);
+              p[u][nt].y = transpose8x8(p[u][nt].y);
+            }
+          if (!wide) {
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) {
               uint32_t r[G][4];
 #pragma unroll
-              for (int u = 0; u < G; ++u) ldsm2t_b8(value_at(u, d), r[u]);
+              for (int u = 0; u < G; ++u) load_v(u, d, r[u]);
 #pragma unroll
               for (int u = 0; u < G; ++u)
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  mma16816_f16(o[4 * d + y], p[u], e4m3_to_f16x2((uint16_t)r[u][y]),
-                               e4m3_to_f16x2((uint16_t)(r[u][y] >> 16)));
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t r0 = r[u][2 * h], r1 = r[u][2 * h + 1];
+                  const uint4 v = make_uint4(e4m3_to_f16x2((uint16_t)r0), e4m3_to_f16x2((uint16_t)r1),
+                                             e4m3_to_f16x2((uint16_t)(r0 >> 16)), e4m3_to_f16x2((uint16_t)(r1 >> 16)));
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * d + h][nt], v, p[u][nt].x, p[u][nt].y);
+                }
             }
           } else {
 #pragma unroll
-            for (int u = 0; u < G; ++u) {
-              const uint4 p = make_uint4(pack_bf16(s[u][0][0], s[u][0][1]), pack_bf16(s[u][0][2], s[u][0][3]),
-                                         pack_bf16(s[u][1][0], s[u][1][1]), pack_bf16(s[u][1][2], s[u][1][3]));
+            for (int u = 0; u < G; ++u)
 #pragma unroll
               for (int d = 0; d < D / 32; ++d) {
                 uint32_t r[4];
-                ldsm2t_b8(value_at(u, d), r);
+                load_v(u, d, r);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  uint32_t b0, b1;
-                  e4m3x4_to_bf16(r[y], b0, b1);
-                  mma16816(o[4 * d + y], p, b0, b1);
+                for (int h = 0; h < 2; ++h) {
+                  uint4 v;
+                  e4m3x4_to_bf16(r[2 * h], v.x, v.z);
+                  e4m3x4_to_bf16(r[2 * h + 1], v.y, v.w);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma16816(o[2 * d + h][nt], v, p[u][nt].x, p[u][nt].y);
                 }
               }
-            }
           }
         }
       }
@@ -631,30 +699,31 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     if (!Q8 && lane == 0) mbar_arrive(&sm.q_empty);
 
     // ---- the warps' results of this tile become one
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    // a NaN sum must survive the merge even when its reference never left -infinity
-    if (l0 != l0) m0 = INFINITY;
-    if (l1 != l1) m1 = INFINITY;
-    if (t == 0) {
-      sm.ml[warp][n][0] = m0; sm.ml[warp][n][1] = l0;
-      sm.ml[warp][n + 8][0] = m1; sm.ml[warp][n + 8][1] = l1;
-    }
-    bar_sync(1, NC);
-    float M0 = -INFINITY, M1 = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < C::kConsumers; ++w) {
-      M0 = fmaxf(M0, sm.ml[w][n][0]);
-      M1 = fmaxf(M1, sm.ml[w][n + 8][0]);
-    }
-    float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
-    if (Q8) {
-      const float unit = v_ref == 0 ? 0.f : __uint_as_float((uint32_t)(v_ref - 7) << 23);   // 2^(v_ref - 134)
-      f0 *= unit;
-      f1 *= unit;
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+        // a NaN sum must survive the merge even when its reference never left -infinity
+        if (l[nt][e] != l[nt][e]) m[nt][e] = INFINITY;
+        if (g == 0) {
+          sm.ml[warp][8 * nt + 2 * t + e][0] = m[nt][e];
+          sm.ml[warp][8 * nt + 2 * t + e][1] = l[nt][e];
+        }
+      }
+    bar_sync(1, NC);
+    float f[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::kConsumers; ++w) top = fmaxf(top, sm.ml[w][8 * nt + 2 * t + e][0]);
+        f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
+        if (Q8) f[nt][e] *= v_ref == 0 ? 0.f : __uint_as_float((uint32_t)(v_ref - 7) << 23);   // 2^(v_ref - 134)
+      }
     const bool whole = sg.whole();
     float* prow = Partials<R, D>::rows(a.ws, cta, sg.slot);
     // Some of the columns at a time: every warp lays its part down, and each thread adds the
@@ -664,11 +733,15 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
     for (int ch = 0; ch < D / C::kChunk; ++ch) {
 #pragma unroll
-      for (int d = 0; d < C::kChunk / 8; ++d) {
-        const float* v = o[ch * (C::kChunk / 8) + d];
-        *reinterpret_cast<float2*>(&sm.o[warp][n][d * 8 + 2 * t]) = make_float2(v[0] * f0, v[1] * f0);
-        *reinterpret_cast<float2*>(&sm.o[warp][n + 8][d * 8 + 2 * t]) = make_float2(v[2] * f1, v[3] * f1);
-      }
+      for (int d = 0; d < C::kChunk / 16; ++d)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float* v = o[ch * (C::kChunk / 16) + d][nt];
+            sm.o[warp][8 * nt + 2 * t + e][16 * d + g] = v[e] * f[nt][e];
+            sm.o[warp][8 * nt + 2 * t + e][16 * d + g + 8] = v[2 + e] * f[nt][e];
+          }
       bar_sync(1, NC);
       for (int r = tid / kPieces; r < rows; r += kStep) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -679,19 +752,19 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         }
         const int d = ch * C::kChunk + piece * 4;
         if (whole || (ch == 0 && piece == 0)) {
-          float M = -INFINITY, l = 0.f;
+          float M = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int w = 0; w < C::kConsumers; ++w) M = fmaxf(M, sm.ml[w][r][0]);
 #pragma unroll
           for (int w = 0; w < C::kConsumers; ++w) {
             const float mw = sm.ml[w][r][0];
-            if (mw != -INFINITY) l += sm.ml[w][r][1] * ex2(mw - M);
+            if (mw != -INFINITY) sum += sm.ml[w][r][1] * ex2(mw - M);
           }
           if (whole) {
-            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
             v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
           } else {
-            __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, sg.slot) + 2 * r), make_float2(M, l));
+            __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, sg.slot) + 2 * r), make_float2(M, sum));
           }
         }
         if (whole) {
@@ -708,38 +781,44 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   }
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int NT>
 int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
-  using C = RowsCfg<D, Q8>;
-  constexpr size_t smem = sizeof(RowsSmem<D, Q8>);
+  using C = RowsCfg<D, Q8, NT>;
+  constexpr size_t smem = sizeof(RowsSmem<D, Q8, NT>);
   static_assert(smem <= 232448 && (smem + 1024) * C::kCtas <= 233472, "shared memory of an SM");
   static const cudaError_t set = cudaFuncSetAttribute(
-      rows_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      rows_kernel<D, Q8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (set != cudaSuccess) return GDN_ERR_CUDA;
   KvMaps maps;
   const int P = 1 << c.page_shift;
   if (!make_kv_maps(c, P < C::kKeys ? P : C::kKeys, &maps)) return GDN_ERR_CUDA;
   const int grid = rows_grid(D, sms), fix = 64 * a.g;
   const int least = 256 * a.g;
-  int rc = launch_dependent(rows_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
+  int rc = launch_dependent(rows_kernel<D, Q8, NT>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
-  return launch_dependent(merge_kernel<kRows, D>, dim3((unsigned)(2 * sms)), kMergeWarps * 32, 0, stream, a, grid);
+  return launch_dependent(merge_kernel<C::kRows, D>, dim3((unsigned)(2 * sms)), kMergeWarps * 32, 0, stream, a, grid);
 }
 
 int rows_grid(int D, int sms) { return min(kMaxPieces, D == 256 ? sms : 2 * sms); }
 
 size_t rows_ws_bytes(int D, int sms) {
   const int grid = rows_grid(D, sms);
-  return D == 64 ? Partials<kRows, 64>::bytes(grid)
-       : D == 128 ? Partials<kRows, 128>::bytes(grid) : Partials<kRows, 256>::bytes(grid);
+  return D == 64 ? Partials<16, 64>::bytes(grid)
+       : D == 128 ? Partials<16, 128>::bytes(grid) : Partials<16, 256>::bytes(grid);
 }
 
-int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
-  const bool q8 = c.ks != nullptr;
-  if (c.D == 64) return q8 ? launch_rows<64, true>(c, b, a, sms, stream) : launch_rows<64, false>(c, b, a, sms, stream);
-  if (c.D == 128) return q8 ? launch_rows<128, true>(c, b, a, sms, stream) : launch_rows<128, false>(c, b, a, sms, stream);
-  return q8 ? launch_rows<256, true>(c, b, a, sms, stream) : launch_rows<256, false>(c, b, a, sms, stream);
+template <int D>
+int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int rows, int sms, cudaStream_t stream) {
+  if (rows <= 8)
+    return c.ks ? launch_rows<D, true, 1>(c, b, a, sms, stream) : launch_rows<D, false, 1>(c, b, a, sms, stream);
+  return c.ks ? launch_rows<D, true, 2>(c, b, a, sms, stream) : launch_rows<D, false, 2>(c, b, a, sms, stream);
+}
+
+int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int rows, int sms, cudaStream_t stream) {
+  return c.D == 64    ? launch_rows<64>(c, b, a, rows, sms, stream)
+         : c.D == 128 ? launch_rows<128>(c, b, a, rows, sms, stream)
+                      : launch_rows<256>(c, b, a, rows, sms, stream);
 }
 
 }  // namespace attn

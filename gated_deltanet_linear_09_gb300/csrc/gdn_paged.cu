@@ -104,7 +104,7 @@ int launch_attn(const KvView& c, const KvBatchView& b, const AttnArgs& a, cudaSt
   const int sms = sm_count();
   if (sms <= 0) return GDN_ERR_CUDA;
   const long long most = b.max_tokens > 0 ? b.max_tokens : b.total;
-  if (most * a.g <= 16) return attn::launch_rows(c, b, a, sms, stream);
+  if (most * a.g <= 16) return attn::launch_rows(c, b, a, (int)(most * a.g), sms, stream);
   return attn::launch_chunk(c, b, a, sms, stream);
 }
 

@@ -24,7 +24,8 @@ bool make_tile_maps(const KvView& c, int rows, int cols, KvMaps* maps);
 namespace attn {
 int rows_grid(int D, int sms);
 size_t rows_ws_bytes(int D, int sms);
-int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream);
+// `rows` (at most 16): the most query rows of a sequence under one key/value head.
+int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int rows, int sms, cudaStream_t stream);
 size_t chunk_ws_bytes(int D, int sms);
 int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream);
 }  // namespace attn

@@ -267,3 +267,39 @@ def test_nan_codes_past_the_end(dim):
             s.fill_(200)
         cache.append(case.whole_batch(runtime), torch.cat(case.k).cuda(), torch.cat(case.v).cuda())
         _check(case, 8, cache=cache)
+
+
+@pytest.mark.parametrize("dim,quantised,heads,group,new", [
+    (64, False, 8, 4, 1), (64, True, 8, 4, 1), (128, False, 4, 8, 1), (128, True, 4, 4, 1), (128, True, 4, 8, 2),
+    (256, False, 2, 8, 1), (256, True, 4, 8, 1), (256, True, 4, 4, 3), (128, False, 4, 8, 40), (128, True, 4, 8, 40),
+    (256, True, 2, 8, 40), (64, True, 4, 8, 40)])
+def test_long_batches(dim, quantised, heads, group, new):
+    """Enough cached positions that every CTA goes round its rings many times, several tiles each."""
+    n, length = 48, 5000
+    g = torch.Generator(device="cuda").manual_seed(15)
+    page = 32
+    per = -(-length // page)
+    lens = [length - 37 * i for i in range(n)]
+    k = torch.randn((n * length, heads, dim), generator=g, device="cuda").to(torch.bfloat16)
+    v = torch.randn((n * length, heads, dim), generator=g, device="cuda").to(torch.bfloat16)
+    cache = runtime.PagedKVCache(n * per, page, heads, dim, quantised)
+    table = torch.randperm(n * per, generator=g, device="cuda").to(torch.int32).view(n, per)
+    cu = torch.arange(0, n * length + 1, length, dtype=torch.int32, device="cuda")
+    full = torch.full((n,), length, dtype=torch.int32, device="cuda")
+    whole = runtime.KVBatch(cu, full, table, n * length, length)
+    cache.append(whole, k, v)
+    k, v = (x.view(n, length, heads, dim) for x in cache.read(whole))
+    q = (torch.randn((n * new, heads * group, dim), generator=g, device="cuda") * 1.5).to(torch.bfloat16)
+    batch = runtime.KVBatch(torch.arange(0, n * new + 1, new, dtype=torch.int32, device="cuda"),
+                            torch.tensor(lens, dtype=torch.int32, device="cuda"), table, n * new, new)
+    got = cache.attend(batch, q).view(n, new, heads, group, dim).double()
+    assert int(cache.status.item()) == 0
+    q = q.view(n, new, heads, group, dim)
+    for i in range(n):
+        t = lens[i]
+        s = torch.einsum("qhgd,jhd->hgqj", q[i].double(), k[i, :t].double()) / math.sqrt(dim)
+        hide = torch.arange(t, device="cuda")[None] > torch.arange(t - new, t, device="cuda")[:, None]
+        w = torch.softmax(s.masked_fill(hide, -math.inf), -1)
+        want = torch.einsum("hgqj,jhd->qhgd", w, v[i, :t].double())
+        spread = torch.einsum("hgqj,jhd->qhgd", w, v[i, :t].double().abs())
+        assert ((got[i] - want).abs() <= ref.attention_bound(want, spread)).all(), i
