@@ -293,6 +293,30 @@ __device__ __forceinline__ void locate_piece(const KvView& c, const KvBatchView&
   __syncthreads();
 }
 
+// ------------------------------------------------------------------ segments, published
+
+constexpr int kSegs = 4;           // segments known ahead
+
+// A segment as the roles of a CTA need it: one warp walks the piece and publishes them in a ring.
+struct SegDesc {
+  int seq, row0, tokens, len;      // the sequence
+  int head, tile, rows;            // key/value head, tile of rows and its rows
+  int keys;                        // keys that the tile's last row sees
+  int ta, n;                       // first key tile, number of them; n < 0: no more segments
+  int whole, owns_empty, slot;
+};
+
+template <int R>
+__device__ __forceinline__ SegDesc describe(const Segment& s, int g) {
+  return SegDesc{s.seq, s.info.row0, s.info.tokens, s.info.len, s.head, s.tile,
+                 min(R, s.info.tokens * g - s.tile * R), min(s.info.len, tile_keys<R>(s.info, g, s.tile)),
+                 s.ta, max(s.tb - s.ta, 0), s.whole(), s.owns_empty, s.slot};
+}
+
+// Nothing to do for a segment: no key tiles, no zeros to write, no split tile to leave an empty
+// share of.
+__device__ __forceinline__ bool idle(const Segment& s) { return s.tb <= s.ta && !s.owns_empty && s.nt == 0; }
+
 // ------------------------------------------------------------------ partial results
 
 // A split tile, noted by the piece it begins in: its pieces are first (slot 1) and the count - 1

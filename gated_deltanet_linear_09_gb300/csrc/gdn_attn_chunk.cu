@@ -34,16 +34,6 @@ using namespace tc;
 namespace attn {
 
 constexpr int kKeys = 128;         // keys of a tile
-constexpr int kSegs = 4;           // segments known ahead
-
-// A segment as the roles need it, published by the scheduling warp.
-struct SegDesc {
-  int seq, row0, tokens, len;      // the sequence
-  int head, tile;                  // key/value head, tile of rows
-  int ta, n;                       // first key tile, number of them; n < 0: no more segments
-  int whole, owns_empty, slot;
-};
-
 template <int D, bool Q8>
 struct ChunkCfg {
   static constexpr int kBlocks = D == 256 ? 1 : 2;          // 128-row query blocks
@@ -327,13 +317,12 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     s.split = false;
     for (bool more = true; more;) {
       more = it.next(&s);
-      const int n = s.tb - s.ta;
-      if (more && n <= 0 && !s.owns_empty && s.nt == 0) continue;
+      if (more && idle(s)) continue;
       wait_bar(&sm.seg_empty[seg.stage], seg.phase ^ 1u, &sm.dead, c.status);
       if (lane == 0) {
-        sm.segs[seg.stage] = more ? SegDesc{s.seq, s.info.row0, s.info.tokens, s.info.len, s.head, s.tile, s.ta,
-                                            max(n, 0), s.whole(), s.owns_empty, s.slot}
-                                  : SegDesc{0, 0, 0, 0, 0, 0, 0, -1, 0, 0, 0};
+        SegDesc d = {};
+        d.n = -1;
+        sm.segs[seg.stage] = more ? describe<R>(s, a.g) : d;
         mbar_arrive(&sm.seg_full[seg.stage]);
       }
       __syncwarp();
@@ -454,7 +443,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         wait_one(&sm.seg_full[seg.stage], seg.phase, &sm.dead, c.status);
         const SegDesc& sd = sm.segs[seg.stage];
         const int n = sd.n;
-        const bool two = (long long)sd.tokens * a.g - (long long)sd.tile * R > 128;
+        const bool two = sd.rows > 128;
         mbar_arrive(&sm.seg_empty[seg.stage]);
         seg.step();
         if (n < 0) break;
@@ -683,7 +672,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
                                : (p >> 3) * 16384 + (lbase + rr) * 128 + (((p & 7) ^ (rr & 7)) << 4)));
     };
     auto active = [&](const SegDesc& s) {
-      return s.n > 0 && (blk == 0 || (long long)s.tokens * a.g - (long long)s.tile * R > 128);
+      return s.n > 0 && s.rows > 128 * blk;
     };
     {
       const SegDesc& first = seg_wait(seg);
@@ -693,7 +682,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       const SegDesc& cur = sm.segs[seg.stage];                   // released at the end
       const int n = cur.n;
       if (n < 0) break;
-      const int rows = (int)min((long long)R, (long long)cur.tokens * a.g - (long long)cur.tile * R);
+      const int rows = cur.rows;
       const int row = cur.tile * R + blk * 128 + r;              // this thread's row
       const bool live = blk * 128 + r < rows;
       const int before = cur.len - cur.tokens;

@@ -52,7 +52,9 @@ struct RowsCfg {
   static constexpr bool kQRegs = NT * D <= 128;                  // query operands stay in registers
   static constexpr int kBox = D * kElem >= 128 ? 128 : 64;       // swizzle span, bytes
   static constexpr int kQLd = 2 * D + 16;                        // bytes of a staged query row
-  static constexpr int kChunk = D / (Q8 && D > 64 ? 8 : 4);      // columns merged at a time
+  // columns merged at a time, as the shared memory beside the ring allows
+  static constexpr int kChunk = NT == 1 ? (D == 256 && !Q8 ? 128 : 64) : D / (Q8 && D > 64 ? 8 : 4);
+  static constexpr int kReaders = kConsumers + 1;                // warps that read a published segment
   static constexpr int kMLd = kChunk + 4;
 };
 
@@ -69,6 +71,8 @@ struct __align__(1024) RowsSmem {
   LineScan<C::kRows, C::kThreads> scan;
   uint64_t full[C::kStages];
   uint64_t empty[C::kStages];
+  SegDesc segs[kSegs];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full, q_empty;
   int dead;
 };
@@ -179,6 +183,10 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       mbar_init(&sm.full[i], Q8 ? 2 + TK / 8 : 2);
       mbar_init(&sm.empty[i], C::kConsumers);
     }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&sm.seg_full[i], 1);
+      mbar_init(&sm.seg_empty[i], C::kReaders);
+    }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, C::kConsumers);
     sm.dead = 0;
@@ -200,10 +208,11 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     if (tid == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, nullptr, 0);
     return;
   }
-  SegIter<R, TK> it;
-  it.start(&b, c.page_shift, c.H, a.g, fix, pieces, cta, sm.scan.at);
-  Segment sg;
-  sg.split = false;
+  int seg = 0;                    // place in the ring of segments
+  uint32_t seg_phase = 0;
+  auto seg_step = [&]() {
+    if (++seg == kSegs) { seg = 0; seg_phase ^= 1u; }
+  };
 
   if (warp >= C::kConsumers) {
     // ---------------------------------------------------------------- producers
@@ -212,23 +221,47 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     const bool values = warp > C::kConsumers;
     int stage = 0;
     uint32_t phase = 0, q_phase = 0;
-    while (it.next(&sg)) {
-      if (sg.ta >= sg.tb) continue;
-      const int rows = (int)min((long long)R, (long long)sg.info.tokens * a.g - sg.tile * R);
+    SegIter<R, TK> it;
+    Segment sg;
+    sg.split = false;
+    if (!values) it.start(&b, c.page_shift, c.H, a.g, fix, pieces, cta, sm.scan.at);
+    while (true) {
+      // the keys' producer walks the piece, for all
+      SegDesc d = {};
+      d.n = -1;
+      if (!values) {
+        bool more = it.next(&sg);
+        while (more && idle(sg)) more = it.next(&sg);
+        if (more) d = describe<R>(sg, a.g);
+        wait_or_die(&sm.seg_empty[seg], seg_phase ^ 1u, &sm.dead, c.status);
+        if (lane == 0) {
+          sm.segs[seg] = d;
+          mbar_arrive(&sm.seg_full[seg]);
+        }
+      } else {
+        wait_or_die(&sm.seg_full[seg], seg_phase, &sm.dead, c.status);
+        d = sm.segs[seg];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.seg_empty[seg]);
+      }
+      __syncwarp();
+      seg_step();
+      if (d.n < 0) break;
+      if (d.n == 0) continue;
+      const int tb = d.ta + d.n, keys = d.keys;
       // the queries' place is free when the tile before has been scored: after what the ring takes
-      const int q_after = min(sg.tb, sg.ta + C::kStages - 1) - 1;
-      const int* table = b.table + (long long)sg.seq * b.table_ld;
-      const int keys = min(sg.info.len, tile_keys<R>(sg.info, a.g, sg.tile));
+      const int q_after = min(tb, d.ta + C::kStages - 1) - 1;
+      const int* table = b.table + (long long)d.seq * b.table_ld;
       // Lane i < TK / 16 looks after the i-th 16 keys of a stage: their page, fetched a stage ahead,
       // the box that begins with them (a box is a page's part of the stage), and their scale bytes.
       constexpr int kLanes = TK / 16;
       const int box = min(1 << c.page_shift, TK);
-      int k0 = sg.ta * TK + (lane % kLanes) * 16;
+      int k0 = d.ta * TK + (lane % kLanes) * 16;
       int page = k0 < keys ? __ldg(table + (k0 >> c.page_shift)) : 0;
-      for (int i = sg.ta; i < sg.tb; ++i) {
+      for (int i = d.ta; i < tb; ++i) {
         const int k1 = k0 + TK;
         int page_next = 0;
-        if (i + 1 < sg.tb && k1 < keys) page_next = __ldg(table + (k1 >> c.page_shift));
+        if (i + 1 < tb && k1 < keys) page_next = __ldg(table + (k1 >> c.page_shift));
         wait_or_die(&sm.empty[stage], phase ^ 1u, &sm.dead, c.status);
         uint64_t* full = &sm.full[stage];
         const int live = (min(TK, keys - i * TK) + box - 1) / box;            // boxes
@@ -241,22 +274,22 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         const int off = k0 & ((1 << c.page_shift) - 1);
         if (lane < kLanes && k0 < keys && ((lane * 16) & (box - 1)) == 0)
           tma_load_5d(sm.ring[stage] + (values ? C::kHalfBytes : 0) + lane * 16 * D * C::kElem,
-                      values ? &maps.v : &maps.k, 0, off, 0, sg.head, page, full);
+                      values ? &maps.v : &maps.k, 0, off, 0, d.head, page, full);
         if (Q8 && lane < kLanes) {
           const bool in = k0 < keys && page < c.num_pages;
           const uint8_t* src = values ? c.vs : c.ks;
-          if (in) src += (((long long)page * c.H + sg.head) << c.page_shift) + off;
+          if (in) src += (((long long)page * c.H + d.head) << c.page_shift) + off;
           cp_async16_mbar(smem_u32(&sm.scales[stage][values][lane * 16]), src, in, full);
         }
         __syncwarp();
         if (values && i == q_after) {
           wait_or_die(&sm.q_empty, q_phase ^ 1u, &sm.dead, c.status);
           q_phase ^= 1u;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)rows * 2 * D);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)d.rows * 2 * D);
           __syncwarp();
-          if (lane < rows) {
+          if (lane < d.rows) {
             int tok, head;
-            row_of(sg.info, a.g, sg.head, sg.tile * R + lane, &tok, &head);
+            row_of(SeqInfo{d.row0, d.tokens, d.len}, a.g, d.head, d.tile * R + lane, &tok, &head);
             bulk_g2s(sm.q[lane], a.q + tok * a.q_ld + head * a.q_head_ld, 2 * D, &sm.q_full);
           }
           __syncwarp();
@@ -285,24 +318,29 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   }
   int stage = 0;
   uint32_t phase = 0, q_phase = 0;
-  while (it.next(&sg)) {
-    const SeqInfo info = sg.info;
-    const int row_base = sg.tile * R;
-    const int rows = min((long long)R, (long long)info.tokens * a.g - row_base);
-    if (sg.ta >= sg.tb) {
-      if (sg.owns_empty)
+  while (true) {
+    wait_or_die(&sm.seg_full[seg], seg_phase, &sm.dead, c.status);
+    const SegDesc sg = sm.segs[seg];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.seg_empty[seg]);
+    seg_step();
+    if (sg.n < 0) break;
+    const SeqInfo info{sg.row0, sg.tokens, sg.len};
+    const int row_base = sg.tile * R, rows = sg.rows, keys = sg.keys;
+    if (sg.n == 0) {
+      if (sg.owns_empty) {
         for (int i = tid; i < rows * (D / 8); i += NC) {
           int tok, head;
           row_of(info, a.g, sg.head, row_base + i / (D / 8), &tok, &head);
           *reinterpret_cast<uint4*>(a.out + ((long long)tok * a.Hq + head) * D + (i % (D / 8)) * 8) =
               make_uint4(0, 0, 0, 0);
         }
-      else if (sg.nt > 0)                                // an empty share of a split tile
+      } else {                                             // an empty share of a split tile
         for (int i = tid; i < rows; i += NC)
           __stcg(reinterpret_cast<float2*>(Partials<R, D>::ml(a.ws, cta, sg.slot) + 2 * i), make_float2(-INFINITY, 0.f));
+      }
       continue;
     }
-    const int keys = min(info.len, tile_keys<R>(info, a.g, sg.tile));
     const int before = info.len - info.tokens;          // position of the first new token
     wait_or_die(&sm.q_full, q_phase, &sm.dead, c.status);
     q_phase ^= 1u;
@@ -385,7 +423,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
 
-    for (int i = sg.ta; i < sg.tb; ++i) {
+    for (int i = sg.ta; i < sg.ta + sg.n; ++i) {
       const int st = stage;
       wait_or_die(&sm.full[st], phase, &sm.dead, c.status);
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
@@ -724,7 +762,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
         if (Q8) f[nt][e] *= v_ref == 0 ? 0.f : __uint_as_float((uint32_t)(v_ref - 7) << 23);   // 2^(v_ref - 134)
       }
-    const bool whole = sg.whole();
+    const bool whole = sg.whole;
     float* prow = Partials<R, D>::rows(a.ws, cta, sg.slot);
     // Some of the columns at a time: every warp lays its part down, and each thread adds the
     // warps' values of the four columns it then writes.
