@@ -191,22 +191,24 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant="none"
     total is x + residual in the activation dtype (None without a residual).  quant "none": y in
     the activation dtype, scales None; "row" / "block": y float8_e4m3fn with f32 scales per row
     [rows][1] or per 128 columns [rows][ceil(n / 128)]."""
-    if x.dim() != 2 or x.stride(1) != 1 or x.dtype != weight.dtype or weight.shape != (x.shape[1],) or \
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2 or x.stride(1) != 1 or dtype != weight.dtype or weight.shape != shape[1:] or \
             weight.stride(0) != 1:
         raise ValueError("rms_norm takes rows [rows][n] and a weight [n] of one dtype")
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or
+    if residual is not None and (residual.shape != shape or residual.dtype != dtype or
                                  residual.stride(1) != 1):
         raise ValueError("residual must have the shape and dtype of x")
     kind = _NORM_KINDS[quant]
-    rows, n = x.shape
-    scales = None
+    rows, n = shape
+    scales = total = None
     if kind == gdn.GDN_NORM_ACT:
-        y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
     else:
-        y = torch.empty((rows, n), dtype=torch.float8_e4m3fn, device=x.device)
+        y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
         scales = torch.empty((rows, 1 if quant == "row" else (n + 127) // 128), dtype=torch.float32,
                              device=x.device)
-    total = None if residual is None else torch.empty((rows, n), dtype=x.dtype, device=x.device)
+    if residual is not None:
+        total = torch.empty(shape, dtype=dtype, device=x.device)
     gdn.gdn_rms_norm(x, weight, y, residual, total, scales, weight_offset, eps, kind, stream)
     return y, scales, total
 
@@ -262,6 +264,7 @@ class PagedKVCache:
                 raise ValueError("an 8-bit cache has contiguous uint8 scales [pages][heads][page_size]")
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
         self.num_kv_heads, self.head_dim = int(k_pages.shape[1]), int(k_pages.shape[3])
+        self.device = k_pages.device
         self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
         self.c = gdn.make_kv_cache(k_pages, v_pages, k_scales, v_scales, self.status)
         self._ws = {}
@@ -278,15 +281,16 @@ class PagedKVCache:
         return ws
 
     def _check(self, t, batch, what):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != batch.total_tokens or \
-                t.shape[2] != self.head_dim or t.stride(2) != 1:
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != batch.total_tokens or shape[2] != self.head_dim or \
+                t.dtype != torch.bfloat16 or t.stride(2) != 1:
             raise ValueError(f"{what}: bf16 [total_tokens][heads][head_dim] with contiguous vectors expected")
+        return shape
 
     def append(self, batch: KVBatch, k, v, stream=None):
         """Stores the new tokens' keys and values, bf16 [total_tokens][num_kv_heads][head_dim]."""
         for t, what in ((k, "k"), (v, "v")):
-            self._check(t, batch, what)
-            if t.shape[1] != self.num_kv_heads or t.stride(1) != self.head_dim:
+            if self._check(t, batch, what)[1] != self.num_kv_heads or t.stride(1) != self.head_dim:
                 raise ValueError(f"{what}: {self.num_kv_heads} adjacent heads expected")
         if batch.total_tokens:
             gdn.gdn_kv_append(self.c, batch.c, k, v, stream)
@@ -295,12 +299,13 @@ class PagedKVCache:
         """The batch's tokens' keys and values back as bf16 (k, v)."""
         shape = (batch.total_tokens, self.num_kv_heads, self.head_dim)
         if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_pages.device)
+            k = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        elif k.shape != shape or k.dtype != torch.bfloat16 or not k.is_contiguous():
+            raise ValueError("k: contiguous bf16 [total_tokens][num_kv_heads][head_dim]")
         if v is None:
-            v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_pages.device)
-        for t in (k, v):
-            if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
-                raise ValueError("k, v: contiguous bf16 [total_tokens][num_kv_heads][head_dim]")
+            v = torch.empty_like(k)
+        elif v.shape != shape or v.dtype != torch.bfloat16 or not v.is_contiguous():
+            raise ValueError("v: contiguous bf16 [total_tokens][num_kv_heads][head_dim]")
         if batch.total_tokens:
             gdn.gdn_kv_read(self.c, batch.c, k, v, stream)
         return k, v
@@ -308,17 +313,17 @@ class PagedKVCache:
     def attend(self, batch: KVBatch, q, gate=None, scale=0.0, out=None, workspace=None, stream=None):
         """Causal attention of the new tokens' queries, bf16 [total_tokens][num_q_heads][head_dim]
         (times sigmoid(gate)), over the cache, which already holds their keys and values."""
-        self._check(q, batch, "q")
-        if gate is not None:
-            self._check(gate, batch, "gate")
-            if gate.shape != q.shape:
-                raise ValueError("gate must have the shape of q")
+        shape = self._check(q, batch, "q")
+        if gate is not None and self._check(gate, batch, "gate") != shape:
+            raise ValueError("gate must have the shape of q")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
             raise ValueError("out: contiguous bf16 with the shape of q")
         if batch.total_tokens:
             if workspace is None:
-                workspace = self.workspace(q.shape[1])
+                workspace = self._ws.get(shape[1])
+                if workspace is None:
+                    workspace = self.workspace(shape[1])
             gdn.gdn_paged_attention(self.c, batch.c, q, out, workspace, gate, scale, stream)
         return out
