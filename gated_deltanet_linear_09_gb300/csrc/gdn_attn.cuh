@@ -407,6 +407,44 @@ __device__ __forceinline__ void zero_padding(const AttnArgs& a, const KvBatchVie
 
 // ------------------------------------------------------------------ merging split tiles
 
+// A running merge of partial results (reference, sum and Q groups of four columns), a few at a time so
+// that their loads are in flight together.
+constexpr int kMergeBatch = 4;
+
+template <int Q>
+struct Merged {
+  float top = -INFINITY, l = 0.f;
+  float4 o[Q];
+  __device__ __forceinline__ Merged() {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(const float2 (&ml)[kMergeBatch], const float4 (&p)[kMergeBatch][Q]) {
+    float to = top;
+#pragma unroll
+    for (int y = 0; y < kMergeBatch; ++y) to = fmaxf(to, ml[y].x);
+    if (to == -INFINITY) return;
+    const float f = exp2f(top - to);      // 0 at first
+    const bool first = top == -INFINITY;
+    top = to;
+    l = first ? 0.f : l * f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      o[q] = first ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[q].x * f, o[q].y * f, o[q].z * f, o[q].w * f);
+#pragma unroll
+    for (int y = 0; y < kMergeBatch; ++y) {
+      if (ml[y].x == -INFINITY) continue;
+      const float w = exp2f(ml[y].x - to);
+      l = fmaf(w, ml[y].y, l);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        o[q].x = fmaf(w, p[y][q].x, o[q].x); o[q].y = fmaf(w, p[y][q].y, o[q].y);
+        o[q].z = fmaf(w, p[y][q].z, o[q].z); o[q].w = fmaf(w, p[y][q].w, o[q].w);
+      }
+    }
+  }
+};
+
 // Merges the split tiles: each piece's rows count 2^(m - M), M the largest reference of the row.
 // The work (8 rows, or one row read by all 8 warps) is spread over the grid by the counts that
 // every CTA of the attention kernel left.
@@ -459,23 +497,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const AttnArgs 
       // lane = row, warp = four columns
       const int v = u - before[lo], r = v / (D / 32) * 32 + lane, col = (v % (D / 32)) * 32 + warp * 4;
       if (r < d.rows) {
-        float top = -INFINITY, l = 0.f;
-#pragma unroll 8
-        for (int j = 0; j < d.count; ++j)
-          top = fmaxf(top, __ldcg(Partials<R, D>::ml(a.ws, lo + j, j == 0 ? 1 : 0) + 2 * r));
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int j = 0; j < d.count; ++j) {
-          const int slot = j == 0 ? 1 : 0;
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(Partials<R, D>::ml(a.ws, lo + j, slot) + 2 * r));
-          if (ml.x == -INFINITY) continue;           // an empty share left only its (m, l)
-          const float w = exp2f(ml.x - top);
-          const float4 p = __ldcg(reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, lo + j, slot)) +
-                                  (size_t)(col / 4) * R + r);
-          l += w * ml.y;
-          o.x = fmaf(w, p.x, o.x); o.y = fmaf(w, p.y, o.y);
-          o.z = fmaf(w, p.z, o.z); o.w = fmaf(w, p.w, o.w);
+        Merged<1> acc;
+        for (int j0 = 0; j0 < d.count; j0 += kMergeBatch) {
+          float2 ml[kMergeBatch];
+          float4 p[kMergeBatch][1];
+#pragma unroll
+          for (int y = 0; y < kMergeBatch; ++y) {
+            const int j = j0 + y, slot = j == 0 ? 1 : 0;
+            ml[y] = make_float2(-INFINITY, 0.f);
+            if (j < d.count) {
+              ml[y] = __ldcg(reinterpret_cast<const float2*>(Partials<R, D>::ml(a.ws, lo + j, slot) + 2 * r));
+              // (where the share was empty this is whatever was there, and not used)
+              p[y][0] = __ldcg(reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, lo + j, slot)) +
+                               (size_t)(col / 4) * R + r);
+            }
+          }
+          acc.add(ml, p);
         }
+        const float l = acc.l;
+        const float4 o = acc.o[0];
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         int tok, head;
         row_of(SeqInfo{d.row0, d.tokens, 0}, a.g, d.head, d.tile * R + r, &tok, &head);
@@ -486,37 +526,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const AttnArgs 
     const bool together = whole_block_rows(d.count);
     const int r = together ? u - before[lo] : (u - before[lo]) * kMergeWarps + warp;
     const int j0 = together ? warp : 0, step = together ? kMergeWarps : 1;
-    float4 sum[Q];
+    Merged<Q> part;
+    if (r < d.rows)
+      for (int jb = j0; jb < d.count; jb += step * kMergeBatch) {
+        float2 ml[kMergeBatch];
+        float4 p[kMergeBatch][Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) sum[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float top = -INFINITY, l = 0.f;
-    if (r < d.rows) {
-      // the references first: a lane each
-      float m0 = -INFINITY;
-      for (int j = lane; j < d.count; j += 32)
-        m0 = fmaxf(m0, __ldcg(Partials<R, D>::ml(a.ws, lo + j, j == 0 ? 1 : 0) + 2 * r));
+        for (int y = 0; y < kMergeBatch; ++y) {
+          const int j = jb + y * step, slot = j == 0 ? 1 : 0;
+          ml[y] = make_float2(-INFINITY, 0.f);
+          if (j < d.count) {
+            ml[y] = __ldcg(reinterpret_cast<const float2*>(Partials<R, D>::ml(a.ws, lo + j, slot) + 2 * r));
+            const float4* src = reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, lo + j, slot) + (size_t)r * D);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-      top = m0;
-#pragma unroll 4
-      for (int j = j0; j < d.count; j += step) {
-        const int slot = j == 0 ? 1 : 0;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(Partials<R, D>::ml(a.ws, lo + j, slot) + 2 * r));
-        const float4* src = reinterpret_cast<const float4*>(Partials<R, D>::rows(a.ws, lo + j, slot) + (size_t)r * D);
-        const bool some = ml.x != -INFINITY;      // an empty share left only its (m, l)
-        const float w = some ? exp2f(ml.x - top) : 0.f;
-        if (some) l += w * ml.y;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          const int col = q * 32 + lane;
-          if (some && col < D / 4) {
-            const float4 v = __ldcg(src + col);
-            sum[q].x = fmaf(w, v.x, sum[q].x); sum[q].y = fmaf(w, v.y, sum[q].y);
-            sum[q].z = fmaf(w, v.z, sum[q].z); sum[q].w = fmaf(w, v.w, sum[q].w);
+            for (int q = 0; q < Q; ++q)
+              if (q * 32 + lane < D / 4) p[y][q] = __ldcg(src + q * 32 + lane);
           }
         }
+        part.add(ml, p);
       }
-    }
+    const float4(&sum)[Q] = part.o;
+    const float l = part.l, top = part.top;
     const SeqInfo info{d.row0, d.tokens, 0};
     int tok = 0, head = 0;
     if (!together) {
@@ -541,12 +571,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const AttnArgs 
       __syncthreads();
       if (tid < D / 4) {
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lt = 0.f;
+        float lt = 0.f, most = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) most = fmaxf(most, acc_ml[w].x);
 #pragma unroll
         for (int w = 0; w < kMergeWarps; ++w) {
+          if (acc_ml[w].x == -INFINITY) continue;
+          const float f = exp2f(acc_ml[w].x - most);
           const float4 v = acc[w][tid];
-          o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-          lt += acc_ml[w].y;
+          o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+          lt = fmaf(f, acc_ml[w].y, lt);
         }
         const float inv = lt == 0.f ? 0.f : 1.0f / lt;
         row_of(info, a.g, d.head, d.tile * R + r, &tok, &head);

@@ -999,7 +999,7 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   int rc = launch_dependent(chunk_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
-  return launch_dependent(merge_kernel<C::kRows, D>, dim3((unsigned)(2 * sms)), kMergeWarps * 32, 0, stream, a, grid);
+  return launch_dependent(merge_kernel<C::kRows, D>, dim3((unsigned)(6 * sms)), kMergeWarps * 32, 0, stream, a, grid);
 }
 
 size_t chunk_ws_bytes(int D, int sms) {

@@ -832,9 +832,9 @@ int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sm
   if (!make_kv_maps(c, P < C::kKeys ? P : C::kKeys, &maps)) return GDN_ERR_CUDA;
   // What a tile costs beside its keys, in keys: some 3 us, in which an 8-bit cache gives twice the
   // keys.  (64 sequences of 255 to 15859: 8-bit 133 us at 64, 121 at 192, 111 at 384; bf16 193, 193,
-  // 195.)  And the fewest keys worth a piece of their own (777 keys: 15 us at 128 or 256, 18 at 512).
+  // 195.)  And the fewest keys worth a piece of their own (777 keys: 14.7 us at 128, 15.5 at 256, 18.4 at 512).
   const int grid = rows_grid(D, sms), fix = (Q8 ? 384 : 128) * a.g;
-  const int least = 256 * a.g;
+  const int least = 128 * a.g;
   int rc = launch_dependent(rows_kernel<D, Q8, NT>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;

@@ -40,103 +40,131 @@ __device__ __forceinline__ uint4 dequant8(uint2 u, uint32_t b) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One thread per 8 elements of the key and the value vector of a (token, head): D / 8 neighbouring
-// lanes share a vector, whose maximum they find by shuffles.  A grid of one pass: every thread
-// issues its two 16-byte loads at once, and the places are found from cu_seqlens by a 32-way
-// search per warp (two steps up to 1,024 sequences) instead of a binary one.
-template <int D, bool Q>
+// One thread per 8 elements of the key and the value vector of U (token, head) pairs: D / 8
+// neighbouring lanes share a vector, whose maximum they find by shuffles.  Bound by the bytes; what
+// keeps a thread from its stores is the chain of lookups to its place (sequence, length, page), so
+// the vectors are loaded first, for all U at once, and sequences are found by a 32-way search per
+// warp (two steps up to 1,024 sequences) instead of a binary one.
+template <int D>
+struct Lane {
+  long long vec;      // (token, head) pair
+  int part, tok, head;
+  bool live;
+  __device__ __forceinline__ Lane(const KvView& c, const KvBatchView& bt, int u) {
+    constexpr int L = D / 8;
+    const long long gid = ((long long)u * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
+    vec = gid / L;
+    part = (int)(gid % L);
+    live = vec < (long long)bt.total * c.H;
+    tok = live ? (int)((unsigned long long)vec >> 32 == 0 ? (unsigned)vec / (unsigned)c.H : vec / c.H) : bt.total - 1;
+    head = live ? (int)(vec - (long long)tok * c.H) : 0;
+  }
+};
+
+template <int D, bool Q, int U>
 __global__ void __launch_bounds__(256) append_kernel(const KvView c, const KvBatchView bt,
                                                      const __nv_bfloat16* __restrict__ k, long long k_ld,
                                                      const __nv_bfloat16* __restrict__ v, long long v_ld) {
-  constexpr int L = D / 8;
   pdl_begin();
-  const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long vec = gid / L;
-  const int part = (int)(gid % L);
-  const bool live = vec < (long long)bt.total * c.H;
-  const int tok = live ? (int)(vec / c.H) : bt.total - 1;
-  const int head = live ? (int)(vec % c.H) : 0;
-  uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-  if (live) {
-    kx = __ldg(reinterpret_cast<const uint4*>(k + (long long)tok * k_ld + head * D + part * 8));
-    vx = __ldg(reinterpret_cast<const uint4*>(v + (long long)tok * v_ld + head * D + part * 8));
-  }
-  const Place p = find_place(c, bt, tok);
-  const bool store = live && p.page >= 0;
-  const long long at = store ? (((long long)p.page * c.H + head) << c.page_shift) + p.off : 0;
-  if constexpr (!Q) {
-    if (store) {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.k) + at * D + part * 8) = kx;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.v) + at * D + part * 8) = vx;
+  uint4 kx[U], vx[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Lane<D> a(c, bt, u);
+    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+    if (a.live) {
+      kx[u] = __ldcs(reinterpret_cast<const uint4*>(k + (long long)a.tok * k_ld + a.head * D + a.part * 8));
+      vx[u] = __ldcs(reinterpret_cast<const uint4*>(v + (long long)a.tok * v_ld + a.head * D + a.part * 8));
     }
-  } else {
+  }
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const uint4 x = which ? vx : kx;
-      uint32_t m = 0;
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        m = max(m, w[i] & 0x7fffu);
-        m = max(m, (w[i] >> 16) & 0x7fffu);
-      }
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int b = scale_byte(m);
-      // 2^(127 - b): exponent field 254 - b, at least 7 (b <= 247 for finite vectors)
-      const float inv = __uint_as_float((uint32_t)(254 - (b == 255 ? 127 : b)) << 23);
-      float f[8];
-      unpack8(x, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= inv;
-      uint2 q = make_uint2(e4m3x4(f), e4m3x4(f + 4));
+  for (int u = 0; u < U; ++u) {
+    const Lane<D> a(c, bt, u);
+    const Place p = find_place(c, bt, a.tok);
+    const bool store = a.live && p.page >= 0;
+    const long long at = store ? (((long long)p.page * c.H + a.head) << c.page_shift) + p.off : 0;
+    if constexpr (!Q) {
       if (store) {
-        // codes of a vector that reads as NaN: any finite ones
-        if (b == 255) q = make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(which ? c.v : c.k) + at * D + part * 8) = q;
-        if (part == 0) (which ? c.vs : c.ks)[at] = (uint8_t)b;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.k) + at * D + a.part * 8) = kx[u];
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.v) + at * D + a.part * 8) = vx[u];
+      }
+    } else {
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const uint4 x = which ? vx[u] : kx[u];
+        uint32_t m = 0;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          m = max(m, w[i] & 0x7fffu);
+          m = max(m, (w[i] >> 16) & 0x7fffu);
+        }
+#pragma unroll
+        for (int o = D / 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int b = scale_byte(m);
+        // 2^(127 - b): exponent field 254 - b, at least 7 (b <= 247 for finite vectors)
+        const float inv = __uint_as_float((uint32_t)(254 - (b == 255 ? 127 : b)) << 23);
+        float f[8];
+        unpack8(x, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= inv;
+        uint2 q = make_uint2(e4m3x4(f), e4m3x4(f + 4));
+        if (store) {
+          // codes of a vector that reads as NaN: any finite ones
+          if (b == 255) q = make_uint2(0, 0);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(which ? c.v : c.k) + at * D + a.part * 8) = q;
+          if (a.part == 0) (which ? c.vs : c.ks)[at] = (uint8_t)b;
+        }
       }
     }
   }
 }
 
-template <int D, bool Q>
+template <int D, bool Q, int U>
 __global__ void __launch_bounds__(256) read_kernel(const KvView c, const KvBatchView bt,
                                                    __nv_bfloat16* __restrict__ k,
                                                    __nv_bfloat16* __restrict__ v) {
-  constexpr int L = D / 8;
   pdl_begin();
-  const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long vec = gid / L;
-  const int part = (int)(gid % L);
-  const bool live = vec < (long long)bt.total * c.H;
-  const int tok = live ? (int)(vec / c.H) : bt.total - 1;
-  const int head = live ? (int)(vec % c.H) : 0;
-  const Place p = find_place(c, bt, tok);
-  if (!live) return;
-  uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-  if (p.page >= 0) {
-    const long long at = (((long long)p.page * c.H + head) << c.page_shift) + p.off;
-    if constexpr (!Q) {
-      kx = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.k) + at * D + part * 8));
-      vx = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + at * D + part * 8));
-    } else {
-      const uint2 kq = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + at * D + part * 8));
-      const uint2 vq = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + at * D + part * 8));
-      const uint32_t kb = c.ks[at], vb = c.vs[at];
-      kx = dequant8(kq, kb);
-      vx = dequant8(vq, vb);
+  uint4 kx[U], vx[U];
+  uint2 kq[U], vq[U];
+  uint32_t kb[U], vb[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Lane<D> a(c, bt, u);
+    const Place p = find_place(c, bt, a.tok);
+    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+    kq[u] = vq[u] = make_uint2(0, 0);
+    kb[u] = vb[u] = 0;
+    if (a.live && p.page >= 0) {
+      const long long at = (((long long)p.page * c.H + a.head) << c.page_shift) + p.off;
+      if constexpr (!Q) {
+        kx[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.k) + at * D + a.part * 8));
+        vx[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + at * D + a.part * 8));
+      } else {
+        kq[u] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + at * D + a.part * 8));
+        vq[u] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + at * D + a.part * 8));
+        kb[u] = c.ks[at];
+        vb[u] = c.vs[at];
+      }
     }
   }
-  const long long o = vec * D + part * 8;
-  __stcs(reinterpret_cast<uint4*>(k + o), kx);
-  __stcs(reinterpret_cast<uint4*>(v + o), vx);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Lane<D> a(c, bt, u);
+    if (!a.live) continue;
+    if constexpr (Q) {
+      kx[u] = dequant8(kq[u], kb[u]);      // (codes 0 and byte 0 give zeros)
+      vx[u] = dequant8(vq[u], vb[u]);
+    }
+    const long long o = a.vec * D + a.part * 8;
+    __stcs(reinterpret_cast<uint4*>(k + o), kx[u]);
+    __stcs(reinterpret_cast<uint4*>(v + o), vx[u]);
+  }
 }
 
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), long long threads, cudaStream_t stream, Args... args) {
+int launch(void (*kern)(KArgs...), int each, long long threads, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((threads + 255) / 256));
+  cfg.gridDim = dim3((unsigned)((threads + 256 * each - 1) / (256 * each)));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -147,6 +175,9 @@ int launch(void (*kern)(KArgs...), long long threads, cudaStream_t stream, Args.
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// More than one pair a thread once there are far more threads than the SMs hold at a time.
+constexpr long long kManyThreads = 1 << 20;
+
 }  // namespace
 
 int launch_kv_append(const KvView& c, const KvBatchView& bt, const void* k, long long k_ld,
@@ -154,26 +185,34 @@ int launch_kv_append(const KvView& c, const KvBatchView& bt, const void* k, long
   const auto* kp = static_cast<const __nv_bfloat16*>(k);
   const auto* vp = static_cast<const __nv_bfloat16*>(v);
   const long long n = (long long)bt.total * c.H * (c.D / 8);
-#define GDN_RUN(DD)                                                                   \
-  return c.ks ? launch(append_kernel<DD, true>, n, stream, c, bt, kp, k_ld, vp, v_ld) \
-              : launch(append_kernel<DD, false>, n, stream, c, bt, kp, k_ld, vp, v_ld)
-  if (c.D == 64) GDN_RUN(64);
-  if (c.D == 128) GDN_RUN(128);
+#define GDN_RUN_U(DD, U)                                                                    \
+  return c.ks ? launch(append_kernel<DD, true, U>, U, n, stream, c, bt, kp, k_ld, vp, v_ld) \
+              : launch(append_kernel<DD, false, U>, U, n, stream, c, bt, kp, k_ld, vp, v_ld)
+#define GDN_RUN(DD)               \
+  if (n > kManyThreads) GDN_RUN_U(DD, 2); \
+  else GDN_RUN_U(DD, 1)
+  if (c.D == 64) { GDN_RUN(64); }
+  if (c.D == 128) { GDN_RUN(128); }
   GDN_RUN(256);
 #undef GDN_RUN
+#undef GDN_RUN_U
 }
 
 int launch_kv_read(const KvView& c, const KvBatchView& bt, void* k, void* v, cudaStream_t stream) {
   auto* kp = static_cast<__nv_bfloat16*>(k);
   auto* vp = static_cast<__nv_bfloat16*>(v);
   const long long n = (long long)bt.total * c.H * (c.D / 8);
-#define GDN_RUN(DD)                                                         \
-  return c.ks ? launch(read_kernel<DD, true>, n, stream, c, bt, kp, vp)     \
-              : launch(read_kernel<DD, false>, n, stream, c, bt, kp, vp)
-  if (c.D == 64) GDN_RUN(64);
-  if (c.D == 128) GDN_RUN(128);
+#define GDN_RUN_U(DD, U)                                                          \
+  return c.ks ? launch(read_kernel<DD, true, U>, U, n, stream, c, bt, kp, vp)     \
+              : launch(read_kernel<DD, false, U>, U, n, stream, c, bt, kp, vp)
+#define GDN_RUN(DD)               \
+  if (n > kManyThreads) GDN_RUN_U(DD, 2); \
+  else GDN_RUN_U(DD, 1)
+  if (c.D == 64) { GDN_RUN(64); }
+  if (c.D == 128) { GDN_RUN(128); }
   GDN_RUN(256);
 #undef GDN_RUN
+#undef GDN_RUN_U
 }
 
 }  // namespace gdn
