@@ -40,131 +40,184 @@ __device__ __forceinline__ uint4 dequant8(uint2 u, uint32_t b) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One thread per 8 elements of the key and the value vector of U (token, head) pairs: D / 8
-// neighbouring lanes share a vector, whose maximum they find by shuffles.  Bound by the bytes; what
-// keeps a thread from its stores is the chain of lookups to its place (sequence, length, page), so
-// the vectors are loaded first, for all U at once, and sequences are found by a 32-way search per
-// warp (two steps up to 1,024 sequences) instead of a binary one.
-template <int D>
-struct Lane {
-  long long vec;      // (token, head) pair
-  int part, tok, head;
-  bool live;
-  __device__ __forceinline__ Lane(const KvView& c, const KvBatchView& bt, int u) {
-    constexpr int L = D / 8;
-    const long long gid = ((long long)u * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
-    vec = gid / L;
-    part = (int)(gid % L);
-    live = vec < (long long)bt.total * c.H;
-    tok = live ? (int)((unsigned long long)vec >> 32 == 0 ? (unsigned)vec / (unsigned)c.H : vec / c.H) : bt.total - 1;
-    head = live ? (int)(vec - (long long)tok * c.H) : 0;
+// A CTA takes TB neighbouring tokens, a warp a token at a time (or a few narrow ones): the lanes walk
+// its heads' vectors in pieces of 8 elements, D / 8 neighbouring lanes to a vector.  Bound by the
+// bytes as long as the work per piece is small: the places (a 32-way search, a length, a page) are
+// looked up once per token by one warp, into shared memory, while the others' first loads are under
+// way.  (Looked up by every thread with 64-bit pair indices, the instructions were the bound: 68 % of
+// the issue slots and 3.6 TB/s.)
+constexpr int kMostTokens = 32;
+
+// The pieces of a CTA's tokens as its 8 warps walk them: every eighth run of 32 pieces each (narrow
+// tokens side by side in a run where they divide a warp).
+struct Walk {
+  int width, side, turns, count;
+  int tok, turn;                   // this run's first token, and run in the token
+  int lane_tok, lane_piece;
+  __device__ __forceinline__ Walk(int pieces, int tokens) {
+    const int lane = threadIdx.x & 31;
+    width = pieces;
+    count = tokens;
+    side = pieces < 32 && 32 % pieces == 0 ? 32 / pieces : 1;
+    turns = (pieces + 31) >> 5;
+    lane_tok = side > 1 ? lane / pieces : 0;
+    lane_piece = side > 1 ? lane % pieces : lane;
+    tok = 0;
+    turn = threadIdx.x >> 5;
+    settle();
   }
+  __device__ __forceinline__ void settle() {
+    while (turn >= turns) { turn -= turns; tok += side; }
+  }
+  __device__ __forceinline__ bool more() const { return tok < count; }
+  __device__ __forceinline__ void next() { turn += 8; settle(); }
+  __device__ __forceinline__ int token() const { return tok + lane_tok; }
+  __device__ __forceinline__ int piece() const { return turn * 32 + lane_piece; }
+  __device__ __forceinline__ bool live() const { return token() < count && piece() < width; }
 };
 
-template <int D, bool Q, int U>
-__global__ void __launch_bounds__(256) append_kernel(const KvView c, const KvBatchView bt,
+// Places of tokens t0 .. t0 + count - 1 (count <= 32) into shared memory, by one warp: the vector
+// index of head 0, or -1.
+__device__ __forceinline__ void find_places(const KvView& c, const KvBatchView& bt, int t0, int count,
+                                            long long* place) {
+  const int lane = threadIdx.x & 31;
+  const Place p = find_place(c, bt, min(t0 + lane, bt.total - 1));
+  if (lane < count) place[lane] = p.page < 0 ? -1 : (((long long)p.page * c.H) << c.page_shift) + p.off;
+}
+
+// Largest of the two halves' magnitudes.
+__device__ __forceinline__ uint32_t top_of(const uint4 x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                              __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+
+// 8 elements of a vector whose largest magnitude `top` the D / 8 lanes share -> codes.
+__device__ __forceinline__ uint2 quantise8(const uint4 x, int b) {
+  // 2^(127 - b): exponent field 254 - b, at least 7 (b <= 247 for finite vectors); the codes of a
+  // vector that reads as NaN: any finite ones
+  if (b == 255) return make_uint2(0, 0);
+  const float inv = __uint_as_float((uint32_t)(254 - b) << 23);
+  float f[8];
+  unpack8(x, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] *= inv;
+  return make_uint2(e4m3x4(f), e4m3x4(f + 4));
+}
+
+template <int D, bool Q>
+__global__ void __launch_bounds__(256) append_kernel(const KvView c, const KvBatchView bt, int tokens,
                                                      const __nv_bfloat16* __restrict__ k, long long k_ld,
                                                      const __nv_bfloat16* __restrict__ v, long long v_ld) {
+  constexpr int L = D / 8;
+  __shared__ long long place[kMostTokens];
+  const int t0 = blockIdx.x * tokens, count = min(tokens, bt.total - t0);
+  Walk w(c.H * L, count);
   pdl_begin();
-  uint4 kx[U], vx[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const Lane<D> a(c, bt, u);
-    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-    if (a.live) {
-      kx[u] = __ldcs(reinterpret_cast<const uint4*>(k + (long long)a.tok * k_ld + a.head * D + a.part * 8));
-      vx[u] = __ldcs(reinterpret_cast<const uint4*>(v + (long long)a.tok * v_ld + a.head * D + a.part * 8));
+  auto load = [&](uint4& kx, uint4& vx) {
+    kx = vx = make_uint4(0, 0, 0, 0);
+    if (w.live()) {
+      kx = __ldcs(reinterpret_cast<const uint4*>(k + (long long)(t0 + w.token()) * k_ld) + w.piece());
+      vx = __ldcs(reinterpret_cast<const uint4*>(v + (long long)(t0 + w.token()) * v_ld) + w.piece());
     }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const Lane<D> a(c, bt, u);
-    const Place p = find_place(c, bt, a.tok);
-    const bool store = a.live && p.page >= 0;
-    const long long at = store ? (((long long)p.page * c.H + a.head) << c.page_shift) + p.off : 0;
+  };
+  uint4 kx, vx;
+  load(kx, vx);
+  if (threadIdx.x < 32) find_places(c, bt, t0, count, place);
+  __syncthreads();
+  while (w.more()) {
+    const long long base = w.live() ? place[w.token()] : -1;
+    const int head = w.piece() / L, part = w.piece() % L;
+    w.next();
+    uint4 kn, vn;
+    load(kn, vn);
+    const long long at = base + ((long long)head << c.page_shift);
     if constexpr (!Q) {
-      if (store) {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.k) + at * D + a.part * 8) = kx[u];
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.v) + at * D + a.part * 8) = vx[u];
+      if (base >= 0) {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.k) + at * D + part * 8) = kx;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.v) + at * D + part * 8) = vx;
       }
     } else {
+      uint32_t km = top_of(kx), vm = top_of(vx);
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const uint4 x = which ? vx[u] : kx[u];
-        uint32_t m = 0;
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          m = max(m, w[i] & 0x7fffu);
-          m = max(m, (w[i] >> 16) & 0x7fffu);
-        }
-#pragma unroll
-        for (int o = D / 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int b = scale_byte(m);
-        // 2^(127 - b): exponent field 254 - b, at least 7 (b <= 247 for finite vectors)
-        const float inv = __uint_as_float((uint32_t)(254 - (b == 255 ? 127 : b)) << 23);
-        float f[8];
-        unpack8(x, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= inv;
-        uint2 q = make_uint2(e4m3x4(f), e4m3x4(f + 4));
-        if (store) {
-          // codes of a vector that reads as NaN: any finite ones
-          if (b == 255) q = make_uint2(0, 0);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(which ? c.v : c.k) + at * D + a.part * 8) = q;
-          if (a.part == 0) (which ? c.vs : c.ks)[at] = (uint8_t)b;
+      for (int o = L / 2; o > 0; o >>= 1) {
+        km = max(km, __shfl_xor_sync(0xffffffffu, km, o));
+        vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+      }
+      if (base >= 0) {
+        const int kb = scale_byte(km), vb = scale_byte(vm);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.k) + at * D + part * 8) = quantise8(kx, kb);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.v) + at * D + part * 8) = quantise8(vx, vb);
+        if (part == 0) {
+          c.ks[at] = (uint8_t)kb;
+          c.vs[at] = (uint8_t)vb;
         }
       }
     }
+    kx = kn;
+    vx = vn;
   }
 }
 
-template <int D, bool Q, int U>
-__global__ void __launch_bounds__(256) read_kernel(const KvView c, const KvBatchView bt,
+template <int D, bool Q>
+__global__ void __launch_bounds__(256) read_kernel(const KvView c, const KvBatchView bt, int tokens,
                                                    __nv_bfloat16* __restrict__ k,
                                                    __nv_bfloat16* __restrict__ v) {
+  constexpr int L = D / 8;
+  __shared__ long long place[kMostTokens];
+  const int t0 = blockIdx.x * tokens, count = min(tokens, bt.total - t0);
+  Walk w(c.H * L, count);
   pdl_begin();
-  uint4 kx[U], vx[U];
-  uint2 kq[U], vq[U];
-  uint32_t kb[U], vb[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const Lane<D> a(c, bt, u);
-    const Place p = find_place(c, bt, a.tok);
-    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-    kq[u] = vq[u] = make_uint2(0, 0);
-    kb[u] = vb[u] = 0;
-    if (a.live && p.page >= 0) {
-      const long long at = (((long long)p.page * c.H + a.head) << c.page_shift) + p.off;
-      if constexpr (!Q) {
-        kx[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.k) + at * D + a.part * 8));
-        vx[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + at * D + a.part * 8));
-      } else {
-        kq[u] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + at * D + a.part * 8));
-        vq[u] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + at * D + a.part * 8));
-        kb[u] = c.ks[at];
-        vb[u] = c.vs[at];
+  if (threadIdx.x < 32) find_places(c, bt, t0, count, place);
+  __syncthreads();
+  // what a piece is loaded as: bf16, or codes and the scale bytes
+  struct Piece {
+    uint4 k, v;
+    uint32_t kb, vb;
+  };
+  auto load = [&](Piece& x) {
+    x.k = x.v = make_uint4(0, 0, 0, 0);
+    x.kb = x.vb = 0;
+    const int p = w.piece();
+    const long long base = w.live() ? place[w.token()] : -1;
+    if (base < 0) return;
+    const long long at = base + ((long long)(p / L) << c.page_shift);
+    if constexpr (!Q) {
+      x.k = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.k) + at * D) + p % L);
+      x.v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + at * D) + p % L);
+    } else {
+      const uint2 kq = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + at * D) + p % L);
+      const uint2 vq = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + at * D) + p % L);
+      x.k.x = kq.x; x.k.y = kq.y;
+      x.v.x = vq.x; x.v.y = vq.y;
+      x.kb = c.ks[at];
+      x.vb = c.vs[at];
+    }
+  };
+  Piece x;
+  load(x);
+  while (w.more()) {
+    const bool live = w.live();
+    const long long o = (long long)(t0 + w.token()) * w.width + w.piece();
+    w.next();
+    Piece next;
+    load(next);
+    if (live) {
+      if constexpr (Q) {                     // (codes 0 and byte 0 give zeros)
+        x.k = dequant8(make_uint2(x.k.x, x.k.y), x.kb);
+        x.v = dequant8(make_uint2(x.v.x, x.v.y), x.vb);
       }
+      __stcs(reinterpret_cast<uint4*>(k) + o, x.k);
+      __stcs(reinterpret_cast<uint4*>(v) + o, x.v);
     }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const Lane<D> a(c, bt, u);
-    if (!a.live) continue;
-    if constexpr (Q) {
-      kx[u] = dequant8(kq[u], kb[u]);      // (codes 0 and byte 0 give zeros)
-      vx[u] = dequant8(vq[u], vb[u]);
-    }
-    const long long o = a.vec * D + a.part * 8;
-    __stcs(reinterpret_cast<uint4*>(k + o), kx[u]);
-    __stcs(reinterpret_cast<uint4*>(v + o), vx[u]);
+    x = next;
   }
 }
 
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), int each, long long threads, cudaStream_t stream, Args... args) {
+int launch(void (*kern)(KArgs...), int blocks, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((threads + 256 * each - 1) / (256 * each)));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -175,8 +228,16 @@ int launch(void (*kern)(KArgs...), int each, long long threads, cudaStream_t str
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// More than one pair a thread once there are far more threads than the SMs hold at a time.
-constexpr long long kManyThreads = 1 << 20;
+// Tokens of a CTA: one run of 32 pieces for each warp, more (up to eight) where that leaves the SMs
+// their fill of CTAs.  (96 tokens of 8 x 128, 8-bit: 6.5 us so, 8.5 us with eight tokens a CTA.)
+int tokens_per_cta(const KvView& c, const KvBatchView& bt) {
+  const int width = c.H * (c.D / 8);
+  const int side = width < 32 && 32 % width == 0 ? 32 / width : 1, turns = (width + 31) / 32;
+  int t = side * (turns < 8 ? 8 / turns : 1);
+  const long long most = (long long)t * 8;
+  while (t < kMostTokens && 2LL * t <= most && bt.total > 2048LL * t) t *= 2;
+  return t < kMostTokens ? t : kMostTokens;
+}
 
 }  // namespace
 
@@ -184,35 +245,27 @@ int launch_kv_append(const KvView& c, const KvBatchView& bt, const void* k, long
                      const void* v, long long v_ld, cudaStream_t stream) {
   const auto* kp = static_cast<const __nv_bfloat16*>(k);
   const auto* vp = static_cast<const __nv_bfloat16*>(v);
-  const long long n = (long long)bt.total * c.H * (c.D / 8);
-#define GDN_RUN_U(DD, U)                                                                    \
-  return c.ks ? launch(append_kernel<DD, true, U>, U, n, stream, c, bt, kp, k_ld, vp, v_ld) \
-              : launch(append_kernel<DD, false, U>, U, n, stream, c, bt, kp, k_ld, vp, v_ld)
-#define GDN_RUN(DD)               \
-  if (n > kManyThreads) GDN_RUN_U(DD, 2); \
-  else GDN_RUN_U(DD, 1)
-  if (c.D == 64) { GDN_RUN(64); }
-  if (c.D == 128) { GDN_RUN(128); }
+  const int tokens = tokens_per_cta(c, bt), blocks = (bt.total + tokens - 1) / tokens;
+#define GDN_RUN(DD)                                                                                \
+  return c.ks ? launch(append_kernel<DD, true>, blocks, stream, c, bt, tokens, kp, k_ld, vp, v_ld) \
+              : launch(append_kernel<DD, false>, blocks, stream, c, bt, tokens, kp, k_ld, vp, v_ld)
+  if (c.D == 64) GDN_RUN(64);
+  if (c.D == 128) GDN_RUN(128);
   GDN_RUN(256);
 #undef GDN_RUN
-#undef GDN_RUN_U
 }
 
 int launch_kv_read(const KvView& c, const KvBatchView& bt, void* k, void* v, cudaStream_t stream) {
   auto* kp = static_cast<__nv_bfloat16*>(k);
   auto* vp = static_cast<__nv_bfloat16*>(v);
-  const long long n = (long long)bt.total * c.H * (c.D / 8);
-#define GDN_RUN_U(DD, U)                                                          \
-  return c.ks ? launch(read_kernel<DD, true, U>, U, n, stream, c, bt, kp, vp)     \
-              : launch(read_kernel<DD, false, U>, U, n, stream, c, bt, kp, vp)
-#define GDN_RUN(DD)               \
-  if (n > kManyThreads) GDN_RUN_U(DD, 2); \
-  else GDN_RUN_U(DD, 1)
-  if (c.D == 64) { GDN_RUN(64); }
-  if (c.D == 128) { GDN_RUN(128); }
+  const int tokens = tokens_per_cta(c, bt), blocks = (bt.total + tokens - 1) / tokens;
+#define GDN_RUN(DD)                                                                    \
+  return c.ks ? launch(read_kernel<DD, true>, blocks, stream, c, bt, tokens, kp, vp)   \
+              : launch(read_kernel<DD, false>, blocks, stream, c, bt, tokens, kp, vp)
+  if (c.D == 64) GDN_RUN(64);
+  if (c.D == 128) GDN_RUN(128);
   GDN_RUN(256);
 #undef GDN_RUN
-#undef GDN_RUN_U
 }
 
 }  // namespace gdn
