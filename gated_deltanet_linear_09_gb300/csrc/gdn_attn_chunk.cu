@@ -533,8 +533,15 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     RingPos<Q8 ? C::kRStages : 1> src;
     RingPos<C::kVStages> dst;
     RingPos<Q8 ? C::kScales : 1> ks, vs;
-    constexpr int kPer = C::kCols / 8;                      // 8-element pieces of a row
-    const int piece = ct % kPer;
+    // A warp converts its own 32 rows, so that a row's multiplier comes from the lane that holds it.
+    // A lane takes 16 codes of a row in two halves, the first of which differs from lane to lane so
+    // that neither the 8-byte loads nor the 16-byte swizzled stores meet in a bank.  The loop is kept
+    // rolled, with the next row's loads ahead: unrolled eight times it does not fit an SM quarter's
+    // instruction cache next to the softmax, and both ran at a third of the speed (one prompt piece
+    // of 4096 on 16384 tokens, D = 256: 3147 us, rolled 1481 us).
+    constexpr int kPer = C::kCols / 16, kStep = 32 / kPer, kSteps = 32 / kStep;
+    const int piece = lane % kPer, sub = lane / kPer, warp_row = (ct >> 5) * 32 + sub;
+    const int odd = kPer == 8 ? (piece >> 2) ^ (sub & 1) : (sub >> 1) & 1;
     while (true) {
       const int n = seg_wait(seg).n;
       seg_done(seg);
@@ -554,29 +561,45 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           return;
         }
         wait_bar(&sm.r_full[src.stage], src.phase, &sm.dead, c.status);
+        const uint32_t bb = sm.scales[vs.stage][1][ct >> shift][ct & (box - 1)];
+        // the code's bits are the value times 2^-120: one multiply by 2^120 times the scale where that
+        // is a bf16 value, else two
+        const uint32_t f = bb <= 134 ? (bb + 120) << 7 : 0x7b80u;
+        const bool large = __any_sync(0xffffffffu, bb > 134);
         wait_bar(&sm.v_empty[dst.stage], dst.phase ^ 1u, &sm.dead, c.status);
-        const uint8_t* raw = sm.raw[src.stage];
+        const uint8_t* raw = sm.raw[src.stage] + warp_row * C::kCols + piece * 16 + odd * 8;
+        const int other = odd ? -8 : 8;
         uint8_t* out = sm.v[dst.stage];
-#pragma unroll 8
-        for (int j = 0; j < kPer; ++j) {
-          const int row = j * (128 / kPer) + ct / kPer;
-          const uint32_t bb = sm.scales[vs.stage][1][row >> shift][row & (box - 1)];
-          const uint2 u = *reinterpret_cast<const uint2*>(raw + row * C::kCols + piece * 8);
-          // the code's bits are the value times 2^-120: one multiply by 2^120 times the scale where
-          // that is a bf16 value, else two
-          const uint32_t f = bb <= 134 ? (bb + 120) << 7 : 0x7b80u, f2 = f | (f << 16);
-          uint32_t w[4];
-          w[0] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.x, 0, 0x1404)), f2);
-          w[1] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.x, 0, 0x3424)), f2);
-          w[2] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.y, 0, 0x1404)), f2);
-          w[3] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u.y, 0, 0x3424)), f2);
-          if (bb > 134) {
-            const uint32_t s = scale_bits(bb), s2 = s | (s << 16);
+        uint2 u[2] = {*reinterpret_cast<const uint2*>(raw), *reinterpret_cast<const uint2*>(raw + other)};
+#pragma unroll 1
+        for (int j = 0; j < kSteps; ++j) {
+          const int row = warp_row + j * kStep, src_lane = sub + j * kStep;
+          const uint32_t fr = __shfl_sync(0xffffffffu, f, src_lane), f2 = fr | (fr << 16);
+          uint2 next[2];
+          raw += j + 1 < kSteps ? kStep * C::kCols : 0;
+          next[0] = *reinterpret_cast<const uint2*>(raw);
+          next[1] = *reinterpret_cast<const uint2*>(raw + other);
+          uint32_t w[2][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = mul_bf16x2(w[e], s2);
+          for (int e = 0; e < 2; ++e) {
+            w[e][0] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].x, 0, 0x1404)), f2);
+            w[e][1] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].x, 0, 0x3424)), f2);
+            w[e][2] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].y, 0, 0x1404)), f2);
+            w[e][3] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].y, 0, 0x3424)), f2);
           }
-          *reinterpret_cast<uint4*>(out + (piece >> 3) * (TK * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          if (large) {
+            const uint32_t b2 = __shfl_sync(0xffffffffu, bb, src_lane);
+            const uint32_t s2 = b2 > 134 ? scale_bits(b2) | (scale_bits(b2) << 16) : 0x3f803f80u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k >> 2][k & 3] = mul_bf16x2(w[k >> 2][k & 3], s2);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int at = 2 * piece + (odd ^ e);
+            *reinterpret_cast<uint4*>(out + (at >> 3) * (TK * 128) + row * 128 + (((at & 7) ^ (row & 7)) << 4)) =
+                make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+            u[e] = next[e];
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -601,6 +624,14 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     RingPos<C::kKStages> kp, k_out;    // (two blocks) and hands their stages back, or block 1 does
     RingPos<C::kVStages> v_out, v_at;
     RingPos<Q8 ? C::kScales : 1> sp;   // 8-bit: the scales' ring
+    // 16-byte piece p of row rr of this warp's 32 rows in the queries' place: the rows that this warp
+    // loads, so warps do not meet in it
+    auto row_piece = [&](int rr, int p) {
+      constexpr bool kNarrow = Q8 && D == 64;                 // 64-byte query rows, in two parts
+      return reinterpret_cast<uint4*>(
+          sm.q[blk] + (kNarrow ? (p >> 2) * 8192 + (lbase + rr) * 64 + (((p & 3) ^ ((rr >> 1) & 3)) << 4)
+                               : (p >> 3) * 16384 + (lbase + rr) * 128 + (((p & 7) ^ (rr & 7)) << 4)));
+    };
     auto load_q = [&](const SegDesc& s) {
       // A warp loads its own 32 rows (lane i knows where row i is), D / 8 lanes a row at a time:
       // 16-byte pieces, swizzled, all in flight at once.
@@ -611,65 +642,63 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       const int mine = min(base + lane, s.tokens * a.g - 1);
       const int t = mine / a.g;
       const long long where = (s.row0 + t) * a.q_ld + (s.head * a.g + (mine - t * a.g)) * a.q_head_ld;
-      if constexpr (!Q8) {
-        const uint32_t dst = smem_u32(sm.q[blk]) + (piece >> 3) * (128 * 128) + lbase * 128;
 #pragma unroll 8
-        for (int j = 0; j < 32 / kStep; ++j) {
-          const int row = j * kStep + first;
-          const long long w = __shfl_sync(0xffffffffu, where, row);
-          cp_async16(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), a.q + w + piece * 8, row < rows);
-        }
-        cp_async_wait_all();
-      } else {
-        // the rows as two e4m3 parts (see split_e4m3)
-        constexpr int kBatch = 8;
+      for (int j = 0; j < 32 / kStep; ++j) {
+        const int row = j * kStep + first;
+        const long long w = __shfl_sync(0xffffffffu, where, row);
+        cp_async16(smem_u32(row_piece(row, piece)), a.q + w + piece * 8, row < rows);
+      }
+      cp_async_wait_all();
+      __syncwarp();
+      if constexpr (Q8) {
+        // the rows become their two e4m3 parts (see split_e4m3), which take the same place: a lane
+        // has its piece before the row's lanes write
+        constexpr int kBatch = 4;
+#pragma unroll 1
         for (int j0 = 0; j0 < 32 / kStep; j0 += kBatch) {
           uint4 u[kBatch];
 #pragma unroll
+          for (int j = 0; j < kBatch; ++j) u[j] = *row_piece((j0 + j) * kStep + first, piece);
+          uint32_t top[kBatch];
+#pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int row = (j0 + j) * kStep + first;
-            const long long w = __shfl_sync(0xffffffffu, where, row & 31);
-            u[j] = make_uint4(0, 0, 0, 0);
-            if (row < rows) u[j] = __ldg(reinterpret_cast<const uint4*>(a.q + w + piece * 8));
+            const uint32_t m = __vmaxu2(__vmaxu2(u[j].x & 0x7fff7fffu, u[j].y & 0x7fff7fffu),
+                                        __vmaxu2(u[j].z & 0x7fff7fffu, u[j].w & 0x7fff7fffu));
+            top[j] = max(m & 0xffffu, m >> 16);
           }
+          if constexpr (kPer == 32) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) top[j] = __reduce_max_sync(0xffffffffu, top[j]);
+          } else {
+#pragma unroll
+            for (int o = kPer / 2; o > 0; o >>= 1)
+#pragma unroll
+              for (int j = 0; j < kBatch; ++j) top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+          }
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int row = (j0 + j) * kStep + first;
-            const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = kPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int bb = scale_byte(top);
+            const int row = (j0 + j) * kStep + first, bb = scale_byte(top[j]);
             const float inv = __uint_as_float((uint32_t)(254 - (bb == 255 ? 127 : bb)) << 23);
+            const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               split_e4m3(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
-            if (row < 32) {
-              if (piece == 0) sm.q_scale[blk][lbase + row] = scale_f32(bb) * a.scale_log2;
-              const int col = piece * 8;                             // byte in the row
-              uint8_t* d = sm.q[blk] + (col >> 7) * (128 * 128) +
-                           (C::kCols == 128 ? (lbase + row) * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
-                                            : (lbase + row) * 64 + (((col >> 4) ^ ((row >> 1) & 3)) << 4)) + (col & 8);
-              *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-              *reinterpret_cast<uint2*>(d + C::kQBytes / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-            }
+            if (piece == 0) sm.q_scale[blk][lbase + row] = scale_f32(bb) * a.scale_log2;
+            const int col = piece * 8;                               // byte in the row
+            uint8_t* d = sm.q[blk] + (col >> 7) * (128 * 128) +
+                         (C::kCols == 128 ? (lbase + row) * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
+                                          : (lbase + row) * 64 + (((col >> 4) ^ ((row >> 1) & 3)) << 4)) + (col & 8);
+            *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(d + C::kQBytes / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
           }
+          __syncwarp();
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_ready[blk]);
-    };
-    // 16-byte piece p of row rr of this warp's 32 rows in the queries' place: the rows that this warp
-    // loads, so warps do not meet in it
-    auto row_piece = [&](int rr, int p) {
-      constexpr bool kNarrow = Q8 && D == 64;                 // 64-byte query rows, in two parts
-      return reinterpret_cast<uint4*>(
-          sm.q[blk] + (kNarrow ? (p >> 2) * 8192 + (lbase + rr) * 64 + (((p & 3) ^ ((rr >> 1) & 3)) << 4)
-                               : (p >> 3) * 16384 + (lbase + rr) * 128 + (((p & 7) ^ (rr & 7)) << 4)));
     };
     auto active = [&](const SegDesc& s) {
       return s.n > 0 && s.rows > 128 * blk;
@@ -728,6 +757,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
               }
             }
           }
+          if (Q8) wait_bar(&sm.s_ready[sp.stage], sp.phase, &sm.dead, c.status);
           wait_bar(&sm.s_full[buf], (C::kBlocks == 2 ? cnt : cnt >> 1) & 1u, &sm.dead, c.status);
           fence_after_sync();
           if (C::kBlocks == 2 && releases && warp == 4 * blk && lane == 0) {
@@ -742,26 +772,37 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           const bool partial = k0 + TK - 1 > pos_min;
           const int lim = pos - k0;                               // columns 0..lim are seen
           uint32_t v[128];
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) tmem_ld32_nw(s_addr + cc * 32, v + cc * 32);
-          tmem_wait_ld();
-#pragma unroll
-          for (int cc = 0; cc < 8; ++cc) reg_fence16(v + cc * 16);
           float scale = a.scale_log2;
-          if constexpr (Q8) {
-            // each key's scale here, the row's with the softmax scale below; a hidden key's scale
-            // may be anything, so hide after scaling
+          if constexpr (!Q8) {
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) tmem_ld32_nw(s_addr + cc * 32, v + cc * 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc) reg_fence16(v + cc * 16);
+          } else {
+            // each key's scale here, 32 keys at a time with the next scores under way; the row's with
+            // the softmax scale below; a hidden key's scale may be anything, so hide after scaling
             scale = sm.q_scale[blk][r];
-            wait_bar(&sm.s_ready[sp.stage], sp.phase, &sm.dead, c.status);
             const float4* f = reinterpret_cast<const float4*>(sm.k_scale[sp.stage]);
+            tmem_ld32_nw(s_addr, v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float4 g = f[e];
-              float y[4];
-              unpair(mul2(pair(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])), pair(g.x, g.y)), y[0], y[1]);
-              unpair(mul2(pair(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])), pair(g.z, g.w)), y[2], y[3]);
+            for (int cc = 0; cc < 4; ++cc) {
+              float4 g[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[4 * e + k] = __float_as_uint(y[k]);
+              for (int e = 0; e < 8; ++e) g[e] = f[cc * 8 + e];
+              tmem_wait_ld();
+              reg_fence16(v + cc * 32);
+              reg_fence16(v + cc * 32 + 16);
+              if (cc < 3) tmem_ld32_nw(s_addr + (cc + 1) * 32, v + (cc + 1) * 32);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                uint32_t* y = v + cc * 32 + 4 * e;
+                float z[4];
+                unpair(mul2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), pair(g[e].x, g[e].y)), z[0], z[1]);
+                unpair(mul2(pair(__uint_as_float(y[2]), __uint_as_float(y[3])), pair(g[e].z, g[e].w)), z[2], z[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __float_as_uint(z[k]);
+              }
             }
             sp.step();
           }
