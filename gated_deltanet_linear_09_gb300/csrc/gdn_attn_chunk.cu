@@ -43,7 +43,7 @@ struct ChunkCfg {
   static constexpr int kHalves = D / kCols;                 // stages of a K or V tile
   // K stages: bf16, or the e4m3 codes themselves; V stages: bf16; R stages: the codes of V
   static constexpr int kKBytes = kKeys * kCols * (Q8 ? 1 : 2), kVBytes = kKeys * kCols * 2, kRBytes = kKeys * kCols;
-  static constexpr int kKStages = D == 64 ? 4 : Q8 ? 3 : D == 128 ? 2 : 3;
+  static constexpr int kKStages = D == 64 ? 4 : Q8 ? (D == 256 ? 2 : 3) : D == 128 ? 2 : 3;
   static constexpr int kVStages = Q8 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
   static constexpr int kRStages = Q8 ? 2 : 0;
   // tiles whose scales are held: a tile's place is taken after the values of two tiles before it
@@ -52,16 +52,17 @@ struct ChunkCfg {
   static constexpr int kSoftWarps = 4 * kBlocks;
   static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kSchedWarp = kSoftWarps + 2, kConvWarp = kSoftWarps + 4;
   // whole warpgroups: softmax (one per block), control (MMA and TMA warps), conversion
-  static constexpr int kGroups = kBlocks + 1 + (Q8 ? 1 : 0);
+  static constexpr int kConvGroups = Q8 ? kHalves : 0;      // one for each half of a V tile
+  static constexpr int kGroups = kBlocks + 1 + kConvGroups;
   static constexpr int kThreads = kGroups * 128;
-  static constexpr int kReaders = kSoftWarps + 2 + (Q8 ? 4 : 0);   // warps that read a segment
+  static constexpr int kReaders = kSoftWarps + 2 + 4 * kConvGroups;   // warps that read a segment
   // registers per thread at launch (65,536 shared by the CTA's threads, in eights) and after the
   // warpgroups have traded: their sum over the warpgroups is the launch's
   static constexpr int kLaunchRegs = kGroups == 2 ? 255 : kGroups == 3 ? 168 : 128;
-  static constexpr int kSoftRegs = kGroups == 3 ? (Q8 ? 216 : 208) : kGroups == 4 ? 176 : 0;
-  static constexpr int kCtrlRegs = kGroups == 3 ? (Q8 ? 120 : 88) : kGroups == 4 ? 64 : 0;
-  static constexpr int kConvRegs = kGroups == 3 ? 168 : kGroups == 4 ? 96 : 0;
-  static_assert(kGroups == 2 || kBlocks * kSoftRegs + kCtrlRegs + (Q8 ? kConvRegs : 0) <= kGroups * kLaunchRegs,
+  static constexpr int kSoftRegs = kGroups == 2 ? 0 : kGroups == 3 ? 208 : kBlocks == 2 ? 176 : 216;
+  static constexpr int kCtrlRegs = kGroups == 2 ? 0 : kGroups == 3 ? 88 : kBlocks == 2 ? 64 : 88;
+  static constexpr int kConvRegs = kGroups < 4 ? 0 : kBlocks == 2 ? 96 : 104;
+  static_assert(kGroups == 2 || kBlocks * kSoftRegs + kCtrlRegs + kConvGroups * kConvRegs <= kGroups * kLaunchRegs,
                 "a share above the launch's registers would wait for ever");
   static constexpr int kQBytes = 128 * D * 2;               // one block
   static constexpr int kO = 256;                            // TMEM column of O (block b: + b D)
@@ -210,6 +211,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool f
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 // Position of a stage in the ring.
 template <int N>
 struct RingPos {
@@ -256,7 +262,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     }
     for (int i = 0; i < C::kScales; ++i) {
       mbar_init(&sm.s_bytes[i], 1);
-      mbar_init(&sm.s_free[i], 4);
+      mbar_init(&sm.s_free[i], 4 * C::kConvGroups);
       mbar_init(&sm.s_ready[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -528,7 +534,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   } else if (Q8 && warp >= C::kConvWarp) {
     // ---------------------------------------------------------------- e4m3 -> bf16
     if constexpr (C::kConvRegs && C::kConvRegs < C::kLaunchRegs) regs_down<C::kConvRegs>();
-    const int ct = tid - C::kConvWarp * 32;
+    const int ct = (tid - C::kConvWarp * 32) & 127, group = (warp - C::kConvWarp) >> 2;
     const int box = min(1 << c.page_shift, TK), shift = 31 - __clz(box);
     RingPos<Q8 ? C::kRStages : 1> src;
     RingPos<C::kVStages> dst;
@@ -536,9 +542,10 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     // A warp converts its own 32 rows, so that a row's multiplier comes from the lane that holds it.
     // A lane takes 16 codes of a row in two halves, the first of which differs from lane to lane so
     // that neither the 8-byte loads nor the 16-byte swizzled stores meet in a bank.  The loop is kept
-    // rolled, with the next row's loads ahead: unrolled eight times it does not fit an SM quarter's
-    // instruction cache next to the softmax, and both ran at a third of the speed (one prompt piece
-    // of 4096 on 16384 tokens, D = 256: 3147 us, rolled 1481 us).
+    // rolled (D = 256: two rows), with the next row's loads ahead: unrolled eight times it does not
+    // fit an SM quarter's instruction cache next to the softmax, and both ran at a third of the speed
+    // (one prompt piece of 4096 on 16384 tokens, D = 256 with one group: 3147 us, rolled 1481 us).
+    // A group of warps for each half of a V tile: 1481 -> 1388 us, two rows 1284 us.
     constexpr int kPer = C::kCols / 16, kStep = 32 / kPer, kSteps = 32 / kStep;
     const int piece = lane % kPer, sub = lane / kPer, warp_row = (ct >> 5) * 32 + sub;
     const int odd = kPer == 8 ? (piece >> 2) ^ (sub & 1) : (sub >> 1) & 1;
@@ -553,60 +560,64 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           // four tiles ago, which is over: a V stage of a later tile has come back since.
           if (half == 0) {
             wait_bar(&sm.s_bytes[ks.stage], ks.phase, &sm.dead, c.status);
-            sm.k_scale[ks.stage][ct] = scale_f32(sm.scales[ks.stage][0][ct >> shift][ct & (box - 1)]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_ready[ks.stage]);
+            if (group == 0) {
+              sm.k_scale[ks.stage][ct] = scale_f32(sm.scales[ks.stage][0][ct >> shift][ct & (box - 1)]);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.s_ready[ks.stage]);
+            }
             ks.step();
           }
           return;
         }
-        wait_bar(&sm.r_full[src.stage], src.phase, &sm.dead, c.status);
-        const uint32_t bb = sm.scales[vs.stage][1][ct >> shift][ct & (box - 1)];
-        // the code's bits are the value times 2^-120: one multiply by 2^120 times the scale where that
-        // is a bf16 value, else two
-        const uint32_t f = bb <= 134 ? (bb + 120) << 7 : 0x7b80u;
-        const bool large = __any_sync(0xffffffffu, bb > 134);
-        wait_bar(&sm.v_empty[dst.stage], dst.phase ^ 1u, &sm.dead, c.status);
-        const uint8_t* raw = sm.raw[src.stage] + warp_row * C::kCols + piece * 16 + odd * 8;
-        const int other = odd ? -8 : 8;
-        uint8_t* out = sm.v[dst.stage];
-        uint2 u[2] = {*reinterpret_cast<const uint2*>(raw), *reinterpret_cast<const uint2*>(raw + other)};
-#pragma unroll 1
-        for (int j = 0; j < kSteps; ++j) {
-          const int row = warp_row + j * kStep, src_lane = sub + j * kStep;
-          const uint32_t fr = __shfl_sync(0xffffffffu, f, src_lane), f2 = fr | (fr << 16);
-          uint2 next[2];
-          raw += j + 1 < kSteps ? kStep * C::kCols : 0;
-          next[0] = *reinterpret_cast<const uint2*>(raw);
-          next[1] = *reinterpret_cast<const uint2*>(raw + other);
-          uint32_t w[2][4];
+        if (half == group) {
+          wait_bar(&sm.r_full[src.stage], src.phase, &sm.dead, c.status);
+          const uint32_t bb = sm.scales[vs.stage][1][ct >> shift][ct & (box - 1)];
+          // the code's bits are the value times 2^-120: one multiply by 2^120 times the scale where that
+          // is a bf16 value, else two
+          const uint32_t f = bb <= 134 ? (bb + 120) << 7 : 0x7b80u;
+          const bool large = __any_sync(0xffffffffu, bb > 134);
+          wait_bar(&sm.v_empty[dst.stage], dst.phase ^ 1u, &sm.dead, c.status);
+          const uint8_t* raw = sm.raw[src.stage] + warp_row * C::kCols + piece * 16 + odd * 8;
+          const int other = odd ? -8 : 8;
+          uint8_t* out = sm.v[dst.stage];
+          uint2 u[2] = {*reinterpret_cast<const uint2*>(raw), *reinterpret_cast<const uint2*>(raw + other)};
+#pragma unroll (C::kConvGroups)
+          for (int j = 0; j < kSteps; ++j) {
+            const int row = warp_row + j * kStep, src_lane = sub + j * kStep;
+            const uint32_t fr = __shfl_sync(0xffffffffu, f, src_lane), f2 = fr | (fr << 16);
+            uint2 next[2];
+            raw += j + 1 < kSteps ? kStep * C::kCols : 0;
+            next[0] = *reinterpret_cast<const uint2*>(raw);
+            next[1] = *reinterpret_cast<const uint2*>(raw + other);
+            uint32_t w[2][4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            w[e][0] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].x, 0, 0x1404)), f2);
-            w[e][1] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].x, 0, 0x3424)), f2);
-            w[e][2] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].y, 0, 0x1404)), f2);
-            w[e][3] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].y, 0, 0x3424)), f2);
-          }
-          if (large) {
-            const uint32_t b2 = __shfl_sync(0xffffffffu, bb, src_lane);
-            const uint32_t s2 = b2 > 134 ? scale_bits(b2) | (scale_bits(b2) << 16) : 0x3f803f80u;
+            for (int e = 0; e < 2; ++e) {
+              w[e][0] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].x, 0, 0x1404)), f2);
+              w[e][1] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].x, 0, 0x3424)), f2);
+              w[e][2] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].y, 0, 0x1404)), f2);
+              w[e][3] = mul_bf16x2(e4m3_hi_bits(__byte_perm(u[e].y, 0, 0x3424)), f2);
+            }
+            if (large) {
+              const uint32_t b2 = __shfl_sync(0xffffffffu, bb, src_lane);
+              const uint32_t s2 = b2 > 134 ? scale_bits(b2) | (scale_bits(b2) << 16) : 0x3f803f80u;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k >> 2][k & 3] = mul_bf16x2(w[k >> 2][k & 3], s2);
-          }
+              for (int k = 0; k < 8; ++k) w[k >> 2][k & 3] = mul_bf16x2(w[k >> 2][k & 3], s2);
+            }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = 2 * piece + (odd ^ e);
-            *reinterpret_cast<uint4*>(out + (at >> 3) * (TK * 128) + row * 128 + (((at & 7) ^ (row & 7)) << 4)) =
-                make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
-            u[e] = next[e];
+            for (int e = 0; e < 2; ++e) {
+              const int at = 2 * piece + (odd ^ e);
+              *reinterpret_cast<uint4*>(out + (at >> 3) * (TK * 128) + row * 128 + (((at & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+              u[e] = next[e];
+            }
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.v_full[dst.stage]);
-          mbar_arrive(&sm.r_empty[src.stage]);
-          if (half == C::kHalves - 1) mbar_arrive(&sm.s_free[vs.stage]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.v_full[dst.stage]);
+            mbar_arrive(&sm.r_empty[src.stage]);
+            mbar_arrive(&sm.s_free[vs.stage]);
+          }
         }
         if (half == C::kHalves - 1) vs.step();
         src.step();
@@ -745,18 +756,21 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           // A parity wait tells a phase from the one before it only when no phase is skipped: so
           // block 0 waits for every stage of the rings, needed or not.  Its p_ready then tells the
           // MMA thread that V(i) (and, with two blocks, K(i + 1)) are there.
-          if (C::kBlocks == 2 && blk == 0) {
+          auto rings = [&]() {
+            if (C::kBlocks != 2 || blk != 0) return;
             v_at = vp;
             wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
             vp.step();
-            {
-              if (i == 0) kp.step();
-              if (i + 1 < n) {
-                wait_bar(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
-                kp.step();
-              }
+            if (i == 0) kp.step();
+            if (i + 1 < n) {
+              wait_bar(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
+              kp.step();
             }
-          }
+          };
+          // D = 128 waits after the exponentials, D = 64, which those bound, before the scores (4096
+          // tokens on 16384, before and after: bf16 D = 128 890 and 847 us, D = 64 683 and 749; 8-bit
+          // D = 128 1160 and 1107 us, D = 64 922 and 978)
+          if (D == 64) rings();
           if (Q8) wait_bar(&sm.s_ready[sp.stage], sp.phase, &sm.dead, c.status);
           wait_bar(&sm.s_full[buf], (C::kBlocks == 2 ? cnt : cnt >> 1) & 1u, &sm.dead, c.status);
           fence_after_sync();
@@ -771,52 +785,70 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           const int k0 = (ta + i) * TK;
           const bool partial = k0 + TK - 1 > pos_min;
           const int lim = pos - k0;                               // columns 0..lim are seen
-          uint32_t v[128];
-          float scale = a.scale_log2;
-          if constexpr (!Q8) {
+          // One block: S has two buffers, so the products run ahead and the scores are read twice, 32 at
+          // a time in rolled loops, which leaves the instruction cache to the conversion (D = 256, 4096
+          // tokens on 16384: 1388 -> 1219 us).  Two blocks: a block's products wait for its softmax, so
+          // it reads them once into registers (read twice, D = 128: 1107 -> 1411 us).
+          constexpr bool kTwice = Q8 && C::kBlocks == 1;
+          uint32_t v[kTwice ? 32 : 128];
+          float xs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const float scale = Q8 ? sm.q_scale[blk][r] : a.scale_log2;
+          // 8-bit: n / 32 scores of 32, each times its key's scale (the row's is in the softmax scale)
+          // with the next 32 under way; a hidden key's scale may be anything, so hide after scaling
+          auto scores = [&](int first, auto count) {
+            constexpr int kCount = decltype(count)::value;
+            if constexpr (!Q8) {
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) tmem_ld32_nw(s_addr + cc * 32, v + cc * 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int cc = 0; cc < 8; ++cc) reg_fence16(v + cc * 16);
-          } else {
-            // each key's scale here, 32 keys at a time with the next scores under way; the row's with
-            // the softmax scale below; a hidden key's scale may be anything, so hide after scaling
-            scale = sm.q_scale[blk][r];
-            const float4* f = reinterpret_cast<const float4*>(sm.k_scale[sp.stage]);
-            tmem_ld32_nw(s_addr, v);
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              float4 g[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) g[e] = f[cc * 8 + e];
+              for (int cc = 0; cc < kCount; ++cc) tmem_ld32_nw(s_addr + cc * 32, v + cc * 32);
               tmem_wait_ld();
-              reg_fence16(v + cc * 32);
-              reg_fence16(v + cc * 32 + 16);
-              if (cc < 3) tmem_ld32_nw(s_addr + (cc + 1) * 32, v + (cc + 1) * 32);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                uint32_t* y = v + cc * 32 + 4 * e;
-                float z[4];
-                unpair(mul2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), pair(g[e].x, g[e].y)), z[0], z[1]);
-                unpair(mul2(pair(__uint_as_float(y[2]), __uint_as_float(y[3])), pair(g[e].z, g[e].w)), z[2], z[3]);
+              for (int cc = 0; cc < 2 * kCount; ++cc) reg_fence16(v + cc * 16);
+            } else {
+              const float4* f = reinterpret_cast<const float4*>(sm.k_scale[sp.stage] + first);
+              tmem_ld32_nw(s_addr + first, v);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __float_as_uint(z[k]);
+              for (int cc = 0; cc < kCount; ++cc) {
+                float4 g[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] = f[cc * 8 + e];
+                tmem_wait_ld();
+                reg_fence16(v + cc * 32);
+                reg_fence16(v + cc * 32 + 16);
+                if (cc + 1 < kCount) tmem_ld32_nw(s_addr + first + (cc + 1) * 32, v + (cc + 1) * 32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  uint32_t* y = v + cc * 32 + 4 * e;
+                  float z[4];
+                  unpair(mul2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), pair(g[e].x, g[e].y)), z[0], z[1]);
+                  unpair(mul2(pair(__uint_as_float(y[2]), __uint_as_float(y[3])), pair(g[e].z, g[e].w)), z[2], z[3]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) y[k] = __float_as_uint(z[k]);
+                }
               }
             }
-            sp.step();
+            if (partial) {
+#pragma unroll
+              for (int e = 0; e < 32 * kCount; ++e)
+                if (first + e > lim) v[e] = 0xff800000u;
+            }
+          };
+          auto maxima = [&](int n) {
+#pragma unroll
+            for (int e = 0; e < n; e += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                xs[j] = fmaxf(xs[j], fmaxf(__uint_as_float(v[e + 2 * j]), __uint_as_float(v[e + 2 * j + 1])));
+          };
+          if constexpr (kTwice) {
+#pragma unroll 1
+            for (int k = 0; k < TK; k += 32) {
+              scores(k, Int<1>{});
+              maxima(32);
+            }
+          } else {
+            scores(0, Int<4>{});
+            maxima(TK);
           }
-          if (partial) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e > lim) v[e] = 0xff800000u;
-          }
-          float xs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 128; e += 8)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              xs[j] = fmaxf(xs[j], fmaxf(__uint_as_float(v[e + 2 * j]), __uint_as_float(v[e + 2 * j + 1])));
           const float x = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])) * scale;
           if (__any_sync(0xffffffffu, x > m + 8.f)) {
             const float mn = fmaxf(m, x);
@@ -841,27 +873,38 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pair(scale, scale), ref2 = pair(-ref, -ref);
           uint64_t l2[2] = {pair(l, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
+          auto exps = [&](const uint32_t* y, uint32_t at) {        // of 16 scores
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const int j = cc * 16 + 2 * e;
               float p0, p1;
-              unpair(fma2(pair(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, ref2), p0, p1);
+              unpair(fma2(pair(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), sc2, ref2), p0, p1);
               p0 = ex2f(p0);
               p1 = ex2f(p1);
               l2[e & 1] = add2(l2[e & 1], pair(p0, p1));
               w[e] = pack2(p0, p1);
             }
-            tmem_st8w_nw(s_addr + cc * 8, w);
+            tmem_st8w_nw(at, w);
+          };
+          if constexpr (kTwice) {
+#pragma unroll 1
+            for (int k = 0; k < TK; k += 32) {
+              scores(k, Int<1>{});
+              exps(v, s_addr + k / 2);                             // the columns of scores read before
+              exps(v + 16, s_addr + k / 2 + 8);
+            }
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc) exps(v + cc * 16, s_addr + cc * 8);
           }
+          if (Q8) sp.step();
           {
             float l0, l1, l3, l4;
             unpair(l2[0], l0, l1);
             unpair(l2[1], l3, l4);
             l = (l0 + l1) + (l3 + l4);
           }
+          if (D != 64) rings();
           // for its parity's sake every tile: one block's s_full does not imply the product before
           if (C::kBlocks == 1 && i > 0) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
           if (C::kBlocks == 1) {         // (one block: two V stages hold one tile, which comes late)
