@@ -383,7 +383,9 @@ __device__ __forceinline__ void row_of(const SeqInfo& s, int g, int h, int r, in
   *head = h * g + (r - t * g);
 }
 
-__device__ __forceinline__ float gate_of(float x) { return 1.0f / (1.0f + __expf(-x)); }
+// sigmoid, to a few units of f32 (zero below -87); its product is rounded to bf16.  With an IEEE
+// division the gate took a third of a mixed batch's time (D = 256, 2720 tokens: 205 us, so 146 us).
+__device__ __forceinline__ float gate_of(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 // Writes 4 consecutive output elements (d a multiple of 4), gated.
 __device__ __forceinline__ void store_out4(const AttnArgs& a, int D, int tok, int head, int d, float4 o) {
