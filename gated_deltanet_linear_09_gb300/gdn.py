@@ -199,6 +199,11 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def stream_handle(stream=None) -> int:
+    """The cudaStream_t of a torch stream (None: the current one)."""
+    return _stream(stream)
+
+
 def act_code(dtype) -> int:
     if dtype == torch.bfloat16:
         return GDN_BF16

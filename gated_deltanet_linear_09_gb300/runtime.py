@@ -269,15 +269,16 @@ class PagedKVCache:
         self.c = gdn.make_kv_cache(k_pages, v_pages, k_scales, v_scales, self.status)
         self._ws = {}
 
-    def workspace(self, num_q_heads: int) -> torch.Tensor:
-        """The attention's workspace for this many query heads (one per cache and stream: calls that
-        overlap need their own, see attend's argument)."""
-        ws = self._ws.get(num_q_heads)
+    def workspace(self, num_q_heads: int, stream=None) -> torch.Tensor:
+        """The attention's workspace for this many query heads on this stream.  Calls on one stream
+        share it; a call that may overlap one of another stream has that stream's."""
+        key = (num_q_heads, gdn.stream_handle(stream))
+        ws = self._ws.get(key)
         if ws is None:
             need = gdn.gdn_paged_attention_workspace_bytes(self.c, num_q_heads)
             if need == 0:
                 raise ValueError(f"{num_q_heads} query heads over this cache are not supported")
-            ws = self._ws[num_q_heads] = torch.empty(need, dtype=torch.uint8, device=self.k_pages.device)
+            ws = self._ws[key] = torch.empty(need, dtype=torch.uint8, device=self.k_pages.device)
         return ws
 
     def _check(self, t, batch, what):
@@ -321,9 +322,8 @@ class PagedKVCache:
         elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
             raise ValueError("out: contiguous bf16 with the shape of q")
         if batch.total_tokens:
+            stream = gdn.stream_handle(stream)
             if workspace is None:
-                workspace = self._ws.get(shape[1])
-                if workspace is None:
-                    workspace = self.workspace(shape[1])
+                workspace = self.workspace(shape[1], stream)
             gdn.gdn_paged_attention(self.c, batch.c, q, out, workspace, gate, scale, stream)
         return out
