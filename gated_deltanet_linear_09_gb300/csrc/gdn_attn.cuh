@@ -396,9 +396,13 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, int D, int tok, in
   Act<__nv_bfloat16>::store4(a.out + ((long long)tok * a.Hq + head) * D + d, o);
 }
 
-// Zeros in the padding rows past the last sequence.
-__device__ __forceinline__ void zero_padding(const AttnArgs& a, const KvBatchView& b, int D) {
-  const int end = b.num_seqs > 0 ? __ldg(b.cu + b.num_seqs) : 0;
+// Where the padding rows past the last sequence begin (loaded early, used late).
+__device__ __forceinline__ int padding_begin(const KvBatchView& b) {
+  return b.num_seqs > 0 ? __ldg(b.cu + b.num_seqs) : 0;
+}
+
+// Zeros in them.
+__device__ __forceinline__ void zero_padding(const AttnArgs& a, const KvBatchView& b, int D, int end) {
   if (end < 0 || end >= b.total) return;
   const long long n = (long long)(b.total - end) * a.Hq * (D / 8);
   uint4* p = reinterpret_cast<uint4*>(a.out + (long long)end * a.Hq * D);

@@ -34,48 +34,51 @@ using namespace tc;
 namespace attn {
 
 constexpr int kKeys = 128;         // keys of a tile
-template <int D, bool Q8>
+// B: 128-row query blocks.  One where TMEM holds no more (D = 256), or where a tile has no rows for
+// two: S then has two buffers, so that the products of one key tile run beside the softmax of another.
+template <int D, bool Q8, int B>
 struct ChunkCfg {
-  static constexpr int kBlocks = D == 256 ? 1 : 2;          // 128-row query blocks
-  static constexpr int kSBufs = D == 256 ? 2 : 1;           // S buffers per block
+  static_assert(B == 1 || (B == 2 && D < 256), "TMEM: S and O of each block");
+  static constexpr int kBlocks = B;
   static constexpr int kRows = 128 * kBlocks;
   static constexpr int kCols = D == 64 ? 64 : 128;          // columns of a ring stage
   static constexpr int kHalves = D / kCols;                 // stages of a K or V tile
   // K stages: bf16, or the e4m3 codes themselves; V stages: bf16; R stages: the codes of V
   static constexpr int kKBytes = kKeys * kCols * (Q8 ? 1 : 2), kVBytes = kKeys * kCols * 2, kRBytes = kKeys * kCols;
-  static constexpr int kKStages = D == 64 ? 4 : Q8 ? (D == 256 ? 2 : 3) : D == 128 ? 2 : 3;
-  static constexpr int kVStages = Q8 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
-  static constexpr int kRStages = Q8 ? 2 : 0;
+  static constexpr int kKStages = D == 64 ? (B == 1 ? 6 : 4) : Q8 ? (D == 256 ? 2 : B == 1 ? 4 : 3) : D == 128 && B == 2 ? 2 : 3;
+  static constexpr int kVStages = Q8 ? 2 : D == 64 ? (B == 1 ? 6 : 4) : D == 128 && B == 2 ? 3 : 2;
+  static constexpr int kRStages = !Q8 ? 0 : B == 1 && D < 256 ? 3 : 2;
   // tiles whose scales are held: a tile's place is taken after the values of two tiles before it
   // have been converted, which with two V stages means that four before it are through
   static constexpr int kScales = Q8 ? 4 : 0;
   static constexpr int kSoftWarps = 4 * kBlocks;
-  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kSchedWarp = kSoftWarps + 2, kConvWarp = kSoftWarps + 4;
+  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kSchedWarp = kSoftWarps + 2, kLoadVWarp = kSoftWarps + 3,
+                       kConvWarp = kSoftWarps + 4;
   // whole warpgroups: softmax (one per block), control (MMA and TMA warps), conversion
   static constexpr int kConvGroups = Q8 ? kHalves : 0;      // one for each half of a V tile
   static constexpr int kGroups = kBlocks + 1 + kConvGroups;
   static constexpr int kThreads = kGroups * 128;
-  static constexpr int kReaders = kSoftWarps + 2 + 4 * kConvGroups;   // warps that read a segment
+  static constexpr int kReaders = kSoftWarps + 3 + 4 * kConvGroups;   // warps that read a segment
   // registers per thread at launch (65,536 shared by the CTA's threads, in eights) and after the
   // warpgroups have traded: their sum over the warpgroups is the launch's
   static constexpr int kLaunchRegs = kGroups == 2 ? 255 : kGroups == 3 ? 168 : 128;
-  static constexpr int kSoftRegs = kGroups == 2 ? 0 : kGroups == 3 ? 208 : kBlocks == 2 ? 176 : 216;
-  static constexpr int kCtrlRegs = kGroups == 2 ? 0 : kGroups == 3 ? 88 : kBlocks == 2 ? 64 : 88;
-  static constexpr int kConvRegs = kGroups < 4 ? 0 : kBlocks == 2 ? 96 : 104;
-  static_assert(kGroups == 2 || kBlocks * kSoftRegs + kCtrlRegs + kConvGroups * kConvRegs <= kGroups * kLaunchRegs,
+  static constexpr int kSoftRegs = kGroups == 2 ? 0 : kGroups == 3 ? 208 : B == 2 ? 176 : 216;
+  static constexpr int kCtrlRegs = kGroups == 2 ? 0 : kGroups == 3 ? 88 : B == 2 ? 64 : 88;
+  static constexpr int kConvRegs = kGroups == 3 ? 168 : B == 2 ? 96 : 104;
+  static_assert(kGroups == 2 || B * kSoftRegs + kCtrlRegs + kConvGroups * kConvRegs <= kGroups * kLaunchRegs,
                 "a share above the launch's registers would wait for ever");
   static constexpr int kQBytes = 128 * D * 2;               // one block
   static constexpr int kO = 256;                            // TMEM column of O (block b: + b D)
 };
 
-template <int D, bool Q8>
+template <int D, bool Q8, int B>
 struct __align__(1024) ChunkSmem {
-  using C = ChunkCfg<D, Q8>;
+  using C = ChunkCfg<D, Q8, B>;
   uint8_t q[C::kBlocks][C::kQBytes];
   uint8_t k[C::kKStages][C::kKBytes];
   uint8_t v[C::kVStages][C::kVBytes];
   uint8_t raw[Q8 ? C::kRStages : 1][Q8 ? C::kRBytes : 128];
-  uint8_t scales[Q8 ? C::kScales : 1][2][Q8 ? 8 : 1][128];   // bytes of a tile's keys and values, by page
+  uint8_t scales[Q8 ? C::kScales : 1][2][kKeys];             // bytes of a tile's keys and values
   float k_scale[Q8 ? C::kScales : 1][kKeys];
   float q_scale[C::kBlocks][Q8 ? 128 : 1];
   LineScan<C::kRows, C::kThreads> scan;
@@ -209,6 +212,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
 }
+// An arrival once this thread's copies so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
 template <int N>
@@ -238,14 +245,14 @@ __device__ __forceinline__ void ring_order(int n, F f) {
   }
 }
 
-template <int D, bool Q8>
-__global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1)
+template <int D, bool Q8, int B>
+__global__ void __launch_bounds__(ChunkCfg<D, Q8, B>::kThreads, 1)
 chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, int least,
              const __grid_constant__ KvMaps maps) {
-  using C = ChunkCfg<D, Q8>;
+  using C = ChunkCfg<D, Q8, B>;
   constexpr int R = C::kRows, TK = kKeys;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  ChunkSmem<D, Q8>& sm = *reinterpret_cast<ChunkSmem<D, Q8>*>(smem_raw);
+  ChunkSmem<D, Q8, B>& sm = *reinterpret_cast<ChunkSmem<D, Q8, B>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
@@ -261,7 +268,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       mbar_init(&sm.r_empty[i], 4);
     }
     for (int i = 0; i < C::kScales; ++i) {
-      mbar_init(&sm.s_bytes[i], 1);
+      mbar_init(&sm.s_bytes[i], 16);
       mbar_init(&sm.s_free[i], 4 * C::kConvGroups);
       mbar_init(&sm.s_ready[i], 4);
     }
@@ -281,11 +288,12 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   }
   for (int i = tid; i < D; i += C::kThreads) sm.bad[i] = INT32_MAX;
   pdl_begin();
-  zero_padding(a, b, D);
+  const int padding = padding_begin(b);
   bool bad_len = false;
   Pieces pieces;
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad_len);
+  zero_padding(a, b, D, padding);
   if (bad_len) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
   if (cta >= pieces.count) {
     if (tid == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, nullptr, 0);
@@ -313,7 +321,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   };
   RingPos<kSegs> seg;
 
-  // All four warps of the control warpgroup (one is idle) give their registers up together.
+  // All four warps of the control warpgroup give their registers up together.
   if (C::kGroups > 2 && warp >= C::kMmaWarp && warp < C::kConvWarp) regs_down<C::kCtrlRegs ? C::kCtrlRegs : 24>();
   if (warp == C::kSchedWarp) {
     // ---------------------------------------------------------------- segments
@@ -336,8 +344,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     }
     // the piece's last tile may be shared with the next ones
     if (lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &s, s.split ? it.sharing(s.nt) : 0);
-  } else if (warp == C::kLoadWarp) {
+  } else if (warp == C::kLoadWarp || warp == C::kLoadVWarp) {
     // ---------------------------------------------------------------- TMA
+    // Copies of one warp go out one after another (some 150 cycles each), hence a warp for the keys
+    // and one for the values (64 sequences of 8000, pages of 16, D = 128, bf16: 359 us with one, 322 us).
+    const bool values = warp == C::kLoadVWarp;
     const int box = min(1 << c.page_shift, TK);            // keys of one copy
     constexpr int kBoxCols = Q8 ? C::kCols : 64;
     constexpr int kBlk = C::kCols / kBoxCols;
@@ -365,41 +376,43 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         }
         return p;
       };
-      int p_cur = 0, p_next = lookup(0), p_ahead = lookup(1);   // pages of tiles i, i + 1, i + 2
-      ring_order<C::kHalves>(n, [&](bool is_v, int i, int half) {
-        if (!is_v && half == 0 && i > 0) {
-          p_cur = p_next;
-          p_next = p_ahead;
-          p_ahead = lookup(i + 1);
-        }
-        // K tiles run one ahead of V tiles; after the last K tile V is the newest tile
-        const int page = !is_v ? p_next : (i + 1 < n ? p_cur : p_next);
+      int p_next = lookup(0), p_ahead = lookup(1);          // pages of tiles i + 1, i + 2
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int page = p_next;
+        p_next = p_ahead;
+        p_ahead = lookup(i + 2);
         const int off = (((ta + i) * TK) & ((1 << c.page_shift) - 1));   // 0 unless pages exceed a tile
-        if (Q8 && !is_v && half == 0) {                     // the tile's scale bytes, keys and values
+        if (Q8 && !values) {                                // the tile's scale bytes, keys and values
           wait_bar(&sm.s_free[sp.stage], sp.phase ^ 1u, &sm.dead, c.status);
-          if (lane == 0) mbar_arrive_expect_tx(&sm.s_bytes[sp.stage], 2 * TK);
-          __syncwarp();
-          if (lane < pages) {
-            tma_load_3d(sm.scales[sp.stage][0][lane], &maps.ks, off, head, page, &sm.s_bytes[sp.stage]);
-            tma_load_3d(sm.scales[sp.stage][1][lane], &maps.vs, off, head, page, &sm.s_bytes[sp.stage]);
+          const int key = (lane & 7) * 16, at = key & (box - 1);
+          const int p = __shfl_sync(0xffffffffu, page, (key / box) * kBlk);
+          const uint8_t* src = (lane & 8 ? c.vs : c.ks) + (((long long)p * c.H + head) << c.page_shift) + off + at;
+          if (lane < 16) {
+            const bool there = p < c.num_pages;             // zeros if not
+            cp_async16(smem_u32(sm.scales[sp.stage][lane >> 3] + key), there ? src : c.ks, there);
+            cp_async_arrive(&sm.s_bytes[sp.stage]);
           }
           __syncwarp();
           sp.step();
         }
-        uint64_t* full = is_v ? &v_full[vp.stage] : &sm.k_full[kp.stage];
-        if (is_v) wait_bar(&v_empty[vp.stage], vp.phase ^ 1u, &sm.dead, c.status);
-        else wait_bar(&sm.k_empty[kp.stage], kp.phase ^ 1u, &sm.dead, c.status);
-        if (lane == 0) mbar_arrive_expect_tx(full, is_v ? (Q8 ? C::kRBytes : C::kVBytes) : C::kKBytes);
-        __syncwarp();
-        if (my_page < pages) {
-          uint8_t* dst = is_v ? (Q8 ? sm.raw[vp.stage] : sm.v[vp.stage]) : sm.k[kp.stage];
-          dst += Q8 ? my_page * box * C::kCols : my_blk * (TK * 128) + my_page * box * 128;
-          tma_load_5d(dst, is_v ? &maps.v : &maps.k, 0, off, half * kBlk + my_blk, head, page, full);
+#pragma unroll
+        for (int half = 0; half < C::kHalves; ++half) {
+          uint64_t* full = values ? &v_full[vp.stage] : &sm.k_full[kp.stage];
+          if (values) wait_bar(&v_empty[vp.stage], vp.phase ^ 1u, &sm.dead, c.status);
+          else wait_bar(&sm.k_empty[kp.stage], kp.phase ^ 1u, &sm.dead, c.status);
+          if (lane == 0) mbar_arrive_expect_tx(full, values ? (Q8 ? C::kRBytes : C::kVBytes) : C::kKBytes);
+          __syncwarp();
+          if (my_page < pages) {
+            uint8_t* dst = values ? (Q8 ? sm.raw[vp.stage] : sm.v[vp.stage]) : sm.k[kp.stage];
+            dst += Q8 ? my_page * box * C::kCols : my_blk * (TK * 128) + my_page * box * 128;
+            tma_load_5d(dst, values ? &maps.v : &maps.k, 0, off, half * kBlk + my_blk, head, page, full);
+          }
+          __syncwarp();
+          if (values) vp.step();
+          else kp.step();
         }
-        __syncwarp();
-        if (is_v) vp.step();
-        else kp.step();
-      });
+      }
     }
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA (one thread)
@@ -533,9 +546,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     __syncwarp();
   } else if (Q8 && warp >= C::kConvWarp) {
     // ---------------------------------------------------------------- e4m3 -> bf16
-    if constexpr (C::kConvRegs && C::kConvRegs < C::kLaunchRegs) regs_down<C::kConvRegs>();
+    if constexpr (C::kConvRegs < C::kLaunchRegs) regs_down<C::kConvRegs>();
     const int ct = (tid - C::kConvWarp * 32) & 127, group = (warp - C::kConvWarp) >> 2;
-    const int box = min(1 << c.page_shift, TK), shift = 31 - __clz(box);
     RingPos<Q8 ? C::kRStages : 1> src;
     RingPos<C::kVStages> dst;
     RingPos<Q8 ? C::kScales : 1> ks, vs;
@@ -548,7 +560,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     // A group of warps for each half of a V tile: 1481 -> 1388 us, two rows 1284 us.
     constexpr int kPer = C::kCols / 16, kStep = 32 / kPer, kSteps = 32 / kStep;
     const int piece = lane % kPer, sub = lane / kPer, warp_row = (ct >> 5) * 32 + sub;
-    constexpr int kUnroll = C::kConvGroups == 2 ? 2 : 1;
+    constexpr int kUnroll = D == 256 ? 2 : 1;
     const int odd = kPer == 8 ? (piece >> 2) ^ (sub & 1) : (sub >> 1) & 1;
     while (true) {
       const int n = seg_wait(seg).n;
@@ -562,7 +574,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           if (half == 0) {
             wait_bar(&sm.s_bytes[ks.stage], ks.phase, &sm.dead, c.status);
             if (group == 0) {
-              sm.k_scale[ks.stage][ct] = scale_f32(sm.scales[ks.stage][0][ct >> shift][ct & (box - 1)]);
+              sm.k_scale[ks.stage][ct] = scale_f32(sm.scales[ks.stage][0][ct]);
               __syncwarp();
               if (lane == 0) mbar_arrive(&sm.s_ready[ks.stage]);
             }
@@ -572,7 +584,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         }
         if (half == group) {
           wait_bar(&sm.r_full[src.stage], src.phase, &sm.dead, c.status);
-          const uint32_t bb = sm.scales[vs.stage][1][ct >> shift][ct & (box - 1)];
+          const uint32_t bb = sm.scales[vs.stage][1][ct];
           // the code's bits are the value times 2^-120: one multiply by 2^120 times the scale where that
           // is a bf16 value, else two
           const uint32_t f = bb <= 134 ? (bb + 120) << 7 : 0x7b80u;
@@ -790,7 +802,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           // a time in rolled loops, which leaves the instruction cache to the conversion (D = 256, 4096
           // tokens on 16384: 1388 -> 1219 us).  Two blocks: a block's products wait for its softmax, so
           // it reads them once into registers (read twice, D = 128: 1107 -> 1411 us).
-          constexpr bool kTwice = Q8 && C::kBlocks == 1;
+          constexpr bool kTwice = Q8 && D == 256;
           uint32_t v[kTwice ? 32 : 128];
           float xs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           const float scale = Q8 ? sm.q_scale[blk][r] : a.scale_log2;
@@ -1066,13 +1078,13 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int B>
 int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
-  using C = ChunkCfg<D, Q8>;
-  constexpr size_t smem = sizeof(ChunkSmem<D, Q8>);
+  using C = ChunkCfg<D, Q8, B>;
+  constexpr size_t smem = sizeof(ChunkSmem<D, Q8, B>);
   static_assert(smem <= 232448, "shared memory of a CTA");
   static const cudaError_t set = cudaFuncSetAttribute(
-      chunk_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      chunk_kernel<D, Q8, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (set != cudaSuccess) return GDN_ERR_CUDA;
   KvMaps maps;
   const int P = 1 << c.page_shift;
@@ -1081,23 +1093,30 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   // at 256, 116 at 512, 110 at 1024), and the fewest keys worth a piece of their own.
   const int grid = sms, fix = 1024 * a.g;
   const int least = 512 * a.g;
-  int rc = launch_dependent(chunk_kernel<D, Q8>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
+  int rc = launch_dependent(chunk_kernel<D, Q8, B>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
   return launch_dependent(merge_kernel<C::kRows, D>, dim3((unsigned)(6 * sms)), kMergeWarps * 32, 0, stream, a, grid);
 }
 
 size_t chunk_ws_bytes(int D, int sms) {
-  return D == 64 ? Partials<ChunkCfg<64, false>::kRows, 64>::bytes(sms)
-       : D == 128 ? Partials<ChunkCfg<128, false>::kRows, 128>::bytes(sms)
-                  : Partials<ChunkCfg<256, false>::kRows, 256>::bytes(sms);
+  return D == 64 ? Partials<256, 64>::bytes(sms)
+       : D == 128 ? Partials<256, 128>::bytes(sms)
+                  : Partials<128, 256>::bytes(sms);
+}
+
+template <int D, int B>
+int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
+  return c.ks != nullptr ? launch_chunk<D, true, B>(c, b, a, sms, stream) : launch_chunk<D, false, B>(c, b, a, sms, stream);
 }
 
 int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sms, cudaStream_t stream) {
-  const bool q8 = c.ks != nullptr;
-  if (c.D == 64) return q8 ? launch_chunk<64, true>(c, b, a, sms, stream) : launch_chunk<64, false>(c, b, a, sms, stream);
-  if (c.D == 128) return q8 ? launch_chunk<128, true>(c, b, a, sms, stream) : launch_chunk<128, false>(c, b, a, sms, stream);
-  return q8 ? launch_chunk<256, true>(c, b, a, sms, stream) : launch_chunk<256, false>(c, b, a, sms, stream);
+  // One block where no tile has rows for a second (64 sequences of 8 tokens and 8000 keys, 32 rows:
+  // bf16 D = 128 374 us with two, 359 with one; 8-bit 464 and 426).
+  const bool one = (long long)(b.max_tokens > 0 ? b.max_tokens : b.total) * a.g <= 128;
+  if (c.D == 64) return one ? launch_chunk<64, 1>(c, b, a, sms, stream) : launch_chunk<64, 2>(c, b, a, sms, stream);
+  if (c.D == 128) return one ? launch_chunk<128, 1>(c, b, a, sms, stream) : launch_chunk<128, 2>(c, b, a, sms, stream);
+  return launch_chunk<256, 1>(c, b, a, sms, stream);
 }
 
 }  // namespace attn

@@ -37,30 +37,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// The maps of keys and values (same geometry) and of an 8-bit cache's scale bytes.
+// The maps of keys and values (same geometry).
 bool encode_all(const KvView& c, PFN_cuTensorMapEncodeTiled_v12000 encode, const cuuint64_t* dims,
-                const cuuint64_t* strides, const cuuint32_t* box, int rows, CUtensorMapSwizzle swizzle_k,
+                const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle_k,
                 CUtensorMapSwizzle swizzle_v, KvMaps* maps) {
   const bool q8 = c.ks != nullptr;
-  const uint64_t P = 1ull << c.page_shift;
   const cuuint32_t one[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < 2; ++i)
     if (encode(i ? &maps->v : &maps->k, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
                i ? c.v : c.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, i ? swizzle_v : swizzle_k,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return false;
-  if (!q8) {
-    maps->ks = maps->k;
-    maps->vs = maps->v;
-    return true;
-  }
-  const cuuint64_t sdims[3] = {P, (cuuint64_t)c.H, (cuuint64_t)c.num_pages};
-  const cuuint64_t sstrides[2] = {P, c.H * P};
-  const cuuint32_t sbox[3] = {(cuuint32_t)rows, 1, 1};
-  for (int i = 0; i < 2; ++i)
-    if (encode(i ? &maps->vs : &maps->ks, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, i ? c.vs : c.ks, sdims, sstrides, sbox,
-               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
   return true;
 }
@@ -77,7 +63,7 @@ bool make_tile_maps(const KvView& c, int rows, int cols, KvMaps* maps) {
   const cuuint64_t strides[4] = {row, span, P * row, c.H * P * row};
   const cuuint32_t box[5] = {(cuuint32_t)cols, (cuuint32_t)rows, 1, 1, 1};
   const CUtensorMapSwizzle swizzle = span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  return encode_all(c, encode, dims, strides, box, rows, swizzle, q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzle, maps);
+  return encode_all(c, encode, dims, strides, box, swizzle, q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzle, maps);
 }
 
 bool make_kv_maps(const KvView& c, int rows, KvMaps* maps) {
@@ -90,7 +76,7 @@ bool make_kv_maps(const KvView& c, int rows, KvMaps* maps) {
   const cuuint64_t strides[4] = {row, span, P * row, c.H * P * row};
   const cuuint32_t box[5] = {(cuuint32_t)(span / elem), (cuuint32_t)rows, (cuuint32_t)(row / span), 1, 1};
   const CUtensorMapSwizzle swizzle = span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  return encode_all(c, encode, dims, strides, box, rows, swizzle, swizzle, maps);
+  return encode_all(c, encode, dims, strides, box, swizzle, swizzle, maps);
 }
 
 size_t attn_ws_bytes(const KvView& c, int) {

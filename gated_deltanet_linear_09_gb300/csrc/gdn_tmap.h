@@ -10,7 +10,7 @@ namespace gdn {
 
 // Keys, values and (8-bit caches) their scale bytes.
 struct KvMaps {
-  CUtensorMap k, v, ks, vs;
+  CUtensorMap k, v;
 };
 
 // Maps whose box is `rows` keys of one page and head, all of head_dim: [D-blocks][rows][128 bytes]
@@ -40,14 +40,6 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];\n" ::"r"(
           smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(x4)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x0, int x1, int x2,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(x0), "r"(x1), "r"(x2)
       : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {

@@ -82,6 +82,16 @@ def test_long_sequence_is_split(dim, quantised):
     _check(case, 4)
 
 
+@pytest.mark.parametrize("new", [3, 5, 15, 16, 17])
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_around_a_block(dim, quantised, new):
+    """Between 17 and 136 rows under a key/value head, from one tile of keys to many."""
+    case = ref.Case([new, 1, new - 1, 2], [new + 2500, 90, new - 1, 129], 2, dim, 32, quantised, seed=15, pad_tokens=1)
+    got = _check(case, 16, gate=new == 16)
+    assert (got[case.cu[-1]:] == 0).all()
+
+
 def test_rows_that_see_nothing_are_zero():
     """More new tokens than cached positions: the first ones have no place and see no key."""
     for quantised in (False, True):
