@@ -289,19 +289,21 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   for (int i = tid; i < D; i += C::kThreads) sm.bad[i] = INT32_MAX;
   pdl_begin();
   const int padding = padding_begin(b);
+  // (never before the wait in pdl_begin: a kernel that this one waits for may need the columns)
+  if (warp == C::kMmaWarp) tmem_alloc(&sm.tmem, 512);
+  fence_before_sync();
   bool bad_len = false;
   Pieces pieces;
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad_len);
   zero_padding(a, b, D, padding);
   if (bad_len) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
+  // (locate_piece has synchronised the block)
   if (cta >= pieces.count) {
     if (tid == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, nullptr, 0);
+    if (warp == C::kMmaWarp) tmem_dealloc(sm.tmem, 512);
     return;
   }
-  if (warp == C::kMmaWarp) tmem_alloc(&sm.tmem, 512);
-  fence_before_sync();
-  __syncthreads();
   fence_after_sync();
   // all 512 columns: they start at column 0, and TMEM addresses are constants from here on
   constexpr uint32_t tmem = 0;
