@@ -31,13 +31,14 @@ __device__ __forceinline__ uint4 dequant8(uint2 u, uint32_t b) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A CTA takes TB neighbouring tokens, a warp a token at a time (or a few narrow ones): the lanes walk
-// its heads' vectors in pieces of 16 elements (8 from each half of the vector, so that a warp's
-// loads and stores are whole), D / 16 neighbouring lanes to a vector.  Bound by the bytes as long as the work per piece is small: the places (a 32-way search, a length, a page) are
-// looked up once per token by one warp, into shared memory, while the others' first loads are under
-// way.  (Looked up by every thread with 64-bit pair indices, the instructions were the bound: 68 % of
-// the issue slots and 3.6 TB/s.  With 8 elements a lane: 4.5 TB/s on seven prompts of 34,000 tokens in
-// all, 2 x 256, 8-bit; with 16, 5.4.)
+// A CTA takes neighbouring tokens, a warp a token at a time (or a few narrow ones): the lanes walk its
+// heads' vectors in pieces of 16 elements (8 from each half of the vector, so that a warp's loads and
+// stores are whole), D / 16 neighbouring lanes to a vector.  Bound by the bytes as long as the work
+// per piece is small: the places (a 32-way search, a length, a page) are looked up once per token by
+// one warp, into shared memory, while the others' first loads are under way.  (Looked up by every
+// thread with 64-bit pair indices, the instructions were the bound: 68 % of the issue slots and
+// 3.6 TB/s.  With 8 elements a lane: 4.5 TB/s on seven prompts of 34,000 tokens in all, 2 x 256,
+// 8-bit; with 16, 5.4.)
 constexpr int kMostTokens = 32;
 
 // The pieces of a CTA's tokens as its 8 warps walk them: every eighth run of 32 pieces each (narrow
