@@ -4,22 +4,29 @@
 //   S = Q K^T,   P = 2^(scale log2(e) S - m),   O += P V,   o = O / l,   l = sum P
 //
 // in one pass over 128-key tiles.  A CTA holds a tile of query rows (row = new token x head of the
-// key/value head's group): two blocks of 128 rows for head dims up to 128, one for 256.  S and O
-// live in TMEM (256 + 2 D columns, or 2 x 128 + 256), P replaces S in place as the TMEM operand of
-// the second product.
+// key/value head's group): two blocks of 128 rows for head dims up to 128, one for 256 and where no
+// sequence has rows for a second.  S and O live in TMEM (256 + 2 D columns, or 2 x 128 + D), P
+// replaces S in place as the TMEM operand of the second product.
 //
 // What bounds it: 4 D flops per (row, key) on the tensor pipe and one exponential per (row, key)
 // on the special-function units, of which D = 128 takes about as long for both; so neither may
 // wait for the other:
-//  * a softmax warpgroup per block of rows (a thread owns a row: no shuffles), one warp issuing
-//    MMAs, one warp issuing TMA copies, for 8-bit caches four more that turn e4m3 tiles into bf16
-//    operands;
+//  * a softmax warpgroup per block of rows (a thread owns a row: no shuffles), one thread issuing
+//    MMAs, a warp each issuing the TMA copies of keys and values, and for 8-bit caches a warpgroup
+//    (two for D = 256) that turns the values' codes into bf16 operands; the keys' codes are operands
+//    of e4m3 MMAs as they are, against the queries in two e4m3 parts;
 //  * the MMA order PV_0(i), QK_0(i+1), PV_1(i), QK_1(i+1) keeps the pipe on one block while the
-//    other block's softmax runs (D = 256: two S buffers, PV(i), QK(i+2));
+//    other block's softmax runs (one block: two S buffers, PV(i), QK(i+2));
 //  * the reference m follows the running maximum only when that outgrows it by 2^8, so O is almost
 //    never rescaled, and never by a warpgroup of its own;
 //  * the next tile's queries are loaded, and its first product issued, before the last tile's
 //    output leaves.
+// Measured, 4096 tokens on 16384 cached ones (1.24 TFLOP at 32 heads of 128 and 16 of 256): bf16
+// D = 128 843 us, 1467 TFLOP/s (78 % of the dense bf16 rate, 63 % of the cycles with the pipe busy at
+// its nominal rate); D = 256 815 us, 1519; D = 64 690 us, 896, where the exponentials bound it.  8-bit:
+// 1101 to 1155 us, 1190 us and 900 us, bound by the conversion of the values, whose instructions share
+// the issue slots and instruction caches with the softmax.  32 rows on 8000 keys (64 sequences of 8
+// tokens): bf16 322 us, 98 % of the copy bandwidth; 8-bit 361 us, 45 %.
 // Values whose key some rows do not see must be finite for the product to leave those rows alone:
 // in tiles that the causal edge crosses, the first warpgroup replaces non-finite ones (and
 // whatever lies past the sequence's end) by zero, and notes column and position, so that the rows
@@ -559,7 +566,9 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     // rolled (D = 256: two rows), with the next row's loads ahead: unrolled eight times it does not
     // fit an SM quarter's instruction cache next to the softmax, and both ran at a third of the speed
     // (one prompt piece of 4096 on 16384 tokens, D = 256 with one group: 3147 us, rolled 1481 us).
-    // A group of warps for each half of a V tile: 1481 -> 1388 us, two rows 1284 us.
+    // A group of warps for each half of a V tile: 1481 -> 1388 us, two rows 1284 us.  The conversion
+    // instruction (to f16 operands, for tiles whose scales f16 holds) is fewer instructions and slower
+    // (1210 -> 1244 us; D = 128 1107 -> 1420): bit operations.
     constexpr int kPer = C::kCols / 16, kStep = 32 / kPer, kSteps = 32 / kStep;
     const int piece = lane % kPer, sub = lane / kPer, warp_row = (ct >> 5) * 32 + sub;
     constexpr int kUnroll = D == 256 ? 2 : 1;
@@ -800,10 +809,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           const int k0 = (ta + i) * TK;
           const bool partial = k0 + TK - 1 > pos_min;
           const int lim = pos - k0;                               // columns 0..lim are seen
-          // One block: S has two buffers, so the products run ahead and the scores are read twice, 32 at
-          // a time in rolled loops, which leaves the instruction cache to the conversion (D = 256, 4096
-          // tokens on 16384: 1388 -> 1219 us).  Two blocks: a block's products wait for its softmax, so
-          // it reads them once into registers (read twice, D = 128: 1107 -> 1411 us).
+          // 8-bit, D = 256: S has two buffers, so the products run ahead, and the scores are read twice,
+          // 32 at a time in rolled loops, which leaves the instruction caches to the conversion (4096
+          // tokens on 16384: 1388 -> 1219 us).  Else once, into registers: with two blocks a block's
+          // products wait for its softmax (read twice, D = 128: 1107 -> 1411 us; one block, 32 rows on
+          // 8000 keys: 426 -> 434 us).
           constexpr bool kTwice = Q8 && D == 256;
           uint32_t v[kTwice ? 32 : 128];
           float xs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

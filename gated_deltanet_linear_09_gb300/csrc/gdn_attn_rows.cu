@@ -22,6 +22,10 @@
 //  * 8-bit caches: the keys' codes are e4m3 MMA operands as they are (the queries as two e4m3
 //    parts, whose sum is exact), their scales applied to the scores; the values' codes become f16 by
 //    the conversion instruction, their scales applied to the probabilities.
+// Measured (the copy bandwidth is 6.69 TB/s): 64 sequences of 8000 positions, 8 x 128, 4 rows, bf16
+// 312 us, 6.7 TB/s, 8-bit 172 us, 6.1 TB/s; ragged 8-bit batch of 64, 200 to 16,000 positions, 88 us,
+// 5.7 TB/s; two sequences of 100,000 to 131,000, 2 x 256, bf16, 77 us, 5.9 TB/s.  16 rows on 8 bits:
+// 266 us, 4.0 TB/s, bound by the instructions of two row tiles.
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 

@@ -378,7 +378,9 @@ typedef enum { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1 } gdn_kv_type;
 /* A paged key/value cache.  k_pages, v_pages: [num_pages][num_kv_heads][page_size][head_dim], bf16
  * or e4m3; k_scales, v_scales (GDN_KV_E4M3 only, else NULL): uint8
  * [num_pages][num_kv_heads][page_size], the exponent byte b of each vector's scale 2^(b - 127)
- * (255: the vector reads as NaN).  head_dim in {64, 128, 256}; page_size in {16, 32, 64, 128, 256};
+ * (255: the vector reads as NaN; else 10 <= b <= 247).  The codes of stored vectors are finite: a NaN
+ * is told by the scale byte, never by a code (gdn_kv_append keeps to both; what lies past a
+ * sequence's end may be anything).  head_dim in {64, 128, 256}; page_size in {16, 32, 64, 128, 256};
  * bases 16-byte aligned.  status: optional device int32 error word. */
 typedef struct {
   void* k_pages;
