@@ -25,7 +25,7 @@
 // Measured (the copy bandwidth is 6.69 TB/s): 64 sequences of 8000 positions, 8 x 128, 4 rows, bf16
 // 312 us, 6.7 TB/s, 8-bit 172 us, 6.1 TB/s; ragged 8-bit batch of 64, 200 to 16,000 positions, 88 us,
 // 5.7 TB/s; two sequences of 100,000 to 131,000, 2 x 256, bf16, 77 us, 5.9 TB/s.  16 rows on 8 bits:
-// 266 us, 4.0 TB/s, bound by the instructions of two row tiles.
+// 258 us, 4.1 TB/s, bound by the instructions of two row tiles.
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 
@@ -46,8 +46,10 @@ struct RowsCfg {
   static constexpr int kConsumers = D == 256 && Q8 && NT == 1 ? 8 : 4;
   static constexpr int kThreads = (kConsumers + 2) * 32;
   // Groups of 16 keys that a warp takes of a stage: with half the bytes to wait for, an 8-bit cache
-  // wants the chains of two side by side.
-  static constexpr int kGroups = Q8 && kConsumers == 4 ? 2 : 1;
+  // wants the chains of two side by side (16 rows on 64 x 8000 keys: D = 64 196 us with one, 160 with
+  // two, D = 256 162 and 136), as far as two CTAs' registers go: with D = 128 and 16 rows they spill
+  // (285 us with two, 258 with one).
+  static constexpr int kGroups = Q8 && kConsumers == 4 && !(NT == 2 && D == 128) ? 2 : 1;
   static constexpr int kKeys = 16 * kGroups * kConsumers;        // of a stage
   static constexpr int kHalfBytes = kKeys * D * kElem;           // a stage's keys
   static constexpr int kStageBytes = 2 * kHalfBytes;
