@@ -686,49 +686,38 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       cp_async_wait_all();
       __syncwarp();
       if constexpr (Q8) {
-        // the rows become their two e4m3 parts (see split_e4m3), which take the same place: a lane
-        // has its piece before the row's lanes write
-        constexpr int kBatch = 4;
+        // The rows become their two e4m3 parts (see split_e4m3), which take the same place: the warp
+        // has a row before it writes it.  Rows past the tile's last are zeros in either form.
+        sm.q_scale[blk][r] = a.scale_log2;
+        uint4 ahead = *row_piece(first, piece);
 #pragma unroll 1
-        for (int j0 = 0; j0 < 32 / kStep; j0 += kBatch) {
-          uint4 u[kBatch];
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) u[j] = *row_piece((j0 + j) * kStep + first, piece);
-          uint32_t top[kBatch];
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const uint32_t m = __vmaxu2(__vmaxu2(u[j].x & 0x7fff7fffu, u[j].y & 0x7fff7fffu),
-                                        __vmaxu2(u[j].z & 0x7fff7fffu, u[j].w & 0x7fff7fffu));
-            top[j] = max(m & 0xffffu, m >> 16);
-          }
+        for (int j = 0; j * kStep < rows; ++j) {
+          const int row = j * kStep + first;
+          const uint4 u = ahead;
+          ahead = *row_piece(min(row + kStep, 31), piece);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                      __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+          uint32_t top = max(m & 0xffffu, m >> 16);
           if constexpr (kPer == 32) {
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) top[j] = __reduce_max_sync(0xffffffffu, top[j]);
+            top = __reduce_max_sync(0xffffffffu, top);
           } else {
 #pragma unroll
-            for (int o = kPer / 2; o > 0; o >>= 1)
-#pragma unroll
-              for (int j = 0; j < kBatch; ++j) top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+            for (int o = kPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
           }
           __syncwarp();
+          const int bb = scale_byte(top);
+          const uint32_t inv = split_factor(bb);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int row = (j0 + j) * kStep + first, bb = scale_byte(top[j]);
-            const float inv = __uint_as_float((uint32_t)(254 - (bb == 255 ? 127 : bb)) << 23);
-            const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              split_e4m3(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
-            if (piece == 0) sm.q_scale[blk][lbase + row] = scale_f32(bb) * a.scale_log2;
-            const int col = piece * 8;                               // byte in the row
-            uint8_t* d = sm.q[blk] + (col >> 7) * (128 * 128) +
-                         (C::kCols == 128 ? (lbase + row) * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
-                                          : (lbase + row) * 64 + (((col >> 4) ^ ((row >> 1) & 3)) << 4)) + (col & 8);
-            *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            *reinterpret_cast<uint2*>(d + C::kQBytes / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          }
-          __syncwarp();
+          for (int e = 0; e < 4; ++e) split_e4m3(mul_bf16x2(w[e], inv), hi[e], lo[e]);
+          if (piece == 0) sm.q_scale[blk][lbase + row] = scale_f32(bb) * a.scale_log2;
+          const int col = piece * 8;                                 // byte in the row
+          uint8_t* d = sm.q[blk] + (col >> 7) * (128 * 128) +
+                       (C::kCols == 128 ? (lbase + row) * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
+                                        : (lbase + row) * 64 + (((col >> 4) ^ ((row >> 1) & 3)) << 4)) + (col & 8);
+          *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(d + C::kQBytes / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         }
       }
       fence_proxy_async_smem();

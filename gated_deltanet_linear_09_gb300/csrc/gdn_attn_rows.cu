@@ -369,15 +369,14 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         for (int e = 0; e < kEl / 2; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         top = __reduce_max_sync(0xffffffffu, top);
         const int bb = scale_byte(top);
-        const float inv = __uint_as_float((uint32_t)(254 - (bb == 255 ? 127 : bb)) << 23);
+        const uint32_t inv = split_factor(bb);
         if (lane == 0) sm.q_scale[r] = scale_f32(bb) * a.scale_log2;
 #pragma unroll
         for (int e = 0; e < kEl / 4; ++e) {
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            split_e4m3(__uint_as_float(w[2 * e + k] << 16) * inv, __uint_as_float(w[2 * e + k] & 0xffff0000u) * inv,
-                       hi[k], lo[k]);
+            split_e4m3(mul_bf16x2(w[2 * e + k], inv), hi[k], lo[k]);
           if (d0 < D) {
             const int d = d0 + 4 * e, ks = d / 64 * 2 + ((d >> 3) & 1), ln = (r & 7) * 4 + ((d >> 4) & 3);
             uint32_t* at0 = &sm.q_part[ks][r >> 3][ln].x + ((d >> 2) & 1);

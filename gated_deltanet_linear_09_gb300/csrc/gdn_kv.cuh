@@ -94,19 +94,29 @@ __device__ __forceinline__ int scale_byte(uint32_t top) {
   return e < 10 ? 10 : e;
 }
 
-// (x, y) = hi + lo in e4m3 codes, |x|, |y| <= 448.  A query row brought to (224, 448] by a power of
-// two is the sum of two e4m3 vectors: the codes nearest to it, and what they leave, which fits their
-// four significant bits again (bf16 has eight).  Elements below 2^-10 of the row's largest lose bits
-// at 2^-18 of it.
-__device__ __forceinline__ void split_e4m3(float x, float y, uint32_t& hi, uint32_t& lo) {
-  uint16_t h, l;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
-  uint32_t f;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
-  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(y - v.y), "f"(x - v.x));
-  hi = h;
-  lo = l;
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
+__device__ __forceinline__ uint32_t bf16x2_to_e4m3(uint32_t w) {
+  uint16_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+      : "=h"(h)
+      : "f"(__uint_as_float(w & 0xffff0000u)), "f"(__uint_as_float(w << 16)));
+  return h;
+}
+
+// Two elements of a query row as hi + lo in e4m3 codes.  A row brought to (224, 448] by a power of two
+// is the sum of two e4m3 vectors: bf16 has eight significant bits and e4m3 four, and splitting by the
+// product with 2^4 + 1 (Veltkamp) leaves four and four, exactly.  Elements below 2^-10 of the row's
+// largest, whose parts fall out of e4m3's exponents, lose bits at 2^-17 of it.
+__device__ __forceinline__ void split_e4m3(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  const uint32_t c = mul_bf16x2(x, 0x41884188u), h = sub_bf16x2(c, sub_bf16x2(c, x));
+  hi = bf16x2_to_e4m3(h);
+  lo = bf16x2_to_e4m3(sub_bf16x2(x, h));
+}
+// What brings a row of this scale byte there, as two bf16 (a row that reads as NaN: ones).
+__device__ __forceinline__ uint32_t split_factor(int b) { return (uint32_t)(b == 255 ? 127 : 254 - b) * 0x00800080u; }
 
 }  // namespace gdn
