@@ -313,3 +313,47 @@ def test_long_batches(dim, quantised, heads, group, new):
         want = torch.einsum("hgqj,jhd->qhgd", w, v[i, :t].double())
         spread = torch.einsum("hgqj,jhd->qhgd", w, v[i, :t].double().abs())
         assert ((got[i] - want).abs() <= ref.attention_bound(want, spread)).all(), i
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+def test_pages_past_32_bit_offsets(quantised):
+    """Pages whose elements lie more than 2^31 from the pool's start: the same bits as from a small
+    pool, for a few rows and for many."""
+    heads, dim, page = 8, 256, 256
+    far = 2 ** 31 // (heads * dim * page)
+    big = runtime.PagedKVCache(far + 6, page, heads, dim, quantised)
+    small = runtime.PagedKVCache(8, page, heads, dim, quantised)
+    g = torch.Generator(device="cuda").manual_seed(16)
+    for new, length in ((1, 700), (40, 600)):
+        kv = torch.randn((length, heads, dim), generator=g, device="cuda").to(torch.bfloat16)
+        q = torch.randn((new, 2 * heads, dim), generator=g, device="cuda").to(torch.bfloat16)
+        got = []
+        for cache, pages in ((big, [far + 5, 1, far + 2]), (small, [6, 1, 3])):
+            table = torch.tensor([pages], dtype=torch.int32, device="cuda")
+            lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+            whole = runtime.KVBatch(torch.tensor([0, length], dtype=torch.int32, device="cuda"), lens, table, length, length)
+            cache.append(whole, kv, kv)
+            some = runtime.KVBatch(torch.tensor([0, new], dtype=torch.int32, device="cuda"), lens, table, new, new)
+            got.append((*cache.read(whole), cache.attend(some, q)))
+            assert int(cache.status.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("dim,quantised", [(64, True), (128, False), (256, True)])
+def test_many_short_pieces(dim, quantised):
+    """More sequences than a CTA has threads, of a few tokens each; most have none."""
+    new = [(5 if i % 7 == 3 else 0) for i in range(1500)]
+    case = ref.Case(new, [n + i % 3 for i, n in enumerate(new)], 1, dim, 16, quantised, seed=17)
+    _check(case, 8)
+
+
+@pytest.mark.parametrize("new", [1, 2, 40])
+def test_unknown_bound_on_new_tokens(new):
+    """max_tokens 0: the same results within their bound as with it."""
+    case = ref.Case([new, 1], [new + 400, 50], 2, 128, 32, False, seed=18)
+    q, _ = _q(case, 8)
+    want, spread = ref.attention(case, q)
+    b = case.device_batch(runtime)
+    free = runtime.KVBatch(*b.tensors, b.total_tokens)
+    got = case.filled_cache(runtime).attend(free, q.cuda()).cpu().double()
+    assert ((got - want).abs() <= ref.attention_bound(want, spread)).all()
