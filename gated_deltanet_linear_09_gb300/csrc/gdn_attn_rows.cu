@@ -231,6 +231,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     SegIter<R, TK> it;
     Segment sg;
     sg.split = false;
+    bool first = true;
     if (!values) it.start(&b, c.page_shift, c.H, a.g, fix, pieces, cta, sm.scan.at);
     while (true) {
       // the keys' producer walks the piece, for all
@@ -256,8 +257,23 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       if (d.n < 0) break;
       if (d.n == 0) continue;
       const int tb = d.ta + d.n, keys = d.keys;
-      // the queries' place is free when the tile before has been scored: after what the ring takes
-      const int q_after = min(tb, d.ta + C::kStages - 1) - 1;
+      // The queries' place is free when the tile before has been scored: after what the ring takes, or
+      // (the piece's first tile) at once (23 sequences of up to 1054, 64 heads over 8 x 64 of 8 bits: 17.9 -> 15.8 us).
+      auto load_queries = [&]() {
+        wait_or_die(&sm.q_empty, q_phase ^ 1u, &sm.dead, c.status);
+        q_phase ^= 1u;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)d.rows * 2 * D);
+        __syncwarp();
+        if (lane < d.rows) {
+          int tok, head;
+          row_of(SeqInfo{d.row0, d.tokens, d.len}, a.g, d.head, d.tile * R + lane, &tok, &head);
+          bulk_g2s(sm.q[lane], a.q + tok * a.q_ld + head * a.q_head_ld, 2 * D, &sm.q_full);
+        }
+        __syncwarp();
+      };
+      const int q_after = first ? -1 : min(tb, d.ta + C::kStages - 1) - 1;
+      if (values && first) load_queries();
+      first = false;
       const int* table = b.table + (long long)d.seq * b.table_ld;
       // Lane i < TK / 16 looks after the i-th 16 keys of a stage: their page, fetched a stage ahead,
       // the box that begins with them (a box is a page's part of the stage), and their scale bytes.
@@ -289,18 +305,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
           cp_async16_mbar(smem_u32(&sm.scales[stage][values][lane * 16]), src, in, full);
         }
         __syncwarp();
-        if (values && i == q_after) {
-          wait_or_die(&sm.q_empty, q_phase ^ 1u, &sm.dead, c.status);
-          q_phase ^= 1u;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)d.rows * 2 * D);
-          __syncwarp();
-          if (lane < d.rows) {
-            int tok, head;
-            row_of(SeqInfo{d.row0, d.tokens, d.len}, a.g, d.head, d.tile * R + lane, &tok, &head);
-            bulk_g2s(sm.q[lane], a.q + tok * a.q_ld + head * a.q_head_ld, 2 * D, &sm.q_full);
-          }
-          __syncwarp();
-        }
+        if (values && i == q_after) load_queries();
         page = page_next;
         k0 = k1;
         if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
