@@ -4,8 +4,7 @@
 // floor is the bytes: x and r read once, the sum and y written once.  A row therefore stays in
 // registers between the pass that sums h^2 and the one that scales: nothing is read twice.
 // Measured: 16384 x 4096 bf16 with residual to block-scaled 8 bits 70.8 us, the copy bandwidth (6.67
-// of 6.69 TB/s); one row of 5120 4.5 us and 1537 x 2047 f32 (rows off 16-byte boundaries, element by
-// element) 7.2 us on the GPU, both below what a call takes on the host.
+// of 6.69 TB/s); one row of 5120 2.0 us on the GPU, below what a call takes on the host.
 #include "gdn_internal.h"
 
 #include <cuda_fp8.h>
@@ -14,11 +13,18 @@ namespace gdn {
 
 namespace {
 
-// VEC consecutive elements at p (16 bytes when VEC > 1).
+// VEC consecutive elements at p: 16 bytes, two elements, or one.
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T* p, float* v) {
   if constexpr (VEC == 1) {
     v[0] = Act<T>::load(p);
+  } else if constexpr (VEC == 2 && sizeof(T) == 4) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    v[0] = f.x; v[1] = f.y;
+  } else if constexpr (VEC == 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xffff0000u);
   } else if constexpr (sizeof(T) == 4) {
     const float4 f = *reinterpret_cast<const float4*>(p);
     v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
@@ -37,6 +43,10 @@ template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T* p, const float* v) {
   if constexpr (VEC == 1) {
     Act<T>::store(p, v[0]);
+  } else if constexpr (VEC == 2 && sizeof(T) == 4) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  } else if constexpr (VEC == 2) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
   } else if constexpr (sizeof(T) == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
@@ -60,6 +70,8 @@ template <int VEC>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, float inv) {
   if constexpr (VEC == 1) {
     *p = (uint8_t)e4m3x2(v[0] * inv, 0.f);
+  } else if constexpr (VEC == 2) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)e4m3x2(v[0] * inv, v[1] * inv);
   } else {
     uint32_t w[VEC / 4];
 #pragma unroll
@@ -76,6 +88,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// The same over a warp, of magnitudes: as bits they order like numbers, a NaN above all.
+__device__ __forceinline__ float warp_max_nan(float m) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu));
 }
 
 __device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.0f / 448.0f), 0x1p-120f); }
@@ -100,9 +117,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
   constexpr int CTA = TPR < 128 ? 128 : TPR;
   constexpr int WARPS = CTA / 32;
   __shared__ float part[WARPS];
-  // group maxima of the element-wise path, as the bits of non-negative floats (a NaN's are above all)
-  constexpr bool SMEM_GROUPS = KIND == GDN_NORM_E4M3_BLOCK && VEC == 1;
-  __shared__ uint32_t gmax[SMEM_GROUPS ? TPR * NV / 128 + 1 : 1];
+  // One or two elements a lane: a warp's columns are a part of a group.  Group maxima, as the bits of
+  // non-negative floats (a NaN's are above all), then the groups' inverse scales.
+  constexpr bool SMEM_GROUPS = KIND == GDN_NORM_E4M3_BLOCK && VEC <= 2 && TPR > 32;
+  __shared__ uint32_t gmax[SMEM_GROUPS ? TPR * NV * VEC / 128 : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = TPR < 128 ? tid % TPR : tid;
   const long long row = (long long)blockIdx.x * (CTA / TPR) + (TPR < 128 ? tid / TPR : 0);
@@ -147,7 +165,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
     }
   }
   if constexpr (SMEM_GROUPS)
-    for (int i = tid; i < TPR * NV / 128 + 1; i += CTA) gmax[i] = 0;
+    for (int i = tid; i < TPR * NV * VEC / 128; i += CTA) gmax[i] = 0;
   ss = warp_sum(ss);
   if constexpr (TPR > 32) {
     if (lane == 0) part[warp] = ss;
@@ -188,15 +206,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
       float mr = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) mr = max_nan(mr, m[j]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mr = max_nan(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+      mr = warp_max_nan(mr);
       if constexpr (TPR > 32) {
         __syncthreads();   // part[] of the sum has been read
         if (lane == 0) part[warp] = mr;
         __syncthreads();
         mr = lane < WARPS ? part[lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mr = max_nan(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+        mr = warp_max_nan(mr);
       }
       const float s = scale_of(mr), inv = 1.0f / s;
       if (t == 0) a.scales[row] = s;
@@ -207,7 +223,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
       }
     } else {
       const int groups = (n + 127) >> 7;
-      if constexpr (VEC > 1) {
+      if constexpr (VEC > 2) {
         // 128 columns are the vectors of 128 / VEC neighbouring lanes
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -221,24 +237,41 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
             store_e4m3<VEC>(y + c, h[j], inv);
           }
         }
+      } else if constexpr (TPR == 32) {
+        // the warp's next few vectors
+        constexpr int kOf = 4 / VEC;
+#pragma unroll
+        for (int j0 = 0; j0 < NV; j0 += kOf) {
+          float mg = 0.f;
+#pragma unroll
+          for (int j = j0; j < j0 + kOf; ++j) mg = max_nan(mg, m[j]);
+          mg = warp_max_nan(mg);
+          const float s = scale_of(mg), inv = 1.0f / s;
+          if (t == 0 && j0 / kOf < groups) a.scales[row * groups + j0 / kOf] = s;
+#pragma unroll
+          for (int j = j0; j < j0 + kOf; ++j) {
+            const int c = (j * TPR + t) * VEC;
+            if (c < n) store_e4m3<VEC>(y + c, h[j], inv);
+          }
+        }
       } else {
-        // a warp's 32 columns lie inside one group
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float mg = m[j];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mg = max_nan(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-          if (lane == 0) atomicMax(&gmax[(j * TPR + t) >> 7], __float_as_uint(mg) & 0x7fffffffu);
+          mg = warp_max_nan(mg);
+          if (lane == 0) atomicMax(&gmax[(j * TPR + t) * VEC >> 7], __float_as_uint(mg));
+        }
+        __syncthreads();
+        for (int i = tid; i < groups; i += CTA) {
+          const float s = scale_of(__uint_as_float(gmax[i]));
+          a.scales[row * groups + i] = s;
+          gmax[i] = __float_as_uint(1.0f / s);
         }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          const int c = j * TPR + t;
-          if (c < n) {
-            const float s = scale_of(__uint_as_float(gmax[c >> 7]));
-            if ((c & 127) == 0) a.scales[row * groups + (c >> 7)] = s;
-            store_e4m3<1>(y + c, h[j], 1.0f / s);
-          }
+          const int c = (j * TPR + t) * VEC;
+          if (c < n) store_e4m3<VEC>(y + c, h[j], __uint_as_float(gmax[c >> 7]));
         }
       }
     }
@@ -278,13 +311,29 @@ int launch_vec(const NormArgs& a, int kind, cudaStream_t s) {
   return launch_one<T, VEC, 1024, 8>(a, kind, s);
 }
 
-// Rows off the 16-byte grid: one element per access, a CTA per row.
+// Rows off the 16-byte grid: two elements per access where they are all even, else one; a warp to a row
+// up to 512 accesses.  (100,000 rows of 130, bf16 with residual: 103 us with a CTA to a row and one
+// element an access, 28 so; 16384 x 2046 to 8 bits by rows 54 and 42 us; 16384 x 2047, which leaves one
+// element an access, 53 us against 41 for 2048.)
+template <typename T, int VEC>
+int launch_narrow(const NormArgs& a, int kind, cudaStream_t s) {
+  const int nv = (a.n + VEC - 1) / VEC;
+  if (nv <= 128) return launch_one<T, VEC, 32, 4>(a, kind, s);
+  if (nv <= 256) return launch_one<T, VEC, 32, 8>(a, kind, s);
+  if (nv <= 512) return launch_one<T, VEC, 32, 16>(a, kind, s);
+  if (nv <= 1024) return launch_one<T, VEC, 128, 8>(a, kind, s);
+  if (nv <= 2048) return launch_one<T, VEC, 256, 8>(a, kind, s);
+  if (nv <= 4096) return launch_one<T, VEC, 512, 8>(a, kind, s);
+  if (nv <= 8192) return launch_one<T, VEC, 1024, 8>(a, kind, s);
+  return launch_one<T, VEC, 1024, VEC == 1 ? 32 : 16>(a, kind, s);
+}
+
 template <typename T>
-int launch_scalar(const NormArgs& a, int kind, cudaStream_t s) {
-  if (a.n <= 1024) return launch_one<T, 1, 128, 8>(a, kind, s);
-  if (a.n <= 2048) return launch_one<T, 1, 256, 8>(a, kind, s);
-  if (a.n <= 8192) return launch_one<T, 1, 1024, 8>(a, kind, s);
-  return launch_one<T, 1, 1024, 32>(a, kind, s);
+int launch_typed(const NormArgs& a, int kind, cudaStream_t s) {
+  constexpr int kVec = 16 / sizeof(T);
+  const long long bits = a.n | a.x_ld | (a.r ? a.r_ld : 0);
+  if (bits % kVec == 0) return launch_vec<T, kVec>(a, kind, s);
+  return bits % 2 == 0 ? launch_narrow<T, 2>(a, kind, s) : launch_narrow<T, 1>(a, kind, s);
 }
 
 }  // namespace
@@ -295,12 +344,7 @@ int launch_rms_norm(const void* x, long long x_ld, const void* residual, long lo
                     cudaStream_t stream) {
   const NormArgs a{x, residual, weight, sum_out, y, scales, x_ld, residual_ld, weight_offset, eps,
                    1.0f / (float)n, rows, n};
-  const int vec = act == GDN_BF16 ? 8 : 4;
-  const bool vectors = n % vec == 0 && x_ld % vec == 0 && (!residual || residual_ld % vec == 0);
-  if (act == GDN_BF16)
-    return vectors ? launch_vec<__nv_bfloat16, 8>(a, kind, stream)
-                   : launch_scalar<__nv_bfloat16>(a, kind, stream);
-  return vectors ? launch_vec<float, 4>(a, kind, stream) : launch_scalar<float>(a, kind, stream);
+  return act == GDN_BF16 ? launch_typed<__nv_bfloat16>(a, kind, stream) : launch_typed<float>(a, kind, stream);
 }
 
 }  // namespace gdn

@@ -95,3 +95,21 @@ def test_no_rows():
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     y, _, _ = runtime.rms_norm(x, torch.ones(64, dtype=torch.bfloat16, device="cuda"))
     assert y.shape == (0, 64)
+
+
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [2, 33, 129, 130, 254, 255, 258, 511, 514, 1022, 1023, 1026, 2046, 4098, 8190, 16382, 20001, 32766])
+def test_norm_off_the_vector_grid(n, act):
+    test_norm(n, act)
+
+
+@pytest.mark.parametrize("n", [300, 301, 1300, 2051])
+def test_non_finite_groups_off_the_vector_grid(n):
+    x = torch.randn((4, n)).to(torch.bfloat16)
+    x[2, 130] = math.inf                           # its row's norm is zero elsewhere, NaN there
+    x[1, 7] = math.nan
+    y, s, _ = runtime.rms_norm(x.cuda(), torch.ones((n,), dtype=torch.bfloat16).cuda(), quant="block")
+    y, s = y.float().cpu(), s.cpu()
+    assert torch.isnan(s[1]).all() and torch.isnan(y[1]).all()
+    assert torch.isnan(s[2, 1]) and torch.isfinite(s[2, 0]) and torch.isfinite(s[2, 2:]).all()
+    assert torch.isfinite(s[[0, 3]]).all() and torch.isfinite(y[[0, 3]]).all()
