@@ -1090,9 +1090,12 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   KvMaps maps;
   const int P = 1 << c.page_shift;
   if (!make_tile_maps(c, P < kKeys ? P : kKeys, Q8 ? C::kCols : 64, &maps)) return GDN_ERR_CUDA;
-  // What a tile of rows costs beside its keys, in keys (12 sequences of 3 to 1456 new tokens: 151 us
-  // at 256, 116 at 512, 110 at 1024), and the fewest keys worth a piece of their own.
-  const int grid = sms, fix = 1024 * a.g;
+  // What a tile of rows costs beside its keys, in keys (the gate's share grows with the columns), and
+  // the fewest keys worth a piece of their own (14 tokens on 8481: 21.5 us at 512, 24.2 at 256).  12
+  // sequences of 3 to 1456 new tokens at 512, 640, 768, 896, 1024 keys: D = 256 bf16 97, 92, 94, 96,
+  // 98 us, 8-bit 139, 133, 128, 128, 131, gated -, 162, 145, 142, 138; D = 128 bf16 54, 56, 58, -, 58.
+  const int base = D < 256 ? 512 : Q8 ? 896 : 640;
+  const int grid = sms, fix = (base + (a.gate ? D / 2 : 0)) * a.g;
   const int least = 512 * a.g;
   int rc = launch_dependent(chunk_kernel<D, Q8, B>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
