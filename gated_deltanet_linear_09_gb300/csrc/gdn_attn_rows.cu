@@ -83,6 +83,11 @@ struct __align__(1024) RowsSmem {
   int dead;
 };
 
+// Scale bytes whose unit 2^(b - 134) is 1, and the least that is used as a unit.
+constexpr int kUnitOne = 134, kLeastUnit = 94;
+// How far below the unit a scale may lie for f16 products.
+constexpr uint32_t kNear = 18;
+
 __device__ __forceinline__ void mma16816(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -426,7 +431,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
       }
-    // 8-bit values: the accumulators count in 2^(v_ref - 134), v_ref the largest scale byte so far
+    // 8-bit values: the accumulators count in 2^(v_ref - 134) (0: nothing added yet)
     int v_ref = 0;
     float o[D / 16][NT][4];       // (columns 16 i + g and + 8) x (rows 2 t, 2 t + 1)
 #pragma unroll
@@ -643,33 +648,48 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             }
           }
         } else {
-          // The probabilities take the values' scales 2^(b - 127) as 2^(b - v_ref + 7), v_ref the
-          // largest b so far: f16 has eleven bits for them from 2^15 down to 2^-14, which is room
-          // for scales 2^18 apart.  Where they are further apart, and past the sequence's end (codes
-          // there may be NaN's, which the bit conversion makes 480), bf16 operands instead.
-          uint32_t most = 0, least = 255;
+          // The probabilities take the values' scales 2^(b - 127) as 2^(b - v_ref + 7).  The unit is
+          // chosen by the first keys that all rows see, two binades above their largest scale, and stays:
+          // what a key adds then depends on no other key.  f16 holds the products of nearby scales;
+          // the other keys', and those of keys that some row does not see or that lie past the
+          // sequence's end (codes there may be NaN's, which the bit conversion makes 480), are bf16,
+          // whose exponents hold any.  Where hidden keys begin, or scales come that the unit is far
+          // too small for (the sum would leave f32), the unit becomes 1 for good, in which a sum holds what
+          // an f32 sum of the values themselves does.
+          bool wide = partial || v_ref == 0;
 #pragma unroll
           for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
-              if (k0 + 16 * u + key_in(f) < keys && v_byte[u][f] != 255) {
-                most = max(most, v_byte[u][f]);
-                least = min(least, v_byte[u][f]);
-              }
-          most = __reduce_max_sync(0xffffffffu, most);
-          least = __reduce_min_sync(0xffffffffu, least);
-          if ((int)most > v_ref) {
-            const int d = v_ref - (int)most;
-            const float f = d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23);
-            v_ref = (int)most;
+            for (int f = 0; f < 2; ++f) wide |= (uint32_t)(v_ref - (int)v_byte[u][f]) > kNear;
+          if (__any_sync(0xffffffffu, wide)) {
+            uint32_t most = 0, least = 255;
+            if (!partial) {
 #pragma unroll
-            for (int y = 0; y < D / 16; ++y)
+              for (int u = 0; u < G; ++u)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                o[y][nt][0] *= f; o[y][nt][1] *= f; o[y][nt][2] *= f; o[y][nt][3] *= f;
+                for (int f = 0; f < 2; ++f)
+                  if (v_byte[u][f] != 255) {
+                    most = max(most, v_byte[u][f]);
+                    least = min(least, v_byte[u][f]);
+                  }
+              most = __reduce_max_sync(0xffffffffu, most);
+              least = __reduce_min_sync(0xffffffffu, least);
+              if (v_ref == 0) v_ref = min(max((int)most + 2, kLeastUnit), kUnitOne);
+            }
+            if (partial || (int)most > v_ref + 24) {
+              if (v_ref != 0 && v_ref != kUnitOne) {
+                const float f = __uint_as_float((uint32_t)(127 + v_ref - kUnitOne) << 23);
+#pragma unroll
+                for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    o[y][nt][0] *= f; o[y][nt][1] *= f; o[y][nt][2] *= f; o[y][nt][3] *= f;
+                  }
               }
+              v_ref = kUnitOne;
+            }
+            wide = partial || (int)most > v_ref || v_ref - (int)least > (int)kNear;
           }
-          const bool wide = v_ref - (int)least > 18 || k0 + 16 * G > keys;
 #pragma unroll
           for (int u = 0; u < G; ++u)
 #pragma unroll
