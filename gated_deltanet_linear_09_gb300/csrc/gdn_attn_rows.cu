@@ -4,7 +4,7 @@
 //   o_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = 2^(s_rj - m_r),   s_rj = scale log2(e) q_r . k_j
 //
 // with one pass over the keys: m_r is a reference that follows the running maximum (it only has to
-// stay within 2^8 of it, so the accumulator is rescaled when a maximum outgrows it by that much,
+// stay within 2^8 of it, or 2^4, so the accumulator is rescaled when a maximum outgrows it by that much,
 // not at every step) and every sum is f32.
 //
 // What bounds it: the cache is read once, 2 D elements per key and head, for 8 or 16 rows, so the
@@ -83,10 +83,21 @@ struct __align__(1024) RowsSmem {
   int dead;
 };
 
-// Scale bytes whose unit 2^(b - 134) is 1, and the least that is used as a unit.
-constexpr int kUnitOne = 134, kLeastUnit = 94;
-// How far below the unit a scale may lie for f16 products.
-constexpr uint32_t kNear = 18;
+// How far (as a power of two) a maximum may outgrow its reference.  f32 and bf16 hold 2^8 times the
+// reference's probability alike; with an 8-bit cache the probabilities become f16, to which the
+// factor 2^kUp moves them.
+template <bool Q8>
+constexpr int kLag = Q8 ? 4 : 8;
+constexpr int kUp = 15 - kLag<true>;
+// Scale byte whose unit 2^(b - 127 - kUp) is 1, and the least that is used as a unit.
+constexpr int kUnitOne = 127 + kUp, kLeastUnit = kUnitOne - 40;
+// How far below the unit a scale may lie for f16 products, and how many keys a warp may add to a tile
+// so: a probability p becomes p 2^(b - unit + kUp), at least 2 p, which f16 holds to 2^-11 of itself
+// from 2^-14 up and to 2^-25 below, so all small ones together are off by kMostNear 2^-26 = 2^-10 of
+// the row's sum, which is at least 1.  (64 x 8000 keys of 8 x 128, 4 rows: 167 us where all keys are
+// so, 193 us where none are; D = 64 102 and 130; two tokens, 16 rows 256 and 322.)
+constexpr uint32_t kNear = kUp - 1;
+constexpr int kMostNear = 1 << 16;
 
 __device__ __forceinline__ void mma16816(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
   asm(
@@ -431,8 +442,9 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
       }
-    // 8-bit values: the accumulators count in 2^(v_ref - 134) (0: nothing added yet)
+    // 8-bit values: the accumulators count in 2^(v_ref - kUnitOne) (0: nothing added yet)
     int v_ref = 0;
+    const bool few = sg.n * 16 * G <= kMostNear;
     float o[D / 16][NT][4];       // (columns 16 i + g and + 8) x (rows 2 t, 2 t + 1)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -543,9 +555,8 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
             x[nt][e] = v;
-            above |= v > m[nt][e] + 8.f;
+            above |= v > m[nt][e] + kLag<Q8>;
           }
-        // 2^8 above the reference is harmless in f32 and in the 16-bit probabilities alike
         if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -648,7 +659,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             }
           }
         } else {
-          // The probabilities take the values' scales 2^(b - 127) as 2^(b - v_ref + 7).  The unit is
+          // The probabilities take the values' scales 2^(b - 127) as 2^(b - v_ref + kUp).  The unit is
           // chosen by the first keys that all rows see, two binades above their largest scale, and stays:
           // what a key adds then depends on no other key.  f16 holds the products of nearby scales;
           // the other keys', and those of keys that some row does not see or that lie past the
@@ -656,7 +667,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
           // whose exponents hold any.  Where hidden keys begin, or scales come that the unit is far
           // too small for (the sum would leave f32), the unit becomes 1 for good, in which a sum holds what
           // an f32 sum of the values themselves does.
-          bool wide = partial || v_ref == 0;
+          bool wide = partial || v_ref == 0 || !few;
 #pragma unroll
           for (int u = 0; u < G; ++u)
 #pragma unroll
@@ -688,7 +699,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
               }
               v_ref = kUnitOne;
             }
-            wide = partial || (int)most > v_ref || v_ref - (int)least > (int)kNear;
+            wide = partial || !few || (int)most > v_ref || v_ref - (int)least > (int)kNear;
           }
 #pragma unroll
           for (int u = 0; u < G; ++u)
@@ -696,7 +707,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             for (int f = 0; f < 2; ++f) {
               const int bb = (int)v_byte[u][f];
               const float y = bb == 255 ? __int_as_float(0x7fffffff)
-                                        : __uint_as_float((uint32_t)max(bb - v_ref + 134, 0) << 23);
+                                        : __uint_as_float((uint32_t)max(bb - v_ref + kUnitOne, 0) << 23);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -791,7 +802,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
         for (int w = 0; w < C::kConsumers; ++w) top = fmaxf(top, sm.ml[w][8 * nt + 2 * t + e][0]);
         f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
-        if (Q8) f[nt][e] *= v_ref == 0 ? 0.f : __uint_as_float((uint32_t)(v_ref - 7) << 23);   // 2^(v_ref - 134)
+        if (Q8) f[nt][e] *= v_ref == 0 ? 0.f : __uint_as_float((uint32_t)(v_ref - kUp) << 23);   // 2^(v_ref - kUnitOne)
       }
     const bool whole = sg.whole;
     float* prow = Partials<R, D>::rows(a.ws, cta, sg.slot);

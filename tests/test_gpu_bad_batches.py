@@ -1,0 +1,44 @@
+"""Inconsistent batches: every output row is written, and the status says so."""
+import math
+
+import pytest
+import torch
+
+import paged_ref as ref
+from gated_deltanet_linear_09_gb300 import gdn, runtime
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_deltanet_linear_09_gb300 import build
+    build.build()
+    gdn.load()
+
+
+@pytest.mark.parametrize("dim,quantised,group", [(64, True, 2), (128, False, 4), (256, False, 4), (128, True, 8)])
+def test_inconsistent_token_ranges_give_zeros(dim, quantised, group):
+    """Rows of a sequence that ends past the packed tokens, and rows before the first sequence, see nothing;
+    the other sequences are attended as ever."""
+    new, lens, tokens = [3, 40], [50, 60], 43
+    case = ref.Case(new, lens, 1, dim, 16, quantised, seed=51)
+    g = torch.Generator().manual_seed(52)
+    q = torch.randn((tokens, group, dim), generator=g).to(torch.bfloat16)
+    cache = case.filled_cache(runtime)
+    b = case.device_batch(runtime)
+    want, spread = ref.attention(case, q)
+    bound = ref.attention_bound(want, spread)
+    for cu, zero, good in (([0, 3, 50], range(3, 43), range(0, 3)), ([2, 3, 43], range(0, 2), range(3, 43)),
+                           ([0, 3, 2 ** 31 - 1], range(3, 43), range(0, 3)), ([-4, 3, 43], range(0, 3), range(3, 43)),
+                           ([0, 50, 43], range(0, 43), ())):
+        for most in (1, 3, 40):        # the host's bound decides which kernel runs
+            b = runtime.KVBatch(torch.tensor(cu, dtype=torch.int32, device="cuda"), b.tensors[1], b.tensors[2], tokens, most)
+            out = torch.full((tokens, group, dim), math.nan, dtype=torch.bfloat16, device="cuda")
+            cache.attend(b, q.cuda(), out=out)
+            got = out.cpu().double()
+            assert int(cache.status.item()) == gdn.GDN_STATUS_BAD_SEQLENS, cu
+            cache.status.zero_()
+            assert (got[list(zero)] == 0).all(), cu
+            good = list(good)
+            assert ((got[good] - want[good]).abs() <= bound[good]).all(), cu

@@ -1,5 +1,7 @@
 """Few query rows over an 8-bit cache whose value vectors' scales lie far apart: what a key adds
 depends on its probability and its own scale, whatever the scales of the others are."""
+import math
+
 import pytest
 import torch
 
@@ -64,3 +66,27 @@ def test_a_large_value_hidden_from_earlier_tokens(dim, group, new):
         got = case.filled_cache(runtime).attend(_repeated(case, n), q.repeat(n, 1, 1).cuda()).cpu().double()
         ok = (got.view(n, new, group, dim) - want).abs() <= ref.attention_bound(want, spread)
         assert ok[:, :new - 1].all(), length
+
+
+@pytest.mark.parametrize("dim,group", [(64, 4), (128, 4), (128, 12), (256, 8)])
+def test_small_probabilities_beside_a_large_value(dim, group):
+    """In every warp's share of the keys: a faint key whose value is 2^17 times the others', a strong key
+    without a value, and hundreds of keys of one small probability that carry the result.  A query of its
+    own for each of the sequences: probabilities from 2^-9 to 2^-11."""
+    length, n = 4096, 150
+    case = ref.Case([1], [length], 2, dim, 32, True, seed=35)
+    g = torch.Generator().manual_seed(36)
+    case.k[0].zero_()
+    case.v[0] = (1.0 + 0.2 * torch.randn((length, 2, dim), generator=g)).to(torch.bfloat16)
+    at = (torch.arange(0, length, 512)[:, None] + torch.arange(0, 128, 16)[None]).flatten()
+    case.k[0][at, :, 0] = 10 * math.log(2.0) * math.sqrt(dim) / 8.0
+    case.v[0][at] = 0
+    case.k[0][at + 1, :, 0] = -400.0
+    case.v[0][at + 1] = 2.0 ** 17
+    q = torch.zeros((n, 2 * group, dim), dtype=torch.bfloat16)
+    q[:, :, 0] = (7.2 + 1.6 * torch.arange(n)[:, None] / n).to(torch.bfloat16)
+    got = case.filled_cache(runtime).attend(_repeated(case, n), q.cuda()).cpu().double()
+    K, V = (x[0] for x in case.held())
+    score = q[:, 0, 0].double()[:, None] * K[None, :, 0, 0] / math.sqrt(dim)
+    want = (torch.softmax(score, 1) @ V.reshape(length, -1)).view(n, 2, 1, dim).expand(n, 2, group, dim).reshape(n, -1, dim)
+    assert ((got - want).abs() <= ref.attention_bound(want, want)).all()      # (no value is negative)
