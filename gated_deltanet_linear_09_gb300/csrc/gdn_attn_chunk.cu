@@ -865,7 +865,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           }
           const float x = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])) * scale;
           if (__any_sync(0xffffffffu, x > m + 8.f)) {
-            const float mn = fmaxf(m, x);
+            // only a row whose own maximum asks for it: no bit of a row depends on another's keys
+            const float mn = x > m + 8.f ? x : m;
             const float f = mn == m ? 1.f : ex2f(m - mn);
             m = mn;
             l *= f;

@@ -160,6 +160,8 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(addr) : "memory");
   return __uint_as_float((uint32_t)v << 16);
 }
+// The sign bits of the halves that hold an infinity or a NaN, of two bf16.
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -562,7 +564,8 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float to = fmaxf(m[nt][e], x[nt][e]);
+              // only a row whose own maximum asks for it: no bit of a row depends on another's keys
+              const float to = x[nt][e] > m[nt][e] + kLag<Q8> ? x[nt][e] : m[nt][e];
               const float f = m[nt][e] == to ? 1.f : ex2(m[nt][e] - to);
               m[nt][e] = to;
               l[nt][e] *= f;
@@ -608,21 +611,19 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
             z0 = (y < keys ? 0xffffu : 0u) | (y + 1 < keys ? 0xffff0000u : 0u);
             z1 = (y + 8 < keys ? 0xffffu : 0u) | (y + 9 < keys ? 0xffff0000u : 0u);
           }
-          bool finite = true;
+          // A key hidden from some rows and seen by others: its value must be finite for the matrix
+          // product to leave the former alone.  Non-finite ones are taken out of it and added to the
+          // rows that see them.
+          uint32_t seen = 0;
           if (partial && info.tokens > 1) {
-            // a key hidden from some rows and seen by others: its value must be finite for the
-            // matrix product to leave the former alone
-            uint32_t seen = 0;
 #pragma unroll 4
             for (int d = 0; d < D / 16; ++d) {
               uint32_t r[4];
               load_v(d, r);
-              seen |= ((r[0] & z0 & 0x7f807f80u) + 0x00800080u) | ((r[1] & z0 & 0x7f807f80u) + 0x00800080u) |
-                      ((r[2] & z1 & 0x7f807f80u) + 0x00800080u) | ((r[3] & z1 & 0x7f807f80u) + 0x00800080u);
+              seen |= non_finite(r[0] & z0) | non_finite(r[1] & z0) | non_finite(r[2] & z1) | non_finite(r[3] & z1);
             }
-            finite = !__any_sync(0xffffffffu, (seen & 0x80008000u) != 0);
           }
-          if (finite) {
+          if (!__any_sync(0xffffffffu, seen != 0)) {
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
               uint32_t r[4];
@@ -633,6 +634,17 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
                 mma16816(o[d][nt], make_uint4(r[0], r[1], r[2], r[3]), p[nt].x, p[nt].y);
             }
           } else {
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              uint32_t r[4];
+              load_v(d, r);
+              r[0] &= z0; r[1] &= z0; r[2] &= z1; r[3] &= z1;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) r[y] &= ~((non_finite(r[y]) >> 15) * 0xffffu);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(o[d][nt], make_uint4(r[0], r[1], r[2], r[3]), p[nt].x, p[nt].y);
+            }
 #pragma unroll 1
             for (int j = 0; j < 16 && k0 + j < keys; ++j) {
               const int src = (j & 7) * 4 + t;
@@ -652,8 +664,8 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 #pragma unroll
                   for (int e = 0; e < 2; ++e)
                     if (k0 + j <= pos[nt][e]) {
-                      o[d][nt][e] = fmaf(pj[nt][e], v0, o[d][nt][e]);
-                      o[d][nt][2 + e] = fmaf(pj[nt][e], v1, o[d][nt][2 + e]);
+                      if (!isfinite(v0)) o[d][nt][e] = fmaf(pj[nt][e], v0, o[d][nt][e]);
+                      if (!isfinite(v1)) o[d][nt][2 + e] = fmaf(pj[nt][e], v1, o[d][nt][2 + e]);
                     }
               }
             }
