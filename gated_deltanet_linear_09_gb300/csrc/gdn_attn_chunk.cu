@@ -30,7 +30,7 @@
 // Values whose key some rows do not see must be finite for the product to leave those rows alone:
 // in tiles that the causal edge crosses, the first warpgroup replaces non-finite ones (and
 // whatever lies past the sequence's end) by zero, and notes column and position, so that the rows
-// that do see them get their NaN.
+// that do see them get their infinity or NaN.
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 
@@ -89,7 +89,7 @@ struct __align__(1024) ChunkSmem {
   float k_scale[Q8 ? C::kScales : 1][kKeys];
   float q_scale[C::kBlocks][Q8 ? 128 : 1];
   LineScan<C::kRows, C::kThreads> scan;
-  int bad[D];                       // first position with a non-finite value, per column
+  uint32_t bad[D];                  // a Notes of each column
   SegDesc segs[kSegs];
   int any_bad;
   uint32_t tmem;
@@ -99,6 +99,24 @@ struct __align__(1024) ChunkSmem {
   uint64_t s_bytes[Q8 ? C::kScales : 1], s_free[Q8 ? C::kScales : 1], s_ready[Q8 ? C::kScales : 1];
   uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
+};
+
+// Where in a column of values the first +inf, -inf and NaN lie that some rows of a tile do not see, as
+// positions past its first row's (at most 256 rows and 128 keys on), ten bits each.  An 8-bit cache has
+// vectors that are NaN throughout and no infinities: there it is one absolute position.
+struct Notes {
+  static constexpr uint32_t kNone = 0xffffffffu;
+  static __device__ __forceinline__ int first(uint32_t notes, int kind) { return (notes >> (10 * kind)) & 1023; }
+  // the bf16 `value` at position `at`
+  static __device__ __forceinline__ void add(uint32_t* notes, uint32_t value, int at) {
+    const int kind = value == 0x7f80u ? 0 : value == 0xff80u ? 1 : 2;
+    uint32_t old = *(volatile uint32_t*)notes;
+    while (first(old, kind) > at) {
+      const uint32_t seen = old;
+      old = atomicCAS(notes, seen, (seen & ~(1023u << (10 * kind))) | ((uint32_t)at << (10 * kind)));
+      if (old == seen) break;
+    }
+  }
 };
 
 // Operand descriptors of 128-byte-swizzled tiles (8-row groups 1,024 bytes apart).  Only the low
@@ -293,7 +311,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     sm.any_bad = 0;
     mbar_fence_init();
   }
-  for (int i = tid; i < D; i += C::kThreads) sm.bad[i] = INT32_MAX;
+  for (int i = tid; i < D; i += C::kThreads) sm.bad[i] = Q8 ? INT32_MAX : Notes::kNone;
   pdl_begin();
   const int padding = padding_begin(b);
   // (never before the wait in pdl_begin: a kernel that this one waits for may need the columns)
@@ -949,8 +967,10 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
 #pragma unroll
                   for (int e = 0; e < 8; ++e)
                     if (((w[e >> 1] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
+                      const uint32_t y = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
                       w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-                      atomicMin(&sm.bad[h * C::kCols + piece * 8 + e], k0 + j);
+                      if constexpr (Q8) atomicMin((int*)&sm.bad[h * C::kCols + piece * 8 + e], k0 + j);
+                      else Notes::add(&sm.bad[h * C::kCols + piece * 8 + e], y, k0 + j - pos_min);
                     }
                   sm.any_bad = 1;
                   *p = make_uint4(w[0], w[1], w[2], w[3]);
@@ -996,9 +1016,21 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           reg_fence16(o);
           reg_fence16(o + 16);
           if (bad) {
+            if constexpr (Q8) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (sm.bad[d + e] <= pos) o[e] = 0x7fffffffu;
+              for (int e = 0; e < 32; ++e)
+                if ((int)sm.bad[d + e] <= pos) o[e] = 0x7fffffffu;
+            } else {
+              const int mine = pos - (cur.len - cur.tokens + min(cur.tile * R, last_row) / a.g);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t notes = sm.bad[d + e];
+                float y = __uint_as_float(o[e]);           // (infinities of both signs add up to NaN)
+                if (Notes::first(notes, 0) <= mine) y += INFINITY;
+                if (Notes::first(notes, 1) <= mine) y -= INFINITY;
+                o[e] = Notes::first(notes, 2) <= mine ? 0x7fffffffu : __float_as_uint(y);
+              }
+            }
           }
         };
         if (whole) {
@@ -1067,7 +1099,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       }
       // both blocks are done with the notes on non-finite values
       if (bar_any(1, C::kSoftWarps * 32, *(volatile int*)&sm.any_bad != 0)) {
-        for (int i = tid; i < D; i += C::kSoftWarps * 32) sm.bad[i] = INT32_MAX;
+        for (int i = tid; i < D; i += C::kSoftWarps * 32) sm.bad[i] = Q8 ? INT32_MAX : Notes::kNone;
         if (tid == 0) sm.any_bad = 0;
         asm volatile("bar.sync 1, %0;\n" ::"n"(C::kSoftWarps * 32) : "memory");
       }

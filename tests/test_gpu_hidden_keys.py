@@ -73,3 +73,34 @@ def test_bytes_past_the_end_change_no_bit(dim, quantised, group, new):
     outs = [_cache(case, x).attend(b, q).view(torch.int16) for x in fills]
     for x, out in zip(fills, outs):
         assert torch.equal(out, outs[0]), x
+
+
+@pytest.mark.parametrize("dim,group,new", [(64, 2, 4), (128, 4, 3), (256, 2, 6), (64, 4, 12), (128, 2, 60), (128, 8, 40), (256, 4, 50)])
+def test_infinite_values_reach_the_rows_that_see_them(dim, group, new):
+    """In a bf16 cache: a row that sees +inf in a column has it there, one that sees both has NaN."""
+    case = ref.Case([new], [new + 30], 1, dim, 16, False, seed=46)
+    g = torch.Generator().manual_seed(47)
+    q = torch.randn((new, group, dim), generator=g).to(torch.bfloat16)
+    last = new + 29
+    case.v[0][last - 2, 0, 3] = math.inf
+    case.v[0][last - 2, 0, 7] = -math.inf
+    case.v[0][last - 1, 0, 9] = math.inf
+    case.v[0][last, 0, 9] = -math.inf
+    case.v[0][last - 1, 0, 20] = math.nan
+    case.v[0][last, 0, 20] = math.inf
+    got = case.filled_cache(runtime).attend(case.device_batch(runtime), q.cuda()).cpu().double()
+    want, spread = ref.attention(case, q)
+    want[:new - 3][want[:new - 3] != want[:new - 3]] = 0      # 0 * inf of keys past a row's own
+    bound = ref.attention_bound(want, spread)
+    for t in range(new):
+        for col, places in ((3, {last - 2: math.inf}), (7, {last - 2: -math.inf}),
+                            (9, {last - 1: math.inf, last: -math.inf}), (20, {last - 1: math.nan, last: math.inf})):
+            seen = [x for p, x in places.items() if p <= t + 30]
+            if not seen:
+                assert torch.isfinite(got[t, :, col]).all(), (t, col)
+            elif len(set(seen)) > 1 or math.isnan(seen[0]):
+                assert torch.isnan(got[t, :, col]).all(), (t, col)
+            else:
+                assert (got[t, :, col] == seen[0]).all(), (t, col)
+    cols = [d for d in range(dim) if d not in (3, 7, 9, 20)]
+    assert ((got - want).abs() <= bound)[:, :, cols].all()
