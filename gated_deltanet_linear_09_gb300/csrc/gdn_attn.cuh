@@ -27,12 +27,16 @@ struct SeqInfo {
   int len;         // cached positions, 0 when the sequence is not usable
 };
 
+// A sequence whose tokens do not lie in the batch's keeps those that do, without cached positions: their
+// rows are written (zeros) like all others.
 __device__ __forceinline__ SeqInfo load_seq(const KvBatchView& b, int page_shift, int s, bool* bad) {
   const int c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1), len = __ldg(b.lens + s);
   SeqInfo r{c0, c1 - c0, len};
   if (c0 < 0 || c1 < c0 || c1 > b.total) {
     *bad = true;
-    r.row0 = r.tokens = r.len = 0;
+    r.row0 = max(0, min(c0, b.total));
+    r.tokens = max(0, min(c1, b.total) - r.row0);
+    r.len = 0;
   } else if (len < 0 || len > ((long long)b.table_ld << page_shift)) {
     *bad = true;
     r.len = 0;
@@ -396,19 +400,30 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, int D, int tok, in
   Act<__nv_bfloat16>::store4(a.out + ((long long)tok * a.Hq + head) * D + d, o);
 }
 
-// Where the padding rows past the last sequence begin (loaded early, used late).
-__device__ __forceinline__ int padding_begin(const KvBatchView& b) {
-  return b.num_seqs > 0 ? __ldg(b.cu + b.num_seqs) : 0;
+// The rows of the sequences: [begin, end) (loaded early, used late).
+struct RowRange {
+  int begin, end;
+};
+__device__ __forceinline__ RowRange batch_rows(const KvBatchView& b) {
+  return b.num_seqs > 0 ? RowRange{__ldg(b.cu), __ldg(b.cu + b.num_seqs)} : RowRange{0, 0};
 }
 
-// Zeros in them.
-__device__ __forceinline__ void zero_padding(const AttnArgs& a, const KvBatchView& b, int D, int end) {
-  if (end < 0 || end >= b.total) return;
-  const long long n = (long long)(b.total - end) * a.Hq * (D / 8);
-  uint4* p = reinterpret_cast<uint4*>(a.out + (long long)end * a.Hq * D);
+// Zeros in rows [begin, end).
+__device__ __forceinline__ void zero_rows(const AttnArgs& a, int D, int begin, int end) {
+  const long long n = (long long)(end - begin) * a.Hq * (D / 8);
+  uint4* p = reinterpret_cast<uint4*>(a.out + (long long)begin * a.Hq * D);
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n;
        i += (long long)gridDim.x * blockDim.x)
     p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// In the padding rows past the last sequence, and in rows before the first (there should be none).
+__device__ __forceinline__ void zero_outside(const AttnArgs& a, const KvBatchView& b, int D, RowRange rows, bool* bad) {
+  if (rows.begin != 0) {
+    *bad = true;
+    zero_rows(a, D, 0, min(rows.begin, b.total));
+  }
+  if (rows.end < b.total) zero_rows(a, D, max(rows.end, 0), b.total);
 }
 
 // ------------------------------------------------------------------ merging split tiles

@@ -313,7 +313,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   }
   for (int i = tid; i < D; i += C::kThreads) sm.bad[i] = Q8 ? INT32_MAX : Notes::kNone;
   pdl_begin();
-  const int padding = padding_begin(b);
+  const RowRange batch = batch_rows(b);
   // (never before the wait in pdl_begin: a kernel that this one waits for may need the columns)
   if (warp == C::kMmaWarp) tmem_alloc(&sm.tmem, 512);
   fence_before_sync();
@@ -321,7 +321,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   Pieces pieces;
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad_len);
-  zero_padding(a, b, D, padding);
+  zero_outside(a, b, D, batch, &bad_len);
   if (bad_len) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
   // (locate_piece has synchronised the block)
   if (cta >= pieces.count) {

@@ -222,12 +222,12 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   pdl_begin();
-  const int padding = padding_begin(b);
+  const RowRange batch = batch_rows(b);
   bool bad = false;
   Pieces pieces;
   const int cta = blockIdx.x;
   locate_piece<R, C::kThreads>(c, b, a.g, fix, grid, least, cta, &pieces, &sm.scan, &bad);
-  zero_padding(a, b, D, padding);
+  zero_outside(a, b, D, batch, &bad);
   if (bad) set_status(c.status, GDN_STATUS_BAD_SEQLENS);
   if (cta >= pieces.count) {
     if (tid == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, nullptr, 0);

@@ -40,5 +40,7 @@ def test_inconsistent_token_ranges_give_zeros(dim, quantised, group):
             assert int(cache.status.item()) == gdn.GDN_STATUS_BAD_SEQLENS, cu
             cache.status.zero_()
             assert (got[list(zero)] == 0).all(), cu
+            assert (cache.read(b)[0][list(zero)] == 0).all() and int(cache.status.item()) == gdn.GDN_STATUS_BAD_SEQLENS, cu
+            cache.status.zero_()
             good = list(good)
             assert ((got[good] - want[good]).abs() <= bound[good]).all(), cu
