@@ -37,7 +37,7 @@ __device__ __forceinline__ SeqInfo load_seq(const KvBatchView& b, int page_shift
     r.row0 = max(0, min(c0, b.total));
     r.tokens = max(0, min(c1, b.total) - r.row0);
     r.len = 0;
-  } else if (len < 0 || len > ((long long)b.table_ld << page_shift)) {
+  } else if (len < 0 || len > ((long long)b.table_cols << page_shift)) {
     *bad = true;
     r.len = 0;
   }

@@ -117,7 +117,7 @@ struct KvBatchView {
   const int32_t* cu;
   const int32_t* lens;
   const int32_t* table;
-  int num_seqs, total, table_ld, max_tokens;
+  int num_seqs, total, table_ld, max_tokens, table_cols;
 };
 
 int launch_kv_append(const KvView& c, const KvBatchView& b, const void* k, long long k_ld,

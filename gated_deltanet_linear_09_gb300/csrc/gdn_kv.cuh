@@ -39,7 +39,7 @@ __device__ __forceinline__ Place find_place(const KvView& c, const KvBatchView& 
   Place p{-1, 0};
   if (t >= c1 && s == b.num_seqs - 1 && c1 >= c0) return p;    // padding past the last sequence
   const long long len = __ldg(b.lens + s);
-  if (c0 < 0 || t < c0 || t >= c1 || c1 > b.total || len < 0 || len > ((long long)b.table_ld << c.page_shift)) {
+  if (c0 < 0 || t < c0 || t >= c1 || c1 > b.total || len < 0 || len > ((long long)b.table_cols << c.page_shift)) {
     set_status(c.status, GDN_STATUS_BAD_SEQLENS);
     return p;
   }

@@ -127,12 +127,14 @@ int check_cache(const gdn_kv_cache* cache, gdn::KvView* v, bool need_memory) {
 int check_batch(const gdn_kv_batch* batch, gdn::KvBatchView* v) {
   if (!batch) return GDN_ERR_INVALID_ARG;
   const gdn_kv_batch& b = *batch;
-  if (b.num_seqs < 0 || b.total_tokens < 0 || b.table_ld < 0 || b.max_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (b.num_seqs < 0 || b.total_tokens < 0 || b.table_ld < 0 || b.max_tokens < 0 || b.table_cols < 0)
+    return GDN_ERR_INVALID_ARG;
+  const int cols = b.table_cols > 0 ? b.table_cols : b.table_ld;
   if (b.num_seqs > 65535) return GDN_ERR_TOO_LARGE;
   if (b.num_seqs == 0 && b.total_tokens > 0) return GDN_ERR_INVALID_ARG;
-  if (b.num_seqs > 0 && (!b.cu_seqlens || !b.kv_lens || (b.table_ld > 0 && !b.block_table))) return GDN_ERR_INVALID_ARG;
+  if (b.num_seqs > 0 && (!b.cu_seqlens || !b.kv_lens || (cols > 0 && !b.block_table))) return GDN_ERR_INVALID_ARG;
   if (!aligned(b.cu_seqlens, 4) || !aligned(b.kv_lens, 4) || !aligned(b.block_table, 4)) return GDN_ERR_MISALIGNED;
-  *v = gdn::KvBatchView{b.cu_seqlens, b.kv_lens, b.block_table, b.num_seqs, b.total_tokens, b.table_ld, b.max_tokens};
+  *v = gdn::KvBatchView{b.cu_seqlens, b.kv_lens, b.block_table, b.num_seqs, b.total_tokens, b.table_ld, b.max_tokens, cols};
   return GDN_OK;
 }
 

@@ -92,7 +92,7 @@ class gdn_kv_batch(ctypes.Structure):
     _fields_ = [("cu_seqlens", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int32),
                 ("total_tokens", ctypes.c_int32), ("table_ld", ctypes.c_int32),
-                ("max_tokens", ctypes.c_int32)]
+                ("max_tokens", ctypes.c_int32), ("table_cols", ctypes.c_int32)]
 
 
 _lib = None
@@ -372,10 +372,11 @@ def make_kv_cache(k_pages, v_pages, k_scales=None, v_scales=None, status=None) -
 
 def make_kv_batch(cu_seqlens, kv_lens, block_table, total_tokens: int, max_tokens: int = 0) -> gdn_kv_batch:
     """Device int32 tensors: cu_seqlens [n + 1], kv_lens [n], block_table [n][table_ld] (rows may be
-    strided)."""
+    strided, or all the same one)."""
+    cols = int(block_table.shape[1])
+    ld = int(block_table.stride(0)) if block_table.shape[0] > 1 and cols else cols
     return gdn_kv_batch(_ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), int(kv_lens.shape[0]),
-                        int(total_tokens), int(block_table.stride(0)) if block_table.shape[0] > 1
-                        else int(block_table.shape[1]), int(max_tokens))
+                        int(total_tokens), ld, int(max_tokens), cols)
 
 
 def gdn_rms_norm(x, weight, y, residual=None, sum_out=None, scales=None, weight_offset=0.0, eps=1e-6,

@@ -402,9 +402,10 @@ typedef struct {
  * int32[num_seqs + 1] non-decreasing from 0; rows in [cu_seqlens[num_seqs], total_tokens) are
  * padding; max_tokens >= every T_n (host bound; 0: unknown).  A token whose position is negative
  * (kv_lens[n] < T_n) has no place: it is not stored, reads as zero, and attends to nothing.
- * Entries of block_table past the sequence's pages are never read.  A sequence with kv_lens[n]
- * outside [0, table_ld * page_size] or an inconsistent cu_seqlens sets GDN_STATUS_BAD_SEQLENS and
- * is treated as having no cached positions; a needed page outside [0, num_pages) sets
+ * Entries of block_table past the sequence's pages are never read.  table_cols is the number of a
+ * row's entries (0: table_ld); rows may be further apart, or all the same one (table_ld 0).  A
+ * sequence with kv_lens[n] outside [0, table_cols * page_size] or an inconsistent cu_seqlens sets
+ * GDN_STATUS_BAD_SEQLENS and is treated as having no cached positions; a needed page outside [0, num_pages) sets
  * GDN_STATUS_PAGE_RANGE, is not written, and its keys and values read as zero.  num_seqs <= 65535. */
 typedef struct {
   const int32_t* cu_seqlens;
@@ -414,6 +415,7 @@ typedef struct {
   int32_t total_tokens;
   int32_t table_ld;
   int32_t max_tokens;
+  int32_t table_cols;
 } gdn_kv_batch;
 
 /* Writes the new tokens' keys and values into their places.  k, v: bf16

@@ -44,3 +44,32 @@ def test_inconsistent_token_ranges_give_zeros(dim, quantised, group):
             cache.status.zero_()
             good = list(good)
             assert ((got[good] - want[good]).abs() <= bound[good]).all(), cu
+
+
+@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("quantised", [False, True])
+def test_tables_that_are_views(new, quantised):
+    """Columns cut out of a wider table: a length past them is reported, and no entry beside them is read;
+    and one row shared by all sequences."""
+    case = ref.Case([new, new], [60, 60], 1, 64, 16, quantised, seed=53, table_extra=0)
+    g = torch.Generator().manual_seed(54)
+    q = torch.randn((2 * new, 4, 64), generator=g).to(torch.bfloat16).cuda()
+    cache = case.filled_cache(runtime)
+    b = case.device_batch(runtime)
+    want = cache.attend(b, q)
+    wide = torch.full((2, 9), 10 ** 9, dtype=torch.int32, device="cuda")
+    wide[:, 3:7] = b.tensors[2]
+    view = runtime.KVBatch(b.tensors[0], b.tensors[1], wide[:, 3:7], 2 * new, new)
+    assert torch.equal(cache.attend(view, q), want) and int(cache.status.item()) == 0
+    short = runtime.KVBatch(b.tensors[0], b.tensors[1], wide[:, 3:6], 2 * new, new)
+    assert (cache.attend(short, q) == 0).all() and int(cache.status.item()) == gdn.GDN_STATUS_BAD_SEQLENS
+    cache.status.zero_()
+    kv = torch.ones((2 * new, 1, 64), dtype=torch.bfloat16, device="cuda")
+    pages = cache.k_pages.clone()
+    cache.append(short, kv, kv)
+    assert torch.equal(pages.view(torch.uint8), cache.k_pages.view(torch.uint8))
+    assert (cache.read(short)[0] == 0).all() and int(cache.status.item()) == gdn.GDN_STATUS_BAD_SEQLENS
+    cache.status.zero_()
+    one = runtime.KVBatch(b.tensors[0], b.tensors[1], b.tensors[2][:1].expand(2, -1), 2 * new, new)
+    same = runtime.KVBatch(b.tensors[0], b.tensors[1], b.tensors[2][:1].repeat(2, 1), 2 * new, new)
+    assert torch.equal(cache.attend(one, q), cache.attend(same, q)) and int(cache.status.item()) == 0
