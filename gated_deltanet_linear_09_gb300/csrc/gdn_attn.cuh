@@ -297,6 +297,45 @@ __device__ __forceinline__ void locate_piece(const KvView& c, const KvBatchView&
   __syncthreads();
 }
 
+// ------------------------------------------------------------------ waits that give up
+
+// Every wait of the attention kernels is bounded.  The first that runs out marks the CTA dead and sets
+// GDN_STATUS_TIMEOUT; from then on no wait blocks, no segment is begun and no copy issued; warps that
+// meet in barriers go on to where they vote to leave.  Copies and products under way are waited for,
+// with a limit, before the CTA ends, and an arrival never meets a phase that only its bytes keep open
+// (it would be one too many).  The results are wrong, in bounds, and told by the status.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  if (*dead == 0) {
+    if (tc::mbar_wait(bar, parity)) return true;
+    *dead = 1;
+    set_status(status, GDN_STATUS_TIMEOUT);
+  }
+  return false;
+}
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, dead, status));
+}
+
+constexpr uint64_t kDrainNs = 100000000;
+// The copies into a ring of N stages that was left at (stage, phase).
+template <int N>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stage, uint32_t phase) {
+  for (int i = 0; i < N; ++i) tc::mbar_wait(&full[i], i < stage ? phase : phase ^ 1u, kDrainNs);
+}
+
+// Barrier over n threads that returns whether any of them passed true.
+__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbarrier.cta.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
 // ------------------------------------------------------------------ segments, published
 
 constexpr int kSegs = 4;           // segments known ahead

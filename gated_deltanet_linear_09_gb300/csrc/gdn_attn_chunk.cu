@@ -93,12 +93,13 @@ struct __align__(1024) ChunkSmem {
   SegDesc segs[kSegs];
   int any_bad;
   uint32_t tmem;
-  int dead;
+  int dead, stopped;
   uint64_t k_full[C::kKStages], k_empty[C::kKStages], v_full[C::kVStages], v_empty[C::kVStages];
   uint64_t r_full[Q8 ? C::kRStages : 1], r_empty[Q8 ? C::kRStages : 1];
   uint64_t s_bytes[Q8 ? C::kScales : 1], s_free[Q8 ? C::kScales : 1], s_ready[Q8 ? C::kScales : 1];
   uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drained;
 };
 
 // Where in a column of values the first +inf, -inf and NaN lie that some rows of a tile do not see, as
@@ -158,31 +159,25 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       : "memory");
 }
 
-// A bounded wait: a timeout marks the CTA dead, after which no wait blocks and the (wrong) results
-// are flagged by the status bit.
-__device__ __forceinline__ void wait_one(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
-  if (!mbar_try_wait(bar, parity) && !*dead && !mbar_wait(bar, parity)) {
-    *dead = 1;
-    set_status(status, GDN_STATUS_TIMEOUT);
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+  return t;
+}
+// A wait of the roles that compute.  One that gives up waits (again with a limit) until both loading
+// warps have stopped, of themselves or because nothing comes back to them; then nothing that the role
+// still hands back, on its way through its segment, is taken for a free place.  Few instructions: they
+// stand at every wait, and the 8-bit kernels are bound by their instruction caches (with two more
+// 64-bit loops here 1116 -> 1200 us).  The status is set at the end.
+__device__ __forceinline__ void wait_held(uint64_t* bar, uint32_t parity, volatile int* dead, volatile int* stopped) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint32_t t0 = globaltimer_lo();
+  while (*dead == 0) {
+    if (mbar_try_wait(bar, parity)) return;
+    if (globaltimer_lo() - t0 > 2000000000u) *dead = 1;
   }
+  while (*stopped < 2 && globaltimer_lo() - t0 < 3000000000u) {}
 }
-// The same for a whole warp.
-__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
-  wait_one(bar, parity, dead, status);
-  __syncwarp();
-}
-
-// Barrier over n threads that returns whether any of them passed true.
-__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbarrier.cta.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(n), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
-
 __device__ __forceinline__ float ex2f(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -307,7 +302,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       mbar_init(&sm.seg_full[i], 1);
       mbar_init(&sm.seg_empty[i], C::kReaders);
     }
-    sm.dead = 0;
+    mbar_init(&sm.drained, 1);
+    sm.dead = sm.stopped = 0;
     sm.any_bad = 0;
     mbar_fence_init();
   }
@@ -333,12 +329,22 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   // all 512 columns: they start at column 0, and TMEM addresses are constants from here on
   constexpr uint32_t tmem = 0;
   if (sm.tmem != 0) {
-    if (tid == 0) set_status(c.status, GDN_STATUS_TIMEOUT);
+    if (tid == 0) {
+      set_status(c.status, GDN_STATUS_TIMEOUT);
+      Partials<R, D>::note(a.ws, grid, cta, a.g, nullptr, 0);
+    }
     if (warp == C::kMmaWarp) tmem_dealloc(sm.tmem, 512);
     return;
   }
+  auto dead = [&]() { return *(volatile int*)&sm.dead != 0; };
+  auto warp_dead = [&]() { return __any_sync(0xffffffffu, dead()) != 0; };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_held(bar, parity, &sm.dead, &sm.stopped); };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    wait(bar, parity);
+    __syncwarp();
+  };
   auto seg_wait = [&](const RingPos<kSegs>& p) -> const SegDesc& {
-    wait_bar(&sm.seg_full[p.stage], p.phase, &sm.dead, c.status);
+    wait_warp(&sm.seg_full[p.stage], p.phase);
     return sm.segs[p.stage];
   };
   auto seg_done = [&](RingPos<kSegs>& p) {
@@ -356,10 +362,12 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     it.start(&b, c.page_shift, c.H, a.g, fix, pieces, cta, sm.scan.at);
     Segment s;
     s.split = false;
+    bool alive = true;
     for (bool more = true; more;) {
       more = it.next(&s);
       if (more && idle(s)) continue;
-      wait_bar(&sm.seg_empty[seg.stage], seg.phase ^ 1u, &sm.dead, c.status);
+      alive = wait_bar(&sm.seg_empty[seg.stage], seg.phase ^ 1u, &sm.dead, c.status);
+      if (!alive) break;
       if (lane == 0) {
         SegDesc d = {};
         d.n = -1;
@@ -370,7 +378,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       seg.step();
     }
     // the piece's last tile may be shared with the next ones
-    if (lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &s, s.split ? it.sharing(s.nt) : 0);
+    if (lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &s, alive && s.split ? it.sharing(s.nt) : 0);
   } else if (warp == C::kLoadWarp || warp == C::kLoadVWarp) {
     // ---------------------------------------------------------------- TMA
     // Copies of one warp go out one after another (some 150 cycles each), hence a warp for the keys
@@ -386,12 +394,14 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     uint64_t* v_full = Q8 ? sm.r_full : sm.v_full;
     uint64_t* v_empty = Q8 ? sm.r_empty : sm.v_empty;
     const int my_page = lane / kBlk, my_blk = lane % kBlk;
-    while (true) {
-      const SegDesc& sd = seg_wait(seg);
+    bool alive = true;
+    while (alive) {
+      alive = wait_bar(&sm.seg_full[seg.stage], seg.phase, &sm.dead, c.status);
+      const SegDesc& sd = sm.segs[seg.stage];
       const int n = sd.n, ta = sd.ta, len = sd.len, head = sd.head;
       const int* table = b.table + (long long)sd.seq * b.table_ld;
       seg_done(seg);
-      if (n < 0) break;
+      if (!alive || n < 0) break;
       if (n == 0) continue;
       auto lookup = [&](int i) {                            // this lane's page of tile i
         const int k = (ta + i) * TK + my_page * box;
@@ -405,13 +415,14 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
       };
       int p_next = lookup(0), p_ahead = lookup(1);          // pages of tiles i + 1, i + 2
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0; i < n && alive; ++i) {
         const int page = p_next;
         p_next = p_ahead;
         p_ahead = lookup(i + 2);
         const int off = (((ta + i) * TK) & ((1 << c.page_shift) - 1));   // 0 unless pages exceed a tile
         if (Q8 && !values) {                                // the tile's scale bytes, keys and values
-          wait_bar(&sm.s_free[sp.stage], sp.phase ^ 1u, &sm.dead, c.status);
+          alive = wait_bar(&sm.s_free[sp.stage], sp.phase ^ 1u, &sm.dead, c.status);
+          if (!alive) break;
           const int key = (lane & 7) * 16, at = key & (box - 1);
           const int p = __shfl_sync(0xffffffffu, page, (key / box) * kBlk);
           const uint8_t* src = (lane & 8 ? c.vs : c.ks) + (((long long)p * c.H + head) << c.page_shift) + off + at;
@@ -426,8 +437,9 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
 #pragma unroll
         for (int half = 0; half < C::kHalves; ++half) {
           uint64_t* full = values ? &v_full[vp.stage] : &sm.k_full[kp.stage];
-          if (values) wait_bar(&v_empty[vp.stage], vp.phase ^ 1u, &sm.dead, c.status);
-          else wait_bar(&sm.k_empty[kp.stage], kp.phase ^ 1u, &sm.dead, c.status);
+          alive = wait_bar(values ? &v_empty[vp.stage] : &sm.k_empty[kp.stage], (values ? vp.phase : kp.phase) ^ 1u,
+                           &sm.dead, c.status);
+          if (!alive) break;
           if (lane == 0) mbar_arrive_expect_tx(full, values ? (Q8 ? C::kRBytes : C::kVBytes) : C::kKBytes);
           __syncwarp();
           if (my_page < pages) {
@@ -441,6 +453,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         }
       }
     }
+    if (lane == 0) atomicAdd(&sm.stopped, 1);
+    // no copy outlives the CTA, whoever has stopped waiting for it
+    cp_async_wait_all();
+    if (values) drain_ring<(Q8 ? C::kRStages : C::kVStages)>(v_full, vp.stage, vp.phase);
+    else drain_ring<C::kKStages>(sm.k_full, kp.stage, kp.phase);
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA (one thread)
     // The tensor pipe queues only a few MMAs, so what this thread does between them leaves the pipe
@@ -486,22 +503,22 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           mma_ts(C::kO + blk * D + half * C::kCols, buf * 128 + ks * 8, v + ks * (2048 / 16), kIdPV, acc || ks > 0);
       };
       while (true) {
-        wait_one(&sm.seg_full[seg.stage], seg.phase, &sm.dead, c.status);
+        wait(&sm.seg_full[seg.stage], seg.phase);
         const SegDesc& sd = sm.segs[seg.stage];
         const int n = sd.n;
         const bool two = sd.rows > 128;
         mbar_arrive(&sm.seg_empty[seg.stage]);
         seg.step();
-        if (n < 0) break;
+        if (dead() || n < 0) break;
         if (n == 0) continue;
-        wait_one(&sm.q_ready[0], q_phase[0], &sm.dead, c.status);
+        wait(&sm.q_ready[0], q_phase[0]);
         q_phase[0] ^= 1u;
         if (C::kBlocks == 2 && two) {
-          wait_one(&sm.q_ready[1], q_phase[1], &sm.dead, c.status);
+          wait(&sm.q_ready[1], q_phase[1]);
           q_phase[1] ^= 1u;
         }
         if constexpr (C::kBlocks == 2) {
-          wait_one(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
+          wait(&sm.k_full[kp.stage], kp.phase);
           fence_after_sync();
           qk_half(0, 0, k_lo(), 0);
           mma_commit(&sm.s_full[0]);
@@ -512,13 +529,13 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           kp.step();
           // Block 0's softmax of tile i has seen V(i) and K(i + 1) arrive before it says p_ready.
           for (int i = 0; i + 1 < n; ++i) {
-            wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
+            wait(&sm.p_ready[0], cnt[0]++ & 1u);
             fence_after_sync();
             pv_half(0, 0, v_lo(), 0, i > 0);
             qk_half(0, 0, k_lo(), 0);
             mma_commit(&sm.s_full[0]);
             if (two) {
-              wait_one(&sm.p_ready[1], cnt[1]++ & 1u, &sm.dead, c.status);
+              wait(&sm.p_ready[1], cnt[1]++ & 1u);
               fence_after_sync();
               pv_half(1, 1, v_lo(), 0, i > 0);
               qk_half(1, 1, k_lo(), 0);
@@ -527,12 +544,12 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             vp.step();
             kp.step();
           }
-          wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
+          wait(&sm.p_ready[0], cnt[0]++ & 1u);
           fence_after_sync();
           pv_half(0, 0, v_lo(), 0, n > 1);
           mma_commit(&sm.o_done[0]);
           if (two) {
-            wait_one(&sm.p_ready[1], cnt[1]++ & 1u, &sm.dead, c.status);
+            wait(&sm.p_ready[1], cnt[1]++ & 1u);
             fence_after_sync();
             pv_half(1, 1, v_lo(), 0, n > 1);
             mma_commit(&sm.o_done[1]);
@@ -543,7 +560,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             const int buf = (int)(s_cnt & 1u);
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
-              wait_one(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
+              wait(&sm.k_full[kp.stage], kp.phase);
               fence_after_sync();
               qk_half(0, buf, k_lo(), h);
               mma_commit(&sm.k_empty[kp.stage]);
@@ -556,7 +573,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           if (n > 1) qk_tile();
           for (int i = 0; i < n; ++i) {
             const int buf = (int)(cnt[0] & 1u);
-            wait_one(&sm.p_ready[0], cnt[0]++ & 1u, &sm.dead, c.status);
+            wait(&sm.p_ready[0], cnt[0]++ & 1u);
             fence_after_sync();
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
@@ -569,6 +586,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           }
         }
       }
+      mma_commit(&sm.drained);          // nor does a product outlive the TMEM
+      mbar_wait(&sm.drained, 0, kDrainNs);
     }
     __syncwarp();
   } else if (Q8 && warp >= C::kConvWarp) {
@@ -594,14 +613,14 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     while (true) {
       const int n = seg_wait(seg).n;
       seg_done(seg);
-      if (n < 0) break;
+      if (warp_dead() || n < 0) break;
       if (n == 0) continue;
       ring_order<C::kHalves>(n, [&](bool is_v, int, int half) {
         if (!is_v) {
           // The scales of a tile's keys, one per thread.  Their place was last read by the softmax
           // four tiles ago, which is over: a V stage of a later tile has come back since.
           if (half == 0) {
-            wait_bar(&sm.s_bytes[ks.stage], ks.phase, &sm.dead, c.status);
+            wait_warp(&sm.s_bytes[ks.stage], ks.phase);
             if (group == 0) {
               sm.k_scale[ks.stage][ct] = scale_f32(sm.scales[ks.stage][0][ct]);
               __syncwarp();
@@ -612,13 +631,13 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           return;
         }
         if (half == group) {
-          wait_bar(&sm.r_full[src.stage], src.phase, &sm.dead, c.status);
+          wait_warp(&sm.r_full[src.stage], src.phase);
           const uint32_t bb = sm.scales[vs.stage][1][ct];
           // the code's bits are the value times 2^-120: one multiply by 2^120 times the scale where that
           // is a bf16 value, else two
           const uint32_t f = bb <= 134 ? (bb + 120) << 7 : 0x7b80u;
           const bool large = __any_sync(0xffffffffu, bb > 134);
-          wait_bar(&sm.v_empty[dst.stage], dst.phase ^ 1u, &sm.dead, c.status);
+          wait_warp(&sm.v_empty[dst.stage], dst.phase ^ 1u);
           const uint8_t* raw = sm.raw[src.stage] + warp_row * C::kCols + piece * 16 + odd * 8;
           const int other = odd ? -8 : 8;
           uint8_t* out = sm.v[dst.stage];
@@ -747,9 +766,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
     };
     {
       const SegDesc& first = seg_wait(seg);
-      if (active(first)) load_q(first);
+      if (!warp_dead() && active(first)) load_q(first);
     }
-    while (true) {
+    // The warps leave together: none acts on a segment that another did not get.
+    bool stop = bar_any(1, C::kSoftWarps * 32, dead());
+    while (!stop) {
       const SegDesc& cur = sm.segs[seg.stage];                   // released at the end
       const int n = cur.n;
       if (n < 0) break;
@@ -775,7 +796,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           v_out.step();
         }
         const SegDesc& next = seg_wait(ahead_seg);
-        if (active(next)) load_q(next);
+        if (!warp_dead() && active(next)) load_q(next);
       } else {
         const int last_row = cur.tokens * a.g - 1, len = cur.len, ta = cur.ta;
         const int pos = before + min(row, last_row) / a.g;
@@ -790,11 +811,11 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           auto rings = [&]() {
             if (C::kBlocks != 2 || blk != 0) return;
             v_at = vp;
-            wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
+            wait_warp(&sm.v_full[vp.stage], vp.phase);
             vp.step();
             if (i == 0) kp.step();
             if (i + 1 < n) {
-              wait_bar(&sm.k_full[kp.stage], kp.phase, &sm.dead, c.status);
+              wait_warp(&sm.k_full[kp.stage], kp.phase);
               kp.step();
             }
           };
@@ -802,8 +823,8 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           // tokens on 16384, before and after: bf16 D = 128 890 and 847 us, D = 64 683 and 749; 8-bit
           // D = 128 1160 and 1107 us, D = 64 922 and 978)
           if (D == 64) rings();
-          if (Q8) wait_bar(&sm.s_ready[sp.stage], sp.phase, &sm.dead, c.status);
-          wait_bar(&sm.s_full[buf], (C::kBlocks == 2 ? cnt : cnt >> 1) & 1u, &sm.dead, c.status);
+          if (Q8) wait_warp(&sm.s_ready[sp.stage], sp.phase);
+          wait_warp(&sm.s_full[buf], (C::kBlocks == 2 ? cnt : cnt >> 1) & 1u);
           fence_after_sync();
           if (C::kBlocks == 2 && releases && warp == 4 * blk && lane == 0) {
             // the last block's scores are there: K(i) has been read, and V(i - 1)
@@ -890,7 +911,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
             l *= f;
             if (i > 0) {
               // two blocks: s_full of this tile came after the product of the one before
-              if (C::kBlocks == 1) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
+              if (C::kBlocks == 1) wait_warp(&sm.o_done[blk], (cnt - 1) & 1u);
               fence_after_sync();
 #pragma unroll 1
               for (int d = 0; d < D; d += 16) {
@@ -939,10 +960,10 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           }
           if (D != 64) rings();
           // for its parity's sake every tile: one block's s_full does not imply the product before
-          if (C::kBlocks == 1 && i > 0) wait_bar(&sm.o_done[blk], (cnt - 1) & 1u, &sm.dead, c.status);
+          if (C::kBlocks == 1 && i > 0) wait_warp(&sm.o_done[blk], (cnt - 1) & 1u);
           if (C::kBlocks == 1) {         // (one block: two V stages hold one tile, which comes late)
             v_at = vp;
-            for (int h = 0; h < C::kHalves; ++h, vp.step()) wait_bar(&sm.v_full[vp.stage], vp.phase, &sm.dead, c.status);
+            for (int h = 0; h < C::kHalves; ++h, vp.step()) wait_warp(&sm.v_full[vp.stage], vp.phase);
           }
           if (blk == 0 && partial) {
             // a causal-edge tile's values: zero past the end, zero and noted where not finite
@@ -1000,7 +1021,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
           }
         }
         // two blocks: one phase of o_done a segment
-        wait_bar(&sm.o_done[blk], (C::kBlocks == 2 ? segments++ : cnt - 1) & 1u, &sm.dead, c.status);
+        wait_warp(&sm.o_done[blk], (C::kBlocks == 2 ? segments++ : cnt - 1) & 1u);
         fence_after_sync();
         if (C::kBlocks == 2) {
           if (releases && warp == 4 * blk && lane == 0) mbar_arrive(&sm.v_empty[v_out.stage]);
@@ -1095,13 +1116,13 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
         fence_before_sync();           // O has been read before the next segment's p_ready
         __syncwarp();
         const SegDesc& next = seg_wait(ahead_seg);
-        if (active(next)) load_q(next);
+        if (!warp_dead() && active(next)) load_q(next);
       }
       // both blocks are done with the notes on non-finite values
-      if (bar_any(1, C::kSoftWarps * 32, *(volatile int*)&sm.any_bad != 0)) {
+      if (bar_any(1, C::kSoftWarps * 32, *(volatile int*)&sm.any_bad != 0 || dead())) {
         for (int i = tid; i < D; i += C::kSoftWarps * 32) sm.bad[i] = Q8 ? INT32_MAX : Notes::kNone;
         if (tid == 0) sm.any_bad = 0;
-        asm volatile("bar.sync 1, %0;\n" ::"n"(C::kSoftWarps * 32) : "memory");
+        stop = bar_any(1, C::kSoftWarps * 32, dead());
       }
       seg_done(seg);
     }
@@ -1109,6 +1130,7 @@ chunk_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, in
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  if (tid == 0 && dead()) set_status(c.status, GDN_STATUS_TIMEOUT);
   if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
 }
 

@@ -183,16 +183,6 @@ __device__ __forceinline__ void cp_async16_mbar(uint32_t dst, const void* src, b
                : "memory");
 }
 
-// A bounded wait: a timeout marks the CTA dead, after which no wait blocks and the (wrong) results
-// are flagged by the status bit.
-__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
-  if (*dead) return;
-  if (!mbar_wait(bar, parity)) {
-    *dead = 1;
-    set_status(status, GDN_STATUS_TIMEOUT);
-  }
-}
-
 template <int D, bool Q8, int NT>
 __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, RowsCfg<D, Q8, NT>::kCtas)
 rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int fix, int least,
@@ -249,9 +239,9 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
     SegIter<R, TK> it;
     Segment sg;
     sg.split = false;
-    bool first = true;
+    bool first = true, alive = true;
     if (!values) it.start(&b, c.page_shift, c.H, a.g, fix, pieces, cta, sm.scan.at);
-    while (true) {
+    while (alive) {
       // the keys' producer walks the piece, for all
       SegDesc d = {};
       d.n = -1;
@@ -259,26 +249,27 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         bool more = it.next(&sg);
         while (more && idle(sg)) more = it.next(&sg);
         if (more) d = describe<R>(sg, a.g);
-        wait_or_die(&sm.seg_empty[seg], seg_phase ^ 1u, &sm.dead, c.status);
-        if (lane == 0) {
+        alive = wait_bar(&sm.seg_empty[seg], seg_phase ^ 1u, &sm.dead, c.status);
+        if (alive && lane == 0) {
           sm.segs[seg] = d;
           mbar_arrive(&sm.seg_full[seg]);
         }
       } else {
-        wait_or_die(&sm.seg_full[seg], seg_phase, &sm.dead, c.status);
+        alive = wait_bar(&sm.seg_full[seg], seg_phase, &sm.dead, c.status);
         d = sm.segs[seg];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.seg_empty[seg]);
+        if (alive && lane == 0) mbar_arrive(&sm.seg_empty[seg]);
       }
       __syncwarp();
       seg_step();
-      if (d.n < 0) break;
+      if (!alive || d.n < 0) break;
       if (d.n == 0) continue;
       const int tb = d.ta + d.n, keys = d.keys;
       // The queries' place is free when the tile before has been scored: after what the ring takes, or
       // (the piece's first tile) at once (23 sequences of up to 1054, 64 heads over 8 x 64 of 8 bits: 17.9 -> 15.8 us).
       auto load_queries = [&]() {
-        wait_or_die(&sm.q_empty, q_phase ^ 1u, &sm.dead, c.status);
+        alive = wait_bar(&sm.q_empty, q_phase ^ 1u, &sm.dead, c.status);
+        if (!alive) return;
         q_phase ^= 1u;
         if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)d.rows * 2 * D);
         __syncwarp();
@@ -299,11 +290,12 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       const int box = min(1 << c.page_shift, TK);
       int k0 = d.ta * TK + (lane % kLanes) * 16;
       int page = k0 < keys ? __ldg(table + (k0 >> c.page_shift)) : 0;
-      for (int i = d.ta; i < tb; ++i) {
+      for (int i = d.ta; i < tb && alive; ++i) {
         const int k1 = k0 + TK;
         int page_next = 0;
         if (i + 1 < tb && k1 < keys) page_next = __ldg(table + (k1 >> c.page_shift));
-        wait_or_die(&sm.empty[stage], phase ^ 1u, &sm.dead, c.status);
+        alive = wait_bar(&sm.empty[stage], phase ^ 1u, &sm.dead, c.status);
+        if (!alive) break;
         uint64_t* full = &sm.full[stage];
         const int live = (min(TK, keys - i * TK) + box - 1) / box;            // boxes
         if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(live * box * D * C::kElem));
@@ -329,8 +321,13 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
       }
     }
+    // no copy outlives the CTA, whoever has stopped waiting for it
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    drain_ring<C::kStages>(sm.full, stage, phase);
+    if (values) mbar_wait(&sm.q_full, q_phase ^ 1u, kDrainNs);
     // the piece's last tile may be shared with the next ones
-    if (!values && lane == 0) Partials<R, D>::note(a.ws, grid, cta, a.g, &sg, sg.split ? it.sharing(sg.nt) : 0);
+    if (!values && lane == 0)
+      Partials<R, D>::note(a.ws, grid, cta, a.g, &sg, alive && sg.split ? it.sharing(sg.nt) : 0);
     return;
   }
 
@@ -348,13 +345,18 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
   }
   int stage = 0;
   uint32_t phase = 0, q_phase = 0;
-  while (true) {
-    wait_or_die(&sm.seg_full[seg], seg_phase, &sm.dead, c.status);
-    const SegDesc sg = sm.segs[seg];
+  bool alive = true;
+  SegDesc sg;
+  // The next segment, for all consumers or for none.
+  auto next_segment = [&]() {
+    alive = wait_bar(&sm.seg_full[seg], seg_phase, &sm.dead, c.status) && alive;
+    sg = sm.segs[seg];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.seg_empty[seg]);
+    if (alive && lane == 0) mbar_arrive(&sm.seg_empty[seg]);
     seg_step();
-    if (sg.n < 0) break;
+    return !bar_any(1, NC, !alive) && sg.n >= 0;
+  };
+  for (bool more = next_segment(); more; more = next_segment()) {
     const SeqInfo info{sg.row0, sg.tokens, sg.len};
     const int row_base = sg.tile * R, rows = sg.rows, keys = sg.keys;
     if (sg.n == 0) {
@@ -372,7 +374,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       continue;
     }
     const int before = info.len - info.tokens;          // position of the first new token
-    wait_or_die(&sm.q_full, q_phase, &sm.dead, c.status);
+    alive = alive && wait_one(&sm.q_full, q_phase, &sm.dead, c.status);
     q_phase ^= 1u;
     if constexpr (Q8) {
       // A warp splits some rows into their parts (see split_e4m3), a lane some columns of them.
@@ -409,7 +411,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         }
       }
       bar_sync(1, NC);
-      if (lane == 0) mbar_arrive(&sm.q_empty);
+      if (alive && lane == 0) mbar_arrive(&sm.q_empty);
     }
     // Query operands of k-step ks and row tile nt: column g is the row, and the columns of the
     // k-step are 16 ks + 2 t, + 1, + 8, + 9; for 8-bit keys (k-step (part, ks)) the eight from
@@ -455,7 +457,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
 
     for (int i = sg.ta; i < sg.ta + sg.n; ++i) {
       const int st = stage;
-      wait_or_die(&sm.full[st], phase, &sm.dead, c.status);
+      alive = alive && wait_one(&sm.full[st], phase, &sm.dead, c.status);
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
       const int k0 = i * TK + warp * G * 16;
       if (k0 < keys) {
@@ -785,10 +787,10 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[st]);
+      if (alive && lane == 0) mbar_arrive(&sm.empty[st]);
     }
 
-    if (!Q8 && lane == 0) mbar_arrive(&sm.q_empty);
+    if (!Q8 && alive && lane == 0) mbar_arrive(&sm.q_empty);
 
     // ---- the warps' results of this tile become one
 #pragma unroll
@@ -869,7 +871,7 @@ rows_kernel(const KvView c, const KvBatchView b, const AttnArgs a, int grid, int
       }
       if (ch + 1 < D / C::kChunk) bar_sync(1, NC);
     }
-    bar_sync(1, NC);
+    // (next_segment has the barrier that frees the warps' results)
   }
 }
 
