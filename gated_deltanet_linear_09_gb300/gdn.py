@@ -8,6 +8,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -202,6 +203,16 @@ def _stream(stream):
 def stream_handle(stream=None) -> int:
     """The cudaStream_t of a torch stream (None: the current one)."""
     return _stream(stream)
+
+
+def on_stream(stream=None):
+    """A context in which this stream (None, a torch stream or a cudaStream_t) is the current one, so
+    that memory allocated in it is the stream's."""
+    if stream is None or _stream(stream) == _stream(None):
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def act_code(dtype) -> int:

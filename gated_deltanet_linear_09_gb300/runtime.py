@@ -2,6 +2,10 @@
 
 Allocation of the weights, the state pool and the prefill workspace happens here (torch owns
 device memory); every computation is a call into libgdn.so through ``gdn``.
+
+``stream`` (None: the current one) is where a call runs.  What a call allocates belongs to that
+stream, as under ``torch.cuda.stream``; ordering it with others, and ``record_stream`` where another
+stream uses a tensor, are the caller's.
 """
 from __future__ import annotations
 
@@ -21,12 +25,21 @@ def to_device(x: np.ndarray, dtype, device="cuda") -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(device=device, dtype=dtype)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory of the stream that is to write it: the allocator gives freed bytes to their stream's next
+    tensor, whatever another stream still does with them."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with gdn.on_stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def pack_weight(w: torch.Tensor, stream=None) -> torch.Tensor:
     """A bf16 linear weight [N][K] on the device -> its packed tile layout (uint8 tensor)."""
     nbytes = gdn.gdn_proj_packed_bytes(w.shape[0], w.shape[1])
     if nbytes == 0:
         raise ValueError(f"cannot pack a weight of shape {tuple(w.shape)} (K must be a multiple of 64)")
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
+    packed = _empty((nbytes,), torch.uint8, w.device, stream)
     gdn.gdn_proj_pack(w, packed, stream)
     return packed
 
@@ -67,15 +80,14 @@ class GatedDeltaNetLayer:
 
     def decode_step(self, slot_idx: torch.Tensor, qkv, z, a, b, out=None, stream=None):
         if out is None:
-            out = torch.empty((slot_idx.shape[0], self.geo.zdim), dtype=self.act, device=self.device)
+            out = _empty((slot_idx.shape[0], self.geo.zdim), self.act, self.device, stream)
         gdn.gdn_decode_step(self.dims, self.w, self.pool, slot_idx, qkv, z, a, b, out, stream)
         return out
 
     def decode_multi(self, slot_idx: torch.Tensor, qkv, z, a, b, out=None, stream=None):
         """T consecutive tokens per row: qkv [B][T][Cqkv], z [B][T][Hv*dv], a/b [B][T][Hv]."""
         if out is None:
-            out = torch.empty((qkv.shape[0], qkv.shape[1], self.geo.zdim), dtype=self.act,
-                              device=self.device)
+            out = _empty((qkv.shape[0], qkv.shape[1], self.geo.zdim), self.act, self.device, stream)
         gdn.gdn_decode_multi(self.dims, self.w, self.pool, slot_idx, qkv, z, a, b, out, stream)
         return out
 
@@ -84,10 +96,8 @@ class GatedDeltaNetLayer:
         (pack_weight of [Cqkv + Hv*dv + 2*Hv][H]): returns the step inputs qkv, z, a, b."""
         rows, g = hidden.shape[0], self.geo
         dev = hidden.device
-        t = {"qkv": torch.empty((rows, g.cqkv), dtype=torch.bfloat16, device=dev),
-             "z": torch.empty((rows, g.zdim), dtype=torch.bfloat16, device=dev),
-             "a": torch.empty((rows, g.Hv), dtype=torch.bfloat16, device=dev),
-             "b": torch.empty((rows, g.Hv), dtype=torch.bfloat16, device=dev)}
+        t = {k: _empty((rows, n), torch.bfloat16, dev, stream)
+             for k, n in (("qkv", g.cqkv), ("z", g.zdim), ("a", g.Hv), ("b", g.Hv))}
         gdn.gdn_in_proj(self.dims, hidden, w_in_packed, t["qkv"], t["z"], t["b"], t["a"],
                         self.status, stream)
         return t
@@ -97,23 +107,23 @@ class GatedDeltaNetLayer:
         """Output projection of the step's bf16 output [rows][Hv*dv] through the packed
         out_proj weight (pack_weight of [hidden_size][Hv*dv])."""
         if y is None:
-            y = torch.empty((out.shape[0], hidden_size), dtype=torch.bfloat16, device=out.device)
+            y = _empty((out.shape[0], hidden_size), torch.bfloat16, out.device, stream)
         gdn.gdn_out_proj(self.dims, out, w_out_packed, y, self.status, stream)
         return y
 
     def conv1d_update(self, slot_idx: torch.Tensor, qkv_in, out=None, stream=None):
         if out is None:
-            out = torch.empty_like(qkv_in)
+            out = _empty(qkv_in.shape, qkv_in.dtype, qkv_in.device, stream)
         gdn.gdn_conv1d_update(self.dims, self.w, self.pool, slot_idx, qkv_in, out, stream)
         return out
 
-    def workspace(self, num_seqs: int, total_tokens: int) -> torch.Tensor:
+    def workspace(self, num_seqs: int, total_tokens: int, stream=None) -> torch.Tensor:
         need = gdn.gdn_prefill_workspace_bytes(self.dims, num_seqs, total_tokens)
         if self.ws_cap is not None:
             # head dims 128: the prefill runs in windows of whole chunks that fit the workspace
             need = max(gdn.gdn_prefill_workspace_bytes(self.dims, 1, 1), min(need, self.ws_cap))
         if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            self._ws = _empty((max(need, 256),), torch.uint8, self.device, stream)
         return self._ws[:max(need, 256)]
 
     def prefill(self, cu_seqlens, slot_idx, has_init, qkv, z, a, b, out=None, stream=None):
@@ -121,8 +131,8 @@ class GatedDeltaNetLayer:
         total = qkv.shape[0]
         n = slot_idx.shape[0]
         if out is None:
-            out = torch.empty((total, self.geo.zdim), dtype=self.act, device=self.device)
-        ws = self.workspace(n, total)
+            out = _empty((total, self.geo.zdim), self.act, self.device, stream)
+        ws = self.workspace(n, total, stream)
         gdn.gdn_prefill_chunked(self.dims, self.w, self.pool, cu_seqlens, slot_idx, has_init, n,
                                 total, qkv, z, a, b, out, ws, stream)
         return out
@@ -202,13 +212,12 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant="none"
     rows, n = shape
     scales = total = None
     if kind == gdn.GDN_NORM_ACT:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
+        y = _empty(shape, dtype, x.device, stream)
     else:
-        y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scales = torch.empty((rows, 1 if quant == "row" else (n + 127) // 128), dtype=torch.float32,
-                             device=x.device)
+        y = _empty(shape, torch.float8_e4m3fn, x.device, stream)
+        scales = _empty((rows, 1 if quant == "row" else (n + 127) // 128), torch.float32, x.device, stream)
     if residual is not None:
-        total = torch.empty(shape, dtype=dtype, device=x.device)
+        total = _empty(shape, dtype, x.device, stream)
     gdn.gdn_rms_norm(x, weight, y, residual, total, scales, weight_offset, eps, kind, stream)
     return y, scales, total
 
@@ -278,7 +287,7 @@ class PagedKVCache:
             need = gdn.gdn_paged_attention_workspace_bytes(self.c, num_q_heads)
             if need == 0:
                 raise ValueError(f"{num_q_heads} query heads over this cache are not supported")
-            ws = self._ws[key] = torch.empty(need, dtype=torch.uint8, device=self.k_pages.device)
+            ws = self._ws[key] = _empty((need,), torch.uint8, self.device, stream)
         return ws
 
     def _check(self, t, batch, what):
@@ -300,11 +309,11 @@ class PagedKVCache:
         """The batch's tokens' keys and values back as bf16 (k, v)."""
         shape = (batch.total_tokens, self.num_kv_heads, self.head_dim)
         if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            k = _empty(shape, torch.bfloat16, self.device, stream)
         elif k.shape != shape or k.dtype != torch.bfloat16 or not k.is_contiguous():
             raise ValueError("k: contiguous bf16 [total_tokens][num_kv_heads][head_dim]")
         if v is None:
-            v = torch.empty_like(k)
+            v = _empty(shape, torch.bfloat16, self.device, stream)
         elif v.shape != shape or v.dtype != torch.bfloat16 or not v.is_contiguous():
             raise ValueError("v: contiguous bf16 [total_tokens][num_kv_heads][head_dim]")
         if batch.total_tokens:
@@ -318,7 +327,7 @@ class PagedKVCache:
         if gate is not None and self._check(gate, batch, "gate") != shape:
             raise ValueError("gate must have the shape of q")
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            out = _empty(shape, torch.bfloat16, self.device, stream)
         elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
             raise ValueError("out: contiguous bf16 with the shape of q")
         if batch.total_tokens:

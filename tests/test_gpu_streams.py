@@ -1,0 +1,47 @@
+"""Calls on a stream that is not the current one, which lags behind while the current stream's
+allocations go on."""
+import pytest
+import torch
+
+import paged_ref as ref
+from gated_deltanet_linear_09_gb300 import runtime
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def late():
+    """A stream whose next work starts some milliseconds from now."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    return s
+
+
+def _overwrite(shapes):
+    """New tensors of the current stream, in whatever memory it thinks free."""
+    for _ in range(4):
+        for shape, dtype in shapes:
+            torch.full(shape, 7, dtype=dtype, device="cuda")
+
+
+def test_outputs_of_a_late_stream(late):
+    case = ref.Case([3, 1], [200, 90], 2, 64, 16, True, seed=61)
+    cache, b = case.filled_cache(runtime), case.device_batch(runtime)
+    q = torch.randn((case.tokens, 8, 64), device="cuda").to(torch.bfloat16)
+    x, w = torch.randn((512, 256), device="cuda"), torch.randn(256, device="cuda")
+    want = [*(t for t in runtime.rms_norm(x, w, residual=x, quant="block")), *cache.read(b), cache.attend(b, q)]
+    late.wait_stream(torch.cuda.current_stream())
+    got = []
+    for call in (lambda: runtime.rms_norm(x, w, residual=x, quant="block", stream=late), lambda: cache.read(b, stream=late),
+                 lambda: (cache.attend(b, q, stream=late),)):
+        out = call()
+        with torch.cuda.stream(late):
+            got += [t.clone() for t in out]
+        shapes = [(t.shape, torch.uint8 if t.element_size() == 1 else t.dtype) for t in out]
+        del out                         # the late stream has yet to write and copy it
+        _overwrite(shapes)
+    late.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

@@ -1,6 +1,9 @@
 """What the Python calls hand to the library, and which tensors they take (no GPU: nothing is launched)."""
+import contextlib
 import ctypes
+import types
 
+import pytest
 import torch
 
 from gated_deltanet_linear_09_gb300 import build as gbuild
@@ -33,3 +36,55 @@ def test_table_width_is_checked():
     assert read(table_cols=-1) == -1
     assert read(table_ld=0, table_cols=3, block_table=None) == -1
     assert read(table_ld=0, table_cols=3) == -7                     # (on to the next check: k is misaligned)
+
+
+class Streams:
+    """Stands in for torch's streams: which one is current, and on which one each tensor was allocated."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.allocated, self.launched = 0, [], []
+        empty = torch.empty
+
+        @contextlib.contextmanager
+        def stream(s):
+            before, self.current = self.current, s.cuda_stream
+            yield
+            self.current = before
+
+        def recorded(*a, **kw):
+            self.allocated.append(self.current)
+            return empty(*a, **kw)
+        monkeypatch.setattr(torch.cuda, "stream", stream)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: types.SimpleNamespace(cuda_stream=handle))
+        monkeypatch.setattr(torch, "empty", recorded)
+        monkeypatch.setattr(gdn, "_stream", lambda s=None: self.current if s is None else s if isinstance(s, int) else s.cuda_stream)
+        for name in gdn.EXPORTED:
+            if hasattr(gdn, name) and not name.endswith("bytes"):
+                monkeypatch.setattr(gdn, name, lambda *a, name=name: self.launched.append((name, a)))
+        monkeypatch.setattr(gdn, "gdn_paged_attention_workspace_bytes", lambda *a: 512)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    return Streams(monkeypatch)
+
+
+SIDE = types.SimpleNamespace(cuda_stream=7)
+
+
+def test_outputs_belong_to_the_stream_that_writes_them(streams):
+    """What a call on another stream allocates is that stream's memory, and the current stream stays."""
+    bf = dict(dtype=torch.bfloat16)
+    x, w = torch.zeros((4, 64), **bf), torch.zeros(64, **bf)
+    cache = runtime.PagedKVCache(4, 16, 2, 64, device="cpu")
+    batch = runtime.KVBatch(ints(3), ints(2), ints(2, 2), 4, 2)
+    q = torch.zeros((4, 4, 64), **bf)
+    calls = [lambda s: runtime.rms_norm(x, w, residual=x, stream=s), lambda s: runtime.rms_norm(x, w, quant="row", stream=s),
+             lambda s: cache.read(batch, stream=s), lambda s: cache.attend(batch, q, stream=s),
+             lambda s: cache.workspace(4, s)]
+    for call in calls:
+        for s, want in ((None, 0), (SIDE, 7), (types.SimpleNamespace(cuda_stream=0), 0)):
+            cache._ws.clear()
+            streams.allocated.clear()
+            call(s)
+            assert streams.allocated and set(streams.allocated) == {want} and streams.current == 0
