@@ -31,26 +31,30 @@ class AttentionLayer:
         self.q_norm, self.k_norm = weights["q_norm"], weights["k_norm"]
         self.status = torch.zeros(1, dtype=torch.int32, device=cache.device)
 
-    def _linear(self, x, packed, widths, stream):
+    def _linear(self, x, packed, widths):
         outs = [torch.empty((x.shape[0], n), dtype=torch.bfloat16, device=x.device) for n in widths]
         route = gdn.make_route([(sum(widths[:i]), n, t) for i, (n, t) in enumerate(zip(widths, outs))])
-        gdn.gdn_linear_bf16(x, packed, sum(widths), route, 0, self.status, stream)
+        gdn.gdn_linear_bf16(x, packed, sum(widths), route, 0, self.status)
         return outs
 
     def forward(self, batch: KVBatch, x, rotate=None, stream=None):
         """x: normed hidden states bf16 [total_tokens][hidden].  rotate(q, k) -> (q, k) applies the
-        position embedding to [tokens][heads][D] tensors."""
+        position embedding to [tokens][heads][D] tensors, on the stream of the call."""
+        with gdn.on_stream(stream):
+            return self._forward(batch, x, rotate)
+
+    def _forward(self, batch, x, rotate):
         T, Hq, H, D = x.shape[0], self.Hq, self.H, self.D
-        qg, k, v = self._linear(x, self.w_in, [Hq * 2 * D, H * D, H * D], stream)
+        qg, k, v = self._linear(x, self.w_in, [Hq * 2 * D, H * D, H * D])
         qg = qg.view(T * Hq, 2 * D)
-        q, _, _ = rms_norm(qg[:, :D], self.q_norm, eps=self.eps, weight_offset=1.0, stream=stream)
-        k, _, _ = rms_norm(k.view(T * H, D), self.k_norm, eps=self.eps, weight_offset=1.0, stream=stream)
+        q, _, _ = rms_norm(qg[:, :D], self.q_norm, eps=self.eps, weight_offset=1.0)
+        k, _, _ = rms_norm(k.view(T * H, D), self.k_norm, eps=self.eps, weight_offset=1.0)
         q, k = q.view(T, Hq, D), k.view(T, H, D)
         if rotate is not None:
             q, k = rotate(q, k)
-        self.cache.append(batch, k, v.view(T, H, D), stream)
-        o = self.cache.attend(batch, q, gate=qg.view(T, Hq, 2 * D)[..., D:], stream=stream)
-        return self._linear(o.view(T, Hq * D), self.w_out, [self.hidden], stream)[0]
+        self.cache.append(batch, k, v.view(T, H, D))
+        o = self.cache.attend(batch, q, gate=qg.view(T, Hq, 2 * D)[..., D:])
+        return self._linear(o.view(T, Hq * D), self.w_out, [self.hidden])[0]
 
 
 class HybridPeriod:

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import paged_ref as ref
-from gated_deltanet_linear_09_gb300 import runtime
+from gated_deltanet_linear_09_gb300 import hybrid, runtime
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,30 @@ def test_outputs_of_a_late_stream(late):
     late.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_a_layer_on_a_late_stream(late):
+    """With a rotation, whose tensors are torch's: the same bits as on the current stream."""
+    n, hidden, new = 4, 128, [9, 1, 30, 4]
+    w = hybrid.attention_weights(hidden, 4, 2, 64, 62)
+    cu = [sum(new[:i]) for i in range(n + 1)]
+    table = torch.arange(n * 2, dtype=torch.int32, device="cuda").view(n, 2)
+    batch = runtime.KVBatch(torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                            torch.tensor(new, dtype=torch.int32, device="cuda"), table, cu[-1], max(new))
+    x = torch.randn((cu[-1], hidden), device="cuda").to(torch.bfloat16)
+
+    def rotate(q, k):
+        return q * 2, (k.float() * 0.5 + 1).to(torch.bfloat16)
+
+    def run(stream):
+        cache = runtime.PagedKVCache(n * 2, 16, 2, 64)
+        layer = hybrid.AttentionLayer(cache, 4, w)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        y = layer.forward(batch, x, rotate, stream=stream)
+        if stream is not None:
+            _overwrite([((cu[-1], c), torch.bfloat16) for c in (512, 256, 128, 128)])
+            stream.synchronize()
+        return y, cache.k_pages
+    for a, b in zip(run(None), run(late)):
+        assert torch.equal(a, b)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from gated_deltanet_linear_09_gb300 import build as gbuild
-from gated_deltanet_linear_09_gb300 import gdn, runtime
+from gated_deltanet_linear_09_gb300 import gdn, hybrid, runtime
 
 
 def ints(*shape):
@@ -88,3 +88,27 @@ def test_outputs_belong_to_the_stream_that_writes_them(streams):
             streams.allocated.clear()
             call(s)
             assert streams.allocated and set(streams.allocated) == {want} and streams.current == 0
+
+
+def test_the_layer_runs_on_one_stream(streams):
+    """Every allocation, launch and the rotation of a layer's call happen on the call's stream."""
+    bf = dict(dtype=torch.bfloat16)
+    cache = runtime.PagedKVCache(4, 16, 2, 64, device="cpu")
+    layer = hybrid.AttentionLayer.__new__(hybrid.AttentionLayer)
+    layer.cache, layer.Hq, layer.H, layer.D, layer.eps, layer.hidden = cache, 4, 2, 64, 1e-6, 32
+    layer.w_in = layer.w_out = layer.status = None
+    layer.q_norm = layer.k_norm = torch.zeros(64, **bf)
+    batch = runtime.KVBatch(ints(3), ints(2), ints(2, 2), 3, 2)
+    x, rotated = torch.zeros((3, 32), **bf), []
+
+    def rotate(q, k):
+        rotated.append(streams.current)
+        return q, k
+    for s, want in ((None, 0), (SIDE, 7)):
+        streams.allocated.clear()
+        streams.launched.clear()
+        layer.forward(batch, x, rotate, stream=s)
+        assert set(streams.allocated) == {want} and rotated.pop() == want and streams.current == 0
+        assert [n for n, _ in streams.launched] == ["gdn_linear_bf16", "gdn_rms_norm", "gdn_rms_norm", "gdn_kv_append",
+                                                    "gdn_paged_attention", "gdn_linear_bf16"]
+        assert {a[-1] for n, a in streams.launched if isinstance(a[-1], (int, types.SimpleNamespace))} <= {want}
