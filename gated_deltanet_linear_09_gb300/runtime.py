@@ -276,18 +276,25 @@ class PagedKVCache:
         self.device = k_pages.device
         self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
         self.c = gdn.make_kv_cache(k_pages, v_pages, k_scales, v_scales, self.status)
-        self._ws = {}
+        self._ws, self._ws_need = {}, {}
 
     def workspace(self, num_q_heads: int, stream=None) -> torch.Tensor:
         """The attention's workspace for this many query heads on this stream.  Calls on one stream
-        share it; a call that may overlap one of another stream has that stream's."""
-        key = (num_q_heads, gdn.stream_handle(stream))
-        ws = self._ws.get(key)
-        if ws is None:
+        share it, as long as the cache lives.  A call that is captured in a CUDA graph gets memory of the
+        graph's own: graphs captured on one stream may be replayed beside each other."""
+        need = self._ws_need.get(num_q_heads)
+        if need is None:
             need = gdn.gdn_paged_attention_workspace_bytes(self.c, num_q_heads)
             if need == 0:
                 raise ValueError(f"{num_q_heads} query heads over this cache are not supported")
-            ws = self._ws[key] = _empty((need,), torch.uint8, self.device, stream)
+            self._ws_need[num_q_heads] = need
+        with gdn.on_stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(need, dtype=torch.uint8, device=self.device)
+            key = gdn.stream_handle()
+            ws = self._ws.get(key)
+            if ws is None or ws.numel() < need:
+                ws = self._ws[key] = torch.empty(need, dtype=torch.uint8, device=self.device)
         return ws
 
     def _check(self, t, batch, what):
@@ -331,7 +338,6 @@ class PagedKVCache:
         elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
             raise ValueError("out: contiguous bf16 with the shape of q")
         if batch.total_tokens:
-            stream = gdn.stream_handle(stream)
             if workspace is None:
                 workspace = self.workspace(shape[1], stream)
             gdn.gdn_paged_attention(self.c, batch.c, q, out, workspace, gate, scale, stream)

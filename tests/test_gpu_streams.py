@@ -72,3 +72,37 @@ def test_a_layer_on_a_late_stream(late):
         return y, cache.k_pages
     for a, b in zip(run(None), run(late)):
         assert torch.equal(a, b)
+
+
+def test_graphs_replayed_beside_each_other():
+    """Two graphs over one cache, captured on the same stream, replayed on two, and eager calls on the
+    capture stream's workspace in between."""
+    case = ref.Case([1] * 6, [900, 3000, 17, 2500, 1, 1200], 2, 128, 32, False, seed=63)
+    cache, b = case.filled_cache(runtime), case.device_batch(runtime)
+    qs = [torch.randn((6, 8, 128), device="cuda").to(torch.bfloat16) for _ in range(3)]
+    want = [cache.attend(b, q).clone() for q in qs]
+    outs, graphs = [torch.empty_like(q) for q in qs], []
+    capture = torch.cuda.Stream()
+    capture.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(capture):
+        cache.attend(b, qs[2], out=outs[2])
+    torch.cuda.synchronize()
+    for q, o in zip(qs[:2], outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=capture):
+            for _ in range(5):
+                cache.attend(b, q, out=o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(capture):
+            cache.attend(b, qs[2], out=outs[2])
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)

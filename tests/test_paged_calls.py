@@ -62,6 +62,8 @@ class Streams:
             if hasattr(gdn, name) and not name.endswith("bytes"):
                 monkeypatch.setattr(gdn, name, lambda *a, name=name: self.launched.append((name, a)))
         monkeypatch.setattr(gdn, "gdn_paged_attention_workspace_bytes", lambda *a: 512)
+        self.capturing = False
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
 
 
 @pytest.fixture
@@ -112,3 +114,22 @@ def test_the_layer_runs_on_one_stream(streams):
         assert [n for n, _ in streams.launched] == ["gdn_linear_bf16", "gdn_rms_norm", "gdn_rms_norm", "gdn_kv_append",
                                                     "gdn_paged_attention", "gdn_linear_bf16"]
         assert {a[-1] for n, a in streams.launched if isinstance(a[-1], (int, types.SimpleNamespace))} <= {want}
+
+
+def test_workspaces_of_streams_and_graphs(streams):
+    """One for each stream, whatever the number of query heads; a captured call's is the graph's alone."""
+    cache = runtime.PagedKVCache(4, 16, 2, 64, device="cpu")
+    here, side = cache.workspace(4), cache.workspace(4, SIDE)
+    assert here is cache.workspace(8) and side is cache.workspace(2, SIDE) and here is not side
+    streams.capturing = True
+    a, b, c = cache.workspace(4), cache.workspace(4), cache.workspace(4, SIDE)
+    assert len({t.data_ptr() for t in (here, side, a, b, c)}) == 5
+    streams.capturing = False
+    assert cache.workspace(4) is here and cache.workspace(4, SIDE) is side and len(cache._ws) == 2
+    batch = runtime.KVBatch(ints(3), ints(2), ints(2, 2), 4, 2)
+    q, used = torch.zeros((4, 4, 64), dtype=torch.bfloat16), []
+    for streams.capturing in (False, True, True):
+        streams.launched.clear()
+        cache.attend(batch, q)
+        used.append(streams.launched[0][1][4])
+    assert used[0] is here and used[1] is not here and used[2] is not here
