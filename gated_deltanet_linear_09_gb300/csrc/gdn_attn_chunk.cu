@@ -1139,9 +1139,9 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   using C = ChunkCfg<D, Q8, B>;
   constexpr size_t smem = sizeof(ChunkSmem<D, Q8, B>);
   static_assert(smem <= 232448, "shared memory of a CTA");
-  static const cudaError_t set = cudaFuncSetAttribute(
-      chunk_kernel<D, Q8, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (set != cudaSuccess) return GDN_ERR_CUDA;
+  static OncePerDevice once;
+  int rc = raise_smem(once, chunk_kernel<D, Q8, B>, smem);
+  if (rc != GDN_OK) return rc;
   KvMaps maps;
   const int P = 1 << c.page_shift;
   if (!make_tile_maps(c, P < kKeys ? P : kKeys, Q8 ? C::kCols : 64, &maps)) return GDN_ERR_CUDA;
@@ -1152,7 +1152,7 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   const int base = D < 256 ? 512 : Q8 ? 896 : 640;
   const int grid = sms, fix = (base + (a.gate ? D / 2 : 0)) * a.g;
   const int least = 512 * a.g;
-  int rc = launch_dependent(chunk_kernel<D, Q8, B>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
+  rc = launch_dependent(chunk_kernel<D, Q8, B>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
   return launch_dependent(merge_kernel<C::kRows, D>, dim3((unsigned)(6 * sms)), kMergeWarps * 32, 0, stream, a, grid);

@@ -880,9 +880,9 @@ int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sm
   using C = RowsCfg<D, Q8, NT>;
   constexpr size_t smem = sizeof(RowsSmem<D, Q8, NT>);
   static_assert(smem <= 232448 && (smem + 1024) * C::kCtas <= 233472, "shared memory of an SM");
-  static const cudaError_t set = cudaFuncSetAttribute(
-      rows_kernel<D, Q8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (set != cudaSuccess) return GDN_ERR_CUDA;
+  static OncePerDevice once;
+  int rc = raise_smem(once, rows_kernel<D, Q8, NT>, smem);
+  if (rc != GDN_OK) return rc;
   KvMaps maps;
   const int P = 1 << c.page_shift;
   if (!make_kv_maps(c, P < C::kKeys ? P : C::kKeys, &maps)) return GDN_ERR_CUDA;
@@ -891,7 +891,7 @@ int launch_rows(const KvView& c, const KvBatchView& b, const AttnArgs& a, int sm
   // 195.)  And the fewest keys worth a piece of their own (777 keys: 14.7 us at 128, 15.5 at 256, 18.4 at 512).
   const int grid = rows_grid(D, sms), fix = (Q8 ? 384 : 128) * a.g;
   const int least = 128 * a.g;
-  int rc = launch_dependent(rows_kernel<D, Q8, NT>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
+  rc = launch_dependent(rows_kernel<D, Q8, NT>, dim3((unsigned)grid), C::kThreads, smem, stream, c, b, a, grid,
                             fix, least, maps);
   if (rc != GDN_OK) return rc;
   return launch_dependent(merge_kernel<C::kRows, D>, dim3((unsigned)(2 * sms)), kMergeWarps * 32, 0, stream, a, grid);

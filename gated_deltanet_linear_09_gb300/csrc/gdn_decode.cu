@@ -18,7 +18,6 @@
 // only the RMSNorm's sum over dv meets in shared memory, once, after the last V-head.
 // The kernel is a programmatic dependent launch: in a stream of decode steps the next step's
 // CTAs are placed while this one drains and wait for its completion before any read.
-#include <mutex>
 
 #include "gdn_internal.h"
 
@@ -351,17 +350,8 @@ int launch_decode_t(const KDims& d, const gdn_weights* w, const gdn_pool* pool,
                     const void* b, void* out, cudaStream_t stream) {
   const size_t smem = sizeof(float) * decode_float_count<DK, DV>(d.r) + sizeof(T) * (d.r + 1) * DV;
   auto kern = decode_kernel<DK, DV, T>;
-  // Raised once per kernel (to the per-block maximum), so that launches -- also those recorded
-  // into a CUDA graph -- never need to change the attribute.
-  static std::once_flag once;
-  static int attr_rc = 0;
-  std::call_once(once, [&] {
-    int dev = 0, optin = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess)
-      attr_rc = GDN_ERR_CUDA;
-  });
+  static OncePerDevice once;
+  const int attr_rc = raise_smem(once, kern, 0);
   if (attr_rc != 0) return attr_rc;
   if (smem > 227 * 1024) return GDN_ERR_TOO_LARGE;
   // programmatic stream serialization: the CTAs may be placed while the previous kernel of the

@@ -16,7 +16,6 @@
 // As in the single-token kernel, one CTA owns one (row, K-head) unit: the K-head's q and k conv
 // channels, the v channels of its r = Hv/Hk V-heads and their states, which keeps the conv-state
 // update race-free within one launch.
-#include <mutex>
 
 #include "gdn_internal.h"
 
@@ -353,16 +352,8 @@ int launch_multi_t(const KDims& d, const gdn_weights* w, const gdn_pool* pool,
   const size_t smem = sizeof(float) * ((size_t)TT * nch + (size_t)(kMW + 1) * 2 * TT * DV +
                                        2 * TT * TT + (size_t)d.r * (4 * TT + 2 * TT * TT));
   auto kern = decode_multi_kernel<DK, DV, T, NT>;
-  // raised once per kernel to the per-block maximum, so that captured launches never change it
-  static std::once_flag once;
-  static int attr_rc = 0;
-  std::call_once(once, [&] {
-    int dev = 0, optin = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess)
-      attr_rc = GDN_ERR_CUDA;
-  });
+  static OncePerDevice once;
+  const int attr_rc = raise_smem(once, kern, 0);
   if (attr_rc != 0) return attr_rc;
   if (smem > 227 * 1024) return GDN_ERR_TOO_LARGE;
   // a programmatic dependent launch: the CTAs may be placed while the previous kernel of the

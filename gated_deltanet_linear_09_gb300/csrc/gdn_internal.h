@@ -2,6 +2,7 @@
 #pragma once
 
 #include "gdn_common.cuh"
+#include "gdn_device.h"
 
 // NVTX ranges around the C-ABI calls: a profiler or tracer attached to the process sees each call
 // as a named range on the calling thread (with none attached a range costs a few nanoseconds).
@@ -96,6 +97,21 @@ size_t proj_packed_bytes(int N, int K);
 int launch_proj_pack(const void* w, int N, int K, void* packed, cudaStream_t stream);
 int launch_proj(const void* x, const void* wp, int M, int N, int K, int ks, const ProjRoute& route,
                 int32_t* status, cudaStream_t stream);
+
+// Raises a kernel's dynamic shared memory to `bytes` (0: to the most a block can have) on the current
+// device, once on each, so that launches -- also those recorded into a CUDA graph -- need not.
+template <typename K>
+int raise_smem(OncePerDevice& once, K kern, size_t bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  return once.run(dev, [&]() -> int {
+    int most = (int)bytes;
+    if (bytes == 0 && cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+      return GDN_ERR_CUDA;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess ? GDN_OK
+                                                                                                  : GDN_ERR_CUDA;
+  });
+}
 
 // RMSNorm with the residual's addition (kind: a gdn_norm_out).
 int launch_rms_norm(const void* x, long long x_ld, const void* residual, long long residual_ld,

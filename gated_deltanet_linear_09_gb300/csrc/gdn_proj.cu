@@ -414,17 +414,10 @@ int launch_proj_pack(const void* w, int N, int K, void* packed, cudaStream_t str
 
 int launch_proj(const void* x, const void* wp, int M, int N, int K, int ks, const ProjRoute& route,
                 int32_t* status, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(proj_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)ProjCfg<64>::SMEM);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(proj_kernel<PROWS_WIDE>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)ProjCfg<PROWS_WIDE>::SMEM);
-  });
-  if (attr_err != cudaSuccess) return GDN_ERR_CUDA;
+  static OncePerDevice once, once_wide;
+  int rc = raise_smem(once, proj_kernel<64>, ProjCfg<64>::SMEM);
+  if (rc == GDN_OK) rc = raise_smem(once_wide, proj_kernel<PROWS_WIDE>, ProjCfg<PROWS_WIDE>::SMEM);
+  if (rc != GDN_OK) return rc;
   // unsplit launches over many rows take the wide form
   const bool wide = ks == 1 && M >= WIDE_MIN_ROWS;
   const int pn = wide ? PROWS_WIDE : ProjCfg<64>::PN;

@@ -1,6 +1,8 @@
 """What the Python calls hand to the library, and which tensors they take (no GPU: nothing is launched)."""
 import contextlib
 import ctypes
+import os
+import subprocess
 import types
 
 import pytest
@@ -133,3 +135,12 @@ def test_workspaces_of_streams_and_graphs(streams):
         cache.attend(batch, q)
         used.append(streams.launched[0][1][4])
     assert used[0] is here and used[1] is not here and used[2] is not here
+
+
+def test_kernel_attributes_are_set_on_every_device(tmp_path):
+    """The guard that the launches share: once on each device, a failure not kept."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "once_check")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", gbuild.CSRC, "-o", exe,
+                    os.path.join(here, "csrc", "once_check.cc")], check=True)
+    assert subprocess.run([exe], capture_output=True, text=True).stdout == "ok\n"
