@@ -405,9 +405,11 @@ def gdn_rms_norm(x, weight, y, residual=None, sum_out=None, scales=None, weight_
 
 def gdn_kv_append(cache, batch, k, v, stream=None):
     """k, v: bf16 [tokens][heads][dim], token rows may be strided."""
+    tokens, heads, dim = k.shape
+    one = heads * dim                 # the stride of a dimension of size one says nothing
     _check("gdn_kv_append", load().gdn_kv_append(
-        ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), k.stride(0), v.data_ptr(),
-        v.stride(0), _stream(stream)))
+        ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), k.stride(0) if tokens > 1 else one,
+        v.data_ptr(), v.stride(0) if tokens > 1 else one, _stream(stream)))
 
 
 def gdn_kv_read(cache, batch, k, v, stream=None):
@@ -423,10 +425,15 @@ def gdn_paged_attention_workspace_bytes(cache, num_q_heads: int) -> int:
 def gdn_paged_attention(cache, batch, q, out, workspace, gate=None, scale=0.0, stream=None):
     """q, gate: bf16 [tokens][heads][dim] (tokens and heads may be strided), out dense, workspace
     uint8."""
+    tokens, heads, dim = q.shape
     q_ld, q_head_ld, _ = q.stride()
     g_ld, g_head_ld, _ = (0, 0, 0) if gate is None else gate.stride()
+    if tokens == 1:                   # the stride of a dimension of size one says nothing
+        q_ld = g_ld = heads * dim
+    if heads == 1:
+        q_head_ld = g_head_ld = dim
     rc = load().gdn_paged_attention(
-        ctypes.byref(cache), ctypes.byref(batch), q.size(1), q.data_ptr(), q_ld, q_head_ld,
+        ctypes.byref(cache), ctypes.byref(batch), heads, q.data_ptr(), q_ld, q_head_ld,
         None if gate is None else gate.data_ptr(), g_ld, g_head_ld, scale, out.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _stream(stream))
     if rc:

@@ -195,6 +195,11 @@ class DecodeGraphs:
 _NORM_KINDS = {"none": gdn.GDN_NORM_ACT, "row": gdn.GDN_NORM_E4M3_ROW, "block": gdn.GDN_NORM_E4M3_BLOCK}
 
 
+def _dense_rows(t) -> bool:
+    """The last dimension's elements are adjacent (one element always is)."""
+    return t.stride(-1) == 1 or t.shape[-1] <= 1
+
+
 def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant="none", stream=None):
     """RMSNorm of x (+ residual), rows [rows][n] of bf16 or f32: returns (y, scales, total).
 
@@ -202,11 +207,11 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant="none"
     the activation dtype, scales None; "row" / "block": y float8_e4m3fn with f32 scales per row
     [rows][1] or per 128 columns [rows][ceil(n / 128)]."""
     shape, dtype = x.shape, x.dtype
-    if len(shape) != 2 or x.stride(1) != 1 or dtype != weight.dtype or weight.shape != shape[1:] or \
-            weight.stride(0) != 1:
+    if len(shape) != 2 or not _dense_rows(x) or dtype != weight.dtype or weight.shape != shape[1:] or \
+            not _dense_rows(weight):
         raise ValueError("rms_norm takes rows [rows][n] and a weight [n] of one dtype")
     if residual is not None and (residual.shape != shape or residual.dtype != dtype or
-                                 residual.stride(1) != 1):
+                                 not _dense_rows(residual)):
         raise ValueError("residual must have the shape and dtype of x")
     kind = _NORM_KINDS[quant]
     rows, n = shape
@@ -229,7 +234,7 @@ class KVBatch:
 
     def __init__(self, cu_seqlens, kv_lens, block_table, total_tokens: int, max_tokens: int = 0):
         for t in (cu_seqlens, kv_lens, block_table):
-            if t.dtype != torch.int32 or (t.numel() > 1 and t.stride(-1) != 1):
+            if t.dtype != torch.int32 or not _dense_rows(t):
                 raise ValueError("cu_seqlens, kv_lens and block_table are int32 with contiguous rows")
         if block_table.dim() != 2 or cu_seqlens.shape[0] != kv_lens.shape[0] + 1 or \
                 block_table.shape[0] != kv_lens.shape[0]:
@@ -307,7 +312,8 @@ class PagedKVCache:
     def append(self, batch: KVBatch, k, v, stream=None):
         """Stores the new tokens' keys and values, bf16 [total_tokens][num_kv_heads][head_dim]."""
         for t, what in ((k, "k"), (v, "v")):
-            if self._check(t, batch, what)[1] != self.num_kv_heads or t.stride(1) != self.head_dim:
+            if self._check(t, batch, what)[1] != self.num_kv_heads or \
+                    (self.num_kv_heads > 1 and t.stride(1) != self.head_dim):
                 raise ValueError(f"{what}: {self.num_kv_heads} adjacent heads expected")
         if batch.total_tokens:
             gdn.gdn_kv_append(self.c, batch.c, k, v, stream)

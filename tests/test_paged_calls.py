@@ -144,3 +144,48 @@ def test_kernel_attributes_are_set_on_every_device(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", gbuild.CSRC, "-o", exe,
                     os.path.join(here, "csrc", "once_check.cc")], check=True)
     assert subprocess.run([exe], capture_output=True, text=True).stdout == "ok\n"
+
+
+def test_strides_of_single_elements_are_not_looked_at(streams):
+    """One token, head, column or page: any stride is as good as the dense one."""
+    bf = dict(dtype=torch.bfloat16)
+    one = runtime.KVBatch(ints(2), ints(1), ints(1, 2), 1, 1)
+    cache = runtime.PagedKVCache(4, 16, 2, 64, device="cpu")
+    x = torch.zeros((2, 1, 64), **bf).transpose(0, 1)                    # head-major: strides 64, 64, 1
+    cache.append(one, x, torch.zeros((1, 2, 64), **bf).as_strided((1, 2, 64), (8, 64, 1)))
+    name, a = streams.launched[-1]
+    assert name == "gdn_kv_append"
+    single = runtime.PagedKVCache(4, 16, 1, 64, device="cpu")
+    two = runtime.KVBatch(ints(2), ints(1), ints(1, 2), 2, 2)
+    single.append(two, torch.zeros((2, 1, 64), **bf).as_strided((2, 1, 64), (64, 1, 1)), torch.zeros((2, 1, 64), **bf))
+    runtime.rms_norm(torch.zeros((1, 5), **bf).t(), torch.zeros(2, **bf)[::2])
+    runtime.KVBatch(ints(3), ints(2), ints(2, 4)[:, ::4], 2)
+    with pytest.raises(ValueError):
+        runtime.rms_norm(torch.zeros((4, 5), **bf).t(), torch.zeros(4, **bf))
+
+
+def test_row_distances_handed_over(monkeypatch):
+    """What the library sees of such tensors."""
+    seen = {}
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.update({name: a}) or 0
+    monkeypatch.setattr(gdn, "load", lambda: Lib())
+    monkeypatch.setattr(gdn, "_stream", lambda s: 0)
+    c = gdn.gdn_kv_cache(num_kv_heads=2, head_dim=64)
+    b = gdn.gdn_kv_batch()
+    x = torch.zeros((2, 1, 64), dtype=torch.bfloat16).transpose(0, 1)
+    gdn.gdn_kv_append(c, b, x, x)
+    assert seen["gdn_kv_append"][3] == seen["gdn_kv_append"][5] == 128
+    two = torch.zeros((3, 400), dtype=torch.bfloat16)[:, :128].view(3, 2, 64)
+    gdn.gdn_kv_append(c, b, two, two)
+    assert seen["gdn_kv_append"][3] == seen["gdn_kv_append"][5] == 400
+    ws = torch.zeros(1, dtype=torch.uint8)
+    gdn.gdn_paged_attention(c, b, x, x, ws, gate=x)
+    assert seen["gdn_paged_attention"][4:6] == (128, 64) and seen["gdn_paged_attention"][7:9] == (128, 64)
+    single = torch.zeros((3, 1, 64), dtype=torch.bfloat16).as_strided((3, 1, 64), (64, 1, 1))
+    gdn.gdn_paged_attention(c, b, single, single, ws)
+    assert seen["gdn_paged_attention"][4:6] == (64, 64)
+    gdn.gdn_paged_attention(c, b, two, two, ws)
+    assert seen["gdn_paged_attention"][4:6] == (400, 64)
