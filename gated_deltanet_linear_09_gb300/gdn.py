@@ -371,6 +371,11 @@ def gdn_out_proj(dims, out, w_out_packed, y, status=None, stream=None):
         _stream(stream)))
 
 
+def _on_host(fn: str):
+    """The library takes addresses as they are: one of host memory would end in a GPU fault."""
+    raise ValueError(f"{fn}: its tensors are not on a GPU")
+
+
 def make_kv_cache(k_pages, v_pages, k_scales=None, v_scales=None, status=None) -> gdn_kv_cache:
     """Pages [num_pages][num_kv_heads][page_size][head_dim] (bf16 or float8_e4m3fn) as a struct."""
     np_, heads, page, dim = (int(x) for x in k_pages.shape)
@@ -394,6 +399,8 @@ def gdn_rms_norm(x, weight, y, residual=None, sum_out=None, scales=None, weight_
                  out_kind=GDN_NORM_ACT, stream=None):
     """x, residual [rows][n] (rows may be strided), y / sum_out dense [rows][n], scales f32."""
     rows, n = x.shape
+    if not x.is_cuda:
+        _on_host("gdn_rms_norm")
     rc = load().gdn_rms_norm(
         x.data_ptr(), x.stride(0) if rows > 1 else n, _ptr(residual),
         0 if residual is None else residual.stride(0) if rows > 1 else n, weight.data_ptr(),
@@ -405,15 +412,23 @@ def gdn_rms_norm(x, weight, y, residual=None, sum_out=None, scales=None, weight_
 
 def gdn_kv_append(cache, batch, k, v, stream=None):
     """k, v: bf16 [tokens][heads][dim], token rows may be strided."""
+    if not k.is_cuda:
+        _on_host("gdn_kv_append")
     tokens, heads, dim = k.shape
-    one = heads * dim                 # the stride of a dimension of size one says nothing
-    _check("gdn_kv_append", load().gdn_kv_append(
-        ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), k.stride(0) if tokens > 1 else one,
-        v.data_ptr(), v.stride(0) if tokens > 1 else one, _stream(stream)))
+    if tokens == 1:                   # the stride of a dimension of size one says nothing
+        k_ld = v_ld = heads * dim
+    else:
+        k_ld, v_ld = k.stride()[0], v.stride()[0]
+    rc = load().gdn_kv_append(ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), k_ld, v.data_ptr(),
+                              v_ld, _stream(stream))
+    if rc:
+        _check("gdn_kv_append", rc)
 
 
 def gdn_kv_read(cache, batch, k, v, stream=None):
     """k, v: dense bf16 [tokens][heads][dim] outputs."""
+    if not k.is_cuda:
+        _on_host("gdn_kv_read")
     _check("gdn_kv_read", load().gdn_kv_read(
         ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), v.data_ptr(), _stream(stream)))
 
@@ -425,6 +440,8 @@ def gdn_paged_attention_workspace_bytes(cache, num_q_heads: int) -> int:
 def gdn_paged_attention(cache, batch, q, out, workspace, gate=None, scale=0.0, stream=None):
     """q, gate: bf16 [tokens][heads][dim] (tokens and heads may be strided), out dense, workspace
     uint8."""
+    if not q.is_cuda:
+        _on_host("gdn_paged_attention")
     tokens, heads, dim = q.shape
     q_ld, q_head_ld, _ = q.stride()
     g_ld, g_head_ld, _ = (0, 0, 0) if gate is None else gate.stride()

@@ -213,7 +213,11 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant="none"
     if residual is not None and (residual.shape != shape or residual.dtype != dtype or
                                  not _dense_rows(residual)):
         raise ValueError("residual must have the shape and dtype of x")
-    kind = _NORM_KINDS[quant]
+    if weight.device != x.device or (residual is not None and residual.device != x.device):
+        raise ValueError("x, weight and residual must be on one device")
+    kind = _NORM_KINDS.get(quant)
+    if kind is None:
+        raise ValueError(f"quant is one of {', '.join(_NORM_KINDS)}, not {quant!r}")
     rows, n = shape
     scales = total = None
     if kind == gdn.GDN_NORM_ACT:
@@ -239,6 +243,11 @@ class KVBatch:
         if block_table.dim() != 2 or cu_seqlens.shape[0] != kv_lens.shape[0] + 1 or \
                 block_table.shape[0] != kv_lens.shape[0]:
             raise ValueError("cu_seqlens [n + 1], kv_lens [n] and block_table [n][pages] expected")
+        if cu_seqlens.dim() != 1 or kv_lens.dim() != 1:
+            raise ValueError("cu_seqlens and kv_lens have one dimension")
+        self.device = cu_seqlens.device
+        if kv_lens.device != self.device or block_table.device != self.device:
+            raise ValueError("cu_seqlens, kv_lens and block_table must be on one device")
         self.tensors = (cu_seqlens, kv_lens, block_table)     # kept alive with the struct
         self.total_tokens = int(total_tokens)
         self.c = gdn.make_kv_batch(cu_seqlens, kv_lens, block_table, total_tokens, max_tokens)
@@ -276,6 +285,8 @@ class PagedKVCache:
             if (s is not None) != q8 or (q8 and (s.dtype != torch.uint8 or s.shape != k_pages.shape[:3] or
                                                  not s.is_contiguous())):
                 raise ValueError("an 8-bit cache has contiguous uint8 scales [pages][heads][page_size]")
+        if any(t is not None and t.device != k_pages.device for t in (v_pages, k_scales, v_scales)):
+            raise ValueError("pages and scales must be on one device")
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
         self.num_kv_heads, self.head_dim = int(k_pages.shape[1]), int(k_pages.shape[3])
         self.device = k_pages.device
@@ -287,33 +298,40 @@ class PagedKVCache:
         """The attention's workspace for this many query heads on this stream.  Calls on one stream
         share it, as long as the cache lives.  A call that is captured in a CUDA graph gets memory of the
         graph's own: graphs captured on one stream may be replayed beside each other."""
+        if stream is not None:
+            with gdn.on_stream(stream):
+                return self._workspace(num_q_heads, gdn.stream_handle())
+        return self._workspace(num_q_heads, gdn.stream_handle())
+
+    def _workspace(self, num_q_heads, current):
         need = self._ws_need.get(num_q_heads)
         if need is None:
             need = gdn.gdn_paged_attention_workspace_bytes(self.c, num_q_heads)
             if need == 0:
                 raise ValueError(f"{num_q_heads} query heads over this cache are not supported")
             self._ws_need[num_q_heads] = need
-        with gdn.on_stream(stream):
-            if torch.cuda.is_current_stream_capturing():
-                return torch.empty(need, dtype=torch.uint8, device=self.device)
-            key = gdn.stream_handle()
-            ws = self._ws.get(key)
-            if ws is None or ws.numel() < need:
-                ws = self._ws[key] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        ws = self._ws.get(current)
+        if ws is None or ws.numel() < need:
+            ws = self._ws[current] = torch.empty(need, dtype=torch.uint8, device=self.device)
         return ws
 
     def _check(self, t, batch, what):
-        shape = t.shape
+        shape, stride = t.shape, t.stride()
         if len(shape) != 3 or shape[0] != batch.total_tokens or shape[2] != self.head_dim or \
-                t.dtype != torch.bfloat16 or t.stride(2) != 1:
+                t.dtype != torch.bfloat16 or stride[2] != 1:
             raise ValueError(f"{what}: bf16 [total_tokens][heads][head_dim] with contiguous vectors expected")
-        return shape
+        device = self.device
+        if t.device != device or batch.device != device:
+            raise ValueError(f"{what} is on {t.device}, the batch on {batch.device}, the cache on {device}")
+        return shape, stride
 
     def append(self, batch: KVBatch, k, v, stream=None):
         """Stores the new tokens' keys and values, bf16 [total_tokens][num_kv_heads][head_dim]."""
         for t, what in ((k, "k"), (v, "v")):
-            if self._check(t, batch, what)[1] != self.num_kv_heads or \
-                    (self.num_kv_heads > 1 and t.stride(1) != self.head_dim):
+            shape, stride = self._check(t, batch, what)
+            if shape[1] != self.num_kv_heads or (stride[1] != self.head_dim and self.num_kv_heads > 1):
                 raise ValueError(f"{what}: {self.num_kv_heads} adjacent heads expected")
         if batch.total_tokens:
             gdn.gdn_kv_append(self.c, batch.c, k, v, stream)
@@ -329,6 +347,8 @@ class PagedKVCache:
             v = _empty(shape, torch.bfloat16, self.device, stream)
         elif v.shape != shape or v.dtype != torch.bfloat16 or not v.is_contiguous():
             raise ValueError("v: contiguous bf16 [total_tokens][num_kv_heads][head_dim]")
+        if k.device != self.device or v.device != self.device or batch.device != self.device:
+            raise ValueError("the batch, k and v must be on the cache's device")
         if batch.total_tokens:
             gdn.gdn_kv_read(self.c, batch.c, k, v, stream)
         return k, v
@@ -336,15 +356,23 @@ class PagedKVCache:
     def attend(self, batch: KVBatch, q, gate=None, scale=0.0, out=None, workspace=None, stream=None):
         """Causal attention of the new tokens' queries, bf16 [total_tokens][num_q_heads][head_dim]
         (times sigmoid(gate)), over the cache, which already holds their keys and values."""
-        shape = self._check(q, batch, "q")
-        if gate is not None and self._check(gate, batch, "gate") != shape:
+        shape, _ = self._check(q, batch, "q")
+        if gate is not None and self._check(gate, batch, "gate")[0] != shape:
             raise ValueError("gate must have the shape of q")
         if out is None:
             out = _empty(shape, torch.bfloat16, self.device, stream)
-        elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
-            raise ValueError("out: contiguous bf16 with the shape of q")
+        elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != self.device:
+            raise ValueError("out: contiguous bf16 with the shape of q, on the cache's device")
+        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or
+                                      workspace.device != self.device):
+            raise ValueError("workspace: contiguous uint8 on the cache's device")
         if batch.total_tokens:
-            if workspace is None:
+            if workspace is not None:
+                pass
+            elif stream is None:
+                stream = gdn.stream_handle()
+                workspace = self._workspace(shape[1], stream)
+            else:
                 workspace = self.workspace(shape[1], stream)
             gdn.gdn_paged_attention(self.c, batch.c, q, out, workspace, gate, scale, stream)
         return out

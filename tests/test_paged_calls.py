@@ -168,6 +168,9 @@ def test_row_distances_handed_over(monkeypatch):
     """What the library sees of such tensors."""
     seen = {}
 
+    class Gpu(torch.Tensor):
+        is_cuda = True
+
     class Lib:
         def __getattr__(self, name):
             return lambda *a: seen.update({name: a}) or 0
@@ -175,17 +178,59 @@ def test_row_distances_handed_over(monkeypatch):
     monkeypatch.setattr(gdn, "_stream", lambda s: 0)
     c = gdn.gdn_kv_cache(num_kv_heads=2, head_dim=64)
     b = gdn.gdn_kv_batch()
-    x = torch.zeros((2, 1, 64), dtype=torch.bfloat16).transpose(0, 1)
+    x = torch.zeros((2, 1, 64), dtype=torch.bfloat16).as_subclass(Gpu).transpose(0, 1)
     gdn.gdn_kv_append(c, b, x, x)
     assert seen["gdn_kv_append"][3] == seen["gdn_kv_append"][5] == 128
-    two = torch.zeros((3, 400), dtype=torch.bfloat16)[:, :128].view(3, 2, 64)
+    two = torch.zeros((3, 400), dtype=torch.bfloat16).as_subclass(Gpu)[:, :128].view(3, 2, 64)
     gdn.gdn_kv_append(c, b, two, two)
     assert seen["gdn_kv_append"][3] == seen["gdn_kv_append"][5] == 400
     ws = torch.zeros(1, dtype=torch.uint8)
     gdn.gdn_paged_attention(c, b, x, x, ws, gate=x)
     assert seen["gdn_paged_attention"][4:6] == (128, 64) and seen["gdn_paged_attention"][7:9] == (128, 64)
-    single = torch.zeros((3, 1, 64), dtype=torch.bfloat16).as_strided((3, 1, 64), (64, 1, 1))
+    single = torch.zeros((3, 1, 64), dtype=torch.bfloat16).as_subclass(Gpu).as_strided((3, 1, 64), (64, 1, 1))
     gdn.gdn_paged_attention(c, b, single, single, ws)
     assert seen["gdn_paged_attention"][4:6] == (64, 64)
     gdn.gdn_paged_attention(c, b, two, two, ws)
     assert seen["gdn_paged_attention"][4:6] == (400, 64)
+
+
+def test_tensors_of_other_devices_are_refused(streams):
+    """Host memory, or memory of another device than the cache's, never reaches the library."""
+    bf = dict(dtype=torch.bfloat16)
+
+    def on(dev, *shape, **kw):
+        return torch.zeros(shape, device=dev, **(kw or bf))
+    cache = runtime.PagedKVCache(4, 16, 2, 64, device="cpu")
+    batch = runtime.KVBatch(ints(3), ints(2), ints(2, 2), 3, 2)
+    far = runtime.KVBatch(*(t.to("meta") for t in batch.tensors), 3, 2)
+    t, m = on("cpu", 3, 2, 64), on("meta", 3, 2, 64)
+    w8, u8 = torch.zeros(512, dtype=torch.uint8), dict(dtype=torch.uint8)
+    refused = [
+        lambda: runtime.KVBatch(ints(3).to("meta"), ints(2), ints(2, 2), 3), lambda: runtime.KVBatch(ints(3), ints(2), ints(2, 2).to("meta"), 3),
+        lambda: runtime.KVBatch(ints(3, 1), ints(2), ints(2, 2), 3),
+        lambda: runtime.PagedKVCache.over(cache.k_pages, cache.v_pages.to("meta")),
+        lambda: cache.append(batch, t, m), lambda: cache.append(batch, m, t), lambda: cache.append(far, t, t),
+        lambda: cache.read(far), lambda: cache.read(batch, m, t), lambda: cache.read(batch, t, m),
+        lambda: cache.attend(batch, m), lambda: cache.attend(far, t), lambda: cache.attend(batch, t, gate=m), lambda: cache.attend(batch, t, out=m),
+        lambda: cache.attend(batch, t, workspace=torch.zeros(1, **u8).expand(512)),
+        lambda: cache.attend(batch, t, workspace=w8.view(torch.int32)), lambda: cache.attend(batch, t, workspace=w8.to("meta")),
+        lambda: runtime.rms_norm(on("cpu", 2, 8), on("meta", 8)), lambda: runtime.rms_norm(on("meta", 2, 8), on("cpu", 8)),
+        lambda: runtime.rms_norm(on("cpu", 2, 8), on("cpu", 8), residual=on("meta", 2, 8)),
+        lambda: runtime.rms_norm(on("cpu", 2, 8), on("cpu", 8), quant="rows"),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError):
+            call()
+        assert not streams.launched, i
+    cache.attend(batch, t, gate=t, out=t.clone(), workspace=w8)
+    assert len(streams.launched) == 1
+
+
+def test_host_memory_is_refused(monkeypatch):
+    monkeypatch.setattr(gdn, "load", lambda: pytest.fail("the library was called"))
+    x, ws = torch.zeros((2, 2, 64), dtype=torch.bfloat16), torch.zeros(8, dtype=torch.uint8)
+    c, b = gdn.gdn_kv_cache(), gdn.gdn_kv_batch()
+    for call in (lambda: gdn.gdn_rms_norm(x[0], x[0, 0], x[0]), lambda: gdn.gdn_kv_append(c, b, x, x),
+                 lambda: gdn.gdn_kv_read(c, b, x, x), lambda: gdn.gdn_paged_attention(c, b, x, x, ws)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call()
