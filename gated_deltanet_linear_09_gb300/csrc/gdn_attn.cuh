@@ -328,8 +328,9 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int stage, uint32_t p
 // Barrier over n threads that returns whether any of them passed true.
 __device__ __forceinline__ bool bar_any(int id, int n, bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbarrier.cta.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(id), "r"(n), "r"((uint32_t)v)
       : "memory");
