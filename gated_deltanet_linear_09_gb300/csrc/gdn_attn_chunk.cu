@@ -19,14 +19,20 @@
 //    other block's softmax runs (one block: two S buffers, PV(i), QK(i+2));
 //  * the reference m follows the running maximum only when that outgrows it by 2^8, so O is almost
 //    never rescaled, and never by a warpgroup of its own;
-//  * the next tile's queries are loaded, and its first product issued, before the last tile's
-//    output leaves.
-// Measured, 4096 tokens on 16384 cached ones (1.24 TFLOP at 32 heads of 128 and 16 of 256): bf16
-// D = 128 843 us, 1467 TFLOP/s (78 % of the dense bf16 rate, 63 % of the cycles with the pipe busy at
-// its nominal rate); D = 256 815 us, 1519; D = 64 690 us, 896, where the exponentials bound it.  8-bit:
-// 1101 to 1155 us, 1190 us and 900 us, bound by the conversion of the values, whose instructions share
-// the issue slots and instruction caches with the softmax.  32 rows on 8000 keys (64 sequences of 8
-// tokens): bf16 322 us, 98 % of the copy bandwidth; 8-bit 361 us, 45 %.
+//  * a tile's queries have the place that its gate and its output then pass through, so the next tile's
+//    are loaded, and its first product issued, after the output has left: between two tiles of rows the
+//    pipe stands still for 9 us (bf16, D = 128 or 256), 13 to 14 us where queries are split for an 8-bit
+//    cache, and 3.5 us more with a gate at D = 256 (5 and 1 tiles a CTA compared, 2 and 18 key tiles each).
+// Measured, 4096 tokens on 16384 cached ones (1.24 TFLOP at 32 heads of 128 and 16 of 256), a few calls
+// in a row: bf16 D = 128 836 to 849 us, 1457 to 1480 TFLOP/s (77 to 78 % of the dense bf16 rate, 63 % of
+// the cycles with the pipe busy at its nominal rate; 899 us in a long row of calls, under the power
+// cap); D = 256 812 us, 1523; D = 64 697 us, 887, where the exponentials bound it.  8-bit: 1120 us, 1183
+// to 1205 us and 909 us, bound by the conversion of the values, whose instructions share the issue slots
+// and instruction caches with the softmax.  32 rows on 8000 keys (64 sequences of 8 tokens): bf16 318 to
+// 322 us, 98 % of the copy bandwidth; 8-bit 354 us, 45 %.
+// Fewer bits: the probabilities become bf16, the type of the second product's other operand (half a step
+// of each, 2^-9 to 2^-8 of it; tf32 products run at half the rate); their sum takes them unrounded.  An
+// 8-bit cache's queries become two e4m3 parts (see split_e4m3).
 // Values whose key some rows do not see must be finite for the product to leave those rows alone:
 // in tiles that the causal edge crosses, the first warpgroup replaces non-finite ones (and
 // whatever lies past the sequence's end) by zero, and notes column and position, so that the rows
@@ -1149,6 +1155,8 @@ int launch_chunk(const KvView& c, const KvBatchView& b, const AttnArgs& a, int s
   // the fewest keys worth a piece of their own (14 tokens on 8481: 21.5 us at 512, 24.2 at 256).  12
   // sequences of 3 to 1456 new tokens at 512, 640, 768, 896, 1024 keys: D = 256 bf16 97, 92, 94, 96,
   // 98 us, 8-bit 139, 133, 128, 128, 131, gated -, 162, 145, 142, 138; D = 128 bf16 54, 56, 58, -, 58.
+  // A tile's time beside its keys alone (5 and 1 tiles a CTA compared): D = 256 bf16 441 keys' time, 8-bit
+  // 724, a gate 180 more; D = 128 716 and 824.
   const int base = D < 256 ? 512 : Q8 ? 896 : 640;
   const int grid = sms, fix = (base + (a.gate ? D / 2 : 0)) * a.g;
   const int least = 512 * a.g;

@@ -23,9 +23,11 @@
 //    parts, whose sum is exact), their scales applied to the scores; the values' codes become f16 by
 //    the conversion instruction, their scales applied to the probabilities.
 // Measured (the copy bandwidth is 6.69 TB/s): 64 sequences of 8000 positions, 8 x 128, 4 rows, bf16
-// 312 us, 6.7 TB/s, 8-bit 172 us, 6.1 TB/s; ragged 8-bit batch of 64, 200 to 16,000 positions, 88 us,
-// 5.7 TB/s; two sequences of 100,000 to 131,000, 2 x 256, bf16, 77 us, 5.9 TB/s.  16 rows on 8 bits:
-// 258 us, 4.1 TB/s, bound by the instructions of two row tiles.
+// 302 to 310 us, 6.8 TB/s, 8-bit 167 to 171 us, 6.2 TB/s; ragged 8-bit batch of 64, 200 to 16,000 positions, 87 us,
+// 5.7 TB/s; two sequences of 100,000 to 131,000, 2 x 256, bf16, 76 us, 5.9 TB/s.  16 rows on 8 bits:
+// 257 us, 4.1 TB/s, bound by the instructions of two row tiles.
+// Fewer bits: the probabilities become bf16, or f16 over 8-bit values (see kNear), as the matrix
+// instructions' operands are; their sum takes them unrounded, and all sums are f32.
 #include "gdn_attn.cuh"
 #include "gdn_tmap.h"
 

@@ -442,13 +442,15 @@ size_t gdn_paged_attention_workspace_bytes(const gdn_kv_cache* cache, int32_t nu
  * themselves: append first).  Query head h reads key/value head h / (num_q_heads / num_kv_heads):
  *   o = softmax_j(scale q . k_j) v_j over the positions j <= p of the token,
  * then, with a gate, o * sigmoid(gate); one rounding to bf16.  A token that sees no position gets
- * zero.  Keys and values at positions a token does not see have no influence, whatever they hold.
+ * zero.  Keys and values at positions a token does not see have no influence, whatever they hold: no
+ * bit of its result depends on them.
  *   q, gate (NULL: none): bf16, element (t, h, d) at t * ld + h * head_ld + d; ld and head_ld
  *   multiples of 8, 16-byte aligned -- a projection's [q | gate] per head is read in place.
  *   scale: 0 selects 1/sqrt(head_dim).  out: bf16 [total_tokens][num_q_heads][head_dim], dense.
  *   num_q_heads % num_kv_heads == 0 (GDN_ERR_HEAD_DIVISIBILITY); total_tokens * num_q_heads <=
  *   2^30 (GDN_ERR_TOO_LARGE).  workspace: device, 256-byte aligned, contents undefined on entry
- *   and exit.  Results do not depend on the workspace's contents and are bitwise reproducible.
+ *   and exit; calls that may run at the same time, replays of captured ones among them, need one each.
+ *   Results do not depend on the workspace's contents and are bitwise reproducible.
  * Two kernel launches. */
 int gdn_paged_attention(const gdn_kv_cache* cache, const gdn_kv_batch* batch, int32_t num_q_heads,
                         const void* q, int64_t q_ld, int64_t q_head_ld, const void* gate,
