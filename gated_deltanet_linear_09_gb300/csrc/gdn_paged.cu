@@ -209,7 +209,8 @@ int gdn_paged_attention(const gdn_kv_cache* cache, const gdn_kv_batch* batch, in
   if ((rc = check_batch(batch, &b)) != GDN_OK) return rc;
   if (num_q_heads <= 0 || !(scale >= 0.f) || !isfinite(scale)) return GDN_ERR_INVALID_ARG;
   if (num_q_heads % c.H != 0) return GDN_ERR_HEAD_DIVISIBILITY;
-  if ((int64_t)b.total * num_q_heads > (1LL << 30)) return GDN_ERR_TOO_LARGE;
+  // (a group's factor of the work's units: thousands of keys times it fit 31 bits)
+  if ((int64_t)b.total * num_q_heads > (1LL << 30) || num_q_heads / c.H > (1 << 20)) return GDN_ERR_TOO_LARGE;
   if (b.total == 0) return GDN_OK;
   if (!q || !out) return GDN_ERR_INVALID_ARG;
   if (q_ld < c.D || q_head_ld < c.D || (gate && (gate_ld < c.D || gate_head_ld < c.D))) return GDN_ERR_INVALID_ARG;

@@ -448,7 +448,7 @@ size_t gdn_paged_attention_workspace_bytes(const gdn_kv_cache* cache, int32_t nu
  *   multiples of 8, 16-byte aligned -- a projection's [q | gate] per head is read in place.
  *   scale: 0 selects 1/sqrt(head_dim).  out: bf16 [total_tokens][num_q_heads][head_dim], dense.
  *   num_q_heads % num_kv_heads == 0 (GDN_ERR_HEAD_DIVISIBILITY); total_tokens * num_q_heads <=
- *   2^30 (GDN_ERR_TOO_LARGE).  workspace: device, 256-byte aligned, contents undefined on entry
+ *   2^30 and num_q_heads <= 2^20 num_kv_heads (GDN_ERR_TOO_LARGE).  workspace: device, 256-byte aligned, contents undefined on entry
  *   and exit; calls that may run at the same time, replays of captured ones among them, need one each.
  *   Results do not depend on the workspace's contents and are bitwise reproducible.
  * Two kernel launches. */

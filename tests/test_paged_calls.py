@@ -234,3 +234,17 @@ def test_host_memory_is_refused(monkeypatch):
                  lambda: gdn.gdn_kv_read(c, b, x, x), lambda: gdn.gdn_paged_attention(c, b, x, x, ws)):
         with pytest.raises(ValueError, match="not on a GPU"):
             call()
+
+
+def test_heads_past_the_units_of_work_are_refused():
+    """Groups so large that keys times heads leave 31 bits."""
+    gbuild.build()
+    A = 0x10000
+    cache = gdn.gdn_kv_cache(A, A, None, None, 4, 16, 1, 128, gdn.GDN_KV_BF16, None)
+    batch = gdn.gdn_kv_batch(A, A, A, 1, 1, 4, 1)
+
+    def attend(heads, ws=A):
+        return gdn.load().gdn_paged_attention(ctypes.byref(cache), ctypes.byref(batch), heads, A, 1 << 31, 128, None, 0, 0, 0.0, A,
+                                              ws, 1 << 40, None)
+    assert attend((1 << 20) + 1) == -9 and attend(1 << 25) == -9
+    assert attend(1 << 20, ws=A + 16) == -7             # (on to the next check: the workspace is misaligned)
