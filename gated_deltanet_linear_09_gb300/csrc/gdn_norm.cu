@@ -3,8 +3,8 @@
 // h = x + r, y = h / sqrt(mean h^2 + eps) * (w0 + w).  Two or three flops per element, so the
 // floor is the bytes: x and r read once, the sum and y written once.  A row therefore stays in
 // registers between the pass that sums h^2 and the one that scales: nothing is read twice.
-// Measured: 16384 x 4096 bf16 with residual to block-scaled 8 bits 70.8 us, the copy bandwidth (6.67
-// of 6.69 TB/s); one row of 5120 2.0 us on the GPU, below what a call takes on the host.
+// Measured: 16384 x 4096 bf16 with residual to block-scaled 8 bits 71.0 us, 99 % of the copy bandwidth
+// (6.65 of 6.69 TB/s); one row of 5120 2.0 us on the GPU, below what a call takes on the host.
 #include "gdn_internal.h"
 
 #include <cuda_fp8.h>
@@ -66,18 +66,53 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-template <int VEC>
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, float inv) {
+// a / b, rounded once: the product with the rounded reciprocal and Markstein's correction by its
+// remainder.  (Codes of the product alone fall to the other side of a halfway point 2.4 times as often as
+// the quotient's.)
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+  const float q = a * inv;
+  return fmaf(fmaf(-q, b, a), inv, q);
+}
+
+// A group's scale and its reciprocal.  An infinite scale is divided by as the reciprocal 0 alone (the
+// correction by the remainder of 0 times infinity would be NaN).
+struct __align__(8) Scale {
+  float by, inv;
+  __device__ __forceinline__ Scale() {}
+  __device__ __forceinline__ explicit Scale(float s) : by(s == INFINITY ? 0.f : s), inv(1.0f / s) {}
+  __device__ __forceinline__ float of(float v) const { return quotient(v, by, inv); }
+  // two at once, as codes
+  __device__ __forceinline__ uint32_t codes(float v0, float v1) const {
+    uint64_t v, q, r;
+    const uint64_t i = pair(inv, inv), b = pair(-by, -by);
+    v = pair(v0, v1);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(v), "l"(i));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(b), "l"(v));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(i), "l"(q));
+    float q0, q1;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(q0), "=f"(q1) : "l"(q));
+    return e4m3x2(q0, q1);
+  }
+  static __device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+  }
+};
+
+// PAIRS: quotients two at once (16384 x 4096 by blocks 71.0 us, one at a time 71.5); not where a warp's
+// scales differ from vector to vector and are held ahead (16384 x 2046 47.5 us, one at a time 45.6).
+template <int VEC, bool PAIRS = true>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Scale& s) {
   if constexpr (VEC == 1) {
-    *p = (uint8_t)e4m3x2(v[0] * inv, 0.f);
+    *p = (uint8_t)e4m3x2(s.of(v[0]), 0.f);
   } else if constexpr (VEC == 2) {
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)e4m3x2(v[0] * inv, v[1] * inv);
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)(PAIRS ? s.codes(v[0], v[1]) : e4m3x2(s.of(v[0]), s.of(v[1])));
   } else {
     uint32_t w[VEC / 4];
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i)
-      w[i] = e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) |
-             (e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16);
+      w[i] = s.codes(v[4 * i], v[4 * i + 1]) | (s.codes(v[4 * i + 2], v[4 * i + 3]) << 16);
     if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
     else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   }
@@ -95,7 +130,9 @@ __device__ __forceinline__ float warp_max_nan(float m) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu));
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.0f / 448.0f), 0x1p-120f); }
+__device__ __forceinline__ float scale_of(float amax) {
+  return max_nan(amax == INFINITY ? amax : quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-120f);
+}
 
 struct NormArgs {
   const void* x;
@@ -118,9 +155,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
   constexpr int WARPS = CTA / 32;
   __shared__ float part[WARPS];
   // One or two elements a lane: a warp's columns are a part of a group.  Group maxima, as the bits of
-  // non-negative floats (a NaN's are above all), then the groups' inverse scales.
+  // non-negative floats (a NaN's are above all), then the groups' scales.
   constexpr bool SMEM_GROUPS = KIND == GDN_NORM_E4M3_BLOCK && VEC <= 2 && TPR > 32;
   __shared__ uint32_t gmax[SMEM_GROUPS ? TPR * NV * VEC / 128 : 1];
+  __shared__ Scale gscale[SMEM_GROUPS ? TPR * NV * VEC / 128 : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = TPR < 128 ? tid % TPR : tid;
   const long long row = (long long)blockIdx.x * (CTA / TPR) + (TPR < 128 ? tid / TPR : 0);
@@ -214,12 +252,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
         mr = lane < WARPS ? part[lane] : 0.f;
         mr = warp_max_nan(mr);
       }
-      const float s = scale_of(mr), inv = 1.0f / s;
+      const float s = scale_of(mr);
+      const Scale scale(s);
       if (t == 0) a.scales[row] = s;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + t) * VEC;
-        if (c < n) store_e4m3<VEC>(y + c, h[j], inv);
+        if (c < n) store_e4m3<VEC>(y + c, h[j], scale);
       }
     } else {
       const int groups = (n + 127) >> 7;
@@ -231,10 +270,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
           float mg = m[j];
 #pragma unroll
           for (int o = 64 / VEC; o > 0; o >>= 1) mg = max_nan(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-          const float s = scale_of(mg), inv = 1.0f / s;
+          const float s = scale_of(mg);
+          const Scale scale(s);
           if (c < n) {
             if ((c & 127) == 0) a.scales[row * groups + (c >> 7)] = s;
-            store_e4m3<VEC>(y + c, h[j], inv);
+            store_e4m3<VEC>(y + c, h[j], scale);
           }
         }
       } else if constexpr (TPR == 32) {
@@ -246,12 +286,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
 #pragma unroll
           for (int j = j0; j < j0 + kOf; ++j) mg = max_nan(mg, m[j]);
           mg = warp_max_nan(mg);
-          const float s = scale_of(mg), inv = 1.0f / s;
+          const float s = scale_of(mg);
+          const Scale scale(s);
           if (t == 0 && j0 / kOf < groups) a.scales[row * groups + j0 / kOf] = s;
 #pragma unroll
           for (int j = j0; j < j0 + kOf; ++j) {
             const int c = (j * TPR + t) * VEC;
-            if (c < n) store_e4m3<VEC>(y + c, h[j], inv);
+            if (c < n) store_e4m3<VEC>(y + c, h[j], scale);
           }
         }
       } else {
@@ -265,13 +306,16 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const NormA
         for (int i = tid; i < groups; i += CTA) {
           const float s = scale_of(__uint_as_float(gmax[i]));
           a.scales[row * groups + i] = s;
-          gmax[i] = __float_as_uint(1.0f / s);
+          gscale[i] = Scale(s);
         }
         __syncthreads();
+        Scale scale[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) scale[j] = gscale[(j * TPR + t) * VEC >> 7];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           const int c = (j * TPR + t) * VEC;
-          if (c < n) store_e4m3<VEC>(y + c, h[j], __uint_as_float(gmax[c >> 7]));
+          if (c < n) store_e4m3<VEC, false>(y + c, h[j], scale[j]);
         }
       }
     }
