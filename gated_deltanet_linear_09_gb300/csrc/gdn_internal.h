@@ -140,6 +140,52 @@ int launch_kv_append(const KvView& c, const KvBatchView& b, const void* k, long 
                      const void* v, long long v_ld, cudaStream_t stream);
 int launch_kv_read(const KvView& c, const KvBatchView& b, void* k, void* v, cudaStream_t stream);
 
+// Rotary positions of queries and keys (outputs dense).
+struct RotaryLaunch {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long q_ld, q_head_ld, k_ld, k_head_ld;
+  const uint64_t* turns;
+  const int32_t* positions;
+  float scale;
+  int rot, interleaved, tokens, dim, q_heads, k_heads;
+};
+int launch_rotary(const RotaryLaunch& r, gdn_dtype act, cudaStream_t stream);
+
+// The cache's append with the heads' norm and rotation.
+struct RotatedAppend {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;
+  long long q_ld, q_head_ld, k_ld, v_ld;
+  const __nv_bfloat16* q_norm;
+  const __nv_bfloat16* k_norm;
+  const uint64_t* turns;
+  const int32_t* positions;
+  float scale, w0, eps;
+  int Hq, half, interleaved;
+};
+int launch_kv_append_rotated(const KvView& c, const KvBatchView& b, const RotatedAppend& a, cudaStream_t stream);
+
+int launch_block_norm(const gdn_block_args& a, int rows, int n, gdn_dtype act, cudaStream_t stream);
+
+// Linear attention with a decay for each head.
+struct DecayView {
+  float* state;
+  int32_t* status;
+  int num_slots, Hk, Hv, dk, dv;
+  float scale;
+};
+int launch_decay_step(const DecayView& l, const gdn_decay_tokens& t, const int32_t* slot_idx, int B, int T,
+                      cudaStream_t stream);
+size_t decay_prefill_ws_bytes(const DecayView& l, int num_seqs, int total_tokens);
+int launch_decay_prefill(const DecayView& l, const gdn_decay_tokens& t, const int32_t* cu_seqlens,
+                         const int32_t* slot_idx, const uint8_t* has_init, int num_seqs, int total_tokens,
+                         void* workspace, cudaStream_t stream);
+
 struct AttnArgs {
   const __nv_bfloat16* q;
   const __nv_bfloat16* gate;

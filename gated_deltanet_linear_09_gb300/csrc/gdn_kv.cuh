@@ -8,9 +8,9 @@
 
 namespace gdn {
 
-// Where a packed token lives: page < 0 when it has no place.
+// Where a packed token lives: page < 0 when it has no place; its position in the sequence.
 struct Place {
-  int page, off;
+  int page, off, pos;
 };
 
 // The sequence holding packed token t: the largest s with cu[s] <= t, by a 32-way search of the
@@ -36,7 +36,7 @@ __device__ __forceinline__ int find_seq(const KvBatchView& b, int t) {
 __device__ __forceinline__ Place find_place(const KvView& c, const KvBatchView& b, int t) {
   const int s = find_seq(b, t);
   const int c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1);
-  Place p{-1, 0};
+  Place p{-1, 0, 0};
   if (t >= c1 && s == b.num_seqs - 1 && c1 >= c0) return p;    // padding past the last sequence
   const long long len = __ldg(b.lens + s);
   if (c0 < 0 || t < c0 || t >= c1 || c1 > b.total || len < 0 || len > ((long long)b.table_cols << c.page_shift)) {
@@ -51,6 +51,7 @@ __device__ __forceinline__ Place find_place(const KvView& c, const KvBatchView& 
     return p;
   }
   p.page = page;
+  p.pos = (int)pos;
   p.off = (int)(pos & ((1 << c.page_shift) - 1));
   return p;
 }

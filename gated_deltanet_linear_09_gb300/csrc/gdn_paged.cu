@@ -192,6 +192,53 @@ int gdn_kv_read(const gdn_kv_cache* cache, const gdn_kv_batch* batch, void* k, v
   return gdn::launch_kv_read(c, b, k, v, stream);
 }
 
+int gdn_kv_append_rotated(const gdn_kv_cache* cache, const gdn_kv_batch* batch, const gdn_rotary* rotary,
+                          const gdn_head_prep* prep, const void* q, int64_t q_ld, int64_t q_head_ld,
+                          int32_t num_q_heads, void* q_out, const void* k, int64_t k_ld, const void* v,
+                          int64_t v_ld, cudaStream_t stream) {
+  GDN_CALL_RANGE("gdn_kv_append_rotated");
+  gdn::KvView c;
+  gdn::KvBatchView b;
+  int rc;
+  if ((rc = check_cache(cache, &c, true)) != GDN_OK) return rc;
+  if ((rc = check_batch(batch, &b)) != GDN_OK) return rc;
+  if (!rotary || !prep || num_q_heads < 0) return GDN_ERR_INVALID_ARG;
+  if (!isfinite(rotary->scale) || !isfinite(prep->weight_offset) || !(prep->eps >= 0.f) || !isfinite(prep->eps))
+    return GDN_ERR_INVALID_ARG;
+  if (rotary->rot_dim < 16 || rotary->rot_dim % 16 != 0 || rotary->rot_dim > c.D) return GDN_ERR_UNSUPPORTED_SHAPE;
+  const int64_t width = (int64_t)c.H * c.D;
+  if (k_ld < width || v_ld < width || (num_q_heads > 0 && (q_ld < c.D || q_head_ld < c.D))) return GDN_ERR_INVALID_ARG;
+  if (num_q_heads > (1 << 20)) return GDN_ERR_TOO_LARGE;
+  if (b.total == 0) return GDN_OK;
+  if (!rotary->turns || !k || !v || (num_q_heads > 0 && (!q || !q_out))) return GDN_ERR_INVALID_ARG;
+  if (!aligned(rotary->turns, 8) || !aligned(prep->positions, 4) || !aligned(prep->q_norm, 16) ||
+      !aligned(prep->k_norm, 16) || !aligned(k, 16) || !aligned(v, 16) || k_ld % 8 != 0 || v_ld % 8 != 0)
+    return GDN_ERR_MISALIGNED;
+  if (num_q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || q_ld % 8 != 0 || q_head_ld % 8 != 0))
+    return GDN_ERR_MISALIGNED;
+  if ((int64_t)b.total * (width + (int64_t)num_q_heads * c.D) > (1LL << 38)) return GDN_ERR_TOO_LARGE;
+  gdn::RotatedAppend a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_ld = q_ld;
+  a.q_head_ld = q_head_ld;
+  a.k_ld = k_ld;
+  a.v_ld = v_ld;
+  a.q_norm = static_cast<const __nv_bfloat16*>(prep->q_norm);
+  a.k_norm = static_cast<const __nv_bfloat16*>(prep->k_norm);
+  a.turns = rotary->turns;
+  a.positions = prep->positions;
+  a.scale = rotary->scale;
+  a.w0 = prep->weight_offset;
+  a.eps = prep->eps;
+  a.Hq = num_q_heads;
+  a.half = rotary->rot_dim / 2;
+  a.interleaved = rotary->interleaved != 0;
+  return gdn::launch_kv_append_rotated(c, b, a, stream);
+}
+
 size_t gdn_paged_attention_workspace_bytes(const gdn_kv_cache* cache, int32_t num_q_heads) {
   gdn::KvView c;
   if (check_cache(cache, &c, false) != GDN_OK || num_q_heads <= 0 || num_q_heads % c.H != 0) return 0;

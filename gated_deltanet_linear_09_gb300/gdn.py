@@ -29,6 +29,10 @@ GDN_NORM_E4M3_BLOCK = 2
 GDN_MAX_NORM_WIDTH = 32768
 GDN_KV_BF16 = 0
 GDN_KV_E4M3 = 1
+GDN_MAX_ROTARY_DIM = 1024
+GDN_GATE_NONE = 0
+GDN_GATE_SIGMOID = 1
+GDN_GATE_SILU = 2
 
 _CODES = {
     0: "GDN_OK", -1: "GDN_ERR_INVALID_ARG", -2: "GDN_ERR_UNSUPPORTED_SHAPE",
@@ -43,7 +47,9 @@ EXPORTED = ("gdn_state_slot_bytes", "gdn_conv1d_update", "gdn_decode_step", "gdn
             "gdn_decode_graphs_buffers", "gdn_decode_graphs_launch", "gdn_decode_graphs_destroy",
             "gdn_proj_packed_bytes", "gdn_proj_pack", "gdn_linear_bf16", "gdn_in_proj",
             "gdn_out_proj", "gdn_rms_norm", "gdn_kv_append", "gdn_kv_read",
-            "gdn_paged_attention_workspace_bytes", "gdn_paged_attention")
+            "gdn_paged_attention_workspace_bytes", "gdn_paged_attention", "gdn_rotary_apply",
+            "gdn_kv_append_rotated", "gdn_block_norm", "gdn_decay_step",
+            "gdn_decay_prefill_workspace_bytes", "gdn_decay_prefill")
 GDN_MAX_DECODE_TOKENS = 8
 GDN_MAX_GRAPH_BUCKETS = 16
 GDN_NOALLOC_PREFILL_SCRATCH_BYTES = 64 << 20
@@ -94,6 +100,36 @@ class gdn_kv_batch(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int32),
                 ("total_tokens", ctypes.c_int32), ("table_ld", ctypes.c_int32),
                 ("max_tokens", ctypes.c_int32), ("table_cols", ctypes.c_int32)]
+
+
+class gdn_rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class gdn_head_prep(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("weight_offset", ctypes.c_float),
+                ("eps", ctypes.c_float), ("positions", ctypes.c_void_p)]
+
+
+class gdn_block_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "gate", "residual", "post", "pre", "channel_scale")] + \
+               [(n, ctypes.c_int64) for n in ("x_ld", "gate_ld", "residual_ld")] + \
+               [("total", ctypes.c_void_p), ("y", ctypes.c_void_p)] + \
+               [(n, ctypes.c_float) for n in ("scale", "weight_offset", "eps")] + \
+               [("group", ctypes.c_int32), ("gate_act", ctypes.c_int)]
+
+
+class gdn_decay_layer(ctypes.Structure):
+    _fields_ = [("state", ctypes.c_void_p), ("num_slots", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
+                ("num_v_heads", ctypes.c_int32), ("head_k_dim", ctypes.c_int32), ("head_v_dim", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("status", ctypes.c_void_p)]
+
+
+class gdn_decay_tokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_ld", ctypes.c_int64),
+                ("k_ld", ctypes.c_int64), ("v_ld", ctypes.c_int64), ("log_decay", ctypes.c_void_p),
+                ("decay_ld", ctypes.c_int64), ("out", ctypes.c_void_p)]
 
 
 _lib = None
@@ -166,6 +202,19 @@ def load(build_if_missing: bool = False):
     lib.gdn_paged_attention.restype = ctypes.c_int
     lib.gdn_paged_attention.argtypes = [_P, _P, _I32, _P, i64, i64, _P, i64, i64, f32, _P, _P,
                                         ctypes.c_size_t, _P]
+    lib.gdn_rotary_apply.restype = ctypes.c_int
+    lib.gdn_rotary_apply.argtypes = [_P, _P, _I32, _I32, ctypes.c_int, _P, i64, i64, _I32, _P, _P, i64, i64,
+                                     _I32, _P, _P]
+    lib.gdn_kv_append_rotated.restype = ctypes.c_int
+    lib.gdn_kv_append_rotated.argtypes = [_P, _P, _P, _P, _P, i64, i64, _I32, _P, _P, i64, _P, i64, _P]
+    lib.gdn_block_norm.restype = ctypes.c_int
+    lib.gdn_block_norm.argtypes = [_P, _I32, _I32, ctypes.c_int, _P]
+    lib.gdn_decay_step.restype = ctypes.c_int
+    lib.gdn_decay_step.argtypes = [_P, _P, _P, _I32, _I32, _P]
+    lib.gdn_decay_prefill_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_decay_prefill_workspace_bytes.argtypes = [_P, _I32, _I32]
+    lib.gdn_decay_prefill.restype = ctypes.c_int
+    lib.gdn_decay_prefill.argtypes = [_P, _P, _P, _P, _P, _I32, _I32, _P, ctypes.c_size_t, _P]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     _lib = lib
@@ -455,6 +504,110 @@ def gdn_paged_attention(cache, batch, q, out, workspace, gate=None, scale=0.0, s
         workspace.data_ptr(), workspace.numel(), _stream(stream))
     if rc:
         _check("gdn_paged_attention", rc)
+
+
+def make_rotary(turns, rot_dim: int, interleaved: bool = False, scale: float = 1.0) -> gdn_rotary:
+    """turns: device int64 [rot_dim / 2], each pair's turns a position in units of 2^-64 (modulo 2^64)."""
+    return gdn_rotary(_ptr(turns), int(rot_dim), int(bool(interleaved)), float(scale))
+
+
+def _head_strides(t):
+    """(token distance, head distance) of [tokens][heads][dim]; of dimensions of size one, the dense ones."""
+    tokens, heads, dim = t.shape
+    ld, head_ld, _ = t.stride()
+    if heads == 1:
+        head_ld = dim
+    if tokens == 1:
+        ld = max(heads * dim, (heads - 1) * head_ld + dim)
+        ld += -ld % 8 if head_ld % 8 == 0 and dim % 8 == 0 else 0
+    return ld, head_ld
+
+
+def gdn_rotary_apply(rotary, positions, q=None, q_out=None, k=None, k_out=None, stream=None):
+    """q, k: [tokens][heads][dim] (tokens and heads may be strided), outputs dense."""
+    t = q if q is not None else k
+    if not t.is_cuda:
+        _on_host("gdn_rotary_apply")
+    args = []
+    for x, y in ((q, q_out), (k, k_out)):
+        args += [None, 0, 0, 0, None] if x is None else [x.data_ptr(), *_head_strides(x), x.shape[1], y.data_ptr()]
+    rc = load().gdn_rotary_apply(ctypes.byref(rotary), positions.data_ptr(), t.shape[0], t.shape[2], act_code(t.dtype),
+                                 *args, _stream(stream))
+    if rc:
+        _check("gdn_rotary_apply", rc)
+
+
+def make_head_prep(q_norm=None, k_norm=None, weight_offset=0.0, eps=1e-6, positions=None) -> gdn_head_prep:
+    return gdn_head_prep(_ptr(q_norm), _ptr(k_norm), float(weight_offset), float(eps), _ptr(positions))
+
+
+def gdn_kv_append_rotated(cache, batch, rotary, prep, q, q_out, k, v, stream=None):
+    """q: bf16 [tokens][heads][dim] (tokens and heads may be strided; None: none), q_out dense; k, v as for
+    gdn_kv_append."""
+    if not k.is_cuda:
+        _on_host("gdn_kv_append_rotated")
+    tokens, heads, dim = k.shape
+    if tokens == 1:                   # the stride of a dimension of size one says nothing
+        k_ld = v_ld = heads * dim
+    else:
+        k_ld, v_ld = k.stride()[0], v.stride()[0]
+    q_args = (None, 0, 0, 0, None) if q is None else (q.data_ptr(), *_head_strides(q), q.shape[1], q_out.data_ptr())
+    rc = load().gdn_kv_append_rotated(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(rotary), ctypes.byref(prep),
+                                      *q_args, k.data_ptr(), k_ld, v.data_ptr(), v_ld, _stream(stream))
+    if rc:
+        _check("gdn_kv_append_rotated", rc)
+
+
+def gdn_block_norm(x, total=None, y=None, post=None, gate=None, gate_act=GDN_GATE_NONE, residual=None, pre=None,
+                   channel_scale=None, scale=1.0, weight_offset=0.0, eps=1e-6, group=0, stream=None):
+    """x, gate, residual [rows][n] (rows may be strided), total and y dense; group 0: the row."""
+    if not x.is_cuda:
+        _on_host("gdn_block_norm")
+    rows, n = x.shape
+    x_ld, gate_ld, residual_ld = (0 if t is None else t.stride(0) if rows > 1 else n for t in (x, gate, residual))
+    a = gdn_block_args(_ptr(x), _ptr(gate), _ptr(residual), _ptr(post), _ptr(pre), _ptr(channel_scale), x_ld, gate_ld,
+                       residual_ld, _ptr(total), _ptr(y), scale, weight_offset, eps, group or n, gate_act)
+    rc = load().gdn_block_norm(ctypes.byref(a), rows, n, act_code(x.dtype), _stream(stream))
+    if rc:
+        _check("gdn_block_norm", rc)
+
+
+def make_decay_layer(state, num_k_heads: int, scale: float = 0.0, status=None) -> gdn_decay_layer:
+    """state f32 [num_slots][num_v_heads][dk][dv]."""
+    n, hv, dk, dv = (int(x) for x in state.shape)
+    return gdn_decay_layer(_ptr(state), n, int(num_k_heads), hv, dk, dv, float(scale), _ptr(status))
+
+
+def make_decay_tokens(q, k, v, log_decay, out) -> gdn_decay_tokens:
+    """q, k, v: bf16 [tokens][heads][dim], adjacent heads, strided tokens; log_decay f32 [heads] or
+    [tokens][heads]; out dense."""
+    def ld(t):                        # the stride of a dimension of size one says nothing
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    g_ld = 0 if log_decay.dim() == 1 else log_decay.stride(0) if log_decay.shape[0] > 1 else log_decay.shape[1]
+    return gdn_decay_tokens(_ptr(q), _ptr(k), _ptr(v), ld(q), ld(k), ld(v), _ptr(log_decay), g_ld, _ptr(out))
+
+
+def gdn_decay_step(layer, tokens, slot_idx, T: int, stream=None):
+    if not slot_idx.is_cuda:
+        _on_host("gdn_decay_step")
+    rc = load().gdn_decay_step(ctypes.byref(layer), ctypes.byref(tokens), slot_idx.data_ptr(), slot_idx.shape[0], T,
+                               _stream(stream))
+    if rc:
+        _check("gdn_decay_step", rc)
+
+
+def gdn_decay_prefill_workspace_bytes(layer, num_seqs: int, total_tokens: int) -> int:
+    return int(load().gdn_decay_prefill_workspace_bytes(ctypes.byref(layer), int(num_seqs), int(total_tokens)))
+
+
+def gdn_decay_prefill(layer, tokens, cu_seqlens, slot_idx, has_initial_state, total_tokens: int, workspace, stream=None):
+    if not slot_idx.is_cuda:
+        _on_host("gdn_decay_prefill")
+    rc = load().gdn_decay_prefill(ctypes.byref(layer), ctypes.byref(tokens), cu_seqlens.data_ptr(), slot_idx.data_ptr(),
+                                  _ptr(has_initial_state), slot_idx.shape[0], total_tokens, workspace.data_ptr(),
+                                  workspace.numel(), _stream(stream))
+    if rc:
+        _check("gdn_decay_prefill", rc)
 
 
 def gdn_status_string(code: int) -> str:

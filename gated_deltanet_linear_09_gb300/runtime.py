@@ -9,6 +9,8 @@ stream uses a tensor, are the caller's.
 """
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import torch
 
@@ -231,6 +233,236 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant="none"
     return y, scales, total
 
 
+class Rotary:
+    """Rotary positions: the first rot_dim elements of a head turned in pairs, adjacent ones (interleaved) or
+    i and i + rot_dim / 2, pair i by position * base^(-2i / rot_dim) radians.  For contexts `factor` times the
+    trained length, scaling "linear" divides every frequency by it; "base" multiplies the base by
+    factor^(rot_dim / (rot_dim - 2)), which stretches the slow pairs only; "bands" keeps pairs that make more
+    than 32 turns within `trained` positions, divides those that make less than one, ramps between, and
+    multiplies what is turned by 0.1 ln(factor) + 1.  The frequencies are held to 2^-64 of a turn, so that the
+    angle of any position is exact."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, trained: int = 8192, device="cuda"):
+        if rot_dim < 2 or rot_dim % 2:
+            raise ValueError("rot_dim is even and at least 2")
+        if not (base > 1.0 and factor > 0.0 and math.isfinite(base) and math.isfinite(factor)):
+            raise ValueError("base > 1 and factor > 0 expected")
+        if scaling == "base":
+            base = base * factor ** (rot_dim / max(2, rot_dim - 2))
+        f = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+        scale = 1.0
+        if scaling == "linear":
+            f = [x / factor for x in f]
+        elif scaling == "bands":
+            lo, hi = (rot_dim * math.log(trained / (2 * math.pi * turns)) / (2 * math.log(base)) for turns in (32.0, 1.0))
+            lo, hi = max(0.0, math.floor(lo)), min(rot_dim - 1.0, math.ceil(hi))
+            ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(rot_dim // 2)]
+            f = [x * (1.0 - r) + x / factor * r for x, r in zip(f, ramp)]
+            scale = 0.1 * math.log(factor) + 1.0
+        elif scaling not in ("none", "base"):
+            raise ValueError(f"scaling is none, linear, base or bands, not {scaling!r}")
+        self._bind(f, interleaved, scale, device)
+
+    @classmethod
+    def of(cls, frequencies, interleaved: bool = False, scale: float = 1.0, device="cuda") -> "Rotary":
+        """From each pair's radians a position."""
+        self = cls.__new__(cls)
+        self._bind([float(x) for x in frequencies], interleaved, float(scale), device)
+        return self
+
+    def _bind(self, frequencies, interleaved, scale, device):
+        if not frequencies or not all(math.isfinite(x) for x in frequencies) or not math.isfinite(scale):
+            raise ValueError("finite frequencies and scale expected")
+        self.frequencies, self.rot_dim, self.scale = frequencies, 2 * len(frequencies), scale
+        turns = [round(x / (2 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for x in frequencies]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.device = self.turns.device
+        self.c = gdn.make_rotary(self.turns, self.rot_dim, interleaved, scale)
+
+    def _check(self, t, out, positions, what):
+        if len(t.shape) != 3 or t.shape[0] != positions.shape[0] or t.shape[2] < self.rot_dim or not _dense_rows(t):
+            raise ValueError(f"{what}: [tokens][heads][dim >= {self.rot_dim}] with contiguous vectors expected")
+        if t.device != self.device:
+            raise ValueError(f"{what} is on {t.device}, the rotation on {self.device}")
+        if out is not None and (out.shape != t.shape or out.dtype != t.dtype or not out.is_contiguous() or
+                                out.device != self.device):
+            raise ValueError(f"{what}'s output: contiguous, with its shape and type, on its device")
+
+    def apply(self, positions, q=None, k=None, q_out=None, k_out=None, stream=None):
+        """(q, k) turned at positions (device int32 [tokens]); q and k bf16 or f32 [tokens][heads][dim], either may
+        be None.  Outputs may be the inputs where those are contiguous."""
+        if positions.dim() != 1 or positions.dtype != torch.int32 or not _dense_rows(positions) or \
+                positions.device != self.device:
+            raise ValueError("positions: contiguous int32 [tokens] on the rotation's device")
+        if q is not None:
+            self._check(q, q_out, positions, "q")
+        if k is not None:
+            self._check(k, k_out, positions, "k")
+        if q is not None and k is not None and (q.dtype != k.dtype or q.shape[2] != k.shape[2]):
+            raise ValueError("q and k have one type and head size")
+        if q is not None and q_out is None:
+            q_out = _empty(q.shape, q.dtype, q.device, stream)
+        if k is not None and k_out is None:
+            k_out = _empty(k.shape, k.dtype, k.device, stream)
+        if q is not None or k is not None:
+            gdn.gdn_rotary_apply(self.c, positions, q, q_out, k, k_out, stream)
+        return q_out, k_out
+
+
+_GATES = {"none": gdn.GDN_GATE_NONE, "sigmoid": gdn.GDN_GATE_SIGMOID, "silu": gdn.GDN_GATE_SILU}
+
+
+def block_norm(x, post=None, gate=None, gate_act="sigmoid", scale=1.0, channel_scale=None, residual=None, pre=None,
+               eps=1e-6, weight_offset=0.0, total=None, y=None, stream=None):
+    """A block's output x [rows][n] (bf16 or f32) on its way to the next block: returns (total, y),
+      total = residual + scale * channel_scale * norm(x; post) * act(gate),  y = norm(total; pre),
+    whatever of it is given (y None without pre).  post [n] norms the row, a shorter post (32, 64, 128 or 256
+    weights) each run of that many columns.  gate_act "sigmoid", or "silu": gate * sigmoid(gate)."""
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if len(shape) != 2 or not _dense_rows(x):
+        raise ValueError("block_norm takes rows [rows][n]")
+    rows, n = shape
+    for t, what in ((gate, "gate"), (residual, "residual"), (total, "total"), (y, "y")):
+        if t is not None and (t.shape != shape or t.dtype != dtype or not _dense_rows(t) or t.device != device):
+            raise ValueError(f"{what} must have the shape, type and device of x")
+    for t, what in ((total, "total"), (y, "y")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+    for t, what in ((post, "post"), (pre, "pre"), (channel_scale, "channel_scale")):
+        if t is not None and (t.dim() != 1 or t.dtype != dtype or not _dense_rows(t) or t.device != device or
+                              (t.shape[0] != n and what != "post")):
+            raise ValueError(f"{what}: a vector of x's type and width on its device")
+    act = "none" if gate is None else gate_act
+    if act not in _GATES or (gate is not None and act == "none"):
+        raise ValueError(f"gate_act is sigmoid or silu, not {gate_act!r}")
+    if total is None:
+        total = _empty(shape, dtype, device, stream)
+    if pre is None:
+        if y is not None:
+            raise ValueError("y is written with pre only")
+    elif y is None:
+        y = _empty(shape, dtype, device, stream)
+    gdn.gdn_block_norm(x, total, y, post, gate, _GATES[act], residual, pre, channel_scale, scale, weight_offset, eps,
+                       n if post is None else post.shape[0], stream)
+    return total, y
+
+
+class DecayAttention:
+    """Linear attention with a decay for each head, S = exp(g) S + k v^T, o = scale S^T q, on a pool of states
+    f32 [num_slots][num_v_heads][dk][dv]; value head h reads query and key head h * num_k_heads // num_v_heads.
+    scale 0: 1/sqrt(dk)."""
+
+    def __init__(self, num_k_heads: int, num_v_heads: int, head_k_dim: int, head_v_dim: int, num_slots: int,
+                 scale: float = 0.0, device="cuda"):
+        self._bind(torch.zeros((num_slots, num_v_heads, head_k_dim, head_v_dim), dtype=torch.float32, device=device),
+                   num_k_heads, scale)
+
+    @classmethod
+    def over(cls, state, num_k_heads: int, scale: float = 0.0) -> "DecayAttention":
+        """On an existing pool of states."""
+        self = cls.__new__(cls)
+        self._bind(state, num_k_heads, scale)
+        return self
+
+    def _bind(self, state, num_k_heads, scale):
+        if state.dim() != 4 or state.dtype != torch.float32 or not state.is_contiguous():
+            raise ValueError("state: contiguous f32 [num_slots][num_v_heads][dk][dv]")
+        if num_k_heads < 1 or state.shape[1] % num_k_heads:
+            raise ValueError("num_v_heads is a multiple of num_k_heads")
+        self.state, self.device = state, state.device
+        self.Hk, self.Hv, self.dk, self.dv = num_k_heads, *(int(x) for x in state.shape[1:])
+        self.status = torch.zeros(1, dtype=torch.int32, device=state.device)
+        self.c = gdn.make_decay_layer(state, num_k_heads, scale, self.status)
+        self._ws = {}
+
+    def _tokens(self, lead, q, k, v, log_decay, out, stream):
+        """(tokens struct, out) of tensors [*lead][heads][dim], flattened to tokens without a copy."""
+        n = 1
+        for x in lead:
+            n *= x
+        flat = []
+        for t, what, heads, dim in ((q, "q", self.Hk, self.dk), (k, "k", self.Hk, self.dk), (v, "v", self.Hv, self.dv)):
+            if t.shape != (*lead, heads, dim) or t.dtype != torch.bfloat16 or t.device != self.device:
+                raise ValueError(f"{what}: bf16 {[*lead, heads, dim]} on {self.device} expected, not {list(t.shape)}")
+            flat.append(self._rows(t, len(lead), what))
+            if n and (t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != dim)):
+                raise ValueError(f"{what}: adjacent heads expected")
+        if log_decay.dtype != torch.float32 or log_decay.device != self.device or \
+                log_decay.shape not in ((self.Hv,), (*lead, self.Hv)) or not _dense_rows(log_decay):
+            raise ValueError(f"log_decay: f32 [{self.Hv}] or {[*lead, self.Hv]} on {self.device}")
+        if log_decay.dim() > 1:
+            log_decay = self._rows(log_decay, len(lead), "log_decay")
+        shape = (*lead, self.Hv, self.dv)
+        if out is None:
+            out = _empty(shape, torch.bfloat16, self.device, stream)
+        elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != self.device:
+            raise ValueError(f"out: contiguous bf16 {list(shape)} on {self.device}")
+        return gdn.make_decay_tokens(*flat, log_decay, out), out
+
+    @staticmethod
+    def _rows(t, lead, what):
+        """The leading dimensions as one, without a copy."""
+        if lead == 1:
+            return t
+        try:
+            return t.view(-1, *t.shape[lead:])
+        except RuntimeError:
+            raise ValueError(f"{what}: its tokens must lie at one distance from each other") from None
+
+    def _check_slots(self, slot_idx, n):
+        if slot_idx.dtype != torch.int32 or slot_idx.shape != (n,) or not _dense_rows(slot_idx) or \
+                slot_idx.device != self.device:
+            raise ValueError(f"slot_idx: contiguous int32 [{n}] on {self.device}")
+
+    def step(self, slot_idx, q, k, v, log_decay, out=None, stream=None):
+        """A token for each row, q and k bf16 [rows][num_k_heads][dk], v [rows][num_v_heads][dv]; or T of them,
+        [rows][T][heads][dim].  log_decay f32 [num_v_heads], or one of each token.  slot_idx int32 [rows], -1:
+        padding.  Returns out, of v's shape."""
+        lead = tuple(v.shape[:-2])
+        if len(lead) not in (1, 2):
+            raise ValueError("v: [rows][num_v_heads][dv] or [rows][T][num_v_heads][dv]")
+        self._check_slots(slot_idx, lead[0])
+        tokens, out = self._tokens(lead, q, k, v, log_decay, out, stream)
+        if lead[0]:
+            gdn.gdn_decay_step(self.c, tokens, slot_idx, lead[1] if len(lead) == 2 else 1, stream)
+        return out
+
+    def workspace(self, num_seqs: int, total_tokens: int, stream=None) -> torch.Tensor:
+        """The prefill's workspace on this stream: calls on one stream share it, a call that is captured in a CUDA
+        graph gets memory of the graph's own."""
+        with gdn.on_stream(stream):
+            current = gdn.stream_handle()
+            need = gdn.gdn_decay_prefill_workspace_bytes(self.c, num_seqs, total_tokens)
+            if need == 0:
+                raise ValueError("unsupported geometry")
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws = self._ws.get(current)
+            if ws is None or ws.numel() < need:
+                ws = self._ws[current] = torch.empty(need, dtype=torch.uint8, device=self.device)
+            return ws
+
+    def prefill(self, cu_seqlens, slot_idx, has_init, q, k, v, log_decay, out=None, stream=None):
+        """Packed prompts: sequence n is tokens cu_seqlens[n] .. cu_seqlens[n + 1] of q, k [tokens][num_k_heads][dk]
+        and v [tokens][num_v_heads][dv], and continues its slot's state where has_init[n] (uint8; None: none does)."""
+        n = slot_idx.shape[0]
+        self._check_slots(slot_idx, n)
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (n + 1,) or not _dense_rows(cu_seqlens) or \
+                cu_seqlens.device != self.device:
+            raise ValueError(f"cu_seqlens: contiguous int32 [{n + 1}] on {self.device}")
+        if has_init is not None and (has_init.dtype not in (torch.uint8, torch.bool) or has_init.shape != (n,) or
+                                     not _dense_rows(has_init) or has_init.device != self.device):
+            raise ValueError(f"has_init: contiguous uint8 [{n}] on {self.device}")
+        if v.dim() != 3:
+            raise ValueError("v: [tokens][num_v_heads][dv]")
+        tokens, out = self._tokens(tuple(v.shape[:1]), q, k, v, log_decay, out, stream)
+        if n:
+            gdn.gdn_decay_prefill(self.c, tokens, cu_seqlens, slot_idx, has_init, v.shape[0],
+                                  self.workspace(n, v.shape[0], stream), stream)
+        return out
+
+
 class KVBatch:
     """The new tokens of one step: device int32 cu_seqlens [n + 1], kv_lens [n] (cached positions
     including the new tokens) and block_table [n][pages].  total_tokens: packed token rows;
@@ -335,6 +567,40 @@ class PagedKVCache:
                 raise ValueError(f"{what}: {self.num_kv_heads} adjacent heads expected")
         if batch.total_tokens:
             gdn.gdn_kv_append(self.c, batch.c, k, v, stream)
+
+    def append_rotated(self, batch: KVBatch, rotary: Rotary, q, k, v, q_norm=None, k_norm=None, eps=1e-6,
+                       weight_offset=0.0, positions=None, q_out=None, stream=None):
+        """append() of keys that are normed (k_norm: bf16 [head_dim]) and turned on the way, beside queries
+        [total_tokens][num_q_heads][head_dim] (or None): returns these, normed and turned.  positions: device
+        int32 [total_tokens]; None: the tokens' places in the cache."""
+        for t, what in ((k, "k"), (v, "v")):
+            shape, stride = self._check(t, batch, what)
+            if shape[1] != self.num_kv_heads or (stride[1] != self.head_dim and self.num_kv_heads > 1):
+                raise ValueError(f"{what}: {self.num_kv_heads} adjacent heads expected")
+        device = self.device
+        if q is not None:
+            shape, _ = self._check(q, batch, "q")
+            if q_out is None:
+                q_out = _empty(shape, torch.bfloat16, device, stream)
+            elif q_out.shape != shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous() or q_out.device != device:
+                raise ValueError("q_out: contiguous bf16 with the shape of q, on the cache's device")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        for t, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if t is not None and (t.shape != (self.head_dim,) or t.dtype != torch.bfloat16 or not _dense_rows(t) or
+                                  t.device != device):
+                raise ValueError(f"{what}: contiguous bf16 [{self.head_dim}] on the cache's device")
+        if positions is not None and (positions.shape != (batch.total_tokens,) or positions.dtype != torch.int32 or
+                                      not _dense_rows(positions) or positions.device != device):
+            raise ValueError("positions: contiguous int32 [total_tokens] on the cache's device")
+        if rotary.device != device:
+            raise ValueError(f"the rotation is on {rotary.device}, the cache on {device}")
+        if rotary.rot_dim > self.head_dim or rotary.rot_dim % 16:
+            raise ValueError(f"a rotated part of {self.head_dim} elements at most, a multiple of 16, expected")
+        if batch.total_tokens:
+            gdn.gdn_kv_append_rotated(self.c, batch.c, rotary.c, gdn.make_head_prep(q_norm, k_norm, weight_offset, eps, positions),
+                                      q, q_out, k, v, stream)
+        return q_out
 
     def read(self, batch: KVBatch, k=None, v=None, stream=None):
         """The batch's tokens' keys and values back as bf16 (k, v)."""

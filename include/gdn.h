@@ -457,6 +457,140 @@ int gdn_paged_attention(const gdn_kv_cache* cache, const gdn_kv_batch* batch, in
                         int64_t gate_ld, int64_t gate_head_ld, float scale, void* out,
                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- Between a layer's projections -----------------------------------------------------------
+ * Rotary positions, the cache's append with the heads' norm and rotation on the way, the norms around
+ * a block with its gate and residual scale, and linear attention with a decay for each head.  The
+ * calls keep the conventions above. */
+
+/* Rotary positions.  The first rot_dim elements of a head are rot_dim / 2 pairs, (2i, 2i + 1) if
+ * interleaved, else (i, i + rot_dim / 2); at position p pair i is turned by p turns[i] 2^-64 of a full
+ * turn and multiplied by scale.  The other elements stay.  turns: device uint64[rot_dim / 2], the
+ * turns a position in units of 2^-64 modulo one turn: a product modulo 2^64 is the exact angle at any
+ * position, negative ones too.  rot_dim even, >= 2; scale finite. */
+typedef struct {
+  const uint64_t* turns;
+  int32_t rot_dim;
+  int32_t interleaved;
+  float scale;
+} gdn_rotary;
+
+/* Largest head_dim of gdn_rotary_apply. */
+#define GDN_MAX_ROTARY_DIM 1024
+
+/* Turns the heads of q and of k (q_heads or k_heads may be 0, its pointers then NULL) of `tokens` tokens
+ * at positions[t] (device int32): x[t][h][d] at t * ld + h * head_ld + d, ld and head_ld >= head_dim (any
+ * values, bases aligned to an element), activation dtype; outputs dense [tokens][heads][head_dim], which
+ * may be the inputs themselves where those are dense, and overlap nothing else.  Computed in f32 and
+ * rounded once.  Rows, heads and pairs on 16- or 8-byte boundaries move in such vectors.  One launch. */
+int gdn_rotary_apply(const gdn_rotary* rotary, const int32_t* positions, int32_t tokens, int32_t head_dim,
+                     gdn_dtype act, const void* q, int64_t q_ld, int64_t q_head_ld, int32_t q_heads,
+                     void* q_out, const void* k, int64_t k_ld, int64_t k_head_ld, int32_t k_heads, void* k_out,
+                     cudaStream_t stream);
+
+/* What gdn_kv_append_rotated does to queries and keys on the way. */
+typedef struct {
+  const void* q_norm;     /* bf16 [head_dim]: RMSNorm of every query head; NULL: none            */
+  const void* k_norm;     /* the same of every key head                                          */
+  float weight_offset;    /* 1 for zero-centred weights, else 0                                  */
+  float eps;
+  const int32_t* positions; /* device int32 [total_tokens]; NULL: each token's place in the cache */
+} gdn_head_prep;
+
+/* gdn_kv_append of keys that are normed and turned on the way, beside queries that go to q_out:
+ *   x -> x / sqrt(mean x^2 + eps) * (weight_offset + w)   (with a weight),  then the rotation,
+ * in f32, rounded once to bf16 (q_out, a bf16 cache), or to e4m3 with the scale of the f32 vector.
+ * Values are stored as by gdn_kv_append.  q: bf16, element (t, h, d) at t * q_ld + h * q_head_ld + d (NULL
+ * with num_q_heads 0), q_out dense [total_tokens][num_q_heads][head_dim]; k, v as in gdn_kv_append.
+ * Distances are multiples of 8, bases 16-byte aligned.  rot_dim <= head_dim, a multiple of 16
+ * (GDN_ERR_UNSUPPORTED_SHAPE).  The queries of tokens without a place are zeros.  One launch. */
+int gdn_kv_append_rotated(const gdn_kv_cache* cache, const gdn_kv_batch* batch, const gdn_rotary* rotary,
+                          const gdn_head_prep* prep, const void* q, int64_t q_ld, int64_t q_head_ld,
+                          int32_t num_q_heads, void* q_out, const void* k, int64_t k_ld, const void* v,
+                          int64_t v_ld, cudaStream_t stream);
+
+typedef enum { GDN_GATE_NONE = 0, GDN_GATE_SIGMOID = 1, GDN_GATE_SILU = 2 } gdn_gate;
+
+/* A block's output x on its way to the next block, rows of n elements (f32 throughout):
+ *   b = x / sqrt(mean_g x^2 + eps) * (weight_offset + post)     (post NULL: b = x)
+ *   h = residual + scale * channel_scale * b * act(gate)        (each of them may be absent)
+ *   y = h / sqrt(mean h^2 + eps) * (weight_offset + pre)        (pre NULL: none)
+ * total = h and y rounded once to the activation dtype; the norm is taken of the unrounded h.  mean_g is
+ * over the row (group = n) or over each run of `group` columns (32, 64, 128 or 256, dividing n), whose
+ * weights post [group] they share.  act: sigmoid(z), or z sigmoid(z) (SILU).
+ *   x, gate, residual: rows x_ld / gate_ld / residual_ld apart (>= n); pre, channel_scale [n]; total (NULL:
+ *   not written, with pre only; may be residual or x, with equal row distance n) and y (NULL without pre)
+ *   dense.  Any n up to GDN_MAX_NORM_WIDTH and any distances; rows that start on 16-byte boundaries and hold
+ *   a multiple of 8 elements move in 16-byte vectors, and groups below n need those
+ *   (GDN_ERR_MISALIGNED).  rows = 0 is a no-op.  One launch. */
+typedef struct {
+  const void* x;
+  const void* gate;
+  const void* residual;
+  const void* post;
+  const void* pre;
+  const void* channel_scale;
+  int64_t x_ld, gate_ld, residual_ld;
+  void* total;
+  void* y;
+  float scale, weight_offset, eps;
+  int32_t group;
+  gdn_gate gate_act;
+} gdn_block_args;
+
+int gdn_block_norm(const gdn_block_args* args, int32_t rows, int32_t n, gdn_dtype act, cudaStream_t stream);
+
+/* Linear attention with a decay for each head:
+ *   S_t = exp(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
+ * on a state f32 [num_slots][num_v_heads][head_k_dim][head_v_dim] (dv fastest); value head h reads the
+ * query and key head h / (num_v_heads / num_k_heads).  Head dims in {64, 128}; scale 0: 1/sqrt(dk).
+ * status: optional device int32 error word. */
+typedef struct {
+  float* state;
+  int32_t num_slots;
+  int32_t num_k_heads;
+  int32_t num_v_heads;
+  int32_t head_k_dim;
+  int32_t head_v_dim;
+  float scale;
+  int32_t* status;
+} gdn_decay_layer;
+
+/* The tokens of a call: q, k bf16 [tokens][num_k_heads][dk], v bf16 [tokens][num_v_heads][dv], heads
+ * adjacent, tokens q_ld / k_ld / v_ld elements apart (multiples of 8); out bf16 [tokens][num_v_heads][dv],
+ * dense.  g of token t and head h: log_decay[t * decay_ld + h] (f32; decay_ld 0: the same for every token),
+ * finite or -inf, which empties the state; below -105 it counts as -inf (exp of it is 0 in f32).  16-byte
+ * aligned, log_decay 4-byte aligned. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_ld, k_ld, v_ld;
+  const float* log_decay;
+  int64_t decay_ld;
+  void* out;
+} gdn_decay_tokens;
+
+/* T (1 to GDN_MAX_DECODE_TOKENS) tokens for each of B rows: tokens row * T .. row * T + T - 1, in order, on
+ * the state of slot slot_idx[row] (device int32[B], distinct; < 0: padding, output zeroed, no state
+ * touched; out of range: GDN_STATUS_SLOT_RANGE and the same).  State read and written once.  f32 sums,
+ * outputs rounded once.  B <= 65535.  One launch. */
+int gdn_decay_step(const gdn_decay_layer* layer, const gdn_decay_tokens* tokens, const int32_t* slot_idx,
+                   int32_t B, int32_t T, cudaStream_t stream);
+
+/* Workspace bytes of gdn_decay_prefill (0: unsupported geometry). */
+size_t gdn_decay_prefill_workspace_bytes(const gdn_decay_layer* layer, int32_t num_seqs, int32_t total_tokens);
+
+/* Whole prompts: sequence n is tokens [cu_seqlens[n], cu_seqlens[n+1]) and continues from slot slot_idx[n]
+ * where has_initial_state[n] (NULL: none do), else from zero; the slot then holds the state after its last
+ * token (a sequence without tokens: the one it began with).  Arrays, padding slots and errors as in
+ * gdn_prefill_chunked; outputs of tokens in no usable sequence are zeros.  The state is kept and added up
+ * in f32, from products of keys that are exact to 2^-16; for the outputs, states and the decayed scores
+ * are rounded to bf16 (half a step, 2^-9, of each).  workspace: device, 256-byte aligned, contents
+ * undefined on entry and exit; calls that may run at the same time need one each.  Bitwise reproducible. */
+int gdn_decay_prefill(const gdn_decay_layer* layer, const gdn_decay_tokens* tokens, const int32_t* cu_seqlens,
+                      const int32_t* slot_idx, const uint8_t* has_initial_state, int32_t num_seqs,
+                      int32_t total_tokens, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Text for a return code. */
 const char* gdn_status_string(int code);
 
