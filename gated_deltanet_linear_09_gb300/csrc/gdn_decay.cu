@@ -24,9 +24,7 @@ struct StepArgs {
   __nv_bfloat16* out;
   long long q_ld, k_ld, v_ld, g_ld;
   const int32_t* slots;
-  const int32_t* cu;             // NULL: T tokens a row
-  const uint8_t* init;           // with cu
-  int T, total;
+  int T;
 };
 
 template <int DK, int DV, int CW>
@@ -41,84 +39,62 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
   const int tid = threadIdx.x, row = blockIdx.z, h = blockIdx.y, c0 = blockIdx.x * CW;
   const int r0 = tid / LPR, c = (tid % LPR) * 4;
   pdl_begin();
-  int t0 = row * a.T, t1 = t0 + a.T;
-  bool bad = false;
-  if (a.cu) {
-    const int rows = gridDim.z, end = __ldg(a.cu + rows);
-    bool wrong = __ldg(a.cu) != 0 || end > a.total;
-    for (int i = tid; i < rows; i += kThreads) wrong |= __ldg(a.cu + i + 1) < __ldg(a.cu + i);
-    bad = __syncthreads_or(wrong);
-    t0 = __ldg(a.cu + row);
-    t1 = __ldg(a.cu + row + 1);
-    if (bad) t0 = t1 = 0;
-    // tokens of no sequence (all of them where the ranges do not fit together): this row's share
-    for (long long t = (bad ? 0 : end) + row; t < a.total; t += rows)
-      for (int i = tid; i < CW; i += kThreads) a.out[(t * a.l.Hv + h) * DV + c0 + i] = __float2bfloat16_rn(0.f);
-  }
+  const long long t0 = (long long)row * a.T;
   const int slot = __ldg(a.slots + row);
-  if (tid == 0) {
-    if (bad) set_status(a.l.status, GDN_STATUS_BAD_SEQLENS);
-    if (slot >= a.l.num_slots) set_status(a.l.status, GDN_STATUS_SLOT_RANGE);
-  }
+  if (tid == 0 && slot >= a.l.num_slots) set_status(a.l.status, GDN_STATUS_SLOT_RANGE);
   const int hk = h / (a.l.Hv / a.l.Hk);
-  if (bad || slot < 0 || slot >= a.l.num_slots) {
-    for (int i = tid; i < (t1 - t0) * CW; i += kThreads)
-      a.out[((long long)(t0 + i / CW) * a.l.Hv + h) * DV + c0 + i % CW] = __float2bfloat16_rn(0.f);
+  if (slot < 0 || slot >= a.l.num_slots) {
+    for (int i = tid; i < a.T * CW; i += kThreads)
+      a.out[((t0 + i / CW) * a.l.Hv + h) * DV + c0 + i % CW] = __float2bfloat16_rn(0.f);
     return;
   }
   float* state = a.l.state + ((long long)slot * a.l.Hv + h) * (DK * DV) + c0;
   float4 s[N];
-  const bool from_zero = a.cu && !(a.init && __ldg(a.init + row));
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    s[i] = from_zero ? make_float4(0.f, 0.f, 0.f, 0.f)
-                     : __ldcs(reinterpret_cast<const float4*>(state + (size_t)(r0 + i * R) * DV + c));
-  for (int tb = t0; tb < t1; tb += kBlock) {
-    const int count = min(kBlock, t1 - tb);
-    for (int i = tid; i < count * DK; i += kThreads) {
-      const int t = i / DK, d = i % DK;
-      qs[t][d] = __bfloat162float(a.q[(tb + t) * a.q_ld + hk * DK + d]) * a.l.scale;
-      ks[t][d] = __bfloat162float(a.k[(tb + t) * a.k_ld + hk * DK + d]);
-    }
-    for (int i = tid; i < count * CW; i += kThreads)
-      vs[i / CW][i % CW] = __bfloat162float(a.v[(tb + i / CW) * a.v_ld + h * DV + c0 + i % CW]);
-    if (tid < count) gs[tid] = expf(__ldg(a.g + (tb + tid) * a.g_ld + h));
-    __syncthreads();
-    for (int t = 0; t < count; ++t) {
-      const float e = gs[t];
-      const float4 v = *reinterpret_cast<const float4*>(&vs[t][c]);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    s[i] = __ldcs(reinterpret_cast<const float4*>(state + (size_t)(r0 + i * R) * DV + c));
+  for (int i = tid; i < a.T * DK; i += kThreads) {
+    const int t = i / DK, d = i % DK;
+    qs[t][d] = __bfloat162float(a.q[(t0 + t) * a.q_ld + hk * DK + d]) * a.l.scale;
+    ks[t][d] = __bfloat162float(a.k[(t0 + t) * a.k_ld + hk * DK + d]);
+  }
+  for (int i = tid; i < a.T * CW; i += kThreads)
+    vs[i / CW][i % CW] = __bfloat162float(a.v[(t0 + i / CW) * a.v_ld + h * DV + c0 + i % CW]);
+  if (tid < a.T) gs[tid] = expf(__ldg(a.g + (t0 + tid) * a.g_ld + h));
+  __syncthreads();
+  for (int t = 0; t < a.T; ++t) {
+    const float e = gs[t];
+    const float4 v = *reinterpret_cast<const float4*>(&vs[t][c]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float k = ks[t][r0 + i * R], q = qs[t][r0 + i * R];
-        // a decay of zero empties the state whatever it held
-        s[i].x = fmaf(k, v.x, e == 0.f ? 0.f : e * s[i].x);
-        s[i].y = fmaf(k, v.y, e == 0.f ? 0.f : e * s[i].y);
-        s[i].z = fmaf(k, v.z, e == 0.f ? 0.f : e * s[i].z);
-        s[i].w = fmaf(k, v.w, e == 0.f ? 0.f : e * s[i].w);
-        o.x = fmaf(q, s[i].x, o.x);
-        o.y = fmaf(q, s[i].y, o.y);
-        o.z = fmaf(q, s[i].z, o.z);
-        o.w = fmaf(q, s[i].w, o.w);
-      }
-#pragma unroll
-      for (int m = LPR; m < 32; m <<= 1) {
-        o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
-        o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
-        o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
-        o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
-      }
-      if ((tid & 31) < LPR) *reinterpret_cast<float4*>(&sums[t][tid >> 5][c]) = o;
+    for (int i = 0; i < N; ++i) {
+      const float k = ks[t][r0 + i * R], q = qs[t][r0 + i * R];
+      // a decay of zero empties the state whatever it held
+      s[i].x = fmaf(k, v.x, e == 0.f ? 0.f : e * s[i].x);
+      s[i].y = fmaf(k, v.y, e == 0.f ? 0.f : e * s[i].y);
+      s[i].z = fmaf(k, v.z, e == 0.f ? 0.f : e * s[i].z);
+      s[i].w = fmaf(k, v.w, e == 0.f ? 0.f : e * s[i].w);
+      o.x = fmaf(q, s[i].x, o.x);
+      o.y = fmaf(q, s[i].y, o.y);
+      o.z = fmaf(q, s[i].z, o.z);
+      o.w = fmaf(q, s[i].w, o.w);
     }
-    __syncthreads();
-    for (int i = tid; i < count * CW; i += kThreads) {
-      const int t = i / CW, d = i % CW;
-      float o = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) o += sums[t][w][d];
-      a.out[((long long)(tb + t) * a.l.Hv + h) * DV + c0 + d] = __float2bfloat16_rn(o);
+    for (int m = LPR; m < 32; m <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
     }
-    __syncthreads();
+    if ((tid & 31) < LPR) *reinterpret_cast<float4*>(&sums[t][tid >> 5][c]) = o;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.T * CW; i += kThreads) {
+    const int t = i / CW, d = i % CW;
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) o += sums[t][w][d];
+    a.out[((long long)(t0 + t) * a.l.Hv + h) * DV + c0 + d] = __float2bfloat16_rn(o);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) __stcs(reinterpret_cast<float4*>(state + (size_t)(r0 + i * R) * DV + c), s[i]);
@@ -170,21 +146,7 @@ int launch_decay_step(const DecayView& l, const gdn_decay_tokens& t, const int32
   StepArgs a = step_args(l, t);
   a.slots = slot_idx;
   a.T = T;
-  a.total = B * T;
   return launch_rows(a, B, stream);
-}
-
-size_t decay_prefill_ws_bytes(const DecayView&, int, int) { return 256; }
-
-int launch_decay_prefill(const DecayView& l, const gdn_decay_tokens& t, const int32_t* cu_seqlens,
-                         const int32_t* slot_idx, const uint8_t* has_init, int num_seqs, int total_tokens,
-                         void*, cudaStream_t stream) {
-  StepArgs a = step_args(l, t);
-  a.slots = slot_idx;
-  a.cu = cu_seqlens;
-  a.init = has_init;
-  a.total = total_tokens;
-  return launch_rows(a, num_seqs, stream);
 }
 
 }  // namespace gdn

@@ -113,6 +113,9 @@ int raise_smem(OncePerDevice& once, K kern, size_t bytes) {
   });
 }
 
+// Number of SMs of the current device (looked up once per device); 0 without one.
+int sm_count();
+
 // RMSNorm with the residual's addition (kind: a gdn_norm_out).
 int launch_rms_norm(const void* x, long long x_ld, const void* residual, long long residual_ld,
                     const void* weight, float weight_offset, float eps, int rows, int n,

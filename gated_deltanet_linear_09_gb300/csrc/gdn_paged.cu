@@ -9,9 +9,6 @@
 
 namespace gdn {
 
-namespace {
-
-// Number of SMs of the current device (looked up once per device).
 int sm_count() {
   constexpr int kMax = 64;
   static int count[kMax] = {};   // written with the same value by every thread that finds it empty
@@ -24,6 +21,8 @@ int sm_count() {
   }
   return n;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -77,6 +76,17 @@ bool make_kv_maps(const KvView& c, int rows, KvMaps* maps) {
   const cuuint32_t box[5] = {(cuuint32_t)(span / elem), (cuuint32_t)rows, (cuuint32_t)(row / span), 1, 1};
   const CUtensorMapSwizzle swizzle = span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   return encode_all(c, encode, dims, strides, box, swizzle, swizzle, maps);
+}
+
+bool make_rows_map(const void* base, long long rows, long long ld, int cols, int box_rows, int box_blocks, CUtensorMap* map) {
+  const auto encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks}, one[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t attn_ws_bytes(const KvView& c, int) {

@@ -21,6 +21,10 @@ bool make_kv_maps(const KvView& c, int rows, KvMaps* maps);
 // but 8-bit values, which a warp reads to convert them.
 bool make_tile_maps(const KvView& c, int rows, int cols, KvMaps* maps);
 
+// A map of bf16 rows `ld` elements apart whose box is box_rows rows of box_blocks blocks of 64 columns:
+// [blocks][rows][128 bytes] in shared memory, 128-byte swizzled.  Rows past the last read as zeros.
+bool make_rows_map(const void* base, long long rows, long long ld, int cols, int box_rows, int box_blocks, CUtensorMap* map);
+
 namespace attn {
 int rows_grid(int D, int sms);
 size_t rows_ws_bytes(int D, int sms);
