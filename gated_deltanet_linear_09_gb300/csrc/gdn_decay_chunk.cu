@@ -50,7 +50,7 @@ struct ChunkArgs {
 };
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, out;
 };
 
 // A piece's share of one head of one sequence: chunks [c0, c1) of n.
@@ -187,13 +187,17 @@ __device__ __forceinline__ void zero_tokens(const ChunkArgs& a, long long begin,
 // ------------------------------------------------------------------ waits that give up
 
 // The first wait that runs out marks the CTA dead and sets the status; from then on no wait blocks, no copy or
-// product is issued, and every role runs through to the end of its loops.
-__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return;
+// product is issued, and every role runs through to the end of its loops.  (Out of line, like all that is rare:
+// the roles' code together has to fit the instruction caches.  With everything inlined and unrolled 38 % of
+// the fetches missed, and the outputs of 4096 tokens of 32 heads took 59 us.)
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
   if (*dead == 0 && !mbar_wait(bar, parity)) {
     *dead = 1;
     set_status(status, GDN_STATUS_TIMEOUT);
   }
+}
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
+  if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, dead, status);
 }
 
 // ------------------------------------------------------------------ operands
@@ -202,8 +206,22 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);          //
 constexpr uint32_t kDescK = (16u >> 4) << 16;                                  // K-major: LBO unused
 constexpr uint32_t kDescMN = ((128u * 128u) >> 4) << 16;                       // MN-major: 64-column blocks
 
-__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t kind) {
-  return ((uint64_t)kDescHi << 32) | (((saddr & 0x3FFFFu) >> 4) | kind);
+__device__ __forceinline__ uint32_t desc(uint32_t saddr, uint32_t kind) { return ((saddr & 0x3FFFFu) >> 4) | kind; }
+// Products of operands whose descriptors' low words (the start address in sixteen-byte units, beside a
+// constant) are these.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
 }
 // bf16 operands, A MN-major too (bit 15).
 __host__ __device__ constexpr uint32_t idesc_bf16_mnmn(int M, int N) { return idesc_bf16_bmn(M, N) | (1u << 15); }
@@ -217,10 +235,25 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
-__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// Whether a pair of bf16 (magnitude bits, larger of several) holds an infinity or a NaN.
-__device__ __forceinline__ bool not_finite(uint32_t m) { return (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u; }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ bool any_nan(uint32_t w) { return (w & 0x7fffu) > 0x7f80u || (w & 0x7fff0000u) > 0x7f800000u; }
+__device__ __forceinline__ bool finite_lo(uint32_t w) { return (w & 0x7f80u) != 0x7f80u; }
+__device__ __forceinline__ bool finite_hi(uint32_t w) { return (w & 0x7f800000u) != 0x7f800000u; }
+// Pairs of f32 in one instruction.
+__device__ __forceinline__ void mul2(float& x, float& y, float f) {
+  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%0, %1};\nmov.b64 b, {%2, %2};\nmul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(f));
+}
 __device__ __forceinline__ void tmem_ld32_nw(uint32_t addr, uint32_t* r) {
   tmem_ld16_nw(addr, r);
   tmem_ld16_nw(addr + 16, r + 16);
@@ -233,16 +266,31 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x0, int x1, int x2, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(map), "r"(x0), "r"(x1),
+               "r"(x2), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
 // A token's log decay, in log2 units.
 __device__ __forceinline__ float decay_log2(const ChunkArgs& a, long long t, int h) {
   const float g = __ldg(a.g + t * a.g_ld + h);
   return (g < kLowest ? kLowest : g) * kLog2e;
 }
 
+// A factor as the sum of two bf16 (exact to 2^-17), the larger in the low half.
+__device__ __forceinline__ uint32_t two_parts(float w) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(w);
+  return pack2(w, w - __bfloat162float(hi));
+}
+
 // The decays of `rows` tokens from t on (a whole warp, lane = 4 tokens): up to and with each token, and of
-// what follows each in the chunk plus `rest`, as a factor (0 past the rows).  Returns the chunk's sum.
+// what follows each in the chunk plus `rest`, as a factor in two parts (0 past the rows).  Returns the chunk's sum.
 __device__ __forceinline__ float chunk_decays(const ChunkArgs& a, int t, int rows, int h, float rest, float* upto,
-                                              float* after) {
+                                              uint32_t* after) {
   const int lane = threadIdx.x & 31;
   float g[4];
 #pragma unroll
@@ -271,71 +319,89 @@ __device__ __forceinline__ float chunk_decays(const ChunkArgs& a, int t, int row
   w.z = lane * 4 + 2 < rows ? ex2f(w.z) : 0.f;
   w.w = lane * 4 + 3 < rows ? ex2f(w.w) : 0.f;
   if (upto) *reinterpret_cast<float4*>(upto + lane * 4) = p;
-  *reinterpret_cast<float4*>(after + lane * 4) = w;
+  *reinterpret_cast<uint4*>(after + lane * 4) = make_uint4(two_parts(w.x), two_parts(w.y), two_parts(w.z), two_parts(w.w));
   return all;
 }
 
 // Turns a K tile [DK / 64][128 rows][128 bytes], 128-byte swizzled, into the high parts of its rows times w, in
-// place, and the low parts beside it.  NT threads, this one the t-th.
+// place, and the low parts beside it.  NT threads, this one the t-th.  With w = w1 + w2 in bf16, all of it is
+// bf16 arithmetic on pairs: h = k w1 rounded, k w1 - h exactly, and l = that plus k w2.  The factor of a 16-byte
+// piece is its row's.
 template <int DK, int NT>
-__device__ __forceinline__ void split_keys(uint8_t* k, uint8_t* lo, const float* w, int t) {
-#pragma unroll 4
-  for (int i = 0; i < DK * kC / 8 / NT; ++i) {
-    const int at = i * NT + t;
-    const float f = w[(at >> 3) & (kC - 1)];
-    uint4* p = reinterpret_cast<uint4*>(k) + at;
-    const uint4 u = *p;
+__device__ __noinline__ void fix_split(uint8_t* k, uint8_t* lo, const uint32_t* w, int t) {
+  // rows of weight 0 are 0 whatever the key; no low part beside an infinity or a NaN
+  for (int at = t; at < DK * kC / 8; at += NT) {
+    uint32_t* h = reinterpret_cast<uint32_t*>(k) + 4 * at;
+    uint32_t* l = reinterpret_cast<uint32_t*>(lo) + 4 * at;
+    const bool none = (w[(at >> 3) & (kC - 1)] & 0x7fffu) == 0;
+    for (int e = 0; e < 4; ++e) {
+      if (none) h[e] = l[e] = 0;
+      if (!finite_lo(h[e])) l[e] &= 0xffff0000u;
+      if (!finite_hi(h[e])) l[e] &= 0xffffu;
+    }
+  }
+}
+template <int DK, int NT>
+__device__ __forceinline__ void split_keys(uint8_t* k, uint8_t* lo, const uint32_t* w, int t) {
+  constexpr int kPer = DK * kC / 8 / NT;
+  uint32_t sum = 0;                        // of the low parts: a NaN beside every key that is not finite
+  uint4* kp = reinterpret_cast<uint4*>(k) + t;
+  uint4* lp = reinterpret_cast<uint4*>(lo) + t;
+  uint4 u = *kp;
+  uint32_t f = w[(t >> 3) & (kC - 1)];
+#pragma unroll 2
+  for (int i = 0; i < kPer; ++i) {
+    const int next = (i + 1 < kPer ? i + 1 : i) * NT;        // (ahead of the stores, which may alias it)
+    const uint4 un = reinterpret_cast<const uint4*>(k)[next + t];
+    const uint32_t fn = w[((next + t) >> 3) & (kC - 1)];
+    const uint32_t w1 = __byte_perm(f, 0, 0x1010), w2 = __byte_perm(f, 0, 0x3232);
     const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-    uint32_t h[4], l[4], top = 0;
+    uint32_t h[4], l[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float a = lo_f32(x[e]) * f, b = hi_f32(x[e]) * f;
-      h[e] = pack2(a, b);
-      l[e] = pack2(a - lo_f32(h[e]), b - hi_f32(h[e]));
-      top = __vmaxu2(top, h[e] & 0x7fff7fffu);
+      h[e] = mul_bf16x2(x[e], w1);
+      l[e] = fma_bf16x2(x[e], w2, fma_bf16x2(x[e], w1, h[e] ^ 0x80008000u));
+      sum = fma_bf16x2(l[e], 0, sum);
     }
-    if (f == 0.f) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = l[e] = 0;      // (whatever the key)
-    } else if (not_finite(top)) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {                      // no low part beside an infinity or a NaN
-        if ((h[e] & 0x7f80u) == 0x7f80u) l[e] &= 0xffff0000u;
-        if ((h[e] & 0x7f800000u) == 0x7f800000u) l[e] &= 0xffffu;
-      }
-    }
-    *p = make_uint4(h[0], h[1], h[2], h[3]);
-    reinterpret_cast<uint4*>(lo)[at] = make_uint4(l[0], l[1], l[2], l[3]);
+    *kp = make_uint4(h[0], h[1], h[2], h[3]);
+    *lp = make_uint4(l[0], l[1], l[2], l[3]);
+    kp += NT;
+    lp += NT;
+    u = un;
+    f = fn;
   }
+  if (any_nan(sum)) fix_split<DK, NT>(k, lo, w, t);
 }
 
 // Zeros in the place of a V tile's non-finite values and rows past the sequence; whether there were any of
 // the former.
-template <int BLOCKS, int NT>
-__device__ __forceinline__ bool clean_values(uint8_t* v, int rows, int t) {
+template <int NT>
+__device__ __noinline__ bool clean_slowly(uint8_t* v, int rows, int t) {
   bool bad = false;
-#pragma unroll 4
-  for (int i = 0; i < BLOCKS * 1024 / NT; ++i) {
-    const int at = i * NT + t, row = (at >> 3) & (kC - 1);
-    uint4* p = reinterpret_cast<uint4*>(v) + at;
-    const uint4 u = *p;
-    uint32_t x[4] = {u.x, u.y, u.z, u.w};
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, x[e] & 0x7fff7fffu);
-    if (row >= rows) {
-      *p = make_uint4(0, 0, 0, 0);
-    } else if (not_finite(top)) {
-      bad = true;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
-        if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu;
-      }
-      *p = make_uint4(x[0], x[1], x[2], x[3]);
+  for (int at = t; at < 2048; at += NT) {
+    uint32_t* x = reinterpret_cast<uint32_t*>(v) + 4 * at;
+    const bool past = ((at >> 3) & (kC - 1)) >= rows;
+    for (int e = 0; e < 4; ++e) {
+      if (past) x[e] = 0;
+      if (!finite_lo(x[e])) { x[e] &= 0xffff0000u; bad = true; }
+      if (!finite_hi(x[e])) { x[e] &= 0xffffu; bad = true; }
     }
   }
   return bad;
+}
+template <int NT>
+__device__ __forceinline__ bool clean_values(uint8_t* v, int rows, int t) {
+  uint32_t sum[4] = {0, 0, 0, 0};          // NaN with any value that is not finite
+#pragma unroll 4
+  for (int i = 0; i < 2048 / NT; ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(v)[i * NT + t];
+    sum[0] = fma_bf16x2(u.x, 0, sum[0]);
+    sum[1] = fma_bf16x2(u.y, 0, sum[1]);
+    sum[2] = fma_bf16x2(u.z, 0, sum[2]);
+    sum[3] = fma_bf16x2(u.w, 0, sum[3]);
+  }
+  const bool odd = any_nan(sum[0]) || any_nan(sum[1]) || any_nan(sum[2]) || any_nan(sum[3]);
+  return odd || rows < kC ? clean_slowly<NT>(v, rows, t) : false;
 }
 
 // Barrier over n threads that returns whether any of them passed true.
@@ -350,33 +416,46 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool v) {
   return r != 0;
 }
 
-// Which of the columns c .. c + 31 a value not finite of tokens t - back .. t has reached by token t.
-__device__ __noinline__ uint32_t reached_columns(const ChunkArgs& a, long long t, int back, int head, int dv, int c) {
-  uint32_t m = 0;
-  float sum = 0.f;
-  for (int j = 0; j <= back && ex2f(sum) != 0.f; ++j) {
-    for (int e = 0; e < 32; ++e)
-      if (!(fabsf(__bfloat162float(a.v[(t - j) * a.v_ld + head * dv + c + e])) < INFINITY)) m |= 1u << e;
-    sum += decay_log2(a, t - j, head);
-  }
-  return m;
+// Byte of 16-byte piece `piece` of a row in an output tile [DV / 64][128 rows][128 bytes], 128-byte swizzled.
+__device__ __forceinline__ int tile_at(int row, int piece) {
+  return (piece >> 3) * (128 * kC) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
-// What the non-finite values of column c among tokens [t, t + rows) add to N elements of the state's column from
-// row d0 on: infinities and NaN, told apart as the recurrence does.
-template <int N>
-__device__ __noinline__ void add_non_finite(const ChunkArgs& a, long long t, int rows, int head, int dk, int dv, int c, int d0,
-                                            float* s) {
-  const int hk = head / (a.l.Hv / a.l.Hk);
+// NaN in those of `columns` columns from c on of an output tile's row that a value not finite of tokens
+// t - row .. t has reached by token t.
+__device__ __noinline__ void mark_reached(const ChunkArgs& a, long long t, int row, int head, int c, int columns, uint8_t* tile) {
   float sum = 0.f;
+  for (int j = 0; j <= row && ex2f(sum) != 0.f; ++j) {
+    for (int e = c; e < c + columns; ++e)
+      if (!(fabsf(__bfloat162float(a.v[(t - j) * a.v_ld + head * a.l.dv + e])) < INFINITY))
+        reinterpret_cast<__nv_bfloat16*>(tile + tile_at(row, e >> 3))[e & 7] = __float2bfloat16_rn(NAN);
+    sum += decay_log2(a, t - j, head);
+  }
+}
+
+// The first rows of an output tile (a sequence's last, when they are fewer than the tile's): 256 threads.
+__device__ __noinline__ void store_rows(const ChunkArgs& a, int t, int rows, int head, const uint8_t* tile, int tid) {
+  const int pieces = a.l.dv / 8;
+  for (int i = tid; i < rows * pieces; i += 256) {
+    const int row = i / pieces, piece = i % pieces;
+    *reinterpret_cast<uint4*>(a.out + ((long long)(t + row) * a.l.Hv + head) * a.l.dv + piece * 8) =
+        *reinterpret_cast<const uint4*>(tile + tile_at(row, piece));
+  }
+}
+
+// What the non-finite values of column c among tokens [t, t + rows) add to element d of the state's column:
+// infinities and NaN, told apart as the recurrence does.
+__device__ __noinline__ float non_finite_part(const ChunkArgs& a, long long t, int rows, int head, int c, int d) {
+  const int hk = head / (a.l.Hv / a.l.Hk);
+  float sum = 0.f, s = 0.f;
   for (int j = rows - 1; j >= 0; --j) {
     const float w = ex2f(sum);
     if (w == 0.f) break;
-    const float v = __bfloat162float(a.v[(t + j) * a.v_ld + head * dv + c]);
-    if (!(fabsf(v) < INFINITY))
-      for (int e = 0; e < N; ++e) s[e] += __bfloat162float(a.k[(t + j) * a.k_ld + hk * dk + d0 + e]) * w * v;
+    const float v = __bfloat162float(a.v[(t + j) * a.v_ld + head * a.l.dv + c]);
+    if (!(fabsf(v) < INFINITY)) s += __bfloat162float(a.k[(t + j) * a.k_ld + hk * a.l.dk + d]) * w * v;
     sum += decay_log2(a, t + j, head);
   }
+  return s;
 }
 
 template <typename... KArgs, typename... Args>
@@ -394,14 +473,33 @@ int launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStre
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// A dv-by-dk state (transposed: a TMEM lane is a column of the state) as 128 threads hold it: lane r is
-// column r, or for 64 columns column r % 64 and half of the rows.
+// A dv-by-dk state (transposed: a TMEM lane is a column of the state) as eight warps hold it: lane r of the
+// warps r / 32 and r / 32 + 4 is column r, half of the rows each, or for 64 columns column r % 64 and a quarter
+// of the rows.
 template <int DK, int DV>
 struct StateRows {
-  static constexpr int kCols = DV == 128 ? DK : DK / 2;       // state rows of a thread
-  static __device__ __forceinline__ int column(int r) { return r & (DV - 1); }
-  static __device__ __forceinline__ int first(int r) { return DV == 128 ? 0 : (r >> 6) * kCols; }
+  static constexpr int kRows = DK * DV / 256, kBlock = kRows < 32 ? kRows : 32;
+  int lanes, column, first;
+  __device__ __forceinline__ explicit StateRows(int t) {
+    const int r = t & 127, half = t >> 7;
+    lanes = r & ~31;
+    column = r & (DV - 1);
+    first = (DV == 128 ? half : (r >> 6) * 2 + half) * kRows;
+  }
 };
+
+// kBlock columns of the lane's row.
+template <int N>
+__device__ __forceinline__ void tmem_row(uint32_t addr, float* s) {
+  uint32_t x[N];
+  if constexpr (N == 32) tmem_ld32_nw(addr, x);
+  else tmem_ld16_nw(addr, x);
+  tmem_wait_ld();
+  reg_fence16(x);
+  if constexpr (N == 32) reg_fence16(x + 16);
+#pragma unroll
+  for (int e = 0; e < N; ++e) s[e] = __uint_as_float(x[e]);
+}
 
 // ------------------------------------------------------------------ what a cut piece adds to the state
 
@@ -410,7 +508,7 @@ struct __align__(1024) SumSmem {
   uint8_t k[2][DK * kC * 2];
   uint8_t lo[2][DK * kC * 2];
   uint8_t v[2][128 * kC * 2];         // 64 columns twice, so that they fill the product's 128 rows
-  float w[2][kC];
+  uint32_t w[2][kC];
   Scan scan;
   Run run;
   float decay;
@@ -493,13 +591,13 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
         wait(&sm.ready[st], (i >> 1) & 1);
         if (dead()) break;
         fence_after_sync();
-        const uint64_t va = desc(smem_u32(sm.v[st]), kDescMN);
-#pragma unroll
+        const uint32_t va = desc(smem_u32(sm.v[st]), kDescMN);
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {
-          const uint64_t kb = desc(smem_u32(part ? sm.lo[st] : sm.k[st]), kDescMN);
+          const uint32_t kb = desc(smem_u32(part ? sm.lo[st] : sm.k[st]), kDescMN);
 #pragma unroll
           for (int ks = 0; ks < kC / 16; ++ks)
-            mma_bf16(tmem, desc_add(va, ks * 2048), desc_add(kb, ks * 2048), idesc_bf16_mnmn(128, DK), i > 0 || part > 0 || ks > 0);
+            mma_ss(tmem, va + ks * 128, kb + ks * 128, idesc_bf16_mnmn(128, DK), i > 0 || part > 0 || ks > 0);
         }
         mma_commit(&sm.empty[st]);
       }
@@ -513,7 +611,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
       wait(&sm.full[st], (i >> 1) & 1);
       __syncwarp();
       split_keys<DK, 256>(sm.k[st], sm.lo[st], sm.w[st], tid);
-      if (clean_values<2, 256>(sm.v[st], kC, tid)) sm.bad = 1;
+      if (clean_values<256>(sm.v[st], kC, tid)) sm.bad = 1;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ready[st]);
@@ -523,41 +621,36 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
   wait(&sm.done, 0);
   __syncthreads();
   fence_after_sync();
-  if (warp < 4) {
+  if (warp < 8) {
     using L = StateRows<DK, DV>;
-    const int c = L::column(tid), d0 = L::first(tid);
+    constexpr int N = L::kBlock;
+    const L at(tid);
     const bool begins = run.c0 == 0 && run.init;        // with a state
     const float f = ex2f(sm.decay);
-    float* kept = a.ws + (size_t)(a.grid + piece) * (DK * DV);
-    const float* src = a.l.state + ((long long)run.slot * a.l.Hv + run.head) * (DK * DV);
-    float* dst = a.ws + (size_t)piece * (DK * DV);
-#pragma unroll
-    for (int b = 0; b < L::kCols; b += 32) {
-      uint32_t r[32];
-      tmem_ld32_nw(tmem + ((uint32_t)(warp * 32) << 16) + d0 + b, r);
-      tmem_wait_ld();
-      reg_fence16(r);
-      reg_fence16(r + 16);
-      float s[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(r[e]);
+    float* kept = a.ws + (size_t)(a.grid + piece) * (DK * DV) + at.column;
+    const float* src = a.l.state + ((long long)run.slot * a.l.Hv + run.head) * (DK * DV) + at.column;
+    float* dst = a.ws + (size_t)piece * (DK * DV) + at.column;
+#pragma unroll 1
+    for (int b = 0; b < L::kRows; b += N) {
+      const int d = at.first + b;
+      float s[N], x[N];
       if (begins) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float x = src[(d0 + b + e) * DV + c];
-          kept[(d0 + b + e) * DV + c] = x;
-          if (f != 0.f) s[e] = fmaf(f, x, s[e]);
+        for (int e = 0; e < N; ++e) x[e] = __ldcg(src + (d + e) * DV);
+      }
+      tmem_row<N>(tmem + ((uint32_t)at.lanes << 16) + d, s);
+      if (begins) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          kept[(d + e) * DV] = x[e];
+          if (f != 0.f) s[e] = fmaf(f, x[e], s[e]);
         }
       }
-      if (sm.bad) {
-        float more[32];
-        for (int e = 0; e < 32; ++e) more[e] = 0.f;
-        add_non_finite<32>(a, run.t0 + run.c0 * kC, n * kC, run.head, DK, DV, c, d0 + b, more);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] += more[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) dst[(d0 + b + e) * DV + c] = s[e];
+      for (int e = 0; e < N; ++e) dst[(d + e) * DV] = s[e];
+      if (sm.bad)
+        for (int e = 0; e < N; ++e)
+          dst[(d + e) * DV] += non_finite_part(a, run.t0 + run.c0 * kC, n * kC, run.head, at.column, d + e);
     }
   }
   if (tid == 0) decays[piece] = sm.decay;
@@ -599,7 +692,8 @@ struct __align__(1024) OutSmem {
   uint8_t v[2][128 * kC * 2];         // 64 columns twice, so that they fill the state product's 128 rows
   uint8_t state[DK * DV * 2];         // bf16 [DK / 64][DV rows][128 bytes]
   uint8_t lo[DK * kC * 2];
-  float upto[2][kC], w[2][kC];
+  float upto[2][kC];
+  uint32_t w[2][kC];
   Run runs[kRing];
   uint32_t tmem;
   int dead;
@@ -608,10 +702,12 @@ struct __align__(1024) OutSmem {
   uint64_t run_full[kRing], run_empty[kRing], drained;
 };
 
-constexpr int kOutThreads = 384;      // scores and outputs; keys and state; MMA, K and V loader, Q loader, runs
-constexpr int kReaders = 11;
+// Eight warps for scores and outputs, eight for keys and state; MMA, K and V loader, Q loader, runs.
+constexpr int kOutThreads = 640;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kLoadQWarp = 18, kRunWarp = 19;
+constexpr int kReaders = 19;
 
-// TMEM columns: scores (their decayed bf16 form in the lower half), the two parts of the output, the state.
+// TMEM columns: scores (their decayed bf16 form in the lower half of each half), the two parts of the output, the state.
 constexpr int kTmS = 0, kTmO = 128, kTmI = 256, kTmState = 384;
 
 template <int DK, int DV>
@@ -630,11 +726,11 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.s_done, 1);
-    mbar_init(&sm.p_ready, 4);
-    mbar_init(&sm.st_ready, 4);
-    mbar_init(&sm.ks_ready, 4);
+    mbar_init(&sm.p_ready, 8);
+    mbar_init(&sm.st_ready, 8);
+    mbar_init(&sm.ks_ready, 8);
     mbar_init(&sm.o_done, 1);
-    mbar_init(&sm.o_empty, 4);
+    mbar_init(&sm.o_empty, 8);
     mbar_init(&sm.g_done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.run_full[i], 1);
@@ -654,7 +750,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   const long long into = scan.into;
   zero_tokens(a, __ldg(a.cu + a.num_seqs), a.total);
   if (piece >= line.pieces) return;
-  if (warp == 8) tmem_alloc(&sm.tmem, 512);
+  if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 512);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -685,7 +781,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   int n = 0;                          // chunks so far
   const int group = a.l.Hv / a.l.Hk;
 
-  if (warp == 11) {
+  if (warp == kRunWarp) {
     // ---------------------------------------------------------------- runs
     Walk walk;
     walk.start(a, line, line.x0, seq, into);
@@ -703,7 +799,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       __syncwarp();
       if (++ring == kRing) { ring = 0; ring_phase ^= 1u; }
     }
-  } else if (warp == 9) {
+  } else if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- keys, values, decays
     for (Run r = next_run(); r.kind != kEnd; r = next_run()) {
       if (r.kind != kRun) continue;
@@ -723,7 +819,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       }
     }
     for (int i = max(0, n - 2); i < n; ++i) mbar_wait(&sm.kv_full[i & 1], (i >> 1) & 1, 100000000ull);
-  } else if (warp == 10) {
+  } else if (warp == kLoadQWarp) {
     // ---------------------------------------------------------------- queries
     for (Run r = next_run(); r.kind != kEnd; r = next_run()) {
       if (r.kind != kRun) continue;
@@ -737,10 +833,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       }
     }
     if (n > 0) mbar_wait(&sm.q_full, (n - 1) & 1, 100000000ull);
-  } else if (warp == 8) {
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA (one thread)
-    const uint64_t qd = desc(smem_u32(sm.q), kDescK), sd = desc(smem_u32(sm.state), kDescK);
-    const uint64_t lod = desc(smem_u32(sm.lo), kDescMN);
+    const uint32_t qd = desc(smem_u32(sm.q), kDescK), sd = desc(smem_u32(sm.state), kDescK);
+    const uint32_t lod = desc(smem_u32(sm.lo), kDescMN);
     while (lane == 0) {
       wait(&sm.run_full[ring], ring_phase);
       const Run r = sm.runs[ring];
@@ -750,8 +846,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       if (r.kind != kRun) continue;
       for (int c = r.c0; c < r.c1; ++c, ++n) {
         const int st = n & 1;
-        const uint64_t kk = desc(smem_u32(sm.k[st]), kDescK), km = desc(smem_u32(sm.k[st]), kDescMN);
-        const uint64_t vm = desc(smem_u32(sm.v[st]), kDescMN);
+        const uint32_t kk = desc(smem_u32(sm.k[st]), kDescK), km = desc(smem_u32(sm.k[st]), kDescMN);
+        const uint32_t vm = desc(smem_u32(sm.v[st]), kDescMN);
         wait(&sm.q_full, n & 1);
         wait(&sm.kv_full[st], (n >> 1) & 1);
         if (dead()) break;
@@ -759,8 +855,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         // scores (the product with the last chunk's, which holds these columns, was issued before)
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
-          const uint32_t o = (ks >> 2) * (128 * kC) + (ks & 3) * 32;
-          mma_bf16(tmem + kTmS, desc_add(qd, o), desc_add(kk, o), idesc_bf16(128, kC), ks > 0);
+          const uint32_t o = ((ks >> 2) * (128 * kC) + (ks & 3) * 32) / 16;
+          mma_ss(tmem + kTmS, qd + o, kk + o, idesc_bf16(128, kC), ks > 0);
         }
         mma_commit(&sm.s_done);
         // queries and the state before the chunk
@@ -770,27 +866,27 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         fence_after_sync();
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks)
-          mma_bf16(tmem + kTmI, desc_add(qd, (ks >> 2) * (128 * kC) + (ks & 3) * 32),
-                   desc_add(sd, (ks >> 2) * (128 * DV) + (ks & 3) * 32), idesc_bf16(128, DV), ks > 0);
+          mma_ss(tmem + kTmI, qd + ((ks >> 2) * (128 * kC) + (ks & 3) * 32) / 16,
+                 sd + ((ks >> 2) * (128 * DV) + (ks & 3) * 32) / 16, idesc_bf16(128, DV), ks > 0);
         mma_commit(&sm.q_empty);
         // the state's update, lanes = its columns
         wait(&sm.ks_ready, n & 1);
         if (dead()) break;
         fence_after_sync();
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          const uint32_t kb = part ? lod : km;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks)
-            mma_bf16(tmem + kTmState, desc_add(vm, ks * 2048), desc_add(part ? lod : km, ks * 2048), idesc_bf16_mnmn(128, DK), 1);
+          for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kTmState, vm + ks * 128, kb + ks * 128, idesc_bf16_mnmn(128, DK), 1);
+        }
         mma_commit(&sm.g_done);
         wait(&sm.p_ready, n & 1);
         if (dead()) break;
         fence_after_sync();
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          mma_bf16_tmem_a(tmem + kTmO, tmem + kTmS + ks * 8, desc_add(vm, ks * 2048), idesc_bf16_bmn(128, DV), ks > 0);
+          mma_ts(tmem + kTmO, tmem + kTmS + (ks >> 2) * 64 + (ks & 3) * 8, vm + ks * 128, idesc_bf16_bmn(128, DV), ks > 0);
         mma_commit(&sm.o_done);
-        mma_commit(&sm.kv_empty[st]);
       }
     }
     if (lane == 0) {                  // no product outlives the TMEM
@@ -798,14 +894,16 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       mbar_wait(&sm.drained, 0, 100000000ull);
     }
     __syncwarp();
-  } else if (warp < 4) {
-    // ---------------------------------------------------------------- scores and outputs: a thread to a token
-    const int i = tid;
-    const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-    for (Run r = next_run(); r.kind != kEnd; r = next_run()) {
+  } else if (warp < 8) {
+    // ------------------------------- scores and outputs: a token to a thread and the one 128 on, half of its columns each
+    const int i = tid & 127, quad = warp & 3, half = warp >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+    while (true) {
+      const Run r = next_run();
+      if (bar_any(2, 256, r.kind == kEnd)) break;         // (together: they meet in barriers)
       if (r.kind == kZeros) {
         const int begin = r.c0 * kC, end = min(r.len, r.c1 * kC);
-        for (int t = begin + i; t < end; t += 128)
+        for (int t = begin + tid; t < end; t += 256)
           for (int d = 0; d < DV; d += 8)
             *reinterpret_cast<uint4*>(a.out + ((long long)(r.t0 + t) * a.l.Hv + r.head) * DV + d) = make_uint4(0, 0, 0, 0);
         continue;
@@ -817,32 +915,31 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         const float mine = upto[i] + a.log2_scale;
         wait_warp(&sm.s_done, n & 1);
         fence_after_sync();
-#pragma unroll
-        for (int b = 0; b < kC / 32; ++b) {
-          uint32_t x[32], p[16];
-          if (b > warp) {                                   // later tokens only
+#pragma unroll 1
+        for (int bb = 0; bb < 2; ++bb) {
+          const int b = half * 2 + bb;
+          float x[32];
+          uint32_t p[16];
+          if (b > quad) {                                   // later tokens only
 #pragma unroll
             for (int e = 0; e < 16; ++e) p[e] = 0;
           } else {
-            tmem_ld32_nw(tl + kTmS + b * 32, x);
-            tmem_wait_ld();
-            reg_fence16(x);
-            reg_fence16(x + 16);
+            tmem_row<32>(tl + kTmS + b * 32, x);
+            const float4* g4 = reinterpret_cast<const float4*>(upto + b * 32);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 g = *reinterpret_cast<const float4*>(upto + b * 32 + e);
-              const float gg[4] = {g.x, g.y, g.z, g.w};
-              float y[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f) {
-                y[f] = __uint_as_float(x[e + f]) * ex2f(mine - gg[f]);
-                if (b == warp && b * 32 + e + f > i) y[f] = 0.f;
-              }
-              p[e / 2] = pack2(y[0], y[1]);
-              p[e / 2 + 1] = pack2(y[2], y[3]);
+              const float4 g = g4[e / 4];
+              x[e] *= ex2f(mine - g.x);
+              x[e + 1] *= ex2f(mine - g.y);
+              x[e + 2] *= ex2f(mine - g.z);
+              x[e + 3] *= ex2f(mine - g.w);
             }
+            const int last = b == quad ? lane : 31;         // the last column that the token sees
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) p[e / 2] = pack2(e <= last ? x[e] : 0.f, e + 1 <= last ? x[e + 1] : 0.f);
           }
-          tmem_st16w_nw(tl + kTmS + b * 16, p);
+          // (over scores that this warp has read)
+          tmem_st16w_nw(tl + kTmS + half * 64 + bb * 16, p);
         }
         tmem_wait_st();
         fence_before_sync();
@@ -851,73 +948,77 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         fence_after_sync();
         const float f = ex2f(mine);
         const bool bad = *(volatile int*)&sm.bad[st] != 0;
-        const long long t = r.t0 + c * kC + i;
-        __nv_bfloat16* dst = a.out + (t * a.l.Hv + r.head) * DV;
-#pragma unroll
-        for (int b = 0; b < DV / 32; ++b) {
-          uint32_t x[32], y[32];
-          tmem_ld32_nw(tl + kTmO + b * 32, x);
-          tmem_ld32_nw(tl + kTmI + b * 32, y);
+        // through the place of the values, which the chunk's products have read
+        uint8_t* tile = sm.v[st];
+#pragma unroll 1
+        for (int b = 0; b < DV / 2; b += 16) {
+          float o[16];
+          uint32_t x[16], z[16];
+          tmem_ld16_nw(tl + kTmO + half * (DV / 2) + b, x);
+          tmem_ld16_nw(tl + kTmI + half * (DV / 2) + b, z);
           tmem_wait_ld();
           reg_fence16(x);
-          reg_fence16(x + 16);
-          reg_fence16(y);
-          reg_fence16(y + 16);
-          float o[32];
+          reg_fence16(z);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = f == 0.f ? __uint_as_float(x[e]) : fmaf(f, __uint_as_float(y[e]), __uint_as_float(x[e]));
-          if (bad && i < rows) {
-            const uint32_t m = reached_columns(a, t, i, r.head, DV, b * 32);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (m >> e & 1) o[e] = NAN;
+          for (int e = 0; e < 16; ++e) {
+            o[e] = __uint_as_float(x[e]);
+            if (f != 0.f) o[e] = fmaf(f, __uint_as_float(z[e]), o[e]);   // (a state that has decayed to nothing: nothing)
           }
-          if (i < rows) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + b * 32 + e) = make_uint4(pack2(o[e], o[e + 1]), pack2(o[e + 2], o[e + 3]),
-                                                                       pack2(o[e + 4], o[e + 5]), pack2(o[e + 6], o[e + 7]));
-          }
+          const int piece = (half * (DV / 2) + b) / 8;
+          *reinterpret_cast<uint4*>(tile + tile_at(i, piece)) =
+              make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+          *reinterpret_cast<uint4*>(tile + tile_at(i, piece + 1)) =
+              make_uint4(pack2(o[8], o[9]), pack2(o[10], o[11]), pack2(o[12], o[13]), pack2(o[14], o[15]));
         }
         fence_before_sync();
         arrive_warp(&sm.o_empty);
+        if (bad && i < rows) mark_reached(a, r.t0 + c * kC + i, i, r.head, half * (DV / 2), DV / 2, tile);
+        fence_proxy_async_smem();
+        bar_any(2, 256, false);
+        if (rows < kC) {
+          store_rows(a, r.t0 + c * kC, rows, r.head, tile, tid);
+          bar_any(2, 256, false);
+        }
+        if (tid == 0) {
+          if (rows == kC && !dead()) {
+            tma_store_3d(&maps.out, 0, r.t0 + c * kC, r.head * (DV / 64), tile);
+            bulk_commit();
+            bulk_wait_read();
+          }
+          mbar_arrive(&sm.kv_empty[st]);
+        }
+        __syncwarp();
       }
     }
+    if (tid == 0) bulk_wait();
   } else {
-    // ---------------------------------------------------------------- keys and state: a thread to a state column
+    // ------------------------------- keys and state
     using L = StateRows<DK, DV>;
-    const int t = tid - 128, col = L::column(t), d0 = L::first(t);
-    const uint32_t tl = tmem + kTmState + ((uint32_t)((warp - 4) * 32) << 16) + d0;
+    constexpr int N = L::kBlock;
+    const int t = tid - 256;
+    const L at(t);
+    const uint32_t tl = tmem + kTmState + ((uint32_t)at.lanes << 16) + at.first;
     constexpr long long kSize = DK * DV;
-    // the state as the products have left it, with what its last chunk's non-finite values add
-    auto held = [&](const Run& r, int c, bool bad, int b, float* s) {
-      uint32_t x[32];
-      tmem_ld32_nw(tl + b, x);
-      tmem_wait_ld();
-      reg_fence16(x);
-      reg_fence16(x + 16);
+    // adds what the non-finite values of chunk c of a run add to N rows of the state's column
+    auto add_bad = [&](const Run& r, int c, int d, float* s) {
+      float more[N];                  // (a copy, so that s stays in registers)
+#pragma unroll 1
+      for (int e = 0; e < N; ++e)
+        more[e] = non_finite_part(a, r.t0 + c * kC, min(kC, r.len - c * kC), r.head, at.column, d + e);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(x[e]);
-      if (bad) {
-        float more[32];               // (a copy, so that s stays in registers)
-        for (int e = 0; e < 32; ++e) more[e] = 0.f;
-        add_non_finite<32>(a, r.t0 + c * kC, min(kC, r.len - c * kC), r.head, DK, DV, col, d0 + b, more);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] += more[e];
-      }
+      for (int e = 0; e < N; ++e) s[e] += more[e];
     };
     while (true) {
       const Run r = next_run();
-      if (bar_any(1, 128, r.kind == kEnd)) break;         // (together: they meet in barriers)
+      if (bar_any(1, 256, r.kind == kEnd)) break;         // (together: they meet in barriers)
       if (r.kind != kRun) continue;
-      float* state = a.l.state + ((long long)r.slot * a.l.Hv + r.head) * kSize;
-      const float* from = r.c0 > 0                ? a.ws + (size_t)(piece - 1) * kSize
-                          : !r.init              ? nullptr
-                          : r.c1 < r.n           ? a.ws + (size_t)(a.grid + piece) * kSize
-                                                 : state;
+      float* state = a.l.state + ((long long)r.slot * a.l.Hv + r.head) * kSize + at.column;
+      const float* from = r.c0 > 0    ? a.ws + (size_t)(piece - 1) * kSize + at.column
+                          : !r.init   ? nullptr
+                          : r.c1 < r.n ? a.ws + (size_t)(a.grid + piece) * kSize + at.column
+                                       : state;
       if (r.n == 0 && !r.init) {
-        for (int e = 0; e < L::kCols; ++e) state[(d0 + e) * DV + col] = 0.f;
+        for (int e = 0; e < L::kRows; ++e) state[(at.first + e) * DV] = 0.f;
       }
       bool bad = false;               // the last chunk's values
       for (int c = r.c0; c < r.c1; ++c, ++n) {
@@ -928,36 +1029,44 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         }
         wait_warp(&sm.g_full[st], (n >> 1) & 1);
         const float f = ex2f(sm.upto[st][kC - 1]);
-#pragma unroll
-        for (int b = 0; b < L::kCols; b += 32) {
-          float s[32];
+#pragma unroll 1
+        for (int b = 0; b < L::kRows; b += N) {
+          const int d = at.first + b;
+          float s[N];
           if (c > r.c0) {
-            held(r, c - 1, bad, b, s);
+            tmem_row<N>(tl + b, s);
+            if (bad) add_bad(r, c - 1, d, s);
+          } else if (from) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e] = __ldcg(from + (d + e) * DV);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = from ? __ldcg(from + (d0 + b + e) * DV + col) : 0.f;
+            for (int e = 0; e < N; ++e) s[e] = 0.f;
           }
-          uint8_t* row = sm.state + ((d0 + b) >> 6) * (128 * DV) + col * 128;
+          uint8_t* row = sm.state + (d >> 6) * (128 * DV) + at.column * 128;
+          const int chunk = (d & 63) >> 3;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            const int at = (((d0 + b) & 63) + e) >> 3;
-            *reinterpret_cast<uint4*>(row + ((at ^ (col & 7)) << 4)) = make_uint4(
+          for (int e = 0; e < N; e += 8)
+            *reinterpret_cast<uint4*>(row + (((chunk + e / 8) ^ (at.column & 7)) << 4)) = make_uint4(
                 pack2(s[e], s[e + 1]), pack2(s[e + 2], s[e + 3]), pack2(s[e + 4], s[e + 5]), pack2(s[e + 6], s[e + 7]));
-          }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = f == 0.f ? 0.f : s[e] * f;
+          for (int e = 0; e < N; e += 2) mul2(s[e], s[e + 1], f);
+          if (f == 0.f) {                                   // (whatever it was)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e] = 0.f;
+          }
           tmem_st16_nw(tl + b, s);
-          tmem_st16_nw(tl + b + 16, s + 16);
+          if constexpr (N == 32) tmem_st16_nw(tl + b + 16, s + 16);
         }
         tmem_wait_st();
         fence_before_sync();
         fence_proxy_async_smem();
         arrive_warp(&sm.st_ready);
         wait_warp(&sm.kv_full[st], (n >> 1) & 1);
-        bad = clean_values<2, 128>(sm.v[st], min(kC, r.len - c * kC), t);
+        bad = clean_values<256>(sm.v[st], min(kC, r.len - c * kC), t);
         wait_warp(&sm.s_done, n & 1);
-        split_keys<DK, 128>(sm.k[st], sm.lo, sm.w[st], t);
-        bad = bar_any(1, 128, bad);
+        split_keys<DK, 256>(sm.k[st], sm.lo, sm.w[st], t);
+        bad = bar_any(1, 256, bad);
         if (t == 0) sm.bad[st] = bad;
         fence_proxy_async_smem();
         arrive_warp(&sm.ks_ready);
@@ -966,12 +1075,13 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         wait_warp(&sm.g_done, (n & 1) ^ 1u);
         fence_after_sync();
         if (r.c1 == r.n) {
+#pragma unroll 1
+          for (int b = 0; b < L::kRows; b += N) {
+            float s[N];
+            tmem_row<N>(tl + b, s);
+            if (bad) add_bad(r, r.c1 - 1, at.first + b, s);
 #pragma unroll
-          for (int b = 0; b < L::kCols; b += 32) {
-            float s[32];
-            held(r, r.c1 - 1, bad, b, s);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) state[(d0 + b + e) * DV + col] = s[e];
+            for (int e = 0; e < N; ++e) state[(at.first + b + e) * DV] = s[e];
           }
         }
         fence_before_sync();
@@ -979,7 +1089,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     }
   }
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <int DK, int DV>
@@ -1027,7 +1137,8 @@ int launch_decay_prefill(const DecayView& l, const gdn_decay_tokens& t, const in
   Maps maps = {};
   if (total_tokens > 0 && !(make_rows_map(t.q, total_tokens, t.q_ld, l.Hk * l.dk, kC, l.dk / 64, &maps.q) &&
                             make_rows_map(t.k, total_tokens, t.k_ld, l.Hk * l.dk, kC, l.dk / 64, &maps.k) &&
-                            make_rows_map(t.v, total_tokens, t.v_ld, l.Hv * l.dv, kC, l.dv / 64, &maps.v)))
+                            make_rows_map(t.v, total_tokens, t.v_ld, l.Hv * l.dv, kC, l.dv / 64, &maps.v) &&
+                            make_rows_map(t.out, total_tokens, (long long)l.Hv * l.dv, l.Hv * l.dv, kC, l.dv / 64, &maps.out)))
     return GDN_ERR_CUDA;
   if (l.dk == 128) return l.dv == 128 ? launch_dims<128, 128>(a, maps, stream) : launch_dims<128, 64>(a, maps, stream);
   return l.dv == 128 ? launch_dims<64, 128>(a, maps, stream) : launch_dims<64, 64>(a, maps, stream);
