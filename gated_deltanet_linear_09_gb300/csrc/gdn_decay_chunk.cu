@@ -191,9 +191,20 @@ __device__ __forceinline__ void zero_tokens(const ChunkArgs& a, long long begin,
 // the roles' code together has to fit the instruction caches.  With everything inlined and unrolled 38 % of
 // the fetches missed, and the outputs of 4096 tokens of 32 heads took 59 us.)
 __device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
-  if (*dead == 0 && !mbar_wait(bar, parity)) {
-    *dead = 1;
-    set_status(status, GDN_STATUS_TIMEOUT);
+  const long long t0 = clock64();
+  while (*dead == 0) {
+    // (asleep until the phase completes, or for some time: polling takes a part of shared memory's bandwidth)
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return;
+    if (clock64() - t0 > 4000000000ll) {            // two seconds
+      *dead = 1;
+      set_status(status, GDN_STATUS_TIMEOUT);
+    }
   }
 }
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status) {
@@ -264,6 +275,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
           smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(x0), "r"(x1), "r"(x2)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x0, int x1, int x2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];\n" ::"l"(map), "r"(x0), "r"(x1), "r"(x2) : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x0, int x1, int x2, const void* src) {
@@ -376,32 +391,41 @@ __device__ __forceinline__ void split_keys(uint8_t* k, uint8_t* lo, const uint32
 // Zeros in the place of a V tile's non-finite values and rows past the sequence; whether there were any of
 // the former.
 template <int NT>
-__device__ __noinline__ bool clean_slowly(uint8_t* v, int rows, int t) {
-  bool bad = false;
+__device__ __noinline__ void clean_slowly(uint8_t* v, int t) {
   for (int at = t; at < 2048; at += NT) {
     uint32_t* x = reinterpret_cast<uint32_t*>(v) + 4 * at;
-    const bool past = ((at >> 3) & (kC - 1)) >= rows;
     for (int e = 0; e < 4; ++e) {
-      if (past) x[e] = 0;
-      if (!finite_lo(x[e])) { x[e] &= 0xffff0000u; bad = true; }
-      if (!finite_hi(x[e])) { x[e] &= 0xffffu; bad = true; }
+      if (!finite_lo(x[e])) x[e] &= 0xffff0000u;
+      if (!finite_hi(x[e])) x[e] &= 0xffffu;
     }
   }
-  return bad;
 }
 template <int NT>
 __device__ __forceinline__ bool clean_values(uint8_t* v, int rows, int t) {
   uint32_t sum[4] = {0, 0, 0, 0};          // NaN with any value that is not finite
-#pragma unroll 4
-  for (int i = 0; i < 2048 / NT; ++i) {
-    const uint4 u = reinterpret_cast<const uint4*>(v)[i * NT + t];
-    sum[0] = fma_bf16x2(u.x, 0, sum[0]);
-    sum[1] = fma_bf16x2(u.y, 0, sum[1]);
-    sum[2] = fma_bf16x2(u.z, 0, sum[2]);
-    sum[3] = fma_bf16x2(u.w, 0, sum[3]);
+  constexpr int kBatch = 8;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 2048 / NT; i0 += kBatch) {
+    uint4 u[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = (i0 + i) * NT + t;    // (of a row past the sequence: row 0)
+      u[i] = reinterpret_cast<const uint4*>(v)[((at >> 3) & (kC - 1)) < rows ? at : at & 7];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      sum[0] = fma_bf16x2(u[i].x, 0, sum[0]);
+      sum[1] = fma_bf16x2(u[i].y, 0, sum[1]);
+      sum[2] = fma_bf16x2(u[i].z, 0, sum[2]);
+      sum[3] = fma_bf16x2(u[i].w, 0, sum[3]);
+    }
   }
+  if (rows < kC)
+    for (int block = 0; block < 2; ++block)
+      for (int at = rows * 8 + t; at < 1024; at += NT) reinterpret_cast<uint4*>(v)[block * 1024 + at] = make_uint4(0, 0, 0, 0);
   const bool odd = any_nan(sum[0]) || any_nan(sum[1]) || any_nan(sum[2]) || any_nan(sum[3]);
-  return odd || rows < kC ? clean_slowly<NT>(v, rows, t) : false;
+  if (odd) clean_slowly<NT>(v, t);
+  return odd;
 }
 
 // Barrier over n threads that returns whether any of them passed true.
@@ -433,13 +457,20 @@ __device__ __noinline__ void mark_reached(const ChunkArgs& a, long long t, int r
   }
 }
 
-// The first rows of an output tile (a sequence's last, when they are fewer than the tile's): 256 threads.
-__device__ __noinline__ void store_rows(const ChunkArgs& a, int t, int rows, int head, const uint8_t* tile, int tid) {
-  const int pieces = a.l.dv / 8;
-  for (int i = tid; i < rows * pieces; i += 256) {
-    const int row = i / pieces, piece = i % pieces;
-    *reinterpret_cast<uint4*>(a.out + ((long long)(t + row) * a.l.Hv + head) * a.l.dv + piece * 8) =
-        *reinterpret_cast<const uint4*>(tile + tile_at(row, piece));
+// The first rows of an output tile (a sequence's last, when they are fewer than the tile's), by a warp.
+template <int DV>
+__device__ __noinline__ void store_rows(const ChunkArgs& a, int t, int rows, int head, const uint8_t* tile, int lane) {
+  constexpr int kPieces = DV / 8, kStep = 32 / kPieces, kBatch = 8;
+  const int piece = lane % kPieces;
+  const long long ld = (long long)a.l.Hv * DV;
+  __nv_bfloat16* out = a.out + ((long long)t * a.l.Hv + head) * DV + piece * 8;
+  for (int row0 = lane / kPieces; row0 < rows; row0 += kStep * kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const uint4*>(tile + tile_at(min(row0 + i * kStep, kC - 1), piece));
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (row0 + i * kStep < rows) *reinterpret_cast<uint4*>(out + (row0 + i * kStep) * ld) = x[i];
   }
 }
 
@@ -661,25 +692,48 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
 
 // ------------------------------------------------------------------ along the pieces
 
-// S_p <- e^g_p S_(p-1) + S_p over each run's pieces, 1,024 elements a CTA.
+// S_p <- e^g_p S_(p-1) + S_p over each run's pieces, 1,024 elements a CTA.  Which pieces follow, and their decays,
+// are read first, and the states a few at a time: the chain itself waits for no load.
 __global__ void __launch_bounds__(256) chain_kernel(const ChunkArgs a) {
+  constexpr int kAhead = 4;
+  __shared__ float decay[256];
+  __shared__ int ends;
   pdl_begin();
-  const int size = a.l.dk * a.l.dv;
+  const int size = a.l.dk * a.l.dv, tid = threadIdx.x;
   const float* decays = a.ws + 2 * (size_t)a.grid * size;
   const int* flags = reinterpret_cast<const int*>(decays + a.grid);
   if (__ldcg(flags + blockIdx.x) != 1) return;
-  float4* p = reinterpret_cast<float4*>(a.ws) + ((size_t)blockIdx.x * size / 4) + blockIdx.y * 256 + threadIdx.x;
+  float4* p = reinterpret_cast<float4*>(a.ws) + ((size_t)blockIdx.x * size / 4) + blockIdx.y * 256 + tid;
   float4 s = __ldcg(p);
-  for (int i = blockIdx.x + 1; i < a.grid && __ldcg(flags + i) == 2; ++i) {
-    p += size / 4;
-    float4 x = __ldcg(p);
-    const float f = ex2f(__ldcg(decays + i));
-    if (f != 0.f) {
-      x.x = fmaf(f, s.x, x.x); x.y = fmaf(f, s.y, x.y);
-      x.z = fmaf(f, s.z, x.z); x.w = fmaf(f, s.w, x.w);
+  for (int first = blockIdx.x + 1; first < a.grid; first += 256) {
+    // pieces first .. first + 255, as far as they go on
+    if (tid == 0) ends = 256;
+    __syncthreads();
+    const bool on = first + tid < a.grid && __ldcg(flags + first + tid) == 2;
+    if (on) decay[tid] = ex2f(__ldcg(decays + first + tid));
+    else atomicMin(&ends, tid);
+    __syncthreads();
+    const int count = ends;
+    for (int i0 = 0; i0 < count; i0 += kAhead) {
+      float4 x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i0 + i < count) x[i] = __ldcg(p + (size_t)(i + 1) * (size / 4));
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i >= count) break;
+        const float f = decay[i0 + i];
+        p += size / 4;
+        if (f != 0.f) {
+          x[i].x = fmaf(f, s.x, x[i].x); x[i].y = fmaf(f, s.y, x[i].y);
+          x[i].z = fmaf(f, s.z, x[i].z); x[i].w = fmaf(f, s.w, x[i].w);
+        }
+        s = x[i];
+        __stcg(p, s);
+      }
     }
-    __stcg(p, x);
-    s = x;
+    if (count < 256) return;
+    __syncthreads();
   }
 }
 
@@ -697,14 +751,14 @@ struct __align__(1024) OutSmem {
   Run runs[kRing];
   uint32_t tmem;
   int dead;
-  int bad[2];
-  uint64_t kv_full[2], kv_empty[2], g_full[2], q_full, q_empty, s_done, p_ready, st_ready, ks_ready, o_done, o_empty, g_done;
+  int bad[4];
+  uint64_t k_full[2], v_full[2], v_ready[2], k_empty[2], v_empty[2], g_full[2], q_full, q_empty, s_done, p_ready, st_ready, ks_ready, o_done, o_empty, g_done, t_ready;
   uint64_t run_full[kRing], run_empty[kRing], drained;
 };
 
-// Eight warps for scores and outputs, eight for keys and state; MMA, K and V loader, Q loader, runs.
+// Eight warps for scores and outputs, eight for keys and state; MMA, K and V loader, runs, Q loader and check of V, outputs.
 constexpr int kOutThreads = 640;
-constexpr int kMmaWarp = 16, kLoadWarp = 17, kLoadQWarp = 18, kRunWarp = 19;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kLoadQWarp = 18, kStoreWarp = 19;
 constexpr int kReaders = 19;
 
 // TMEM columns: scores (their decayed bf16 form in the lower half of each half), the two parts of the output, the state.
@@ -719,8 +773,11 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   pdl_begin();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 1);
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.v_ready[i], 1);
       mbar_init(&sm.g_full[i], 1);
     }
     mbar_init(&sm.q_full, 1);
@@ -731,6 +788,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     mbar_init(&sm.ks_ready, 8);
     mbar_init(&sm.o_done, 1);
     mbar_init(&sm.o_empty, 8);
+    mbar_init(&sm.t_ready, 8);
     mbar_init(&sm.g_done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.run_full[i], 1);
@@ -781,24 +839,25 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   int n = 0;                          // chunks so far
   const int group = a.l.Hv / a.l.Hk;
 
-  if (warp == kRunWarp) {
-    // ---------------------------------------------------------------- runs
-    Walk walk;
-    walk.start(a, line, line.x0, seq, into);
-    Run r;
-    for (bool more = true; more;) {
-      more = walk.next(&r);
-      wait_warp(&sm.run_empty[ring], ring_phase ^ 1u);
-      if (warp_dead()) break;
-      if (lane == 0) {
-        if (more && r.slot >= a.l.num_slots) set_status(a.l.status, GDN_STATUS_SLOT_RANGE);
-        if (!more) r.kind = kEnd;
-        sm.runs[ring] = r;
-        mbar_arrive(&sm.run_full[ring]);
+  if (warp == kStoreWarp) {
+    // ---------------------------------------------------------------- outputs to memory
+    for (Run r = next_run(); r.kind != kEnd; r = next_run()) {
+      if (r.kind != kRun) continue;
+      for (int c = r.c0; c < r.c1; ++c, ++n) {
+        const int st = n & 1, rows = min(kC, r.len - c * kC);
+        wait_warp(&sm.t_ready, n & 1);
+        if (rows < kC) {
+          store_rows<DV>(a, r.t0 + c * kC, rows, r.head, sm.v[st], lane);
+          fence_proxy_async_smem();                         // (the next values come by the other proxy)
+        } else if (lane == 0 && !dead()) {
+          tma_store_3d(&maps.out, 0, r.t0 + c * kC, r.head * (DV / 64), sm.v[st]);
+          bulk_commit();
+          bulk_wait_read();
+        }
+        arrive_warp(&sm.v_empty[st]);
       }
-      __syncwarp();
-      if (++ring == kRing) { ring = 0; ring_phase ^= 1u; }
     }
+    if (lane == 0) bulk_wait();
   } else if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- keys, values, decays
     for (Run r = next_run(); r.kind != kEnd; r = next_run()) {
@@ -806,31 +865,64 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       const int hk = r.head / group;
       for (int c = r.c0; c < r.c1; ++c, ++n) {
         const int st = n & 1, t = r.t0 + c * kC;
-        if (n >= 2) wait_warp(&sm.kv_empty[st], ((n >> 1) & 1) ^ 1u);
+        if (n >= 2) wait_warp(&sm.k_empty[st], ((n >> 1) & 1) ^ 1u);
         if (lane == 0 && !dead()) {
-          mbar_arrive_expect_tx(&sm.kv_full[st], DK * kC * 2 + 128 * kC * 2);
-          tma_load_3d(sm.k[st], &maps.k, 0, t, hk * (DK / 64), &sm.kv_full[st]);
-          tma_load_3d(sm.v[st], &maps.v, 0, t, r.head * (DV / 64), &sm.kv_full[st]);
-          if (DV == 64) tma_load_3d(sm.v[st] + 64 * kC * 2, &maps.v, 0, t, r.head, &sm.kv_full[st]);
+          mbar_arrive_expect_tx(&sm.k_full[st], DK * kC * 2);
+          tma_load_3d(sm.k[st], &maps.k, 0, t, hk * (DK / 64), &sm.k_full[st]);
         }
         __syncwarp();
         chunk_decays(a, t, min(kC, r.len - c * kC), r.head, 0.f, sm.upto[st], sm.w[st]);
         arrive_warp(&sm.g_full[st]);
+        if (n >= 2) wait_warp(&sm.v_empty[st], ((n >> 1) & 1) ^ 1u);
+        if (lane == 0 && !dead()) {
+          mbar_arrive_expect_tx(&sm.v_full[st], 128 * kC * 2);
+          tma_load_3d(sm.v[st], &maps.v, 0, t, r.head * (DV / 64), &sm.v_full[st]);
+          if (DV == 64) tma_load_3d(sm.v[st] + 64 * kC * 2, &maps.v, 0, t, r.head, &sm.v_full[st]);
+        }
+        __syncwarp();
       }
     }
-    for (int i = max(0, n - 2); i < n; ++i) mbar_wait(&sm.kv_full[i & 1], (i >> 1) & 1, 100000000ull);
+    for (int i = max(0, n - 2); i < n; ++i) {
+      mbar_wait(&sm.k_full[i & 1], (i >> 1) & 1, 100000000ull);
+      mbar_wait(&sm.v_full[i & 1], (i >> 1) & 1, 100000000ull);
+    }
   } else if (warp == kLoadQWarp) {
-    // ---------------------------------------------------------------- queries
-    for (Run r = next_run(); r.kind != kEnd; r = next_run()) {
-      if (r.kind != kRun) continue;
-      for (int c = r.c0; c < r.c1; ++c, ++n) {
+    // ---------------------------------------------------------------- runs, one ahead, queries, check of the values
+    Walk walk;
+    walk.start(a, line, line.x0, seq, into);
+    auto publish = [&](Run* r) {
+      if (!walk.next(r)) r->kind = kEnd;
+      wait_warp(&sm.run_empty[ring], ring_phase ^ 1u);
+      if (lane == 0 && !dead()) {
+        if (r->kind != kEnd && r->slot >= a.l.num_slots) set_status(a.l.status, GDN_STATUS_SLOT_RANGE);
+        sm.runs[ring] = *r;
+        mbar_arrive(&sm.run_full[ring]);
+      }
+      __syncwarp();
+      if (++ring == kRing) { ring = 0; ring_phase ^= 1u; }
+    };
+    Run r, ahead;
+    publish(&r);
+    while (r.kind != kEnd && !warp_dead()) {
+      publish(&ahead);
+      for (int c = r.c0; r.kind == kRun && c < r.c1; ++c, ++n) {
         if (n >= 1) wait_warp(&sm.q_empty, (n & 1) ^ 1u);
         if (lane == 0 && !dead()) {
           mbar_arrive_expect_tx(&sm.q_full, DK * kC * 2);
           tma_load_3d(sm.q, &maps.q, 0, r.t0 + c * kC, r.head / group * (DK / 64), &sm.q_full);
+          // (one place for queries: the next ones wait in L2)
+          if (c + 1 < r.c1) tma_prefetch_3d(&maps.q, 0, r.t0 + (c + 1) * kC, r.head / group * (DK / 64));
         }
         __syncwarp();
+        // values that are not finite
+        const int st = n & 1;
+        wait_warp(&sm.v_full[st], (n >> 1) & 1);
+        const bool bad = __any_sync(0xffffffffu, clean_values<32>(sm.v[st], min(kC, r.len - c * kC), lane));
+        if (lane == 0) sm.bad[n & 3] = bad;
+        fence_proxy_async_smem();
+        arrive_warp(&sm.v_ready[st]);
       }
+      r = ahead;
     }
     if (n > 0) mbar_wait(&sm.q_full, (n - 1) & 1, 100000000ull);
   } else if (warp == kMmaWarp) {
@@ -849,7 +941,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         const uint32_t kk = desc(smem_u32(sm.k[st]), kDescK), km = desc(smem_u32(sm.k[st]), kDescMN);
         const uint32_t vm = desc(smem_u32(sm.v[st]), kDescMN);
         wait(&sm.q_full, n & 1);
-        wait(&sm.kv_full[st], (n >> 1) & 1);
+        wait(&sm.k_full[st], (n >> 1) & 1);
         if (dead()) break;
         fence_after_sync();
         // scores (the product with the last chunk's, which holds these columns, was issued before)
@@ -859,7 +951,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
           mma_ss(tmem + kTmS, qd + o, kk + o, idesc_bf16(128, kC), ks > 0);
         }
         mma_commit(&sm.s_done);
-        // queries and the state before the chunk
+        // queries and the state before the chunk (first: the place of its bf16 form is free once the update is done)
         wait(&sm.st_ready, n & 1);
         if (n > 0) wait(&sm.o_empty, (n & 1) ^ 1u);
         if (dead()) break;
@@ -870,6 +962,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
                  sd + ((ks >> 2) * (128 * DV) + (ks & 3) * 32) / 16, idesc_bf16(128, DV), ks > 0);
         mma_commit(&sm.q_empty);
         // the state's update, lanes = its columns
+        wait(&sm.v_ready[st], (n >> 1) & 1);
         wait(&sm.ks_ready, n & 1);
         if (dead()) break;
         fence_after_sync();
@@ -887,6 +980,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         for (int ks = 0; ks < kC / 16; ++ks)
           mma_ts(tmem + kTmO, tmem + kTmS + (ks >> 2) * 64 + (ks & 3) * 8, vm + ks * 128, idesc_bf16_bmn(128, DV), ks > 0);
         mma_commit(&sm.o_done);
+        mma_commit(&sm.k_empty[st]);
       }
     }
     if (lane == 0) {                  // no product outlives the TMEM
@@ -898,9 +992,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     // ------------------------------- scores and outputs: a token to a thread and the one 128 on, half of its columns each
     const int i = tid & 127, quad = warp & 3, half = warp >> 2;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-    while (true) {
-      const Run r = next_run();
-      if (bar_any(2, 256, r.kind == kEnd)) break;         // (together: they meet in barriers)
+    for (Run r = next_run(); r.kind != kEnd; r = next_run()) {
       if (r.kind == kZeros) {
         const int begin = r.c0 * kC, end = min(r.len, r.c1 * kC);
         for (int t = begin + tid; t < end; t += 256)
@@ -947,8 +1039,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         wait_warp(&sm.o_done, n & 1);
         fence_after_sync();
         const float f = ex2f(mine);
-        const bool bad = *(volatile int*)&sm.bad[st] != 0;
-        // through the place of the values, which the chunk's products have read
+        // into the place of the values, which the chunk's products have read; a warp of its own sends them off
         uint8_t* tile = sm.v[st];
 #pragma unroll 1
         for (int b = 0; b < DV / 2; b += 16) {
@@ -972,25 +1063,12 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         }
         fence_before_sync();
         arrive_warp(&sm.o_empty);
-        if (bad && i < rows) mark_reached(a, r.t0 + c * kC + i, i, r.head, half * (DV / 2), DV / 2, tile);
+        if (*(volatile int*)&sm.bad[n & 3] && i < rows)
+          mark_reached(a, r.t0 + c * kC + i, i, r.head, half * (DV / 2), DV / 2, tile);
         fence_proxy_async_smem();
-        bar_any(2, 256, false);
-        if (rows < kC) {
-          store_rows(a, r.t0 + c * kC, rows, r.head, tile, tid);
-          bar_any(2, 256, false);
-        }
-        if (tid == 0) {
-          if (rows == kC && !dead()) {
-            tma_store_3d(&maps.out, 0, r.t0 + c * kC, r.head * (DV / 64), tile);
-            bulk_commit();
-            bulk_wait_read();
-          }
-          mbar_arrive(&sm.kv_empty[st]);
-        }
-        __syncwarp();
+        arrive_warp(&sm.t_ready);
       }
     }
-    if (tid == 0) bulk_wait();
   } else {
     // ------------------------------- keys and state
     using L = StateRows<DK, DV>;
@@ -1020,7 +1098,6 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       if (r.n == 0 && !r.init) {
         for (int e = 0; e < L::kRows; ++e) state[(at.first + e) * DV] = 0.f;
       }
-      bool bad = false;               // the last chunk's values
       for (int c = r.c0; c < r.c1; ++c, ++n) {
         const int st = n & 1;
         if (c > r.c0) {
@@ -1035,7 +1112,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
           float s[N];
           if (c > r.c0) {
             tmem_row<N>(tl + b, s);
-            if (bad) add_bad(r, c - 1, d, s);
+            if (*(volatile int*)&sm.bad[(n - 1) & 3]) add_bad(r, c - 1, d, s);
           } else if (from) {
 #pragma unroll
             for (int e = 0; e < N; ++e) s[e] = __ldcg(from + (d + e) * DV);
@@ -1062,12 +1139,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         fence_before_sync();
         fence_proxy_async_smem();
         arrive_warp(&sm.st_ready);
-        wait_warp(&sm.kv_full[st], (n >> 1) & 1);
-        bad = clean_values<256>(sm.v[st], min(kC, r.len - c * kC), t);
         wait_warp(&sm.s_done, n & 1);
         split_keys<DK, 256>(sm.k[st], sm.lo, sm.w[st], t);
-        bad = bar_any(1, 256, bad);
-        if (t == 0) sm.bad[st] = bad;
         fence_proxy_async_smem();
         arrive_warp(&sm.ks_ready);
       }
@@ -1079,7 +1152,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
           for (int b = 0; b < L::kRows; b += N) {
             float s[N];
             tmem_row<N>(tl + b, s);
-            if (bad) add_bad(r, r.c1 - 1, at.first + b, s);
+            if (*(volatile int*)&sm.bad[(n - 1) & 3]) add_bad(r, r.c1 - 1, at.first + b, s);
 #pragma unroll
             for (int e = 0; e < N; ++e) state[(at.first + b + e) * DV] = s[e];
           }
