@@ -84,6 +84,25 @@ __device__ __forceinline__ void gates(float A_log, float dt_bias, float a, float
   beta = sigmoidf_(b);
 }
 
+// Pairs of f32 in one instruction.
+__device__ __forceinline__ void mul_pair(float& x, float& y, float a, float b) {
+  asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
+  asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nadd.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+// (x, y) = (x, y) * (a, b) + (c, d)
+__device__ __forceinline__ void fma_pair(float& x, float& y, float a, float b, float c, float d) {
+  asm("{\n.reg .b64 p, q, r;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmov.b64 r, {%4, %5};\n"
+      "fma.rn.f32x2 p, p, q, r;\nmov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
 // ------------------------------------------------------------------ launch order
 
 // For a kernel launched as a programmatic dependent of the previous kernel in the stream: waits

@@ -73,43 +73,169 @@ __device__ __forceinline__ float lanes_max(float v) {
   return __uint_as_float(u);
 }
 
+enum Part { kQueries, kKeys, kValues };
+
+template <int D, bool Q8, bool INTER>
+struct Kernel {
+  static constexpr int L = D / 8, kSide = 32 / L;       // lanes of a vector, vectors of a warp at a time
+  static constexpr int kStep = 8 * kSide;               // vectors of the CTA's warps at a time
+  static constexpr int kBatch = 4;                      // of these in flight
+
+  // All vectors of one part of the CTA's tokens.
+  template <int PART>
+  static __device__ __forceinline__ void run(const KvView& c, const RotatedAppend& a, int t0, int count,
+                                             const long long* place, const float* cs, const float* sn) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L;
+    const int heads = PART == kQueries ? a.Hq : c.H, n = count * heads;
+    if (n == 0) return;
+    const __nv_bfloat16* src = PART == kQueries ? a.q : PART == kKeys ? a.k : a.v;
+    const long long ld = PART == kQueries ? a.q_ld : PART == kKeys ? a.k_ld : a.v_ld;
+    const long long head_ld = PART == kQueries ? a.q_head_ld : D;
+    src += (long long)t0 * ld + l * 8;
+    // the lane's pairs: its elements are the first or the second of them (INTER: both)
+    const bool turned = PART != kValues && l * 8 < 2 * a.half;
+    const bool second = !INTER && l * 8 >= a.half;
+    const int away = INTER ? 0 : second ? -a.half : a.half;
+    const int angle = INTER ? l * 4 : second ? l * 8 - a.half : l * 8;
+    const __nv_bfloat16* weight = PART == kQueries ? a.q_norm : PART == kKeys ? a.k_norm : nullptr;
+    float g[8], gy[8];
+    if (PART != kValues) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = gy[j] = 1.f;
+      if (weight) {
+        unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + l), g);
+        if (!INTER && turned) unpack8(__ldg(reinterpret_cast<const uint4*>(weight + away) + l), gy);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          g[j] += a.w0;
+          gy[j] += a.w0;
+        }
+      }
+    }
+    const int first = warp * kSide + lane / L, skip_tok = kStep / heads, skip_head = kStep % heads;
+    int tok = first / heads, head = first % heads;
+    // a step along the vectors, and back from the last head to the next token's first
+    src += tok * ld + head * head_ld;
+    const long long skip = skip_tok * ld + skip_head * head_ld, wrap = ld - heads * head_ld;
+    // (whole warps go round together: the shuffles take every lane)
+#pragma unroll 1
+    for (int v = warp * kSide; v < n; v += kStep * kBatch) {
+      uint4 raw[kBatch], other[kBatch];
+      int at_tok[kBatch], at_head[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        at_tok[i] = tok;
+        at_head[i] = head;
+        raw[i] = other[i] = make_uint4(0, 0, 0, 0);
+        if (tok < count) {
+          raw[i] = __ldg(reinterpret_cast<const uint4*>(src));
+          if (!INTER && turned) other[i] = __ldg(reinterpret_cast<const uint4*>(src + away));
+        }
+        src += skip;
+        tok += skip_tok;
+        head += skip_head;
+        if (head >= heads) {
+          head -= heads;
+          ++tok;
+          src += wrap;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const bool live = at_tok[i] < count;
+        const long long base = live ? place[at_tok[i]] : -1;
+        float x[8];
+        if (PART != kValues || Q8) unpack8(raw[i], x);
+        if constexpr (PART != kValues) {
+          float rs = 1.f;
+          if (weight) {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              float u = x[j], z = x[j + 1];
+              fma_pair(u, z, u, z, s0, s1);
+              s0 = u;
+              s1 = z;
+            }
+            rs = rsqrtf(lanes_sum<L>(s0 + s1) * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              mul_pair(x[j], x[j + 1], g[j], g[j + 1]);
+              mul_pair(x[j], x[j + 1], rs, rs);
+            }
+          }
+          if (turned && live) {
+            const float* cp = cs + at_tok[i] * a.half + angle;
+            const float* sp = sn + at_tok[i] * a.half + angle;
+            if constexpr (INTER) {
+              const float4 co = *reinterpret_cast<const float4*>(cp), si = *reinterpret_cast<const float4*>(sp);
+              const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float u = x[2 * j], z = x[2 * j + 1];
+                x[2 * j] = turned_a(u, z, cc[j], sc[j]);
+                x[2 * j + 1] = turned_b(u, z, cc[j], sc[j]);
+              }
+            } else {
+              float y[8];
+              unpack8(other[i], y);
+              const float by = second ? rs : -rs;      // (the sign of the sine with the norm's factor)
+#pragma unroll
+              for (int j0 = 0; j0 < 8; j0 += 4) {
+                const float4 co = *reinterpret_cast<const float4*>(cp + j0), si = *reinterpret_cast<const float4*>(sp + j0);
+                const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                  float* u = y + j0 + j;
+                  if (weight) mul_pair(u[0], u[1], gy[j0 + j], gy[j0 + j + 1]);
+                  mul_pair(u[0], u[1], by, by);
+                  mul_pair(u[0], u[1], sc[j], sc[j + 1]);
+                  fma_pair(x[j0 + j], x[j0 + j + 1], cc[j], cc[j + 1], u[0], u[1]);
+                }
+              }
+            }
+          }
+        }
+        if constexpr (PART == kQueries) {
+          if (live) {
+            const uint4 o = base < 0 ? make_uint4(0, 0, 0, 0) : pack8(x);
+            reinterpret_cast<uint4*>(a.q_out)[((long long)t0 * a.Hq + v + i * kStep + lane / L) * L + l] = o;
+          }
+        } else {
+          const long long at = base + ((long long)at_head[i] << c.page_shift);
+          if constexpr (Q8) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+            const int b = scale_byte_f32(lanes_max<L>(__uint_as_float(top)));
+            if (base >= 0) {
+              reinterpret_cast<uint2*>(static_cast<uint8_t*>(PART == kValues ? c.v : c.k) + at * D)[l] = codes8(x, b);
+              if (l == 0) (PART == kValues ? c.vs : c.ks)[at] = (uint8_t)b;
+            }
+          } else if (base >= 0) {
+            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(PART == kValues ? c.v : c.k) + at * D)[l] =
+                PART == kValues ? raw[i] : pack8(x);
+          }
+        }
+      }
+    }
+  }
+};
+
 template <int D, bool Q8, bool INTER>
 __global__ void __launch_bounds__(256) append_rotated_kernel(const KvView c, const KvBatchView bt, int tokens,
                                                              const RotatedAppend a) {
-  constexpr int L = D / 8, kSide = 32 / L;       // lanes of a vector, vectors of a warp at a time
   __shared__ long long place[kMostTokens];
   __shared__ int angle_at[kMostTokens];
   __shared__ __align__(16) float cs[kMostTurns], sn[kMostTurns];
   const int t0 = blockIdx.x * tokens, count = min(tokens, bt.total - t0);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L;
-  const int heads = a.Hq + 2 * c.H, vectors = count * heads;
+  const int tid = threadIdx.x;
   pdl_begin();
-  struct Item {
-    uint4 x, y;          // the lane's elements, and in the half layout their partners
-    int tok, head;
-  };
-  const bool turned = l * 8 < 2 * a.half;
-  const int away = INTER ? 0 : (l * 8 < a.half ? a.half : -a.half);
-  auto load = [&](int v, Item& it) {
-    it.x = it.y = make_uint4(0, 0, 0, 0);
-    it.tok = v / heads;
-    it.head = v - it.tok * heads;
-    if (v >= vectors) return;
-    const long long row = t0 + it.tok;
-    const __nv_bfloat16* p = it.head < a.Hq ? a.q + row * a.q_ld + it.head * a.q_head_ld
-                             : it.head < a.Hq + c.H ? a.k + row * a.k_ld + (it.head - a.Hq) * D
-                                                    : a.v + row * a.v_ld + (it.head - a.Hq - c.H) * D;
-    it.x = __ldg(reinterpret_cast<const uint4*>(p) + l);
-    if (!INTER && turned && it.head < a.Hq + c.H) it.y = __ldg(reinterpret_cast<const uint4*>(p + away) + l);
-  };
-  const int first = warp * kSide + lane / L, step = 8 * kSide;
-  Item it;
-  load(first, it);
-  if (warp == 0) {
-    const Place p = find_place(c, bt, min(t0 + lane, bt.total - 1));
-    if (lane < count) {
-      place[lane] = p.page < 0 ? -1 : (((long long)p.page * c.H) << c.page_shift) + p.off;
-      angle_at[lane] = a.positions ? __ldg(a.positions + t0 + lane) : p.pos;
+  if (tid < 32) {
+    const Place p = find_place(c, bt, min(t0 + tid, bt.total - 1));
+    if (tid < count) {
+      place[tid] = p.page < 0 ? -1 : (((long long)p.page * c.H) << c.page_shift) + p.off;
+      angle_at[tid] = a.positions ? __ldg(a.positions + t0 + tid) : p.pos;
     }
   }
   __syncthreads();
@@ -119,97 +245,20 @@ __global__ void __launch_bounds__(256) append_rotated_kernel(const KvView c, con
     cs[i] = r.x;
     sn[i] = r.y;
   }
+  Kernel<D, Q8, INTER>::template run<kValues>(c, a, t0, count, place, cs, sn);
   __syncthreads();
-  // (whole warps go round together: the shuffles take every lane)
-  for (int v = first; v - lane / L < vectors; v += step) {
-    Item next;
-    load(v + step, next);
-    const bool live = v < vectors;
-    const long long base = live ? place[it.tok] : -1;
-    const bool is_q = it.head < a.Hq, is_v = it.head >= a.Hq + c.H;
-    float x[8];
-    unpack8(it.x, x);
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    ss = lanes_sum<L>(ss);                        // (every lane, whatever its vector)
-    if (!is_v) {
-      const __nv_bfloat16* w = is_q ? a.q_norm : a.k_norm;
-      float y[8];
-      if constexpr (!INTER) unpack8(it.y, y);
-      if (w) {
-        const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
-        float g[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + l), g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= rs * (a.w0 + g[j]);
-        if (!INTER && turned) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(w + away) + l), g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] *= rs * (a.w0 + g[j]);
-        }
-      }
-      if (turned && live) {
-        if constexpr (INTER) {
-          const float4 co = *reinterpret_cast<const float4*>(cs + it.tok * a.half + l * 4);
-          const float4 si = *reinterpret_cast<const float4*>(sn + it.tok * a.half + l * 4);
-          const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = x[2 * j], z = x[2 * j + 1];
-            x[2 * j] = turned_a(u, z, cc[j], sc[j]);
-            x[2 * j + 1] = turned_b(u, z, cc[j], sc[j]);
-          }
-        } else {
-          const int at = it.tok * a.half + (away > 0 ? l * 8 : l * 8 - a.half);
-          const float sign = away > 0 ? -1.f : 1.f;
-#pragma unroll
-          for (int j0 = 0; j0 < 8; j0 += 4) {
-            const float4 co = *reinterpret_cast<const float4*>(cs + at + j0);
-            const float4 si = *reinterpret_cast<const float4*>(sn + at + j0);
-            const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j0 + j] = fmaf(x[j0 + j], cc[j], sign * __fmul_rn(y[j0 + j], sc[j]));
-          }
-        }
-      }
-    }
-    if (is_q) {
-      if (live) {
-        const uint4 o = base < 0 ? make_uint4(0, 0, 0, 0) : pack8(x);
-        reinterpret_cast<uint4*>(a.q_out + ((long long)(t0 + it.tok) * a.Hq + it.head) * D)[l] = o;
-      }
-    }
-    if constexpr (Q8) {
-      float top = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(x[j]) & 0x7fffffffu));
-      top = lanes_max<L>(top);
-      if (!is_q && base >= 0) {
-        const int h = it.head - a.Hq - (is_v ? c.H : 0), b = scale_byte_f32(top);
-        const long long at = base + ((long long)h << c.page_shift);
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at * D)[l] = codes8(x, b);
-        if (l == 0) (is_v ? c.vs : c.ks)[at] = (uint8_t)b;
-      }
-    } else if (!is_q && base >= 0) {
-      const int h = it.head - a.Hq - (is_v ? c.H : 0);
-      const long long at = base + ((long long)h << c.page_shift);
-      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? c.v : c.k) + at * D)[l] = is_v ? it.x : pack8(x);
-    }
-    it = next;
-  }
+  Kernel<D, Q8, INTER>::template run<kKeys>(c, a, t0, count, place, cs, sn);
+  Kernel<D, Q8, INTER>::template run<kQueries>(c, a, t0, count, place, cs, sn);
 }
 
 }  // namespace
 
 int launch_kv_append_rotated(const KvView& c, const KvBatchView& bt, const RotatedAppend& a, cudaStream_t stream) {
-  // tokens of a CTA: two rounds of its warps, more (up to eight times that) where that leaves the SMs
-  // their fill of CTAs
+  // tokens of a CTA: a round of its warps, more where that leaves the SMs some waves of CTAs
   const long long lanes = (long long)(a.Hq + 2 * c.H) * (c.D / 8);
   const int most = kMostTurns / a.half < kMostTokens ? kMostTurns / a.half : kMostTokens;
-  long long t = (512 + lanes - 1) / lanes;
-  const long long top = t * 8;
-  while (2 * t <= top && bt.total > 2048 * t) t *= 2;
+  long long t = (256 + lanes - 1) / lanes;
+  while (bt.total > 2048 * t) t *= 2;
   const int tokens = t < most ? (int)t : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((bt.total + tokens - 1) / tokens));
