@@ -6,6 +6,7 @@
 // A dozen flops per element: the floor is the bytes, x, z and r read once, h and y written once.  A row stays
 // in registers from the first load to the last store, between the two sums that it waits for.
 #include "gdn_internal.h"
+#include "gdn_tc.cuh"
 
 namespace gdn {
 
@@ -246,6 +247,189 @@ __global__ void __launch_bounds__(MOST) block_kernel(const BlockArgs a) {
   }
 }
 
+// The same for many rows: CTAs that stay, with the next row's x, gate and residual on their way into shared memory
+// by bulk copies while a row is worked on.  (A CTA to a row has nothing in flight while it starts, waits for its
+// sums and stores: 8192 rows of 4096 with a gate 46 us, so 36.)  Two vectors a thread (NV)
+// leave room for the weights in registers; with four they come from L1.
+template <typename T, int NV, bool GROUPED, int MOST>
+__global__ void __launch_bounds__(MOST) block_rows_kernel(const BlockArgs a, int stages) {
+  using R = Raw<T, 8>;
+  constexpr int kMostStages = 4;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float part[4][32];
+  __shared__ __align__(8) uint64_t full[kMostStages];
+  const gdn_block_args& p = a.p;
+  const int threads = blockDim.x, t = threadIdx.x, n = a.n;
+  const uint32_t plane = (uint32_t)n * sizeof(T), planes = 1 + (p.gate != nullptr) + (p.residual != nullptr);
+  const uint32_t gate_at = plane, residual_at = p.gate ? 2 * plane : plane;
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) tc::mbar_init(&full[i], 1);
+    tc::mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_begin();
+  constexpr bool kHold = NV <= 2;
+  R post[NV], channel[NV], pre[NV];
+#pragma unroll
+  for (int j = 0; j < NV && kHold; ++j) {
+    const int c = (j * threads + t) * 8;
+    if (c >= n) continue;
+    if (p.post) post[j].load(static_cast<const T*>(p.post) + (GROUPED ? c & (p.group - 1) : c));
+    if (p.channel_scale) channel[j].load(static_cast<const T*>(p.channel_scale) + c);
+    if (p.pre) pre[j].load(static_cast<const T*>(p.pre) + c);
+  }
+  auto fetch = [&](long long row, int st) {            // one thread
+    if (row >= a.rows) return;
+    uint8_t* to = ring + (size_t)st * planes * plane;
+    tc::mbar_arrive_expect_tx(&full[st], planes * plane);
+    tc::bulk_g2s(to, static_cast<const T*>(p.x) + row * p.x_ld, plane, &full[st]);
+    if (p.gate) tc::bulk_g2s(to + gate_at, static_cast<const T*>(p.gate) + row * p.gate_ld, plane, &full[st]);
+    if (p.residual) tc::bulk_g2s(to + residual_at, static_cast<const T*>(p.residual) + row * p.residual_ld, plane, &full[st]);
+  };
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) fetch(blockIdx.x + (long long)i * gridDim.x, i);
+  int st = 0, turn = 0;
+  uint32_t phase = 0;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const uint8_t* in = ring + (size_t)st * planes * plane;
+    tc::mbar_wait(&full[st], phase);
+    float h[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * threads + t) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[j][e] = 0.f;
+      if (c < n) {
+        R x;
+        x.load(reinterpret_cast<const T*>(in) + c);
+        x.get(h[j]);
+      }
+    }
+    if (p.post) {
+      float rs = 0.f;
+      if constexpr (!GROUPED) {
+        float ss = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) add_squares<8>(h[j], ss, s2);
+        rs = rsqrtf(row_sum<true>(ss + s2, part[turn]) * a.inv_n + p.eps);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * threads + t) * 8;
+        if constexpr (GROUPED) {
+          float ss = 0.f, s2 = 0.f;
+          add_squares<8>(h[j], ss, s2);
+          ss += s2;
+          for (int o = p.group / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          rs = rsqrtf(ss * a.inv_g + p.eps);
+        }
+        if (c < n) {
+          float g[8];
+          if (!kHold) post[j].load(static_cast<const T*>(p.post) + (GROUPED ? c & (p.group - 1) : c));
+          post[j].get(g);
+          weigh<8>(h[j], g, rs, p.weight_offset);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * threads + t) * 8;
+      if (c >= n) continue;
+      R w;
+      float g[8];
+      if (p.gate) {
+        w.load(reinterpret_cast<const T*>(in + gate_at) + c);
+        w.get(g);
+        float s[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = sizeof(T) == 4 ? sigmoidf_(g[e]) : sigmoid_fast(g[e]);
+        if (p.gate_act == GDN_GATE_SILU) mul_by<8>(s, g);
+        mul_by<8>(h[j], s);
+      }
+      if (p.channel_scale) {
+        if (!kHold) channel[j].load(static_cast<const T*>(p.channel_scale) + c);
+        channel[j].get(g);
+        mul_by<8>(h[j], g);
+      }
+      if (p.residual) {
+        w.load(reinterpret_cast<const T*>(in + residual_at) + c);
+        w.get(g);
+        fma_by<8>(h[j], p.scale, g);
+      } else {
+        mul_by<8>(h[j], p.scale);
+      }
+      if (p.total) R::put(static_cast<T*>(p.total) + row * n + c, h[j]);
+    }
+    float rs = 0.f;
+    if (p.pre) {
+      float ss = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) add_squares<8>(h[j], ss, s2);
+      rs = rsqrtf(row_sum<true>(ss + s2, part[2 + turn]) * a.inv_n + p.eps);
+    } else {
+      __syncthreads();
+    }
+    // (every thread has read the row)
+    if (t == 0) fetch(row + (long long)stages * gridDim.x, st);
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1u;
+    }
+    if (p.pre) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * threads + t) * 8;
+        if (c >= n) continue;
+        float g[8];
+        if (!kHold) pre[j].load(static_cast<const T*>(p.pre) + c);
+        pre[j].get(g);
+        weigh<8>(h[j], g, rs, p.weight_offset);
+        R::put(static_cast<T*>(p.y) + row * n + c, h[j]);
+      }
+    }
+  }
+}
+
+// Launches it where the rows are many and a few fit an SM's shared memory; GDN_ERR_UNSUPPORTED_SHAPE: use the other.
+template <typename T, int NV>
+int launch_rows(const BlockArgs& a, int ctas, int sms, size_t stage, cudaStream_t stream) {
+  constexpr int kRing = 208 * 1024;
+  const int threads = (a.n / 8 + NV * 32 - 1) / (NV * 32) * 32;
+  if (ctas > 1024 / threads) ctas = 1024 / threads;
+  if (a.rows < 4 * ctas * sms) return GDN_ERR_UNSUPPORTED_SHAPE;
+  int stages = (int)(kRing / (ctas * stage));
+  if (stages > 4) stages = 4;
+  const bool grouped = a.p.post && a.p.group < a.n;
+  auto kern = grouped ? block_rows_kernel<T, NV, true, 512> : block_rows_kernel<T, NV, false, 512>;
+  static OncePerDevice once[2];
+  const int rc = raise_smem(once[grouped], kern, kRing);
+  if (rc != GDN_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas * sms));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = stages * stage;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, stages) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// Two rows' ring for each of as many CTAs as fit an SM.  Four vectors a thread (of bf16) where that makes CTAs small
+// and they are four or more: many rows at once hide a row's sums (8192 x 4096 with a gate 36 us, with two
+// vectors 40); else two, so that a row is done sooner (8192 x 5120 with everything 74 us, with four 84).
+template <typename T>
+int launch_ring(const BlockArgs& a, cudaStream_t stream) {
+  const int sms = sm_count(), planes = 1 + (a.p.gate != nullptr) + (a.p.residual != nullptr);
+  const size_t stage = (size_t)planes * a.n * sizeof(T);
+  const int ctas = (int)(208 * 1024 / (2 * stage));
+  if (sms <= 0 || ctas < 2) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (sizeof(T) == 2 && ctas >= 4) return launch_rows<T, 4>(a, ctas, sms, stage, stream);
+  return launch_rows<T, 2>(a, ctas, sms, stage, stream);
+}
+
 template <typename T, int VEC, int NV, bool SHARED, int MOST>
 int launch_one(const BlockArgs& a, cudaStream_t stream) {
   const int vectors = (a.n + VEC - 1) / VEC;
@@ -276,6 +460,10 @@ int launch_wide(const BlockArgs& a, cudaStream_t s) {
   constexpr int NV = sizeof(T) == 4 ? 2 : 4;
   const int nv = a.n / 8;
   if (nv <= 32) return launch_one<T, 8, 1, false, 128>(a, s);
+  if (nv <= 1024) {
+    const int rc = launch_ring<T>(a, s);
+    if (rc != GDN_ERR_UNSUPPORTED_SHAPE) return rc;
+  }
   if (nv <= NV * 256) return launch_one<T, 8, NV, true, 256>(a, s);
   if (nv <= NV * 512) return launch_one<T, 8, NV, true, 512>(a, s);
   return launch_one<T, 8, 4, true, 1024>(a, s);

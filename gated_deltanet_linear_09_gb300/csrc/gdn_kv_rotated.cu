@@ -117,20 +117,18 @@ struct Kernel {
     // a step along the vectors, and back from the last head to the next token's first
     src += tok * ld + head * head_ld;
     const long long skip = skip_tok * ld + skip_head * head_ld, wrap = ld - heads * head_ld;
-    // (whole warps go round together: the shuffles take every lane)
-#pragma unroll 1
-    for (int v = warp * kSide; v < n; v += kStep * kBatch) {
-      uint4 raw[kBatch], other[kBatch];
-      int at_tok[kBatch], at_head[kBatch];
+    struct Batch {
+      uint4 raw[kBatch];
+      const __nv_bfloat16* from[kBatch];
+      int tok[kBatch], head[kBatch];
+    };
+    auto load = [&](Batch& b) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        at_tok[i] = tok;
-        at_head[i] = head;
-        raw[i] = other[i] = make_uint4(0, 0, 0, 0);
-        if (tok < count) {
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(src));
-          if (!INTER && turned) other[i] = __ldg(reinterpret_cast<const uint4*>(src + away));
-        }
+        b.tok[i] = tok;
+        b.head[i] = head;
+        b.from[i] = src;
+        b.raw[i] = tok < count ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
         src += skip;
         tok += skip_tok;
         head += skip_head;
@@ -140,12 +138,25 @@ struct Kernel {
           src += wrap;
         }
       }
+    };
+    Batch now, next;
+    load(now);
+    // (whole warps go round together: the shuffles take every lane)
+#pragma unroll 1
+    for (int v = warp * kSide; v < n; v += kStep * kBatch) {
+      load(next);                       // (nothing past the last token)
+      uint4 other[kBatch];              // the partners: the lines are in L1
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const bool live = at_tok[i] < count;
-        const long long base = live ? place[at_tok[i]] : -1;
+        other[i] = make_uint4(0, 0, 0, 0);
+        if (!INTER && turned && now.tok[i] < count) other[i] = __ldg(reinterpret_cast<const uint4*>(now.from[i] + away));
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const bool live = now.tok[i] < count;
+        const long long base = live ? place[now.tok[i]] : -1;
         float x[8];
-        if (PART != kValues || Q8) unpack8(raw[i], x);
+        if (PART != kValues || Q8) unpack8(now.raw[i], x);
         if constexpr (PART != kValues) {
           float rs = 1.f;
           if (weight) {
@@ -165,8 +176,8 @@ struct Kernel {
             }
           }
           if (turned && live) {
-            const float* cp = cs + at_tok[i] * a.half + angle;
-            const float* sp = sn + at_tok[i] * a.half + angle;
+            const float* cp = cs + now.tok[i] * a.half + angle;
+            const float* sp = sn + now.tok[i] * a.half + angle;
             if constexpr (INTER) {
               const float4 co = *reinterpret_cast<const float4*>(cp), si = *reinterpret_cast<const float4*>(sp);
               const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
@@ -202,7 +213,7 @@ struct Kernel {
             reinterpret_cast<uint4*>(a.q_out)[((long long)t0 * a.Hq + v + i * kStep + lane / L) * L + l] = o;
           }
         } else {
-          const long long at = base + ((long long)at_head[i] << c.page_shift);
+          const long long at = base + ((long long)now.head[i] << c.page_shift);
           if constexpr (Q8) {
             uint32_t top = 0;
 #pragma unroll
@@ -214,10 +225,11 @@ struct Kernel {
             }
           } else if (base >= 0) {
             reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(PART == kValues ? c.v : c.k) + at * D)[l] =
-                PART == kValues ? raw[i] : pack8(x);
+                PART == kValues ? now.raw[i] : pack8(x);
           }
         }
       }
+      now = next;
     }
   }
 };
@@ -258,7 +270,7 @@ int launch_kv_append_rotated(const KvView& c, const KvBatchView& bt, const Rotat
   const long long lanes = (long long)(a.Hq + 2 * c.H) * (c.D / 8);
   const int most = kMostTurns / a.half < kMostTokens ? kMostTurns / a.half : kMostTokens;
   long long t = (256 + lanes - 1) / lanes;
-  while (bt.total > 2048 * t) t *= 2;
+  while (t < 16 && bt.total > 2048 * t) t *= 2;
   const int tokens = t < most ? (int)t : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((bt.total + tokens - 1) / tokens));
