@@ -2,11 +2,11 @@
 //
 // Between an attention layer's projection and its cache every query and key vector is normed and turned:
 // a chain of element-wise steps, so one pass does them all, and q, k and v are read once.  The floor is
-// the bytes.  A CTA takes neighbouring tokens; a vector is D / 8 neighbouring lanes with 16 bytes each, so
-// the norm's sum is a few shuffles.  In the half layout a lane's partner elements are loaded a second time,
-// as raw bf16 (a hit in L1: the lines are the warp's own), which costs one instruction where exchanging
-// them costs four.  Angles belong to tokens: they are computed once into shared memory, while the vectors'
-// first loads are under way.
+// the bytes.  A CTA takes neighbouring tokens; a vector is a few neighbouring lanes, so the norm's sum is a
+// few shuffles.  In the half layout a lane's partner elements are loaded a second time, as raw bf16 (a
+// hit in L1: the lines are the warp's own), which costs one instruction where exchanging them costs four.
+// Angles belong to tokens: they are computed once into shared memory, while the vectors' first loads are
+// under way.
 #include "gdn_kv.cuh"
 #include "gdn_rotary.cuh"
 
@@ -75,41 +75,86 @@ __device__ __forceinline__ float lanes_max(float v) {
 
 enum Part { kQueries, kKeys, kValues };
 
+// A vector is L = D / 16 neighbouring lanes, each with two pieces of 8 elements: one from either half of the
+// vector, so that a warp's accesses are whole, and what a vector costs beside its elements (its place, its sum)
+// is spread over twice as many.
 template <int D, bool Q8, bool INTER>
 struct Kernel {
-  static constexpr int L = D / 8, kSide = 32 / L;       // lanes of a vector, vectors of a warp at a time
+  static constexpr int L = D / 16, kSide = 32 / L;      // lanes of a vector, vectors of a warp at a time
   static constexpr int kStep = 8 * kSide;               // vectors of the CTA's warps at a time
-  static constexpr int kBatch = 4;                      // of these in flight
+  static constexpr int kBatch = 2;                      // of these in flight, and as many ahead
 
-  // All vectors of one part of the CTA's tokens.
-  template <int PART>
+  // One piece's rotation: x its elements, other its partners' as they are in memory (half layout).
+  // wy their weights (held by no register: another hit in L1), NULL without a norm.
+  static __device__ __forceinline__ void turn(float* x, const uint4& other, const __nv_bfloat16* wy, float w0, float by,
+                                              const float* cp, const float* sp) {
+    if constexpr (INTER) {
+      const float4 co = *reinterpret_cast<const float4*>(cp), si = *reinterpret_cast<const float4*>(sp);
+      const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float u = x[2 * j], z = x[2 * j + 1];
+        x[2 * j] = turned_a(u, z, cc[j], sc[j]);
+        x[2 * j + 1] = turned_b(u, z, cc[j], sc[j]);
+      }
+    } else {
+      float y[8];
+      unpack8(other, y);
+      if (wy) {
+        float g[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(wy)), g);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          add_pair(g[j], g[j + 1], w0, w0);
+          mul_pair(y[j], y[j + 1], g[j], g[j + 1]);
+        }
+      }
+#pragma unroll
+      for (int j0 = 0; j0 < 8; j0 += 4) {
+        const float4 co = *reinterpret_cast<const float4*>(cp + j0), si = *reinterpret_cast<const float4*>(sp + j0);
+        const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          float* u = y + j0 + j;
+          mul_pair(u[0], u[1], by, by);               // (the sine's sign with the norm's factor)
+          mul_pair(u[0], u[1], sc[j], sc[j + 1]);
+          fma_pair(x[j0 + j], x[j0 + j + 1], cc[j], cc[j + 1], u[0], u[1]);
+        }
+      }
+    }
+  }
+
+  // All vectors of one part of the CTA's tokens.  ready(): called by all threads between the first loads and
+  // the first use of places and angles.
+  template <int PART, typename F>
   static __device__ __forceinline__ void run(const KvView& c, const RotatedAppend& a, int t0, int count,
-                                             const long long* place, const float* cs, const float* sn) {
+                                             const long long* place, const float* cs, const float* sn, F ready) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L;
     const int heads = PART == kQueries ? a.Hq : c.H, n = count * heads;
-    if (n == 0) return;
+    if (n == 0) {
+      ready();
+      return;
+    }
     const __nv_bfloat16* src = PART == kQueries ? a.q : PART == kKeys ? a.k : a.v;
     const long long ld = PART == kQueries ? a.q_ld : PART == kKeys ? a.k_ld : a.v_ld;
     const long long head_ld = PART == kQueries ? a.q_head_ld : D;
     src += (long long)t0 * ld + l * 8;
-    // the lane's pairs: its elements are the first or the second of them (INTER: both)
-    const bool turned = PART != kValues && l * 8 < 2 * a.half;
-    const bool second = !INTER && l * 8 >= a.half;
-    const int away = INTER ? 0 : second ? -a.half : a.half;
-    const int angle = INTER ? l * 4 : second ? l * 8 - a.half : l * 8;
     const __nv_bfloat16* weight = PART == kQueries ? a.q_norm : PART == kKeys ? a.k_norm : nullptr;
-    float g[8], gy[8];
-    if (PART != kValues) {
+    // of either piece: whether it is turned, where its partners are and which angles are its
+    bool turned[2], second[2];
+    int away[2], angle[2];
+    float g[2][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = gy[j] = 1.f;
-      if (weight) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + l), g);
-        if (!INTER && turned) unpack8(__ldg(reinterpret_cast<const uint4*>(weight + away) + l), gy);
+    for (int h = 0; h < 2; ++h) {
+      const int at = h * (D / 2) + l * 8;
+      turned[h] = PART != kValues && at < 2 * a.half;
+      second[h] = !INTER && at >= a.half;
+      away[h] = INTER ? 0 : second[h] ? -a.half : a.half;
+      angle[h] = INTER ? at / 2 : second[h] ? at - a.half : at;
+      if (PART != kValues && weight) {
+        unpack8(__ldg(reinterpret_cast<const uint4*>(weight + at)), g[h]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          g[j] += a.w0;
-          gy[j] += a.w0;
-        }
+        for (int j = 0; j < 8; ++j) g[h][j] += a.w0;
       }
     }
     const int first = warp * kSide + lane / L, skip_tok = kStep / heads, skip_head = kStep % heads;
@@ -118,7 +163,7 @@ struct Kernel {
     src += tok * ld + head * head_ld;
     const long long skip = skip_tok * ld + skip_head * head_ld, wrap = ld - heads * head_ld;
     struct Batch {
-      uint4 raw[kBatch];
+      uint4 raw[kBatch][2];
       const __nv_bfloat16* from[kBatch];
       int tok[kBatch], head[kBatch];
     };
@@ -128,7 +173,9 @@ struct Kernel {
         b.tok[i] = tok;
         b.head[i] = head;
         b.from[i] = src;
-        b.raw[i] = tok < count ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          b.raw[i][h] = tok < count ? __ldg(reinterpret_cast<const uint4*>(src + h * (D / 2))) : make_uint4(0, 0, 0, 0);
         src += skip;
         tok += skip_tok;
         head += skip_head;
@@ -141,91 +188,77 @@ struct Kernel {
     };
     Batch now, next;
     load(now);
+    ready();
     // (whole warps go round together: the shuffles take every lane)
 #pragma unroll 1
     for (int v = warp * kSide; v < n; v += kStep * kBatch) {
       load(next);                       // (nothing past the last token)
-      uint4 other[kBatch];              // the partners: the lines are in L1
+      uint4 other[kBatch][2];           // the partners: the lines are in L1
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        other[i] = make_uint4(0, 0, 0, 0);
-        if (!INTER && turned && now.tok[i] < count) other[i] = __ldg(reinterpret_cast<const uint4*>(now.from[i] + away));
-      }
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          other[i][h] = make_uint4(0, 0, 0, 0);
+          if (!INTER && turned[h] && now.tok[i] < count)
+            other[i][h] = __ldg(reinterpret_cast<const uint4*>(now.from[i] + h * (D / 2) + away[h]));
+        }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const bool live = now.tok[i] < count;
         const long long base = live ? place[now.tok[i]] : -1;
-        float x[8];
-        if (PART != kValues || Q8) unpack8(now.raw[i], x);
+        float x[2][8];
+        if (PART != kValues || Q8) {
+          unpack8(now.raw[i][0], x[0]);
+          unpack8(now.raw[i][1], x[1]);
+        }
         if constexpr (PART != kValues) {
           float rs = 1.f;
           if (weight) {
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              float u = x[j], z = x[j + 1];
+            for (int j = 0; j < 16; j += 2) {
+              float u = x[j >> 3][j & 7], z = x[j >> 3][(j & 7) + 1];
               fma_pair(u, z, u, z, s0, s1);
               s0 = u;
               s1 = z;
             }
             rs = rsqrtf(lanes_sum<L>(s0 + s1) * (1.0f / D) + a.eps);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              mul_pair(x[j], x[j + 1], g[j], g[j + 1]);
-              mul_pair(x[j], x[j + 1], rs, rs);
+            for (int j = 0; j < 16; j += 2) {
+              float* u = &x[j >> 3][j & 7];
+              mul_pair(u[0], u[1], g[j >> 3][j & 7], g[j >> 3][(j & 7) + 1]);
+              mul_pair(u[0], u[1], rs, rs);
             }
           }
-          if (turned && live) {
-            const float* cp = cs + now.tok[i] * a.half + angle;
-            const float* sp = sn + now.tok[i] * a.half + angle;
-            if constexpr (INTER) {
-              const float4 co = *reinterpret_cast<const float4*>(cp), si = *reinterpret_cast<const float4*>(sp);
-              const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float u = x[2 * j], z = x[2 * j + 1];
-                x[2 * j] = turned_a(u, z, cc[j], sc[j]);
-                x[2 * j + 1] = turned_b(u, z, cc[j], sc[j]);
-              }
-            } else {
-              float y[8];
-              unpack8(other[i], y);
-              const float by = second ? rs : -rs;      // (the sign of the sine with the norm's factor)
-#pragma unroll
-              for (int j0 = 0; j0 < 8; j0 += 4) {
-                const float4 co = *reinterpret_cast<const float4*>(cp + j0), si = *reinterpret_cast<const float4*>(sp + j0);
-                const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                  float* u = y + j0 + j;
-                  if (weight) mul_pair(u[0], u[1], gy[j0 + j], gy[j0 + j + 1]);
-                  mul_pair(u[0], u[1], by, by);
-                  mul_pair(u[0], u[1], sc[j], sc[j + 1]);
-                  fma_pair(x[j0 + j], x[j0 + j + 1], cc[j], cc[j + 1], u[0], u[1]);
-                }
-              }
-            }
-          }
+          for (int h = 0; h < 2; ++h)
+            if (turned[h] && live)
+              turn(x[h], other[i][h], weight ? weight + h * (D / 2) + l * 8 + away[h] : nullptr, a.w0, second[h] ? rs : -rs,
+                   cs + now.tok[i] * a.half + angle[h], sn + now.tok[i] * a.half + angle[h]);
         }
         if constexpr (PART == kQueries) {
           if (live) {
-            const uint4 o = base < 0 ? make_uint4(0, 0, 0, 0) : pack8(x);
-            reinterpret_cast<uint4*>(a.q_out)[((long long)t0 * a.Hq + v + i * kStep + lane / L) * L + l] = o;
+            uint4* out = reinterpret_cast<uint4*>(a.q_out) + ((long long)t0 * a.Hq + v + i * kStep + lane / L) * (2 * L) + l;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) out[h * L] = base < 0 ? make_uint4(0, 0, 0, 0) : pack8(x[h]);
           }
         } else {
           const long long at = base + ((long long)now.head[i] << c.page_shift);
           if constexpr (Q8) {
             uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+            for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j >> 3][j & 7]) & 0x7fffffffu);
             const int b = scale_byte_f32(lanes_max<L>(__uint_as_float(top)));
             if (base >= 0) {
-              reinterpret_cast<uint2*>(static_cast<uint8_t*>(PART == kValues ? c.v : c.k) + at * D)[l] = codes8(x, b);
+              uint2* out = reinterpret_cast<uint2*>(static_cast<uint8_t*>(PART == kValues ? c.v : c.k) + at * D) + l;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) out[h * L] = codes8(x[h], b);
               if (l == 0) (PART == kValues ? c.vs : c.ks)[at] = (uint8_t)b;
             }
           } else if (base >= 0) {
-            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(PART == kValues ? c.v : c.k) + at * D)[l] =
-                PART == kValues ? now.raw[i] : pack8(x);
+            uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(PART == kValues ? c.v : c.k) + at * D) + l;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) out[h * L] = PART == kValues ? now.raw[i][h] : pack8(x[h]);
           }
         }
       }
@@ -235,7 +268,7 @@ struct Kernel {
 };
 
 template <int D, bool Q8, bool INTER>
-__global__ void __launch_bounds__(256) append_rotated_kernel(const KvView c, const KvBatchView bt, int tokens,
+__global__ void __launch_bounds__(256, 2) append_rotated_kernel(const KvView c, const KvBatchView bt, int tokens,
                                                              const RotatedAppend a) {
   __shared__ long long place[kMostTokens];
   __shared__ int angle_at[kMostTokens];
@@ -250,24 +283,25 @@ __global__ void __launch_bounds__(256) append_rotated_kernel(const KvView c, con
       angle_at[tid] = a.positions ? __ldg(a.positions + t0 + tid) : p.pos;
     }
   }
-  __syncthreads();
-  for (int i = tid; i < count * a.half; i += 256) {
-    const int t = i / a.half;
-    const float2 r = rotary_turn(__ldg(a.turns + i - t * a.half), angle_at[t], a.scale);
-    cs[i] = r.x;
-    sn[i] = r.y;
-  }
-  Kernel<D, Q8, INTER>::template run<kValues>(c, a, t0, count, place, cs, sn);
-  __syncthreads();
-  Kernel<D, Q8, INTER>::template run<kKeys>(c, a, t0, count, place, cs, sn);
-  Kernel<D, Q8, INTER>::template run<kQueries>(c, a, t0, count, place, cs, sn);
+  using K = Kernel<D, Q8, INTER>;
+  K::template run<kValues>(c, a, t0, count, place, cs, sn, [&]() {
+    __syncthreads();
+    for (int i = tid; i < count * a.half; i += 256) {
+      const int t = i / a.half;
+      const float2 r = rotary_turn(__ldg(a.turns + i - t * a.half), angle_at[t], a.scale);
+      cs[i] = r.x;
+      sn[i] = r.y;
+    }
+  });
+  K::template run<kKeys>(c, a, t0, count, place, cs, sn, []() { __syncthreads(); });
+  K::template run<kQueries>(c, a, t0, count, place, cs, sn, []() {});
 }
 
 }  // namespace
 
 int launch_kv_append_rotated(const KvView& c, const KvBatchView& bt, const RotatedAppend& a, cudaStream_t stream) {
   // tokens of a CTA: a round of its warps, more where that leaves the SMs some waves of CTAs
-  const long long lanes = (long long)(a.Hq + 2 * c.H) * (c.D / 8);
+  const long long lanes = (long long)(a.Hq + 2 * c.H) * (c.D / 16);
   const int most = kMostTurns / a.half < kMostTokens ? kMostTurns / a.half : kMostTokens;
   long long t = (256 + lanes - 1) / lanes;
   while (t < 16 && bt.total > 2048 * t) t *= 2;
