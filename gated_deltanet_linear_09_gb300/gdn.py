@@ -565,7 +565,7 @@ def gdn_block_norm(x, total=None, y=None, post=None, gate=None, gate_act=GDN_GAT
         _on_host("gdn_block_norm")
     rows, n = x.shape
     x_ld, gate_ld, residual_ld = (0 if t is None else t.stride(0) if rows > 1 else n for t in (x, gate, residual))
-    a = gdn_block_args(_ptr(x), _ptr(gate), _ptr(residual), _ptr(post), _ptr(pre), _ptr(channel_scale), x_ld, gate_ld,
+    a = gdn_block_args(x.data_ptr(), _ptr(gate), _ptr(residual), _ptr(post), _ptr(pre), _ptr(channel_scale), x_ld, gate_ld,
                        residual_ld, _ptr(total), _ptr(y), scale, weight_offset, eps, group or n, gate_act)
     rc = load().gdn_block_norm(ctypes.byref(a), rows, n, act_code(x.dtype), _stream(stream))
     if rc:
@@ -578,13 +578,11 @@ def make_decay_layer(state, num_k_heads: int, scale: float = 0.0, status=None) -
     return gdn_decay_layer(_ptr(state), n, int(num_k_heads), hv, dk, dv, float(scale), _ptr(status))
 
 
-def make_decay_tokens(q, k, v, log_decay, out) -> gdn_decay_tokens:
-    """q, k, v: bf16 [tokens][heads][dim], adjacent heads, strided tokens; log_decay f32 [heads] or
-    [tokens][heads]; out dense."""
-    def ld(t):                        # the stride of a dimension of size one says nothing
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    g_ld = 0 if log_decay.dim() == 1 else log_decay.stride(0) if log_decay.shape[0] > 1 else log_decay.shape[1]
-    return gdn_decay_tokens(_ptr(q), _ptr(k), _ptr(v), ld(q), ld(k), ld(v), _ptr(log_decay), g_ld, _ptr(out))
+def make_decay_tokens(q, k, v, log_decay, out, q_ld: int, k_ld: int, v_ld: int, decay_ld: int) -> gdn_decay_tokens:
+    """q, k, v: bf16 tokens of adjacent heads, q_ld .. elements apart; log_decay f32 [heads] (decay_ld 0) or of
+    each token; out dense."""
+    return gdn_decay_tokens(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_ld, k_ld, v_ld, log_decay.data_ptr(), decay_ld,
+                            out.data_ptr())
 
 
 def gdn_decay_step(layer, tokens, slot_idx, T: int, stream=None):

@@ -280,37 +280,44 @@ class Rotary:
         self.device = self.turns.device
         self.c = gdn.make_rotary(self.turns, self.rot_dim, interleaved, scale)
 
-    def _check(self, t, out, positions, what):
-        if len(t.shape) != 3 or t.shape[0] != positions.shape[0] or t.shape[2] < self.rot_dim or not _dense_rows(t):
+    def _refuse(self, t, out, tokens, what):
+        """Why t, or its output, is not taken."""
+        if len(t.shape) != 3 or t.shape[0] != tokens or t.shape[2] < self.rot_dim or not _dense_rows(t):
             raise ValueError(f"{what}: [tokens][heads][dim >= {self.rot_dim}] with contiguous vectors expected")
         if t.device != self.device:
             raise ValueError(f"{what} is on {t.device}, the rotation on {self.device}")
-        if out is not None and (out.shape != t.shape or out.dtype != t.dtype or not out.is_contiguous() or
-                                out.device != self.device):
-            raise ValueError(f"{what}'s output: contiguous, with its shape and type, on its device")
+        raise ValueError(f"{what}'s output: contiguous, with its shape and type, on its device")
+
+    def _output(self, t, out, tokens, what, stream):
+        """t checked, and its output, a new one or `out`."""
+        shape, device = t.shape, self.device
+        if len(shape) != 3 or shape[0] != tokens or shape[2] < self.rot_dim or t.stride()[2] != 1 or t.device != device:
+            self._refuse(t, out, tokens, what)
+        if out is None:
+            return _empty(shape, t.dtype, device, stream)
+        if out.shape != shape or out.dtype != t.dtype or not out.is_contiguous() or out.device != device:
+            self._refuse(t, out, tokens, what)
+        return out
 
     def apply(self, positions, q=None, k=None, q_out=None, k_out=None, stream=None):
         """(q, k) turned at positions (device int32 [tokens]); q and k bf16 or f32 [tokens][heads][dim], either may
         be None.  Outputs may be the inputs where those are contiguous."""
-        if positions.dim() != 1 or positions.dtype != torch.int32 or not _dense_rows(positions) or \
+        if positions.dtype != torch.int32 or positions.dim() != 1 or not _dense_rows(positions) or \
                 positions.device != self.device:
             raise ValueError("positions: contiguous int32 [tokens] on the rotation's device")
+        tokens = positions.shape[0]
         if q is not None:
-            self._check(q, q_out, positions, "q")
+            if k is not None and (q.dtype != k.dtype or q.shape[-1] != k.shape[-1]):
+                raise ValueError("q and k have one type and head size")
+            q_out = self._output(q, q_out, tokens, "q", stream)
         if k is not None:
-            self._check(k, k_out, positions, "k")
-        if q is not None and k is not None and (q.dtype != k.dtype or q.shape[2] != k.shape[2]):
-            raise ValueError("q and k have one type and head size")
-        if q is not None and q_out is None:
-            q_out = _empty(q.shape, q.dtype, q.device, stream)
-        if k is not None and k_out is None:
-            k_out = _empty(k.shape, k.dtype, k.device, stream)
+            k_out = self._output(k, k_out, tokens, "k", stream)
         if q is not None or k is not None:
             gdn.gdn_rotary_apply(self.c, positions, q, q_out, k, k_out, stream)
         return q_out, k_out
 
 
-_GATES = {"none": gdn.GDN_GATE_NONE, "sigmoid": gdn.GDN_GATE_SIGMOID, "silu": gdn.GDN_GATE_SILU}
+_GATES = {"sigmoid": gdn.GDN_GATE_SIGMOID, "silu": gdn.GDN_GATE_SILU}
 
 
 def block_norm(x, post=None, gate=None, gate_act="sigmoid", scale=1.0, channel_scale=None, residual=None, pre=None,
@@ -322,29 +329,42 @@ def block_norm(x, post=None, gate=None, gate_act="sigmoid", scale=1.0, channel_s
     shape, dtype, device = x.shape, x.dtype, x.device
     if len(shape) != 2 or not _dense_rows(x):
         raise ValueError("block_norm takes rows [rows][n]")
-    rows, n = shape
-    for t, what in ((gate, "gate"), (residual, "residual"), (total, "total"), (y, "y")):
-        if t is not None and (t.shape != shape or t.dtype != dtype or not _dense_rows(t) or t.device != device):
+
+    def rows(t, what):
+        if t.shape != shape or t.dtype != dtype or not _dense_rows(t) or t.device != device:
             raise ValueError(f"{what} must have the shape, type and device of x")
-    for t, what in ((total, "total"), (y, "y")):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-    for t, what in ((post, "post"), (pre, "pre"), (channel_scale, "channel_scale")):
-        if t is not None and (t.dim() != 1 or t.dtype != dtype or not _dense_rows(t) or t.device != device or
-                              (t.shape[0] != n and what != "post")):
+        return t
+
+    def vector(t, what):
+        if t.dim() != 1 or t.dtype != dtype or t.device != device or not _dense_rows(t) or \
+                (what != "post" and t.shape[0] != shape[1]):
             raise ValueError(f"{what}: a vector of x's type and width on its device")
-    act = "none" if gate is None else gate_act
-    if act not in _GATES or (gate is not None and act == "none"):
-        raise ValueError(f"gate_act is sigmoid or silu, not {gate_act!r}")
+        return t
+    act = gdn.GDN_GATE_NONE
+    if gate is not None:
+        rows(gate, "gate")
+        act = _GATES.get(gate_act)
+        if act is None:
+            raise ValueError(f"gate_act is sigmoid or silu, not {gate_act!r}")
+    if residual is not None:
+        rows(residual, "residual")
+    group = shape[1] if post is None else vector(post, "post").shape[0]
+    if channel_scale is not None:
+        vector(channel_scale, "channel_scale")
     if total is None:
         total = _empty(shape, dtype, device, stream)
+    elif not rows(total, "total").is_contiguous():
+        raise ValueError("total must be contiguous")
     if pre is None:
         if y is not None:
             raise ValueError("y is written with pre only")
-    elif y is None:
-        y = _empty(shape, dtype, device, stream)
-    gdn.gdn_block_norm(x, total, y, post, gate, _GATES[act], residual, pre, channel_scale, scale, weight_offset, eps,
-                       n if post is None else post.shape[0], stream)
+    else:
+        vector(pre, "pre")
+        if y is None:
+            y = _empty(shape, dtype, device, stream)
+        elif not rows(y, "y").is_contiguous():
+            raise ValueError("y must be contiguous")
+    gdn.gdn_block_norm(x, total, y, post, gate, act, residual, pre, channel_scale, scale, weight_offset, eps, group, stream)
     return total, y
 
 
@@ -376,39 +396,39 @@ class DecayAttention:
         self.c = gdn.make_decay_layer(state, num_k_heads, scale, self.status)
         self._ws = {}
 
-    def _tokens(self, lead, q, k, v, log_decay, out, stream):
-        """(tokens struct, out) of tensors [*lead][heads][dim], flattened to tokens without a copy."""
-        n = 1
-        for x in lead:
-            n *= x
-        flat = []
-        for t, what, heads, dim in ((q, "q", self.Hk, self.dk), (k, "k", self.Hk, self.dk), (v, "v", self.Hv, self.dv)):
-            if t.shape != (*lead, heads, dim) or t.dtype != torch.bfloat16 or t.device != self.device:
-                raise ValueError(f"{what}: bf16 {[*lead, heads, dim]} on {self.device} expected, not {list(t.shape)}")
-            flat.append(self._rows(t, len(lead), what))
-            if n and (t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != dim)):
-                raise ValueError(f"{what}: adjacent heads expected")
-        if log_decay.dtype != torch.float32 or log_decay.device != self.device or \
-                log_decay.shape not in ((self.Hv,), (*lead, self.Hv)) or not _dense_rows(log_decay):
-            raise ValueError(f"log_decay: f32 [{self.Hv}] or {[*lead, self.Hv]} on {self.device}")
-        if log_decay.dim() > 1:
-            log_decay = self._rows(log_decay, len(lead), "log_decay")
-        shape = (*lead, self.Hv, self.dv)
-        if out is None:
-            out = _empty(shape, torch.bfloat16, self.device, stream)
-        elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != self.device:
-            raise ValueError(f"out: contiguous bf16 {list(shape)} on {self.device}")
-        return gdn.make_decay_tokens(*flat, log_decay, out), out
-
     @staticmethod
-    def _rows(t, lead, what):
-        """The leading dimensions as one, without a copy."""
-        if lead == 1:
-            return t
-        try:
-            return t.view(-1, *t.shape[lead:])
-        except RuntimeError:
-            raise ValueError(f"{what}: its tokens must lie at one distance from each other") from None
+    def _distance(strides, lead, dense, what):
+        """The distance of the tokens that the leading dimensions count (1, or rows and their T tokens); that of a
+        dimension of size one says nothing."""
+        if len(lead) == 1:
+            return strides[0] if lead[0] > 1 else dense
+        rows, T = lead
+        if T == 1:
+            return strides[0] if rows > 1 else dense
+        if rows > 1 and strides[0] != T * strides[1]:
+            raise ValueError(f"{what}: its tokens must lie at one distance from each other")
+        return strides[1]
+
+    def _tokens(self, lead, q, k, v, log_decay, out, stream):
+        """(tokens struct, out) of tensors [*lead][heads][dim], without a copy."""
+        device, distances = self.device, []
+        for t, what, heads, dim in ((q, "q", self.Hk, self.dk), (k, "k", self.Hk, self.dk), (v, "v", self.Hv, self.dv)):
+            if t.shape != (*lead, heads, dim) or t.dtype != torch.bfloat16 or t.device != device:
+                raise ValueError(f"{what}: bf16 {[*lead, heads, dim]} on {device} expected, not {list(t.shape)}")
+            strides = t.stride()
+            if strides[-1] != 1 or (heads > 1 and strides[-2] != dim):
+                raise ValueError(f"{what}: adjacent heads expected")
+            distances.append(self._distance(strides, lead, heads * dim, what))
+        Hv, g = self.Hv, log_decay.shape
+        if log_decay.dtype != torch.float32 or log_decay.device != device or (g != (Hv,) and g != (*lead, Hv)) or \
+                not _dense_rows(log_decay):
+            raise ValueError(f"log_decay: f32 [{Hv}] or {[*lead, Hv]} on {device}")
+        distances.append(self._distance(log_decay.stride(), lead, Hv, "log_decay") if len(g) > 1 else 0)
+        if out is None:
+            out = _empty(v.shape, torch.bfloat16, device, stream)
+        elif out.shape != v.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != device:
+            raise ValueError(f"out: contiguous bf16 {list(v.shape)} on {device}")
+        return gdn.make_decay_tokens(q, k, v, log_decay, out, *distances), out
 
     def _check_slots(self, slot_idx, n):
         if slot_idx.dtype != torch.int32 or slot_idx.shape != (n,) or not _dense_rows(slot_idx) or \
