@@ -47,6 +47,7 @@ struct ChunkArgs {
   float* ws;
   float log2_scale;
   int num_seqs, total, grid;
+  int chained;                        // pieces may cut sequences: sum and chain kernels come first
 };
 
 struct Maps {
@@ -474,16 +475,21 @@ __device__ __noinline__ void store_rows(const ChunkArgs& a, int t, int rows, int
   }
 }
 
-// What the non-finite values of column c among tokens [t, t + rows) add to element d of the state's column:
-// infinities and NaN, told apart as the recurrence does.
+// What the non-finite values of column c among tokens [t, t + rows) (KEYS: and the non-finite keys' elements d) add
+// to element d of the state's column: infinities and NaN, told apart as the recurrence does.
+template <bool KEYS>
 __device__ __noinline__ float non_finite_part(const ChunkArgs& a, long long t, int rows, int head, int c, int d) {
   const int hk = head / (a.l.Hv / a.l.Hk);
   float sum = 0.f, s = 0.f;
   for (int j = rows - 1; j >= 0; --j) {
     const float w = ex2f(sum);
-    if (w == 0.f) break;
-    const float v = __bfloat162float(a.v[(t + j) * a.v_ld + head * a.l.dv + c]);
-    if (!(fabsf(v) < INFINITY)) s += __bfloat162float(a.k[(t + j) * a.k_ld + hk * a.l.dk + d]) * w * v;
+    if (w != 0.f) {
+      const float v = __bfloat162float(a.v[(t + j) * a.v_ld + head * a.l.dv + c]);
+      if (KEYS || !(fabsf(v) < INFINITY)) {
+        const float k = __bfloat162float(a.k[(t + j) * a.k_ld + hk * a.l.dk + d]);
+        if (!(fabsf(v) < INFINITY) || !(fabsf(k) < INFINITY)) s += k * w * v;
+      }
+    }
     sum += decay_log2(a, t + j, head);
   }
   return s;
@@ -544,7 +550,7 @@ struct __align__(1024) SumSmem {
   Run run;
   float decay;
   uint32_t tmem;
-  int dead, bad;
+  int dead;
   uint64_t full[2], ready[2], empty[2], weights[2], done;
 };
 
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
       mbar_init(&sm.weights[i], 1);
     }
     mbar_init(&sm.done, 1);
-    sm.dead = sm.bad = 0;
+    sm.dead = 0;
     mbar_fence_init();
   }
   __syncthreads();
@@ -642,7 +648,6 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
       wait(&sm.full[st], (i >> 1) & 1);
       __syncwarp();
       split_keys<DK, 256>(sm.k[st], sm.lo[st], sm.w[st], tid);
-      if (clean_values<256>(sm.v[st], kC, tid)) sm.bad = 1;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ready[st]);
@@ -677,11 +682,18 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
           if (f != 0.f) s[e] = fmaf(f, x[e], s[e]);
         }
       }
+      bool odd = false;
 #pragma unroll
-      for (int e = 0; e < N; ++e) dst[(d + e) * DV] = s[e];
-      if (sm.bad)
-        for (int e = 0; e < N; ++e)
-          dst[(d + e) * DV] += non_finite_part(a, run.t0 + run.c0 * kC, n * kC, run.head, at.column, d + e);
+      for (int e = 0; e < N; ++e) {
+        dst[(d + e) * DV] = s[e];
+        odd |= !(fabsf(s[e]) < INFINITY);
+      }
+      // (a value that is not finite times a part of a key that is zero: not what it should be)
+      if (odd)
+        for (int e = 0; e < N; ++e) {
+          const float x = non_finite_part<true>(a, run.t0 + run.c0 * kC, n * kC, run.head, at.column, d + e);
+          if (x != 0.f) dst[(d + e) * DV] = x + (begins ? f * __ldcg(src + (d + e) * DV) : 0.f);
+        }
     }
   }
   if (tid == 0) decays[piece] = sm.decay;
@@ -692,48 +704,65 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
 
 // ------------------------------------------------------------------ along the pieces
 
-// S_p <- e^g_p S_(p-1) + S_p over each run's pieces, 1,024 elements a CTA.  Which pieces follow, and their decays,
-// are read first, and the states a few at a time: the chain itself waits for no load.
-__global__ void __launch_bounds__(256) chain_kernel(const ChunkArgs a) {
-  constexpr int kAhead = 4;
-  __shared__ float decay[256];
-  __shared__ int ends;
+// S_p <- e^g_p S_(p-1) + S_p over each run's pieces.  Every CTA reads which pieces begin a chain and how it goes on,
+// takes its share of the chains (4,096 elements of one at a time), and loads the states ahead: the chain
+// itself waits for no load.
+constexpr int kChainThreads = 1024, kMostGrid = 1024;
+
+__global__ void __launch_bounds__(kChainThreads) chain_kernel(const ChunkArgs a) {
+  constexpr int kAhead = 6;
+  __shared__ float decay[kMostGrid];
+  __shared__ int flag[kMostGrid + 1], start[kMostGrid], before[33];
   pdl_begin();
-  const int size = a.l.dk * a.l.dv, tid = threadIdx.x;
+  const int size = a.l.dk * a.l.dv, slices = size / 4096, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* decays = a.ws + 2 * (size_t)a.grid * size;
-  const int* flags = reinterpret_cast<const int*>(decays + a.grid);
-  if (__ldcg(flags + blockIdx.x) != 1) return;
-  float4* p = reinterpret_cast<float4*>(a.ws) + ((size_t)blockIdx.x * size / 4) + blockIdx.y * 256 + tid;
-  float4 s = __ldcg(p);
-  for (int first = blockIdx.x + 1; first < a.grid; first += 256) {
-    // pieces first .. first + 255, as far as they go on
-    if (tid == 0) ends = 256;
-    __syncthreads();
-    const bool on = first + tid < a.grid && __ldcg(flags + first + tid) == 2;
-    if (on) decay[tid] = ex2f(__ldcg(decays + first + tid));
-    else atomicMin(&ends, tid);
-    __syncthreads();
-    const int count = ends;
-    for (int i0 = 0; i0 < count; i0 += kAhead) {
+  const int mine = tid < a.grid ? __ldcg(reinterpret_cast<const int*>(decays + a.grid) + tid) : 0;
+  if (mine == 2) decay[tid] = ex2f(__ldcg(decays + tid));
+  flag[tid] = mine;
+  const uint32_t starts = __ballot_sync(0xffffffffu, mine == 1);
+  if (lane == 0) before[warp] = __popc(starts);
+  if (tid == 0) flag[kMostGrid] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    const int n = before[lane];
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    before[lane] = incl - n;
+    if (lane == 31) before[32] = incl;
+  }
+  __syncthreads();
+  if (mine == 1) start[before[warp] + __popc(starts & ((1u << lane) - 1u))] = tid;
+  __syncthreads();
+  for (int i = blockIdx.x; i < before[32] * slices; i += gridDim.x) {
+    int piece = start[i / slices];
+    float4* p = reinterpret_cast<float4*>(a.ws) + ((size_t)piece * size + (i % slices) * 4096) / 4 + tid;
+    float4 s = __ldcg(p);
+    while (flag[piece + 1] == 2) {
       float4 x[kAhead];
+      int n = 0;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (i0 + i < count) x[i] = __ldcg(p + (size_t)(i + 1) * (size / 4));
+      for (int j = 0; j < kAhead; ++j)
+        if (n == j && flag[piece + 1 + j] == 2) {
+          x[j] = __ldcg(p + (size_t)(j + 1) * (size / 4));
+          ++n;
+        }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (i0 + i >= count) break;
-        const float f = decay[i0 + i];
+      for (int j = 0; j < kAhead; ++j) {
+        if (j >= n) break;
+        const float f = decay[++piece];
         p += size / 4;
         if (f != 0.f) {
-          x[i].x = fmaf(f, s.x, x[i].x); x[i].y = fmaf(f, s.y, x[i].y);
-          x[i].z = fmaf(f, s.z, x[i].z); x[i].w = fmaf(f, s.w, x[i].w);
+          x[j].x = fmaf(f, s.x, x[j].x); x[j].y = fmaf(f, s.y, x[j].y);
+          x[j].z = fmaf(f, s.z, x[j].z); x[j].w = fmaf(f, s.w, x[j].w);
         }
-        s = x[i];
+        s = x[j];
         __stcg(p, s);
       }
     }
-    if (count < 256) return;
-    __syncthreads();
   }
 }
 
@@ -770,7 +799,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   OutSmem<DK, DV>& sm = *reinterpret_cast<OutSmem<DK, DV>*>(smem_raw);
   Scan& scan = *reinterpret_cast<Scan*>(sm.lo);          // (before the roles begin)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, piece = blockIdx.x;
-  pdl_begin();
+  // After a chain kernel (which began when everything before this call was done) only the states depend on the
+  // kernel before this one: all but the warps that use them begin at once.
+  if (!a.chained) pdl_wait_primary();
+  pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.k_full[i], 1);
@@ -802,12 +834,16 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   if (!locate<kOutThreads, false>(a, piece, &line, &scan)) {
     if (tid == 0) set_status(a.l.status, GDN_STATUS_BAD_SEQLENS);
     zero_tokens(a, 0, a.total);
+    pdl_wait_primary();
     return;
   }
   const int seq = scan.seq;
   const long long into = scan.into;
   zero_tokens(a, __ldg(a.cu + a.num_seqs), a.total);
-  if (piece >= line.pieces) return;
+  if (piece >= line.pieces) {
+    pdl_wait_primary();
+    return;
+  }
   if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 512);
   fence_before_sync();
   __syncthreads();
@@ -1071,6 +1107,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     }
   } else {
     // ------------------------------- keys and state
+    pdl_wait_primary();
     using L = StateRows<DK, DV>;
     constexpr int N = L::kBlock;
     const int t = tid - 256;
@@ -1082,7 +1119,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       float more[N];                  // (a copy, so that s stays in registers)
 #pragma unroll 1
       for (int e = 0; e < N; ++e)
-        more[e] = non_finite_part(a, r.t0 + c * kC, min(kC, r.len - c * kC), r.head, at.column, d + e);
+        more[e] = non_finite_part<false>(a, r.t0 + c * kC, min(kC, r.len - c * kC), r.head, at.column, d + e);
 #pragma unroll
       for (int e = 0; e < N; ++e) s[e] += more[e];
     };
@@ -1172,9 +1209,12 @@ int launch_dims(const ChunkArgs& a, const Maps& maps, cudaStream_t stream) {
   int rc;
   if ((rc = raise_smem(once_sum, sum_kernel<DK, DV>, sizeof(SumSmem<DK, DV>))) != GDN_OK) return rc;
   if ((rc = raise_smem(once_out, out_kernel<DK, DV>, sizeof(OutSmem<DK, DV>))) != GDN_OK) return rc;
-  if ((rc = launch(sum_kernel<DK, DV>, dim3((unsigned)a.grid), kSumThreads, sizeof(SumSmem<DK, DV>), stream, a, maps)) != GDN_OK)
-    return rc;
-  if ((rc = launch(chain_kernel, dim3((unsigned)a.grid, DK * DV / 1024), 256, 0, stream, a)) != GDN_OK) return rc;
+  if (a.chained) {
+    rc = launch(sum_kernel<DK, DV>, dim3((unsigned)a.grid), kSumThreads, sizeof(SumSmem<DK, DV>), stream, a, maps);
+    if (rc != GDN_OK) return rc;
+    rc = launch(chain_kernel, dim3((unsigned)a.grid), kChainThreads, 0, stream, a);
+    if (rc != GDN_OK) return rc;
+  }
   return launch(out_kernel<DK, DV>, dim3((unsigned)a.grid), kOutThreads, sizeof(OutSmem<DK, DV>), stream, a, maps);
 }
 
@@ -1206,7 +1246,8 @@ int launch_decay_prefill(const DecayView& l, const gdn_decay_tokens& t, const in
   a.num_seqs = num_seqs;
   a.total = total_tokens;
   a.grid = sm_count();
-  if (a.grid <= 0) return GDN_ERR_CUDA;
+  if (a.grid <= 0 || a.grid >= kMostGrid) return GDN_ERR_CUDA;
+  a.chained = total_tokens > kC;      // (one chunk is not cut)
   Maps maps = {};
   if (total_tokens > 0 && !(make_rows_map(t.q, total_tokens, t.q_ld, l.Hk * l.dk, kC, l.dk / 64, &maps.q) &&
                             make_rows_map(t.k, total_tokens, t.k_ld, l.Hk * l.dk, kC, l.dk / 64, &maps.k) &&
