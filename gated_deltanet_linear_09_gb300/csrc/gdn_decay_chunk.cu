@@ -75,6 +75,12 @@ __device__ __forceinline__ int chunk_at(long long o, int n) {
   return o <= kRunCost ? 0 : c < n ? (int)c : n;
 }
 
+// Where a place of the line lies: in which sequence, how far into it, and the sequence.
+struct Found {
+  long long into;
+  int seq, t0, len, slot, init;
+};
+
 struct Walk {
   const ChunkArgs* a;
   long long x0, x1, r0;    // the piece, and the current run's place on the line
@@ -86,15 +92,18 @@ struct Walk {
     slot = __ldg(a->slots + s);
     init = a->init != nullptr && __ldg(a->init + s) != 0;
   }
-  // `into`: the place x of the line, as an offset into sequence `seq`
-  __device__ __forceinline__ void start(const ChunkArgs& args, const Line& line, long long x, int seq, long long into) {
+  // from the place x of the line
+  __device__ __forceinline__ void start(const ChunkArgs& args, const Line& line, long long x, const Found& at) {
     a = &args;
     x0 = line.x0;
     x1 = line.x1;
-    s = seq;
-    load();
-    h = (int)(into / head_cost(len));
-    r0 = x - (into - h * head_cost(len));
+    s = at.seq;
+    t0 = at.t0;
+    len = at.len;
+    slot = at.slot;
+    init = at.init;
+    h = (int)(at.into / head_cost(len));
+    r0 = x - (at.into - h * head_cost(len));
   }
   // The piece's share of the current run.
   __device__ __forceinline__ Run here() const {
@@ -121,15 +130,52 @@ struct Walk {
 
 struct Scan {
   long long warp_sum[32];
-  long long into;
-  int seq;
+  Line line;
+  Found found;
+  int end;              // the tokens of the sequences
+  int wrong;
 };
 
-// Cuts the line (all NT threads).  False: the ranges do not fit together.  sc->seq and sc->into: where this
-// CTA's piece begins (END: its last unit).
+__device__ __forceinline__ Line cut_line(long long total, int grid, int index) {
+  Line line;
+  const long long most = total / kLeast;
+  line.pieces = (int)(most < 1 ? 1 : most < grid ? most : grid);
+  const long long each = total / line.pieces;
+  const int more = (int)(total - each * line.pieces);
+  line.x0 = each * index + min(index, more);
+  line.x1 = each * (index + 1) + min(index + 1, more);
+  return line;
+}
+
+// Cuts the line and finds where this CTA's piece begins (END: its last unit; all NT threads).  False: the
+// ranges do not fit together.
 template <int NT, bool END>
-__device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Line* line, Scan* sc) {
+__device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Scan* sc) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (a.num_seqs <= 32) {                 // one warp, all that it needs loaded at once
+    if (warp == 0) {
+      const bool on = lane < a.num_seqs;
+      const int c0 = on ? __ldg(a.cu + lane) : 0, c1 = on ? __ldg(a.cu + lane + 1) : 0, slot = on ? __ldg(a.slots + lane) : -1;
+      const int init = on && a.init && __ldg(a.init + lane) != 0;
+      const bool wrong = (lane == 0 && c0 != 0) || c1 < c0 || c1 > a.total;
+      const long long cost = on ? head_cost(max(c1 - c0, 0)) * a.l.Hv : 0;
+      long long incl = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const Line line = cut_line(__shfl_sync(0xffffffffu, incl, 31), a.grid, index);
+      const long long x = END ? line.x1 - 1 : line.x0, before = incl - cost;
+      if (on && before <= x && x < incl) sc->found = Found{x - before, lane, c0, c1 - c0, slot, init};
+      if (lane == a.num_seqs - 1) sc->end = c1;
+      if (lane == 0) sc->line = line;
+      const bool any = __any_sync(0xffffffffu, wrong);
+      if (lane == 0) sc->wrong = any;
+    }
+    __syncthreads();
+    return !sc->wrong;
+  }
   const int per = (a.num_seqs + NT - 1) / NT, s0 = tid * per, s1 = min(a.num_seqs, s0 + per);
   long long sum = 0;
   bool wrong = tid == 0 && (__ldg(a.cu) != 0 || __ldg(a.cu + a.num_seqs) > a.total);
@@ -151,26 +197,22 @@ __device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Line* line
     if (w < warp) incl += sc->warp_sum[w];
     total += sc->warp_sum[w];
   }
-  const long long most = total / kLeast;
-  const int pieces = (int)(most < 1 ? 1 : most < a.grid ? most : a.grid);
-  line->pieces = pieces;
-  const long long each = total / pieces;
-  const int more = (int)(total - each * pieces);
-  line->x0 = each * index + min(index, more);
-  line->x1 = each * (index + 1) + min(index + 1, more);
-  if (index < pieces) {
-    const long long x = END ? line->x1 - 1 : line->x0;
-    long long at = incl - sum;
-    if (at <= x && x < incl) {
-      for (int s = s0; s < s1; ++s) {
-        const long long c = head_cost(__ldg(a.cu + s + 1) - __ldg(a.cu + s)) * a.l.Hv;
-        if (x < at + c) {
-          sc->seq = s;
-          sc->into = x - at;
-          break;
-        }
-        at += c;
+  const Line line = cut_line(total, a.grid, index);
+  if (tid == 0) {
+    sc->line = line;
+    sc->end = __ldg(a.cu + a.num_seqs);
+  }
+  const long long x = END ? line.x1 - 1 : line.x0;
+  long long at = incl - sum;
+  if (at <= x && x < incl) {
+    for (int s = s0; s < s1; ++s) {
+      const int c0 = __ldg(a.cu + s), len = __ldg(a.cu + s + 1) - c0;
+      const long long c = head_cost(len) * a.l.Hv;
+      if (x < at + c) {
+        sc->found = Found{x - at, s, c0, len, __ldg(a.slots + s), a.init && __ldg(a.init + s) != 0};
+        break;
       }
+      at += c;
     }
   }
   __syncthreads();
@@ -564,15 +606,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
   pdl_begin();
   float* decays = a.ws + 2 * (size_t)a.grid * (DK * DV);
   int* flags = reinterpret_cast<int*>(decays + a.grid);
-  Line line;
-  if (!locate<kSumThreads, true>(a, piece, &line, &sm.scan)) return;
+  if (!locate<kSumThreads, true>(a, piece, &sm.scan)) return;
   if (tid == 0) {
     // only the run that holds the piece's last unit can go on after it
     Run last = {};
     bool cut = false;
+    const Line line = sm.scan.line;
     if (piece < line.pieces) {
       Walk walk;
-      walk.start(a, line, line.x1 - 1, sm.scan.seq, sm.scan.into);
+      walk.start(a, line, line.x1 - 1, sm.scan.found);
       last = walk.here();
       cut = last.kind == kRun && last.c1 > last.c0 && last.c1 < last.n;
     }
@@ -830,16 +872,15 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     sm.dead = 0;
     mbar_fence_init();
   }
-  Line line;
-  if (!locate<kOutThreads, false>(a, piece, &line, &scan)) {
+  if (!locate<kOutThreads, false>(a, piece, &scan)) {
     if (tid == 0) set_status(a.l.status, GDN_STATUS_BAD_SEQLENS);
     zero_tokens(a, 0, a.total);
     pdl_wait_primary();
     return;
   }
-  const int seq = scan.seq;
-  const long long into = scan.into;
-  zero_tokens(a, __ldg(a.cu + a.num_seqs), a.total);
+  const Line line = scan.line;
+  const Found found = scan.found;
+  zero_tokens(a, scan.end, a.total);
   if (piece >= line.pieces) {
     pdl_wait_primary();
     return;
@@ -925,7 +966,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   } else if (warp == kLoadQWarp) {
     // ---------------------------------------------------------------- runs, one ahead, queries, check of the values
     Walk walk;
-    walk.start(a, line, line.x0, seq, into);
+    walk.start(a, line, line.x0, found);
     auto publish = [&](Run* r) {
       if (!walk.next(r)) r->kind = kEnd;
       wait_warp(&sm.run_empty[ring], ring_phase ^ 1u);
