@@ -3,9 +3,7 @@
 // Between an attention layer's projection and its cache every query and key vector is normed and turned:
 // a chain of element-wise steps, so one pass does them all, and q, k and v are read once.  The floor is
 // the bytes.  A CTA takes neighbouring tokens; a vector is a few neighbouring lanes, so the norm's sum is a
-// few shuffles.  In the half layout a lane's partner elements are loaded a second time, as raw bf16 (a
-// hit in L1: the lines are the warp's own), which costs one instruction where exchanging them costs four.
-// Angles belong to tokens: they are computed once into shared memory, while the vectors' first loads are
+// few shuffles.  A lane holds both elements of its pairs in either layout, so nothing is exchanged.  Angles belong to tokens: they are computed once into shared memory, while the vectors' first loads are
 // under way.
 #include "gdn_kv.cuh"
 #include "gdn_rotary.cuh"
@@ -75,51 +73,28 @@ __device__ __forceinline__ float lanes_max(float v) {
 
 enum Part { kQueries, kKeys, kValues };
 
-// A vector is L = D / 16 neighbouring lanes, each with two pieces of 8 elements: one from either half of the
-// vector, so that a warp's accesses are whole, and what a vector costs beside its elements (its place, its sum)
-// is spread over twice as many.
+// A vector is L = D / 16 neighbouring lanes, each with two pieces of 8 elements: what a vector costs beside its
+// elements (its place, its sum) is spread over many.  In the half layout lane l's are pieces l and l + half / 8,
+// each other's partners, for the rotated part, and for the rest l + half / 8 and l + L; else l and l + L.
 template <int D, bool Q8, bool INTER>
 struct Kernel {
   static constexpr int L = D / 16, kSide = 32 / L;      // lanes of a vector, vectors of a warp at a time
   static constexpr int kStep = 8 * kSide;               // vectors of the CTA's warps at a time
   static constexpr int kBatch = 2;                      // of these in flight, and as many ahead
 
-  // One piece's rotation: x its elements, other its partners' as they are in memory (half layout).
-  // wy their weights (held by no register: another hit in L1), NULL without a norm.
-  static __device__ __forceinline__ void turn(float* x, const uint4& other, const __nv_bfloat16* wy, float w0, float by,
-                                              const float* cp, const float* sp) {
-    if constexpr (INTER) {
-      const float4 co = *reinterpret_cast<const float4*>(cp), si = *reinterpret_cast<const float4*>(sp);
+  // The rotation of one piece of pairs, or of two whose elements are each other's partners (half layout).
+  static __device__ __forceinline__ void turn(float* x, float* y, const float* cp, const float* sp) {
+#pragma unroll
+    for (int j0 = 0; j0 < (INTER ? 4 : 8); j0 += 4) {
+      const float4 co = *reinterpret_cast<const float4*>(cp + j0), si = *reinterpret_cast<const float4*>(sp + j0);
       const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float u = x[2 * j], z = x[2 * j + 1];
-        x[2 * j] = turned_a(u, z, cc[j], sc[j]);
-        x[2 * j + 1] = turned_b(u, z, cc[j], sc[j]);
-      }
-    } else {
-      float y[8];
-      unpack8(other, y);
-      if (wy) {
-        float g[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(wy)), g);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          add_pair(g[j], g[j + 1], w0, w0);
-          mul_pair(y[j], y[j + 1], g[j], g[j + 1]);
-        }
-      }
-#pragma unroll
-      for (int j0 = 0; j0 < 8; j0 += 4) {
-        const float4 co = *reinterpret_cast<const float4*>(cp + j0), si = *reinterpret_cast<const float4*>(sp + j0);
-        const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          float* u = y + j0 + j;
-          mul_pair(u[0], u[1], by, by);               // (the sine's sign with the norm's factor)
-          mul_pair(u[0], u[1], sc[j], sc[j + 1]);
-          fma_pair(x[j0 + j], x[j0 + j + 1], cc[j], cc[j + 1], u[0], u[1]);
-        }
+        float& p = INTER ? x[2 * j] : x[j0 + j];
+        float& q = INTER ? x[2 * j + 1] : y[j0 + j];
+        const float u = p, z = q;
+        p = turned_a(u, z, cc[j], sc[j]);
+        q = turned_b(u, z, cc[j], sc[j]);
       }
     }
   }
@@ -138,21 +113,26 @@ struct Kernel {
     const __nv_bfloat16* src = PART == kQueries ? a.q : PART == kKeys ? a.k : a.v;
     const long long ld = PART == kQueries ? a.q_ld : PART == kKeys ? a.k_ld : a.v_ld;
     const long long head_ld = PART == kQueries ? a.q_head_ld : D;
-    src += (long long)t0 * ld + l * 8;
+    src += (long long)t0 * ld;
     const __nv_bfloat16* weight = PART == kQueries ? a.q_norm : PART == kKeys ? a.k_norm : nullptr;
-    // of either piece: whether it is turned, where its partners are and which angles are its
-    bool turned[2], second[2];
-    int away[2], angle[2];
+    // the pieces' places in the vector, whether they are turned and which angles are theirs
+    int at[2], angle[2];
+    bool turned[2];
     float g[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int at = h * (D / 2) + l * 8;
-      turned[h] = PART != kValues && at < 2 * a.half;
-      second[h] = !INTER && at >= a.half;
-      away[h] = INTER ? 0 : second[h] ? -a.half : a.half;
-      angle[h] = INTER ? at / 2 : second[h] ? at - a.half : at;
+      if (INTER) {
+        at[h] = (l + h * L) * 8;
+        turned[h] = at[h] < 2 * a.half;
+        angle[h] = at[h] / 2;
+      } else {
+        turned[h] = l * 8 < a.half;
+        at[h] = turned[h] ? l * 8 + h * a.half : h == 0 ? l * 8 + a.half : (L + l) * 8;
+        angle[h] = l * 8;
+      }
+      turned[h] = turned[h] && PART != kValues;
       if (PART != kValues && weight) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(weight + at)), g[h]);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(weight + at[h])), g[h]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[h][j] += a.w0;
       }
@@ -164,7 +144,6 @@ struct Kernel {
     const long long skip = skip_tok * ld + skip_head * head_ld, wrap = ld - heads * head_ld;
     struct Batch {
       uint4 raw[kBatch][2];
-      const __nv_bfloat16* from[kBatch];
       int tok[kBatch], head[kBatch];
     };
     auto load = [&](Batch& b) {
@@ -172,10 +151,9 @@ struct Kernel {
       for (int i = 0; i < kBatch; ++i) {
         b.tok[i] = tok;
         b.head[i] = head;
-        b.from[i] = src;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          b.raw[i][h] = tok < count ? __ldg(reinterpret_cast<const uint4*>(src + h * (D / 2))) : make_uint4(0, 0, 0, 0);
+          b.raw[i][h] = tok < count ? __ldg(reinterpret_cast<const uint4*>(src + at[h])) : make_uint4(0, 0, 0, 0);
         src += skip;
         tok += skip_tok;
         head += skip_head;
@@ -193,15 +171,6 @@ struct Kernel {
 #pragma unroll 1
     for (int v = warp * kSide; v < n; v += kStep * kBatch) {
       load(next);                       // (nothing past the last token)
-      uint4 other[kBatch][2];           // the partners: the lines are in L1
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          other[i][h] = make_uint4(0, 0, 0, 0);
-          if (!INTER && turned[h] && now.tok[i] < count)
-            other[i][h] = __ldg(reinterpret_cast<const uint4*>(now.from[i] + h * (D / 2) + away[h]));
-        }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const bool live = now.tok[i] < count;
@@ -230,35 +199,39 @@ struct Kernel {
               mul_pair(u[0], u[1], rs, rs);
             }
           }
+          const float* cp = cs + (live ? now.tok[i] * a.half : 0);
+          const float* sp = sn + (live ? now.tok[i] * a.half : 0);
+          if (INTER) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (turned[h] && live)
-              turn(x[h], other[i][h], weight ? weight + h * (D / 2) + l * 8 + away[h] : nullptr, a.w0, second[h] ? rs : -rs,
-                   cs + now.tok[i] * a.half + angle[h], sn + now.tok[i] * a.half + angle[h]);
+            for (int h = 0; h < 2; ++h)
+              if (turned[h]) turn(x[h], nullptr, cp + angle[h], sp + angle[h]);
+          } else if (turned[0]) {
+            turn(x[0], x[1], cp + angle[0], sp + angle[0]);
+          }
         }
         if constexpr (PART == kQueries) {
           if (live) {
-            uint4* out = reinterpret_cast<uint4*>(a.q_out) + ((long long)t0 * a.Hq + v + i * kStep + lane / L) * (2 * L) + l;
+            uint4* out = reinterpret_cast<uint4*>(a.q_out) + ((long long)t0 * a.Hq + v + i * kStep + lane / L) * (2 * L);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) out[h * L] = base < 0 ? make_uint4(0, 0, 0, 0) : pack8(x[h]);
+            for (int h = 0; h < 2; ++h) out[at[h] / 8] = base < 0 ? make_uint4(0, 0, 0, 0) : pack8(x[h]);
           }
         } else {
-          const long long at = base + ((long long)now.head[i] << c.page_shift);
+          const long long slot = base + ((long long)now.head[i] << c.page_shift);
           if constexpr (Q8) {
             uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j >> 3][j & 7]) & 0x7fffffffu);
             const int b = scale_byte_f32(lanes_max<L>(__uint_as_float(top)));
             if (base >= 0) {
-              uint2* out = reinterpret_cast<uint2*>(static_cast<uint8_t*>(PART == kValues ? c.v : c.k) + at * D) + l;
+              uint2* out = reinterpret_cast<uint2*>(static_cast<uint8_t*>(PART == kValues ? c.v : c.k) + slot * D);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) out[h * L] = codes8(x[h], b);
-              if (l == 0) (PART == kValues ? c.vs : c.ks)[at] = (uint8_t)b;
+              for (int h = 0; h < 2; ++h) out[at[h] / 8] = codes8(x[h], b);
+              if (l == 0) (PART == kValues ? c.vs : c.ks)[slot] = (uint8_t)b;
             }
           } else if (base >= 0) {
-            uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(PART == kValues ? c.v : c.k) + at * D) + l;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(PART == kValues ? c.v : c.k) + slot * D);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) out[h * L] = PART == kValues ? now.raw[i][h] : pack8(x[h]);
+            for (int h = 0; h < 2; ++h) out[at[h] / 8] = PART == kValues ? now.raw[i][h] : pack8(x[h]);
           }
         }
       }
@@ -307,7 +280,7 @@ int launch_kv_append_rotated(const KvView& c, const KvBatchView& bt, const Rotat
   while (t < 16 && bt.total > 2048 * t) t *= 2;
   const int tokens = t < most ? (int)t : most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((bt.total + tokens - 1) / tokens));
+  cfg.gridDim = dim3((unsigned)((bt.total - 1) / tokens + 1));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
