@@ -27,6 +27,14 @@ struct StepArgs {
   int T;
 };
 
+// (x, y) += f * (a, b)
+__device__ __forceinline__ void add_product(float& x, float& y, float f, float a, float b) {
+  float u = f, w = f;
+  fma_pair(u, w, a, b, x, y);
+  x = u;
+  y = w;
+}
+
 template <int DK, int DV, int CW>
 __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
   constexpr int LPR = CW / 4;                // lanes (of float4) to a row
@@ -34,8 +42,8 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
   constexpr int N = DK / R;                  // rows of a thread
   static_assert(DK % R == 0, "rows of a thread");
   constexpr int SUMS = R < 8 ? R : 8;        // partial sums that meet: a warp's rows are added by shuffles
-  __shared__ float qs[kBlock][DK], ks[kBlock][DK], vs[kBlock][CW], gs[kBlock];
-  __shared__ __align__(16) float sums[kBlock][SUMS][CW];
+  __shared__ __align__(16) float qs[kBlock][DK], ks[kBlock][DK], vs[kBlock][CW], sums[kBlock][SUMS][CW];
+  __shared__ float gs[kBlock];
   const int tid = threadIdx.x, row = blockIdx.z, h = blockIdx.y, c0 = blockIdx.x * CW;
   const int r0 = tid / LPR, c = (tid % LPR) * 4;
   pdl_begin();
@@ -53,31 +61,43 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
     s[i] = __ldcs(reinterpret_cast<const float4*>(state + (size_t)(r0 + i * R) * DV + c));
-  for (int i = tid; i < a.T * DK; i += kThreads) {
-    const int t = i / DK, d = i % DK;
-    qs[t][d] = __bfloat162float(a.q[(t0 + t) * a.q_ld + hk * DK + d]) * a.l.scale;
-    ks[t][d] = __bfloat162float(a.k[(t0 + t) * a.k_ld + hk * DK + d]);
+  // vectors of 8: queries, keys and values of all tokens
+  constexpr int KV = DK / 8, VV = CW / 8;
+  for (int i = tid; i < a.T * (2 * KV + VV); i += kThreads) {
+    const int t = i / (2 * KV + VV), p = i % (2 * KV + VV);
+    const bool q = p < KV, k = !q && p < 2 * KV;
+    const int d = (q ? p : k ? p - KV : p - 2 * KV) * 8;
+    const __nv_bfloat16* src = q ? a.q + (t0 + t) * a.q_ld + hk * DK : k ? a.k + (t0 + t) * a.k_ld + hk * DK
+                                                                      : a.v + (t0 + t) * a.v_ld + h * DV + c0;
+    float* dst = q ? qs[t] : k ? ks[t] : vs[t];
+    const uint4 u = *reinterpret_cast<const uint4*>(src + d);
+    const float f = q ? a.l.scale : 1.f;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+      *reinterpret_cast<float4*>(dst + d + 2 * e) =
+          make_float4(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f,
+                      __uint_as_float(w[e + 1] << 16) * f, __uint_as_float(w[e + 1] & 0xffff0000u) * f);
   }
-  for (int i = tid; i < a.T * CW; i += kThreads)
-    vs[i / CW][i % CW] = __bfloat162float(a.v[(t0 + i / CW) * a.v_ld + h * DV + c0 + i % CW]);
   if (tid < a.T) gs[tid] = expf(__ldg(a.g + (t0 + tid) * a.g_ld + h));
   __syncthreads();
   for (int t = 0; t < a.T; ++t) {
     const float e = gs[t];
     const float4 v = *reinterpret_cast<const float4*>(&vs[t][c]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (e == 0.f) {                  // a decay of zero empties the state whatever it held
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = o;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float k = ks[t][r0 + i * R], q = qs[t][r0 + i * R];
-      // a decay of zero empties the state whatever it held
-      s[i].x = fmaf(k, v.x, e == 0.f ? 0.f : e * s[i].x);
-      s[i].y = fmaf(k, v.y, e == 0.f ? 0.f : e * s[i].y);
-      s[i].z = fmaf(k, v.z, e == 0.f ? 0.f : e * s[i].z);
-      s[i].w = fmaf(k, v.w, e == 0.f ? 0.f : e * s[i].w);
-      o.x = fmaf(q, s[i].x, o.x);
-      o.y = fmaf(q, s[i].y, o.y);
-      o.z = fmaf(q, s[i].z, o.z);
-      o.w = fmaf(q, s[i].w, o.w);
+      mul_pair(s[i].x, s[i].y, e, e);
+      mul_pair(s[i].z, s[i].w, e, e);
+      add_product(s[i].x, s[i].y, k, v.x, v.y);
+      add_product(s[i].z, s[i].w, k, v.z, v.w);
+      add_product(o.x, o.y, q, s[i].x, s[i].y);
+      add_product(o.z, o.w, q, s[i].z, s[i].w);
     }
 #pragma unroll
     for (int m = LPR; m < 32; m <<= 1) {
