@@ -59,6 +59,8 @@ struct Vec {
       if constexpr (V == 8) {
         const uint4 u = *reinterpret_cast<const uint4*>(p);
         w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+      } else if constexpr (V == 2) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
       } else {
         const uint2 u = *reinterpret_cast<const uint2*>(p);
         w[0] = u.x; w[1] = u.y;
@@ -84,6 +86,7 @@ struct Vec {
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
       if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
       else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
   }
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
   __syncthreads();
   const uint32_t n = (uint32_t)count * a.heads * a.items.d;
   const int paired = INTER && V > 1 ? 0 : a.half / V;
-#pragma unroll 2
+#pragma unroll(V <= 2 ? 4 : 2)
   for (uint32_t i = tid; i < n; i += 256) {
     const uint32_t th = a.items.div(i), e = i - th * a.items.d, t = a.all_heads.div(th);
     int h = (int)(th - t * a.all_heads.d);
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
 template <typename T, int V>
 int launch_as(const RotaryArgs& a, bool inter, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.tokens + a.per_cta - 1) / a.per_cta));
+  cfg.gridDim = dim3((unsigned)((a.tokens - 1) / a.per_cta + 1));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -182,7 +185,7 @@ int launch_typed(const RotaryLaunch& r, cudaStream_t stream) {
     return bases % (v * sizeof(T)) == 0 && n % v == 0;
   };
   constexpr int kWide = 16 / sizeof(T), kMid = 8 / sizeof(T);
-  const int v = fits(kWide) ? kWide : fits(kMid) ? kMid : 1;
+  const int v = fits(kWide) ? kWide : fits(kMid) ? kMid : fits(2) ? 2 : 1;
   const int heads = r.q_heads + r.k_heads;
   const int items = r.interleaved && v > 1 ? r.dim / v : (r.dim - half) / v;
   // tokens of a CTA: some four items a thread, as far as their sines fit
@@ -194,6 +197,7 @@ int launch_typed(const RotaryLaunch& r, cudaStream_t stream) {
                      FastDiv((uint32_t)heads), FastDiv((uint32_t)half)};
   if (v == kWide) return launch_as<T, kWide>(a, r.interleaved, stream);
   if (v == kMid) return launch_as<T, kMid>(a, r.interleaved, stream);
+  if (v == 2) return launch_as<T, 2>(a, r.interleaved, stream);
   return launch_as<T, 1>(a, r.interleaved, stream);
 }
 

@@ -106,6 +106,31 @@ def test_special_values():
     assert bad == [[0, 0, 3], [0, 0, 11], [1, 0, 20]]
 
 
+@pytest.mark.parametrize("rot", [20, 36, 10])
+def test_vectors_of_all_sizes(rot):
+    """Halves on 16-, 8- and 4-byte boundaries and on none: the bits of the plain call on a shifted copy."""
+    plan = runtime.Rotary(rot)
+    pos = torch.arange(50, dtype=torch.int32, device="cuda") * 777
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn((50, 3, 72), device="cuda").to(dtype)
+        want = plan.apply(pos, x)[0]
+        for shift, ld in ((1, 77), (2, 78), (4, 80), (8, 80)):
+            wide = torch.zeros((50, 3, ld + 8), dtype=dtype, device="cuda")
+            wide[..., shift:shift + 72] = x
+            assert torch.equal(plan.apply(pos, wide[..., shift:shift + 72])[0], want)
+
+
+def test_most_tokens():
+    """Token counts at the end of 31 bits."""
+    tokens = 2 ** 31 - 1
+    plan = runtime.Rotary.of([math.pi / 2])
+    pos = torch.zeros(tokens, dtype=torch.int32, device="cuda")
+    pos[-1] = 1
+    x = torch.ones((tokens, 1, 2), dtype=torch.bfloat16, device="cuda")
+    plan.apply(pos, x, q_out=x)
+    assert x[-1, 0].tolist() == [-1.0, 1.0] and x[-2, 0].tolist() == [1.0, 1.0] and int((x[: 1 << 30] != 1.0).sum()) == 0
+
+
 # ---------------------------------------------------------------- append with rotation
 
 def case_inputs(case, Hq, seed, norm):
