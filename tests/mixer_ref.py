@@ -70,7 +70,7 @@ def decay(S, q, k, v, g, scale=None):
 
 def close(got, want, bound, what=""):
     """|got - want| <= bound where want is finite; the same infinities and NaN elsewhere."""
-    got = got.detach().cpu().double()
+    got, want, bound = got.detach().cpu().double(), want.cpu(), bound.cpu()
     fine = want.isfinite()
     assert torch.equal(got.isnan(), want.isnan()), f"{what}: NaN in other places"
     assert torch.equal(got[~fine & ~want.isnan()], want[~fine & ~want.isnan()]), f"{what}: infinities"

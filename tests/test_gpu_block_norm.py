@@ -124,3 +124,45 @@ def test_special_values_and_graph():
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
     assert runtime.block_norm(x["x"][:0])[0].shape == (0, 512)
     assert gdn.GDN_GATE_SILU == 2
+
+
+@pytest.mark.parametrize("dtype,rows,n,pad", [
+    (torch.bfloat16, 20000, 264, 0), (torch.bfloat16, 5000, 1600, 8), (torch.bfloat16, 1300, 12296, 0),     # aligned rows
+    (torch.bfloat16, 20001, 129, 0), (torch.bfloat16, 20000, 130, 2), (torch.bfloat16, 7001, 1001, 2),       # pairs
+    (torch.bfloat16, 3001, 4097, 4), (torch.bfloat16, 1301, 8191, 0), (torch.bfloat16, 611, 15001, 0),
+    (torch.bfloat16, 20001, 131, 1), (torch.bfloat16, 7001, 1002, 1), (torch.bfloat16, 650, 20001, 1),       # anywhere
+    (torch.float32, 20001, 257, 0), (torch.float32, 4001, 1500, 4), (torch.float32, 1301, 7001, 0),
+    (torch.float32, 1301, 8192, 0), (torch.float32, 620, 12289, 3)])
+def test_many_rows(dtype, rows, n, pad):
+    """Rows enough for CTAs that stay, on and off the boundaries, with NaN between them."""
+    t = make(rows, n, n, dtype, rows + n)
+    dev = {k: v.cuda() for k, v in t.items()}
+    for k in ("x", "gate", "residual"):
+        wide = torch.full((rows, n + pad), math.nan, dtype=dtype, device="cuda")
+        wide[:, :n] = dev[k]
+        dev[k] = wide[:, :n]
+    total, y = Guarded((rows, n), dtype), Guarded((rows, n), dtype)
+    got = runtime.block_norm(**dev, weight_offset=1.0, gate_act="silu", scale=0.5, total=total.view, y=y.view)
+    total.check()
+    y.check()
+    check({k: v.cuda() for k, v in t.items()}, dtype, got, "silu", 0.5)
+    # parts of it, in place of the residual
+    dense = t["residual"].cuda()
+    alone, _ = runtime.block_norm(dev["x"], dev["post"], residual=dense.clone(), weight_offset=1.0)
+    runtime.block_norm(dev["x"], dev["post"], residual=dense, total=dense, weight_offset=1.0)
+    assert torch.equal(alone, dense)
+    check({k: t[k].cuda() for k in ("x", "post", "residual")}, dtype, (dense, None))
+    # its last rows by themselves
+    few = runtime.block_norm(**{k: v[-3:].clone() if k in ("x", "gate", "residual") else v for k, v in dev.items()},
+                             weight_offset=1.0, gate_act="silu", scale=0.5)
+    check({k: (v[-3:] if k in ("x", "gate", "residual") else v).cuda() for k, v in t.items()}, dtype, few, "silu", 0.5)
+
+
+def test_most_rows():
+    """Row counts at the end of 31 bits."""
+    rows = 2 ** 31 - 1
+    x = torch.ones((rows, 1), dtype=torch.bfloat16, device="cuda")
+    x[-1], x[-2] = 3.0, -5.0
+    total, _ = runtime.block_norm(x, scale=2.0)
+    assert total[-1].item() == 6.0 and total[-2].item() == -10.0 and total[0].item() == 2.0
+    assert int((total[: 1 << 30] != 2.0).sum()) == 0
