@@ -158,7 +158,7 @@ __device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Scan* sc) 
       const int c0 = on ? __ldg(a.cu + lane) : 0, c1 = on ? __ldg(a.cu + lane + 1) : 0, slot = on ? __ldg(a.slots + lane) : -1;
       const int init = on && a.init && __ldg(a.init + lane) != 0;
       const bool wrong = (lane == 0 && c0 != 0) || c1 < c0 || c1 > a.total;
-      const long long cost = on ? head_cost(max(c1 - c0, 0)) * a.l.Hv : 0;
+      const long long cost = on ? head_cost(c1 > c0 ? c1 - c0 : 0) * a.l.Hv : 0;
       long long incl = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -178,11 +178,11 @@ __device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Scan* sc) 
   }
   const int per = (a.num_seqs + NT - 1) / NT, s0 = tid * per, s1 = min(a.num_seqs, s0 + per);
   long long sum = 0;
-  bool wrong = tid == 0 && (__ldg(a.cu) != 0 || __ldg(a.cu + a.num_seqs) > a.total);
+  bool wrong = tid == 0 && __ldg(a.cu) != 0;
   for (int s = s0; s < s1; ++s) {
-    const int len = __ldg(a.cu + s + 1) - __ldg(a.cu + s);
-    wrong |= len < 0;
-    sum += head_cost(max(len, 0)) * a.l.Hv;
+    const int c0 = __ldg(a.cu + s), c1 = __ldg(a.cu + s + 1);
+    wrong |= c1 < c0 || c1 > a.total;
+    sum += head_cost(c1 > c0 ? c1 - c0 : 0) * a.l.Hv;
   }
   long long incl = sum;
 #pragma unroll

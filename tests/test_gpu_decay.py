@@ -249,3 +249,52 @@ def test_graphs_streams_and_repeats():
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
     assert torch.equal(layers[0].state, layers[1].state)
+
+
+def test_many_sequences():
+    """More sequences than a CTA has threads, most of them short, some empty; and ranges that do not fit together
+    among many, such as lengths that wrap around 32 bits."""
+    g = torch.Generator().manual_seed(50)
+    lens = torch.randint(0, 5, (1500,), generator=g).tolist()
+    lens[700], lens[1499] = 400, 150
+    run_prompts(lens, 1, 1, 64, 64, True, [i % 3 == 0 for i in range(1500)])
+    row, decay = inputs((100,), 1, 2, 64, 64, 5, True)
+    q, k, v = views(row.cuda(), 1, 2, 64, 64)
+    for at, cuts in ((20, [2 ** 31 - 1, -2 ** 31, -1]), (0, [3]), (30, [101, 100]), (39, [50, 20])):
+        cu = [0] * at + cuts + [100] * (41 - at - len(cuts))
+        state = pool(40, 2, 64, 64, 4)
+        layer = runtime.DecayAttention.over(state.cuda(), 1)
+        out = layer.prefill(torch.tensor(cu, dtype=torch.int32, device="cuda"), torch.arange(40, dtype=torch.int32, device="cuda"), None,
+                            q, k, v, decay.cuda())
+        assert int(layer.status.item()) == gdn.GDN_STATUS_BAD_SEQLENS, cuts
+        assert bool((out == 0).all()) and torch.equal(layer.state.cpu(), state)
+
+
+def test_no_tokens():
+    """Sequences without any tokens: states begin, or stay."""
+    state = pool(4, 2, 128, 64, 6)
+    for n in (3, 40):
+        layer = runtime.DecayAttention.over(state.cuda(), 1)
+        slots = torch.full((n,), -1, dtype=torch.int32)
+        slots[:3] = torch.tensor([2, 0, -1])
+        flags = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        flags[0] = 1
+        nothing = torch.zeros((0, 2, 128), dtype=torch.bfloat16, device="cuda")
+        out = layer.prefill(torch.zeros(n + 1, dtype=torch.int32, device="cuda"), slots.cuda(), flags, nothing[:, :1], nothing[:, :1],
+                            torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros(2, device="cuda"))
+        want = state.clone()
+        want[0] = 0
+        assert out.shape == (0, 2, 64) and torch.equal(layer.state.cpu(), want) and int(layer.status.item()) == 0
+
+
+def test_many_tokens_that_empty_the_state():
+    """Decays of the lowest value add up to thousands in a chunk; what is left between them is still exact to a bf16."""
+    T, Hv = 300, 4
+    row, _ = inputs((T,), 1, Hv, 64, 64, 12, True)
+    g = torch.Generator().manual_seed(13)
+    decay = -0.05 * torch.rand((T, Hv), generator=g)
+    decay[:64, 0] = -math.inf
+    decay[::2, 1] = -math.inf
+    decay[torch.rand(T, generator=g) < 0.7, 2] = -200.0
+    decay[:120, 3] = -104.0
+    run_prompts([T], 1, Hv, 64, 64, True, [1], row=row, decay=decay)
