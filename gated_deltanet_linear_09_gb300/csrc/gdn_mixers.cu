@@ -8,6 +8,10 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+bool dense(int tokens, int heads, int dim, int64_t ld, int64_t head_ld) {
+  return (heads == 1 || head_ld == dim) && (tokens == 1 || ld == (int64_t)heads * dim);
+}
+
 int check_layer(const gdn_decay_layer* layer, gdn::DecayView* v, bool need_memory) {
   if (!layer) return GDN_ERR_INVALID_ARG;
   const gdn_decay_layer& l = *layer;
@@ -38,6 +42,9 @@ int check_tokens(const gdn_decay_tokens* tokens, const gdn::DecayView& l, long l
   return GDN_OK;
 }
 
+// The outputs are not the inputs.
+bool apart(const gdn_decay_tokens& t, long long count) { return count == 0 || (t.out != t.q && t.out != t.k && t.out != t.v); }
+
 }  // namespace
 
 extern "C" {
@@ -58,10 +65,12 @@ int gdn_rotary_apply(const gdn_rotary* rotary, const int32_t* positions, int32_t
   if (q_heads > 0) {
     if (!q || !q_out || q_ld < head_dim || q_head_ld < head_dim) return GDN_ERR_INVALID_ARG;
     if (!aligned(q, size) || !aligned(q_out, size)) return GDN_ERR_MISALIGNED;
+    if (q_out == q && !dense(tokens, q_heads, head_dim, q_ld, q_head_ld)) return GDN_ERR_INVALID_ARG;
   }
   if (k_heads > 0) {
     if (!k || !k_out || k_ld < head_dim || k_head_ld < head_dim) return GDN_ERR_INVALID_ARG;
     if (!aligned(k, size) || !aligned(k_out, size)) return GDN_ERR_MISALIGNED;
+    if (k_out == k && !dense(tokens, k_heads, head_dim, k_ld, k_head_ld)) return GDN_ERR_INVALID_ARG;
   }
   const gdn::RotaryLaunch r{q_heads ? q : nullptr, k_heads ? k : nullptr, q_heads ? q_out : nullptr, k_heads ? k_out : nullptr,
                             q_heads ? q_ld : 0, q_heads ? q_head_ld : 0, k_heads ? k_ld : 0, k_heads ? k_head_ld : 0,
@@ -88,6 +97,7 @@ int gdn_block_norm(const gdn_block_args* args, int32_t rows, int32_t n, gdn_dtyp
     if (!aligned(p, 16)) return GDN_ERR_MISALIGNED;
   if (a.post && a.group != n && (a.x_ld % 8 != 0 || (a.gate && a.gate_ld % 8 != 0) || (a.residual && a.residual_ld % 8 != 0)))
     return GDN_ERR_MISALIGNED;
+  if (a.total == a.y) return GDN_ERR_INVALID_ARG;
   return gdn::launch_block_norm(a, rows, n, act, stream);
 }
 
@@ -103,6 +113,7 @@ int gdn_decay_step(const gdn_decay_layer* layer, const gdn_decay_tokens* tokens,
   if (B == 0) return GDN_OK;
   if (!slot_idx) return GDN_ERR_INVALID_ARG;
   if (!aligned(slot_idx, 4)) return GDN_ERR_MISALIGNED;
+  if (!apart(*tokens, B)) return GDN_ERR_INVALID_ARG;
   return gdn::launch_decay_step(l, *tokens, slot_idx, B, T, stream);
 }
 
@@ -128,6 +139,7 @@ int gdn_decay_prefill(const gdn_decay_layer* layer, const gdn_decay_tokens* toke
   if (!workspace || workspace_bytes < gdn::decay_prefill_ws_bytes(l, num_seqs, total_tokens))
     return GDN_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 256)) return GDN_ERR_MISALIGNED;
+  if (!apart(*tokens, total_tokens)) return GDN_ERR_INVALID_ARG;
   return gdn::launch_decay_prefill(l, *tokens, cu_seqlens, slot_idx, has_initial_state, num_seqs, total_tokens,
                                    workspace, stream);
 }

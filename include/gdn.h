@@ -500,7 +500,8 @@ typedef struct {
  *   x -> x / sqrt(mean x^2 + eps) * (weight_offset + w)   (with a weight),  then the rotation,
  * in f32, rounded once to bf16 (q_out, a bf16 cache), or to e4m3 with the scale of the f32 vector.
  * Values are stored as by gdn_kv_append.  q: bf16, element (t, h, d) at t * q_ld + h * q_head_ld + d (NULL
- * with num_q_heads 0), q_out dense [total_tokens][num_q_heads][head_dim]; k, v as in gdn_kv_append.
+ * with num_q_heads 0), q_out dense [total_tokens][num_q_heads][head_dim], overlapping no input; k, v as in
+ * gdn_kv_append.
  * Distances are multiples of 8, bases 16-byte aligned.  rot_dim <= head_dim, a multiple of 16
  * (GDN_ERR_UNSUPPORTED_SHAPE).  The queries of tokens without a place are zeros.  One launch. */
 int gdn_kv_append_rotated(const gdn_kv_cache* cache, const gdn_kv_batch* batch, const gdn_rotary* rotary,
@@ -519,7 +520,7 @@ typedef enum { GDN_GATE_NONE = 0, GDN_GATE_SIGMOID = 1, GDN_GATE_SILU = 2 } gdn_
  * weights post [group] they share.  act: sigmoid(z), or z sigmoid(z) (SILU).
  *   x, gate, residual: rows x_ld / gate_ld / residual_ld apart (>= n); pre, channel_scale [n]; total (NULL:
  *   not written, with pre only; may be residual or x, with equal row distance n) and y (NULL without pre)
- *   dense.  Any n up to GDN_MAX_NORM_WIDTH and any distances; rows that start on 16-byte boundaries and hold
+ *   dense, overlapping nothing else.  Any n up to GDN_MAX_NORM_WIDTH and any distances; rows that start on 16-byte boundaries and hold
  *   a multiple of 8 elements move in 16-byte vectors, and groups below n need those
  *   (GDN_ERR_MISALIGNED).  rows = 0 is a no-op.  One launch. */
 typedef struct {
@@ -557,7 +558,7 @@ typedef struct {
 
 /* The tokens of a call: q, k bf16 [tokens][num_k_heads][dk], v bf16 [tokens][num_v_heads][dv], heads
  * adjacent, tokens q_ld / k_ld / v_ld elements apart (multiples of 8); out bf16 [tokens][num_v_heads][dv],
- * dense.  g of token t and head h: log_decay[t * decay_ld + h] (f32; decay_ld 0: the same for every token),
+ * dense, overlapping no input.  g of token t and head h: log_decay[t * decay_ld + h] (f32; decay_ld 0: the same for every token),
  * finite or -inf, which empties the state; below -105 it counts as -inf (exp of it is 0 in f32).  16-byte
  * aligned, log_decay 4-byte aligned. */
 typedef struct {
@@ -586,7 +587,8 @@ size_t gdn_decay_prefill_workspace_bytes(const gdn_decay_layer* layer, int32_t n
  * gdn_prefill_chunked; outputs of tokens in no usable sequence are zeros.  The state is kept and added up
  * in f32, from products of keys that are exact to 2^-16; for the outputs, states and the decayed scores
  * are rounded to bf16 (half a step, 2^-9, of each).  workspace: device, 256-byte aligned, contents
- * undefined on entry and exit; calls that may run at the same time need one each.  Bitwise reproducible. */
+ * undefined on entry and exit; calls that may run at the same time need one each.  Bitwise reproducible.
+ * Three launches; one for up to 128 tokens. */
 int gdn_decay_prefill(const gdn_decay_layer* layer, const gdn_decay_tokens* tokens, const int32_t* cu_seqlens,
                       const int32_t* slot_idx, const uint8_t* has_initial_state, int32_t num_seqs,
                       int32_t total_tokens, void* workspace, size_t workspace_bytes, cudaStream_t stream);

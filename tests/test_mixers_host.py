@@ -117,6 +117,27 @@ def test_decay_refusals(lib):
     assert lib.gdn_decay_step(None, None, A, 1, 1, None) == INV
 
 
+def test_outputs_are_not_the_inputs(lib):
+    """Outputs in the place of inputs, where the call cannot have them there."""
+    r = rot()
+    for heads, ld, head_ld, tokens in ((2, 256, 128, 2), (2, 257, 128, 2), (2, 258, 129, 2), (2, 258, 129, 1)):
+        want = 0 if (ld, head_ld) == (256, 128) else INV
+        if want:            # (the first would launch)
+            assert lib.gdn_rotary_apply(ctypes.byref(r), A, tokens, 128, gdn.GDN_BF16, A, ld, head_ld, heads, A, None, 0, 0, 0, None, None) == want
+            assert lib.gdn_rotary_apply(ctypes.byref(r), A, tokens, 128, gdn.GDN_BF16, None, 0, 0, 0, None, A, ld, head_ld, heads, A, None) == want
+    c = gdn.gdn_kv_cache(A, A, None, None, 4, 16, 2, 128, gdn.GDN_KV_BF16, None)
+    b = gdn.gdn_kv_batch(cu_seqlens=A, kv_lens=A, block_table=A, num_seqs=1, total_tokens=1, table_ld=4, max_tokens=1)
+    p = gdn.gdn_head_prep(A, A, 1.0, 1e-6, None)
+    assert lib.gdn_kv_append_rotated(ctypes.byref(c), ctypes.byref(b), ctypes.byref(r), ctypes.byref(p), A, 512, 128, 4, A, A, 256, A, 256, None) == INV
+    a = gdn.gdn_block_args(x=A, pre=A, total=2 * A, y=2 * A, x_ld=256, scale=1.0, weight_offset=0.0, eps=1e-6, group=256, gate_act=0)
+    assert lib.gdn_block_norm(ctypes.byref(a), 2, 256, gdn.GDN_BF16, None) == INV
+    for name in ("q", "k", "v"):
+        l = gdn.gdn_decay_layer(A, 4, 2, 4, 128, 64, 0.0, None)
+        t = gdn.gdn_decay_tokens(**{**dict(q=A, k=A, v=A, q_ld=256, k_ld=256, v_ld=256, log_decay=A, decay_ld=4, out=2 * A), name: 2 * A})
+        assert lib.gdn_decay_step(ctypes.byref(l), ctypes.byref(t), A, 2, 1, None) == INV
+        assert lib.gdn_decay_prefill(ctypes.byref(l), ctypes.byref(t), A, A, None, 2, 10, A, 1 << 40, None) == INV
+
+
 def test_structs_match_the_header():
     """Sizes as the C compiler lays them out on a 64-bit machine."""
     assert ctypes.sizeof(gdn.gdn_rotary) == 24 and ctypes.sizeof(gdn.gdn_head_prep) == 32
