@@ -333,6 +333,8 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
+
 // A token's log decay, in log2 units.
 __device__ __forceinline__ float decay_log2(const ChunkArgs& a, long long t, int h) {
   const float g = __ldg(a.g + t * a.g_ld + h);
@@ -969,6 +971,11 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     walk.start(a, line, line.x0, found);
     auto publish = [&](Run* r) {
       if (!walk.next(r)) r->kind = kEnd;
+      // the state that it begins with comes from DRAM: on its way to L2
+      if (r->kind == kRun && r->c0 == 0 && r->c1 == r->n && r->init) {
+        const float* state = a.l.state + ((long long)r->slot * a.l.Hv + r->head) * (DK * DV);
+        for (int i = lane * 32; i < DK * DV; i += 32 * 32) prefetch_l2(state + i);
+      }
       wait_warp(&sm.run_empty[ring], ring_phase ^ 1u);
       if (lane == 0 && !dead()) {
         if (r->kind != kEnd && r->slot >= a.l.num_slots) set_status(a.l.status, GDN_STATUS_SLOT_RANGE);
