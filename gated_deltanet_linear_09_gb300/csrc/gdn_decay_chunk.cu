@@ -57,6 +57,8 @@ struct Maps {
 // A piece's share of one head of one sequence: chunks [c0, c1) of n.
 struct Run {
   int t0, len, head, slot, c0, c1, n, kind, init;
+  // chunk c is the first of a sequence that begins without a state
+  __device__ __forceinline__ bool fresh(int c) const { return c == 0 && !init; }
 };
 enum { kEnd = 0, kRun = 1, kZeros = 2 };      // no more runs; a run; one without a usable slot
 
@@ -1040,8 +1042,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         if (n > 0) wait(&sm.o_empty, (n & 1) ^ 1u);
         if (dead()) break;
         fence_after_sync();
+        const bool fresh = r.fresh(c);
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks)
+        for (int ks = 0; ks < DK / 16 && !fresh; ++ks)
           mma_ss(tmem + kTmI, qd + ((ks >> 2) * (128 * kC) + (ks & 3) * 32) / 16,
                  sd + ((ks >> 2) * (128 * DV) + (ks & 3) * 32) / 16, idesc_bf16(128, DV), ks > 0);
         mma_commit(&sm.q_empty);
@@ -1054,7 +1057,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         for (int part = 0; part < 2; ++part) {
           const uint32_t kb = part ? lod : km;
 #pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kTmState, vm + ks * 128, kb + ks * 128, idesc_bf16_mnmn(128, DK), 1);
+          for (int ks = 0; ks < kC / 16; ++ks)
+            mma_ss(tmem + kTmState, vm + ks * 128, kb + ks * 128, idesc_bf16_mnmn(128, DK), !fresh || part > 0 || ks > 0);
         }
         mma_commit(&sm.g_done);
         wait(&sm.p_ready, n & 1);
@@ -1122,7 +1126,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         arrive_warp(&sm.p_ready);
         wait_warp(&sm.o_done, n & 1);
         fence_after_sync();
-        const float f = ex2f(mine);
+        const float f = r.fresh(c) ? 0.f : ex2f(mine);
         // into the place of the values, which the chunk's products have read; a warp of its own sends them off
         uint8_t* tile = sm.v[st];
 #pragma unroll 1
@@ -1137,7 +1141,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             o[e] = __uint_as_float(x[e]);
-            if (f != 0.f) o[e] = fmaf(f, __uint_as_float(z[e]), o[e]);   // (a state that has decayed to nothing: nothing)
+            if (f != 0.f) o[e] = fmaf(f, __uint_as_float(z[e]), o[e]);   // (no state, or one that has decayed to nothing: nothing)
           }
           const int piece = (half * (DV / 2) + b) / 8;
           *reinterpret_cast<uint4*>(tile + tile_at(i, piece)) =
@@ -1176,8 +1180,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       if (bar_any(1, 256, r.kind == kEnd)) break;         // (together: they meet in barriers)
       if (r.kind != kRun) continue;
       float* state = a.l.state + ((long long)r.slot * a.l.Hv + r.head) * kSize + at.column;
-      const float* from = r.c0 > 0    ? a.ws + (size_t)(piece - 1) * kSize + at.column
-                          : !r.init   ? nullptr
+      const float* from = r.c0 > 0     ? a.ws + (size_t)(piece - 1) * kSize + at.column
                           : r.c1 < r.n ? a.ws + (size_t)(a.grid + piece) * kSize + at.column
                                        : state;
       if (r.n == 0 && !r.init) {
@@ -1192,18 +1195,15 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         wait_warp(&sm.g_full[st], (n >> 1) & 1);
         const float f = ex2f(sm.upto[st][kC - 1]);
 #pragma unroll 1
-        for (int b = 0; b < L::kRows; b += N) {
+        for (int b = 0; b < L::kRows && !r.fresh(c); b += N) {
           const int d = at.first + b;
           float s[N];
           if (c > r.c0) {
             tmem_row<N>(tl + b, s);
             if (*(volatile int*)&sm.bad[(n - 1) & 3]) add_bad(r, c - 1, d, s);
-          } else if (from) {
-#pragma unroll
-            for (int e = 0; e < N; ++e) s[e] = __ldcg(from + (d + e) * DV);
           } else {
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[e] = 0.f;
+            for (int e = 0; e < N; ++e) s[e] = __ldcg(from + (d + e) * DV);
           }
           uint8_t* row = sm.state + (d >> 6) * (128 * DV) + at.column * 128;
           const int chunk = (d & 63) >> 3;
