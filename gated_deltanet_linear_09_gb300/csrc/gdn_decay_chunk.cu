@@ -569,7 +569,7 @@ int launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStre
 // of the rows.
 template <int DK, int DV>
 struct StateRows {
-  static constexpr int kRows = DK * DV / 256, kBlock = kRows < 32 ? kRows : 32;
+  static constexpr int kRows = DK * DV / 256, kBlock = kRows < 16 ? kRows : 16;
   int lanes, column, first;
   __device__ __forceinline__ explicit StateRows(int t) {
     const int r = t & 127, half = t >> 7;
