@@ -9,13 +9,15 @@
 //
 // The chunks of all heads of all sequences, laid end to end, form one line (a constant per sequence and
 // head beside its chunks), and CTA w of G takes the w-th of G equal pieces: long and short prompts, many heads
-// or one, are balanced alike with no plan from the host.  Where pieces cut a sequence, three kernels: the
-// first sums up what each cut piece adds to the state (its keys weighted to the piece's end, so nothing is
-// rescaled), the second chains these along the pieces, the third computes the outputs, each piece from the
-// state it begins with.
+// or one, are balanced alike with no plan from the host.  Where pieces cut a sequence, a first kernel sums up what
+// each cut piece adds to the state (its keys weighted to the piece's end, so nothing is rescaled), and the outputs'
+// kernel starts each piece from its state: the sums of a run's pieces before it, which it adds up itself, or with few
+// heads, where a run has many pieces, finds chained by a kernel between the two (a prompt of 16384 tokens of 6 heads 50
+// us, without that kernel 54; 4096 of 32 heads 53, without it 52).  Runs that lie in one piece need no sums, and the
+// outputs' kernel begins with them as soon as the sums' kernel leaves an SM.
 //
-// 4096 tokens of 32 heads of 128 x 128: 53.5 us, of which the sums take 15, the chain 2 and the outputs 33; 14
-// ragged prompts of 2924 tokens, 448 runs in all: 69.  A chunk takes the outputs 5,700 clocks: shared memory's
+// 4096 tokens of 32 heads of 128 x 128: 52 us, of which the sums take 15 and the outputs 33; 14 ragged prompts of 2924
+// tokens, 448 runs in all: 61, and 69 when the outputs waited for all sums.  A chunk takes the outputs 5,700 clocks: shared memory's
 // bandwidth, 2,300 wavefronts of operands, 2,600 of the threads' accesses and some 1,000 of copies, of 128 bytes a
 // clock.  (The tensor pipe is busy for 2,560 of them.)  A run of one chunk takes 9,300: the roles' steps one after
 // another, as no chunk of the same run keeps them busy meanwhile.
@@ -31,9 +33,9 @@ using namespace tc;
 namespace {
 
 constexpr int kC = 128;               // tokens of a chunk
-// the line's units: beginning and ending a run, a chunk of it (runs at 6, 8, 10: 55, 57, 57 us for 53 above, and
-// 73, 78, 85 for 71)
-constexpr int kRunCost = 4, kChunkCost = 4;
+// The line's units: beginning and ending a run, the same of a run of one chunk, which does not wait for sums, and a
+// chunk.  (The prompts above at 4, 1: 52 and 61 us; at 3, 1 52 and 65; at 5, 1 52 and 68; at 4, 2 52 and 62.)
+constexpr int kRunCost = 4, kShortCost = 1, kChunkCost = 4;
 constexpr int kLeast = 16;            // units of a piece at least (whole chunks in every piece of a long run)
 constexpr int kRing = 4;              // runs known ahead
 constexpr float kLog2e = 1.4426950408889634f;
@@ -51,11 +53,12 @@ struct ChunkArgs {
   const int32_t* slots;
   const uint8_t* init;
   // [grid] states of the pieces' ends, [grid] states that cut runs began with (the slot is written by the run's
-  // last piece, whenever that comes to it), [grid] log2 decays, [grid] flags
+  // last piece, whenever that comes to it), [grid] states that pieces begin with, [grid] log2 decays, [grid] flags
   float* ws;
   float log2_scale;
   int num_seqs, total, grid;
-  int chained;                        // pieces may cut sequences: sum and chain kernels come first
+  int cut;                            // pieces may cut sequences: the sums come before the outputs
+  int chained;                        // and a kernel that chains them; else each piece adds up what came before it
 };
 
 struct Maps {
@@ -78,11 +81,16 @@ struct Line {
 };
 
 __device__ __forceinline__ int chunks_of(int len) { return (len + kC - 1) / kC; }
-__device__ __forceinline__ long long head_cost(int len) { return kRunCost + (long long)kChunkCost * chunks_of(len); }
+__device__ __forceinline__ int run_cost(int n) { return n == 1 ? kShortCost : kRunCost; }
+__device__ __forceinline__ long long head_cost(int len) {
+  const int n = chunks_of(len);
+  return run_cost(n) + (long long)kChunkCost * n;
+}
 // chunks of a run before offset o
 __device__ __forceinline__ int chunk_at(long long o, int n) {
-  const long long c = (o - kRunCost + kChunkCost - 1) / kChunkCost;
-  return o <= kRunCost ? 0 : c < n ? (int)c : n;
+  const int begin = run_cost(n);
+  const long long c = (o - begin + kChunkCost - 1) / kChunkCost;
+  return o <= begin ? 0 : c < n ? (int)c : n;
 }
 
 // Where a place of the line lies: in which sequence, how far into it, and the sequence.
@@ -616,7 +624,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
   SumSmem<DK, DV>& sm = *reinterpret_cast<SumSmem<DK, DV>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, piece = blockIdx.x;
   pdl_begin();
-  float* decays = a.ws + 2 * (size_t)a.grid * (DK * DV);
+  float* decays = a.ws + 3 * (size_t)a.grid * (DK * DV);
   int* flags = reinterpret_cast<int*>(decays + a.grid);
   if (!locate<kSumThreads, true>(a, piece, &sm.scan)) return;
   if (tid == 0) {
@@ -769,7 +777,7 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const ChunkArgs a)
   __shared__ int flag[kMostGrid + 1], start[kMostGrid], before[33];
   pdl_begin();
   const int size = a.l.dk * a.l.dv, slices = size / 4096, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float* decays = a.ws + 2 * (size_t)a.grid * size;
+  const float* decays = a.ws + 3 * (size_t)a.grid * size;
   const int mine = tid < a.grid ? __ldcg(reinterpret_cast<const int*>(decays + a.grid) + tid) : 0;
   if (mine == 2) decay[tid] = ex2f(__ldcg(decays + tid));
   flag[tid] = mine;
@@ -820,6 +828,41 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const ChunkArgs a)
   }
 }
 
+// The same for one piece that a run cut before it reaches: the state that it begins with, from the sums of the
+// run's pieces before it (at most 32), by T threads of whole warps.
+template <int SIZE, int T>
+__device__ __noinline__ void carry(const ChunkArgs& a, int piece, int t) {
+  constexpr int kSlots = SIZE / 4 / T;
+  const int lane = t & 31;
+  const float* decays = a.ws + 3 * (size_t)a.grid * SIZE;
+  const int flag = lane < piece ? __ldcg(reinterpret_cast<const int*>(decays + a.grid) + piece - 1 - lane) : 0;
+  const float mine = ex2f(lane < piece ? __ldcg(decays + piece - 1 - lane) : 0.f);
+  const uint32_t first = __ballot_sync(0xffffffffu, flag == 1);
+  int i = first ? __ffs(first) - 1 : 0;                       // pieces from the run's first to the last but one
+  const float4* p = reinterpret_cast<const float4*>(a.ws) + (size_t)(piece - 1 - i) * (SIZE / 4) + t;
+  float4 s[kSlots];
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) s[j] = __ldcg(p + j * T);
+#pragma unroll 1
+  while (--i >= 0) {
+    const float f = __shfl_sync(0xffffffffu, mine, i);
+    p += SIZE / 4;
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      float4 x = __ldcg(p + j * T);
+      if (f != 0.f) {
+        x.x = fmaf(f, s[j].x, x.x); x.y = fmaf(f, s[j].y, x.y);
+        x.z = fmaf(f, s[j].z, x.z); x.w = fmaf(f, s[j].w, x.w);
+      }
+      s[j] = x;
+    }
+  }
+  float4* to = reinterpret_cast<float4*>(a.ws) + (size_t)(2 * a.grid + piece) * (SIZE / 4) + t;
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) __stcg(to + j * T, s[j]);
+  __threadfence();
+}
+
 // ------------------------------------------------------------------ outputs
 
 template <int DK, int DV>
@@ -853,9 +896,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   OutSmem<DK, DV>& sm = *reinterpret_cast<OutSmem<DK, DV>*>(smem_raw);
   Scan& scan = *reinterpret_cast<Scan*>(sm.lo);          // (before the roles begin)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, piece = blockIdx.x;
-  // After a chain kernel (which began when everything before this call was done) only the states depend on the
-  // kernel before this one: all but the warps that use them begin at once.
-  if (!a.chained) pdl_wait_primary();
+  // After the sums or the chain (which began when everything before this call was done) only the states of cut runs
+  // depend on the kernel before this one: everything else begins at once, beside it.
+  if (!a.cut) pdl_wait_primary();
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -927,6 +970,18 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   };
   int n = 0;                          // chunks so far
   const int group = a.l.Hv / a.l.Hk;
+  // A run that was cut before this piece: the state that it begins with here.  (In front of the roles: called from
+  // within them, it costs their loops registers, and the prompts above 53 and 64 us.)
+  if (warp < kMmaWarp && a.cut && !a.chained) {
+    Walk walk;
+    walk.start(a, line, line.x0, found);
+    const Run r = walk.here();
+    if (r.kind == kRun && r.c0 > 0 && r.c1 > r.c0) {
+      pdl_wait_primary();
+      carry<DK * DV, 512>(a, piece, tid);
+      bar_any(2, 512, false);
+    }
+  }
 
   if (warp == kStoreWarp) {
     // ---------------------------------------------------------------- outputs to memory
@@ -1167,7 +1222,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
     }
   } else {
     // ------------------------------- keys and state
-    pdl_wait_primary();
+    if (a.chained) pdl_wait_primary();
     using L = StateRows<DK, DV>;
     constexpr int N = L::kBlock;
     const int t = tid - 256;
@@ -1188,7 +1243,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       if (bar_any(1, 256, r.kind == kEnd)) break;         // (together: they meet in barriers)
       if (r.kind != kRun) continue;
       float* state = a.l.state + ((long long)r.slot * a.l.Hv + r.head) * kSize + at.column;
-      const float* from = r.c0 > 0     ? a.ws + (size_t)(piece - 1) * kSize + at.column
+      if (!a.chained && r.c1 < r.n && r.init) pdl_wait_primary();
+      const float* from = r.c0 > 0     ? a.ws + (size_t)(a.chained ? piece - 1 : 2 * a.grid + piece) * kSize + at.column
                           : r.c1 < r.n ? a.ws + (size_t)(a.grid + piece) * kSize + at.column
                                        : state;
       if (r.n == 0 && !r.init) {
@@ -1253,6 +1309,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
         fence_before_sync();
       }
     }
+    pdl_wait_primary();                 // (this kernel ends after the one before it)
   }
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
@@ -1265,9 +1322,11 @@ int launch_dims(const ChunkArgs& a, const Maps& maps, cudaStream_t stream) {
   int rc;
   if ((rc = raise_smem(once_sum, sum_kernel<DK, DV>, sizeof(SumSmem<DK, DV>))) != GDN_OK) return rc;
   if ((rc = raise_smem(once_out, out_kernel<DK, DV>, sizeof(OutSmem<DK, DV>))) != GDN_OK) return rc;
-  if (a.chained) {
+  if (a.cut) {
     rc = launch(sum_kernel<DK, DV>, dim3((unsigned)a.grid), kSumThreads, sizeof(SumSmem<DK, DV>), stream, a, maps);
     if (rc != GDN_OK) return rc;
+  }
+  if (a.chained) {
     rc = launch(chain_kernel, dim3((unsigned)a.grid), kChainThreads, 0, stream, a);
     if (rc != GDN_OK) return rc;
   }
@@ -1279,7 +1338,7 @@ int launch_dims(const ChunkArgs& a, const Maps& maps, cudaStream_t stream) {
 size_t decay_prefill_ws_bytes(const DecayView& l, int, int) {
   const int sms = sm_count();
   const size_t grid = sms > 0 ? sms : 160;      // without a device (host-side sizing): at least the part's SMs
-  return grid * (2 * (size_t)l.dk * l.dv * 4 + 8);
+  return grid * (3 * (size_t)l.dk * l.dv * 4 + 8);
 }
 
 int launch_decay_prefill(const DecayView& l, const gdn_decay_tokens& t, const int32_t* cu_seqlens,
@@ -1303,7 +1362,9 @@ int launch_decay_prefill(const DecayView& l, const gdn_decay_tokens& t, const in
   a.total = total_tokens;
   a.grid = sm_count();
   if (a.grid <= 0 || a.grid >= kMostGrid) return GDN_ERR_CUDA;
-  a.chained = total_tokens > kC;      // (one chunk is not cut)
+  a.cut = total_tokens > kC;          // (one chunk is not cut)
+  // a sequence's heads share the line equally, so a run lies in at most grid / Hv + 2 pieces
+  a.chained = a.cut && a.grid > 10 * l.Hv;
   Maps maps = {};
   if (total_tokens > 0 && !(make_rows_map(t.q, total_tokens, t.q_ld, l.Hk * l.dk, kC, l.dk / 64, &maps.q) &&
                             make_rows_map(t.k, total_tokens, t.k_ld, l.Hk * l.dk, kC, l.dk / 64, &maps.k) &&

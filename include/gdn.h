@@ -588,7 +588,7 @@ size_t gdn_decay_prefill_workspace_bytes(const gdn_decay_layer* layer, int32_t n
  * in f32, from products of keys that are exact to 2^-16; for the outputs, states and the decayed scores
  * are rounded to bf16 (half a step, 2^-9, of each).  workspace: device, 256-byte aligned, contents
  * undefined on entry and exit; calls that may run at the same time need one each.  Bitwise reproducible.
- * Three launches; one for up to 128 tokens. */
+ * Two launches, three with few heads (16 or more take two), one for up to 128 tokens. */
 int gdn_decay_prefill(const gdn_decay_layer* layer, const gdn_decay_tokens* tokens, const int32_t* cu_seqlens,
                       const int32_t* slot_idx, const uint8_t* has_initial_state, int32_t num_seqs,
                       int32_t total_tokens, void* workspace, size_t workspace_bytes, cudaStream_t stream);

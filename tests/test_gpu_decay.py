@@ -298,3 +298,61 @@ def test_many_tokens_that_empty_the_state():
     decay[torch.rand(T, generator=g) < 0.7, 2] = -200.0
     decay[:120, 3] = -104.0
     run_prompts([T], 1, Hv, 64, 64, True, [1], row=row, decay=decay)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64), (64, 128), (128, 128)])
+def test_many_heads(dk, dv):
+    """Heads enough that a piece of the work adds up the sums before it by itself: long sequences cut into several
+    pieces, short ones that need no sums, continued ones, decays that empty the state, an infinity on the way."""
+    lens, Hk, Hv = [900, 1, 130, 3, 0, 40, 1300, 257], 8, 16
+    init = [1, 0, 1, 0, 1, 1, 0, 1]
+    row, decay = inputs((sum(lens),), Hk, Hv, dk, dv, 60, True, rate=0.02)
+    for t, h in ((10, 0), (899, 1), (500, 2), (1200, 3), (1201, 3), (2300, 4)):
+        decay[t, h] = -math.inf
+    _, layer = run_prompts(lens, Hk, Hv, dk, dv, True, init, seed=60, row=row, decay=decay)
+    assert int(layer.status.item()) == 0
+    run_prompts([2600], Hk, Hv, dk, dv, False, None, seed=61, rate=0.01)
+
+
+def test_many_heads_again_and_beside_each_other():
+    """Heads enough as above: the same bits again, in two graphs replayed beside each other, and calls in a row that
+    continue each other's states; a value that is not finite reaches its own column only."""
+    Hk, Hv, d, T = 8, 16, 128, 1500
+    row, decay = inputs((T + 60,), Hk, Hv, d, d, 70, True, rate=0.02)
+    q, k, v = views(row.cuda(), Hk, Hv, d, d)
+    g = decay.cuda()
+    cu = torch.tensor([0, 20, T, T + 60], dtype=torch.int32, device="cuda")
+    slots = torch.arange(3, dtype=torch.int32, device="cuda")
+    init = torch.tensor([1, 1, 0], dtype=torch.uint8, device="cuda")
+
+    def calls(layer, out):
+        for i in range(4):
+            layer.prefill(cu, slots, init if i else None, q, k, v, g, out=out)
+    layers = [runtime.DecayAttention(Hk, Hv, d, d, 3) for _ in range(4)]
+    outs = [torch.zeros((T + 60, Hv, d), dtype=torch.bfloat16, device="cuda") for _ in layers]
+    calls(layers[0], outs[0])
+    calls(layers[1], outs[1])
+    graphs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for layer, o, s in zip(layers[2:], outs[2:], streams):
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            calls(layer, o)
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for layer, o in zip(layers[1:], outs[1:]):
+        assert torch.equal(o, outs[0]) and torch.equal(layer.state, layers[0].state)
+    for t, value in ((21, math.nan), (700, math.inf)):
+        spoiled = v.clone()
+        spoiled[t, 5, 9] = value
+        layer, clean = runtime.DecayAttention(Hk, Hv, d, d, 3), runtime.DecayAttention(Hk, Hv, d, d, 3)
+        got = layer.prefill(cu, slots, None, q, k, spoiled, g)
+        want = clean.prefill(cu, slots, None, q, k, v, g)
+        assert not bool(got[t:T, 5, 9].isfinite().any()) and not bool(layer.state[1, 5, :, 9].isfinite().any())
+        got[t:T, 5, 9], want[t:T, 5, 9], layer.state[1, 5, :, 9], clean.state[1, 5, :, 9] = 0, 0, 0, 0
+        assert torch.equal(got, want) and torch.equal(layer.state, clean.state)
