@@ -368,8 +368,7 @@ struct Piece<T, kAnywhere> {             // the element and the one `step` on, w
 // by bulk copies while a row is worked on.  (A CTA to a row has nothing in flight while it starts, waits for its
 // sums and stores: 8192 x 4096 with a gate 46 us, so 37.)  The weights of aligned rows come from L1.  Other rows are
 // copied from the 16-byte boundary before them to the one behind them, and read an element or two at a time; their
-// weights lie beside the ring (KEPT: `weights` bytes), or come from L1 and L2 where
-// there is no room.
+// weights lie beside the ring (KEPT: `weights` bytes), or come from L1 and L2 where there is no room.
 template <typename T, Lie LIE, int NV, bool GROUPED, bool KEPT, int MOST>
 __global__ void __launch_bounds__(MOST, 1024 / MOST) block_rows_kernel(const BlockArgs a, int stages, uint32_t weights) {
   using P = Piece<T, LIE>;
@@ -593,8 +592,9 @@ int launch_rows(const BlockArgs& a, int ctas, int sms, cudaStream_t stream) {
 // Two rows' ring for each of as many CTAs as fit an SM.  Aligned rows: two vectors a thread, so that a row is done
 // soon (13107 bf16 x 4096 with everything 87 us, with four vectors 111), four where 512 threads need that.  Other
 // rows: 8 elements a thread, of bf16 rows above 256 elements, which take half the instructions, 16, so that more rows
-// are under way (43669 x 2049 156 us, with 8 elements 184; 5240 f32 x 6401 104 us, with 16 elements 185), unless
-// there is one CTA to an SM (10483 bf16 x 5121 with everything 185 us, with 16 elements 231).
+// are under way (43669 x 2049 156 us, with 8 elements 184; 6989 f32 x 6401 104 us, with 16 elements 193), unless
+// there is one CTA to an SM (10483 bf16 x 5121 with everything 185 us, with 16 elements 231).  Rows too long for 1024
+// threads of these: 16 elements, or 32.
 template <typename T, Lie LIE>
 int launch_ring(const BlockArgs& a, cudaStream_t stream) {
   const int sms = sm_count();
