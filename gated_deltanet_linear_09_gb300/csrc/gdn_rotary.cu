@@ -4,7 +4,7 @@
 // belongs to a token and a pair, whatever the head: a CTA takes a few neighbouring tokens, computes
 // their sines and cosines into shared memory, and then walks all heads of q and k with them.  An item of
 // work is a vector of one head, or for the half layout the two vectors that hold its pairs, so nothing is
-// read twice.  16384 tokens of 40 bf16 heads of 128: 53.8 us, 6.2 TB/s, 92 % of a copy.
+// read twice.  16384 tokens of 40 bf16 heads of 128: 53.0 us, 6.3 TB/s, 93 % of a copy.
 #include "gdn_rotary.cuh"
 
 namespace gdn {
@@ -33,6 +33,8 @@ struct RotaryArgs {
   float scale;
   int tokens, per_cta, dim, half, q_heads, heads;   // half: pairs of a head; heads: q's and k's
   FastDiv items, all_heads, pairs;                  // items of a head, heads, pairs
+  int step_item, step_head, step_token;             // 256 items on
+  int rest;                                         // items past the rotated part
 };
 
 constexpr int kTurns = 2048;      // (cos, sin) of a CTA: tokens * pairs of a head
@@ -92,10 +94,10 @@ struct Vec {
   }
 };
 
-// V elements a vector.  Half layout: items 0 .. half / V - 1 of a head are its pairs' vectors, the others
-// vectors past the rotated part.  Interleaved (V > 1): an item is a vector, holding whole pairs; V = 1:
-// items 0 .. half - 1 are the pairs, the others elements.
-template <typename T, int V, bool INTER>
+// V elements a vector.  Half layout: items 0 .. half / V - 1 of a head are its pairs' vectors, the others two vectors
+// each past the rotated part (the last perhaps one).  Interleaved (V > 1): an item is a vector, holding whole pairs;
+// V = 1: items 0 .. half - 1 are the pairs, the others two elements each.  WHOLE: nothing past the rotated part.
+template <typename T, int V, bool INTER, bool WHOLE>
 __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
   __shared__ __align__(16) float2 turn[kTurns];
   const int t0 = blockIdx.x * a.per_cta, count = min(a.per_cta, a.tokens - t0), tid = threadIdx.x;
@@ -105,24 +107,37 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
     turn[i] = rotary_turn(__ldg(a.turns + p), __ldg(a.pos + t0 + t), a.scale);
   }
   __syncthreads();
-  const uint32_t n = (uint32_t)count * a.heads * a.items.d;
   const int paired = INTER && V > 1 ? 0 : a.half / V;
-#pragma unroll(V <= 2 ? 4 : 2)
-  for (uint32_t i = tid; i < n; i += 256) {
-    const uint32_t th = a.items.div(i), e = i - th * a.items.d, t = a.all_heads.div(th);
-    int h = (int)(th - t * a.all_heads.d);
-    const bool is_q = h < a.q_heads;
-    if (!is_q) h -= a.q_heads;
-    const long long row = t0 + (int)t;
+  const int th = a.items.div(tid);
+  int e = tid - th * (int)a.items.d, t = a.all_heads.div(th), head = th - t * a.heads;
+  auto next = [&]() {
+    e += a.step_item;
+    head += a.step_head;
+    t += a.step_token;
+    if (e >= (int)a.items.d) {
+      e -= a.items.d;
+      ++head;
+    }
+    if (head >= a.heads) {
+      head -= a.heads;
+      ++t;
+    }
+  };
+  // (unrolled by two 54.5 us for the 53 above)
+#pragma unroll 1
+  for (; t < count; next()) {
+    const bool is_q = head < a.q_heads;
+    const int h = is_q ? head : head - a.q_heads;
+    const long long row = t0 + t;
     const T* src = is_q ? static_cast<const T*>(a.q) + row * a.q_ld + h * a.q_head_ld
                         : static_cast<const T*>(a.k) + row * a.k_ld + h * a.k_head_ld;
     T* dst = is_q ? static_cast<T*>(a.q_out) + (row * a.q_heads + h) * a.dim
                   : static_cast<T*>(a.k_out) + (row * (a.heads - a.q_heads) + h) * a.dim;
-    const float2* cs = turn + (int)t * a.half;
+    const float2* cs = turn + t * a.half;
     if constexpr (INTER && V > 1) {
       Vec<T, V> x;
       x.load(src + e * V);
-      const int p = (int)e * (V / 2);
+      const int p = e * (V / 2);
       if (p < a.half) {
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
@@ -134,11 +149,16 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
       }
       x.store(dst + e * V);
     } else {
-      if ((int)e < paired) {
-        const int lo = INTER ? 2 * (int)e : (int)e * V, hi = INTER ? lo + 1 : lo + a.half;
-        Vec<T, V> x, y;
-        x.load(src + lo);
-        y.load(src + hi);
+      // (all lanes' loads alike, whether their vectors are turned or not: a warp's lanes hold both kinds, and a quarter
+      // of heads of 256 turned takes 83 us of 537 MB, in branches of their own 133)
+      const bool turned = WHOLE || e < paired;
+      const int lo = !turned ? 2 * a.half + (e - paired) * V : INTER ? 2 * e : e * V;
+      const int hi = lo + (!turned ? a.rest * V : INTER ? 1 : a.half);
+      const bool two = turned || hi < a.dim;
+      Vec<T, V> x, y;
+      x.load(src + lo);
+      if (two) y.load(src + hi);
+      if (turned) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float2 c = cs[e * V + j];
@@ -146,14 +166,9 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
           x.v[j] = turned_a(u, w, c.x, c.y);
           y.v[j] = turned_b(u, w, c.x, c.y);
         }
-        x.store(dst + lo);
-        y.store(dst + hi);
-      } else {
-        const int at = 2 * a.half + ((int)e - paired) * V;
-        Vec<T, V> x;
-        x.load(src + at);
-        x.store(dst + at);
       }
+      x.store(dst + lo);
+      if (two) y.store(dst + hi);
     }
   }
 }
@@ -169,8 +184,9 @@ int launch_as(const RotaryArgs& a, bool inter, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = inter ? cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, true>, a)
-                              : cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, false>, a);
+  const cudaError_t e = inter            ? cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, true, false>, a)
+                        : a.rest == 0 ? cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, false, true>, a)
+                                      : cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, false, false>, a);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -187,16 +203,16 @@ int launch_typed(const RotaryLaunch& r, cudaStream_t stream) {
   constexpr int kWide = 16 / sizeof(T), kMid = 8 / sizeof(T);
   const int v = fits(kWide) ? kWide : fits(kMid) ? kMid : fits(2) ? 2 : 1;
   const int heads = r.q_heads + r.k_heads;
-  const int items = r.interleaved && v > 1 ? r.dim / v : (r.dim - half) / v;
-  // (16 bytes, 8, 4 of bf16, or an element: 104,857 tokens of 16 bf16 heads of 80 with halves of 40 111 us, with halves
-  // of 20 142, 83,886 of 100 with halves of 50 144 in pairs and 239 by elements)
+  const int rest = ((r.dim - r.rot) / v + 1) / 2, items = r.interleaved && v > 1 ? r.dim / v : half / v + rest;
+  // (16 bytes, 8, 4 of bf16, or an element: of 537 MB of bf16, vectors of 16 bytes take 82 to 96 us, of 8 98, of 4 128,
+  // elements 240)
   // tokens of a CTA: some four items a thread, as far as their sines fit
   const long long per_token = (long long)heads * items;
   long long per = (1024 + per_token - 1) / per_token;
   if (per > kTurns / half) per = kTurns / half;
   const RotaryArgs a{r.q, r.k, r.q_out, r.k_out, r.q_ld, r.q_head_ld, r.k_ld, r.k_head_ld, r.turns, r.positions,
                      r.scale, r.tokens, (int)per, r.dim, half, r.q_heads, heads, FastDiv((uint32_t)items),
-                     FastDiv((uint32_t)heads), FastDiv((uint32_t)half)};
+                     FastDiv((uint32_t)heads), FastDiv((uint32_t)half), 256 % items, 256 / items % heads, 256 / items / heads, rest};
   if (v == kWide) return launch_as<T, kWide>(a, r.interleaved, stream);
   if (v == kMid) return launch_as<T, kMid>(a, r.interleaved, stream);
   if (v == 2) return launch_as<T, 2>(a, r.interleaved, stream);
