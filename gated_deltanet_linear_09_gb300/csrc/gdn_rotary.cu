@@ -95,7 +95,7 @@ struct Vec {
 };
 
 // V elements a vector.  Half layout: items 0 .. half / V - 1 of a head are its pairs' vectors, the others two vectors
-// each past the rotated part (the last perhaps one).  Interleaved (V > 1): an item is a vector, holding whole pairs;
+// each past the rotated part (the last perhaps one).  Interleaved (V > 1): an item is two vectors, holding whole pairs;
 // V = 1: items 0 .. half - 1 are the pairs, the others two elements each.  WHOLE: nothing past the rotated part.
 template <typename T, int V, bool INTER, bool WHOLE>
 __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
@@ -135,19 +135,26 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
                   : static_cast<T*>(a.k_out) + (row * (a.heads - a.q_heads) + h) * a.dim;
     const float2* cs = turn + t * a.half;
     if constexpr (INTER && V > 1) {
-      Vec<T, V> x;
-      x.load(src + e * V);
-      const int p = e * (V / 2);
-      if (p < a.half) {
+      const int at[2] = {e * V, (e + (int)a.items.d) * V};
+      const bool two = at[1] < a.dim;
+      Vec<T, V> x[2];
+      x[0].load(src + at[0]);
+      if (two) x[1].load(src + at[1]);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const float2 c = cs[p + j];
-          const float u = x.v[2 * j], w = x.v[2 * j + 1];
-          x.v[2 * j] = turned_a(u, w, c.x, c.y);
-          x.v[2 * j + 1] = turned_b(u, w, c.x, c.y);
+      for (int i = 0; i < 2; ++i) {
+        const int p = at[i] / 2;
+        if (p < a.half) {
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            const float2 c = cs[p + j];
+            const float u = x[i].v[2 * j], w = x[i].v[2 * j + 1];
+            x[i].v[2 * j] = turned_a(u, w, c.x, c.y);
+            x[i].v[2 * j + 1] = turned_b(u, w, c.x, c.y);
+          }
         }
       }
-      x.store(dst + e * V);
+      x[0].store(dst + at[0]);
+      if (two) x[1].store(dst + at[1]);
     } else {
       // (all lanes' loads alike, whether their vectors are turned or not: a warp's lanes hold both kinds, and a quarter
       // of heads of 256 turned takes 83 us of 537 MB, in branches of their own 133)
@@ -203,8 +210,8 @@ int launch_typed(const RotaryLaunch& r, cudaStream_t stream) {
   constexpr int kWide = 16 / sizeof(T), kMid = 8 / sizeof(T);
   const int v = fits(kWide) ? kWide : fits(kMid) ? kMid : fits(2) ? 2 : 1;
   const int heads = r.q_heads + r.k_heads;
-  const int rest = ((r.dim - r.rot) / v + 1) / 2, items = r.interleaved && v > 1 ? r.dim / v : half / v + rest;
-  // (16 bytes, 8, 4 of bf16, or an element: of 537 MB of bf16, vectors of 16 bytes take 82 to 96 us, of 8 98, of 4 128,
+  const int rest = ((r.dim - r.rot) / v + 1) / 2, items = r.interleaved && v > 1 ? (r.dim / v + 1) / 2 : half / v + rest;
+  // (16 bytes, 8, 4 of bf16, or an element: of 537 MB of bf16, vectors of 16 bytes take 82 to 93 us, of 8 98, of 4 128,
   // elements 240)
   // tokens of a CTA: some four items a thread, as far as their sines fit
   const long long per_token = (long long)heads * items;
