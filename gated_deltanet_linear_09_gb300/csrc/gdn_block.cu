@@ -119,12 +119,27 @@ __device__ __forceinline__ void add_squares(const float* x, float& a, float& b) 
       b = v;
     }
 }
-// sigmoid for a result that is rounded to bf16: both approximations are off by about 2^-22.
-__device__ __forceinline__ float sigmoid_fast(float z) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return r;
+// s = sigmoid(z).  For a result that is rounded to bf16 by approximations that are off by about 2^-22, two elements at a
+// time where there are two.
+template <typename T, int VEC>
+__device__ __forceinline__ void sigmoids(const float* z, float* s) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[e] = sigmoidf_(z[e]);
+  } else {
+    constexpr float kMinusLog2e = -1.4426950408889634f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[e] = z[e];
+    mul_by<VEC>(s, kMinusLog2e);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[e]));
+    if constexpr (VEC == 1) s[0] += 1.0f;
+    else
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) add_pair(s[e], s[e + 1], 1.0f, 1.0f);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[e]));
+  }
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
@@ -236,8 +251,7 @@ __global__ void __launch_bounds__(MOST) block_kernel(const BlockArgs a) {
       if constexpr (!HOLD) z[j].load(static_cast<const T*>(p.gate) + row * p.gate_ld + c);
       z[j].get(g);
       float s[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s[e] = sizeof(T) == 4 ? sigmoidf_(g[e]) : sigmoid_fast(g[e]);
+      sigmoids<T, VEC>(g, s);
       if (p.gate_act == GDN_GATE_SILU) mul_by<VEC>(s, g);
       mul_by<VEC>(h[j], s);
     }
@@ -512,8 +526,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) block_rows_kernel(const Blo
       if (p.gate) {
         P::get(gate_in, c, threads, n, g);
         float s[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s[e] = sizeof(T) == 4 ? sigmoidf_(g[e]) : sigmoid_fast(g[e]);
+        sigmoids<T, VEC>(g, s);
         if (p.gate_act == GDN_GATE_SILU) mul_by<VEC>(s, g);
         mul_by<VEC>(h[j], s);
       }
