@@ -865,6 +865,23 @@ __device__ __noinline__ void carry(const ChunkArgs& a, int piece, int t) {
 
 // ------------------------------------------------------------------ outputs
 
+// The decayed scores of 32 columns (from `from` on) to `to`, for a warp of which some came out not finite: a token that a
+// decay of zero keeps from this one counts nothing, whatever the score (a factor of zero would make it NaN).  `last`: the
+// last column that the token sees.
+__device__ __noinline__ void scores_slowly(uint32_t from, uint32_t to, const float* upto, float mine, int last) {
+  uint32_t x[32], p[16];
+  tmem_ld32_nw(from, x);
+  tmem_wait_ld();
+  reg_fence16(x);
+  reg_fence16(x + 16);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float f0 = e <= last ? ex2f(mine - upto[e]) : 0.f, f1 = e + 1 <= last ? ex2f(mine - upto[e + 1]) : 0.f;
+    p[e / 2] = pack2(f0 != 0.f ? __uint_as_float(x[e]) * f0 : 0.f, f1 != 0.f ? __uint_as_float(x[e + 1]) * f1 : 0.f);
+  }
+  tmem_st16w_nw(to, p);
+}
+
 template <int DK, int DV>
 struct __align__(1024) OutSmem {
   uint8_t q[DK * kC * 2];
@@ -1161,8 +1178,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
 #pragma unroll 1
         for (int bb = 0; bb < 2; ++bb) {
           const int b = half * 2 + bb;
+          const int last = b == quad ? lane : 31;           // the last column that the token sees
           float x[32];
-          uint32_t p[16];
+          uint32_t p[16], odd[2] = {0, 0};                  // odd: NaN with any that is not finite
           if (b > quad) {                                   // later tokens only
 #pragma unroll
             for (int e = 0; e < 16; ++e) p[e] = 0;
@@ -1177,12 +1195,15 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
               x[e + 2] *= ex2f(mine - g.z);
               x[e + 3] *= ex2f(mine - g.w);
             }
-            const int last = b == quad ? lane : 31;         // the last column that the token sees
 #pragma unroll
             for (int e = 0; e < 32; e += 2) p[e / 2] = pack2(e <= last ? x[e] : 0.f, e + 1 <= last ? x[e + 1] : 0.f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) odd[e & 1] = fma_bf16x2(p[e], 0, odd[e & 1]);
           }
           // (over scores that this warp has read)
-          tmem_st16w_nw(tl + kTmS + half * 64 + bb * 16, p);
+          const uint32_t to = tl + kTmS + half * 64 + bb * 16;
+          if (__any_sync(0xffffffffu, any_nan(odd[0]) || any_nan(odd[1]))) scores_slowly(tl + kTmS + b * 32, to, upto + b * 32, mine, last);
+          else tmem_st16w_nw(to, p);
         }
         tmem_wait_st();
         fence_before_sync();
