@@ -537,20 +537,17 @@ __device__ __noinline__ void store_rows(const ChunkArgs& a, int t, int rows, int
   }
 }
 
-// What the non-finite values of column c among tokens [t, t + rows) (KEYS: and the non-finite keys' elements d) add
-// to element d of the state's column: infinities and NaN, told apart as the recurrence does.
-template <bool KEYS>
-__device__ __noinline__ float non_finite_part(const ChunkArgs& a, long long t, int rows, int head, int c, int d) {
+// What the non-finite values of column c among tokens [t, t + rows) add to element d of the state's column: infinities
+// and NaN, told apart as the recurrence does.  ALL: what all of its values add.
+template <bool ALL>
+__device__ __noinline__ float column_part(const ChunkArgs& a, long long t, int rows, int head, int c, int d) {
   const int hk = head / (a.l.Hv / a.l.Hk);
   float sum = 0.f, s = 0.f;
   for (int j = rows - 1; j >= 0; --j) {
     const float w = ex2f(sum);
     if (w != 0.f) {
       const float v = __bfloat162float(a.v[(t + j) * a.v_ld + head * a.l.dv + c]);
-      if (KEYS || !(fabsf(v) < INFINITY)) {
-        const float k = __bfloat162float(a.k[(t + j) * a.k_ld + hk * a.l.dk + d]);
-        if (!(fabsf(v) < INFINITY) || !(fabsf(k) < INFINITY)) s += k * w * v;
-      }
+      if (ALL || !(fabsf(v) < INFINITY)) s += __bfloat162float(a.k[(t + j) * a.k_ld + hk * a.l.dk + d]) * w * v;
     }
     sum += decay_log2(a, t + j, head);
   }
@@ -750,11 +747,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
         dst[(d + e) * DV] = s[e];
         odd |= !(fabsf(s[e]) < INFINITY);
       }
-      // (a value that is not finite times a part of a key that is zero: not what it should be)
+      // (a value that is not finite times a zero, which may be a part of a key or a key that a decay of zero has cut off:
+      // such elements are summed again, from the tokens that do count)
       if (odd)
+#pragma unroll 1
         for (int e = 0; e < N; ++e) {
-          const float x = non_finite_part<true>(a, run.t0 + run.c0 * kC, n * kC, run.head, at.column, d + e);
-          if (x != 0.f) dst[(d + e) * DV] = x + (begins ? f * __ldcg(src + (d + e) * DV) : 0.f);
+          if (fabsf(__ldcg(dst + (d + e) * DV)) < INFINITY) continue;
+          float x = column_part<true>(a, run.t0 + run.c0 * kC, n * kC, run.head, at.column, d + e);
+          if (begins && f != 0.f) x = fmaf(f, __ldcg(src + (d + e) * DV), x);
+          dst[(d + e) * DV] = x;
         }
     }
   }
@@ -1255,7 +1256,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       float more[N];                  // (a copy, so that s stays in registers)
 #pragma unroll 1
       for (int e = 0; e < N; ++e)
-        more[e] = non_finite_part<false>(a, r.t0 + c * kC, min(kC, r.len - c * kC), r.head, at.column, d + e);
+        more[e] = column_part<false>(a, r.t0 + c * kC, min(kC, r.len - c * kC), r.head, at.column, d + e);
 #pragma unroll
       for (int e = 0; e < N; ++e) s[e] += more[e];
     };

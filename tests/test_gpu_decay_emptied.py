@@ -49,3 +49,31 @@ def test_keys_before_an_emptying_token(T, value):
     got, layer = check_prompts([T], Hk, Hv, d, d, [1], row, decay, pool(2, Hv, d, d, T), slots)
     assert bool(got[14:90, 0].isfinite().all()) and bool(got[91:, 0].isfinite().all()) and bool(got[95:, 1].isfinite().all())
     assert not bool(got[10:, 2].isfinite().any()) and not bool(got[10:95, 1].isfinite().any())
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("Hk,Hv", [(1, 2), (8, 16)])
+def test_long_prompts_with_emptying_tokens(Hk, Hv, dk, dv):
+    """In a sequence that is cut into pieces, with heads few (chained) and many (summed by the pieces): values, keys and
+    a first state that are not finite, emptied in the same piece, in a later one, or not at all."""
+    lens = [1500, 60, 900]
+    row, decay = inputs((sum(lens),), Hk, Hv, dk, dv, 5, True, rate=0.01)
+    state = pool(4, Hv, dk, dv, 5)
+    slots = torch.tensor([2, 0, 3], dtype=torch.int32)
+    v0 = 2 * Hk * dk
+    # head 0: a value, and a first state in its column, emptied soon after
+    row[5, v0 + 9], state[2, 0, 11, 9], state[2, 0, 2, 8] = math.inf, math.inf, math.nan
+    decay[40, 0] = -math.inf
+    # head 1: a value that is emptied pieces later, another that stays in the state
+    row[300, v0 + dv + 1] = math.nan
+    decay[1000, 1] = -math.inf
+    row[1200, v0 + dv + 4] = -math.inf
+    # a key of the last sequence, emptied in head 0 and, a chunk later, in head 1
+    row[1560 + 70, Hk * dk + 3] = math.nan
+    decay[1560 + 75, 0] = -math.inf
+    decay[1560 + 200, 1] = -200.0
+    got, layer = check_prompts(lens, Hk, Hv, dk, dv, [1, 1, 1], row, decay, state, slots)
+    assert int(layer.status.item()) == 0
+    assert bool(got[40:1500, 0].isfinite().all()) and bool(layer.state[2, 0].isfinite().all())
+    assert bool(got[1000:1200, 1].isfinite().all()) and not bool(layer.state[2, 1, :, 4].isfinite().any())
+    assert bool(got[1635:, 0].isfinite().all()) and bool(layer.state[3, :2].isfinite().all())
