@@ -476,6 +476,8 @@ class DecayAttention:
             raise ValueError(f"has_init: contiguous uint8 [{n}] on {self.device}")
         if v.dim() != 3:
             raise ValueError("v: [tokens][num_v_heads][dv]")
+        if n == 0 and v.shape[0]:
+            raise ValueError("tokens, but no sequence that they are in")
         tokens, out = self._tokens(tuple(v.shape[:1]), q, k, v, log_decay, out, stream)
         if n:
             gdn.gdn_decay_prefill(self.c, tokens, cu_seqlens, slot_idx, has_init, v.shape[0],
