@@ -98,6 +98,10 @@ int gdn_block_norm(const gdn_block_args* args, int32_t rows, int32_t n, gdn_dtyp
   if (a.post && a.group != n && (a.x_ld % 8 != 0 || (a.gate && a.gate_ld % 8 != 0) || (a.residual && a.residual_ld % 8 != 0)))
     return GDN_ERR_MISALIGNED;
   if (a.total == a.y) return GDN_ERR_INVALID_ARG;
+  // (dense outputs in the place of rows further apart: over rows that other CTAs have yet to read)
+  for (const void* out : {(const void*)a.total, (const void*)a.y})
+    if (rows > 1 && out && ((out == a.x && a.x_ld != n) || (out == a.gate && a.gate_ld != n) || (out == a.residual && a.residual_ld != n)))
+      return GDN_ERR_INVALID_ARG;
   return gdn::launch_block_norm(a, rows, n, act, stream);
 }
 

@@ -1,8 +1,20 @@
 """Host checks of the mixers' calls: what they refuse, before any CUDA call."""
+import ctypes
+
 import pytest
 import torch
 
+from gated_deltanet_linear_09_gb300 import build as gbuild
 from gated_deltanet_linear_09_gb300 import gdn, runtime
+
+A = 0x10000
+INV = -1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    gbuild.build()
+    return gdn.load()
 
 
 def test_tokens_of_no_sequence(monkeypatch):
@@ -14,3 +26,13 @@ def test_tokens_of_no_sequence(monkeypatch):
     with pytest.raises(ValueError):
         layer.prefill(cu, slots, None, q, q, v, g)
     assert layer.prefill(cu, slots, None, q[:0], q[:0], v[:0], g).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("name", ["x", "gate", "residual"])
+@pytest.mark.parametrize("out", ["total", "y"])
+def test_block_outputs_in_place_of_strided_inputs(lib, name, out):
+    """A dense output in the place of rows that lie further apart would overwrite rows that are still to be read."""
+    d = dict(x=A, gate=2 * A, residual=3 * A, post=4 * A, pre=5 * A, x_ld=256, gate_ld=256, residual_ld=256, total=6 * A, y=7 * A,
+             scale=1.0, weight_offset=1.0, eps=1e-6, group=256, gate_act=gdn.GDN_GATE_SILU)
+    a = gdn.gdn_block_args(**{**d, out: d[name], f"{name}_ld": 264})
+    assert lib.gdn_block_norm(ctypes.byref(a), 2, 256, gdn.GDN_BF16, None) == INV
