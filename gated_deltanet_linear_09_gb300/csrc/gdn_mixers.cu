@@ -72,6 +72,7 @@ int gdn_rotary_apply(const gdn_rotary* rotary, const int32_t* positions, int32_t
     if (!aligned(k, size) || !aligned(k_out, size)) return GDN_ERR_MISALIGNED;
     if (k_out == k && !dense(tokens, k_heads, head_dim, k_ld, k_head_ld)) return GDN_ERR_INVALID_ARG;
   }
+  if (q_heads > 0 && k_heads > 0 && (q_out == k || k_out == q || q_out == k_out)) return GDN_ERR_INVALID_ARG;
   const gdn::RotaryLaunch r{q_heads ? q : nullptr, k_heads ? k : nullptr, q_heads ? q_out : nullptr, k_heads ? k_out : nullptr,
                             q_heads ? q_ld : 0, q_heads ? q_head_ld : 0, k_heads ? k_ld : 0, k_heads ? k_head_ld : 0,
                             rotary->turns, positions, rotary->scale, rotary->rot_dim, rotary->interleaved != 0, tokens,

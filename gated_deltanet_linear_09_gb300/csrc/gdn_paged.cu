@@ -226,7 +226,7 @@ int gdn_kv_append_rotated(const gdn_kv_cache* cache, const gdn_kv_batch* batch, 
     return GDN_ERR_MISALIGNED;
   if (num_q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || q_ld % 8 != 0 || q_head_ld % 8 != 0))
     return GDN_ERR_MISALIGNED;
-  if (num_q_heads > 0 && q_out == q) return GDN_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && (q_out == q || q_out == k || q_out == v)) return GDN_ERR_INVALID_ARG;
   if ((int64_t)b.total * (width + (int64_t)num_q_heads * c.D) > (1LL << 38)) return GDN_ERR_TOO_LARGE;
   gdn::RotatedAppend a;
   a.q = static_cast<const __nv_bfloat16*>(q);

@@ -36,3 +36,16 @@ def test_block_outputs_in_place_of_strided_inputs(lib, name, out):
              scale=1.0, weight_offset=1.0, eps=1e-6, group=256, gate_act=gdn.GDN_GATE_SILU)
     a = gdn.gdn_block_args(**{**d, out: d[name], f"{name}_ld": 264})
     assert lib.gdn_block_norm(ctypes.byref(a), 2, 256, gdn.GDN_BF16, None) == INV
+
+
+def test_outputs_in_place_of_the_other_input(lib):
+    """Queries' output in the place of the keys, or the other way round, or both outputs in one place."""
+    r = gdn.gdn_rotary(turns=A, rot_dim=64, interleaved=0, scale=1.0)
+    for q_out, k_out in ((2 * A, 4 * A), (3 * A, A), (3 * A, 3 * A)):
+        assert lib.gdn_rotary_apply(ctypes.byref(r), A, 2, 128, gdn.GDN_BF16, A, 256, 128, 2, q_out, 2 * A, 256, 128, 2, k_out, None) == INV
+    c = gdn.gdn_kv_cache(A, A, None, None, 4, 16, 2, 128, gdn.GDN_KV_BF16, None)
+    b = gdn.gdn_kv_batch(cu_seqlens=A, kv_lens=A, block_table=A, num_seqs=1, total_tokens=1, table_ld=4, max_tokens=1)
+    p = gdn.gdn_head_prep(A, A, 1.0, 1e-6, None)
+    for q_out in (2 * A, 3 * A):
+        assert lib.gdn_kv_append_rotated(ctypes.byref(c), ctypes.byref(b), ctypes.byref(r), ctypes.byref(p), A, 512, 128, 4, q_out, 2 * A,
+                                         256, 3 * A, 256, None) == INV
