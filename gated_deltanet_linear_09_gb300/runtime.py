@@ -239,8 +239,8 @@ class Rotary:
     trained length, scaling "linear" divides every frequency by it; "base" multiplies the base by
     factor^(rot_dim / (rot_dim - 2)), which stretches the slow pairs only; "bands" keeps pairs that make more
     than 32 turns within `trained` positions, divides those that make less than one, ramps between, and
-    multiplies what is turned by 0.1 ln(factor) + 1.  The frequencies are held to 2^-64 of a turn, so that the
-    angle of any position is exact."""
+    multiplies what is turned by 0.1 ln(factor) + 1 (by 1 for a factor below 1).  The frequencies are held to
+    2^-64 of a turn, so that the angle of any position is exact."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
                  factor: float = 1.0, trained: int = 8192, device="cuda"):
@@ -259,7 +259,7 @@ class Rotary:
             lo, hi = max(0.0, math.floor(lo)), min(rot_dim - 1.0, math.ceil(hi))
             ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(rot_dim // 2)]
             f = [x * (1.0 - r) + x / factor * r for x, r in zip(f, ramp)]
-            scale = 0.1 * math.log(factor) + 1.0
+            scale = 0.1 * math.log(max(factor, 1.0)) + 1.0
         elif scaling not in ("none", "base"):
             raise ValueError(f"scaling is none, linear, base or bands, not {scaling!r}")
         self._bind(f, interleaved, scale, device)

@@ -1,5 +1,6 @@
-"""Host checks of the mixers' calls: what they refuse, before any CUDA call."""
+"""Host checks of the mixers' calls: what they refuse, before any CUDA call; the magnitude of scaled rotations."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -49,3 +50,10 @@ def test_outputs_in_place_of_the_other_input(lib):
     for q_out in (2 * A, 3 * A):
         assert lib.gdn_kv_append_rotated(ctypes.byref(c), ctypes.byref(b), ctypes.byref(r), ctypes.byref(p), A, 512, 128, 4, q_out, 2 * A,
                                          256, 3 * A, 256, None) == INV
+
+
+@pytest.mark.parametrize("factor", [0.5, 1.0, 1.5, 8.0])
+def test_magnitude_of_scaled_bands(factor):
+    """0.1 ln(factor) + 1 of a stretched context; 1 where nothing is stretched."""
+    plan = runtime.Rotary(64, 1e4, scaling="bands", factor=factor, trained=4096, device="cpu")
+    assert plan.scale == (pytest.approx(0.1 * math.log(factor) + 1.0) if factor > 1.0 else 1.0)
