@@ -305,6 +305,8 @@ class Rotary:
         if positions.dtype != torch.int32 or positions.dim() != 1 or not _dense_rows(positions) or \
                 positions.device != self.device:
             raise ValueError("positions: contiguous int32 [tokens] on the rotation's device")
+        if (q is None and q_out is not None) or (k is None and k_out is not None):
+            raise ValueError("an output without its input")
         tokens = positions.shape[0]
         if q is not None:
             if k is not None and (q.dtype != k.dtype or q.shape[-1] != k.shape[-1]):

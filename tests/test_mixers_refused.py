@@ -57,3 +57,13 @@ def test_magnitude_of_scaled_bands(factor):
     """0.1 ln(factor) + 1 of a stretched context; 1 where nothing is stretched."""
     plan = runtime.Rotary(64, 1e4, scaling="bands", factor=factor, trained=4096, device="cpu")
     assert plan.scale == (pytest.approx(0.1 * math.log(factor) + 1.0) if factor > 1.0 else 1.0)
+
+
+def test_rotary_output_without_its_input(monkeypatch):
+    """It would be returned unwritten."""
+    monkeypatch.setattr(gdn, "load", lambda: pytest.fail("the library was called"))
+    plan, pos, x = runtime.Rotary(64, device="cpu"), torch.zeros(3, dtype=torch.int32), torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    for args in (dict(q_out=x), dict(k_out=x), dict(q=x, k_out=x), dict(k=x, q_out=x)):
+        with pytest.raises(ValueError):
+            plan.apply(pos, **args)
+    assert plan.apply(pos) == (None, None)
