@@ -378,6 +378,23 @@ struct Piece<T, kAnywhere> {             // the element and the one `step` on, w
   }
 };
 
+// What is left to do for a CTA that stopped at a row whose copies did not come within the wait's limit: NaN in its outputs
+// of that row and the later ones (there is no status word to set, and nothing that looks like a result is left), and a
+// wait, with a limit too, for copies under way, whose stages follow from the row's turn.
+template <typename T>
+__device__ __noinline__ void leave_stopped(T* total, T* y, int row, int rows, int n, uint64_t* full, int stages) {
+  const float nan = __uint_as_float(0x7fffffffu);
+  for (long long r = row; r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < n; c += blockDim.x) {
+      if (total) Act<T>::store(total + r * n + c, nan);
+      if (y) Act<T>::store(y + r * n + c, nan);
+    }
+  if (threadIdx.x != 0) return;
+  int turn = (row - (int)blockIdx.x) / (int)gridDim.x;
+  for (long long r = row; r < rows && r < row + (long long)stages * gridDim.x; r += gridDim.x, ++turn)
+    tc::mbar_wait(&full[turn % stages], (uint32_t)(turn / stages) & 1u, 100000000ull);
+}
+
 // The same for many rows: CTAs that stay, with the next row's x, gate and residual on their way into shared memory
 // by bulk copies while a row is worked on.  (A CTA to a row has nothing in flight while it starts, waits for its
 // sums and stores: 8192 x 4096 with a gate 46 us, so 37.)  The weights of aligned rows come from L1.  Other rows are
@@ -393,6 +410,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) block_rows_kernel(const Blo
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float part[4][32];
   __shared__ __align__(8) uint64_t full[kMostStages];
+  __shared__ int stopped;              // the row whose copies did not come, or -1
   const gdn_block_args& p = a.p;
   const int threads = blockDim.x, t = threadIdx.x, n = a.n;
   const uint32_t plane = ring_plane<T, LIE>(n), planes = 1 + (p.gate != nullptr) + (p.residual != nullptr);
@@ -400,6 +418,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) block_rows_kernel(const Blo
   uint8_t* const rows_at = ring + weights;
   if (t == 0) {
     for (int i = 0; i < stages; ++i) tc::mbar_init(&full[i], 1);
+    stopped = -1;
     tc::mbar_fence_init();
   }
   __syncthreads();
@@ -542,6 +561,8 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) block_rows_kernel(const Blo
       }
       if (p.total) P::put(static_cast<T*>(p.total) + row * n, c, threads, n, h[j]);
     }
+    // (one thread looks whether the wait ran out: every thread keeping what its own said costs rows off the boundaries 5 %)
+    if (t == threads - 1 && !tc::mbar_try_wait(&full[st], phase)) stopped = (int)row;
     float rs = 0.f;
     if (p.pre) {
       float ss = 0.f, s2 = 0.f;
@@ -551,6 +572,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) block_rows_kernel(const Blo
     } else {
       __syncthreads();
     }
+    if ((uint32_t)*(volatile int*)&stopped <= (uint32_t)row) break;     // (the next row's is above it: the same for all threads)
     // (every thread has read the row)
     if (t == 0) fetch(row + (long long)stages * gridDim.x, st);
     if (++st == stages) {
@@ -569,6 +591,8 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) block_rows_kernel(const Blo
       }
     }
   }
+  __syncthreads();
+  if (stopped >= 0) leave_stopped<T>(static_cast<T*>(p.total), static_cast<T*>(p.y), stopped, a.rows, n, full, stages);
 }
 
 // Launches it where the rows are many and a few fit an SM's shared memory; GDN_ERR_UNSUPPORTED_SHAPE: use the other.
