@@ -105,10 +105,10 @@ struct Walk {
   int s, h, t0, len, slot, init;
 
   __device__ __forceinline__ void load() {
-    t0 = __ldg(a->cu + s);
-    len = __ldg(a->cu + s + 1) - t0;
-    slot = __ldg(a->slots + s);
-    init = a->init != nullptr && __ldg(a->init + s) != 0;
+    t0 = __ldcg(a->cu + s);
+    len = __ldcg(a->cu + s + 1) - t0;
+    slot = __ldcg(a->slots + s);
+    init = a->init != nullptr && __ldcg(a->init + s) != 0;
   }
   // from the place x of the line
   __device__ __forceinline__ void start(const ChunkArgs& args, const Line& line, long long x, const Found& at) {
@@ -173,8 +173,8 @@ __device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Scan* sc) 
   if (a.num_seqs <= 32) {                 // one warp, all that it needs loaded at once
     if (warp == 0) {
       const bool on = lane < a.num_seqs;
-      const int c0 = on ? __ldg(a.cu + lane) : 0, c1 = on ? __ldg(a.cu + lane + 1) : 0, slot = on ? __ldg(a.slots + lane) : -1;
-      const int init = on && a.init && __ldg(a.init + lane) != 0;
+      const int c0 = on ? __ldcg(a.cu + lane) : 0, c1 = on ? __ldcg(a.cu + lane + 1) : 0, slot = on ? __ldcg(a.slots + lane) : -1;
+      const int init = on && a.init && __ldcg(a.init + lane) != 0;
       const bool wrong = (lane == 0 && c0 != 0) || c1 < c0 || c1 > a.total;
       const long long cost = on ? head_cost(c1 > c0 ? c1 - c0 : 0) * a.l.Hv : 0;
       long long incl = cost;
@@ -196,9 +196,9 @@ __device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Scan* sc) 
   }
   const int per = (a.num_seqs + NT - 1) / NT, s0 = tid * per, s1 = min(a.num_seqs, s0 + per);
   long long sum = 0;
-  bool wrong = tid == 0 && __ldg(a.cu) != 0;
+  bool wrong = tid == 0 && __ldcg(a.cu) != 0;
   for (int s = s0; s < s1; ++s) {
-    const int c0 = __ldg(a.cu + s), c1 = __ldg(a.cu + s + 1);
+    const int c0 = __ldcg(a.cu + s), c1 = __ldcg(a.cu + s + 1);
     wrong |= c1 < c0 || c1 > a.total;
     sum += head_cost(c1 > c0 ? c1 - c0 : 0) * a.l.Hv;
   }
@@ -218,16 +218,16 @@ __device__ __forceinline__ bool locate(const ChunkArgs& a, int index, Scan* sc) 
   const Line line = cut_line(total, a.grid, index);
   if (tid == 0) {
     sc->line = line;
-    sc->end = __ldg(a.cu + a.num_seqs);
+    sc->end = __ldcg(a.cu + a.num_seqs);
   }
   const long long x = END ? line.x1 - 1 : line.x0;
   long long at = incl - sum;
   if (at <= x && x < incl) {
     for (int s = s0; s < s1; ++s) {
-      const int c0 = __ldg(a.cu + s), len = __ldg(a.cu + s + 1) - c0;
+      const int c0 = __ldcg(a.cu + s), len = __ldcg(a.cu + s + 1) - c0;
       const long long c = head_cost(len) * a.l.Hv;
       if (x < at + c) {
-        sc->found = Found{x - at, s, c0, len, __ldg(a.slots + s), a.init && __ldg(a.init + s) != 0};
+        sc->found = Found{x - at, s, c0, len, __ldcg(a.slots + s), a.init && __ldcg(a.init + s) != 0};
         break;
       }
       at += c;
@@ -355,7 +355,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 
 // A token's log decay, in log2 units.
 __device__ __forceinline__ float decay_log2(const ChunkArgs& a, long long t, int h) {
-  const float g = __ldg(a.g + t * a.g_ld + h);
+  const float g = __ldcg(a.g + t * a.g_ld + h);
   return (g < kLowest ? kLowest : g) * kLog2e;
 }
 
@@ -365,17 +365,24 @@ __device__ __forceinline__ uint32_t two_parts(float w) {
   return pack2(w, w - __bfloat162float(hi));
 }
 
-// The decays of `rows` tokens from t on (a whole warp, lane = 4 tokens): up to and with each token, and of
-// what follows each in the chunk plus `rest`, as a factor in two parts (0 past the rows).  Returns the chunk's sum.
-__device__ __forceinline__ float chunk_decays(const ChunkArgs& a, int t, int rows, int h, float rest, float* upto,
-                                              uint32_t* after) {
-  const int lane = threadIdx.x & 31;
+// The log decays of `rows` tokens from t on, four to a lane (0 past the rows).
+struct Decays {
   float g[4];
+  __device__ __forceinline__ Decays(const ChunkArgs& a, int t, int rows, int h) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int j = lane * 4 + e;
-    g[e] = j < rows ? decay_log2(a, t + j, h) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+      const int j = lane * 4 + e;
+      g[e] = j < rows ? decay_log2(a, t + j, h) : 0.f;
+    }
   }
+};
+
+// Their sums (a whole warp): up to and with each token, and of what follows each in the chunk plus `rest`, as a factor
+// in two parts (0 past the rows).  Returns the chunk's sum.
+__device__ __forceinline__ float chunk_decays(const Decays& d, int rows, float rest, float* upto, uint32_t* after) {
+  const int lane = threadIdx.x & 31;
+  const float* g = d.g;
   const float own = (g[0] + g[1]) + (g[2] + g[3]);
   float up = own, down = own;
 #pragma unroll
@@ -514,7 +521,7 @@ __device__ __noinline__ void mark_reached(const ChunkArgs& a, long long t, int r
   float sum = 0.f;
   for (int j = 0; j <= row && ex2f(sum) != 0.f; ++j) {
     for (int e = c; e < c + columns; ++e)
-      if (!(fabsf(__bfloat162float(a.v[(t - j) * a.v_ld + head * a.l.dv + e])) < INFINITY))
+      if (!(fabsf(__bfloat162float(__ldcg(a.v + (t - j) * a.v_ld + head * a.l.dv + e))) < INFINITY))
         reinterpret_cast<__nv_bfloat16*>(tile + tile_at(row, e >> 3))[e & 7] = __float2bfloat16_rn(NAN);
     sum += decay_log2(a, t - j, head);
   }
@@ -546,8 +553,8 @@ __device__ __noinline__ float column_part(const ChunkArgs& a, long long t, int r
   for (int j = rows - 1; j >= 0; --j) {
     const float w = ex2f(sum);
     if (w != 0.f) {
-      const float v = __bfloat162float(a.v[(t + j) * a.v_ld + head * a.l.dv + c]);
-      if (ALL || !(fabsf(v) < INFINITY)) s += __bfloat162float(a.k[(t + j) * a.k_ld + hk * a.l.dk + d]) * w * v;
+      const float v = __bfloat162float(__ldcg(a.v + (t + j) * a.v_ld + head * a.l.dv + c));
+      if (ALL || !(fabsf(v) < INFINITY)) s += __bfloat162float(__ldcg(a.k + (t + j) * a.k_ld + hk * a.l.dk + d)) * w * v;
     }
     sum += decay_log2(a, t + j, head);
   }
@@ -665,6 +672,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
     float rest = 0.f;
     for (int i = 0; i < n; ++i) {
       const int st = i & 1, t = run.t0 + (run.c1 - 1 - i) * kC;
+      const Decays own(a, t, kC, run.head);                 // (on their way while the stage is waited for)
       if (i >= 2) wait(&sm.empty[st], ((i >> 1) & 1) ^ 1u);
       __syncwarp();
       if (lane == 0 && !dead()) {
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const ChunkArgs a, 
         tma_load_3d(sm.v[st], &maps.v, 0, t, run.head * (DV / 64), &sm.full[st]);
         if (DV == 64) tma_load_3d(sm.v[st] + 64 * kC * 2, &maps.v, 0, t, run.head, &sm.full[st]);
       }
-      rest += chunk_decays(a, t, kC, run.head, rest, nullptr, sm.w[st]);
+      rest += chunk_decays(own, kC, rest, nullptr, sm.w[st]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.weights[st]);
     }
@@ -914,8 +922,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
   OutSmem<DK, DV>& sm = *reinterpret_cast<OutSmem<DK, DV>*>(smem_raw);
   Scan& scan = *reinterpret_cast<Scan*>(sm.lo);          // (before the roles begin)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, piece = blockIdx.x;
-  // After the sums or the chain (which began when everything before this call was done) only the states of cut runs
-  // depend on the kernel before this one: everything else begins at once, beside it.
+  // After the sums or the chain only the states of cut runs depend on the kernel before this one: everything else begins
+  // at once, beside it.  (That kernel let this one start when everything before this call was done and written back.
+  // This one has not waited for that itself, which is what makes writes visible to all of its loads, so what it reads of
+  // the call's inputs comes from L2, by tensor copies and loads past L1, whose lines may be from before.)
   if (!a.cut) pdl_wait_primary();
   pdl_launch_dependents();
   if (tid == 0) {
@@ -1026,14 +1036,15 @@ __global__ void __launch_bounds__(kOutThreads, 1) out_kernel(const ChunkArgs a, 
       if (r.kind != kRun) continue;
       const int hk = r.head / group;
       for (int c = r.c0; c < r.c1; ++c, ++n) {
-        const int st = n & 1, t = r.t0 + c * kC;
+        const int st = n & 1, t = r.t0 + c * kC, rows = min(kC, r.len - c * kC);
+        const Decays own(a, t, rows, r.head);               // (on their way while the stage is waited for)
         if (n >= 2) wait_warp(&sm.k_empty[st], ((n >> 1) & 1) ^ 1u);
         if (lane == 0 && !dead()) {
           mbar_arrive_expect_tx(&sm.k_full[st], DK * kC * 2);
           tma_load_3d(sm.k[st], &maps.k, 0, t, hk * (DK / 64), &sm.k_full[st]);
         }
         __syncwarp();
-        chunk_decays(a, t, min(kC, r.len - c * kC), r.head, 0.f, sm.upto[st], sm.w[st]);
+        chunk_decays(own, rows, 0.f, sm.upto[st], sm.w[st]);
         arrive_warp(&sm.g_full[st]);
         if (n >= 2) wait_warp(&sm.v_empty[st], ((n >> 1) & 1) ^ 1u);
         if (lane == 0 && !dead()) {
