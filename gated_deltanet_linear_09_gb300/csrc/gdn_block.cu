@@ -5,7 +5,7 @@
 //
 // A dozen flops per element: the floor is the bytes, x, z and r read once, h and y written once.  A row stays
 // in registers from the first load to the last store, between the two sums that it waits for.  bf16: 8192 x 5120 with
-// everything 72 us, 5.8 TB/s, 86 % of a copy; 8192 x 4096 in heads of 128 with a gate 37 us, 80 %; 13107 x 4096 with
+// everything 72.5 us, 5.8 TB/s, 85 % of a copy; 8192 x 4096 in heads of 128 with a gate 37 us, 81 %; 13107 x 4096 with
 // everything 87 us, 91 %.  bf16 rows off the boundaries run at half of that, bound by the instructions of single
 // elements and pairs.
 #include <type_traits>
@@ -119,8 +119,9 @@ __device__ __forceinline__ void add_squares(const float* x, float& a, float& b) 
       b = v;
     }
 }
-// s = sigmoid(z).  For a result that is rounded to bf16 by approximations that are off by about 2^-22, two elements at a
-// time where there are two.
+// s = sigmoid(z).  For a result that is rounded to bf16 by approximations, off by about 2^-22 of it for z of a few units and
+// by |z| 2^-24 far below (its argument's rounding): less than 2^-17 as long as it is not 0.  Two elements at a time where
+// there are two.
 template <typename T, int VEC>
 __device__ __forceinline__ void sigmoids(const float* z, float* s) {
   if constexpr (sizeof(T) == 4) {

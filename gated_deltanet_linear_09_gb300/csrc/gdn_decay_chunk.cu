@@ -13,14 +13,19 @@
 // each cut piece adds to the state (its keys weighted to the piece's end, so nothing is rescaled), and the outputs'
 // kernel starts each piece from its state: the sums of a run's pieces before it, which it adds up itself, or with few
 // heads, where a run has many pieces, finds chained by a kernel between the two (a prompt of 16384 tokens of 6 heads 50
-// us, without that kernel 54; 4096 of 32 heads 53, without it 52).  Runs that lie in one piece need no sums, and the
+// us, without that kernel 54; 4096 of 32 heads 53, without it 52, before the checks below).  Runs that lie in one piece need no sums, and the
 // outputs' kernel begins with them as soon as the sums' kernel leaves an SM.
 //
-// 4096 tokens of 32 heads of 128 x 128: 52 us, of which the sums take 15 and the outputs 33; 14 ragged prompts of 2924
-// tokens, 448 runs in all: 61, and 69 when the outputs waited for all sums.  A chunk takes the outputs 5,700 clocks: shared memory's
-// bandwidth, 2,300 wavefronts of operands, 2,600 of the threads' accesses and some 1,000 of copies, of 128 bytes a
-// clock.  (The tensor pipe is busy for 2,560 of them.)  A run of one chunk takes 9,300: the roles' steps one after
-// another, as no chunk of the same run keeps them busy meanwhile.
+// 4096 tokens of 32 heads of 128 x 128: 52.4 us, of which the sums take 15 and the outputs 33; 14 ragged prompts of 2924
+// tokens, 448 runs in all: 62, and 8 more when the outputs waited for all sums.  A chunk takes the outputs 5,700 clocks:
+// shared memory's bandwidth, 2,300 wavefronts of operands, 2,600 of the threads' accesses and some 1,000 of copies, of
+// 128 bytes a clock.  (The tensor pipe is busy for 2,560 of them.)  A run of one chunk takes 9,300: the roles' steps one
+// after another, as no chunk of the same run keeps them busy meanwhile.
+//
+// Fewer than 32 bits: the decayed scores and, for the outputs, the state are operands in bf16 (2^-8 of each at most, in
+// f32 sums; more bits would take a second product each and shared memory that is not there), the decayed keys two bf16
+// parts.  Tokens before one whose decay is 0 count nothing, whatever they hold, where scores and sums come out not finite
+// too (looking for those takes 1 % of the time).
 #include <math.h>
 
 #include "gdn_internal.h"
@@ -34,7 +39,8 @@ namespace {
 
 constexpr int kC = 128;               // tokens of a chunk
 // The line's units: beginning and ending a run, the same of a run of one chunk, which does not wait for sums, and a
-// chunk.  (The prompts above at 4, 1: 52 and 61 us; at 3, 1 52 and 65; at 5, 1 52 and 68; at 4, 2 52 and 62.)
+// chunk.  (The prompts above, before the looks for what is not finite: at 4, 1 52 and 61 us; at 3, 1 52 and 65; at 5, 1 52
+// and 68; at 4, 2 52 and 62.)
 constexpr int kRunCost = 4, kShortCost = 1, kChunkCost = 4;
 constexpr int kLeast = 16;            // units of a piece at least (whole chunks in every piece of a long run)
 constexpr int kRing = 4;              // runs known ahead

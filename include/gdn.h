@@ -519,10 +519,11 @@ typedef enum { GDN_GATE_NONE = 0, GDN_GATE_SIGMOID = 1, GDN_GATE_SILU = 2 } gdn_
  * over the row (group = n) or over each run of `group` columns (32, 64, 128 or 256, dividing n), whose
  * weights post [group] they share.  act: sigmoid(z), or z sigmoid(z) (SILU).
  *   x, gate, residual: rows x_ld / gate_ld / residual_ld apart (>= n); pre, channel_scale [n]; total (NULL:
- *   not written, with pre only; may be residual or x, with equal row distance n) and y (NULL without pre)
- *   dense, overlapping nothing else.  Any n up to GDN_MAX_NORM_WIDTH and any distances; rows that start on 16-byte boundaries and hold
- *   a multiple of 8 elements move in 16-byte vectors, and groups below n need those
- *   (GDN_ERR_MISALIGNED).  rows = 0 is a no-op.  One launch. */
+ *   not written, with pre only; may be residual or x where their row distance is n, GDN_ERR_INVALID_ARG
+ *   otherwise) and y (NULL without pre) dense, overlapping nothing else.  Any n up to GDN_MAX_NORM_WIDTH and any
+ *   distances; rows that start on 16-byte boundaries and hold a multiple of 8 elements move in 16-byte vectors,
+ *   and groups below n need those (GDN_ERR_MISALIGNED).  Should a copy on the device not come within two
+ *   seconds, its row and some later ones hold NaN.  rows = 0 is a no-op.  One launch. */
 typedef struct {
   const void* x;
   const void* gate;
@@ -558,9 +559,9 @@ typedef struct {
 
 /* The tokens of a call: q, k bf16 [tokens][num_k_heads][dk], v bf16 [tokens][num_v_heads][dv], heads
  * adjacent, tokens q_ld / k_ld / v_ld elements apart (multiples of 8); out bf16 [tokens][num_v_heads][dv],
- * dense, overlapping no input.  g of token t and head h: log_decay[t * decay_ld + h] (f32; decay_ld 0: the same for every token),
- * finite or -inf, which empties the state; below -105 it counts as -inf (exp of it is 0 in f32).  16-byte
- * aligned, log_decay 4-byte aligned. */
+ * dense, overlapping no input.  g of token t and head h: log_decay[t * decay_ld + h] (f32; decay_ld 0: the
+ * same for every token), finite or -inf, which empties the state whatever it held; below -105 it counts as -inf
+ * (exp of it is 0 in f32).  16-byte aligned, log_decay 4-byte aligned. */
 typedef struct {
   const void* q;
   const void* k;
@@ -584,10 +585,13 @@ size_t gdn_decay_prefill_workspace_bytes(const gdn_decay_layer* layer, int32_t n
 /* Whole prompts: sequence n is tokens [cu_seqlens[n], cu_seqlens[n+1]) and continues from slot slot_idx[n]
  * where has_initial_state[n] (NULL: none do), else from zero; the slot then holds the state after its last
  * token (a sequence without tokens: the one it began with).  Arrays, padding slots and errors as in
- * gdn_prefill_chunked; outputs of tokens in no usable sequence are zeros.  The state is kept and added up
- * in f32, from products of keys that are exact to 2^-16; for the outputs, states and the decayed scores
- * are rounded to bf16 (half a step, 2^-9, of each).  workspace: device, 256-byte aligned, contents
- * undefined on entry and exit; calls that may run at the same time need one each.  Bitwise reproducible.
+ * gdn_prefill_chunked (tokens with num_seqs 0: GDN_ERR_INVALID_ARG); outputs of tokens in no usable sequence
+ * are zeros.  The state is kept and added up in f32, from products of keys that are exact to 2^-16; for the
+ * outputs, states and the decayed scores are rounded to bf16 (half a step, at most 2^-8 of each).  The decay
+ * between two tokens is the exp of a difference of f32 sums over up to 128 tokens, off by at most 2^-19 of the sum
+ * of their |g| (2e-3 is the most seen, where most are -105), and 0 below 2^-126.  workspace: device, 256-byte
+ * aligned, contents undefined on entry and exit; calls that may run at the same time need one each.  Bitwise
+ * reproducible.
  * Two launches, three with few heads (16 or more take two), one for up to 128 tokens. */
 int gdn_decay_prefill(const gdn_decay_layer* layer, const gdn_decay_tokens* tokens, const int32_t* cu_seqlens,
                       const int32_t* slot_idx, const uint8_t* has_initial_state, int32_t num_seqs,
